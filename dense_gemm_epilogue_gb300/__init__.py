@@ -41,6 +41,13 @@ TG_EPILOGUE_RELU = 1
 TG_OUT_F32 = 0
 TG_OUT_BF16 = 1
 TG_OUT_F16 = 2
+TG_ACT_NONE = 0
+TG_ACT_RELU = 1
+TG_ACT_SILU = 2
+TG_ACT_GELU_TANH = 3
+ACT_CODES = {"none": TG_ACT_NONE, "relu": TG_ACT_RELU, "silu": TG_ACT_SILU,
+             "gelu_tanh": TG_ACT_GELU_TANH}
+
 OUT_CODES = {"f32": TG_OUT_F32, "bf16": TG_OUT_BF16, "fp16": TG_OUT_F16}
 
 # Every symbol include/tg_gemm.h declares.
@@ -64,6 +71,17 @@ EXPORTED = (
     "tg_mx_pack_scales",
     "tg_bs_scale_bytes",
     "tg_bs_pack_scales",
+    "tg_linear_workspace_bytes",
+    "tg_linear",
+    "tg_linear_backward_workspace_bytes",
+    "tg_linear_backward",
+    "tg_gated_workspace_bytes",
+    "tg_gated",
+    "tg_gated_backward_workspace_bytes",
+    "tg_gated_backward",
+    "tg_layer_norm",
+    "tg_layer_norm_backward_workspace_bytes",
+    "tg_layer_norm_backward",
 )
 
 
@@ -197,6 +215,37 @@ def load(path: str | None = None) -> ctypes.CDLL:
         lib.tg_bs_scale_bytes.restype = i64
         lib.tg_bs_pack_scales.argtypes = [i64, i64, ctypes.c_int, vp, i64, vp, vp]
         lib.tg_bs_pack_scales.restype = ctypes.c_int
+        c = ctypes.c_int
+        lib.tg_linear_workspace_bytes.argtypes = [i64, i64, i64, vp, i64, vp, i64, c]
+        lib.tg_linear_workspace_bytes.restype = i64
+        lib.tg_linear.argtypes = [i64, i64, i64, vp, i64, vp, i64, vp, c, vp, i64, vp, i64, vp,
+                                  i64, c, vp, i64, vp]
+        lib.tg_linear.restype = c
+        lib.tg_linear_backward_workspace_bytes.argtypes = [i64, i64, i64, vp, i64, vp, i64, vp,
+                                                           i64, c, c]
+        lib.tg_linear_backward_workspace_bytes.restype = i64
+        lib.tg_linear_backward.argtypes = [i64, i64, i64, vp, i64, vp, i64, vp, i64, vp, i64, c,
+                                           vp, i64, vp, i64, c, vp, c, vp, i64, vp]
+        lib.tg_linear_backward.restype = c
+        lib.tg_gated_workspace_bytes.argtypes = [i64, i64, i64, vp, i64, vp, i64, vp, i64, c]
+        lib.tg_gated_workspace_bytes.restype = i64
+        lib.tg_gated.argtypes = [i64, i64, i64, vp, i64, vp, i64, vp, i64, c, vp, i64, vp, i64,
+                                 vp, i64, c, vp, i64, vp]
+        lib.tg_gated.restype = c
+        lib.tg_gated_backward_workspace_bytes.argtypes = [i64, i64, i64, vp, i64, vp, i64, vp,
+                                                          i64, c]
+        lib.tg_gated_backward_workspace_bytes.restype = i64
+        lib.tg_gated_backward.argtypes = [i64, i64, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp,
+                                          i64, vp, i64, c, vp, i64, vp, i64, vp, i64, c, c, vp,
+                                          i64, vp]
+        lib.tg_gated_backward.restype = c
+        lib.tg_layer_norm.argtypes = [i64, i64, vp, i64, vp, vp, f32, vp, i64, vp, vp, c, vp]
+        lib.tg_layer_norm.restype = c
+        lib.tg_layer_norm_backward_workspace_bytes.argtypes = [i64, i64]
+        lib.tg_layer_norm_backward_workspace_bytes.restype = i64
+        lib.tg_layer_norm_backward.argtypes = [i64, i64, vp, i64, vp, i64, vp, vp, vp, vp, i64,
+                                               vp, vp, c, vp, i64, vp]
+        lib.tg_layer_norm_backward.restype = c
         lib.tg_version.argtypes = []
         lib.tg_version.restype = i32
         if path is None:
@@ -373,6 +422,103 @@ def tg_bs_pack_scales(rows, K, in_dtype, src, ld_src, dst, stream=None) -> int:
     block size (32 K per scale; nvf4: 16)."""
     return load().tg_bs_pack_scales(rows, K, _dtype(in_dtype), _ptr(src), ld_src, _ptr(dst),
                                     _stream(stream))
+
+
+def _act(a):
+    return ACT_CODES[a] if isinstance(a, str) else int(a)
+
+
+def _out(d):
+    return OUT_CODES[d] if isinstance(d, str) else int(d)
+
+
+def _space(w):
+    """(pointer, bytes) of a workspace: None, a tensor, or such a pair."""
+    if w is None:
+        return None, 0
+    if isinstance(w, tuple):
+        return _ptr(w[0]), int(w[1])
+    return w.data_ptr(), w.numel() * w.element_size()
+
+
+def tg_linear_workspace_bytes(M, N, K, X, ldx, W, ldw, dtype) -> int:
+    return load().tg_linear_workspace_bytes(M, N, K, _ptr(X), ldx, _ptr(W), ldw, _dtype(dtype))
+
+
+def tg_linear(M, N, K, X, ldx, W, ldw, bias, act, R, ldr, Y, ldy, Z, ldz, dtype, workspace=None,
+              stream=None) -> int:
+    """Y = act(X W^T + bias) + R and, when Z is given, Z = X W^T + bias (row-major; bias, R and Z
+    may be None; act a name of ACT_CODES).  workspace: None, a tensor or (pointer, bytes)."""
+    ws, n = _space(workspace)
+    return load().tg_linear(M, N, K, _ptr(X), ldx, _ptr(W), ldw, _ptr(bias), _act(act), _ptr(R),
+                            ldr, _ptr(Y), ldy, _ptr(Z), ldz, _dtype(dtype), ws, n, _stream(stream))
+
+
+def tg_linear_backward_workspace_bytes(M, N, K, dY, lddy, X, ldx, W, ldw, act, dtype) -> int:
+    return load().tg_linear_backward_workspace_bytes(M, N, K, _ptr(dY), lddy, _ptr(X), ldx,
+                                                     _ptr(W), ldw, _act(act), _dtype(dtype))
+
+
+def tg_linear_backward(M, N, K, dY, lddy, X, ldx, W, ldw, Z, ldz, act, dX, lddx, dW, lddw,
+                       dw_dtype, db, dtype, workspace=None, stream=None) -> int:
+    """dZ = dY act'(Z); dX = dZ W, dW = dZ^T X (of type dw_dtype), db = sum over rows of dZ;
+    each of the three may be None."""
+    ws, n = _space(workspace)
+    return load().tg_linear_backward(M, N, K, _ptr(dY), lddy, _ptr(X), ldx, _ptr(W), ldw, _ptr(Z),
+                                     ldz, _act(act), _ptr(dX), lddx, _ptr(dW), lddw,
+                                     _out(dw_dtype), _ptr(db), _dtype(dtype), ws, n,
+                                     _stream(stream))
+
+
+def tg_gated_workspace_bytes(M, N, K, X, ldx, Wg, ldwg, Wu, ldwu, dtype) -> int:
+    return load().tg_gated_workspace_bytes(M, N, K, _ptr(X), ldx, _ptr(Wg), ldwg, _ptr(Wu), ldwu,
+                                           _dtype(dtype))
+
+
+def tg_gated(M, N, K, X, ldx, Wg, ldwg, Wu, ldwu, act, H, ldh, G, ldg, U, ldu, dtype,
+             workspace=None, stream=None) -> int:
+    """H = act(X Wg^T) * (X Wu^T) in one kernel; G and U (the two products) are stored when
+    given."""
+    ws, n = _space(workspace)
+    return load().tg_gated(M, N, K, _ptr(X), ldx, _ptr(Wg), ldwg, _ptr(Wu), ldwu, _act(act),
+                           _ptr(H), ldh, _ptr(G), ldg, _ptr(U), ldu, _dtype(dtype), ws, n,
+                           _stream(stream))
+
+
+def tg_gated_backward_workspace_bytes(M, N, K, X, ldx, Wg, ldwg, Wu, ldwu, dtype) -> int:
+    return load().tg_gated_backward_workspace_bytes(M, N, K, _ptr(X), ldx, _ptr(Wg), ldwg,
+                                                    _ptr(Wu), ldwu, _dtype(dtype))
+
+
+def tg_gated_backward(M, N, K, dH, lddh, X, ldx, Wg, ldwg, Wu, ldwu, G, ldg, U, ldu, act, dX, lddx,
+                      dWg, lddwg, dWu, lddwu, dw_dtype, dtype, workspace=None, stream=None) -> int:
+    """dX = dG Wg + dU Wu, dWg = dG^T X, dWu = dU^T X with dG = dH U act'(G), dU = dH act(G);
+    each of the three may be None."""
+    ws, n = _space(workspace)
+    return load().tg_gated_backward(M, N, K, _ptr(dH), lddh, _ptr(X), ldx, _ptr(Wg), ldwg,
+                                    _ptr(Wu), ldwu, _ptr(G), ldg, _ptr(U), ldu, _act(act),
+                                    _ptr(dX), lddx, _ptr(dWg), lddwg, _ptr(dWu), lddwu,
+                                    _out(dw_dtype), _dtype(dtype), ws, n, _stream(stream))
+
+
+def tg_layer_norm(M, N, X, ldx, gamma, beta, eps, Y, ldy, mean, rstd, dtype, stream=None) -> int:
+    """Y = (X - mean) rstd gamma + beta per row; gamma, beta, mean and rstd may be None; dtype a
+    name of OUT_CODES."""
+    return load().tg_layer_norm(M, N, _ptr(X), ldx, _ptr(gamma), _ptr(beta), eps, _ptr(Y), ldy,
+                                _ptr(mean), _ptr(rstd), _out(dtype), _stream(stream))
+
+
+def tg_layer_norm_backward_workspace_bytes(M, N) -> int:
+    return load().tg_layer_norm_backward_workspace_bytes(M, N)
+
+
+def tg_layer_norm_backward(M, N, dY, lddy, X, ldx, gamma, mean, rstd, dX, lddx, dgamma, dbeta,
+                           dtype, workspace=None, stream=None) -> int:
+    """dX, dgamma and dbeta (each may be None) of tg_layer_norm."""
+    ws, n = _space(workspace)
+    return load().tg_layer_norm_backward(M, N, _ptr(dY), lddy, _ptr(X), ldx, _ptr(gamma),
+                                         _ptr(mean), _ptr(rstd), _ptr(dX), lddx, _ptr(dgamma),
+                                         _ptr(dbeta), _out(dtype), ws, n, _stream(stream))
 
 
 def tg_status_string(status: int) -> str:

@@ -19,6 +19,7 @@
 #include <vector>
 
 #include "../../include/tg_gemm.h"
+#include "tg_host.h"
 #include "tg_launch.h"
 
 namespace tg {
@@ -151,10 +152,12 @@ DeviceState g_dev[kMaxDevices];
 
 // Split-K workspace of one (device, stream): room for `tiles` partial
 // 256 x 256 FP32 pair tiles; ready flags (four per tile: one per segment and
-// tile half of a two-segment exchange) and the ticket counter after them, all
-// kept at zero between launches by the kernel itself.
+// tile half of a two-segment exchange), the ticket counter after them and the
+// weight-streaming kernel's flags after that, all kept at zero between
+// launches by the kernels themselves.
 constexpr int64_t kFlagsPerTile = 4;
-constexpr int64_t kFlagWordsExtra = 32;
+constexpr int64_t kTicketWords = 32;
+constexpr int64_t kFlagWordsExtra = kTicketWords + tg::host::kStreamFlags;
 int64_t flag_words(int64_t tiles) { return kFlagsPerTile * tiles + kFlagWordsExtra; }
 uint32_t *ticket_counter(uint32_t *flags, int64_t tiles) { return flags + kFlagsPerTile * tiles; }
 
@@ -874,6 +877,59 @@ tg_status run(const Problem &q, tg_epilogue epi, const tg_options *opts, void *s
     else e = tg::launch_tf32(la);
     return e == cudaSuccess ? TG_OK : TG_ERR_CUDA;
 }
+
+}  // namespace
+
+// ------------------------------------------------------------------ services for the other operators
+
+namespace tg {
+namespace host {
+
+tg_status device(Device *out) {
+    DeviceState *ds = nullptr;
+    const tg_status st = device_state(&out->id, &ds);
+    if (st != TG_OK) return st;
+    out->sms = ds->sms;
+    out->status = ds->status;
+    out->wait_limit_ns = g_wait_limit_ns.load(std::memory_order_relaxed);
+    return TG_OK;
+}
+
+tg_status scratch(const Device &dev, cudaStream_t stream, int64_t tiles, Scratch *out) {
+    Workspace w;
+    const tg_status st = workspace_for(dev.id, stream, tiles, &w);
+    if (st != TG_OK) return st;
+    out->ws = w.ws;
+    out->tiles = w.tiles;
+    out->flags = w.flags;
+    out->ticket = ticket_counter(w.flags, w.tiles);
+    out->stream_flags = out->ticket + kTicketWords;
+    return TG_OK;
+}
+
+bool encode_rows(CUtensorMap *map, tg_out_dtype t, const void *base, int64_t rows, int64_t cols,
+                 int64_t ld, int box_rows, int row_bytes) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const int e = t == TG_OUT_F32 ? 4 : 2;
+    const CUtensorMapDataType dt = t == TG_OUT_F32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                   : t == TG_OUT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                      : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)(ld * e)};
+    cuuint32_t box[2] = {(cuuint32_t)(row_bytes / e), (cuuint32_t)box_rows};
+    cuuint32_t estr[2] = {1, 1};
+    return fn(map, dt, 2, const_cast<void *>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE,
+              row_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace host
+}  // namespace tg
+
+namespace {
 
 // ------------------------------------------------------------------ block-scaled products
 

@@ -1,0 +1,787 @@
+// CTA-pair GEMM of the feed-forward operators: row-major outputs, operands
+// contiguous along either axis, and epilogues that need more than the
+// accumulator.
+//
+// Role space: out(r, c) = f(sum_k A(r, k) B(c, k)), r < m, c < n, row-major.
+// One cluster of two CTAs computes 256 rows x BN accumulator columns with
+// tcgen05.mma.cta_group::2; the persistent schedule, the barriers between the
+// pair, the ticket ring and the bounded waits are those of the CTA-pair GEMM
+// (tg_kernel_pair.cuh).  What differs:
+//
+//   operands  Each of A and B is either K-major (rows of K) or MN-major (rows
+//             of the reduction index, the role-space row index contiguous):
+//             dX = dZ W reads W by columns, dW = dZ^T X reads both operands
+//             by columns.  An MN-major operand lands as 64 x 64 boxes (64
+//             reduction rows of 128 bytes, 128-byte swizzle), 8 KB apart
+//             along the role-space rows, and the MMA's transpose bits take it
+//             from there; nothing is transposed in memory.
+//   two pairs The reduction may run over two operand pairs in turn (dX = dG
+//             Wg + dU Wu): K blocks from k_blocks0 on come from the second
+//             pair of maps, into the same accumulator.
+//   dual      The gated unit's forward tile holds BN/2 gate columns and BN/2
+//             up columns of the same features: the leader stages Wg rows, the
+//             peer Wu rows, one MMA serves both, and one thread of the
+//             epilogue owns g and u of the same element.
+//   entries   A second problem of the same shape in the same launch (dWg and
+//             dWu share X): tiles from tiles_per_batch on use the second A map
+//             and the second output.
+//   epilogue  Warps stage 32 rows x 128 bytes in shared memory (swizzled, 4 KB
+//             each) and store them by TMA, which clips at the edges and writes
+//             whole lines; row-major rows stored from registers would touch 32
+//             lines per instruction.  The residual comes in through the same
+//             buffer by TMA before the accumulator is ready.  Outputs or
+//             residuals that TMA cannot address (row stride or base not a
+//             multiple of 16 bytes) go through the same buffer with plain
+//             2-byte accesses, a row per instruction.
+//
+// Bound: tensor throughput for token counts above about 300 (arithmetic
+// intensity 256 x 256 / (256 + 256) = 128 FLOP per byte of L2 traffic).
+#pragma once
+
+#include <cstdint>
+#include "tg_kernel_pair.cuh"
+
+namespace tg {
+
+enum MlpAct : int32_t { MLP_NONE = 0, MLP_RELU = 1, MLP_SILU = 2, MLP_GELU = 3, MLP_ACTS = 4 };
+
+// 1 / (1 + exp(-x)) by the hardware's exponential and reciprocal: relative
+// error about 2^-21 for the |x| that matter, far below a 16-bit output's
+// 2^-9, and below the 1e-6 that an FP32 column sum over it is held to.
+// exp(-x) = inf for x < -88 gives 0, the limit.
+__device__ __forceinline__ float mlp_sigmoid(float x) {
+    return __fdividef(1.0f, 1.0f + __expf(-x));
+}
+
+// The tanh form of GELU is y/2 (1 + tanh(v)) = y sigmoid(2v), v =
+// sqrt(2/pi) (y + 0.044715 y^3): no cancellation in 1 + tanh(v) for negative
+// v.  |y| is held to 16 inside the argument (there sigmoid is 0 or 1 to all
+// FP32 digits), which keeps y^3 and the gradient's product finite.
+constexpr float kGelu2C = 1.5957691216057308f;  // 2 sqrt(2/pi)
+__device__ __forceinline__ float mlp_gelu_arg(float y) {
+    return y < -16.0f ? -16.0f : (y > 16.0f ? 16.0f : y);  // NaN stays
+}
+
+__device__ __forceinline__ float mlp_act(int act, float y) {
+    switch (act) {
+    case MLP_RELU: return (!(y > 0.0f) && !(y != y)) ? 0.0f : y;
+    case MLP_SILU: return y * mlp_sigmoid(y);
+    case MLP_GELU: {
+        const float t = mlp_gelu_arg(y);
+        return y * mlp_sigmoid(kGelu2C * (t + 0.044715f * t * t * t));
+    }
+    default: return y;
+    }
+}
+
+// Activation and its derivative.  ReLU'(0) = 0.
+__device__ __forceinline__ void mlp_act_grad(int act, float y, float &a, float &d) {
+    switch (act) {
+    case MLP_RELU: {
+        const bool on = y > 0.0f || y != y;
+        a = on ? y : 0.0f;
+        d = on ? 1.0f : 0.0f;
+        return;
+    }
+    case MLP_SILU: {
+        const float s = mlp_sigmoid(y);
+        a = y * s;
+        d = s + a * (1.0f - s);
+        return;
+    }
+    case MLP_GELU: {
+        const float t = mlp_gelu_arg(y);
+        const float s = mlp_sigmoid(kGelu2C * (t + 0.044715f * t * t * t));
+        a = y * s;
+        d = s + t * s * (1.0f - s) * kGelu2C * (1.0f + 0.134145f * t * t);
+        return;
+    }
+    default: a = y; d = 1.0f; return;
+    }
+}
+
+template <Kind KD>
+__device__ __forceinline__ float mlp_to_float(uint32_t half_bits) {
+    if constexpr (KD == Kind::BF16) return __uint_as_float(half_bits << 16);
+    else return __half2float(__ushort_as_half((unsigned short)half_bits));
+}
+template <Kind KD>
+__device__ __forceinline__ uint32_t mlp_pack2(float lo, float hi) {
+    if constexpr (KD == Kind::BF16) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&v);
+    } else {
+        const __half2 v = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&v);
+    }
+}
+
+// TMA store of a swizzled shared-memory box; bounds are the map's.
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, uint32_t src, int32_t c0,
+                                             int32_t c1) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(src), "r"(c0), "r"(c1)
+                 : "memory");
+}
+__device__ __forceinline__ void bulk_commit() {
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+// The issuing thread's stores have read their shared memory / are complete.
+__device__ __forceinline__ void bulk_wait_read() {
+    asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+}
+__device__ __forceinline__ void bulk_wait_all() {
+    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
+
+// Descriptor of an MN-major operand tile: 64-element rows of 128 bytes along
+// the role-space rows, one per reduction index, 128-byte swizzle.  Leading
+// byte offset: the next 64 role-space rows (one 64 x 64 box, 8 KB); stride
+// byte offset: the next 8 reduction indexes (1 KB).
+__device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t saddr) {
+    uint64_t d = 0;
+    d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
+    d |= (uint64_t)(8192u >> 4) << 16;
+    d |= (uint64_t)(1024u >> 4) << 32;
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)2 << 61;
+    return d;
+}
+
+enum class MlpEpi : int { LINEAR = 0, GATED = 1, PLAIN = 2 };
+
+struct MlpOut {
+    void *ptr;       // row-major output (NULL: not wanted)
+    int64_t ld;      // elements between rows
+    int32_t tma;     // 1: stored by TMA through its map
+    int32_t pad_;
+};
+
+struct MlpMaps {
+    CUtensorMap a[2], b[2], out[3], r;
+};
+
+struct MlpParams {
+    GemmParams g;             // schedule, split, status (m, n: rows and columns of one output)
+    int32_t k_blocks0;        // K blocks of the first operand pair (rest: the second)
+    int32_t act;
+    const float *bias;        // n values or NULL
+    const void *r;            // residual (m x n) or NULL
+    int64_t ldr;
+    int32_t r_tma;
+    int32_t out_f32;          // PLAIN: outputs are FP32 (else the operands' type)
+    int32_t clip;             // 1: a row's bytes are a multiple of 16, so TMA may clip a box there
+    MlpOut out[3];            // LINEAR: Y, Z; GATED: H, G, U; PLAIN: one per entry
+};
+
+// AM, BM: 0 = K-major, 1 = MN-major operand.
+template <Kind KD, int BN, int AM, int BM, MlpEpi EP>
+struct MlpConfig {
+    using T = KindTraits<KD>;
+    static constexpr int BK = T::block_k;
+    static constexpr int PAIR_M = 2 * BLOCK_M;
+    static constexpr int B_ROWS = BN / 2;
+    static constexpr bool DUAL = EP == MlpEpi::GATED;
+    static constexpr int OUT_N = DUAL ? BN / 2 : BN;  // output columns per tile
+    static constexpr int A_BYTES = BLOCK_M * ROW_BYTES;
+    static constexpr int B_BYTES = B_ROWS * ROW_BYTES;
+    static constexpr int EPI_WARPS = 8;
+    static constexpr int COLS = OUT_N / 2;            // output columns of an epilogue warp
+    // A staged row: 128 bytes (64 16-bit columns), or the 64 bytes of the 32
+    // columns a warp has in the gated 128-column tile.
+    static constexpr int STG_ROW = COLS * 2 < ROW_BYTES ? COLS * 2 : ROW_BYTES;
+    static constexpr int STG_BYTES = 32 * STG_ROW;    // one warp's staging buffer
+    static constexpr int FIT = (SMEM_LIMIT - 2048 - EPI_WARPS * STG_BYTES) / (A_BYTES + B_BYTES);
+    static constexpr int STAGES = FIT > 8 ? 8 : FIT;
+    static constexpr int A_OFF = 0;
+    static constexpr int B_OFF = STAGES * A_BYTES;
+    static constexpr int STG_OFF = B_OFF + STAGES * B_BYTES;
+    static constexpr int BAR_OFF = STG_OFF + EPI_WARPS * STG_BYTES;
+    static constexpr int FULL0 = 0, EMPTY0 = STAGES;
+    static constexpr int ACCF0 = 2 * STAGES, ACCE0 = ACCF0 + 2, DRAIN = ACCE0 + 2;
+    static constexpr int SLOTS = 4;
+    static constexpr int TKF0 = DRAIN + 1, TKE0 = TKF0 + SLOTS;
+    static constexpr int RES0 = TKE0 + SLOTS;  // one per epilogue warp: residual landed
+    static constexpr int NUM_BARS = RES0 + EPI_WARPS;
+    static constexpr int MISC_OFF = BAR_OFF + NUM_BARS * 8;
+    static constexpr int TK_OFF = (MISC_OFF + 16 + 15) / 16 * 16;
+    static constexpr int TICKET_OFF = TK_OFF + 16 * SLOTS;
+    static constexpr int SMEM_BYTES = TICKET_OFF + 16 * SLOTS + 1024;
+    static constexpr int TMEM_COLS = 2 * BN;
+    static constexpr int NUM_WARPS = 2 + EPI_WARPS;
+    static constexpr int NUM_THREADS = NUM_WARPS * 32;
+    static constexpr int MMAS_PER_STAGE = BK / T::umma_k;
+    static constexpr int READERS = 2 * (1 + EPI_WARPS) + 1;
+    static constexpr uint32_t IDESC = (1u << 4) | (T::fmt << 7) | (T::fmt << 10) |
+                                      ((uint32_t)AM << 15) | ((uint32_t)BM << 16) |
+                                      ((uint32_t)(BN >> 3) << 17) |
+                                      ((uint32_t)(PAIR_M >> 4) << 24);
+    static_assert(T::mma == MmaKind::F16, "16-bit kinds");
+    static_assert(SMEM_BYTES <= SMEM_LIMIT, "shared memory budget");
+    static_assert(BN == 128 || BN == 256, "tile N");
+};
+
+// Byte `b` of row `r` of a staging buffer with TMA's 128-byte (64-byte) swizzle
+// for rows of 128 (64) bytes.
+template <int ROW>
+__device__ __forceinline__ int stg_offset(int r, int b) {
+    const int x = ROW == 128 ? (r & 7) : ((r >> 1) & 3);
+    return r * ROW + ((((b >> 4) ^ x) << 4) | (b & 15));
+}
+
+// A staging buffer's rows from or to rows that TMA cannot address: one row per
+// step, neighbouring lanes on neighbouring elements, bounds checked.
+template <int ROW, typename E>
+__device__ __forceinline__ void stg_to_global(const uint8_t *stg, E *dst, int64_t ld, int64_t row0,
+                                              int64_t col0, int64_t rows, int64_t cols, int lane) {
+    constexpr int PER = ROW / (int)sizeof(E);
+    for (int r = 0; r < 32 && row0 + r < rows; ++r) {
+#pragma unroll
+        for (int c = lane; c < PER; c += 32) {
+            const int b = c * (int)sizeof(E);
+            if (col0 + c < cols)
+                dst[(row0 + r) * ld + col0 + c] =
+                    *reinterpret_cast<const E *>(stg + stg_offset<ROW>(r, b));
+        }
+    }
+}
+template <int ROW>
+__device__ __forceinline__ void global_to_stg(uint8_t *stg, const uint16_t *src, int64_t ld,
+                                              int64_t row0, int64_t col0, int64_t rows,
+                                              int64_t cols, int lane) {
+    for (int r = 0; r < 32; ++r) {
+#pragma unroll
+        for (int c = lane; c < ROW / 2; c += 32) {
+            const bool in = row0 + r < rows && col0 + c < cols;
+            *reinterpret_cast<uint16_t *>(stg + stg_offset<ROW>(r, c * 2)) =
+                in ? src[(row0 + r) * ld + col0 + c] : (uint16_t)0;
+        }
+    }
+}
+
+template <Kind KD, int BN, int AM, int BM, MlpEpi EP>
+__global__ void __launch_bounds__(MlpConfig<KD, BN, AM, BM, EP>::NUM_THREADS, 1)
+    tg_mlp_kernel(const __grid_constant__ MlpMaps maps, const __grid_constant__ MlpParams mp) {
+    using C = MlpConfig<KD, BN, AM, BM, EP>;
+    constexpr int S = C::STAGES;
+    const GemmParams &p = mp.g;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    const uint32_t sbase = smem_u32(smem);
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();  // 0: leader, 1: peer
+    const bool leader = rank == 0;
+    const int64_t pair = blockIdx.x / 2;
+    const int64_t num_pairs = gridDim.x / 2;
+
+    auto bar = [&](int i) -> uint32_t { return sbase + C::BAR_OFF + 8 * i; };
+    auto a_stage = [&](int s) -> uint32_t { return sbase + C::A_OFF + s * C::A_BYTES; };
+    auto b_stage = [&](int s) -> uint32_t { return sbase + C::B_OFF + s * C::B_BYTES; };
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::MISC_OFF);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::MISC_OFF + 4);
+    volatile int *fin_ready = reinterpret_cast<volatile int *>(smem + C::MISC_OFF + 8);
+    const PairWaitCtl ctl{abort_flag, map_shared_rank(smem_u32(smem + C::MISC_OFF + 4), rank ^ 1u),
+                          p.status, p.wait_limit_ns};
+    const int nkb = p.num_k_blocks;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(bar(C::FULL0 + s), 1);
+            mbar_init(bar(C::EMPTY0 + s), 1);
+        }
+        for (int a = 0; a < 2; ++a) {
+            mbar_init(bar(C::ACCF0 + a), 1);
+            mbar_init(bar(C::ACCE0 + a), 2 * C::EPI_WARPS);
+        }
+        mbar_init(bar(C::DRAIN), 1);
+        for (int c = 0; c < C::SLOTS; ++c) {
+            mbar_init(bar(C::TKF0 + c), 1);
+            mbar_init(bar(C::TKE0 + c), C::READERS);
+        }
+        for (int w = 0; w < C::EPI_WARPS; ++w) mbar_init(bar(C::RES0 + w), 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+        if (nkb > 0) {
+            prefetch_tensormap(&maps.a[0]);
+            prefetch_tensormap(&maps.b[0]);
+        }
+        if (mp.out[0].tma) prefetch_tensormap(&maps.out[0]);
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(smem_u32(tmem_slot), C::TMEM_COLS);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before();
+    cluster_sync_all();
+    tc_fence_after();
+    griddep_launch();
+    const uint32_t tmem_base = *tmem_slot;
+    const UnitPlan up = make_unit_plan(p, num_pairs);
+    // Tickets as in the CTA-pair GEMM: the first unit static, later ones
+    // claimed in order; the launch's last claim resets the counter.
+    const bool tick = p.ticket != nullptr && up.units >= num_pairs;
+    auto tk_read = [&](int64_t step) -> int64_t {
+        const int slot = (int)(step % C::SLOTS);
+        int64_t next = -2;
+        if (pair_wait(bar(C::TKF0 + slot), (uint32_t)((step / C::SLOTS) & 1), ctl, SITE_SCHED)) {
+            const volatile uint64_t *r =
+                reinterpret_cast<const volatile uint64_t *>(smem + C::TK_OFF + 16 * slot);
+            next = (int64_t)r[0];
+        }
+        if (leader) mbar_arrive(bar(C::TKE0 + slot));
+        else mbar_arrive_cluster(map_shared_rank(bar(C::TKE0 + slot), 0));
+        return next;
+    };
+    auto tk_read_warp = [&](int64_t step) -> int64_t {
+        int64_t next = 0;
+        if (lane == 0) next = tk_read(step);
+        return __shfl_sync(0xffffffffu, next, 0);
+    };
+
+    if (warp == 0) {
+        // ------------------------------------------------------ producer (both CTAs)
+        if (lane == 0) {
+            int s = 0;
+            uint32_t ph = 0;
+            int64_t issued = 0;
+            bool ok = true;
+            int64_t step = 0;
+            bool waited = false;
+            for (int64_t u = pair; ok && u >= 0 && u < up.units;) {
+                const Unit un = decode_unit(up, u, nkb);
+                int bt, mb, nb;
+                batch_tile_coords(un.tile, p, bt, mb, nb);
+                if (!waited) {
+                    griddep_wait();
+                    waited = true;
+                }
+                if (tick) {
+                    const int slot = (int)(step % C::SLOTS);
+                    mbar_arrive_expect_tx(bar(C::TKF0 + slot), 16);
+                    if (leader) {
+                        if (step >= C::SLOTS &&
+                            !pair_wait(bar(C::TKE0 + slot),
+                                       (uint32_t)(((step / C::SLOTS) - 1) & 1), ctl, SITE_SCHED)) {
+                            ok = false;
+                            break;
+                        }
+                        const uint32_t v = atomicAdd(p.ticket, 1u);
+                        int64_t next = num_pairs + (int64_t)v;
+                        if (next >= up.units) {
+                            next = -1;
+                            if ((int64_t)v == up.units - 1) atomicExch(p.ticket, 0u);
+                        }
+                        volatile int64_t *stg =
+                            reinterpret_cast<volatile int64_t *>(smem + C::TICKET_OFF + 16 * slot);
+                        stg[0] = next;
+                        stg[1] = 0;
+                        fence_proxy_async_smem();
+                        const uint32_t src = sbase + C::TICKET_OFF + 16 * slot;
+                        const uint32_t dst = sbase + C::TK_OFF + 16 * slot;
+                        const uint32_t fb = bar(C::TKF0 + slot);
+                        bulk_copy_s2cluster(map_shared_rank(dst, 0), src, 16,
+                                            map_shared_rank(fb, 0));
+                        bulk_copy_s2cluster(map_shared_rank(dst, 1), src, 16,
+                                            map_shared_rank(fb, 1));
+                    }
+                }
+                const int32_t arow = mb * C::PAIR_M + (int32_t)rank * BLOCK_M;
+                const int32_t brow =
+                    C::DUAL ? nb * C::OUT_N : nb * BN + (int32_t)rank * C::B_ROWS;
+                const bool down = p.k_snake && ((un.tile / num_pairs) & 1);
+                for (int i = 0; i < un.k1 - un.k0; ++i) {
+                    const int kb = down ? un.k1 - 1 - i : un.k0 + i;
+                    const bool second = kb >= mp.k_blocks0;
+                    const int32_t kc = (second ? kb - mp.k_blocks0 : kb) * C::BK;
+                    const CUtensorMap *ma = &maps.a[second || bt ? 1 : 0];
+                    const CUtensorMap *mb_ = &maps.b[(C::DUAL ? rank != 0 : second) ? 1 : 0];
+                    if (!pair_wait(bar(C::EMPTY0 + s), ph ^ 1, ctl, SITE_EMPTY)) { ok = false; break; }
+                    const uint32_t full = map_shared_rank(bar(C::FULL0 + s), 0);
+                    if (leader) mbar_arrive_expect_tx(bar(C::FULL0 + s), 2 * (C::A_BYTES + C::B_BYTES));
+                    if constexpr (AM == 0) {
+                        tma_load_2d_pair(a_stage(s), ma, full, kc, arow);
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < BLOCK_M / 64; ++q)
+                            tma_load_2d_pair(a_stage(s) + q * 8192, ma, full, arow + q * 64, kc);
+                    }
+                    if constexpr (BM == 0) {
+                        tma_load_2d_pair(b_stage(s), mb_, full, kc, brow);
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < C::B_ROWS / 64; ++q)
+                            tma_load_2d_pair(b_stage(s) + q * 8192, mb_, full, brow + q * 64, kc);
+                    }
+                    ++issued;
+                    if (++s == S) { s = 0; ph ^= 1; }
+                }
+                if (!ok) break;
+                u = tick ? tk_read(step++) : u + num_pairs;
+            }
+            // Copies already issued land within microseconds; their barriers
+            // may be the peer's, which this thread cannot poll.
+            if (!ok && issued) pair_pause_ns(200000);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ------------------------------------------------------ MMA issuer (leader)
+        griddep_wait();
+        if (leader && lane == 0) {
+            int s = 0;
+            uint32_t ph = 0;
+            uint32_t tl = 0;
+            bool ok = true;
+            int64_t step = 0;
+            for (int64_t u = pair; ok && u >= 0 && u < up.units; ++tl) {
+                const Unit un = decode_unit(up, u, nkb);
+                const uint32_t acc = tl & 1, use = tl >> 1;
+                if (!pair_wait(bar(C::ACCE0 + acc), (use & 1) ^ 1, ctl, SITE_ACC_EMPTY)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t d_tmem = tmem_base + acc * BN;
+                for (int i = 0; i < un.k1 - un.k0; ++i) {
+                    if (!pair_wait(bar(C::FULL0 + s), ph, ctl, SITE_FULL)) { ok = false; break; }
+                    tc_fence_after();
+                    const uint32_t a0 = a_stage(s), b0 = b_stage(s);
+#pragma unroll
+                    for (int kk = 0; kk < C::MMAS_PER_STAGE; ++kk) {
+                        // 16 reduction indexes: 32 bytes of a K-major row, 16
+                        // rows of 128 bytes of an MN-major box.
+                        const uint64_t ad = AM ? smem_desc_mn_sw128(a0 + kk * 2048)
+                                               : smem_desc_sw128(a0 + kk * 32);
+                        const uint64_t bd = BM ? smem_desc_mn_sw128(b0 + kk * 2048)
+                                               : smem_desc_sw128(b0 + kk * 32);
+                        mma_f16_pair(d_tmem, ad, bd, C::IDESC, (i != 0) || (kk != 0));
+                    }
+                    mma_commit_pair_mcast(bar(C::EMPTY0 + s), (uint16_t)0x3);
+                    if (++s == S) { s = 0; ph ^= 1; }
+                }
+                if (!ok) break;
+                mma_commit_pair_mcast(bar(C::ACCF0 + acc), (uint16_t)0x3);
+                u = tick ? tk_read(step++) : u + num_pairs;
+            }
+            if (!ok) {
+                mma_commit_pair_mcast(bar(C::DRAIN), (uint16_t)1);
+                const uint64_t t0 = globaltimer_ns();
+                while (!mbar_try_wait(bar(C::DRAIN), 0)) {
+                    if (globaltimer_ns() - t0 > p.wait_limit_ns) {
+                        atomicCAS(p.status, 0u, (uint32_t)SITE_DRAIN);
+                        break;
+                    }
+                }
+            }
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------ epilogue (both CTAs)
+        griddep_wait();
+        const int q = warp & 3;
+        const int ew = warp - 2;
+        constexpr int EPI_THREADS = C::EPI_WARPS * 32;
+        const int etid = threadIdx.x - 64;
+        constexpr int COLS = C::COLS;
+        constexpr int CW = C::STG_ROW / 2;  // 16-bit columns of a staged row
+        const int cbase = (ew / 4) * COLS;
+        uint8_t *stg = smem + C::STG_OFF + ew * C::STG_BYTES;
+        const uint32_t stg_s = smem_u32(stg);
+        uint32_t res_phase = 0;
+        uint32_t tl = 0;
+        int64_t step = 0;
+        bool alive = true;
+        for (int64_t u = pair;; ++tl) {
+            // With split tiles the epilogue warps meet on named barriers, so
+            // they leave together: a warp whose wait gave up takes all along.
+            if (up.segs > 1 ? named_bar_any(2, EPI_THREADS, u == -2 || !alive)
+                            : (u == -2 || !alive))
+                break;
+            if (u < 0 || u >= up.units) break;
+            const Unit un = decode_unit(up, u, nkb);
+            int bt, mb, nb;
+            batch_tile_coords(un.tile, p, bt, mb, nb);
+            const uint32_t acc = tl & 1, use = tl >> 1;
+            const int32_t row0 = mb * C::PAIR_M + (int32_t)rank * BLOCK_M + q * 32;
+            const int32_t colw = nb * C::OUT_N + cbase;  // first output column of this warp
+            const bool writer = un.seg >= 0 && un.seg < up.segs - 1;
+            const bool finisher = un.seg >= 0 && !writer;
+
+            // Ask for the first residual box while the MMAs still run.
+            auto ask_residual = [&](int32_t col) {
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    bulk_wait_read();
+                    mbar_arrive_expect_tx(bar(C::RES0 + ew), C::STG_BYTES);
+                    tma_load_2d(stg_s, &maps.r, bar(C::RES0 + ew), col, row0);
+                }
+            };
+            bool asked = false;
+            if constexpr (EP == MlpEpi::LINEAR) {
+                // Z goes through the same buffer first when it is saved.
+                if (mp.r && mp.r_tma && !mp.out[1].ptr && !writer && row0 < p.m && colw < p.n) {
+                    ask_residual(colw);
+                    asked = true;
+                }
+            }
+
+            const bool got = pair_wait(bar(C::ACCF0 + acc), use & 1, ctl, SITE_ACC_FULL);
+            if (up.segs > 1 ? named_bar_any(2, EPI_THREADS, !got) : !__all_sync(0xffffffffu, got)) {
+                alive = false;
+            }
+            if (!alive) {
+                if (asked) pair_pause_ns(200000);  // the box may still be landing
+                break;
+            }
+            tc_fence_after();
+            const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + acc * BN;
+            auto part = [&](int32_t k) -> float * {
+                const int64_t pidx = un.tail * (up.segs - 1) + k;
+                return p.ws + ((pidx * 2 + rank) * BN) * (int64_t)BLOCK_M + q * 32 + lane;
+            };
+            auto flag = [&](int32_t k) -> uint32_t * {
+                return p.flags + (un.tail * (up.segs - 1) + k) * 2 + rank;
+            };
+            if (writer) {
+                float *dst = part(un.seg);
+                constexpr int ACOLS = BN / 2;
+                const int a0 = (ew / 4) * ACOLS;
+#pragma unroll 1
+                for (int c0 = a0; c0 < a0 + ACOLS; c0 += 32) {
+                    uint32_t v[32];
+                    tmem_ld_32x32b_x32(taddr + c0, v);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        __stcg(dst + (int64_t)(c0 + j) * BLOCK_M, __uint_as_float(v[j]));
+                }
+                __threadfence();
+                named_bar_sync(1, EPI_THREADS);
+                if (etid == 0) st_release_gpu_u32(flag(un.seg), 1u);
+            } else {
+                bool ready = true;
+                if (finisher) {
+                    if (etid == 0) {
+                        const uint64_t t0 = globaltimer_ns();
+                        for (int32_t k = 0; k < up.segs - 1 && ready; ++k) {
+                            while (ld_acquire_gpu_u32(flag(k)) == 0u) {
+                                if (*abort_flag || globaltimer_ns() - t0 > p.wait_limit_ns) {
+                                    if (!*abort_flag) pair_raise_abort(ctl, SITE_PARTIAL);
+                                    ready = false;
+                                    break;
+                                }
+                            }
+                        }
+                        *fin_ready = ready ? 1 : 0;
+                    }
+                    named_bar_sync(1, EPI_THREADS);
+                    ready = *fin_ready != 0;
+                    if (ready)
+                        for (int32_t k = 0; k < up.segs - 1; ++k) (void)ld_acquire_gpu_u32(flag(k));
+                }
+                // 32 accumulator columns of this thread's row (plus the other
+                // segments' partial sums, in segment order).
+                auto load_acc = [&](int c0, float (&y)[32]) {
+                    if (nkb == 0) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) y[j] = 0.0f;
+                        return;
+                    }
+                    uint32_t v[32];
+                    tmem_ld_32x32b_x32(taddr + c0, v);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) y[j] = __uint_as_float(v[j]);
+                    if (finisher) {
+                        for (int32_t k = 0; k < up.segs - 1; ++k) {
+                            const float *src = part(k) + (int64_t)c0 * BLOCK_M;
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) y[j] += __ldcg(src + (int64_t)j * BLOCK_M);
+                        }
+                    }
+                };
+                auto stg16 = [&](int piece) -> uint4 * {
+                    return reinterpret_cast<uint4 *>(stg + stg_offset<C::STG_ROW>(lane, piece * 16));
+                };
+                auto free_stg = [&]() {
+                    if (lane == 0) bulk_wait_read();
+                    __syncwarp();
+                };
+                // The staged box goes out as columns col.. of output o.
+                auto send = [&](int o, int32_t col) {
+                    const int wide = EP == MlpEpi::PLAIN && mp.out_f32 ? C::STG_ROW / 4 : CW;
+                    if (mp.out[o].tma && (mp.clip || col + wide <= p.n)) {
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            tma_store_2d(&maps.out[o], stg_s, col, row0);
+                            bulk_commit();
+                        }
+                    } else {
+                        __syncwarp();
+                        if (EP == MlpEpi::PLAIN && mp.out_f32)
+                            stg_to_global<C::STG_ROW, float>(stg, static_cast<float *>(mp.out[o].ptr),
+                                                 mp.out[o].ld, row0, col, p.m, p.n, lane);
+                        else
+                            stg_to_global<C::STG_ROW, uint16_t>(stg, static_cast<uint16_t *>(mp.out[o].ptr),
+                                                    mp.out[o].ld, row0, col, p.m, p.n, lane);
+                        __syncwarp();
+                    }
+                };
+                // Pack 32 values as half `h` of a 64-column 16-bit row.
+                auto put = [&](int h, const float (&y)[32]) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        *stg16(h * 4 + j) = make_uint4(mlp_pack2<KD>(y[8 * j], y[8 * j + 1]),
+                                                       mlp_pack2<KD>(y[8 * j + 2], y[8 * j + 3]),
+                                                       mlp_pack2<KD>(y[8 * j + 4], y[8 * j + 5]),
+                                                       mlp_pack2<KD>(y[8 * j + 6], y[8 * j + 7]));
+                };
+                const bool rows_in = ready && row0 < p.m;
+                if constexpr (EP == MlpEpi::LINEAR) {
+                    auto add_bias = [&](int32_t col, float (&y)[32]) {
+                        if (mp.bias) {
+                            const float b = col + lane < p.n ? __ldg(mp.bias + col + lane) : 0.0f;
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) y[j] += __shfl_sync(0xffffffffu, b, j);
+                        }
+                    };
+#pragma unroll 1
+                    for (int c = 0; c < COLS && rows_in && colw + c < p.n; c += CW) {
+                        const int32_t col = colw + c;
+                        if (mp.out[1].ptr) {
+                            free_stg();
+#pragma unroll 1
+                            for (int h = 0; h < CW / 32; ++h) {
+                                float y[32];
+                                load_acc(cbase + c + h * 32, y);
+                                add_bias(col + h * 32, y);
+                                put(h, y);
+                            }
+                            send(1, col);
+                        }
+                        if (mp.r && mp.r_tma) {
+                            if (!asked) ask_residual(col);
+                            asked = false;
+                            const bool landed =
+                                pair_wait(bar(C::RES0 + ew), res_phase, ctl, SITE_RESIDUAL);
+                            res_phase ^= 1;
+                            if (!__all_sync(0xffffffffu, landed)) {
+                                pair_pause_ns(200000);
+                                alive = false;
+                                break;
+                            }
+                        } else {
+                            free_stg();
+                            if (mp.r) {
+                                global_to_stg<C::STG_ROW>(stg, static_cast<const uint16_t *>(mp.r), mp.ldr, row0,
+                                              col, p.m, p.n, lane);
+                                __syncwarp();
+                            }
+                        }
+#pragma unroll 1
+                        for (int h = 0; h < CW / 32; ++h) {
+                            float y[32];
+                            load_acc(cbase + c + h * 32, y);
+                            add_bias(col + h * 32, y);
+                            if (mp.act != MLP_NONE) {
+#pragma unroll
+                                for (int j = 0; j < 32; ++j) y[j] = mlp_act(mp.act, y[j]);
+                            }
+                            if (mp.r) {
+#pragma unroll
+                                for (int j = 0; j < 4; ++j) {
+                                    const uint4 w = *stg16(h * 4 + j);
+                                    const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e) {
+                                        y[8 * j + 2 * e] += mlp_to_float<KD>(ws[e] & 0xffffu);
+                                        y[8 * j + 2 * e + 1] += mlp_to_float<KD>(ws[e] >> 16);
+                                    }
+                                }
+                            }
+                            put(h, y);
+                        }
+                        send(0, col);
+                    }
+                } else if constexpr (EP == MlpEpi::GATED) {
+                    constexpr int UP = BN / 2;  // accumulator column of the up half
+#pragma unroll 1
+                    for (int c = 0; c < COLS && rows_in && colw + c < p.n; c += CW) {
+                        const int32_t col = colw + c;
+#pragma unroll 1
+                        for (int o = 1; o < 3; ++o) {
+                            if (!mp.out[o].ptr) continue;
+                            free_stg();
+#pragma unroll 1
+                            for (int h = 0; h < CW / 32; ++h) {
+                                float y[32];
+                                load_acc((o - 1) * UP + cbase + c + h * 32, y);
+                                put(h, y);
+                            }
+                            send(o, col);
+                        }
+                        free_stg();
+#pragma unroll 1
+                        for (int h = 0; h < CW / 32; ++h) {
+                            float y[32], w[32];
+                            load_acc(cbase + c + h * 32, y);
+                            load_acc(UP + cbase + c + h * 32, w);
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) y[j] = mlp_act(mp.act, y[j]) * w[j];
+                            put(h, y);
+                        }
+                        send(0, col);
+                    }
+                } else {
+                    const int cw = mp.out_f32 ? CW / 2 : CW;
+#pragma unroll 1
+                    for (int c = 0; c < COLS && rows_in && colw + c < p.n; c += cw) {
+                        free_stg();
+#pragma unroll 1
+                        for (int h = 0; h < cw / 32; ++h) {
+                            float y[32];
+                            load_acc(cbase + c + h * 32, y);
+                            if (mp.out_f32) {
+#pragma unroll
+                                for (int j = 0; j < 8; ++j)
+                                    *stg16(j) = make_uint4(
+                                        __float_as_uint(y[4 * j]), __float_as_uint(y[4 * j + 1]),
+                                        __float_as_uint(y[4 * j + 2]), __float_as_uint(y[4 * j + 3]));
+                            } else {
+                                put(h, y);
+                            }
+                        }
+                        send(bt, colw + c);
+                    }
+                }
+                if (finisher) {
+                    named_bar_sync(1, EPI_THREADS);
+                    if (etid == 0 && ready)
+                        for (int32_t k = 0; k < up.segs - 1; ++k) *flag(k) = 0u;
+                }
+            }
+            if (asked) pair_pause_ns(200000);  // an unread box (the finisher gave up): let it land
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if (leader) mbar_arrive(bar(C::ACCE0 + acc));
+                else mbar_arrive_cluster_relaxed(map_shared_rank(bar(C::ACCE0 + acc), 0));
+            }
+            u = tick ? tk_read_warp(step++) : u + num_pairs;
+        }
+        if (lane == 0) bulk_wait_all();
+    }
+
+    tc_fence_before();
+    cluster_sync_all();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem_base, C::TMEM_COLS);
+    }
+}
+
+}  // namespace tg

@@ -392,6 +392,136 @@ tg_status tg_gemm_mx_batched(int64_t M, int64_t N, int64_t K, float alpha,
                              const tg_epi_op *ops, int32_t n_ops,
                              const tg_options *opts, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Feed-forward operators: a transformer block's linear layer, gated unit and
+ * layer norm, forward and backward.
+ *
+ * Layout: every matrix is row-major (tokens are rows) with its own leading
+ * stride in elements, at least its column count; stride padding is neither
+ * read nor written.  X is (M, K): M tokens of K features; weights are (N, K);
+ * activations and their gradients (M, N).  dtype is TG_BF16 or TG_FP16 for the
+ * products (FP32 accumulation), and any tg_out_dtype for the layer norm.
+ * bias, gamma, beta, the statistics and the gradients of these vectors are
+ * FP32.  Matrices must be aligned to their element size, FP32 vectors to 4
+ * bytes.  Bases or row strides that are not multiples of 16 bytes are not
+ * errors: an operand is then copied to aligned rows in the workspace, an
+ * output stored element by element.
+ *
+ * Workspace: device memory of the caller, 16-byte aligned, at least as many
+ * bytes as the call's *_workspace_bytes query returns for the same arguments
+ * (-1 there: invalid arguments or no device; 0: NULL is fine).  Its contents
+ * need no initialisation and are free again once the call's work is done; two
+ * calls that may overlap on the GPU must not share one.  The products also use
+ * the library's workspace of the stream (see the top of this file: its first
+ * allocation synchronises the device, so make one call of each operator on
+ * the stream before capturing it).
+ *
+ * Ownership, asynchrony and errors are tg_gemm's: everything is enqueued on
+ * `stream`, arguments are checked before anything is launched, and repeated
+ * calls give bitwise identical results.  An output may not overlap an input
+ * unless the call says so.  M, N, K < 2^31 - 512.
+ */
+typedef enum {
+    TG_ACT_NONE = 0,      /* y */
+    TG_ACT_RELU = 1,      /* max(y, 0); derivative 0 at 0 */
+    TG_ACT_SILU = 2,      /* y / (1 + exp(-y)) */
+    TG_ACT_GELU_TANH = 3  /* y/2 (1 + tanh(sqrt(2/pi) (y + 0.044715 y^3))) */
+} tg_activation;
+
+/*
+ * Linear layer:  Z = X W^T + bias,  Y = act(Z) + R, rounded once to dtype.
+ * bias (N floats), R (M x N) and Z (M x N, the pre-activation that the
+ * backward pass reads) may be NULL: no bias, no residual, Z not stored.  Y may
+ * be R itself (same pointer and stride: the residual stream updated in place).
+ * K == 0 gives act(bias) + R; M == 0 or N == 0 launches nothing.
+ */
+int64_t tg_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, const void *X, int64_t ldx,
+                                  const void *W, int64_t ldw, tg_dtype dtype);
+tg_status tg_linear(int64_t M, int64_t N, int64_t K, const void *X, int64_t ldx,
+                    const void *W, int64_t ldw, const float *bias, tg_activation act,
+                    const void *R, int64_t ldr, void *Y, int64_t ldy, void *Z, int64_t ldz,
+                    tg_dtype dtype, void *workspace, int64_t workspace_bytes, void *stream);
+
+/*
+ * Gradients of the linear layer, from dY (M x N):
+ *   dZ = dY act'(Z),  dX = dZ W,  dW = dZ^T X,  db[n] = sum over m of dZ[m, n]
+ * (the residual's gradient is dY itself).  Z is read when act is not
+ * TG_ACT_NONE.  dX, dW and db may each be NULL (not wanted); X is read for dW
+ * only, W for dX only.  dW is stored as dw_dtype: dtype's own format or
+ * TG_OUT_F32.  dZ is rounded to dtype where the products read it; db sums it
+ * unrounded.  Empty reductions give zeros.
+ */
+int64_t tg_linear_backward_workspace_bytes(int64_t M, int64_t N, int64_t K, const void *dY,
+                                           int64_t lddy, const void *X, int64_t ldx,
+                                           const void *W, int64_t ldw, tg_activation act,
+                                           tg_dtype dtype);
+tg_status tg_linear_backward(int64_t M, int64_t N, int64_t K, const void *dY, int64_t lddy,
+                             const void *X, int64_t ldx, const void *W, int64_t ldw,
+                             const void *Z, int64_t ldz, tg_activation act,
+                             void *dX, int64_t lddx, void *dW, int64_t lddw,
+                             tg_out_dtype dw_dtype, float *db, tg_dtype dtype,
+                             void *workspace, int64_t workspace_bytes, void *stream);
+
+/*
+ * Gated unit:  G = X Wg^T,  U = X Wu^T,  H = act(G) * U, in one kernel.  G and
+ * U (M x N) are stored, rounded to dtype, unless NULL; H is computed from the
+ * unrounded FP32 values.  K == 0 gives zeros.
+ */
+int64_t tg_gated_workspace_bytes(int64_t M, int64_t N, int64_t K, const void *X, int64_t ldx,
+                                 const void *Wg, int64_t ldwg, const void *Wu, int64_t ldwu,
+                                 tg_dtype dtype);
+tg_status tg_gated(int64_t M, int64_t N, int64_t K, const void *X, int64_t ldx,
+                   const void *Wg, int64_t ldwg, const void *Wu, int64_t ldwu,
+                   tg_activation act, void *H, int64_t ldh, void *G, int64_t ldg,
+                   void *U, int64_t ldu, tg_dtype dtype,
+                   void *workspace, int64_t workspace_bytes, void *stream);
+
+/*
+ * Gradients of the gated unit, from dH, G and U (M x N):
+ *   dG = dH U act'(G),  dU = dH act(G),
+ *   dX = dG Wg + dU Wu,  dWg = dG^T X,  dWu = dU^T X
+ * dX, dWg and dWu may each be NULL.  dG and dU are rounded to dtype where the
+ * products read them; dWg and dWu are stored as dw_dtype (as above).
+ */
+int64_t tg_gated_backward_workspace_bytes(int64_t M, int64_t N, int64_t K, const void *X,
+                                          int64_t ldx, const void *Wg, int64_t ldwg,
+                                          const void *Wu, int64_t ldwu, tg_dtype dtype);
+tg_status tg_gated_backward(int64_t M, int64_t N, int64_t K, const void *dH, int64_t lddh,
+                            const void *X, int64_t ldx, const void *Wg, int64_t ldwg,
+                            const void *Wu, int64_t ldwu, const void *G, int64_t ldg,
+                            const void *U, int64_t ldu, tg_activation act,
+                            void *dX, int64_t lddx, void *dWg, int64_t lddwg,
+                            void *dWu, int64_t lddwu, tg_out_dtype dw_dtype, tg_dtype dtype,
+                            void *workspace, int64_t workspace_bytes, void *stream);
+
+/*
+ * Layer norm over each row of X (M x N):
+ *   mean = sum x / N,  rstd = 1 / sqrt(sum (x - mean)^2 / N + eps),
+ *   Y = (X - mean) rstd gamma + beta
+ * gamma and beta (N floats) may be NULL (ones, zeros); mean and rstd (M
+ * floats, what the backward pass reads) are stored unless NULL.  Y may be X
+ * itself (same pointer and stride).  N <= 65536 (TG_ERR_UNSUPPORTED beyond);
+ * N == 0 with M > 0 is an error.
+ */
+tg_status tg_layer_norm(int64_t M, int64_t N, const void *X, int64_t ldx, const float *gamma,
+                        const float *beta, float eps, void *Y, int64_t ldy, float *mean,
+                        float *rstd, tg_out_dtype dtype, void *stream);
+
+/*
+ * Gradients of the layer norm, from dY (M x N) and the forward's mean, rstd:
+ *   xh = (X - mean) rstd,  a = dY gamma,
+ *   dX = rstd (a - sum a / N - xh sum (a xh) / N),
+ *   dgamma = sum over rows of dY xh,  dbeta = sum over rows of dY
+ * dX, dgamma and dbeta may each be NULL; dX may be dY itself.  M == 0 gives
+ * zero sums.
+ */
+int64_t tg_layer_norm_backward_workspace_bytes(int64_t M, int64_t N);
+tg_status tg_layer_norm_backward(int64_t M, int64_t N, const void *dY, int64_t lddy,
+                                 const void *X, int64_t ldx, const float *gamma,
+                                 const float *mean, const float *rstd, void *dX, int64_t lddx,
+                                 float *dgamma, float *dbeta, tg_out_dtype dtype,
+                                 void *workspace, int64_t workspace_bytes, void *stream);
+
 /* Static text for a status code ("TG_OK", ...); never NULL. */
 const char *tg_status_string(tg_status status);
 
