@@ -39,64 +39,74 @@
 #pragma once
 
 #include <cstdint>
+#include <type_traits>
 #include "tg_kernel_pair.cuh"
 
 namespace tg {
 
 enum MlpAct : int32_t { MLP_NONE = 0, MLP_RELU = 1, MLP_SILU = 2, MLP_GELU = 3, MLP_ACTS = 4 };
 
-// 1 / (1 + exp(-x)) by the hardware's exponential and reciprocal: relative
-// error about 2^-21 for the |x| that matter, far below a 16-bit output's
-// 2^-9, and below the 1e-6 that an FP32 column sum over it is held to.
-// exp(-x) = inf for x < -88 gives 0, the limit.
-__device__ __forceinline__ float mlp_sigmoid(float x) {
-    return __fdividef(1.0f, 1.0f + __expf(-x));
+// The activations and their derivatives all come from one logistic function,
+// sigmoid(v) = 1 / (1 + 2^(-v log2 e)), by the hardware's base-2 exponential
+// and reciprocal: relative error about 2^-21 for the |v| that matter, far
+// below a 16-bit output's 2^-9, and below the 1e-6 that an FP32 column sum over
+// it is held to.  2^(-v log2 e) = inf for large negative v gives 0, the limit.
+constexpr float kLog2E = 1.4426950408889634f;
+__device__ __forceinline__ float mlp_sigmoid_2(float u) {  // u = -v log2 e
+    float e, s;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(u));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.0f + e));
+    return s;
 }
 
 // The tanh form of GELU is y/2 (1 + tanh(v)) = y sigmoid(2v), v =
 // sqrt(2/pi) (y + 0.044715 y^3): no cancellation in 1 + tanh(v) for negative
-// v.  |y| is held to 16 inside the argument (there sigmoid is 0 or 1 to all
-// FP32 digits), which keeps y^3 and the gradient's product finite.
+// v.  y^2 is held to 256 inside the argument (for |y| >= 16 sigmoid is 0 or 1
+// to all FP32 digits), which keeps it and the derivative's product finite.
 constexpr float kGelu2C = 1.5957691216057308f;  // 2 sqrt(2/pi)
-__device__ __forceinline__ float mlp_gelu_arg(float y) {
-    return y < -16.0f ? -16.0f : (y > 16.0f ? 16.0f : y);  // NaN stays
+__device__ __forceinline__ float mlp_gelu_sigmoid(float y, float y2) {
+    return mlp_sigmoid_2(y * fmaf(-kLog2E * kGelu2C * 0.044715f, y2, -kLog2E * kGelu2C));
 }
 
-__device__ __forceinline__ float mlp_act(int act, float y) {
-    switch (act) {
-    case MLP_RELU: return (!(y > 0.0f) && !(y != y)) ? 0.0f : y;
-    case MLP_SILU: return y * mlp_sigmoid(y);
-    case MLP_GELU: {
-        const float t = mlp_gelu_arg(y);
-        return y * mlp_sigmoid(kGelu2C * (t + 0.044715f * t * t * t));
-    }
-    default: return y;
-    }
+template <int ACT>
+__device__ __forceinline__ float mlp_act(float y) {
+    if constexpr (ACT == MLP_RELU) return (!(y > 0.0f) && !(y != y)) ? 0.0f : y;
+    else if constexpr (ACT == MLP_SILU) return y * mlp_sigmoid_2(-kLog2E * y);
+    else if constexpr (ACT == MLP_GELU) return y * mlp_gelu_sigmoid(y, fminf(y * y, 256.0f));
+    else return y;
 }
 
 // Activation and its derivative.  ReLU'(0) = 0.
-__device__ __forceinline__ void mlp_act_grad(int act, float y, float &a, float &d) {
-    switch (act) {
-    case MLP_RELU: {
+template <int ACT>
+__device__ __forceinline__ void mlp_act_grad(float y, float &a, float &d) {
+    if constexpr (ACT == MLP_RELU) {
         const bool on = y > 0.0f || y != y;
         a = on ? y : 0.0f;
         d = on ? 1.0f : 0.0f;
-        return;
-    }
-    case MLP_SILU: {
-        const float s = mlp_sigmoid(y);
+    } else if constexpr (ACT == MLP_SILU) {
+        const float s = mlp_sigmoid_2(-kLog2E * y);
         a = y * s;
-        d = s + a * (1.0f - s);
-        return;
-    }
-    case MLP_GELU: {
-        const float t = mlp_gelu_arg(y);
-        const float s = mlp_sigmoid(kGelu2C * (t + 0.044715f * t * t * t));
+        d = fmaf(a, 1.0f - s, s);
+    } else if constexpr (ACT == MLP_GELU) {
+        const float y2 = fminf(y * y, 256.0f);
+        const float s = mlp_gelu_sigmoid(y, y2);
         a = y * s;
-        d = s + t * s * (1.0f - s) * kGelu2C * (1.0f + 0.134145f * t * t);
-        return;
+        d = fmaf(a * (1.0f - s), fmaf(kGelu2C * 0.134145f, y2, kGelu2C), s);
+    } else {
+        a = y;
+        d = 1.0f;
     }
-    default: a = y; d = 1.0f; return;
+}
+
+// f(integral constant of the activation) for a runtime one: the branch is
+// taken once around a loop, not per element.
+template <class F>
+__device__ __forceinline__ void mlp_with_act(int act, F f) {
+    switch (act) {
+    case MLP_RELU: f(std::integral_constant<int, MLP_RELU>{}); return;
+    case MLP_SILU: f(std::integral_constant<int, MLP_SILU>{}); return;
+    case MLP_GELU: f(std::integral_constant<int, MLP_GELU>{}); return;
+    default: f(std::integral_constant<int, MLP_NONE>{}); return;
     }
 }
 
@@ -687,10 +697,10 @@ __global__ void __launch_bounds__(MlpConfig<KD, BN, AM, BM, EP>::NUM_THREADS, 1)
                             float y[32];
                             load_acc(cbase + c + h * 32, y);
                             add_bias(col + h * 32, y);
-                            if (mp.act != MLP_NONE) {
+                            mlp_with_act(mp.act, [&](auto a) {
 #pragma unroll
-                                for (int j = 0; j < 32; ++j) y[j] = mlp_act(mp.act, y[j]);
-                            }
+                                for (int j = 0; j < 32; ++j) y[j] = mlp_act<a.value>(y[j]);
+                            });
                             if (mp.r) {
 #pragma unroll
                                 for (int j = 0; j < 4; ++j) {
@@ -730,8 +740,10 @@ __global__ void __launch_bounds__(MlpConfig<KD, BN, AM, BM, EP>::NUM_THREADS, 1)
                             float y[32], w[32];
                             load_acc(cbase + c + h * 32, y);
                             load_acc(UP + cbase + c + h * 32, w);
+                            mlp_with_act(mp.act, [&](auto a) {
 #pragma unroll
-                            for (int j = 0; j < 32; ++j) y[j] = mlp_act(mp.act, y[j]) * w[j];
+                                for (int j = 0; j < 32; ++j) y[j] = mlp_act<a.value>(y[j]) * w[j];
+                            });
                             put(h, y);
                         }
                         send(0, col);

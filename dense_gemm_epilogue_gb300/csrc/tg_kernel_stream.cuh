@@ -322,8 +322,10 @@ __global__ void __launch_bounds__(StreamConfig<KD, NT, DUAL>::NUM_THREADS, 1)
                         load_acc(NT + j0, j0, w);
                         if (p.out[1].ptr) store(1, j0, y);
                         if (p.out[2].ptr) store(2, j0, w);
+                        mlp_with_act(p.act, [&](auto a) {
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) y[j] = mlp_act(p.act, y[j]) * w[j];
+                            for (int j = 0; j < 16; ++j) y[j] = mlp_act<a.value>(y[j]) * w[j];
+                        });
                     } else {
                         uint16_t rr[16];
                         if (p.r) {
@@ -336,10 +338,10 @@ __global__ void __launch_bounds__(StreamConfig<KD, NT, DUAL>::NUM_THREADS, 1)
 #pragma unroll
                         for (int j = 0; j < 16; ++j) y[j] += b;
                         if (p.out[1].ptr) store(1, j0, y);
-                        if (p.act != MLP_NONE) {
+                        mlp_with_act(p.act, [&](auto a) {
 #pragma unroll
-                            for (int j = 0; j < 16; ++j) y[j] = mlp_act(p.act, y[j]);
-                        }
+                            for (int j = 0; j < 16; ++j) y[j] = mlp_act<a.value>(y[j]);
+                        });
                         if (p.r) {
 #pragma unroll
                             for (int j = 0; j < 16; ++j) y[j] += mlp_to_float<KD>(rr[j]);

@@ -38,46 +38,97 @@ struct ActParams {
     float *partial;     // [gridDim.y][n] or NULL
 };
 
+// Eight values of a row: consecutive ones from column c (16 bytes), or with
+// VEC false the values at c, c + 32, ... (c = the lane's first column).
 template <class Ty, bool VEC>
 struct ActRow {
-    float v[8];
-    // Lane columns: 8 consecutive ones (VEC), or 32 apart.
-    __device__ __forceinline__ static int64_t col(int64_t c0, int lane, int i) {
-        return VEC ? c0 + lane * 8 + i : c0 + lane + 32 * i;
-    }
-    __device__ __forceinline__ void load(const void *base, int64_t r, int64_t ld, int64_t c0,
-                                         int lane, int64_t n) {
-        const typename Ty::T *row = static_cast<const typename Ty::T *>(base) + r * ld;
-        if constexpr (VEC) {
-            const int64_t c = c0 + lane * 8;
-            const uint4 w = c < n ? row_load<Ty>(row, c, n) : make_uint4(0, 0, 0, 0);
-            row_unpack<Ty>(w, v);
-        } else {
+    __device__ __forceinline__ static int first(int lane) { return VEC ? lane * 8 : lane; }
+    __device__ __forceinline__ static int col(int lane, int i) { return VEC ? lane * 8 + i : lane + 32 * i; }
+    // Any columns, bounds checked.
+    __device__ __forceinline__ static void load(const typename Ty::T *row, int64_t c, int64_t n,
+                                                float (&v)[8]) {
+        constexpr int STEP = VEC ? 1 : 32;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int64_t c = col(c0, lane, i);
-                v[i] = c < n ? Ty::up(row[c]) : 0.0f;
-            }
-        }
+        for (int i = 0; i < 8; ++i) v[i] = c + STEP * i < n ? Ty::up(row[c + STEP * i]) : 0.0f;
     }
-    __device__ __forceinline__ void store(void *base, int64_t r, int64_t ld, int64_t c0, int lane,
-                                          int64_t n) const {
-        typename Ty::T *row = static_cast<typename Ty::T *>(base) + r * ld;
-        if constexpr (VEC) {
-            const int64_t c = c0 + lane * 8;
-            if (c < n) row_store<Ty>(row, c, n, v);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int64_t c = col(c0, lane, i);
-                if (c < n) row[c] = Ty::down(v[i]);
-            }
+    __device__ __forceinline__ static void store(typename Ty::T *row, int64_t c, int64_t n,
+                                                 const float (&v)[8]) {
+        if (VEC && c + 8 <= n) {
+            row_store<Ty>(row, c, n, v);
+            return;
         }
+        constexpr int STEP = VEC ? 1 : 32;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (c + STEP * i < n) row[c + STEP * i] = Ty::down(v[i]);
     }
 };
 
+// One block's band.  INSIDE: 16-byte vectors that all lie inside the rows, so
+// that the loads of FLY rows leave together; rows past the band load its last
+// row again and are dropped.
+template <class Ty, bool VEC, bool GATED, int ACT, bool INSIDE>
+__device__ __forceinline__ void act_band(const ActParams &p, int64_t c, int64_t r0, int64_t r1,
+                                         float (&s)[8]) {
+    using T = typename Ty::T;
+    using Row = ActRow<Ty, VEC>;
+    const T *dy = static_cast<const T *>(p.dy), *z = static_cast<const T *>(p.z);
+    const T *u = static_cast<const T *>(p.u);
+    T *o0 = static_cast<T *>(p.out0), *o1 = static_cast<T *>(p.out1);
+    constexpr bool READ_Z = GATED || ACT != MLP_NONE;
+    constexpr int FLY = INSIDE ? 4 : 1;
+    for (int64_t r = r0 + (threadIdx.x >> 5); r < r1; r += 8 * FLY) {
+        uint4 vd[FLY], vz[FLY], vu[FLY];
+        if constexpr (INSIDE) {
+#pragma unroll
+            for (int k = 0; k < FLY; ++k) {
+                const int64_t rr = r + 8 * k < r1 ? r + 8 * k : r1 - 1;
+                vd[k] = __ldcs(reinterpret_cast<const uint4 *>(dy + rr * p.lddy + c));
+                if (READ_Z) vz[k] = __ldcs(reinterpret_cast<const uint4 *>(z + rr * p.ldz + c));
+                if (GATED) vu[k] = __ldcs(reinterpret_cast<const uint4 *>(u + rr * p.ldu + c));
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < FLY; ++k) {
+            const int64_t rr = r + 8 * k;
+            if (rr < r1) {
+                float d[8], a[8], g[8];
+                if constexpr (INSIDE) row_unpack<Ty>(vd[k], d);
+                else Row::load(dy + rr * p.lddy, c, p.n, d);
+                if constexpr (READ_Z) {
+                    float y[8];
+                    if constexpr (INSIDE) row_unpack<Ty>(vz[k], y);
+                    else Row::load(z + rr * p.ldz, c, p.n, y);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) mlp_act_grad<ACT>(y[i], a[i], g[i]);
+                }
+                if constexpr (GATED) {
+                    float w[8];
+                    if constexpr (INSIDE) row_unpack<Ty>(vu[k], w);
+                    else Row::load(u + rr * p.ldu, c, p.n, w);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        a[i] *= d[i];
+                        d[i] *= w[i] * g[i];
+                    }
+                    Row::store(o0 + rr * p.ldo0, c, p.n, d);
+                    Row::store(o1 + rr * p.ldo1, c, p.n, a);
+                } else {
+                    if constexpr (READ_Z) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) d[i] *= g[i];
+                    }
+                    if (o0) Row::store(o0 + rr * p.ldo0, c, p.n, d);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) s[i] += d[i];
+                }
+            }
+        }
+    }
+}
+
 template <class Ty, bool VEC, bool GATED>
-__global__ void __launch_bounds__(256) tg_act_backward_kernel(const ActParams p) {
+__global__ void __launch_bounds__(256, 3) tg_act_backward_kernel(const ActParams p) {
     __shared__ float sums[GATED ? 1 : 8][GATED ? 1 : 256];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     griddep_launch();
@@ -89,59 +140,23 @@ __global__ void __launch_bounds__(256) tg_act_backward_kernel(const ActParams p)
     float s[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) s[i] = 0.0f;
-    constexpr int FLY = GATED ? 2 : 4;  // rows in flight per warp
-    for (int64_t r = r0 + warp; r < r1; r += 8 * FLY) {
-        Row dy[FLY], z[FLY], u[FLY];
-#pragma unroll
-        for (int k = 0; k < FLY; ++k) {
-            const int64_t rr = r + 8 * k;
-            if (rr < r1) {
-                dy[k].load(p.dy, rr, p.lddy, c0, lane, p.n);
-                if (GATED || p.z) z[k].load(p.z, rr, p.ldz, c0, lane, p.n);
-                if (GATED) u[k].load(p.u, rr, p.ldu, c0, lane, p.n);
-            }
-        }
-#pragma unroll
-        for (int k = 0; k < FLY; ++k) {
-            const int64_t rr = r + 8 * k;
-            if (rr >= r1) break;
-            if constexpr (GATED) {
-                Row dg, du;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    float a, d;
-                    mlp_act_grad(p.act, z[k].v[i], a, d);
-                    dg.v[i] = dy[k].v[i] * u[k].v[i] * d;
-                    du.v[i] = dy[k].v[i] * a;
-                }
-                dg.store(p.out0, rr, p.ldo0, c0, lane, p.n);
-                du.store(p.out1, rr, p.ldo1, c0, lane, p.n);
-            } else {
-                if (p.z) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        float a, d;
-                        mlp_act_grad(p.act, z[k].v[i], a, d);
-                        dy[k].v[i] *= d;
-                    }
-                }
-                if (p.out0) dy[k].store(p.out0, rr, p.ldo0, c0, lane, p.n);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) s[i] += dy[k].v[i];
-            }
-        }
-    }
+    const int64_t c = c0 + Row::first(lane);
+    const bool inside = VEC && c0 + 256 <= p.n;
+    mlp_with_act(p.act, [&](auto act) {
+        if (inside) act_band<Ty, VEC, GATED, act.value, VEC>(p, c, r0, r1, s);
+        else act_band<Ty, VEC, GATED, act.value, false>(p, c, r0, r1, s);
+    });
     if constexpr (!GATED) {
         if (!p.partial) return;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sums[warp][Row::col(0, lane, i)] = s[i];
+        for (int i = 0; i < 8; ++i) sums[warp][Row::col(lane, i)] = s[i];
         __syncthreads();
-        const int64_t c = c0 + threadIdx.x;
-        if (c < p.n) {
+        const int64_t cc = c0 + threadIdx.x;
+        if (cc < p.n) {
             float t = 0.0f;
 #pragma unroll
             for (int w = 0; w < 8; ++w) t += sums[w][threadIdx.x];
-            p.partial[(int64_t)blockIdx.y * p.n + c] = t;
+            p.partial[(int64_t)blockIdx.y * p.n + cc] = t;
         }
     }
 }

@@ -18,9 +18,12 @@
 // Backward keeps each thread's columns fixed over all rows of its group, so
 // the column sums dgamma and dbeta accumulate in registers and leave the block
 // once; tg_colsum_finish_kernel adds the blocks' partials in a fixed order.
-// No atomics: repeated calls agree bit for bit.  Rows are prefetched one
-// ahead, so that a row's loads overlap the row before's reductions.
+// No atomics: repeated calls agree bit for bit.  Two or three rows
+// are in flight behind the one in work (NormRows), so that their loads overlap
+// its reductions.
 #include <cuda_runtime.h>
+
+#include <atomic>
 
 #include "../../include/tg_gemm.h"
 #include "tg_host.h"
@@ -45,58 +48,117 @@ struct NormParams {
 };
 
 // A thread's 16 elements of a row.  VEC: 16-byte vectors, vector v at column
-// (v * threads + t) * VW.  Else single elements, element i at i * threads + t.
-template <class Ty, bool VEC>
-struct NormRow {
+// (v * THREADS + t) * VW.  Else single elements, element i at i * THREADS + t.
+template <class Ty, int THREADS, bool VEC>
+struct NormCols {
     static constexpr int VW = Ty::VW;
-    static constexpr int RAW = VEC ? NORM_PER / VW : NORM_PER;
-    uint4 vec[VEC ? RAW : 1];
-    typename Ty::T el[VEC ? 1 : RAW];
-
-    __device__ __forceinline__ static int64_t col(int i, int t, int threads) {
-        return VEC ? ((int64_t)(i / VW) * threads + t) * VW + i % VW : (int64_t)i * threads + t;
+    __device__ __forceinline__ static int at(int i, int t) {
+        return VEC ? ((i / VW) * THREADS + t) * VW + i % VW : i * THREADS + t;
     }
-    __device__ __forceinline__ void load(const typename Ty::T *row, int t, int threads, int64_t n) {
-        if constexpr (VEC) {
-#pragma unroll
-            for (int v = 0; v < RAW; ++v) {
-                const int64_t c = ((int64_t)v * threads + t) * VW;
-                vec[v] = c < n ? row_load<Ty>(row, c, n) : make_uint4(0, 0, 0, 0);
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < RAW; ++i) {
-                const int64_t c = (int64_t)i * threads + t;
-                el[i] = c < n ? __ldcs(row + c) : (typename Ty::T)0;
-            }
-        }
-    }
-    __device__ __forceinline__ void unpack(float (&y)[NORM_PER]) const {
-        if constexpr (VEC) {
-#pragma unroll
-            for (int v = 0; v < RAW; ++v) row_unpack<Ty>(vec[v], y + v * VW);
-        } else {
-#pragma unroll
-            for (int i = 0; i < RAW; ++i) y[i] = Ty::up(el[i]);
-        }
-    }
-    __device__ __forceinline__ static void store(typename Ty::T *row, int t, int threads, int64_t n,
+    __device__ __forceinline__ static void store(typename Ty::T *row, int t, int n,
                                                  const float (&y)[NORM_PER]) {
         if constexpr (VEC) {
 #pragma unroll
-            for (int v = 0; v < RAW; ++v) {
-                const int64_t c = ((int64_t)v * threads + t) * VW;
+            for (int v = 0; v < NORM_PER / VW; ++v) {
+                const int c = (v * THREADS + t) * VW;
                 if (c < n) row_store<Ty>(row, c, n, y + v * VW);
             }
         } else {
 #pragma unroll
             for (int i = 0; i < NORM_PER; ++i) {
-                const int64_t c = (int64_t)i * threads + t;
+                const int c = i * THREADS + t;
                 if (c < n) row[c] = Ty::down(y[i]);
             }
         }
     }
 };
+
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void *src, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Rows on their way: MATS matrices' rows r, r + groups, ... of this group.
+// VEC: each thread copies its own vectors into its own slots of a DEPTH-row
+// ring in shared memory (cp.async, zero fill past the row's end) and reads
+// them back itself, so no barrier is needed and DEPTH - 1 rows are in flight
+// without a register.  Else: one row ahead, in registers.
+template <class Ty, int THREADS, bool VEC, int MATS, int DEPTH>
+struct NormRows {
+    using T = typename Ty::T;
+    static constexpr int VW = Ty::VW, VECS = NORM_PER / VW;
+    const T *base[MATS];
+    int64_t ld[MATS];
+    int64_t m, groups;
+    int n, t, slot;
+    uint4 *ring;
+    T ahead[MATS][VEC ? 1 : NORM_PER];
+
+    __device__ __forceinline__ void ask(int64_t r, int at) {
+        if constexpr (VEC) {
+            if (r < m) {
+#pragma unroll
+                for (int a = 0; a < MATS; ++a) {
+                    const T *row = base[a] + r * ld[a];
+#pragma unroll
+                    for (int v = 0; v < VECS; ++v) {
+                        const int c = (v * THREADS + t) * VW;
+                        const int left = n - c;
+                        const uint32_t bytes =
+                            left >= VW ? 16u : (left > 0 ? (uint32_t)(left * (int)sizeof(T)) : 0u);
+                        cp_async_16(smem_u32(ring + ((at * MATS + a) * VECS + v) * blockDim.x + threadIdx.x),
+                                    left > 0 ? row + c : row, bytes);
+                    }
+                }
+            }
+            cp_async_commit();
+        } else {
+            if (r < m) {
+#pragma unroll
+                for (int a = 0; a < MATS; ++a) {
+                    const T *row = base[a] + r * ld[a];
+#pragma unroll
+                    for (int i = 0; i < NORM_PER; ++i) {
+                        const int c = i * THREADS + t;
+                        ahead[a][i] = c < n ? __ldcs(row + c) : (T)0;
+                    }
+                }
+            }
+        }
+    }
+    __device__ __forceinline__ void start(int64_t first) {
+        slot = 0;
+#pragma unroll
+        for (int d = 0; d < (VEC ? DEPTH - 1 : 1); ++d) ask(first + d * groups, d);
+    }
+    // This row's values, with the row after the last one asked for set off.
+    __device__ __forceinline__ void take(int64_t r, float (&y)[MATS][NORM_PER]) {
+        if constexpr (VEC) {
+            cp_async_wait<DEPTH - 2>();
+#pragma unroll
+            for (int a = 0; a < MATS; ++a)
+#pragma unroll
+                for (int v = 0; v < VECS; ++v)
+                    row_unpack<Ty>(ring[((slot * MATS + a) * VECS + v) * blockDim.x + threadIdx.x],
+                                   y[a] + v * VW);
+            ask(r + (DEPTH - 1) * groups, slot == 0 ? DEPTH - 1 : slot - 1);
+            slot = slot + 1 == DEPTH ? 0 : slot + 1;
+        } else {
+#pragma unroll
+            for (int a = 0; a < MATS; ++a)
+#pragma unroll
+                for (int i = 0; i < NORM_PER; ++i) y[a][i] = Ty::up(ahead[a][i]);
+            ask(r + groups, 0);
+        }
+    }
+};
+
+constexpr int NORM_DEPTH = 4, NORM_BACK_DEPTH = 3;
 
 __device__ __forceinline__ float2 warp_sum2(float2 v) {
 #pragma unroll
@@ -153,36 +215,57 @@ constexpr int norm_block() {
 template <class Ty, int TR, int CS, bool VEC>
 __global__ void __launch_bounds__(norm_block<TR>()) tg_norm_kernel(const NormParams p) {
     using T = typename Ty::T;
+    extern __shared__ uint4 ring[];
     __shared__ float2 warps[2 * 16];
     __shared__ float2 blocks[2 * 8];
     constexpr int GROUPS = norm_block<TR>() / TR;
     constexpr int THREADS = TR * CS;  // threads that share a row
+    using Cols = NormCols<Ty, THREADS, VEC>;
     const int t = (int)(threadIdx.x % TR) + (CS > 1 ? (int)cluster_ctarank() * TR : 0);
     const int64_t group = ((int64_t)blockIdx.x / CS) * GROUPS + threadIdx.x / TR;
     const int64_t groups = ((int64_t)gridDim.x / CS) * GROUPS;
+    const int n = (int)p.n;
     GroupSum<TR, CS> sum{warps, blocks, 0};
     griddep_launch();
     if constexpr (CS > 1) cluster_sync_all();  // every block runs before its memory is written
     griddep_wait();
-    const T *x = static_cast<const T *>(p.x);
+    NormRows<Ty, THREADS, VEC, 1, NORM_DEPTH> rows;
+    rows.base[0] = static_cast<const T *>(p.x);
+    rows.ld[0] = p.ldx;
+    rows.m = p.m;
+    rows.groups = groups;
+    rows.n = n;
+    rows.t = t;
+    rows.ring = ring;
+    rows.start(group);
+    // The group's columns never change: gamma and beta stay in registers.
+    float gam[NORM_PER], bet[NORM_PER];
+#pragma unroll
+    for (int i = 0; i < NORM_PER; ++i) {
+        const int c = Cols::at(i, t);
+        gam[i] = (p.gamma && c < n) ? __ldg(p.gamma + c) : 1.0f;
+        bet[i] = (p.beta && c < n) ? __ldg(p.beta + c) : 0.0f;
+    }
     T *y = static_cast<T *>(p.y);
-    NormRow<Ty, VEC> next;
-    if (group < p.m) next.load(x + group * p.ldx, t, THREADS, p.n);
+    const bool whole = n == THREADS * NORM_PER;
     for (int64_t r = group; r < p.m; r += groups) {
-        float v[NORM_PER];
-        next.unpack(v);
-        if (r + groups < p.m) next.load(x + (r + groups) * p.ldx, t, THREADS, p.n);
+        float w[1][NORM_PER];
+        rows.take(r, w);
+        float(&v)[NORM_PER] = w[0];
         float s = 0.0f;
 #pragma unroll
         for (int i = 0; i < NORM_PER; ++i) s += v[i];
         const float mean = sum(make_float2(s, 0.0f)).x * p.inv_n;
+#pragma unroll
+        for (int i = 0; i < NORM_PER; ++i) v[i] -= mean;
+        if (!whole) {
+#pragma unroll
+            for (int i = 0; i < NORM_PER; ++i)
+                if (Cols::at(i, t) >= n) v[i] = 0.0f;
+        }
         float q = 0.0f;
 #pragma unroll
-        for (int i = 0; i < NORM_PER; ++i) {
-            const float d = NormRow<Ty, VEC>::col(i, t, THREADS) < p.n ? v[i] - mean : 0.0f;
-            v[i] = d;
-            q += d * d;
-        }
+        for (int i = 0; i < NORM_PER; ++i) q = fmaf(v[i], v[i], q);
         const float var = sum(make_float2(q, 0.0f)).x * p.inv_n;
         const float rstd = 1.0f / sqrtf(var + p.eps);
         if (t == 0) {
@@ -190,62 +273,58 @@ __global__ void __launch_bounds__(norm_block<TR>()) tg_norm_kernel(const NormPar
             if (p.rstd) p.rstd[r] = rstd;
         }
 #pragma unroll
-        for (int i = 0; i < NORM_PER; ++i) {
-            const int64_t c = NormRow<Ty, VEC>::col(i, t, THREADS);
-            float z = v[i] * rstd;
-            if (c < p.n) {
-                if (p.gamma) z *= __ldg(p.gamma + c);
-                if (p.beta) z += __ldg(p.beta + c);
-            }
-            v[i] = z;
-        }
-        NormRow<Ty, VEC>::store(y + r * p.ldy, t, THREADS, p.n, v);
+        for (int i = 0; i < NORM_PER; ++i) v[i] = fmaf(v[i] * rstd, gam[i], bet[i]);
+        Cols::store(y + r * p.ldy, t, n, v);
     }
 }
 
 template <class Ty, int TR, int CS, bool VEC>
 __global__ void __launch_bounds__(norm_block<TR>()) tg_norm_backward_kernel(const NormParams p) {
     using T = typename Ty::T;
+    extern __shared__ uint4 ring[];
     __shared__ float2 warps[2 * 16];
     __shared__ float2 blocks[2 * 8];
     constexpr int GROUPS = norm_block<TR>() / TR;
     constexpr int THREADS = TR * CS;
+    using Cols = NormCols<Ty, THREADS, VEC>;
     const int t = (int)(threadIdx.x % TR) + (CS > 1 ? (int)cluster_ctarank() * TR : 0);
     const int64_t group = ((int64_t)blockIdx.x / CS) * GROUPS + threadIdx.x / TR;
     const int64_t groups = ((int64_t)gridDim.x / CS) * GROUPS;
+    const int n = (int)p.n;
     GroupSum<TR, CS> sum{warps, blocks, 0};
     griddep_launch();
-    if constexpr (CS > 1) cluster_sync_all();  // every block runs before its memory is written
+    if constexpr (CS > 1) cluster_sync_all();
     griddep_wait();
-    const T *x = static_cast<const T *>(p.x);
-    const T *dy = static_cast<const T *>(p.dy);
+    NormRows<Ty, THREADS, VEC, 2, NORM_BACK_DEPTH> rows;
+    rows.base[0] = static_cast<const T *>(p.x);
+    rows.base[1] = static_cast<const T *>(p.dy);
+    rows.ld[0] = p.ldx;
+    rows.ld[1] = p.lddy;
+    rows.m = p.m;
+    rows.groups = groups;
+    rows.n = n;
+    rows.t = t;
+    rows.ring = ring;
+    rows.start(group);
     T *dx = static_cast<T *>(p.y);
     float gam[NORM_PER], sg[NORM_PER], sb[NORM_PER];
 #pragma unroll
     for (int i = 0; i < NORM_PER; ++i) {
-        const int64_t c = NormRow<Ty, VEC>::col(i, t, THREADS);
-        gam[i] = (p.gamma && c < p.n) ? __ldg(p.gamma + c) : 1.0f;
+        const int c = Cols::at(i, t);
+        gam[i] = (p.gamma && c < n) ? __ldg(p.gamma + c) : 1.0f;
         sg[i] = sb[i] = 0.0f;
     }
-    NormRow<Ty, VEC> nx, nd;
-    float nmean = 0.0f, nrstd = 0.0f;
-    if (group < p.m) {
-        nx.load(x + group * p.ldx, t, THREADS, p.n);
-        nd.load(dy + group * p.lddy, t, THREADS, p.n);
-        nmean = __ldg(p.mean_in + group);
-        nrstd = __ldg(p.rstd_in + group);
-    }
+    float nmean = group < p.m ? __ldg(p.mean_in + group) : 0.0f;
+    float nrstd = group < p.m ? __ldg(p.rstd_in + group) : 0.0f;
     for (int64_t r = group; r < p.m; r += groups) {
-        float xh[NORM_PER], d[NORM_PER];
-        nx.unpack(xh);
-        nd.unpack(d);
+        float w[2][NORM_PER];
+        rows.take(r, w);
+        float(&xh)[NORM_PER] = w[0];
+        float(&d)[NORM_PER] = w[1];
         const float mean = nmean, rstd = nrstd;
-        const int64_t r2 = r + groups;
-        if (r2 < p.m) {
-            nx.load(x + r2 * p.ldx, t, THREADS, p.n);
-            nd.load(dy + r2 * p.lddy, t, THREADS, p.n);
-            nmean = __ldg(p.mean_in + r2);
-            nrstd = __ldg(p.rstd_in + r2);
+        if (r + groups < p.m) {
+            nmean = __ldg(p.mean_in + r + groups);
+            nrstd = __ldg(p.rstd_in + r + groups);
         }
         float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
@@ -253,24 +332,24 @@ __global__ void __launch_bounds__(norm_block<TR>()) tg_norm_backward_kernel(cons
             // Columns past the row's end hold dy = 0 and add nothing.
             const float h = (xh[i] - mean) * rstd;
             xh[i] = h;
-            sg[i] += d[i] * h;
+            sg[i] = fmaf(d[i], h, sg[i]);
             sb[i] += d[i];
             d[i] *= gam[i];
             s1 += d[i];
-            s2 += d[i] * h;
+            s2 = fmaf(d[i], h, s2);
         }
         const float2 s = sum(make_float2(s1, s2));
-        const float c1 = s.x * p.inv_n, c2 = s.y * p.inv_n;
         if (dx) {
+            const float c1 = s.x * p.inv_n, c2 = s.y * p.inv_n;
 #pragma unroll
-            for (int i = 0; i < NORM_PER; ++i) d[i] = rstd * (d[i] - c1 - xh[i] * c2);
-            NormRow<Ty, VEC>::store(dx + r * p.ldy, t, THREADS, p.n, d);
+            for (int i = 0; i < NORM_PER; ++i) d[i] = rstd * (d[i] - fmaf(xh[i], c2, c1));
+            Cols::store(dx + r * p.ldy, t, n, d);
         }
     }
 #pragma unroll
     for (int i = 0; i < NORM_PER; ++i) {
-        const int64_t c = NormRow<Ty, VEC>::col(i, t, THREADS);
-        if (c < p.n) {
+        const int c = Cols::at(i, t);
+        if (c < n) {
             if (p.pgamma) p.pgamma[group * p.n + c] = sg[i];
             if (p.pbeta) p.pbeta[group * p.n + c] = sb[i];
         }
@@ -310,9 +389,10 @@ int64_t norm_grid(const NormShape &s, int64_t m, int sms, int per_sm) {
     return blocks * s.cs;
 }
 
-// Backward blocks per SM: the partial column sums cost 8 n bytes per group,
-// written and read once, against 3 rows per group and row; 2 blocks of 256
-// threads keep 32 KB a SM in flight.
+// Blocks per SM: what registers and rings leave room for; in backward also few
+// enough that the partial column sums (8 n bytes per group, written and read
+// once) stay small beside the rows.
+int forward_per_sm(const NormShape &s) { return s.tr >= 512 ? 1 : s.tr == 256 ? 3 : 6; }
 int backward_per_sm(const NormShape &s) { return s.tr >= 512 ? 1 : s.tr == 256 ? 2 : 4; }
 int64_t backward_groups(int64_t m, int64_t n, int sms) {
     const NormShape s = norm_shape(n);
@@ -321,7 +401,21 @@ int64_t backward_groups(int64_t m, int64_t n, int sms) {
 }
 
 template <class Ty, int TR, int CS, bool VEC>
-cudaError_t launch_shape(const NormParams &p, bool backward, int64_t grid, cudaStream_t stream) {
+cudaError_t launch_shape(const NormParams &p, bool backward, int64_t grid, int device,
+                         cudaStream_t stream) {
+    constexpr int ROW = norm_block<TR>() * NORM_PER * (int)sizeof(typename Ty::T);
+    constexpr int SMEM = VEC ? NORM_DEPTH * ROW : 0, SMEM_BACK = VEC ? NORM_BACK_DEPTH * 2 * ROW : 0;
+    static std::atomic<uint64_t> done{0};
+    const uint64_t bit = 1ull << device;
+    if (VEC && !(done.load(std::memory_order_acquire) & bit)) {
+        cudaError_t e = cudaFuncSetAttribute(tg_norm_kernel<Ty, TR, CS, VEC>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(tg_norm_backward_kernel<Ty, TR, CS, VEC>,
+                                     cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BACK);
+        if (e != cudaSuccess) return e;
+        done.fetch_or(bit, std::memory_order_acq_rel);
+    }
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -332,6 +426,7 @@ cudaError_t launch_shape(const NormParams &p, bool backward, int64_t grid, cudaS
     attr[1].val.clusterDim.z = 1;
     cfg.gridDim = dim3((unsigned)grid, 1, 1);
     cfg.blockDim = dim3(norm_block<TR>(), 1, 1);
+    cfg.dynamicSmemBytes = backward ? SMEM_BACK : SMEM;
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = CS > 1 ? 2 : 1;
@@ -340,27 +435,28 @@ cudaError_t launch_shape(const NormParams &p, bool backward, int64_t grid, cudaS
 }
 
 template <class Ty, bool VEC>
-cudaError_t launch_type(const NormParams &p, bool backward, int64_t grid, cudaStream_t stream) {
+cudaError_t launch_type(const NormParams &p, bool backward, int64_t grid, int device,
+                        cudaStream_t stream) {
     const NormShape s = norm_shape(p.n);
-    if (s.tr == 32) return launch_shape<Ty, 32, 1, VEC>(p, backward, grid, stream);
-    if (s.tr == 128) return launch_shape<Ty, 128, 1, VEC>(p, backward, grid, stream);
-    if (s.tr == 256) return launch_shape<Ty, 256, 1, VEC>(p, backward, grid, stream);
-    if (s.cs == 1) return launch_shape<Ty, 512, 1, VEC>(p, backward, grid, stream);
-    if (s.cs == 2) return launch_shape<Ty, 512, 2, VEC>(p, backward, grid, stream);
-    if (s.cs == 4) return launch_shape<Ty, 512, 4, VEC>(p, backward, grid, stream);
-    return launch_shape<Ty, 512, 8, VEC>(p, backward, grid, stream);
+    if (s.tr == 32) return launch_shape<Ty, 32, 1, VEC>(p, backward, grid, device, stream);
+    if (s.tr == 128) return launch_shape<Ty, 128, 1, VEC>(p, backward, grid, device, stream);
+    if (s.tr == 256) return launch_shape<Ty, 256, 1, VEC>(p, backward, grid, device, stream);
+    if (s.cs == 1) return launch_shape<Ty, 512, 1, VEC>(p, backward, grid, device, stream);
+    if (s.cs == 2) return launch_shape<Ty, 512, 2, VEC>(p, backward, grid, device, stream);
+    if (s.cs == 4) return launch_shape<Ty, 512, 4, VEC>(p, backward, grid, device, stream);
+    return launch_shape<Ty, 512, 8, VEC>(p, backward, grid, device, stream);
 }
 
 cudaError_t launch_norm(const NormParams &p, tg_out_dtype t, bool backward, bool vec, int64_t grid,
-                        cudaStream_t stream) {
+                        int device, cudaStream_t stream) {
     if (t == TG_OUT_F32)
-        return vec ? launch_type<TypeF32, true>(p, backward, grid, stream)
-                   : launch_type<TypeF32, false>(p, backward, grid, stream);
+        return vec ? launch_type<TypeF32, true>(p, backward, grid, device, stream)
+                   : launch_type<TypeF32, false>(p, backward, grid, device, stream);
     if (t == TG_OUT_BF16)
-        return vec ? launch_type<TypeBF16, true>(p, backward, grid, stream)
-                   : launch_type<TypeBF16, false>(p, backward, grid, stream);
-    return vec ? launch_type<TypeF16, true>(p, backward, grid, stream)
-               : launch_type<TypeF16, false>(p, backward, grid, stream);
+        return vec ? launch_type<TypeBF16, true>(p, backward, grid, device, stream)
+                   : launch_type<TypeBF16, false>(p, backward, grid, device, stream);
+    return vec ? launch_type<TypeF16, true>(p, backward, grid, device, stream)
+               : launch_type<TypeF16, false>(p, backward, grid, device, stream);
 }
 
 bool norm_type_ok(tg_out_dtype t) { return t == TG_OUT_F32 || t == TG_OUT_BF16 || t == TG_OUT_F16; }
@@ -406,9 +502,9 @@ extern "C" tg_status tg_layer_norm(int64_t M, int64_t N, const void *X, int64_t 
     p.rstd = rstd;
     p.inv_n = 1.0f / (float)N;
     const NormShape s = norm_shape(N);
-    const int64_t grid = norm_grid(s, M, dev.sms, s.tr >= 512 ? 2 : s.tr == 256 ? 4 : 8);
+    const int64_t grid = norm_grid(s, M, dev.sms, forward_per_sm(s));
     const bool vec = vec_ok(X, ldx, e) && vec_ok(Y, ldy, e);
-    return launch_norm(p, dtype, false, vec, grid, static_cast<cudaStream_t>(stream)) == cudaSuccess
+    return launch_norm(p, dtype, false, vec, grid, dev.id, static_cast<cudaStream_t>(stream)) == cudaSuccess
                ? TG_OK
                : TG_ERR_CUDA;
 }
@@ -466,7 +562,8 @@ extern "C" tg_status tg_layer_norm_backward(int64_t M, int64_t N, const void *dY
         if (dbeta) p.pbeta = static_cast<float *>(workspace) + groups * N;
         const NormShape s = norm_shape(N);
         const bool vec = vec_ok(X, ldx, e) && vec_ok(dY, lddy, e) && (!dX || vec_ok(dX, lddx, e));
-        if (launch_norm(p, dtype, true, vec, norm_grid(s, M, dev.sms, backward_per_sm(s)), stream) !=
+        if (launch_norm(p, dtype, true, vec, norm_grid(s, M, dev.sms, backward_per_sm(s)), dev.id,
+                        stream) !=
             cudaSuccess)
             return TG_ERR_CUDA;
     }
