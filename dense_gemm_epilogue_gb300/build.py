@@ -22,7 +22,8 @@ LIB = os.path.join(OUT_DIR, "libtg_gemm.so")
 OBJ_DIR = os.path.join(HERE, "_build")
 SOURCES = ["tg_gemm.cu", "tg_inst_bf16.cu", "tg_inst_fp16.cu", "tg_inst_tf32.cu",
            "tg_inst_e4m3.cu", "tg_inst_e5m2.cu", "tg_inst_mx.cu", "tg_noalloc.cu", "tg_mlp.cu",
-           "tg_norm.cu", "tg_inst_mlp_bf16.cu", "tg_inst_mlp_fp16.cu", "tg_inst_stream_bf16.cu",
+           "tg_norm.cu", "tg_inst_mlp_bf16_cg1.cu", "tg_inst_mlp_bf16_cg2.cu",
+           "tg_inst_mlp_fp16_cg1.cu", "tg_inst_mlp_fp16_cg2.cu", "tg_inst_stream_bf16.cu",
            "tg_inst_stream_fp16.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",

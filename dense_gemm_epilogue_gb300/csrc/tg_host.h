@@ -31,7 +31,7 @@ struct Scratch {
     uint32_t *ticket = nullptr;
     uint32_t *stream_flags = nullptr;  // of the weight-streaming kernel (kStreamFlags words)
 };
-constexpr int64_t kStreamFlags = 4 * 512;
+constexpr int64_t kStreamFlags = 8 * 512;
 tg_status scratch(const Device &dev, cudaStream_t stream, int64_t tiles, Scratch *out);
 
 // 2-D tensor map of a row-major matrix of 2- or 4-byte elements: box of

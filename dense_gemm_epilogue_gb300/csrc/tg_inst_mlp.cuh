@@ -26,21 +26,21 @@ static cudaError_t mlp_configure(K kernel, int smem, int device, std::atomic<uin
     return cudaSuccess;
 }
 
-template <Kind KD, int BN, int AM, int BM, MlpEpi EP>
+template <Kind KD, int CG, int BN, int AM, int BM, MlpEpi EP>
 static cudaError_t launch_mlp_one(const MlpLaunch &a) {
-    using C = MlpConfig<KD, BN, AM, BM, EP>;
-    auto kernel = tg_mlp_kernel<KD, BN, AM, BM, EP>;
+    using C = MlpConfig<KD, CG, BN, AM, BM, EP>;
+    auto kernel = tg_mlp_kernel<KD, CG, BN, AM, BM, EP>;
     static std::atomic<uint64_t> done{0};
     static int max_clusters[64] = {0};
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.x = CG;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3(2, 1, 1);
+    cfg.gridDim = dim3(CG, 1, 1);
     cfg.blockDim = dim3(C::NUM_THREADS, 1, 1);
     cfg.dynamicSmemBytes = C::SMEM_BYTES;
     cfg.stream = a.stream;
@@ -49,27 +49,27 @@ static cudaError_t launch_mlp_one(const MlpLaunch &a) {
     cudaError_t e = mlp_configure(kernel, C::SMEM_BYTES, a.device, done, &cfg, max_clusters);
     if (e != cudaSuccess) return e;
     int grid = a.grid;
-    if (a.device >= 0 && a.device < 64 && grid > 2 * max_clusters[a.device])
-        grid = 2 * max_clusters[a.device];
-    cfg.gridDim = dim3(grid < 2 ? 2 : grid, 1, 1);
+    if (a.device >= 0 && a.device < 64 && grid > CG * max_clusters[a.device])
+        grid = CG * max_clusters[a.device];
+    cfg.gridDim = dim3(grid < CG ? CG : grid, 1, 1);
     cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, kernel, a.maps, a.p);
 }
 
-template <Kind KD, int BN>
+template <Kind KD, int CG, int BN>
 static cudaError_t launch_mlp_bn(const MlpLaunch &a) {
     switch (a.op) {
-    case MlpOp::LINEAR: return launch_mlp_one<KD, BN, 0, 0, MlpEpi::LINEAR>(a);
-    case MlpOp::GATED: return launch_mlp_one<KD, BN, 0, 0, MlpEpi::GATED>(a);
-    case MlpOp::DGRAD: return launch_mlp_one<KD, BN, 0, 1, MlpEpi::PLAIN>(a);
-    case MlpOp::WGRAD: return launch_mlp_one<KD, BN, 1, 1, MlpEpi::PLAIN>(a);
+    case MlpOp::LINEAR: return launch_mlp_one<KD, CG, BN, 0, 0, MlpEpi::LINEAR>(a);
+    case MlpOp::GATED: return launch_mlp_one<KD, CG, BN, 0, 0, MlpEpi::GATED>(a);
+    case MlpOp::DGRAD: return launch_mlp_one<KD, CG, BN, 0, 1, MlpEpi::PLAIN>(a);
+    case MlpOp::WGRAD: return launch_mlp_one<KD, CG, BN, 1, 1, MlpEpi::PLAIN>(a);
     }
     return cudaErrorInvalidValue;
 }
 
-template <Kind KD>
+template <Kind KD, int CG>
 static cudaError_t launch_mlp_kind(const MlpLaunch &a) {
-    return a.block_n == 256 ? launch_mlp_bn<KD, 256>(a) : launch_mlp_bn<KD, 128>(a);
+    return a.block_n == 256 ? launch_mlp_bn<KD, CG, 256>(a) : launch_mlp_bn<KD, CG, 128>(a);
 }
 
 template <Kind KD, int NT, bool DUAL>

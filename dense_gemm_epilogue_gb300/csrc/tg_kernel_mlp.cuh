@@ -1,12 +1,14 @@
-// CTA-pair GEMM of the feed-forward operators: row-major outputs, operands
+// Tile GEMM of the feed-forward operators: row-major outputs, operands
 // contiguous along either axis, and epilogues that need more than the
 // accumulator.
 //
 // Role space: out(r, c) = f(sum_k A(r, k) B(c, k)), r < m, c < n, row-major.
-// One cluster of two CTAs computes 256 rows x BN accumulator columns with
-// tcgen05.mma.cta_group::2; the persistent schedule, the barriers between the
-// pair, the ticket ring and the bounded waits are those of the CTA-pair GEMM
-// (tg_kernel_pair.cuh).  What differs:
+// A team of CG CTAs computes 128 CG rows x BN accumulator columns with
+// tcgen05.mma.cta_group::CG: a pair on neighbouring SMs (CG = 2, half the B
+// bytes per SM), or a single CTA (CG = 1, for products whose 256-row tiles
+// would leave SMs idle or rows empty).  The persistent schedule, the barriers
+// between a pair, the ticket ring and the bounded waits are those of the
+// CTA-pair GEMM (tg_kernel_pair.cuh).  What differs:
 //
 //   operands  Each of A and B is either K-major (rows of K) or MN-major (rows
 //             of the reduction index, the role-space row index contiguous):
@@ -19,20 +21,22 @@
 //             Wg + dU Wu): K blocks from k_blocks0 on come from the second
 //             pair of maps, into the same accumulator.
 //   dual      The gated unit's forward tile holds BN/2 gate columns and BN/2
-//             up columns of the same features: the leader stages Wg rows, the
-//             peer Wu rows, one MMA serves both, and one thread of the
-//             epilogue owns g and u of the same element.
+//             up columns of the same features: Wg rows and Wu rows are halves
+//             of the B stage (a pair's leader stages the one, its peer the
+//             other), one MMA serves both, and one thread of the epilogue owns
+//             g and u of the same element.
 //   entries   A second problem of the same shape in the same launch (dWg and
 //             dWu share X): tiles from tiles_per_batch on use the second A map
 //             and the second output.
-//   epilogue  Warps stage 32 rows x 128 bytes in shared memory (swizzled, 4 KB
-//             each) and store them by TMA, which clips at the edges and writes
-//             whole lines; row-major rows stored from registers would touch 32
-//             lines per instruction.  The residual comes in through the same
-//             buffer by TMA before the accumulator is ready.  Outputs or
-//             residuals that TMA cannot address (row stride or base not a
-//             multiple of 16 bytes) go through the same buffer with plain
-//             2-byte accesses, a row per instruction.
+//   epilogue  Warps stage 32 rows x 64 bytes in shared memory (swizzled, two
+//             2 KB buffers each, so one is filled while the other drains) and
+//             store them by TMA, which clips at the edges; row-major rows
+//             stored from registers would touch 32 lines per instruction.  The
+//             residual comes in through the same buffers by TMA, the first box
+//             before the accumulator is ready and each next one while the last
+//             is in work.  Outputs or residuals that TMA cannot address (row
+//             stride or base not a multiple of 16 bytes) go through the same
+//             buffers with plain 2-byte accesses, a row per instruction.
 //
 // Bound: tensor throughput for token counts above about 300 (arithmetic
 // intensity 256 x 256 / (256 + 256) = 128 FLOP per byte of L2 traffic).
@@ -137,9 +141,11 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, uint32_t sr
 __device__ __forceinline__ void bulk_commit() {
     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
-// The issuing thread's stores have read their shared memory / are complete.
+// All but the issuing thread's last LEFT stores have read their shared memory;
+// all its stores are complete.
+template <int LEFT>
 __device__ __forceinline__ void bulk_wait_read() {
-    asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(LEFT) : "memory");
 }
 __device__ __forceinline__ void bulk_wait_all() {
     asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
@@ -158,6 +164,9 @@ __device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t saddr) {
     d |= (uint64_t)2 << 61;
     return d;
 }
+
+// K segments of a split tile, less the finisher's own: at most this many.
+constexpr int SPLIT_PARTS = 3;
 
 enum class MlpEpi : int { LINEAR = 0, GATED = 1, PLAIN = 2 };
 
@@ -185,35 +194,34 @@ struct MlpParams {
     MlpOut out[3];            // LINEAR: Y, Z; GATED: H, G, U; PLAIN: one per entry
 };
 
-// AM, BM: 0 = K-major, 1 = MN-major operand.
-template <Kind KD, int BN, int AM, int BM, MlpEpi EP>
+// AM, BM: 0 = K-major, 1 = MN-major operand.  CG: CTAs per team.
+template <Kind KD, int CG, int BN, int AM, int BM, MlpEpi EP>
 struct MlpConfig {
     using T = KindTraits<KD>;
     static constexpr int BK = T::block_k;
-    static constexpr int PAIR_M = 2 * BLOCK_M;
-    static constexpr int B_ROWS = BN / 2;
+    static constexpr int TILE_M = CG * BLOCK_M;
+    static constexpr int B_ROWS = BN / CG;  // B-role rows staged by each CTA
     static constexpr bool DUAL = EP == MlpEpi::GATED;
     static constexpr int OUT_N = DUAL ? BN / 2 : BN;  // output columns per tile
     static constexpr int A_BYTES = BLOCK_M * ROW_BYTES;
     static constexpr int B_BYTES = B_ROWS * ROW_BYTES;
     static constexpr int EPI_WARPS = 8;
     static constexpr int COLS = OUT_N / 2;            // output columns of an epilogue warp
-    // A staged row: 128 bytes (64 16-bit columns), or the 64 bytes of the 32
-    // columns a warp has in the gated 128-column tile.
-    static constexpr int STG_ROW = COLS * 2 < ROW_BYTES ? COLS * 2 : ROW_BYTES;
-    static constexpr int STG_BYTES = 32 * STG_ROW;    // one warp's staging buffer
-    static constexpr int FIT = (SMEM_LIMIT - 2048 - EPI_WARPS * STG_BYTES) / (A_BYTES + B_BYTES);
+    static constexpr int STG_ROW = 64;                // a staged row: 32 16-bit columns
+    static constexpr int STG_BYTES = 32 * STG_ROW;    // one staging buffer, two per warp
+    static constexpr int FIT = (SMEM_LIMIT - 3072 - 2 * EPI_WARPS * STG_BYTES) / (A_BYTES + B_BYTES);
     static constexpr int STAGES = FIT > 8 ? 8 : FIT;
     static constexpr int A_OFF = 0;
     static constexpr int B_OFF = STAGES * A_BYTES;
     static constexpr int STG_OFF = B_OFF + STAGES * B_BYTES;
-    static constexpr int BAR_OFF = STG_OFF + EPI_WARPS * STG_BYTES;
+    static constexpr int BIAS_OFF = STG_OFF + 2 * EPI_WARPS * STG_BYTES;  // 32 floats per warp
+    static constexpr int BAR_OFF = BIAS_OFF + EPI_WARPS * 128;
     static constexpr int FULL0 = 0, EMPTY0 = STAGES;
     static constexpr int ACCF0 = 2 * STAGES, ACCE0 = ACCF0 + 2, DRAIN = ACCE0 + 2;
     static constexpr int SLOTS = 4;
     static constexpr int TKF0 = DRAIN + 1, TKE0 = TKF0 + SLOTS;
-    static constexpr int RES0 = TKE0 + SLOTS;  // one per epilogue warp: residual landed
-    static constexpr int NUM_BARS = RES0 + EPI_WARPS;
+    static constexpr int RES0 = TKE0 + SLOTS;  // two per epilogue warp: residual box landed
+    static constexpr int NUM_BARS = RES0 + 2 * EPI_WARPS;
     static constexpr int MISC_OFF = BAR_OFF + NUM_BARS * 8;
     static constexpr int TK_OFF = (MISC_OFF + 16 + 15) / 16 * 16;
     static constexpr int TICKET_OFF = TK_OFF + 16 * SLOTS;
@@ -222,58 +230,48 @@ struct MlpConfig {
     static constexpr int NUM_WARPS = 2 + EPI_WARPS;
     static constexpr int NUM_THREADS = NUM_WARPS * 32;
     static constexpr int MMAS_PER_STAGE = BK / T::umma_k;
-    static constexpr int READERS = 2 * (1 + EPI_WARPS) + 1;
+    static constexpr int READERS = CG * (1 + EPI_WARPS) + 1;
     static constexpr uint32_t IDESC = (1u << 4) | (T::fmt << 7) | (T::fmt << 10) |
                                       ((uint32_t)AM << 15) | ((uint32_t)BM << 16) |
                                       ((uint32_t)(BN >> 3) << 17) |
-                                      ((uint32_t)(PAIR_M >> 4) << 24);
+                                      ((uint32_t)(TILE_M >> 4) << 24);
     static_assert(T::mma == MmaKind::F16, "16-bit kinds");
     static_assert(SMEM_BYTES <= SMEM_LIMIT, "shared memory budget");
     static_assert(BN == 128 || BN == 256, "tile N");
 };
 
-// Byte `b` of row `r` of a staging buffer with TMA's 128-byte (64-byte) swizzle
-// for rows of 128 (64) bytes.
-template <int ROW>
+// Byte `b` of row `r` of a staging buffer: 64-byte rows with TMA's 64-byte
+// swizzle (the 16-byte piece's index xor row bits 1-2).
 __device__ __forceinline__ int stg_offset(int r, int b) {
-    const int x = ROW == 128 ? (r & 7) : ((r >> 1) & 3);
-    return r * ROW + ((((b >> 4) ^ x) << 4) | (b & 15));
+    return r * 64 + ((((b >> 4) ^ ((r >> 1) & 3)) << 4) | (b & 15));
 }
 
 // A staging buffer's rows from or to rows that TMA cannot address: one row per
 // step, neighbouring lanes on neighbouring elements, bounds checked.
-template <int ROW, typename E>
+template <typename E>
 __device__ __forceinline__ void stg_to_global(const uint8_t *stg, E *dst, int64_t ld, int64_t row0,
                                               int64_t col0, int64_t rows, int64_t cols, int lane) {
-    constexpr int PER = ROW / (int)sizeof(E);
+    constexpr int PER = 64 / (int)sizeof(E);
     for (int r = 0; r < 32 && row0 + r < rows; ++r) {
-#pragma unroll
-        for (int c = lane; c < PER; c += 32) {
-            const int b = c * (int)sizeof(E);
-            if (col0 + c < cols)
-                dst[(row0 + r) * ld + col0 + c] =
-                    *reinterpret_cast<const E *>(stg + stg_offset<ROW>(r, b));
-        }
+        if (lane < PER && col0 + lane < cols)
+            dst[(row0 + r) * ld + col0 + lane] =
+                *reinterpret_cast<const E *>(stg + stg_offset(r, lane * (int)sizeof(E)));
     }
 }
-template <int ROW>
 __device__ __forceinline__ void global_to_stg(uint8_t *stg, const uint16_t *src, int64_t ld,
                                               int64_t row0, int64_t col0, int64_t rows,
                                               int64_t cols, int lane) {
     for (int r = 0; r < 32; ++r) {
-#pragma unroll
-        for (int c = lane; c < ROW / 2; c += 32) {
-            const bool in = row0 + r < rows && col0 + c < cols;
-            *reinterpret_cast<uint16_t *>(stg + stg_offset<ROW>(r, c * 2)) =
-                in ? src[(row0 + r) * ld + col0 + c] : (uint16_t)0;
-        }
+        const bool in = row0 + r < rows && col0 + lane < cols;
+        *reinterpret_cast<uint16_t *>(stg + stg_offset(r, lane * 2)) =
+            in ? src[(row0 + r) * ld + col0 + lane] : (uint16_t)0;
     }
 }
 
-template <Kind KD, int BN, int AM, int BM, MlpEpi EP>
-__global__ void __launch_bounds__(MlpConfig<KD, BN, AM, BM, EP>::NUM_THREADS, 1)
+template <Kind KD, int CG, int BN, int AM, int BM, MlpEpi EP>
+__global__ void __launch_bounds__(MlpConfig<KD, CG, BN, AM, BM, EP>::NUM_THREADS, 1)
     tg_mlp_kernel(const __grid_constant__ MlpMaps maps, const __grid_constant__ MlpParams mp) {
-    using C = MlpConfig<KD, BN, AM, BM, EP>;
+    using C = MlpConfig<KD, CG, BN, AM, BM, EP>;
     constexpr int S = C::STAGES;
     const GemmParams &p = mp.g;
     extern __shared__ uint8_t smem_raw[];
@@ -282,10 +280,10 @@ __global__ void __launch_bounds__(MlpConfig<KD, BN, AM, BM, EP>::NUM_THREADS, 1)
     const uint32_t sbase = smem_u32(smem);
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
-    const uint32_t rank = cluster_ctarank();  // 0: leader, 1: peer
+    const uint32_t rank = CG == 2 ? cluster_ctarank() : 0;  // 0: leader, 1: a pair's peer
     const bool leader = rank == 0;
-    const int64_t pair = blockIdx.x / 2;
-    const int64_t num_pairs = gridDim.x / 2;
+    const int64_t pair = blockIdx.x / CG;  // this team
+    const int64_t num_pairs = gridDim.x / CG;
 
     auto bar = [&](int i) -> uint32_t { return sbase + C::BAR_OFF + 8 * i; };
     auto a_stage = [&](int s) -> uint32_t { return sbase + C::A_OFF + s * C::A_BYTES; };
@@ -293,7 +291,7 @@ __global__ void __launch_bounds__(MlpConfig<KD, BN, AM, BM, EP>::NUM_THREADS, 1)
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::MISC_OFF);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::MISC_OFF + 4);
     volatile int *fin_ready = reinterpret_cast<volatile int *>(smem + C::MISC_OFF + 8);
-    const PairWaitCtl ctl{abort_flag, map_shared_rank(smem_u32(smem + C::MISC_OFF + 4), rank ^ 1u),
+    const PairWaitCtl ctl{abort_flag, map_shared_rank(smem_u32(smem + C::MISC_OFF + 4), rank ^ (CG - 1u)),
                           p.status, p.wait_limit_ns};
     const int nkb = p.num_k_blocks;
 
@@ -304,14 +302,14 @@ __global__ void __launch_bounds__(MlpConfig<KD, BN, AM, BM, EP>::NUM_THREADS, 1)
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(bar(C::ACCF0 + a), 1);
-            mbar_init(bar(C::ACCE0 + a), 2 * C::EPI_WARPS);
+            mbar_init(bar(C::ACCE0 + a), CG * C::EPI_WARPS);
         }
         mbar_init(bar(C::DRAIN), 1);
         for (int c = 0; c < C::SLOTS; ++c) {
             mbar_init(bar(C::TKF0 + c), 1);
             mbar_init(bar(C::TKE0 + c), C::READERS);
         }
-        for (int w = 0; w < C::EPI_WARPS; ++w) mbar_init(bar(C::RES0 + w), 1);
+        for (int w = 0; w < 2 * C::EPI_WARPS; ++w) mbar_init(bar(C::RES0 + w), 1);
         *abort_flag = 0;
         fence_mbar_init();
         if (nkb > 0) {
@@ -321,11 +319,17 @@ __global__ void __launch_bounds__(MlpConfig<KD, BN, AM, BM, EP>::NUM_THREADS, 1)
         if (mp.out[0].tma) prefetch_tensormap(&maps.out[0]);
     }
     if (warp == 1) {
-        tmem_alloc_pair(smem_u32(tmem_slot), C::TMEM_COLS);
-        tmem_relinquish_pair();
+        if constexpr (CG == 2) {
+            tmem_alloc_pair(smem_u32(tmem_slot), C::TMEM_COLS);
+            tmem_relinquish_pair();
+        } else {
+            tmem_alloc(smem_u32(tmem_slot), C::TMEM_COLS);
+            tmem_relinquish();
+        }
     }
     tc_fence_before();
-    cluster_sync_all();
+    if constexpr (CG == 2) cluster_sync_all();
+    else __syncthreads();
     tc_fence_after();
     griddep_launch();
     const uint32_t tmem_base = *tmem_slot;
@@ -394,13 +398,13 @@ __global__ void __launch_bounds__(MlpConfig<KD, BN, AM, BM, EP>::NUM_THREADS, 1)
                         const uint32_t fb = bar(C::TKF0 + slot);
                         bulk_copy_s2cluster(map_shared_rank(dst, 0), src, 16,
                                             map_shared_rank(fb, 0));
-                        bulk_copy_s2cluster(map_shared_rank(dst, 1), src, 16,
-                                            map_shared_rank(fb, 1));
+                        if constexpr (CG == 2)
+                            bulk_copy_s2cluster(map_shared_rank(dst, 1), src, 16,
+                                                map_shared_rank(fb, 1));
                     }
                 }
-                const int32_t arow = mb * C::PAIR_M + (int32_t)rank * BLOCK_M;
-                const int32_t brow =
-                    C::DUAL ? nb * C::OUT_N : nb * BN + (int32_t)rank * C::B_ROWS;
+                const int32_t arow = mb * C::TILE_M + (int32_t)rank * BLOCK_M;
+                const int32_t brow = nb * C::OUT_N + (C::DUAL ? 0 : (int32_t)rank * C::B_ROWS);
                 const bool down = p.k_snake && ((un.tile / num_pairs) & 1);
                 for (int i = 0; i < un.k1 - un.k0; ++i) {
                     const int kb = down ? un.k1 - 1 - i : un.k0 + i;
@@ -409,21 +413,29 @@ __global__ void __launch_bounds__(MlpConfig<KD, BN, AM, BM, EP>::NUM_THREADS, 1)
                     const CUtensorMap *ma = &maps.a[second || bt ? 1 : 0];
                     const CUtensorMap *mb_ = &maps.b[(C::DUAL ? rank != 0 : second) ? 1 : 0];
                     if (!pair_wait(bar(C::EMPTY0 + s), ph ^ 1, ctl, SITE_EMPTY)) { ok = false; break; }
-                    const uint32_t full = map_shared_rank(bar(C::FULL0 + s), 0);
-                    if (leader) mbar_arrive_expect_tx(bar(C::FULL0 + s), 2 * (C::A_BYTES + C::B_BYTES));
+                    const uint32_t full =
+                        CG == 2 ? map_shared_rank(bar(C::FULL0 + s), 0) : bar(C::FULL0 + s);
+                    if (leader)
+                        mbar_arrive_expect_tx(bar(C::FULL0 + s), CG * (C::A_BYTES + C::B_BYTES));
+                    auto load = [&](uint32_t dst, const CUtensorMap *map, int32_t x, int32_t y) {
+                        if constexpr (CG == 2) tma_load_2d_pair(dst, map, full, x, y);
+                        else tma_load_2d(dst, map, full, x, y);
+                    };
                     if constexpr (AM == 0) {
-                        tma_load_2d_pair(a_stage(s), ma, full, kc, arow);
+                        load(a_stage(s), ma, kc, arow);
                     } else {
 #pragma unroll
                         for (int q = 0; q < BLOCK_M / 64; ++q)
-                            tma_load_2d_pair(a_stage(s) + q * 8192, ma, full, arow + q * 64, kc);
+                            load(a_stage(s) + q * 8192, ma, arow + q * 64, kc);
                     }
                     if constexpr (BM == 0) {
-                        tma_load_2d_pair(b_stage(s), mb_, full, kc, brow);
+                        load(b_stage(s), mb_, kc, brow);
+                        if constexpr (C::DUAL && CG == 1)
+                            load(b_stage(s) + C::B_BYTES / 2, &maps.b[1], kc, brow);
                     } else {
 #pragma unroll
                         for (int q = 0; q < C::B_ROWS / 64; ++q)
-                            tma_load_2d_pair(b_stage(s) + q * 8192, mb_, full, brow + q * 64, kc);
+                            load(b_stage(s) + q * 8192, mb_, brow + q * 64, kc);
                     }
                     ++issued;
                     if (++s == S) { s = 0; ph ^= 1; }
@@ -445,6 +457,10 @@ __global__ void __launch_bounds__(MlpConfig<KD, BN, AM, BM, EP>::NUM_THREADS, 1)
             uint32_t tl = 0;
             bool ok = true;
             int64_t step = 0;
+            auto commit = [&](uint32_t b) {  // an arrival in every CTA of the team
+                if constexpr (CG == 2) mma_commit_pair_mcast(b, (uint16_t)0x3);
+                else mma_commit(b);
+            };
             for (int64_t u = pair; ok && u >= 0 && u < up.units; ++tl) {
                 const Unit un = decode_unit(up, u, nkb);
                 const uint32_t acc = tl & 1, use = tl >> 1;
@@ -466,17 +482,19 @@ __global__ void __launch_bounds__(MlpConfig<KD, BN, AM, BM, EP>::NUM_THREADS, 1)
                                                : smem_desc_sw128(a0 + kk * 32);
                         const uint64_t bd = BM ? smem_desc_mn_sw128(b0 + kk * 2048)
                                                : smem_desc_sw128(b0 + kk * 32);
-                        mma_f16_pair(d_tmem, ad, bd, C::IDESC, (i != 0) || (kk != 0));
+                        if constexpr (CG == 2) mma_f16_pair(d_tmem, ad, bd, C::IDESC, (i != 0) || (kk != 0));
+                        else mma_f16(d_tmem, ad, bd, C::IDESC, (i != 0) || (kk != 0));
                     }
-                    mma_commit_pair_mcast(bar(C::EMPTY0 + s), (uint16_t)0x3);
+                    commit(bar(C::EMPTY0 + s));
                     if (++s == S) { s = 0; ph ^= 1; }
                 }
                 if (!ok) break;
-                mma_commit_pair_mcast(bar(C::ACCF0 + acc), (uint16_t)0x3);
+                commit(bar(C::ACCF0 + acc));
                 u = tick ? tk_read(step++) : u + num_pairs;
             }
             if (!ok) {
-                mma_commit_pair_mcast(bar(C::DRAIN), (uint16_t)1);
+                if constexpr (CG == 2) mma_commit_pair_mcast(bar(C::DRAIN), (uint16_t)1);
+                else mma_commit(bar(C::DRAIN));
                 const uint64_t t0 = globaltimer_ns();
                 while (!mbar_try_wait(bar(C::DRAIN), 0)) {
                     if (globaltimer_ns() - t0 > p.wait_limit_ns) {
@@ -495,11 +513,12 @@ __global__ void __launch_bounds__(MlpConfig<KD, BN, AM, BM, EP>::NUM_THREADS, 1)
         constexpr int EPI_THREADS = C::EPI_WARPS * 32;
         const int etid = threadIdx.x - 64;
         constexpr int COLS = C::COLS;
-        constexpr int CW = C::STG_ROW / 2;  // 16-bit columns of a staged row
         const int cbase = (ew / 4) * COLS;
-        uint8_t *stg = smem + C::STG_OFF + ew * C::STG_BYTES;
-        const uint32_t stg_s = smem_u32(stg);
-        uint32_t res_phase = 0;
+        // Two staging buffers, used in turn: `cur` is the next one to fill.
+        uint8_t *const stg0 = smem + C::STG_OFF + ew * 2 * C::STG_BYTES;
+        float4 *const bias_s = reinterpret_cast<float4 *>(smem + C::BIAS_OFF + ew * 128);
+        uint32_t cur = 0;
+        uint32_t res_phase = 0;  // one bit per buffer
         uint32_t tl = 0;
         int64_t step = 0;
         bool alive = true;
@@ -514,26 +533,27 @@ __global__ void __launch_bounds__(MlpConfig<KD, BN, AM, BM, EP>::NUM_THREADS, 1)
             int bt, mb, nb;
             batch_tile_coords(un.tile, p, bt, mb, nb);
             const uint32_t acc = tl & 1, use = tl >> 1;
-            const int32_t row0 = mb * C::PAIR_M + (int32_t)rank * BLOCK_M + q * 32;
+            const int32_t row0 = mb * C::TILE_M + (int32_t)rank * BLOCK_M + q * 32;
             const int32_t colw = nb * C::OUT_N + cbase;  // first output column of this warp
             const bool writer = un.seg >= 0 && un.seg < up.segs - 1;
             const bool finisher = un.seg >= 0 && !writer;
 
-            // Ask for the first residual box while the MMAs still run.
-            auto ask_residual = [&](int32_t col) {
+            // Ask for the residual box at column `col` into buffer `at`, whose
+            // last store, if any, must have left it (wait: all stores so far).
+            auto ask_residual = [&](int32_t col, uint32_t at) {
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
-                    bulk_wait_read();
-                    mbar_arrive_expect_tx(bar(C::RES0 + ew), C::STG_BYTES);
-                    tma_load_2d(stg_s, &maps.r, bar(C::RES0 + ew), col, row0);
+                    bulk_wait_read<0>();
+                    const uint32_t b = bar(C::RES0 + 2 * ew + at);
+                    mbar_arrive_expect_tx(b, C::STG_BYTES);
+                    tma_load_2d(smem_u32(stg0 + at * C::STG_BYTES), &maps.r, b, col, row0);
                 }
             };
             bool asked = false;
             if constexpr (EP == MlpEpi::LINEAR) {
-                // Z goes through the same buffer first when it is saved.
                 if (mp.r && mp.r_tma && !mp.out[1].ptr && !writer && row0 < p.m && colw < p.n) {
-                    ask_residual(colw);
+                    ask_residual(colw, cur);
                     asked = true;
                 }
             }
@@ -550,10 +570,10 @@ __global__ void __launch_bounds__(MlpConfig<KD, BN, AM, BM, EP>::NUM_THREADS, 1)
             const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + acc * BN;
             auto part = [&](int32_t k) -> float * {
                 const int64_t pidx = un.tail * (up.segs - 1) + k;
-                return p.ws + ((pidx * 2 + rank) * BN) * (int64_t)BLOCK_M + q * 32 + lane;
+                return p.ws + ((pidx * CG + rank) * BN) * (int64_t)BLOCK_M + q * 32 + lane;
             };
             auto flag = [&](int32_t k) -> uint32_t * {
-                return p.flags + (un.tail * (up.segs - 1) + k) * 2 + rank;
+                return p.flags + (un.tail * (up.segs - 1) + k) * CG + rank;
             };
             if (writer) {
                 float *dst = part(un.seg);
@@ -606,168 +626,187 @@ __global__ void __launch_bounds__(MlpConfig<KD, BN, AM, BM, EP>::NUM_THREADS, 1)
 #pragma unroll
                     for (int j = 0; j < 32; ++j) y[j] = __uint_as_float(v[j]);
                     if (finisher) {
-                        for (int32_t k = 0; k < up.segs - 1; ++k) {
-                            const float *src = part(k) + (int64_t)c0 * BLOCK_M;
+                        // All segments' loads of these columns at once: one
+                        // round trip to L2, not one per segment.
+                        const int32_t parts = up.segs - 1;
+                        float w[SPLIT_PARTS][32];
 #pragma unroll
-                            for (int j = 0; j < 32; ++j) y[j] += __ldcg(src + (int64_t)j * BLOCK_M);
+                        for (int k = 0; k < SPLIT_PARTS; ++k) {
+                            const float *src = part(k < parts ? k : 0) + (int64_t)c0 * BLOCK_M;
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                w[k][j] = k < parts ? __ldcg(src + (int64_t)j * BLOCK_M) : 0.0f;
                         }
+#pragma unroll
+                        for (int k = 0; k < SPLIT_PARTS; ++k)
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) y[j] += w[k][j];
                     }
                 };
                 auto stg16 = [&](int piece) -> uint4 * {
-                    return reinterpret_cast<uint4 *>(stg + stg_offset<C::STG_ROW>(lane, piece * 16));
+                    return reinterpret_cast<uint4 *>(stg0 + cur * C::STG_BYTES +
+                                                     stg_offset(lane, piece * 16));
                 };
+                // Buffer `cur` may be written: its store, the one before the
+                // last, has left it.
                 auto free_stg = [&]() {
-                    if (lane == 0) bulk_wait_read();
+                    if (lane == 0) bulk_wait_read<1>();
                     __syncwarp();
                 };
-                // The staged box goes out as columns col.. of output o.
+                // Buffer `cur` goes out as columns col.. of output o.
                 auto send = [&](int o, int32_t col) {
-                    const int wide = EP == MlpEpi::PLAIN && mp.out_f32 ? C::STG_ROW / 4 : CW;
-                    if (mp.out[o].tma && (mp.clip || col + wide <= p.n)) {
+                    const bool f32 = EP == MlpEpi::PLAIN && mp.out_f32;
+                    uint8_t *stg = stg0 + cur * C::STG_BYTES;
+                    if (mp.out[o].tma && (mp.clip || col + (f32 ? 16 : 32) <= p.n)) {
                         fence_proxy_async_smem();
                         __syncwarp();
-                        if (lane == 0) {
-                            tma_store_2d(&maps.out[o], stg_s, col, row0);
-                            bulk_commit();
-                        }
+                        if (lane == 0) tma_store_2d(&maps.out[o], smem_u32(stg), col, row0);
                     } else {
                         __syncwarp();
-                        if (EP == MlpEpi::PLAIN && mp.out_f32)
-                            stg_to_global<C::STG_ROW, float>(stg, static_cast<float *>(mp.out[o].ptr),
+                        if (f32)
+                            stg_to_global<float>(stg, static_cast<float *>(mp.out[o].ptr),
                                                  mp.out[o].ld, row0, col, p.m, p.n, lane);
                         else
-                            stg_to_global<C::STG_ROW, uint16_t>(stg, static_cast<uint16_t *>(mp.out[o].ptr),
+                            stg_to_global<uint16_t>(stg, static_cast<uint16_t *>(mp.out[o].ptr),
                                                     mp.out[o].ld, row0, col, p.m, p.n, lane);
                         __syncwarp();
                     }
+                    if (lane == 0) bulk_commit();  // one group per buffer filled
+                    cur ^= 1;
                 };
-                // Pack 32 values as half `h` of a 64-column 16-bit row.
-                auto put = [&](int h, const float (&y)[32]) {
+                // 32 values as a 16-bit staged row.
+                auto put = [&](const float (&y)[32]) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        *stg16(h * 4 + j) = make_uint4(mlp_pack2<KD>(y[8 * j], y[8 * j + 1]),
-                                                       mlp_pack2<KD>(y[8 * j + 2], y[8 * j + 3]),
-                                                       mlp_pack2<KD>(y[8 * j + 4], y[8 * j + 5]),
-                                                       mlp_pack2<KD>(y[8 * j + 6], y[8 * j + 7]));
+                        *stg16(j) = make_uint4(mlp_pack2<KD>(y[8 * j], y[8 * j + 1]),
+                                               mlp_pack2<KD>(y[8 * j + 2], y[8 * j + 3]),
+                                               mlp_pack2<KD>(y[8 * j + 4], y[8 * j + 5]),
+                                               mlp_pack2<KD>(y[8 * j + 6], y[8 * j + 7]));
                 };
                 const bool rows_in = ready && row0 < p.m;
                 if constexpr (EP == MlpEpi::LINEAR) {
-                    auto add_bias = [&](int32_t col, float (&y)[32]) {
-                        if (mp.bias) {
-                            const float b = col + lane < p.n ? __ldg(mp.bias + col + lane) : 0.0f;
-#pragma unroll
-                            for (int j = 0; j < 32; ++j) y[j] += __shfl_sync(0xffffffffu, b, j);
-                        }
-                    };
 #pragma unroll 1
-                    for (int c = 0; c < COLS && rows_in && colw + c < p.n; c += CW) {
+                    for (int c = 0; c < COLS && rows_in && colw + c < p.n; c += 32) {
                         const int32_t col = colw + c;
+                        float y[32];
+                        if (mp.bias) {
+                            __syncwarp();
+                            reinterpret_cast<float *>(bias_s)[lane] =
+                                col + lane < p.n ? __ldg(mp.bias + col + lane) : 0.0f;
+                            __syncwarp();
+                        }
+                        load_acc(cbase + c, y);
+                        if (mp.bias) {
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) {
+                                const float4 b = bias_s[j];
+                                y[4 * j] += b.x;
+                                y[4 * j + 1] += b.y;
+                                y[4 * j + 2] += b.z;
+                                y[4 * j + 3] += b.w;
+                            }
+                        }
                         if (mp.out[1].ptr) {
                             free_stg();
-#pragma unroll 1
-                            for (int h = 0; h < CW / 32; ++h) {
-                                float y[32];
-                                load_acc(cbase + c + h * 32, y);
-                                add_bias(col + h * 32, y);
-                                put(h, y);
-                            }
+                            put(y);
                             send(1, col);
                         }
-                        if (mp.r && mp.r_tma) {
-                            if (!asked) ask_residual(col);
-                            asked = false;
-                            const bool landed =
-                                pair_wait(bar(C::RES0 + ew), res_phase, ctl, SITE_RESIDUAL);
-                            res_phase ^= 1;
+                        const bool r_tma = mp.r && mp.r_tma;
+                        if (r_tma) {
+                            // With Z both buffers turn over every 32 columns, so
+                            // the box is asked for here; else it was asked for one
+                            // step ago, and the next one goes out now.
+                            if (!asked) ask_residual(col, cur);
+                            asked = !mp.out[1].ptr && c + 32 < COLS && col + 32 < p.n;
+                            if (asked) ask_residual(col + 32, cur ^ 1);
+                        }
+                        mlp_with_act(mp.act, [&](auto a) {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) y[j] = mlp_act<a.value>(y[j]);
+                        });
+                        if (r_tma) {
+                            const bool landed = pair_wait(bar(C::RES0 + 2 * ew + cur),
+                                                          (res_phase >> cur) & 1, ctl, SITE_RESIDUAL);
+                            res_phase ^= 1u << cur;
                             if (!__all_sync(0xffffffffu, landed)) {
                                 pair_pause_ns(200000);
+                                asked = false;
                                 alive = false;
                                 break;
                             }
                         } else {
                             free_stg();
                             if (mp.r) {
-                                global_to_stg<C::STG_ROW>(stg, static_cast<const uint16_t *>(mp.r), mp.ldr, row0,
-                                              col, p.m, p.n, lane);
+                                global_to_stg(stg0 + cur * C::STG_BYTES,
+                                              static_cast<const uint16_t *>(mp.r), mp.ldr, row0, col,
+                                              p.m, p.n, lane);
                                 __syncwarp();
                             }
                         }
-#pragma unroll 1
-                        for (int h = 0; h < CW / 32; ++h) {
-                            float y[32];
-                            load_acc(cbase + c + h * 32, y);
-                            add_bias(col + h * 32, y);
-                            mlp_with_act(mp.act, [&](auto a) {
+                        if (mp.r) {
 #pragma unroll
-                                for (int j = 0; j < 32; ++j) y[j] = mlp_act<a.value>(y[j]);
-                            });
-                            if (mp.r) {
+                            for (int j = 0; j < 4; ++j) {
+                                const uint4 w = *stg16(j);
+                                const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-                                for (int j = 0; j < 4; ++j) {
-                                    const uint4 w = *stg16(h * 4 + j);
-                                    const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                                    for (int e = 0; e < 4; ++e) {
-                                        y[8 * j + 2 * e] += mlp_to_float<KD>(ws[e] & 0xffffu);
-                                        y[8 * j + 2 * e + 1] += mlp_to_float<KD>(ws[e] >> 16);
-                                    }
+                                for (int e = 0; e < 4; ++e) {
+                                    y[8 * j + 2 * e] += mlp_to_float<KD>(ws[e] & 0xffffu);
+                                    y[8 * j + 2 * e + 1] += mlp_to_float<KD>(ws[e] >> 16);
                                 }
                             }
-                            put(h, y);
                         }
+                        put(y);
                         send(0, col);
                     }
                 } else if constexpr (EP == MlpEpi::GATED) {
                     constexpr int UP = BN / 2;  // accumulator column of the up half
 #pragma unroll 1
-                    for (int c = 0; c < COLS && rows_in && colw + c < p.n; c += CW) {
+                    for (int c = 0; c < COLS && rows_in && colw + c < p.n; c += 32) {
                         const int32_t col = colw + c;
-#pragma unroll 1
-                        for (int o = 1; o < 3; ++o) {
-                            if (!mp.out[o].ptr) continue;
+                        float y[32], w[32];
+                        load_acc(cbase + c, y);
+                        load_acc(UP + cbase + c, w);
+                        if (mp.out[1].ptr) {
                             free_stg();
-#pragma unroll 1
-                            for (int h = 0; h < CW / 32; ++h) {
-                                float y[32];
-                                load_acc((o - 1) * UP + cbase + c + h * 32, y);
-                                put(h, y);
-                            }
-                            send(o, col);
+                            put(y);
+                            send(1, col);
                         }
-                        free_stg();
-#pragma unroll 1
-                        for (int h = 0; h < CW / 32; ++h) {
-                            float y[32], w[32];
-                            load_acc(cbase + c + h * 32, y);
-                            load_acc(UP + cbase + c + h * 32, w);
-                            mlp_with_act(mp.act, [&](auto a) {
+                        if (mp.out[2].ptr) {
+                            free_stg();
+                            put(w);
+                            send(2, col);
+                        }
+                        mlp_with_act(mp.act, [&](auto a) {
 #pragma unroll
-                                for (int j = 0; j < 32; ++j) y[j] = mlp_act<a.value>(y[j]) * w[j];
-                            });
-                            put(h, y);
-                        }
+                            for (int j = 0; j < 32; ++j) y[j] = mlp_act<a.value>(y[j]) * w[j];
+                        });
+                        free_stg();
+                        put(y);
                         send(0, col);
                     }
                 } else {
-                    const int cw = mp.out_f32 ? CW / 2 : CW;
 #pragma unroll 1
-                    for (int c = 0; c < COLS && rows_in && colw + c < p.n; c += cw) {
-                        free_stg();
-#pragma unroll 1
-                        for (int h = 0; h < cw / 32; ++h) {
-                            float y[32];
-                            load_acc(cbase + c + h * 32, y);
-                            if (mp.out_f32) {
+                    for (int c = 0; c < COLS && rows_in && colw + c < p.n; c += 32) {
+                        float y[32];
+                        load_acc(cbase + c, y);
+                        if (mp.out_f32) {
 #pragma unroll
-                                for (int j = 0; j < 8; ++j)
-                                    *stg16(j) = make_uint4(
-                                        __float_as_uint(y[4 * j]), __float_as_uint(y[4 * j + 1]),
-                                        __float_as_uint(y[4 * j + 2]), __float_as_uint(y[4 * j + 3]));
-                            } else {
-                                put(h, y);
+                            for (int h = 0; h < 2; ++h) {
+                                if (colw + c + 16 * h >= p.n) break;
+                                free_stg();
+#pragma unroll
+                                for (int j = 0; j < 4; ++j)
+                                    *stg16(j) = make_uint4(__float_as_uint(y[16 * h + 4 * j]),
+                                                           __float_as_uint(y[16 * h + 4 * j + 1]),
+                                                           __float_as_uint(y[16 * h + 4 * j + 2]),
+                                                           __float_as_uint(y[16 * h + 4 * j + 3]));
+                                send(bt, colw + c + 16 * h);
                             }
+                        } else {
+                            free_stg();
+                            put(y);
+                            send(bt, colw + c);
                         }
-                        send(bt, colw + c);
                     }
                 }
                 if (finisher) {
@@ -789,10 +828,12 @@ __global__ void __launch_bounds__(MlpConfig<KD, BN, AM, BM, EP>::NUM_THREADS, 1)
     }
 
     tc_fence_before();
-    cluster_sync_all();
+    if constexpr (CG == 2) cluster_sync_all();
+    else __syncthreads();
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc_pair(tmem_base, C::TMEM_COLS);
+        if constexpr (CG == 2) tmem_dealloc_pair(tmem_base, C::TMEM_COLS);
+        else tmem_dealloc(tmem_base, C::TMEM_COLS);
     }
 }
 

@@ -8,8 +8,10 @@
 // 128-row operand and the tokens the NT-column one (NT = 16, 32, 64 or 128,
 // zero rows beyond the tokens), so every weight byte crosses shared memory
 // once and the accumulator wastes columns, which cost nothing, instead of
-// rows.  One CTA per SM keeps a ring of up to 12 stages (180-200 KB) of TMA
-// loads in flight: 6.7 TB/s at about 1 us of latency needs 44 KB per SM.
+// rows.  One CTA per SM keeps a ring of 100 KB (200 KB for 64 tokens and more) of
+// TMA loads in flight: 6.7 TB/s at about 1 us of latency needs 44 KB per SM.  With
+// the small ring the next kernel's CTA fits beside this one: its set-up and an
+// L2 prefetch of its first weights run under this kernel's end.
 //
 // Work split: the (tile, K block) iterations of all 128-feature tiles are cut
 // into equal contiguous shares, one per CTA, so that 112 tiles (say) load 152
@@ -38,8 +40,12 @@ struct StreamConfig {
     static constexpr int A_BYTES = BLOCK_M * ROW_BYTES;
     static constexpr int B_BYTES = NT * ROW_BYTES;
     static constexpr int STAGE_BYTES = MATS * A_BYTES + B_BYTES;
-    static constexpr int FIT = (SMEM_LIMIT - 2048) / STAGE_BYTES;
+    // Up to 32 tokens a ring of about 100 KB (two CTAs to an SM), else all of
+    // shared memory.
+    static constexpr int BUDGET = NT <= 32 ? SMEM_LIMIT / 2 - 1024 : SMEM_LIMIT;
+    static constexpr int FIT = (BUDGET - 2048) / STAGE_BYTES;
     static constexpr int STAGES = FIT > 12 ? 12 : FIT;
+    static constexpr int PREFETCH = 16 / MATS;  // K blocks prefetched into L2 (256 KB a CTA)
     static constexpr int BAR_OFF = STAGES * STAGE_BYTES;
     static constexpr int FULL0 = 0, EMPTY0 = STAGES, ACCF0 = 2 * STAGES, ACCE0 = ACCF0 + 2,
                          DRAIN = ACCE0 + 2, NUM_BARS = DRAIN + 1;
@@ -47,7 +53,7 @@ struct StreamConfig {
     static constexpr int SMEM_BYTES = MISC_OFF + 16 + 1024;
     static constexpr int ACC_COLS = MATS * NT;
     static constexpr int TMEM_COLS = 2 * ACC_COLS;
-    static constexpr int EPI_WARPS = 4;
+    static constexpr int EPI_WARPS = 8;  // two per tensor-memory lane quarter
     static constexpr int NUM_THREADS = (2 + EPI_WARPS) * 32;
     static constexpr int MMAS_PER_STAGE = BK / T::umma_k;
     static constexpr uint32_t IDESC = (1u << 4) | (T::fmt << 7) | (T::fmt << 10) |
@@ -69,7 +75,7 @@ struct StreamParams {
     int64_t ldr;
     MlpOut out[3];  // LINEAR: Y, Z; GATED: H, G, U
     float *ws;      // one slot of 128 x 256 floats per CTA
-    uint32_t *flags;  // four per CTA (one per epilogue warp), zero between launches
+    uint32_t *flags;  // eight per CTA (one per epilogue warp), zero between launches
     uint32_t *status;
     uint64_t wait_limit_ns;
 };
@@ -114,7 +120,7 @@ __device__ __forceinline__ uint16_t mlp_narrow(float y) {
 }
 
 template <Kind KD, int NT, bool DUAL>
-__global__ void __launch_bounds__(StreamConfig<KD, NT, DUAL>::NUM_THREADS, 1)
+__global__ void __launch_bounds__(StreamConfig<KD, NT, DUAL>::NUM_THREADS, NT <= 32 ? 2 : 1)
     tg_stream_kernel(const __grid_constant__ StreamMaps maps, const StreamParams p) {
     using C = StreamConfig<KD, NT, DUAL>;
     constexpr int S = C::STAGES;
@@ -161,6 +167,17 @@ __global__ void __launch_bounds__(StreamConfig<KD, NT, DUAL>::NUM_THREADS, 1)
 
     if (warp == 0) {
         if (lane == 0) {
+            // The first weights on their way into L2 while the kernel before
+            // this one ends: a prefetch consumes no value, so it may run ahead
+            // of whatever that kernel still writes.
+            {
+                StreamUnits un(p);
+                for (int left = C::PREFETCH; left > 0 && un.next(p);)
+                    for (int kb = un.k0; kb < un.k1 && left > 0; ++kb, --left) {
+                        tma_prefetch_l2_2d(&maps.w[0], kb * C::BK, un.t * BLOCK_M);
+                        if (DUAL) tma_prefetch_l2_2d(&maps.w[1], kb * C::BK, un.t * BLOCK_M);
+                    }
+            }
             griddep_wait();
             int s = 0;
             uint32_t ph = 0;
@@ -233,7 +250,9 @@ __global__ void __launch_bounds__(StreamConfig<KD, NT, DUAL>::NUM_THREADS, 1)
     } else {
         // ------------------------------------------------------ epilogue
         griddep_wait();
-        const int q = warp & 3;
+        // Warp: lane quarter q, tokens [16 h, 16 h + 16), [16 h + 32, ...).
+        const int q = warp & 3, h = (warp - 2) >> 2;
+        const int ew = warp - 2;
         uint32_t tl = 0;
         bool ok = true;
         StreamUnits un(p);
@@ -248,112 +267,136 @@ __global__ void __launch_bounds__(StreamConfig<KD, NT, DUAL>::NUM_THREADS, 1)
             if (un.k1 < nkb) {
                 float *dst = slot0 + (int64_t)blockIdx.x * SK_SLOT_FLOATS;
 #pragma unroll 1
-                for (int c0 = 0; c0 < C::ACC_COLS; c0 += 16) {
-                    const int j0 = c0 % NT;  // token of the chunk's first column
-                    if (j0 >= p.tokens) continue;
-                    uint32_t v[16];
-                    tmem_ld_32x32b_x16(taddr + c0, v);
+                for (int j0 = 16 * h; j0 < p.tokens; j0 += 32) {
+                    uint32_t v[C::MATS][16];
+#pragma unroll
+                    for (int a = 0; a < C::MATS; ++a) tmem_ld_32x32b_x16(taddr + a * NT + j0, v[a]);
                     tmem_ld_wait();
 #pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        if (j0 + j < p.tokens)
-                            __stcg(dst + (int64_t)(c0 + j) * BLOCK_M, __uint_as_float(v[j]));
+                    for (int a = 0; a < C::MATS; ++a)
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            if (j0 + j < p.tokens)
+                                __stcg(dst + (int64_t)(a * NT + j0 + j) * BLOCK_M,
+                                       __uint_as_float(v[a][j]));
                 }
                 __threadfence();
                 __syncwarp();
-                if (lane == 0) st_release_gpu_u32(p.flags + blockIdx.x * 4 + q, 1u);
+                // (a warp without tokens has no reader to put its flag back)
+                if (lane == 0 && 16 * h < p.tokens)
+                    st_release_gpu_u32(p.flags + blockIdx.x * 8 + ew, 1u);
             } else {
                 // The CTAs before this one that hold the tile's first K blocks.
-                int first = blockIdx.x;
-                if (un.k0 > 0) {
+                const int me = (int)blockIdx.x;
+                int first = me;
+                if (un.k0 > 0 && 16 * h < p.tokens) {
                     const int64_t total = (int64_t)p.tiles * nkb, base = (int64_t)un.t * nkb;
                     do {
                         --first;
                     } while (sk_start(total, first, gridDim.x) > base);
-                    if (lane == 0) {
-                        const uint64_t t0 = globaltimer_ns();
-                        for (int c = (int)blockIdx.x - 1; c >= first && ok; --c) {
-                            while (ld_acquire_gpu_u32(p.flags + c * 4 + q) == 0u) {
-                                if (*abort_flag || globaltimer_ns() - t0 > p.wait_limit_ns) {
-                                    if (!*abort_flag) {
-                                        *abort_flag = 1;
-                                        atomicCAS(p.status, 0u, (uint32_t)SITE_PARTIAL);
-                                    }
-                                    ok = false;
-                                    break;
+                    // One lane per flag.
+                    const uint64_t t0 = globaltimer_ns();
+                    for (int c = me - 1 - lane; c >= first && ok; c -= 32) {
+                        while (ld_acquire_gpu_u32(p.flags + c * 8 + ew) == 0u) {
+                            if (*abort_flag || globaltimer_ns() - t0 > p.wait_limit_ns) {
+                                if (!*abort_flag) {
+                                    *abort_flag = 1;
+                                    atomicCAS(p.status, 0u, (uint32_t)SITE_PARTIAL);
                                 }
+                                ok = false;
+                                break;
                             }
                         }
                     }
-                    ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+                    ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
-                    for (int c = first; c < (int)blockIdx.x; ++c)
-                        (void)ld_acquire_gpu_u32(p.flags + c * 4 + q);
+                    __threadfence();
+                    __syncwarp();
                 }
-                auto load_acc = [&](int c0, int j0, float (&y)[16]) {
-                    uint32_t v[16];
-                    tmem_ld_32x32b_x16(taddr + c0, v);
-                    tmem_ld_wait();
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) y[j] = __uint_as_float(v[j]);
-                    for (int c = (int)blockIdx.x - 1; c >= first; --c) {
-                        const float *src = slot0 + (int64_t)c * SK_SLOT_FLOATS + (int64_t)c0 * BLOCK_M;
-#pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            if (j0 + j < p.tokens) y[j] += __ldcg(src + (int64_t)j * BLOCK_M);
-                    }
-                };
                 const int32_t f = un.t * BLOCK_M + q * 32 + lane;
                 const bool in = f < p.features;
-                auto store = [&](int o, int j0, const float (&y)[16]) {
-                    if (!in) return;
-                    uint16_t *dst = static_cast<uint16_t *>(p.out[o].ptr) + (int64_t)j0 * p.out[o].ld + f;
-#pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        if (j0 + j < p.tokens) dst[(int64_t)j * p.out[o].ld] = mlp_narrow<KD>(y[j]);
-                };
                 const float b = (p.bias && in) ? __ldg(p.bias + f) : 0.0f;
+                // The epilogue of TC tokens from j0 on.
+                auto finish = [&](auto tc, int j0) {
+                    constexpr int TC = tc.value;
+                    // The tokens' sums: this CTA's and the partials, nearest
+                    // first, WAYS CTAs' loads in flight at once.
+                    constexpr int WAYS = TC == 4 ? 8 : 2;
+                    auto load_acc = [&](int a, float (&y)[TC]) {
+                        uint32_t v[16];
+                        tmem_ld_32x32b_x16(taddr + a * NT + j0, v);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int j = 0; j < TC; ++j) y[j] = __uint_as_float(v[j]);
 #pragma unroll 1
-                for (int j0 = 0; j0 < p.tokens; j0 += 16) {
-                    float y[16];
+                        for (int c = me - 1; c >= first; c -= WAYS) {
+                            float w[WAYS][TC];
+#pragma unroll
+                            for (int i = 0; i < WAYS; ++i) {
+                                const float *src = slot0 + (int64_t)(c - i) * SK_SLOT_FLOATS +
+                                                   (int64_t)(a * NT + j0) * BLOCK_M;
+#pragma unroll
+                                for (int j = 0; j < TC; ++j)
+                                    w[i][j] = c - i >= first && j0 + j < p.tokens
+                                                  ? __ldcg(src + (int64_t)j * BLOCK_M)
+                                                  : 0.0f;
+                            }
+#pragma unroll
+                            for (int i = 0; i < WAYS; ++i)
+#pragma unroll
+                                for (int j = 0; j < TC; ++j) y[j] += w[i][j];
+                        }
+                    };
+                    auto store = [&](int o, const float (&y)[TC]) {
+                        if (!in) return;
+                        uint16_t *dst = static_cast<uint16_t *>(p.out[o].ptr) + (int64_t)j0 * p.out[o].ld + f;
+#pragma unroll
+                        for (int j = 0; j < TC; ++j)
+                            if (j0 + j < p.tokens) dst[(int64_t)j * p.out[o].ld] = mlp_narrow<KD>(y[j]);
+                    };
+                    float y[TC];
                     if constexpr (DUAL) {
-                        float w[16];
-                        load_acc(j0, j0, y);
-                        load_acc(NT + j0, j0, w);
-                        if (p.out[1].ptr) store(1, j0, y);
-                        if (p.out[2].ptr) store(2, j0, w);
+                        float w[TC];
+                        load_acc(0, y);
+                        load_acc(1, w);
+                        if (p.out[1].ptr) store(1, y);
+                        if (p.out[2].ptr) store(2, w);
                         mlp_with_act(p.act, [&](auto a) {
 #pragma unroll
-                            for (int j = 0; j < 16; ++j) y[j] = mlp_act<a.value>(y[j]) * w[j];
+                            for (int j = 0; j < TC; ++j) y[j] = mlp_act<a.value>(y[j]) * w[j];
                         });
                     } else {
-                        uint16_t rr[16];
+                        uint16_t rr[TC];
                         if (p.r) {
                             const uint16_t *src = static_cast<const uint16_t *>(p.r) + (int64_t)j0 * p.ldr + f;
 #pragma unroll
-                            for (int j = 0; j < 16; ++j)
+                            for (int j = 0; j < TC; ++j)
                                 rr[j] = in && j0 + j < p.tokens ? src[(int64_t)j * p.ldr] : (uint16_t)0;
                         }
-                        load_acc(j0, j0, y);
+                        load_acc(0, y);
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) y[j] += b;
-                        if (p.out[1].ptr) store(1, j0, y);
+                        for (int j = 0; j < TC; ++j) y[j] += b;
+                        if (p.out[1].ptr) store(1, y);
                         mlp_with_act(p.act, [&](auto a) {
 #pragma unroll
-                            for (int j = 0; j < 16; ++j) y[j] = mlp_act<a.value>(y[j]);
+                            for (int j = 0; j < TC; ++j) y[j] = mlp_act<a.value>(y[j]);
                         });
                         if (p.r) {
 #pragma unroll
-                            for (int j = 0; j < 16; ++j) y[j] += mlp_to_float<KD>(rr[j]);
+                            for (int j = 0; j < TC; ++j) y[j] += mlp_to_float<KD>(rr[j]);
                         }
                     }
-                    store(0, j0, y);
+                    store(0, y);
+                };
+                if (p.tokens <= 4) {
+                    if (h == 0) finish(std::integral_constant<int, 4>{}, 0);
+                } else {
+#pragma unroll 1
+                    for (int j0 = 16 * h; j0 < p.tokens; j0 += 32)
+                        finish(std::integral_constant<int, 16>{}, j0);
                 }
-                if (un.k0 > 0) {
-                    __syncwarp();
-                    if (lane == 0)
-                        for (int c = first; c < (int)blockIdx.x; ++c) p.flags[c * 4 + q] = 0u;
-                }
+                __syncwarp();
+                for (int c = me - 1 - lane; c >= first; c -= 32) p.flags[c * 8 + ew] = 0u;
             }
             tc_fence_before();
             __syncwarp();

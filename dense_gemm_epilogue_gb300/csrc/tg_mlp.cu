@@ -279,39 +279,42 @@ struct Product {
     Mat r;             // residual (p NULL: none)
 };
 
-struct PairPlan {
-    int block_n;
+struct TilePlan {
+    int cg, block_n;
     int64_t tiles, tiles_per_entry;
     int grid, split_max, group;
     bool ticket;
 };
 
 // Times of the planner's cost model, in microseconds: one 64-deep K block of a
-// 256-row tile, and what a tile's epilogue or a split tile's join adds where
+// team's tile, and what a tile's epilogue or a split tile's join adds where
 // nothing overlaps it.
-constexpr double kBlock256 = 0.34, kBlock128 = 0.22;
-constexpr double kEpi256 = 4.0, kEpi128 = 2.5;
-constexpr double kJoin = 3.0, kJoinPart = 1.2;
-constexpr int kSplitMax = 4;
+struct TileCost {
+    int cg, bn;
+    double block, epilogue;
+};
+constexpr TileCost kTiles[] = {
+    {2, 256, 0.350, 4.5}, {2, 128, 0.286, 2.0}, {1, 256, 0.395, 4.5}, {1, 128, 0.283, 2.0}};
+constexpr double kJoin = 3.0, kJoinPart = 0.5;
+constexpr int kSplitMax = SPLIT_PARTS + 1;
 constexpr int64_t kMlpTicketWaves = 6;
 
-PairPlan plan_pair(const Product &q, int sms) {
+TilePlan plan_tiles(const Product &q, int sms) {
     const bool dual = q.op == MlpOp::GATED;
-    const int64_t pairs = sms / 2 > 0 ? sms / 2 : 1;
     const int64_t nkb = div_up(q.k[0], 64) + div_up(q.k[1], 64);
-    PairPlan best = {};
+    TilePlan best = {};
     double best_t = -1;
-    for (int bn : {256, 128}) {
-        const int64_t mb = div_up(q.m, 256), nb = div_up(q.n, dual ? bn / 2 : bn);
+    for (const TileCost &tc : kTiles) {
+        const int64_t teams = sms / tc.cg > 0 ? sms / tc.cg : 1;
+        const int64_t mb = div_up(q.m, 128 * tc.cg), nb = div_up(q.n, dual ? tc.bn / 2 : tc.bn);
         const int64_t tiles = q.entries * mb * nb;
-        const double blk = bn == 256 ? kBlock256 : kBlock128, epi = bn == 256 ? kEpi256 : kEpi128;
-        const int64_t rem = tiles % pairs;
-        const double whole = (double)(tiles / pairs) * nkb * blk;
-        double t = whole + (rem ? nkb * blk : 0.0) + epi;
+        const int64_t rem = tiles % teams;
+        const double whole = (double)(tiles / teams) * nkb * tc.block;
+        double t = whole + (rem ? nkb * tc.block : 0.0) + tc.epilogue;
         int split = 1;
         for (int s = 2; s <= kSplitMax && rem > 0; ++s) {
-            if (s > pairs / rem || s > nkb / SPLIT_MIN_KBLOCKS) break;
-            const double ts = whole + nkb * blk / s + epi + kJoin + kJoinPart * (s - 1);
+            if (s > teams / rem || s > nkb / SPLIT_MIN_KBLOCKS) break;
+            const double ts = whole + nkb * tc.block / s + tc.epilogue + kJoin + kJoinPart * (s - 1);
             if (ts < t) {
                 t = ts;
                 split = s;
@@ -319,29 +322,30 @@ PairPlan plan_pair(const Product &q, int sms) {
         }
         if (best_t >= 0 && t >= best_t) continue;
         best_t = t;
-        best.block_n = bn;
+        best.cg = tc.cg;
+        best.block_n = tc.bn;
         best.tiles = tiles;
         best.tiles_per_entry = mb * nb;
         best.split_max = split;
-        best.ticket = tiles >= kMlpTicketWaves * pairs;
-        // With a wave or more the grid is every pair; below that, one pair per
+        best.ticket = tiles >= kMlpTicketWaves * teams;
+        // With a wave or more the grid is every team; below that, one team per
         // tile and K segment.
-        best.grid = (int)(2 * (tiles >= pairs ? pairs : tiles * split));
-        const int64_t g = best.ticket ? 12 : 8;
+        best.grid = (int)(tc.cg * (tiles >= teams ? teams : tiles * split));
+        const int64_t g = (best.ticket ? 12 : 8) * 2 / tc.cg;
         best.group = (int)(mb < g ? mb : g);
     }
     return best;
 }
 
-// Outputs and the residual move in the staging buffers' boxes: 32 rows of 128
-// bytes, 64 for the gated 128-column tile.
-bool encode_out(CUtensorMap *map, const Mat &o, tg_dtype t, bool f32, bool narrow) {
+// Outputs and the residual move in the staging buffers' boxes: 32 rows of 64
+// bytes.
+bool encode_out(CUtensorMap *map, const Mat &o, tg_dtype t, bool f32) {
     return host::encode_rows(map, f32 ? TG_OUT_F32 : out_type(t), o.p, o.rows, o.cols, o.ld, 32,
-                             narrow ? 64 : 128);
+                             64);
 }
 
-tg_status run_pair(const Product &q, tg_dtype t, const Device &dev, cudaStream_t stream) {
-    const PairPlan plan = plan_pair(q, dev.sms);
+tg_status run_tiles(const Product &q, tg_dtype t, const Device &dev, cudaStream_t stream) {
+    const TilePlan plan = plan_tiles(q, dev.sms);
     MlpLaunch la;
     std::memset(&la, 0, sizeof(la));
     const bool am = q.op == MlpOp::WGRAD, bm = q.op == MlpOp::DGRAD || am;
@@ -352,20 +356,19 @@ tg_status run_pair(const Product &q, tg_dtype t, const Device &dev, cudaStream_t
         const Mat &a = q.a[i].p ? q.a[i] : q.a[0], &b = q.b[i].p ? q.b[i] : q.b[0];
         if (!host::encode_rows(&la.maps.a[i], ot, a.p, a.rows, a.cols, a.ld, am ? 64 : BLOCK_M) ||
             !host::encode_rows(&la.maps.b[i], ot, b.p, b.rows, b.cols, b.ld,
-                               bm ? 64 : plan.block_n / 2))
+                               bm ? 64 : q.op == MlpOp::GATED ? plan.block_n / 2 : plan.block_n / plan.cg))
             return TG_ERR_INVALID_VALUE;
     }
     MlpParams &p = la.p;
-    const bool narrow = q.op == MlpOp::GATED && plan.block_n == 128;
     p.clip = (q.n * (q.out_f32 ? 4 : 2)) % 16 == 0;
     for (int i = 0; i < 3; ++i) {
         p.out[i].ptr = const_cast<void *>(q.out[i].p);
         p.out[i].ld = q.out[i].ld;
-        p.out[i].tma = q.out[i].p && tma_ok(q.out[i]) && encode_out(&la.maps.out[i], q.out[i], t, q.out_f32, narrow);
+        p.out[i].tma = q.out[i].p && tma_ok(q.out[i]) && encode_out(&la.maps.out[i], q.out[i], t, q.out_f32);
     }
     p.r = q.r.p;
     p.ldr = q.r.ld;
-    p.r_tma = q.r.p && tma_ok(q.r) && encode_out(&la.maps.r, q.r, t, false, narrow);
+    p.r_tma = q.r.p && tma_ok(q.r) && encode_out(&la.maps.r, q.r, t, false);
     p.bias = q.bias;
     p.act = q.act;
     p.out_f32 = q.out_f32;
@@ -373,7 +376,7 @@ tg_status run_pair(const Product &q, tg_dtype t, const Device &dev, cudaStream_t
     GemmParams &g = p.g;
     g.m = (int32_t)q.m;
     g.n = (int32_t)q.n;
-    g.num_m_blocks = (int32_t)div_up(q.m, 256);
+    g.num_m_blocks = (int32_t)div_up(q.m, 128 * plan.cg);
     g.num_n_blocks = (int32_t)(plan.tiles_per_entry / g.num_m_blocks);
     g.num_k_blocks = (int32_t)nkb;
     g.raster_group = plan.group;
@@ -388,18 +391,21 @@ tg_status run_pair(const Product &q, tg_dtype t, const Device &dev, cudaStream_t
         const tg_status st = host::scratch(dev, stream, div_up(dev.sms, 2), &w);
         if (st != TG_OK) return st;
         g.split_max = plan.split_max;
-        g.ws_tiles = (int32_t)w.tiles;
+        g.ws_tiles = (int32_t)(w.tiles * 2 / plan.cg);
         g.ws = w.ws;
         g.flags = w.flags;
         g.k_snake = plan.ticket ? 1 : 0;
         if (plan.ticket) g.ticket = w.ticket;
     }
     la.op = q.op;
+    la.cg = plan.cg;
     la.block_n = plan.block_n;
     la.grid = plan.grid;
     la.device = dev.id;
     la.stream = stream;
-    const cudaError_t e = t == TG_BF16 ? launch_mlp_bf16(la) : launch_mlp_fp16(la);
+    const cudaError_t e =
+        t == TG_BF16 ? (plan.cg == 2 ? launch_mlp_bf16_cg2(la) : launch_mlp_bf16_cg1(la))
+                     : (plan.cg == 2 ? launch_mlp_fp16_cg2(la) : launch_mlp_fp16_cg1(la));
     return e == cudaSuccess ? TG_OK : TG_ERR_CUDA;
 }
 
@@ -491,7 +497,7 @@ tg_status forward(MlpOp op, int64_t M, int64_t N, int64_t K, Mat x, Mat w, Mat w
     q.b[0] = w;
     q.b[1] = w2;
     if (M <= kStreamTokens && K > 0) return run_stream(q, dtype, dev, stream);
-    return run_pair(q, dtype, dev, stream);
+    return run_tiles(q, dtype, dev, stream);
 }
 
 }  // namespace
@@ -632,7 +638,7 @@ extern "C" tg_status tg_linear_backward(int64_t M, int64_t N, int64_t K, const v
         q.a[0] = s.dz;
         q.b[0] = s.w;
         q.out[0] = mat(dX, lddx, M, K);
-        st = run_pair(q, dtype, dev, stream);
+        st = run_tiles(q, dtype, dev, stream);
         if (st != TG_OK) return st;
     }
     if (dw) {
@@ -646,7 +652,7 @@ extern "C" tg_status tg_linear_backward(int64_t M, int64_t N, int64_t K, const v
         q.b[0] = s.x;
         q.out[0] = mat(dW, lddw, N, K, ew);
         q.out_f32 = dw_dtype == TG_OUT_F32;
-        st = run_pair(q, dtype, dev, stream);
+        st = run_tiles(q, dtype, dev, stream);
         if (st != TG_OK) return st;
     }
     return TG_OK;
@@ -774,7 +780,7 @@ extern "C" tg_status tg_gated_backward(int64_t M, int64_t N, int64_t K, const vo
         q.b[0] = s.wg;
         q.b[1] = s.wu;
         q.out[0] = mat(dX, lddx, M, K);
-        st = run_pair(q, dtype, dev, stream);
+        st = run_tiles(q, dtype, dev, stream);
         if (st != TG_OK) return st;
     }
     if (dw) {
@@ -790,7 +796,7 @@ extern "C" tg_status tg_gated_backward(int64_t M, int64_t N, int64_t K, const vo
         q.out[0] = dWg ? mat(dWg, lddwg, N, K, ew) : mat(dWu, lddwu, N, K, ew);
         if (q.entries == 2) q.out[1] = mat(dWu, lddwu, N, K, ew);
         q.out_f32 = dw_dtype == TG_OUT_F32;
-        st = run_pair(q, dtype, dev, stream);
+        st = run_tiles(q, dtype, dev, stream);
         if (st != TG_OK) return st;
     }
     return TG_OK;

@@ -9,7 +9,7 @@
 
 namespace tg {
 
-// The products the CTA-pair kernel runs (operand majorness and epilogue).
+// The products the tile kernel runs (operand majorness and epilogue).
 enum class MlpOp : int {
     LINEAR = 0,  // K-major x K-major; bias, activation, residual, saved Z
     GATED = 1,   // K-major x two K-major; act(g) * u, saved G and U
@@ -21,8 +21,9 @@ struct MlpLaunch {
     MlpMaps maps;
     MlpParams p;
     MlpOp op;
+    int cg;        // CTAs per team (1 or 2)
     int block_n;
-    int grid;      // CTAs (even)
+    int grid;      // CTAs (a multiple of cg)
     int device;
     cudaStream_t stream;
 };
@@ -37,8 +38,10 @@ struct StreamLaunch {
     cudaStream_t stream;
 };
 
-cudaError_t launch_mlp_bf16(const MlpLaunch &a);
-cudaError_t launch_mlp_fp16(const MlpLaunch &a);
+cudaError_t launch_mlp_bf16_cg1(const MlpLaunch &a);
+cudaError_t launch_mlp_bf16_cg2(const MlpLaunch &a);
+cudaError_t launch_mlp_fp16_cg1(const MlpLaunch &a);
+cudaError_t launch_mlp_fp16_cg2(const MlpLaunch &a);
 cudaError_t launch_stream_bf16(const StreamLaunch &a);
 cudaError_t launch_stream_fp16(const StreamLaunch &a);
 
