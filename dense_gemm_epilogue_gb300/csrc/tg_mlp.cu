@@ -194,10 +194,8 @@ struct Mat {
 Mat mat(const void *p, int64_t ld, int64_t rows, int64_t cols, int e = 2) {
     return {p, rows <= 1 && ((uintptr_t)p % 16 == 0) ? round8(cols) : ld, rows, cols, e};
 }
-// TMA takes 16-byte aligned bases and rows (a single row's stride is free).
-bool tma_ok(const Mat &a) {
-    return (uintptr_t)a.p % 16 == 0 && (a.ld * a.e) % 16 == 0 && a.rows > 0 && a.cols > 0;
-}
+// Rows that TMA and 16-byte accesses can address (a single row's stride is free).
+bool aligned16(const Mat &a) { return (uintptr_t)a.p % 16 == 0 && (a.ld * a.e) % 16 == 0; }
 
 // The caller's workspace, handed out in 256-byte steps.  With no base it only
 // counts (the size queries).
@@ -218,7 +216,7 @@ struct Arena {
         return b;
     }
 };
-bool needs_repack(const Mat &a) { return a.rows > 0 && a.cols > 0 && !tma_ok(a); }
+bool needs_repack(const Mat &a) { return a.rows > 0 && a.cols > 0 && !aligned16(a); }
 
 // ------------------------------------------------------------------ launches
 
@@ -286,16 +284,20 @@ struct TilePlan {
     bool ticket;
 };
 
-// Times of the planner's cost model, in microseconds: one 64-deep K block of a
-// team's tile, and what a tile's epilogue or a split tile's join adds where
-// nothing overlaps it.
+// Times of the planner's cost model, in microseconds, measured on long and
+// short products of each tile shape: one 64-deep K block of a team's tile; what
+// its epilogue adds where nothing overlaps it; and what joining s segments adds
+// to a split tile (FP32 partial sums written, then s - 1 of them read back).
+// The 128-column tiles move 3/4 of the bytes per K block for half the work, so
+// they pay only where they fill SMs that 256-column tiles leave idle.
 struct TileCost {
     int cg, bn;
-    double block, epilogue;
+    double block, epilogue, join, join_part;
 };
-constexpr TileCost kTiles[] = {
-    {2, 256, 0.350, 4.5}, {2, 128, 0.286, 2.0}, {1, 256, 0.395, 4.5}, {1, 128, 0.283, 2.0}};
-constexpr double kJoin = 3.0, kJoinPart = 0.5;
+constexpr TileCost kTiles[] = {{2, 256, 0.350, 4.5, 5.0, 3.0},
+                               {2, 128, 0.286, 2.0, 3.0, 1.2},
+                               {1, 256, 0.395, 4.5, 5.0, 3.0},
+                               {1, 128, 0.283, 2.0, 3.0, 1.2}};
 constexpr int kSplitMax = SPLIT_PARTS + 1;
 constexpr int64_t kMlpTicketWaves = 6;
 
@@ -314,7 +316,7 @@ TilePlan plan_tiles(const Product &q, int sms) {
         int split = 1;
         for (int s = 2; s <= kSplitMax && rem > 0; ++s) {
             if (s > teams / rem || s > nkb / SPLIT_MIN_KBLOCKS) break;
-            const double ts = whole + nkb * tc.block / s + tc.epilogue + kJoin + kJoinPart * (s - 1);
+            const double ts = whole + nkb * tc.block / s + tc.epilogue + tc.join + tc.join_part * (s - 1);
             if (ts < t) {
                 t = ts;
                 split = s;
@@ -337,13 +339,6 @@ TilePlan plan_tiles(const Product &q, int sms) {
     return best;
 }
 
-// Outputs and the residual move in the staging buffers' boxes: 32 rows of 64
-// bytes.
-bool encode_out(CUtensorMap *map, const Mat &o, tg_dtype t, bool f32) {
-    return host::encode_rows(map, f32 ? TG_OUT_F32 : out_type(t), o.p, o.rows, o.cols, o.ld, 32,
-                             64);
-}
-
 tg_status run_tiles(const Product &q, tg_dtype t, const Device &dev, cudaStream_t stream) {
     const TilePlan plan = plan_tiles(q, dev.sms);
     MlpLaunch la;
@@ -360,15 +355,14 @@ tg_status run_tiles(const Product &q, tg_dtype t, const Device &dev, cudaStream_
             return TG_ERR_INVALID_VALUE;
     }
     MlpParams &p = la.p;
-    p.clip = (q.n * (q.out_f32 ? 4 : 2)) % 16 == 0;
     for (int i = 0; i < 3; ++i) {
         p.out[i].ptr = const_cast<void *>(q.out[i].p);
         p.out[i].ld = q.out[i].ld;
-        p.out[i].tma = q.out[i].p && tma_ok(q.out[i]) && encode_out(&la.maps.out[i], q.out[i], t, q.out_f32);
+        p.out[i].vec = q.out[i].p && aligned16(q.out[i]);
     }
     p.r = q.r.p;
     p.ldr = q.r.ld;
-    p.r_tma = q.r.p && tma_ok(q.r) && encode_out(&la.maps.r, q.r, t, false);
+    p.r_vec = q.r.p && aligned16(q.r);
     p.bias = q.bias;
     p.act = q.act;
     p.out_f32 = q.out_f32;
