@@ -8,19 +8,25 @@
 //
 // Bound: memory; forward reads and writes each row once, backward reads x and
 // dy and writes dx once.  A row stays in registers (16 elements a thread)
-// between its statistics and its output, so nothing is read twice; the
-// variance is the second moment about the mean just found, not a difference
-// of large sums.  A group of 32, 128, 256 or 512 threads takes a row of up to
-// 512, 2048, 4096 or 8192 columns; a cluster of 2, 4 or 8 blocks of 512
-// shares longer rows (to 65536) and adds its partial sums through distributed
-// shared memory.  All sums are FP32.
+// between its statistics and its output, so nothing is read twice; the variance
+// is the second moment about the mean just found, not a difference of large
+// sums.  A group of 32 to 512 threads takes a row of up to 16 elements each; a
+// cluster of 2, 4 or 8 blocks of 512 shares longer rows (to 65536) and adds its
+// partial sums through distributed shared memory.  All sums are FP32.
+//
+// On 16-bit rows what stands between a row and the memory's rate is the number
+// of instructions (a build with 8 elements a thread issued 36 per element
+// backward, 26 forward, and ran at 0.63 of the copy rate whatever the
+// occupancy).  So the arithmetic is on pairs of FP32 values (fma.rn.f32x2), rows
+// are copied by pointers that advance by a constant, forward takes two rows per
+// step through one reduction, and a thread holds 16 elements, over which a
+// reduction's shuffles spread.
 //
 // Backward keeps each thread's columns fixed over all rows of its group, so
-// the column sums dgamma and dbeta accumulate in registers and leave the block
-// once; tg_colsum_finish_kernel adds the blocks' partials in a fixed order.
-// No atomics: repeated calls agree bit for bit.  Two or three rows
-// are in flight behind the one in work (NormRows), so that their loads overlap
-// its reductions.
+// the column sums dgamma and dbeta accumulate in registers; the block's groups
+// add theirs in shared memory in order, and tg_colsum_finish_kernel adds the
+// blocks' partials in order.  No atomics: repeated calls agree bit for bit.
+// Two steps' rows are in flight behind the one in work (NormRows).
 #include <cuda_runtime.h>
 
 #include <atomic>
@@ -31,7 +37,44 @@
 
 namespace tg {
 
-constexpr int NORM_PER = 16;  // elements of a row per thread
+constexpr int NORM_PER = 16;   // elements of a row per thread
+constexpr int NORM_ROWS = 2;   // rows per step of the forward pass
+constexpr int NORM_DEPTH = 3;  // steps in the ring: one in work, two in flight
+constexpr int NORM_SM = 512;   // threads a SM (128 registers each)
+
+// Two FP32 values in one 64-bit register, and the arithmetic on both at once.
+struct F2 {
+    unsigned long long v;
+};
+__device__ __forceinline__ F2 f2(float a, float b) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ F2 f2(float a) { return f2(a, a); }
+__device__ __forceinline__ void f2_split(F2 x, float &a, float &b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x.v));
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+__device__ __forceinline__ float sum2(F2 x) {
+    float a, b;
+    f2_split(x, a, b);
+    return a + b;
+}
 
 struct NormParams {
     int64_t m, n;
@@ -47,7 +90,7 @@ struct NormParams {
     float inv_n;
 };
 
-// A thread's 16 elements of a row.  VEC: 16-byte vectors, vector v at column
+// A thread's elements of a row.  VEC: 16-byte vectors, vector v at column
 // (v * THREADS + t) * VW.  Else single elements, element i at i * THREADS + t.
 template <class Ty, int THREADS, bool VEC>
 struct NormCols {
@@ -55,19 +98,25 @@ struct NormCols {
     __device__ __forceinline__ static int at(int i, int t) {
         return VEC ? ((i / VW) * THREADS + t) * VW + i % VW : i * THREADS + t;
     }
-    __device__ __forceinline__ static void store(typename Ty::T *row, int t, int n,
-                                                 const float (&y)[NORM_PER]) {
+    // Elements 2i, 2i + 1 as pair i.
+    __device__ __forceinline__ static void store(typename Ty::T *row, int t, int n, bool whole,
+                                                 const F2 (&y)[NORM_PER / 2]) {
+        float e[NORM_PER];
+#pragma unroll
+        for (int i = 0; i < NORM_PER / 2; ++i) f2_split(y[i], e[2 * i], e[2 * i + 1]);
         if constexpr (VEC) {
+            typename Ty::T *q = row + t * VW;
 #pragma unroll
             for (int v = 0; v < NORM_PER / VW; ++v) {
                 const int c = (v * THREADS + t) * VW;
-                if (c < n) row_store<Ty>(row, c, n, y + v * VW);
+                if (whole) row_store_vec<Ty>(q + v * THREADS * VW, e + v * VW);
+                else if (c < n) row_store<Ty>(row, c, n, e + v * VW);
             }
         } else {
 #pragma unroll
             for (int i = 0; i < NORM_PER; ++i) {
                 const int c = i * THREADS + t;
-                if (c < n) row[c] = Ty::down(y[i]);
+                if (c < n) row[c] = Ty::down(e[i]);
             }
         }
     }
@@ -77,115 +126,155 @@ __device__ __forceinline__ void cp_async_16(uint32_t dst, const void *src, uint3
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
                  : "memory");
 }
+__device__ __forceinline__ void cp_async_4(uint32_t dst, const void *src, uint32_t bytes) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+                 : "memory");
+}
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Rows on their way: MATS matrices' rows r, r + groups, ... of this group.
-// VEC: each thread copies its own vectors into its own slots of a DEPTH-row
-// ring in shared memory (cp.async, zero fill past the row's end) and reads
-// them back itself, so no barrier is needed and DEPTH - 1 rows are in flight
-// without a register.  Else: one row ahead, in registers.
-template <class Ty, int THREADS, bool VEC, int MATS, int DEPTH>
+// Rows on their way: two rows per step (two rows of x, or a row of x and one
+// of dy), from pointers that advance by a constant.  Each thread copies its own
+// vectors (or FP32 elements) into its own slots of a ring in shared memory
+// (cp.async, zero fill past the row's end) and reads them back itself, so no
+// barrier is needed and NORM_DEPTH - 1 steps are in flight without a register.
+// 16-bit elements of rows that are not 16-byte aligned, which cp.async cannot
+// copy, come one step ahead in registers.
+template <class Ty, bool VEC>
+constexpr bool norm_async() {
+    return VEC || sizeof(typename Ty::T) == 4;
+}
+template <class Ty, int THREADS, int BLOCK, bool VEC>
 struct NormRows {
     using T = typename Ty::T;
     static constexpr int VW = Ty::VW, VECS = NORM_PER / VW;
-    const T *base[MATS];
-    int64_t ld[MATS];
-    int64_t m, groups;
-    int n, t, slot;
-    uint4 *ring;
-    T ahead[MATS][VEC ? 1 : NORM_PER];
+    static constexpr bool ASYNC = norm_async<Ty, VEC>();
+    static constexpr int PIECE = VEC ? 16 : 4, PIECES = VEC ? VECS : NORM_PER;
+    static constexpr int PIECE_COLS = VEC ? VW : 1;
+    static constexpr uint32_t STEP_BYTES = 2 * NORM_PER * BLOCK * (uint32_t)sizeof(T);
+    const T *ptr[2];  // this thread's first element of the next rows to ask for
+    int64_t hop[2];   // elements to the step after
+    int left[2];      // steps that still have such a row
+    int n, t;
+    uint32_t ring, fill, read;  // shared addresses: this thread's slots; next to fill, to read
+    T ahead[2][ASYNC ? 1 : NORM_PER];
 
-    __device__ __forceinline__ void ask(int64_t r, int at) {
-        if constexpr (VEC) {
-            if (r < m) {
+    __device__ __forceinline__ void set(int a, const T *base, int64_t ld, int64_t first,
+                                        int64_t step, int64_t m) {
+        ptr[a] = base + first * ld + t * PIECE_COLS;
+        hop[a] = step * ld;
+        left[a] = first < m ? (int)((m - first + step - 1) / step) : 0;
+    }
+    __device__ __forceinline__ void start(void *smem) {
+        ring = smem_u32(smem) + threadIdx.x * PIECE;
+        fill = read = ring;
 #pragma unroll
-                for (int a = 0; a < MATS; ++a) {
-                    const T *row = base[a] + r * ld[a];
+        for (int d = 0; d < (ASYNC ? NORM_DEPTH - 1 : 1); ++d) ask();
+    }
+    __device__ __forceinline__ void advance(uint32_t &at) {
+        at = at == ring + (NORM_DEPTH - 1) * STEP_BYTES ? ring : at + STEP_BYTES;
+    }
+    __device__ __forceinline__ void ask() {
 #pragma unroll
-                    for (int v = 0; v < VECS; ++v) {
-                        const int c = (v * THREADS + t) * VW;
-                        const int left = n - c;
-                        const uint32_t bytes =
-                            left >= VW ? 16u : (left > 0 ? (uint32_t)(left * (int)sizeof(T)) : 0u);
-                        cp_async_16(smem_u32(ring + ((at * MATS + a) * VECS + v) * blockDim.x + threadIdx.x),
-                                    left > 0 ? row + c : row, bytes);
+        for (int a = 0; a < 2; ++a) {
+            if (left[a] > 0) {
+                --left[a];
+                if constexpr (ASYNC) {
+#pragma unroll
+                    for (int v = 0; v < PIECES; ++v) {
+                        const int over = n - (v * THREADS + t) * PIECE_COLS;  // columns left here
+                        const uint32_t dst = fill + (a * PIECES + v) * BLOCK * PIECE;
+                        const T *src = ptr[a] + (over > 0 ? v * THREADS * PIECE_COLS : -t * PIECE_COLS);
+                        if constexpr (VEC)
+                            cp_async_16(dst, src, over >= VW ? 16u : over > 0 ? over * (uint32_t)sizeof(T) : 0u);
+                        else
+                            cp_async_4(dst, src, over > 0 ? 4u : 0u);
                     }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < NORM_PER; ++i)
+                        ahead[a][i] = i * THREADS + t < n ? __ldcs(ptr[a] + i * THREADS) : (T)0;
                 }
+                ptr[a] += hop[a];
             }
+        }
+        if constexpr (ASYNC) {
             cp_async_commit();
-        } else {
-            if (r < m) {
+            advance(fill);
+        }
+    }
+    // The values of the next step, as pairs, with the step after the last one
+    // asked for set off.  (A row past the last leaves stale values: the caller
+    // drops them.)
+    __device__ __forceinline__ void take(F2 (&y)[2][NORM_PER / 2]) {
+        if constexpr (ASYNC) {
+            cp_async_wait<NORM_DEPTH - 2>();
 #pragma unroll
-                for (int a = 0; a < MATS; ++a) {
-                    const T *row = base[a] + r * ld[a];
+            for (int a = 0; a < 2; ++a) {
 #pragma unroll
-                    for (int i = 0; i < NORM_PER; ++i) {
-                        const int c = i * THREADS + t;
-                        ahead[a][i] = c < n ? __ldcs(row + c) : (T)0;
+                for (int v = 0; v < PIECES; ++v) {
+                    const uint32_t src = read + (a * PIECES + v) * BLOCK * PIECE;
+                    if constexpr (VEC) {
+                        uint4 w;
+                        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                     : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+                                     : "r"(src)
+                                     : "memory");
+                        float e[VW];
+                        row_unpack<Ty>(w, e);
+#pragma unroll
+                        for (int i = 0; i < VW / 2; ++i) y[a][v * VW / 2 + i] = f2(e[2 * i], e[2 * i + 1]);
+                    } else if (v % 2 == 0) {
+                        float e0, e1;
+                        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(e0) : "r"(src) : "memory");
+                        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(e1) : "r"(src + BLOCK * PIECE) : "memory");
+                        y[a][v / 2] = f2(e0, e1);
                     }
                 }
             }
-        }
-    }
-    __device__ __forceinline__ void start(int64_t first) {
-        slot = 0;
-#pragma unroll
-        for (int d = 0; d < (VEC ? DEPTH - 1 : 1); ++d) ask(first + d * groups, d);
-    }
-    // This row's values, with the row after the last one asked for set off.
-    __device__ __forceinline__ void take(int64_t r, float (&y)[MATS][NORM_PER]) {
-        if constexpr (VEC) {
-            cp_async_wait<DEPTH - 2>();
-#pragma unroll
-            for (int a = 0; a < MATS; ++a)
-#pragma unroll
-                for (int v = 0; v < VECS; ++v)
-                    row_unpack<Ty>(ring[((slot * MATS + a) * VECS + v) * blockDim.x + threadIdx.x],
-                                   y[a] + v * VW);
-            ask(r + (DEPTH - 1) * groups, slot == 0 ? DEPTH - 1 : slot - 1);
-            slot = slot + 1 == DEPTH ? 0 : slot + 1;
+            advance(read);
         } else {
 #pragma unroll
-            for (int a = 0; a < MATS; ++a)
+            for (int a = 0; a < 2; ++a)
 #pragma unroll
-                for (int i = 0; i < NORM_PER; ++i) y[a][i] = Ty::up(ahead[a][i]);
-            ask(r + groups, 0);
+                for (int i = 0; i < NORM_PER / 2; ++i)
+                    y[a][i] = f2(Ty::up(ahead[a][2 * i]), Ty::up(ahead[a][2 * i + 1]));
         }
+        ask();
     }
 };
 
-constexpr int NORM_DEPTH = 4, NORM_BACK_DEPTH = 3;
-
-__device__ __forceinline__ float2 warp_sum2(float2 v) {
+template <int LANES>
+__device__ __forceinline__ float2 lanes_sum2(float2 v) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
+    for (int o = LANES / 2; o > 0; o >>= 1) {
         v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
         v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
     }
     return v;
 }
 
-// Sum of two values over the group of TR threads, times the cluster's CS
-// blocks.  `turn` alternates between two buffers, so one barrier per call
-// suffices: a buffer is written again two calls later, after every reader
-// has passed the barrier in between.
-template <int TR, int CS>
+// Sum of two values over a group of TR threads, times the cluster's CS blocks.
+// `turn` alternates between two buffers, so one barrier per call suffices: a
+// buffer is written again two calls later, after every reader has passed the
+// barrier in between.
+template <int TR, int BLOCK, int CS>
 struct GroupSum {
-    float2 *warps;   // [2][16]
+    float2 *warps;   // [2][32]
     float2 *blocks;  // [2][8]
     int turn;
     __device__ __forceinline__ float2 operator()(float2 v) {
-        v = warp_sum2(v);
+        v = lanes_sum2<32>(v);
         if constexpr (TR > 32) {
+            constexpr int WARPS = TR / 32;
             const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-            if (lane == 0) warps[turn * 16 + w] = v;
-            __syncthreads();
-            v = lane < TR / 32 ? warps[turn * 16 + lane] : make_float2(0.0f, 0.0f);
-            v = warp_sum2(v);
+            if (lane == 0) warps[turn * 32 + w] = v;
+            if constexpr (TR < BLOCK) named_bar_sync(1 + threadIdx.x / TR, TR);
+            else __syncthreads();
+            v = lanes_sum2<WARPS>(warps[turn * 32 + w / WARPS * WARPS + lane % WARPS]);
             if constexpr (CS > 1) {
                 if (threadIdx.x < CS) {
                     const uint32_t dst = map_shared_rank(
@@ -207,151 +296,198 @@ struct GroupSum {
     }
 };
 
+// Threads of a block: forward 256 or a row's group, backward 512 (its groups'
+// column sums meet in shared memory).
 template <int TR>
 constexpr int norm_block() {
-    return TR < 128 ? 128 : TR;
+    return TR < 256 ? 256 : TR;
 }
 
 template <class Ty, int TR, int CS, bool VEC>
-__global__ void __launch_bounds__(norm_block<TR>()) tg_norm_kernel(const NormParams p) {
+__global__ void __launch_bounds__(norm_block<TR>(), NORM_SM / norm_block<TR>())
+    tg_norm_kernel(const NormParams p) {
     using T = typename Ty::T;
     extern __shared__ uint4 ring[];
-    __shared__ float2 warps[2 * 16];
+    __shared__ float2 warps[2 * 32];
     __shared__ float2 blocks[2 * 8];
-    constexpr int GROUPS = norm_block<TR>() / TR;
+    constexpr int BLOCK = norm_block<TR>(), GROUPS = BLOCK / TR;
     constexpr int THREADS = TR * CS;  // threads that share a row
     using Cols = NormCols<Ty, THREADS, VEC>;
     const int t = (int)(threadIdx.x % TR) + (CS > 1 ? (int)cluster_ctarank() * TR : 0);
     const int64_t group = ((int64_t)blockIdx.x / CS) * GROUPS + threadIdx.x / TR;
     const int64_t groups = ((int64_t)gridDim.x / CS) * GROUPS;
     const int n = (int)p.n;
-    GroupSum<TR, CS> sum{warps, blocks, 0};
+    GroupSum<TR, BLOCK, CS> sum{warps, blocks, 0};
     griddep_launch();
     if constexpr (CS > 1) cluster_sync_all();  // every block runs before its memory is written
     griddep_wait();
-    NormRows<Ty, THREADS, VEC, 1, NORM_DEPTH> rows;
-    rows.base[0] = static_cast<const T *>(p.x);
-    rows.ld[0] = p.ldx;
-    rows.m = p.m;
-    rows.groups = groups;
+    NormRows<Ty, THREADS, BLOCK, VEC> rows;
     rows.n = n;
     rows.t = t;
-    rows.ring = ring;
-    rows.start(group);
-    // The group's columns never change: gamma and beta stay in registers.
-    float gam[NORM_PER], bet[NORM_PER];
 #pragma unroll
-    for (int i = 0; i < NORM_PER; ++i) {
-        const int c = Cols::at(i, t);
-        gam[i] = (p.gamma && c < n) ? __ldg(p.gamma + c) : 1.0f;
-        bet[i] = (p.beta && c < n) ? __ldg(p.beta + c) : 0.0f;
+    for (int k = 0; k < NORM_ROWS; ++k)
+        rows.set(k, static_cast<const T *>(p.x), p.ldx, group + k * groups, NORM_ROWS * groups, p.m);
+    rows.start(ring);
+    // The group's columns never change: gamma and beta stay in registers.
+    F2 gam[NORM_PER / 2], bet[NORM_PER / 2];
+#pragma unroll
+    for (int i = 0; i < NORM_PER / 2; ++i) {
+        const int c = Cols::at(2 * i, t), d = Cols::at(2 * i + 1, t);
+        gam[i] = f2(p.gamma && c < n ? __ldg(p.gamma + c) : 1.0f, p.gamma && d < n ? __ldg(p.gamma + d) : 1.0f);
+        bet[i] = f2(p.beta && c < n ? __ldg(p.beta + c) : 0.0f, p.beta && d < n ? __ldg(p.beta + d) : 0.0f);
     }
     T *y = static_cast<T *>(p.y);
     const bool whole = n == THREADS * NORM_PER;
-    for (int64_t r = group; r < p.m; r += groups) {
-        float w[1][NORM_PER];
-        rows.take(r, w);
-        float(&v)[NORM_PER] = w[0];
-        float s = 0.0f;
+    for (int64_t r = group; r < p.m; r += NORM_ROWS * groups) {
+        F2 v[NORM_ROWS][NORM_PER / 2];
+        rows.take(v);
+        float s[NORM_ROWS];
 #pragma unroll
-        for (int i = 0; i < NORM_PER; ++i) s += v[i];
-        const float mean = sum(make_float2(s, 0.0f)).x * p.inv_n;
+        for (int k = 0; k < NORM_ROWS; ++k) {
+            F2 a = v[k][0];
 #pragma unroll
-        for (int i = 0; i < NORM_PER; ++i) v[i] -= mean;
-        if (!whole) {
-#pragma unroll
-            for (int i = 0; i < NORM_PER; ++i)
-                if (Cols::at(i, t) >= n) v[i] = 0.0f;
+            for (int i = 1; i < NORM_PER / 2; ++i) a = add2(a, v[k][i]);
+            s[k] = sum2(a);
         }
-        float q = 0.0f;
+        const float2 total = sum(make_float2(s[0], s[1]));
+        const float mean[NORM_ROWS] = {total.x * p.inv_n, total.y * p.inv_n};
 #pragma unroll
-        for (int i = 0; i < NORM_PER; ++i) q = fmaf(v[i], v[i], q);
-        const float var = sum(make_float2(q, 0.0f)).x * p.inv_n;
-        const float rstd = 1.0f / sqrtf(var + p.eps);
-        if (t == 0) {
-            if (p.mean) p.mean[r] = mean;
-            if (p.rstd) p.rstd[r] = rstd;
+        for (int k = 0; k < NORM_ROWS; ++k) {
+            const F2 minus = f2(-mean[k]);
+#pragma unroll
+            for (int i = 0; i < NORM_PER / 2; ++i) v[k][i] = add2(v[k][i], minus);
+            if (!whole) {
+#pragma unroll
+                for (int i = 0; i < NORM_PER / 2; ++i) {
+                    float a, b;
+                    f2_split(v[k][i], a, b);
+                    v[k][i] = f2(Cols::at(2 * i, t) < n ? a : 0.0f, Cols::at(2 * i + 1, t) < n ? b : 0.0f);
+                }
+            }
+            F2 q = mul2(v[k][0], v[k][0]);
+#pragma unroll
+            for (int i = 1; i < NORM_PER / 2; ++i) q = fma2(v[k][i], v[k][i], q);
+            s[k] = sum2(q);
         }
+        const float2 second = sum(make_float2(s[0], s[1]));
+        const float rstd[NORM_ROWS] = {1.0f / sqrtf(second.x * p.inv_n + p.eps),
+                                       1.0f / sqrtf(second.y * p.inv_n + p.eps)};
 #pragma unroll
-        for (int i = 0; i < NORM_PER; ++i) v[i] = fmaf(v[i] * rstd, gam[i], bet[i]);
-        Cols::store(y + r * p.ldy, t, n, v);
+        for (int k = 0; k < NORM_ROWS; ++k) {
+            const int64_t rr = r + k * groups;
+            if (rr >= p.m) break;
+            if (t == 0) {
+                if (p.mean) p.mean[rr] = mean[k];
+                if (p.rstd) p.rstd[rr] = rstd[k];
+            }
+            const F2 scale = f2(rstd[k]);
+#pragma unroll
+            for (int i = 0; i < NORM_PER / 2; ++i) v[k][i] = fma2(mul2(v[k][i], scale), gam[i], bet[i]);
+            Cols::store(y + rr * p.ldy, t, n, whole, v[k]);
+        }
     }
 }
 
 template <class Ty, int TR, int CS, bool VEC>
-__global__ void __launch_bounds__(norm_block<TR>()) tg_norm_backward_kernel(const NormParams p) {
+__global__ void __launch_bounds__(NORM_SM, 1) tg_norm_backward_kernel(const NormParams p) {
     using T = typename Ty::T;
     extern __shared__ uint4 ring[];
-    __shared__ float2 warps[2 * 16];
+    __shared__ float2 warps[2 * 32];
     __shared__ float2 blocks[2 * 8];
-    constexpr int GROUPS = norm_block<TR>() / TR;
+    constexpr int BLOCK = NORM_SM, GROUPS = BLOCK / TR;
     constexpr int THREADS = TR * CS;
     using Cols = NormCols<Ty, THREADS, VEC>;
     const int t = (int)(threadIdx.x % TR) + (CS > 1 ? (int)cluster_ctarank() * TR : 0);
     const int64_t group = ((int64_t)blockIdx.x / CS) * GROUPS + threadIdx.x / TR;
     const int64_t groups = ((int64_t)gridDim.x / CS) * GROUPS;
     const int n = (int)p.n;
-    GroupSum<TR, CS> sum{warps, blocks, 0};
+    GroupSum<TR, BLOCK, CS> sum{warps, blocks, 0};
     griddep_launch();
     if constexpr (CS > 1) cluster_sync_all();
     griddep_wait();
-    NormRows<Ty, THREADS, VEC, 2, NORM_BACK_DEPTH> rows;
-    rows.base[0] = static_cast<const T *>(p.x);
-    rows.base[1] = static_cast<const T *>(p.dy);
-    rows.ld[0] = p.ldx;
-    rows.ld[1] = p.lddy;
-    rows.m = p.m;
-    rows.groups = groups;
+    NormRows<Ty, THREADS, BLOCK, VEC> rows;
     rows.n = n;
     rows.t = t;
-    rows.ring = ring;
-    rows.start(group);
+    rows.set(0, static_cast<const T *>(p.x), p.ldx, group, groups, p.m);
+    rows.set(1, static_cast<const T *>(p.dy), p.lddy, group, groups, p.m);
+    rows.start(ring);
     T *dx = static_cast<T *>(p.y);
-    float gam[NORM_PER], sg[NORM_PER], sb[NORM_PER];
+    F2 gam[NORM_PER / 2], sg[NORM_PER / 2], sb[NORM_PER / 2];
 #pragma unroll
-    for (int i = 0; i < NORM_PER; ++i) {
-        const int c = Cols::at(i, t);
-        gam[i] = (p.gamma && c < n) ? __ldg(p.gamma + c) : 1.0f;
-        sg[i] = sb[i] = 0.0f;
+    for (int i = 0; i < NORM_PER / 2; ++i) {
+        const int c = Cols::at(2 * i, t), d = Cols::at(2 * i + 1, t);
+        gam[i] = f2(p.gamma && c < n ? __ldg(p.gamma + c) : 1.0f, p.gamma && d < n ? __ldg(p.gamma + d) : 1.0f);
+        sg[i] = sb[i] = f2(0.0f);
     }
+    const bool whole = n == THREADS * NORM_PER;
     float nmean = group < p.m ? __ldg(p.mean_in + group) : 0.0f;
     float nrstd = group < p.m ? __ldg(p.rstd_in + group) : 0.0f;
     for (int64_t r = group; r < p.m; r += groups) {
-        float w[2][NORM_PER];
-        rows.take(r, w);
-        float(&xh)[NORM_PER] = w[0];
-        float(&d)[NORM_PER] = w[1];
-        const float mean = nmean, rstd = nrstd;
+        F2 w[2][NORM_PER / 2];
+        rows.take(w);
+        F2(&xh)[NORM_PER / 2] = w[0];
+        F2(&d)[NORM_PER / 2] = w[1];
+        const F2 minus = f2(-nmean), scale = f2(nrstd);
+        const float rstd = nrstd;
         if (r + groups < p.m) {
             nmean = __ldg(p.mean_in + r + groups);
             nrstd = __ldg(p.rstd_in + r + groups);
         }
-        float s1 = 0.0f, s2 = 0.0f;
+        F2 s1 = f2(0.0f), s2 = f2(0.0f);
 #pragma unroll
-        for (int i = 0; i < NORM_PER; ++i) {
+        for (int i = 0; i < NORM_PER / 2; ++i) {
             // Columns past the row's end hold dy = 0 and add nothing.
-            const float h = (xh[i] - mean) * rstd;
-            xh[i] = h;
-            sg[i] = fmaf(d[i], h, sg[i]);
-            sb[i] += d[i];
-            d[i] *= gam[i];
-            s1 += d[i];
-            s2 = fmaf(d[i], h, s2);
+            xh[i] = mul2(add2(xh[i], minus), scale);
+            sg[i] = fma2(d[i], xh[i], sg[i]);
+            sb[i] = add2(sb[i], d[i]);
+            d[i] = mul2(d[i], gam[i]);
+            s1 = add2(s1, d[i]);
+            s2 = fma2(d[i], xh[i], s2);
         }
-        const float2 s = sum(make_float2(s1, s2));
+        const float2 s = sum(make_float2(sum2(s1), sum2(s2)));
         if (dx) {
-            const float c1 = s.x * p.inv_n, c2 = s.y * p.inv_n;
+            // rstd (d - c1 - xh c2)
+            const F2 k1 = f2(-rstd * s.x * p.inv_n), k2 = f2(-rstd * s.y * p.inv_n);
 #pragma unroll
-            for (int i = 0; i < NORM_PER; ++i) d[i] = rstd * (d[i] - fmaf(xh[i], c2, c1));
-            Cols::store(dx + r * p.ldy, t, n, d);
+            for (int i = 0; i < NORM_PER / 2; ++i) d[i] = fma2(d[i], scale, fma2(xh[i], k2, k1));
+            Cols::store(dx + r * p.ldy, t, n, whole, d);
         }
+    }
+    // The groups' column sums meet in shared memory, group by group (the ring
+    // is done with: every thread has waited for its own copies).
+    const int64_t part = blockIdx.x / CS;
+    float eg[NORM_PER], eb[NORM_PER];
+#pragma unroll
+    for (int i = 0; i < NORM_PER / 2; ++i) {
+        f2_split(sg[i], eg[2 * i], eg[2 * i + 1]);
+        f2_split(sb[i], eb[2 * i], eb[2 * i + 1]);
+    }
+    if constexpr (GROUPS > 1) {
+        float *acc = reinterpret_cast<float *>(ring) + threadIdx.x % TR;  // [2][NORM_PER][TR]
+        if constexpr (norm_async<Ty, VEC>()) cp_async_wait<0>();
+        for (int g = 0; g < GROUPS; ++g) {
+            __syncthreads();
+            if ((int)threadIdx.x / TR == g) {
+#pragma unroll
+                for (int i = 0; i < NORM_PER; ++i) {
+                    float *a = acc + i * TR, *b = a + TR * NORM_PER;
+                    if (g) {
+                        eg[i] = *a + eg[i];
+                        eb[i] = *b + eb[i];
+                    }
+                    *a = eg[i];
+                    *b = eb[i];
+                }
+            }
+        }
+        if ((int)threadIdx.x / TR != GROUPS - 1) return;  // the last group holds the totals
     }
 #pragma unroll
     for (int i = 0; i < NORM_PER; ++i) {
         const int c = Cols::at(i, t);
         if (c < n) {
-            if (p.pgamma) p.pgamma[group * p.n + c] = sg[i];
-            if (p.pbeta) p.pbeta[group * p.n + c] = sb[i];
+            if (p.pgamma) p.pgamma[part * p.n + c] = eg[i];
+            if (p.pbeta) p.pbeta[part * p.n + c] = eb[i];
         }
     }
 }
@@ -369,45 +505,37 @@ struct NormShape {
     int tr, cs;
 };
 NormShape norm_shape(int64_t n) {
-    if (n <= 32 * NORM_PER) return {32, 1};
-    if (n <= 128 * NORM_PER) return {128, 1};
-    if (n <= 256 * NORM_PER) return {256, 1};
-    if (n <= 512 * NORM_PER) return {512, 1};
-    if (n <= 2 * 512 * NORM_PER) return {512, 2};
-    if (n <= 4 * 512 * NORM_PER) return {512, 4};
+    for (int tr : {32, 64, 128, 256, 512})
+        if (n <= tr * NORM_PER) return {tr, 1};
+    for (int cs : {2, 4})
+        if (n <= cs * 512 * NORM_PER) return {512, cs};
     return {512, 8};
 }
 
-// Row groups of a launch: at most `waves` blocks per SM (rounded to clusters),
-// no more groups than rows.
-int64_t norm_grid(const NormShape &s, int64_t m, int sms, int per_sm) {
-    const int64_t groups = s.tr < 128 ? 128 / s.tr : 1;  // per block
-    int64_t blocks = (m + groups - 1) / groups;
-    int64_t cap = (int64_t)sms * per_sm / s.cs;
-    if (cap < 1) cap = 1;
-    if (blocks > cap) blocks = cap;
-    return blocks * s.cs;
+// Clusters of the launch: NORM_SM threads a SM, no more row slots than rows.
+int64_t norm_clusters(const NormShape &s, int64_t m, int sms, int block, int rows) {
+    const int64_t per = (int64_t)rows * (block / s.tr);  // rows of a cluster's step
+    int64_t c = (m + per - 1) / per;
+    const int64_t cap = (int64_t)sms * (NORM_SM / block) / s.cs;
+    if (c > cap) c = cap;
+    return c < 1 ? 1 : c;
 }
-
-// Blocks per SM: what registers and rings leave room for; in backward also few
-// enough that the partial column sums (8 n bytes per group, written and read
-// once) stay small beside the rows.
-int forward_per_sm(const NormShape &s) { return s.tr >= 512 ? 1 : s.tr == 256 ? 3 : 6; }
-int backward_per_sm(const NormShape &s) { return s.tr >= 512 ? 1 : s.tr == 256 ? 2 : 4; }
-int64_t backward_groups(int64_t m, int64_t n, int sms) {
-    const NormShape s = norm_shape(n);
-    const int64_t per_block = s.tr < 128 ? 128 / s.tr : 1;
-    return norm_grid(s, m, sms, backward_per_sm(s)) / s.cs * per_block;
+// Rows of partial column sums that the backward pass leaves.
+int64_t backward_parts(int64_t m, int64_t n, int sms) {
+    return norm_clusters(norm_shape(n), m, sms, NORM_SM, 1);
 }
 
 template <class Ty, int TR, int CS, bool VEC>
 cudaError_t launch_shape(const NormParams &p, bool backward, int64_t grid, int device,
                          cudaStream_t stream) {
-    constexpr int ROW = norm_block<TR>() * NORM_PER * (int)sizeof(typename Ty::T);
-    constexpr int SMEM = VEC ? NORM_DEPTH * ROW : 0, SMEM_BACK = VEC ? NORM_BACK_DEPTH * 2 * ROW : 0;
+    constexpr int STEP = 2 * NORM_PER * (int)sizeof(typename Ty::T);  // ring bytes a thread and step
+    constexpr bool ASYNC = norm_async<Ty, VEC>();
+    constexpr int SMEM = ASYNC ? NORM_DEPTH * STEP * norm_block<TR>() : 0;
+    // (without a ring: the groups' column sums)
+    constexpr int SMEM_BACK = ASYNC ? NORM_DEPTH * STEP * NORM_SM : 2 * 4 * TR * NORM_PER;
     static std::atomic<uint64_t> done{0};
     const uint64_t bit = 1ull << device;
-    if (VEC && !(done.load(std::memory_order_acquire) & bit)) {
+    if (!(done.load(std::memory_order_acquire) & bit)) {
         cudaError_t e = cudaFuncSetAttribute(tg_norm_kernel<Ty, TR, CS, VEC>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
         if (e == cudaSuccess)
@@ -425,7 +553,7 @@ cudaError_t launch_shape(const NormParams &p, bool backward, int64_t grid, int d
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.gridDim = dim3((unsigned)grid, 1, 1);
-    cfg.blockDim = dim3(norm_block<TR>(), 1, 1);
+    cfg.blockDim = dim3(backward ? NORM_SM : norm_block<TR>(), 1, 1);
     cfg.dynamicSmemBytes = backward ? SMEM_BACK : SMEM;
     cfg.stream = stream;
     cfg.attrs = attr;
@@ -439,6 +567,7 @@ cudaError_t launch_type(const NormParams &p, bool backward, int64_t grid, int de
                         cudaStream_t stream) {
     const NormShape s = norm_shape(p.n);
     if (s.tr == 32) return launch_shape<Ty, 32, 1, VEC>(p, backward, grid, device, stream);
+    if (s.tr == 64) return launch_shape<Ty, 64, 1, VEC>(p, backward, grid, device, stream);
     if (s.tr == 128) return launch_shape<Ty, 128, 1, VEC>(p, backward, grid, device, stream);
     if (s.tr == 256) return launch_shape<Ty, 256, 1, VEC>(p, backward, grid, device, stream);
     if (s.cs == 1) return launch_shape<Ty, 512, 1, VEC>(p, backward, grid, device, stream);
@@ -502,7 +631,8 @@ extern "C" tg_status tg_layer_norm(int64_t M, int64_t N, const void *X, int64_t 
     p.rstd = rstd;
     p.inv_n = 1.0f / (float)N;
     const NormShape s = norm_shape(N);
-    const int64_t grid = norm_grid(s, M, dev.sms, forward_per_sm(s));
+    const int block = s.tr < 256 ? 256 : s.tr;
+    const int64_t grid = s.cs * norm_clusters(s, M, dev.sms, block, NORM_ROWS);
     const bool vec = vec_ok(X, ldx, e) && vec_ok(Y, ldy, e);
     return launch_norm(p, dtype, false, vec, grid, dev.id, static_cast<cudaStream_t>(stream)) == cudaSuccess
                ? TG_OK
@@ -513,7 +643,7 @@ extern "C" int64_t tg_layer_norm_backward_workspace_bytes(int64_t M, int64_t N) 
     if (M < 0 || N < 0 || M > INT32_MAX || N > kNormMaxCols) return -1;
     tg::host::Device dev;
     if (tg::host::device(&dev) != TG_OK) return -1;
-    return M == 0 || N == 0 ? 0 : 2 * 4 * N * backward_groups(M, N, dev.sms);
+    return M == 0 || N == 0 ? 0 : 2 * 4 * N * backward_parts(M, N, dev.sms);
 }
 
 extern "C" tg_status tg_layer_norm_backward(int64_t M, int64_t N, const void *dY, int64_t lddy,
@@ -540,10 +670,10 @@ extern "C" tg_status tg_layer_norm_backward(int64_t M, int64_t N, const void *dY
     tg_status st = tg::host::device(&dev);
     if (st != TG_OK) return st;
     const bool sums = dgamma || dbeta;
-    int64_t groups = 0;
+    int64_t parts = 0;
     if (M > 0) {
-        groups = backward_groups(M, N, dev.sms);
-        if (sums && (!workspace || (uintptr_t)workspace % 4 || workspace_bytes < 2 * 4 * N * groups))
+        parts = backward_parts(M, N, dev.sms);
+        if (sums && (!workspace || (uintptr_t)workspace % 4 || workspace_bytes < 2 * 4 * N * parts))
             return TG_ERR_INVALID_VALUE;
         NormParams p = {};
         p.m = M;
@@ -559,19 +689,17 @@ extern "C" tg_status tg_layer_norm_backward(int64_t M, int64_t N, const void *dY
         p.ldy = lddx;
         p.inv_n = 1.0f / (float)N;
         if (dgamma) p.pgamma = static_cast<float *>(workspace);
-        if (dbeta) p.pbeta = static_cast<float *>(workspace) + groups * N;
+        if (dbeta) p.pbeta = static_cast<float *>(workspace) + parts * N;
         const NormShape s = norm_shape(N);
         const bool vec = vec_ok(X, ldx, e) && vec_ok(dY, lddy, e) && (!dX || vec_ok(dX, lddx, e));
-        if (launch_norm(p, dtype, true, vec, norm_grid(s, M, dev.sms, backward_per_sm(s)), dev.id,
-                        stream) !=
-            cudaSuccess)
+        if (launch_norm(p, dtype, true, vec, parts * s.cs, dev.id, stream) != cudaSuccess)
             return TG_ERR_CUDA;
     }
     if (!sums) return TG_OK;
-    // M == 0: no groups, the sums are zero.
+    // M == 0: no parts, the sums are zero.
     const float *w = static_cast<const float *>(workspace);
-    return tg::host::colsum_finish(dgamma ? w : w + groups * N, dgamma && dbeta ? w + groups * N : nullptr,
-                                   (int32_t)groups, N, dgamma ? dgamma : dbeta,
+    return tg::host::colsum_finish(dgamma ? w : w + parts * N, dgamma && dbeta ? w + parts * N : nullptr,
+                                   (int32_t)parts, N, dgamma ? dgamma : dbeta,
                                    dgamma && dbeta ? dbeta : nullptr, stream) == cudaSuccess
                ? TG_OK
                : TG_ERR_CUDA;

@@ -15,18 +15,29 @@ struct TypeF32 {
     static constexpr int VW = 4;  // elements per 16 bytes
     __device__ static float up(T x) { return x; }
     __device__ static T down(float x) { return x; }
+    __device__ static uint32_t down2(float, float) { return 0; }  // 16-bit types only
 };
 struct TypeBF16 {
     using T = unsigned short;
     static constexpr int VW = 8;
     __device__ static float up(T x) { return __uint_as_float((uint32_t)x << 16); }
+    __device__ static float up_high(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
     __device__ static T down(float x) { return __bfloat16_as_ushort(__float2bfloat16_rn(x)); }
+    __device__ static uint32_t down2(float lo, float hi) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&v);
+    }
 };
 struct TypeF16 {
     using T = unsigned short;
     static constexpr int VW = 8;
     __device__ static float up(T x) { return __half2float(__ushort_as_half(x)); }
+    __device__ static float up_high(uint32_t w) { return up((T)(w >> 16)); }
     __device__ static T down(float x) { return __half_as_ushort(__float2half_rn(x)); }
+    __device__ static uint32_t down2(float lo, float hi) {
+        const __half2 v = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&v);
+    }
 };
 
 // One 16-byte vector of a row at column c: whole when it lies inside the
@@ -58,26 +69,28 @@ __device__ __forceinline__ void row_unpack(const uint4 &v, float *y) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             y[2 * i] = Ty::up((unsigned short)(w[i] & 0xffffu));
-            y[2 * i + 1] = Ty::up((unsigned short)(w[i] >> 16));
+            y[2 * i + 1] = Ty::up_high(w[i]);
         }
     }
 }
 
 template <class Ty>
+__device__ __forceinline__ void row_store_vec(typename Ty::T *q, const float *y) {
+    uint4 v;
+    if constexpr (Ty::VW == 4) {
+        v = make_uint4(__float_as_uint(y[0]), __float_as_uint(y[1]), __float_as_uint(y[2]),
+                       __float_as_uint(y[3]));
+    } else {
+        v = make_uint4(Ty::down2(y[0], y[1]), Ty::down2(y[2], y[3]), Ty::down2(y[4], y[5]),
+                       Ty::down2(y[6], y[7]));
+    }
+    *reinterpret_cast<uint4 *>(q) = v;
+}
+
+template <class Ty>
 __device__ __forceinline__ void row_store(typename Ty::T *row, int64_t c, int64_t n, const float *y) {
     if (c + Ty::VW <= n) {
-        uint4 v;
-        if constexpr (Ty::VW == 4) {
-            v = make_uint4(__float_as_uint(y[0]), __float_as_uint(y[1]), __float_as_uint(y[2]),
-                           __float_as_uint(y[3]));
-        } else {
-            uint32_t w[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                w[i] = (uint32_t)Ty::down(y[2 * i]) | ((uint32_t)Ty::down(y[2 * i + 1]) << 16);
-            v = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-        *reinterpret_cast<uint4 *>(row + c) = v;
+        row_store_vec<Ty>(row + c, y);
     } else {
 #pragma unroll
         for (int i = 0; i < Ty::VW; ++i)
