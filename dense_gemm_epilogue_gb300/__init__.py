@@ -155,6 +155,8 @@ _lib = None
 def load(path: str | None = None) -> ctypes.CDLL:
     """Load the built library (raises if it has not been built)."""
     global _lib
+    if _lib is not None and path is None:
+        return _lib
     with _lock:
         if _lib is not None and path is None:
             return _lib
@@ -256,20 +258,24 @@ def load(path: str | None = None) -> ctypes.CDLL:
 def _ptr(x):
     if x is None:
         return None
+    try:
+        return x.data_ptr()
+    except AttributeError:
+        pass
     if isinstance(x, int):
         return x
-    if hasattr(x, "data_ptr"):
-        return x.data_ptr()
     raise TypeError(f"cannot pass {type(x).__name__} as a pointer")
 
 
 def _stream(s):
     if s is None:
         return None
+    try:
+        return s.cuda_stream
+    except AttributeError:
+        pass
     if isinstance(s, int):
         return s
-    if hasattr(s, "cuda_stream"):
-        return s.cuda_stream
     raise TypeError(f"cannot pass {type(s).__name__} as a stream")
 
 

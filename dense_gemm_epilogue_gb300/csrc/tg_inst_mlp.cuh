@@ -72,10 +72,10 @@ static cudaError_t launch_mlp_kind(const MlpLaunch &a) {
     return a.block_n == 256 ? launch_mlp_bn<KD, CG, 256>(a) : launch_mlp_bn<KD, CG, 128>(a);
 }
 
-template <Kind KD, int NT, bool DUAL>
+template <Kind KD, int NT, StreamOp OP>
 static cudaError_t launch_stream_one(const StreamLaunch &a) {
-    using C = StreamConfig<KD, NT, DUAL>;
-    auto kernel = tg_stream_kernel<KD, NT, DUAL>;
+    using C = StreamConfig<KD, NT, OP>;
+    auto kernel = tg_stream_kernel<KD, NT, OP>;
     static std::atomic<uint64_t> done{0};
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
@@ -92,19 +92,23 @@ static cudaError_t launch_stream_one(const StreamLaunch &a) {
     return cudaLaunchKernelEx(&cfg, kernel, a.maps, a.p);
 }
 
-template <Kind KD, bool DUAL>
+template <Kind KD, StreamOp OP>
 static cudaError_t launch_stream_nt(const StreamLaunch &a) {
     switch (a.nt) {
-    case 16: return launch_stream_one<KD, 16, DUAL>(a);
-    case 32: return launch_stream_one<KD, 32, DUAL>(a);
-    case 64: return launch_stream_one<KD, 64, DUAL>(a);
-    default: return launch_stream_one<KD, 128, DUAL>(a);
+    case 16: return launch_stream_one<KD, 16, OP>(a);
+    case 32: return launch_stream_one<KD, 32, OP>(a);
+    case 64: return launch_stream_one<KD, 64, OP>(a);
+    default: return launch_stream_one<KD, 128, OP>(a);
     }
 }
 
 template <Kind KD>
 static cudaError_t launch_stream_kind(const StreamLaunch &a) {
-    return a.dual ? launch_stream_nt<KD, true>(a) : launch_stream_nt<KD, false>(a);
+    switch (a.op) {
+    case StreamOp::GATED: return launch_stream_nt<KD, StreamOp::GATED>(a);
+    case StreamOp::DGRAD: return launch_stream_nt<KD, StreamOp::DGRAD>(a);
+    default: return launch_stream_nt<KD, StreamOp::LINEAR>(a);
+    }
 }
 
 }  // namespace tg

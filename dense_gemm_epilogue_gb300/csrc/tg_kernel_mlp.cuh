@@ -229,10 +229,44 @@ __device__ __forceinline__ int stg_offset(int r, int b) {
     return r * ROW + ((((b >> 4) ^ x) << 4) | (b & 15));
 }
 
+// The 16-bit values of a staged box (32 rows of ROW bytes) to output rows that
+// are not 16-byte aligned: a row per step, neighbouring lanes on neighbouring
+// four-byte words from the row's first 4-byte boundary on (element 0 or 1), and
+// single elements where one is left over; eight rows' reads before their
+// stores.  Out of line, so that the aligned path keeps its registers.
+template <int ROW>
+__device__ __noinline__ void stg_to_global_odd(const uint8_t *stg, uint16_t *dst, int64_t ld,
+                                               int32_t rows_left, int32_t cols_left, int lane) {
+    const int left = cols_left < ROW / 2 ? cols_left : ROW / 2;
+    const int even = (int)((uintptr_t)dst >> 1), step = (int)(ld & 1);
+#pragma unroll 1
+    for (int g = 0; g < 32 && g < rows_left; g += 8) {
+        uint32_t w[8], first[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int r = g + i, c = 2 * lane + ((even + r * step) & 1);
+            const int c0 = c < ROW / 2 ? c : 0, c1 = c + 1 < ROW / 2 ? c + 1 : 0;
+            const uint32_t lo = *reinterpret_cast<const uint16_t *>(stg + stg_offset<ROW>(r, 2 * c0));
+            const uint32_t hi = *reinterpret_cast<const uint16_t *>(stg + stg_offset<ROW>(r, 2 * c1));
+            first[i] = *reinterpret_cast<const uint16_t *>(stg + stg_offset<ROW>(r, 0));
+            w[i] = lo | (hi << 16);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int r = g + i, odd = (even + r * step) & 1, c = 2 * lane + odd;
+            if (r < rows_left) {
+                uint16_t *q = dst + (int64_t)r * ld;
+                if (c + 1 < left) *reinterpret_cast<uint32_t *>(q + c) = w[i];
+                else if (c < left) q[c] = (uint16_t)w[i];
+                if (odd && lane == 0) q[0] = (uint16_t)first[i];
+            }
+        }
+    }
+}
+
 // A staged box (32 rows of ROW bytes, E elements) to columns col0.. of rows
 // row0.. of an output, bounds checked.  vec: 16 bytes a lane; a piece that the
-// row's end cuts goes element by element, as do rows that are not 16-byte
-// aligned (a row per step, neighbouring lanes on neighbours).
+// row's end cuts goes element by element.
 template <int ROW, typename E>
 __device__ __forceinline__ void stg_to_global(const uint8_t *stg, const MlpOut &o, int32_t row0,
                                               int32_t col0, int32_t rows, int32_t cols, int lane) {
@@ -256,13 +290,15 @@ __device__ __forceinline__ void stg_to_global(const uint8_t *stg, const MlpOut &
                 }
             }
         }
+    } else if constexpr (sizeof(E) == 2) {
+        stg_to_global_odd<ROW>(stg, dst, o.ld, rows - row0, cols - col0, lane);
     } else {
-        for (int r = 0; r < 32 && row0 + r < rows; ++r)
-#pragma unroll
-            for (int c = lane; c < ROW / (int)sizeof(E); c += 32)
-                if (col0 + c < cols)
-                    dst[(int64_t)r * o.ld + c] =
-                        *reinterpret_cast<const E *>(stg + stg_offset<ROW>(r, c * (int)sizeof(E)));
+#pragma unroll 4
+        for (int r = 0; r < 32; ++r) {
+            if (row0 + r >= rows) break;
+            if (lane < ROW / 4 && col0 + lane < cols)
+                dst[(int64_t)r * o.ld + lane] = *reinterpret_cast<const E *>(stg + stg_offset<ROW>(r, lane * 4));
+        }
     }
 }
 

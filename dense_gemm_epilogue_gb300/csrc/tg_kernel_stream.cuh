@@ -25,6 +25,10 @@
 //
 // Gated: each stage holds 128 gate rows and the same 128 up rows; two MMAs
 // share the token operand and one thread holds g and u of its feature.
+// Transposed (the input gradient, dX = dZ W or dG Wg + dU Wu): the streamed
+// operand's rows are the products' reduction index, so its 128 features lie
+// along its rows (MN-major, two 64 x 64 boxes a stage), and the K blocks may
+// run over two operand pairs in turn.
 #pragma once
 
 #include <cstdint>
@@ -32,9 +36,12 @@
 
 namespace tg {
 
-template <Kind KD, int NT, bool DUAL>
+enum class StreamOp : int { LINEAR = 0, GATED = 1, DGRAD = 2 };
+
+template <Kind KD, int NT, StreamOp OP>
 struct StreamConfig {
     using T = KindTraits<KD>;
+    static constexpr bool DUAL = OP == StreamOp::GATED, TRANS = OP == StreamOp::DGRAD;
     static constexpr int BK = T::block_k;
     static constexpr int MATS = DUAL ? 2 : 1;
     static constexpr int A_BYTES = BLOCK_M * ROW_BYTES;
@@ -57,18 +64,19 @@ struct StreamConfig {
     static constexpr int NUM_THREADS = (2 + EPI_WARPS) * 32;
     static constexpr int MMAS_PER_STAGE = BK / T::umma_k;
     static constexpr uint32_t IDESC = (1u << 4) | (T::fmt << 7) | (T::fmt << 10) |
-                                      ((uint32_t)(NT >> 3) << 17) |
+                                      ((uint32_t)TRANS << 15) | ((uint32_t)(NT >> 3) << 17) |
                                       ((uint32_t)(BLOCK_M >> 4) << 24);
     static_assert(SMEM_BYTES <= SMEM_LIMIT, "shared memory budget");
     static_assert(TMEM_COLS >= 32 && TMEM_COLS <= 512, "tensor-memory allocation");
 };
 
 struct StreamMaps {
-    CUtensorMap w[2], x;
+    CUtensorMap w[2], x[2];
 };
 
 struct StreamParams {
     int32_t tokens, features, tiles, num_k_blocks;
+    int32_t k_blocks0;  // K blocks of the first operand pair (DGRAD)
     int32_t act;
     const float *bias;
     const void *r;
@@ -119,10 +127,11 @@ __device__ __forceinline__ uint16_t mlp_narrow(float y) {
     else return __half_as_ushort(__float2half_rn(y));
 }
 
-template <Kind KD, int NT, bool DUAL>
-__global__ void __launch_bounds__(StreamConfig<KD, NT, DUAL>::NUM_THREADS, NT <= 32 ? 2 : 1)
+template <Kind KD, int NT, StreamOp OP>
+__global__ void __launch_bounds__(StreamConfig<KD, NT, OP>::NUM_THREADS, NT <= 32 ? 2 : 1)
     tg_stream_kernel(const __grid_constant__ StreamMaps maps, const StreamParams p) {
-    using C = StreamConfig<KD, NT, DUAL>;
+    using C = StreamConfig<KD, NT, OP>;
+    constexpr bool DUAL = C::DUAL, TRANS = C::TRANS;
     constexpr int S = C::STAGES;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
@@ -152,7 +161,7 @@ __global__ void __launch_bounds__(StreamConfig<KD, NT, DUAL>::NUM_THREADS, NT <=
         fence_mbar_init();
         prefetch_tensormap(&maps.w[0]);
         if (DUAL) prefetch_tensormap(&maps.w[1]);
-        prefetch_tensormap(&maps.x);
+        prefetch_tensormap(&maps.x[0]);
     }
     if (warp == 1) {
         tmem_alloc(smem_u32(tmem_slot), C::TMEM_COLS);
@@ -174,8 +183,16 @@ __global__ void __launch_bounds__(StreamConfig<KD, NT, DUAL>::NUM_THREADS, NT <=
                 StreamUnits un(p);
                 for (int left = C::PREFETCH; left > 0 && un.next(p);)
                     for (int kb = un.k0; kb < un.k1 && left > 0; ++kb, --left) {
-                        tma_prefetch_l2_2d(&maps.w[0], kb * C::BK, un.t * BLOCK_M);
-                        if (DUAL) tma_prefetch_l2_2d(&maps.w[1], kb * C::BK, un.t * BLOCK_M);
+                        const int second = TRANS && kb >= p.k_blocks0;
+                        const int32_t kc = (kb - (second ? p.k_blocks0 : 0)) * C::BK;
+                        const int32_t f = un.t * BLOCK_M;
+                        if constexpr (TRANS) {
+                            tma_prefetch_l2_2d(&maps.w[second], f, kc);
+                            tma_prefetch_l2_2d(&maps.w[second], f + 64, kc);
+                        } else {
+                            tma_prefetch_l2_2d(&maps.w[0], kc, f);
+                            if (DUAL) tma_prefetch_l2_2d(&maps.w[1], kc, f);
+                        }
                     }
             }
             griddep_wait();
@@ -189,11 +206,17 @@ __global__ void __launch_bounds__(StreamConfig<KD, NT, DUAL>::NUM_THREADS, NT <=
                     if (!wait_phase(bar(C::EMPTY0 + s), ph ^ 1, ctl, SITE_EMPTY)) { ok = false; break; }
                     const uint32_t full = bar(C::FULL0 + s);
                     mbar_arrive_expect_tx(full, C::STAGE_BYTES);
-                    tma_load_2d(stage(s), &maps.w[0], full, kb * C::BK, un.t * BLOCK_M);
-                    if (DUAL)
-                        tma_load_2d(stage(s) + C::A_BYTES, &maps.w[1], full, kb * C::BK,
-                                    un.t * BLOCK_M);
-                    tma_load_2d(stage(s) + C::MATS * C::A_BYTES, &maps.x, full, kb * C::BK, 0);
+                    const int second = TRANS && kb >= p.k_blocks0;
+                    const int32_t kc = (kb - (second ? p.k_blocks0 : 0)) * C::BK;
+                    const int32_t f = un.t * BLOCK_M;
+                    if constexpr (TRANS) {
+                        tma_load_2d(stage(s), &maps.w[second], full, f, kc);
+                        tma_load_2d(stage(s) + 8192, &maps.w[second], full, f + 64, kc);
+                    } else {
+                        tma_load_2d(stage(s), &maps.w[0], full, kc, f);
+                        if (DUAL) tma_load_2d(stage(s) + C::A_BYTES, &maps.w[1], full, kc, f);
+                    }
+                    tma_load_2d(stage(s) + C::MATS * C::A_BYTES, &maps.x[second], full, kc, 0);
                     ++issued;
                     if (++s == S) { s = 0; ph ^= 1; }
                 }
@@ -230,7 +253,8 @@ __global__ void __launch_bounds__(StreamConfig<KD, NT, DUAL>::NUM_THREADS, NT <=
                     for (int kk = 0; kk < C::MMAS_PER_STAGE; ++kk) {
                         const uint64_t bd = smem_desc_sw128(b0 + kk * 32);
                         const uint32_t keep = (kb != un.k0) || (kk != 0);
-                        mma_f16(d, smem_desc_sw128(a0 + kk * 32), bd, C::IDESC, keep);
+                        mma_f16(d, TRANS ? smem_desc_mn_sw128(a0 + kk * 2048) : smem_desc_sw128(a0 + kk * 32),
+                                bd, C::IDESC, keep);
                         if (DUAL)
                             mma_f16(d + NT, smem_desc_sw128(a0 + C::A_BYTES + kk * 32), bd,
                                     C::IDESC, keep);
@@ -321,7 +345,7 @@ __global__ void __launch_bounds__(StreamConfig<KD, NT, DUAL>::NUM_THREADS, NT <=
                     constexpr int TC = tc.value;
                     // The tokens' sums: this CTA's and the partials, nearest
                     // first, WAYS CTAs' loads in flight at once.
-                    constexpr int WAYS = TC == 4 ? 8 : 2;
+                    constexpr int WAYS = TC == 4 ? 8 : NT <= 32 ? 2 : 4;
                     auto load_acc = [&](int a, float (&y)[TC]) {
                         uint32_t v[16];
                         tmem_ld_32x32b_x16(taddr + a * NT + j0, v);

@@ -15,110 +15,150 @@
 
 namespace tg {
 
-// ------------------------------------------------------------------ row-wise backward kernels
+// ------------------------------------------------------------------ row-wise jobs
 
-// LINEAR: dz = dy act'(z) (rounded to the operands' type: it is an operand of
-// two tensor-core products) and, from the unrounded FP32 values, each block's
-// column sums; without z, dz = dy (a repack to aligned rows, or the sums
-// alone).  GATED: dg = dh u act'(g), du = dh act(g).
+// What the products need done to whole matrices first, as up to four jobs of
+// one launch (each with its own blocks):
+//   LINEAR  dz = dy act'(z), rounded to the operands' type (it is an operand of
+//           two tensor-core products), and from the unrounded FP32 values the
+//           column sums db; without z, dz = dy: a repack to aligned rows, or
+//           the sums alone;
+//   GATED   dg = dh u act'(g), du = dh act(g).
 //
-// Bound: memory (LINEAR reads 2 and writes 1, GATED reads 3 and writes 2
-// values per element).  A warp takes 256 columns of a row, 16 bytes a lane;
-// eight warps take rows r, r + 8, ... of the block's band, four rows in flight
-// each.  The column sums of a band add up over its rows in registers, then over
-// the eight warps in order.
-struct ActParams {
+// Bound: memory (LINEAR reads 2 and writes 1, GATED reads 3 and writes 2 values
+// per element; 4096 x 16384 with GELU and column sums 55 us).  A warp takes 256
+// columns of a row, 8 values a lane; eight warps take rows r, r + 8, ... of the
+// block's band, two (GATED: one; without z: four) rows in flight each.  Rows that are not
+// 16-byte aligned are read as the two aligned 16-byte words that hold a lane's
+// values and shifted into place (the shift is the same for a whole row); a
+// row's first and last values, whose words reach past it, come one by one.
+//
+// Column sums: a band's add up over its rows in registers, then over the eight
+// warps in order, into the workspace; tg_colsum_finish_kernel adds the bands in
+// order, after the products, which do not wait for it (the last block of each
+// strip finishing its own sums held them up by 4 us at 777 x 1001).
+constexpr int ROW_JOBS = 4;
+constexpr int ROW_COLS = 256;
+
+struct RowJob {
     int64_t m, n;
     const void *dy, *z, *u;
     int64_t lddy, ldz, ldu;
-    int32_t act;
-    int32_t band;       // rows per block
-    void *out0, *out1;  // dz, or dg and du (out0 NULL: sums only)
+    void *out0, *out1;  // dz, or dg and du (out0 NULL: sums only); 16-byte aligned rows
     int64_t ldo0, ldo1;
-    float *partial;     // [gridDim.y][n] or NULL
+    float *partial;     // [bands][n] or NULL
+    int32_t act;
+    int32_t gated;
+    int32_t aligned;    // every input's rows are 16-byte aligned
+    int32_t band;       // rows per block
+    int32_t bands, strips;
+};
+struct RowJobs {
+    RowJob job[ROW_JOBS];
+    int32_t first[ROW_JOBS + 1];  // first block of each job
+    int32_t count;
 };
 
-// Eight values of a row: consecutive ones from column c (16 bytes), or with
-// VEC false the values at c, c + 32, ... (c = the lane's first column).
-template <class Ty, bool VEC>
-struct ActRow {
-    __device__ __forceinline__ static int first(int lane) { return VEC ? lane * 8 : lane; }
-    __device__ __forceinline__ static int col(int lane, int i) { return VEC ? lane * 8 + i : lane + 32 * i; }
-    // Any columns, bounds checked.
-    __device__ __forceinline__ static void load(const typename Ty::T *row, int64_t c, int64_t n,
-                                                float (&v)[8]) {
-        constexpr int STEP = VEC ? 1 : 32;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = c + STEP * i < n ? Ty::up(row[c + STEP * i]) : 0.0f;
+// Eight 16-bit values at any 2-byte aligned address, from the two aligned
+// 16-byte words around them.
+__device__ __forceinline__ uint4 load_shifted(const unsigned short *q) {
+    const uintptr_t at = (uintptr_t)q;
+    const uint4 *w = reinterpret_cast<const uint4 *>(at & ~(uintptr_t)15);
+    const uint32_t s = (uint32_t)at & 15u;
+    const uint4 a = __ldg(w);
+    if (s == 0) return a;
+    const uint4 b = __ldg(w + 1);
+    const uint32_t bits = (s & 2u) * 8;
+    uint32_t x0, x1, x2, x3, x4;
+    switch (s >> 2) {
+    case 0: x0 = a.x; x1 = a.y; x2 = a.z; x3 = a.w; x4 = b.x; break;
+    case 1: x0 = a.y; x1 = a.z; x2 = a.w; x3 = b.x; x4 = b.y; break;
+    case 2: x0 = a.z; x1 = a.w; x2 = b.x; x3 = b.y; x4 = b.z; break;
+    default: x0 = a.w; x1 = b.x; x2 = b.y; x3 = b.z; x4 = b.w; break;
     }
-    __device__ __forceinline__ static void store(typename Ty::T *row, int64_t c, int64_t n,
-                                                 const float (&v)[8]) {
-        if (VEC && c + 8 <= n) {
-            row_store<Ty>(row, c, n, v);
-            return;
-        }
-        constexpr int STEP = VEC ? 1 : 32;
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (c + STEP * i < n) row[c + STEP * i] = Ty::down(v[i]);
-    }
-};
+    return make_uint4(__funnelshift_r(x0, x1, bits), __funnelshift_r(x1, x2, bits),
+                      __funnelshift_r(x2, x3, bits), __funnelshift_r(x3, x4, bits));
+}
 
-// One block's band.  INSIDE: 16-byte vectors that all lie inside the rows, so
-// that the loads of FLY rows leave together; rows past the band load its last
-// row again and are dropped.
-template <class Ty, bool VEC, bool GATED, int ACT, bool INSIDE>
-__device__ __forceinline__ void act_band(const ActParams &p, int64_t c, int64_t r0, int64_t r1,
+// Values c .. c + 7 of a row, one by one, zero past its end.
+__device__ __forceinline__ uint4 load_edge(const unsigned short *row, int64_t c, int64_t n) {
+    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (c + i < n) w[i / 2] |= (uint32_t)row[c + i] << (16 * (i & 1));
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// One block's band; c: this lane's first column.
+template <class Ty, bool GATED, int ACT, bool ALIGNED>
+__device__ __forceinline__ void row_band(const RowJob &p, int64_t c, int64_t r0, int64_t r1,
                                          float (&s)[8]) {
-    using T = typename Ty::T;
-    using Row = ActRow<Ty, VEC>;
+    using T = unsigned short;
     const T *dy = static_cast<const T *>(p.dy), *z = static_cast<const T *>(p.z);
     const T *u = static_cast<const T *>(p.u);
     T *o0 = static_cast<T *>(p.out0), *o1 = static_cast<T *>(p.out1);
     constexpr bool READ_Z = GATED || ACT != MLP_NONE;
-    constexpr int FLY = INSIDE ? 4 : 1;
+    constexpr int FLY = GATED ? 1 : READ_Z ? 2 : 4;  // rows in flight per warp
+    if (c >= p.n) return;
+    // Whole vectors: aligned ones that end inside the row; shifted ones whose
+    // two words lie inside it.
+    const bool mid = ALIGNED ? c + 8 <= p.n : c >= 8 && c + 16 <= p.n;
     for (int64_t r = r0 + (threadIdx.x >> 5); r < r1; r += 8 * FLY) {
         uint4 vd[FLY], vz[FLY], vu[FLY];
-        if constexpr (INSIDE) {
+        auto load = [&](auto get) {
 #pragma unroll
             for (int k = 0; k < FLY; ++k) {
+                // (rows past the band load its last row again and are dropped)
                 const int64_t rr = r + 8 * k < r1 ? r + 8 * k : r1 - 1;
-                vd[k] = __ldcs(reinterpret_cast<const uint4 *>(dy + rr * p.lddy + c));
-                if (READ_Z) vz[k] = __ldcs(reinterpret_cast<const uint4 *>(z + rr * p.ldz + c));
-                if (GATED) vu[k] = __ldcs(reinterpret_cast<const uint4 *>(u + rr * p.ldu + c));
+                vd[k] = get(dy + rr * p.lddy);
+                if (READ_Z) vz[k] = get(z + rr * p.ldz);
+                if (GATED) vu[k] = get(u + rr * p.ldu);
             }
+        };
+        if (mid) {
+            if (ALIGNED) load([&](const T *row) { return __ldcs(reinterpret_cast<const uint4 *>(row + c)); });
+            else load([&](const T *row) { return load_shifted(row + c); });
+        } else {
+            load([&](const T *row) { return load_edge(row, c, p.n); });
         }
 #pragma unroll
         for (int k = 0; k < FLY; ++k) {
             const int64_t rr = r + 8 * k;
             if (rr < r1) {
                 float d[8], a[8], g[8];
-                if constexpr (INSIDE) row_unpack<Ty>(vd[k], d);
-                else Row::load(dy + rr * p.lddy, c, p.n, d);
+                row_unpack<Ty>(vd[k], d);
                 if constexpr (READ_Z) {
                     float y[8];
-                    if constexpr (INSIDE) row_unpack<Ty>(vz[k], y);
-                    else Row::load(z + rr * p.ldz, c, p.n, y);
+                    row_unpack<Ty>(vz[k], y);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) mlp_act_grad<ACT>(y[i], a[i], g[i]);
                 }
                 if constexpr (GATED) {
                     float w[8];
-                    if constexpr (INSIDE) row_unpack<Ty>(vu[k], w);
-                    else Row::load(u + rr * p.ldu, c, p.n, w);
+                    row_unpack<Ty>(vu[k], w);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         a[i] *= d[i];
                         d[i] *= w[i] * g[i];
                     }
-                    Row::store(o0 + rr * p.ldo0, c, p.n, d);
-                    Row::store(o1 + rr * p.ldo1, c, p.n, a);
-                } else {
-                    if constexpr (READ_Z) {
+                    row_store<Ty>(o0 + rr * p.ldo0, c, p.n, d);
+                    row_store<Ty>(o1 + rr * p.ldo1, c, p.n, a);
+                } else if constexpr (READ_Z) {
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) d[i] *= g[i];
+                    for (int i = 0; i < 8; ++i) d[i] *= g[i];
+                    if (o0) row_store<Ty>(o0 + rr * p.ldo0, c, p.n, d);
+                } else if (o0) {  // a plain copy keeps every bit (NaN payloads too)
+                    T *q = o0 + rr * p.ldo0 + c;
+                    if (c + 8 <= p.n) {
+                        *reinterpret_cast<uint4 *>(q) = vd[k];
+                    } else {
+                        const T *e = reinterpret_cast<const T *>(&vd[k]);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            if (c + i < p.n) q[i] = e[i];
                     }
-                    if (o0) Row::store(o0 + rr * p.ldo0, c, p.n, d);
+                }
+                if constexpr (!GATED) {
 #pragma unroll
                     for (int i = 0; i < 8; ++i) s[i] += d[i];
                 }
@@ -127,37 +167,42 @@ __device__ __forceinline__ void act_band(const ActParams &p, int64_t c, int64_t 
     }
 }
 
-template <class Ty, bool VEC, bool GATED>
-__global__ void __launch_bounds__(256, 3) tg_act_backward_kernel(const ActParams p) {
-    __shared__ float sums[GATED ? 1 : 8][GATED ? 1 : 256];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+template <class Ty>
+__global__ void __launch_bounds__(256, 4) tg_row_jobs_kernel(const __grid_constant__ RowJobs jobs) {
+    __shared__ float sums[8][ROW_COLS];
     griddep_launch();
     griddep_wait();
-    const int64_t c0 = (int64_t)blockIdx.x * 256;
-    const int64_t r0 = (int64_t)blockIdx.y * p.band;
+    int j = 0;
+    while (j + 1 < jobs.count && (int)blockIdx.x >= jobs.first[j + 1]) ++j;
+    const RowJob &p = jobs.job[j];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int local = (int)blockIdx.x - jobs.first[j];
+    const int band = local / p.strips, strip = local - band * p.strips;
+    const int64_t c0 = (int64_t)strip * ROW_COLS, c = c0 + lane * 8;
+    const int64_t r0 = (int64_t)band * p.band;
     const int64_t r1 = r0 + p.band < p.m ? r0 + p.band : p.m;
-    using Row = ActRow<Ty, VEC>;
     float s[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) s[i] = 0.0f;
-    const int64_t c = c0 + Row::first(lane);
-    const bool inside = VEC && c0 + 256 <= p.n;
     mlp_with_act(p.act, [&](auto act) {
-        if (inside) act_band<Ty, VEC, GATED, act.value, VEC>(p, c, r0, r1, s);
-        else act_band<Ty, VEC, GATED, act.value, false>(p, c, r0, r1, s);
-    });
-    if constexpr (!GATED) {
-        if (!p.partial) return;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) sums[warp][Row::col(lane, i)] = s[i];
-        __syncthreads();
-        const int64_t cc = c0 + threadIdx.x;
-        if (cc < p.n) {
-            float t = 0.0f;
-#pragma unroll
-            for (int w = 0; w < 8; ++w) t += sums[w][threadIdx.x];
-            p.partial[(int64_t)blockIdx.y * p.n + cc] = t;
+        if (p.gated) {
+            if (p.aligned) row_band<Ty, true, act.value, true>(p, c, r0, r1, s);
+            else row_band<Ty, true, act.value, false>(p, c, r0, r1, s);
+        } else {
+            if (p.aligned) row_band<Ty, false, act.value, true>(p, c, r0, r1, s);
+            else row_band<Ty, false, act.value, false>(p, c, r0, r1, s);
         }
+    });
+    if (!p.partial) return;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sums[warp][lane * 8 + i] = s[i];
+    __syncthreads();
+    const int64_t cc = c0 + threadIdx.x;
+    if (cc < p.n) {
+        float t = 0.0f;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) t += sums[w][threadIdx.x];
+        p.partial[(int64_t)band * p.n + cc] = t;
     }
 }
 
@@ -220,50 +265,65 @@ bool needs_repack(const Mat &a) { return a.rows > 0 && a.cols > 0 && !aligned16(
 
 // ------------------------------------------------------------------ launches
 
-// Bands of the row-wise kernel: about eight blocks per SM in all, at least 32
-// rows each (four per warp).
-int64_t act_bands(int64_t m, int64_t n, int sms) {
-    const int64_t gx = div_up(n, 256);
-    int64_t bands = div_up((int64_t)sms * 8, gx);
+// Bands of a row-wise job: about eight blocks per SM in all, at least 32 rows
+// each (four per warp).
+int64_t row_bands(int64_t m, int64_t n, int sms) {
+    const int64_t strips = div_up(n, ROW_COLS);
+    int64_t bands = div_up((int64_t)sms * 8, strips);
     if (bands > div_up(m, 32)) bands = div_up(m, 32);
-    return bands < 1 ? 1 : (bands > 65535 ? 65535 : bands);
+    if (bands < 1) bands = 1;
+    return m > 0 ? div_up(m, div_up(m, bands)) : 1;
 }
 
-template <bool GATED>
-cudaError_t launch_act(tg_dtype t, ActParams p, int sms, cudaStream_t stream) {
-    const int64_t bands = act_bands(p.m, p.n, sms);
-    p.band = (int32_t)div_up(p.m, bands);
-    auto al = [](const void *q, int64_t ld) { return (uintptr_t)q % 16 == 0 && ld % 8 == 0; };
-    const bool vec = al(p.dy, p.lddy) && (!p.z || al(p.z, p.ldz)) && (!p.u || al(p.u, p.ldu));
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3((unsigned)div_up(p.n, 256), (unsigned)div_up(p.m, p.band), 1);
-    cfg.blockDim = dim3(256, 1, 1);
-    cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (t == TG_BF16)
-        return vec ? cudaLaunchKernelEx(&cfg, tg_act_backward_kernel<TypeBF16, true, GATED>, p)
-                   : cudaLaunchKernelEx(&cfg, tg_act_backward_kernel<TypeBF16, false, GATED>, p);
-    return vec ? cudaLaunchKernelEx(&cfg, tg_act_backward_kernel<TypeF16, true, GATED>, p)
-               : cudaLaunchKernelEx(&cfg, tg_act_backward_kernel<TypeF16, false, GATED>, p);
-}
+// The jobs of one launch.
+struct RowWork {
+    RowJobs jobs;
+    int64_t blocks = 0;
+    int sms;
+    explicit RowWork(int sms_) : sms(sms_) { jobs.count = 0; }
+    RowJob &add(int64_t m, int64_t n) {
+        RowJob &p = jobs.job[jobs.count];
+        std::memset(&p, 0, sizeof(p));
+        p.m = m;
+        p.n = n;
+        p.bands = (int32_t)row_bands(m, n, sms);
+        p.band = (int32_t)div_up(m, p.bands);
+        p.strips = (int32_t)div_up(n, ROW_COLS);
+        jobs.first[jobs.count++] = (int32_t)blocks;
+        blocks += (int64_t)p.bands * p.strips;
+        return p;
+    }
+    // `from`, repacked into `to`'s aligned rows.
+    void repack(const Mat &from, const Mat &to) {
+        RowJob &p = add(from.rows, from.cols);
+        p.dy = from.p;
+        p.lddy = from.ld;
+        p.out0 = const_cast<void *>(to.p);
+        p.ldo0 = to.ld;
+    }
+    cudaError_t launch(tg_dtype t, cudaStream_t stream) {
+        if (jobs.count == 0) return cudaSuccess;
+        if (blocks > INT32_MAX) return cudaErrorInvalidValue;
+        for (int i = 0; i < jobs.count; ++i) {
+            RowJob &p = jobs.job[i];
+            auto al = [](const void *q, int64_t ld) { return (uintptr_t)q % 16 == 0 && ld % 8 == 0; };
+            p.aligned = al(p.dy, p.lddy) && (!p.z || al(p.z, p.ldz)) && (!p.u || al(p.u, p.ldu));
+        }
+        cudaLaunchConfig_t cfg = {};
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.gridDim = dim3((unsigned)blocks, 1, 1);
+        cfg.blockDim = dim3(256, 1, 1);
+        cfg.stream = stream;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        return t == TG_BF16 ? cudaLaunchKernelEx(&cfg, tg_row_jobs_kernel<TypeBF16>, jobs)
+                            : cudaLaunchKernelEx(&cfg, tg_row_jobs_kernel<TypeF16>, jobs);
+    }
+};
 
-// `from`, repacked into `to`'s aligned rows.
-cudaError_t repack(tg_dtype t, const Mat &from, const Mat &to, int sms, cudaStream_t stream) {
-    ActParams p = {};
-    p.m = from.rows;
-    p.n = from.cols;
-    p.dy = from.p;
-    p.lddy = from.ld;
-    p.out0 = const_cast<void *>(to.p);
-    p.ldo0 = to.ld;
-    return launch_act<false>(t, p, sms, stream);
-}
-
-// One product of the CTA-pair kernel, in role space.
+// One product, in role space.
 struct Product {
     MlpOp op;
     int64_t m, n;      // rows and columns of one output
@@ -299,7 +359,10 @@ constexpr TileCost kTiles[] = {{2, 256, 0.350, 4.5, 5.0, 3.0},
                                {1, 256, 0.395, 4.5, 5.0, 3.0},
                                {1, 128, 0.283, 2.0, 3.0, 1.2}};
 constexpr int kSplitMax = SPLIT_PARTS + 1;
-constexpr int64_t kMlpTicketWaves = 6;
+// Tickets (units claimed in order from a counter) from six waves of tiles up,
+// as in the CTA-pair GEMM, and only for tiles that take longer than a claim
+// (about 2 us: at one K block, 1 x 1168 x 7568, tickets cost 18 of 22 us).
+constexpr int64_t kMlpTicketWaves = 6, kMlpTicketBlocks = 16;
 
 TilePlan plan_tiles(const Product &q, int sms) {
     const bool dual = q.op == MlpOp::GATED;
@@ -329,7 +392,7 @@ TilePlan plan_tiles(const Product &q, int sms) {
         best.tiles = tiles;
         best.tiles_per_entry = mb * nb;
         best.split_max = split;
-        best.ticket = tiles >= kMlpTicketWaves * teams;
+        best.ticket = tiles >= kMlpTicketWaves * teams && nkb >= kMlpTicketBlocks;
         // With a wave or more the grid is every team; below that, one team per
         // tile and K segment.
         best.grid = (int)(tc.cg * (tiles >= teams ? teams : tiles * split));
@@ -339,7 +402,16 @@ TilePlan plan_tiles(const Product &q, int sms) {
     return best;
 }
 
-tg_status run_tiles(const Product &q, tg_dtype t, const Device &dev, cudaStream_t stream) {
+tg_status run_stream(const Product &q, tg_dtype t, const Device &dev, cudaStream_t stream);
+
+// The weight-streaming kernel takes up to this many tokens: its token operand
+// is one MMA's columns, re-read by every weight tile from L2 (16 KB per 16 KB
+// of weights at 128 tokens); beyond, 128- and 256-row token tiles waste less.
+constexpr int64_t kStreamTokens = 128;
+
+tg_status run_product(const Product &q, tg_dtype t, const Device &dev, cudaStream_t stream) {
+    if (q.op != MlpOp::WGRAD && q.m <= kStreamTokens && q.k[0] > 0 && !q.out_f32)
+        return run_stream(q, t, dev, stream);
     const TilePlan plan = plan_tiles(q, dev.sms);
     MlpLaunch la;
     std::memset(&la, 0, sizeof(la));
@@ -347,11 +419,12 @@ tg_status run_tiles(const Product &q, tg_dtype t, const Device &dev, cudaStream_
     const tg_out_dtype ot = out_type(t);
     const int64_t nkb = div_up(q.k[0], 64) + div_up(q.k[1], 64);
     if (nkb > INT32_MAX / 2 || plan.tiles > INT32_MAX) return TG_ERR_INVALID_VALUE;
+    const int b_box = bm ? 64 : q.op == MlpOp::GATED ? plan.block_n / 2 : plan.block_n / plan.cg;
     for (int i = 0; i < 2 && nkb > 0; ++i) {
-        const Mat &a = q.a[i].p ? q.a[i] : q.a[0], &b = q.b[i].p ? q.b[i] : q.b[0];
-        if (!host::encode_rows(&la.maps.a[i], ot, a.p, a.rows, a.cols, a.ld, am ? 64 : BLOCK_M) ||
-            !host::encode_rows(&la.maps.b[i], ot, b.p, b.rows, b.cols, b.ld,
-                               bm ? 64 : q.op == MlpOp::GATED ? plan.block_n / 2 : plan.block_n / plan.cg))
+        const Mat &a = q.a[i], &b = q.b[i];
+        if (a.p && !host::encode_rows(&la.maps.a[i], ot, a.p, a.rows, a.cols, a.ld, am ? 64 : BLOCK_M))
+            return TG_ERR_INVALID_VALUE;
+        if (b.p && !host::encode_rows(&la.maps.b[i], ot, b.p, b.rows, b.cols, b.ld, b_box))
             return TG_ERR_INVALID_VALUE;
     }
     MlpParams &p = la.p;
@@ -403,30 +476,35 @@ tg_status run_tiles(const Product &q, tg_dtype t, const Device &dev, cudaStream_
     return e == cudaSuccess ? TG_OK : TG_ERR_CUDA;
 }
 
-// The weight-streaming kernel takes up to this many tokens: its token operand
-// is one MMA's columns, re-read by every weight tile from L2 (16 KB per 16 KB
-// of weights at 128 tokens); beyond, 256-row token tiles waste less.
-constexpr int64_t kStreamTokens = 128;
-// K blocks a CTA's share spans at least: below that the join costs more than
-// the loads it spreads.
-constexpr int64_t kStreamMinBlocks = 4;
+// K blocks a CTA's share spans at least: below that the join, whose reads grow
+// with the tokens, costs more than the loads it spreads (68 x 1216 x 2560: 14.9
+// us at 4 blocks).
+int64_t stream_min_blocks(int nt) { return nt <= 16 ? 4 : nt <= 32 ? 6 : nt <= 64 ? 8 : 12; }
 
 tg_status run_stream(const Product &q, tg_dtype t, const Device &dev, cudaStream_t stream) {
     StreamLaunch la;
     std::memset(&la, 0, sizeof(la));
-    la.dual = q.op == MlpOp::GATED;
+    la.op = q.op == MlpOp::GATED   ? StreamOp::GATED
+            : q.op == MlpOp::DGRAD ? StreamOp::DGRAD
+                                   : StreamOp::LINEAR;
     la.nt = q.m <= 16 ? 16 : q.m <= 32 ? 32 : q.m <= 64 ? 64 : 128;
     const tg_out_dtype ot = out_type(t);
-    bool ok = host::encode_rows(&la.maps.w[0], ot, q.b[0].p, q.n, q.k[0], q.b[0].ld, BLOCK_M) &&
-              host::encode_rows(&la.maps.x, ot, q.a[0].p, q.m, q.k[0], q.a[0].ld, la.nt);
-    if (ok && la.dual)
-        ok = host::encode_rows(&la.maps.w[1], ot, q.b[1].p, q.n, q.k[0], q.b[1].ld, BLOCK_M);
-    if (!ok) return TG_ERR_INVALID_VALUE;
+    // Weights: 128-row boxes, or 64 x 64 ones where they are read transposed.
+    const int box = q.op == MlpOp::DGRAD ? 64 : BLOCK_M;
+    for (int i = 0; i < 2; ++i) {
+        if (i > 0 && !q.b[i].p) break;
+        const Mat &a = q.a[i].p ? q.a[i] : q.a[0];
+        if (!host::encode_rows(&la.maps.w[i], ot, q.b[i].p, q.b[i].rows, q.b[i].cols, q.b[i].ld, box) ||
+            !host::encode_rows(&la.maps.x[i], ot, a.p, a.rows, a.cols, a.ld, la.nt))
+            return TG_ERR_INVALID_VALUE;
+    }
     StreamParams &p = la.p;
     p.tokens = (int32_t)q.m;
     p.features = (int32_t)q.n;
     p.tiles = (int32_t)div_up(q.n, BLOCK_M);
-    p.num_k_blocks = (int32_t)div_up(q.k[0], 64);
+    p.k_blocks0 = (int32_t)div_up(q.k[0], 64);
+    if (p.k_blocks0 > INT32_MAX / 4) return TG_ERR_INVALID_VALUE;
+    p.num_k_blocks = p.k_blocks0 + (int32_t)div_up(q.k[1], 64);
     p.act = q.act;
     p.bias = q.bias;
     p.r = q.r.p;
@@ -436,7 +514,7 @@ tg_status run_stream(const Product &q, tg_dtype t, const Device &dev, cudaStream
         p.out[i].ld = q.out[i].ld;
     }
     const int64_t total = (int64_t)p.tiles * p.num_k_blocks;
-    int64_t grid = total / kStreamMinBlocks;
+    int64_t grid = total / stream_min_blocks(la.nt);
     const int64_t cap = dev.sms < 512 ? dev.sms : 512;
     if (grid > cap) grid = cap;
     if (grid < 1) grid = 1;
@@ -480,8 +558,10 @@ tg_status forward(MlpOp op, int64_t M, int64_t N, int64_t K, Mat x, Mat w, Mat w
     Device dev;
     const tg_status st = host::device(&dev);
     if (st != TG_OK) return st;
+    RowWork work(dev.sms);
     for (int i = 0; i < count; ++i)
-        if (moved[i]) TG_TRY(repack(dtype, from[i], *ops[i], dev.sms, stream));
+        if (moved[i]) work.repack(from[i], *ops[i]);
+    TG_TRY(work.launch(dtype, stream));
     q.op = op;
     q.m = M;
     q.n = N;
@@ -490,8 +570,7 @@ tg_status forward(MlpOp op, int64_t M, int64_t N, int64_t K, Mat x, Mat w, Mat w
     q.a[0] = x;
     q.b[0] = w;
     q.b[1] = w2;
-    if (M <= kStreamTokens && K > 0) return run_stream(q, dtype, dev, stream);
-    return run_tiles(q, dtype, dev, stream);
+    return run_product(q, dtype, dev, stream);
 }
 
 }  // namespace
@@ -553,8 +632,7 @@ LinearSpace linear_space(int64_t M, int64_t N, int64_t K, const Mat &dy, const M
         if (s.w_moved) s.w = s.arena.repacked(w);
     }
     if (db) {
-        s.bands = act_bands(M, N, sms);
-        s.bands = div_up(M, div_up(M, s.bands));
+        s.bands = row_bands(M, N, sms);
         s.partial = static_cast<float *>(s.arena.take(4 * N * s.bands));
     }
     (void)K;
@@ -601,10 +679,9 @@ extern "C" tg_status tg_linear_backward(int64_t M, int64_t N, int64_t K, const v
     const Mat dy = mat(dY, lddy, M, N), x = mat(X, ldx, M, K), w = mat(W, ldw, N, K);
     LinearSpace s = linear_space(M, N, K, dy, x, w, act != TG_ACT_NONE, dx, dw, sum, dev.sms, workspace);
     if (!space_ok(s.arena, workspace, workspace_bytes)) return TG_ERR_INVALID_VALUE;
+    RowWork work(dev.sms);
     if (s.dz_made || s.partial) {
-        ActParams p = {};
-        p.m = M;
-        p.n = N;
+        RowJob &p = work.add(M, N);
         p.dy = dY;
         p.lddy = lddy;
         if (act != TG_ACT_NONE) {
@@ -617,11 +694,10 @@ extern "C" tg_status tg_linear_backward(int64_t M, int64_t N, int64_t K, const v
             p.ldo0 = s.dz.ld;
         }
         p.partial = s.partial;
-        TG_TRY(launch_act<false>(dtype, p, dev.sms, stream));
     }
-    if (sum) TG_TRY(host::colsum_finish(s.partial, nullptr, (int32_t)s.bands, N, db, nullptr, stream));
-    if (s.w_moved) TG_TRY(repack(dtype, w, s.w, dev.sms, stream));
-    if (s.x_moved) TG_TRY(repack(dtype, x, s.x, dev.sms, stream));
+    if (s.w_moved) work.repack(w, s.w);
+    if (s.x_moved) work.repack(x, s.x);
+    TG_TRY(work.launch(dtype, stream));
     if (dx) {
         Product q = {};
         q.op = MlpOp::DGRAD;
@@ -632,7 +708,7 @@ extern "C" tg_status tg_linear_backward(int64_t M, int64_t N, int64_t K, const v
         q.a[0] = s.dz;
         q.b[0] = s.w;
         q.out[0] = mat(dX, lddx, M, K);
-        st = run_tiles(q, dtype, dev, stream);
+        st = run_product(q, dtype, dev, stream);
         if (st != TG_OK) return st;
     }
     if (dw) {
@@ -646,9 +722,11 @@ extern "C" tg_status tg_linear_backward(int64_t M, int64_t N, int64_t K, const v
         q.b[0] = s.x;
         q.out[0] = mat(dW, lddw, N, K, ew);
         q.out_f32 = dw_dtype == TG_OUT_F32;
-        st = run_tiles(q, dtype, dev, stream);
+        st = run_product(q, dtype, dev, stream);
         if (st != TG_OK) return st;
     }
+    if (sum)
+        TG_TRY(host::colsum_finish(s.partial, nullptr, (int32_t)s.bands, N, db, nullptr, stream));
     return TG_OK;
 }
 
@@ -742,10 +820,10 @@ extern "C" tg_status tg_gated_backward(int64_t M, int64_t N, int64_t K, const vo
     const Mat x = mat(X, ldx, M, K), wg = mat(Wg, ldwg, N, K), wu = mat(Wu, ldwu, N, K);
     GatedSpace s = gated_space(M, N, x, wg, wu, dx, dw, workspace);
     if (!space_ok(s.arena, workspace, workspace_bytes)) return TG_ERR_INVALID_VALUE;
+    RowWork work(dev.sms);
     if (M > 0 && N > 0) {
-        ActParams p = {};
-        p.m = M;
-        p.n = N;
+        RowJob &p = work.add(M, N);
+        p.gated = 1;
         p.dy = dH;
         p.lddy = lddh;
         p.z = G;
@@ -757,11 +835,11 @@ extern "C" tg_status tg_gated_backward(int64_t M, int64_t N, int64_t K, const vo
         p.ldo0 = s.dg.ld;
         p.out1 = const_cast<void *>(s.du.p);
         p.ldo1 = s.du.ld;
-        TG_TRY(launch_act<true>(dtype, p, dev.sms, stream));
     }
-    if (s.wg_moved) TG_TRY(repack(dtype, wg, s.wg, dev.sms, stream));
-    if (s.wu_moved) TG_TRY(repack(dtype, wu, s.wu, dev.sms, stream));
-    if (s.x_moved) TG_TRY(repack(dtype, x, s.x, dev.sms, stream));
+    if (s.wg_moved) work.repack(wg, s.wg);
+    if (s.wu_moved) work.repack(wu, s.wu);
+    if (s.x_moved) work.repack(x, s.x);
+    TG_TRY(work.launch(dtype, stream));
     if (dx) {
         Product q = {};
         q.op = MlpOp::DGRAD;
@@ -774,7 +852,7 @@ extern "C" tg_status tg_gated_backward(int64_t M, int64_t N, int64_t K, const vo
         q.b[0] = s.wg;
         q.b[1] = s.wu;
         q.out[0] = mat(dX, lddx, M, K);
-        st = run_tiles(q, dtype, dev, stream);
+        st = run_product(q, dtype, dev, stream);
         if (st != TG_OK) return st;
     }
     if (dw) {
@@ -790,7 +868,7 @@ extern "C" tg_status tg_gated_backward(int64_t M, int64_t N, int64_t K, const vo
         q.out[0] = dWg ? mat(dWg, lddwg, N, K, ew) : mat(dWu, lddwu, N, K, ew);
         if (q.entries == 2) q.out[1] = mat(dWu, lddwu, N, K, ew);
         q.out_f32 = dw_dtype == TG_OUT_F32;
-        st = run_tiles(q, dtype, dev, stream);
+        st = run_product(q, dtype, dev, stream);
         if (st != TG_OK) return st;
     }
     return TG_OK;

@@ -32,7 +32,7 @@ struct StreamLaunch {
     StreamMaps maps;
     StreamParams p;
     int nt;
-    bool dual;
+    StreamOp op;
     int grid;
     int device;
     cudaStream_t stream;
