@@ -8,10 +8,12 @@
 // 128-row operand and the tokens the NT-column one (NT = 16, 32, 64 or 128,
 // zero rows beyond the tokens), so every weight byte crosses shared memory
 // once and the accumulator wastes columns, which cost nothing, instead of
-// rows.  One CTA per SM keeps a ring of 100 KB (200 KB for 64 tokens and more) of
-// TMA loads in flight: 6.7 TB/s at about 1 us of latency needs 44 KB per SM.  With
-// the small ring the next kernel's CTA fits beside this one: its set-up and an
-// L2 prefetch of its first weights run under this kernel's end.
+// rows.  One CTA per SM keeps a ring of 100 or 200 KB of TMA loads in flight: 6.7
+// TB/s at about 1 us of latency needs 44 KB per SM.  With the small ring the next
+// kernel's CTA fits beside this one: its set-up and, for short shares, an L2
+// prefetch of its first weights run under this kernel's end.  What a call costs
+// above its bytes is about 5 us of start, join and end; in between the weights
+// arrive at 6.5 TB/s.
 //
 // Work split: the (tile, K block) iterations of all 128-feature tiles are cut
 // into equal contiguous shares, one per CTA, so that 112 tiles (say) load 152
@@ -47,12 +49,17 @@ struct StreamConfig {
     static constexpr int A_BYTES = BLOCK_M * ROW_BYTES;
     static constexpr int B_BYTES = NT * ROW_BYTES;
     static constexpr int STAGE_BYTES = MATS * A_BYTES + B_BYTES;
-    // Up to 32 tokens a ring of about 100 KB (two CTAs to an SM), else all of
-    // shared memory.
-    static constexpr int BUDGET = NT <= 32 ? SMEM_LIMIT / 2 - 1024 : SMEM_LIMIT;
+    // One weight matrix and up to 32 tokens: a ring of about 100 KB, two CTAs to
+    // an SM (1 x 4096 x 4096 10.1 us, 10.4 with all of shared memory); else all of
+    // it (gated, 4 x 14336 x 4096: 40.9 us, 42.9 with half).
+    static constexpr bool SMALL = NT <= 32 && !DUAL;
+    static constexpr int BUDGET = SMALL ? SMEM_LIMIT / 2 - 1024 : SMEM_LIMIT;
     static constexpr int FIT = (BUDGET - 2048) / STAGE_BYTES;
     static constexpr int STAGES = FIT > 12 ? 12 : FIT;
-    static constexpr int PREFETCH = 16 / MATS;  // K blocks prefetched into L2 (256 KB a CTA)
+    // K blocks prefetched into L2 ahead of the first load (256 KB a CTA), and the
+    // longest share that this pays for: 1 x 4096 x 4096 (13 blocks a CTA) 10.1 us
+    // with it and 10.8 without, 1 x 16384 x 4096 (54) 26.6 and 25.9.
+    static constexpr int PREFETCH = 16 / MATS, PREFETCH_SHARE = 32;
     static constexpr int BAR_OFF = STAGES * STAGE_BYTES;
     static constexpr int FULL0 = 0, EMPTY0 = STAGES, ACCF0 = 2 * STAGES, ACCE0 = ACCF0 + 2,
                          DRAIN = ACCE0 + 2, NUM_BARS = DRAIN + 1;
@@ -128,7 +135,8 @@ __device__ __forceinline__ uint16_t mlp_narrow(float y) {
 }
 
 template <Kind KD, int NT, StreamOp OP>
-__global__ void __launch_bounds__(StreamConfig<KD, NT, OP>::NUM_THREADS, NT <= 32 ? 2 : 1)
+__global__ void __launch_bounds__(StreamConfig<KD, NT, OP>::NUM_THREADS,
+                                  StreamConfig<KD, NT, OP>::SMALL ? 2 : 1)
     tg_stream_kernel(const __grid_constant__ StreamMaps maps, const StreamParams p) {
     using C = StreamConfig<KD, NT, OP>;
     constexpr bool DUAL = C::DUAL, TRANS = C::TRANS;
@@ -181,7 +189,8 @@ __global__ void __launch_bounds__(StreamConfig<KD, NT, OP>::NUM_THREADS, NT <= 3
             // of whatever that kernel still writes.
             {
                 StreamUnits un(p);
-                for (int left = C::PREFETCH; left > 0 && un.next(p);)
+                for (int left = un.pos - un.lo <= C::PREFETCH_SHARE ? C::PREFETCH : 0;
+                     left > 0 && un.next(p);)
                     for (int kb = un.k0; kb < un.k1 && left > 0; ++kb, --left) {
                         const int second = TRANS && kb >= p.k_blocks0;
                         const int32_t kc = (kb - (second ? p.k_blocks0 : 0)) * C::BK;
@@ -345,7 +354,7 @@ __global__ void __launch_bounds__(StreamConfig<KD, NT, OP>::NUM_THREADS, NT <= 3
                     constexpr int TC = tc.value;
                     // The tokens' sums: this CTA's and the partials, nearest
                     // first, WAYS CTAs' loads in flight at once.
-                    constexpr int WAYS = TC == 4 ? 8 : NT <= 32 ? 2 : 4;
+                    constexpr int WAYS = TC == 4 ? 8 : C::SMALL ? 2 : 4;
                     auto load_acc = [&](int a, float (&y)[TC]) {
                         uint32_t v[16];
                         tmem_ld_32x32b_x16(taddr + a * NT + j0, v);

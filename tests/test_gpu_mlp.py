@@ -390,3 +390,57 @@ def test_ragged_columns_on_aligned_rows(tg, n):
     h.check_linear_backward(tg, 64, 72, n, "fp16", pad=pad)
     h.check_linear_backward(tg, 64, 72, n, "fp16", pad=-n % 4, dw="f32")
     h.check_gated(tg, 150, n, 64, "bf16", save=True, pad=0)
+
+
+def test_offsets_beyond_32_bits(tg):
+    """Outputs, residuals and inputs whose element offsets pass 2^31."""
+    m, n, k, ld = 70000, 72, 64, 33000
+    g = h.gen(14)
+    st = torch.cuda.current_stream()
+    wide = torch.empty(m, ld, dtype=torch.bfloat16, device="cuda")  # 4.6 GB
+    x = torch.randn(m, k, generator=g, device="cuda").to(torch.bfloat16)
+    w = h.rows(g, n, k, "bf16", scale=0.1)
+    y = wide[:, 100:100 + n]
+    y.copy_(torch.randn(m, n, generator=g, device="cuda"))
+    r = y[-300:].double()
+    h.done(tg, tg.tg_linear(m, n, k, x, k, w, w.ld, None, "none", y, ld, y, ld, None, 0, "bf16", None,
+                            st), "wide rows")
+    want = x[-300:].double() @ w.d().t() + r
+    e = h.product_error(k, x[-300:].double().abs() @ w.d().abs().t()) + 2.0 ** -23 * want.abs()
+    h.check(y[-300:], want, h.rounded("bf16", want, e), "rows beyond 2^31 elements")
+    x = wide[:, :512]
+    x.copy_(torch.randn(m, 512, generator=g, device="cuda"))
+    out = torch.empty(m, 512, dtype=torch.bfloat16, device="cuda")
+    h.done(tg, tg.tg_layer_norm(m, 512, x, ld, None, None, 1e-5, out, 512, None, None, "bf16", st), "norm")
+    mean, rstd = h.norm_stats(x[-300:].double(), 1e-5)
+    want = (x[-300:].double() - mean) * rstd
+    h.check(out[-300:], want, h.rounded("bf16", want, 1e-5 * (1 + want.abs())), "norm beyond 2^31 elements")
+    # The backward pass reads dY there too (and repacks X's odd rows).
+    dx = torch.empty(m, k, dtype=torch.bfloat16, device="cuda")
+    db = torch.empty(n, device="cuda")
+    ws = h.space(tg.tg_linear_backward_workspace_bytes(m, n, k, y, ld, wide[:, 1:], ld, w, w.ld, "none", "bf16"))
+    h.done(tg, tg.tg_linear_backward(m, n, k, y, ld, None, k, w, w.ld, None, 0, "none", dx, k, None, k,
+                                     "bf16", db, "bf16", ws, st), "backward")
+    want = y[-300:].double() @ w.d()
+    e = h.product_error(n, y[-300:].double().abs() @ w.d().abs())
+    h.check(dx[-300:], want, h.rounded("bf16", want, e), "dX beyond 2^31 elements")
+    s = y.double()
+    h.check(db, s.sum(0), m * 2.0 ** -24 * s.abs().sum(0), "db over all rows")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("m", [1, 5, 16, 33, 64, 100, 128])
+def test_input_gradients_of_few_tokens(tg, m, dtype):
+    """Transposed weights through the streaming kernel, long reductions cut
+    into shares, one and two operand pairs."""
+    h.check_linear_backward(tg, m, 2000, 300, dtype, "silu", want_dw=False, bias=False)
+    h.check_gated_backward(tg, m, 1000, 520, dtype, want=(True, False, False))
+
+
+@pytest.mark.parametrize("ld_pad", range(8))
+def test_every_row_alignment(tg, ld_pad):
+    """Row strides and bases of every residue modulo 16 bytes."""
+    for skew in range(8):
+        h.check_linear(tg, 40, 70, 150, "bf16", bias=True, residual=True, save=True, pad=ld_pad, skew=skew)
+        h.check_linear_backward(tg, 33, 70, 150, "fp16", "relu", pad=ld_pad, skew=skew)
+        h.check_linear(tg, 140, 70, 24, "bf16", residual=True, pad=ld_pad, skew=skew)
