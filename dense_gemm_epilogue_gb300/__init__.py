@@ -13,10 +13,13 @@ legacy default stream).
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 import threading
 
 from .build import LIB as LIBRARY_PATH
+from .build import PYCALL as _PYCALL_PATH
 from .build import build, source_hash  # noqa: F401
 
 TG_OK = 0
@@ -150,11 +153,26 @@ class tg_plan_info(ctypes.Structure):
 
 _lock = threading.Lock()
 _lib = None
+_call = None  # the hot calls without ctypes (csrc/tg_pycall.c), when built
+_CALLS = ("tg_linear_workspace_bytes", "tg_linear", "tg_gated_workspace_bytes", "tg_gated",
+          "tg_layer_norm", "tg_layer_norm_backward_workspace_bytes", "tg_layer_norm_backward")
+
+
+def _load_calls(lib):
+    """The marshalling module bound to this library's entry points, or None."""
+    if not os.path.exists(_PYCALL_PATH):
+        return None
+    loader = importlib.machinery.ExtensionFileLoader("_tgcall", _PYCALL_PATH)
+    spec = importlib.util.spec_from_loader("_tgcall", loader)
+    mod = importlib.util.module_from_spec(spec)
+    loader.exec_module(mod)
+    mod.bind({n: ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in _CALLS})
+    return mod
 
 
 def load(path: str | None = None) -> ctypes.CDLL:
     """Load the built library (raises if it has not been built)."""
-    global _lib
+    global _lib, _call
     if _lib is not None and path is None:
         return _lib
     with _lock:
@@ -251,6 +269,7 @@ def load(path: str | None = None) -> ctypes.CDLL:
         lib.tg_version.argtypes = []
         lib.tg_version.restype = i32
         if path is None:
+            _call = _load_calls(lib)
             _lib = lib
         return lib
 
@@ -448,6 +467,8 @@ def _space(w):
 
 
 def tg_linear_workspace_bytes(M, N, K, X, ldx, W, ldw, dtype) -> int:
+    if _call is not None:
+        return _call.tg_linear_workspace_bytes(M, N, K, X, ldx, W, ldw, dtype)
     return load().tg_linear_workspace_bytes(M, N, K, _ptr(X), ldx, _ptr(W), ldw, _dtype(dtype))
 
 
@@ -455,6 +476,9 @@ def tg_linear(M, N, K, X, ldx, W, ldw, bias, act, R, ldr, Y, ldy, Z, ldz, dtype,
               stream=None) -> int:
     """Y = act(X W^T + bias) + R and, when Z is given, Z = X W^T + bias (row-major; bias, R and Z
     may be None; act a name of ACT_CODES).  workspace: None, a tensor or (pointer, bytes)."""
+    if _call is not None:
+        return _call.tg_linear(M, N, K, X, ldx, W, ldw, bias, act, R, ldr, Y, ldy, Z, ldz, dtype,
+                               workspace, stream)
     ws, n = _space(workspace)
     return load().tg_linear(M, N, K, _ptr(X), ldx, _ptr(W), ldw, _ptr(bias), _act(act), _ptr(R),
                             ldr, _ptr(Y), ldy, _ptr(Z), ldz, _dtype(dtype), ws, n, _stream(stream))
@@ -477,6 +501,8 @@ def tg_linear_backward(M, N, K, dY, lddy, X, ldx, W, ldw, Z, ldz, act, dX, lddx,
 
 
 def tg_gated_workspace_bytes(M, N, K, X, ldx, Wg, ldwg, Wu, ldwu, dtype) -> int:
+    if _call is not None:
+        return _call.tg_gated_workspace_bytes(M, N, K, X, ldx, Wg, ldwg, Wu, ldwu, dtype)
     return load().tg_gated_workspace_bytes(M, N, K, _ptr(X), ldx, _ptr(Wg), ldwg, _ptr(Wu), ldwu,
                                            _dtype(dtype))
 
@@ -485,6 +511,9 @@ def tg_gated(M, N, K, X, ldx, Wg, ldwg, Wu, ldwu, act, H, ldh, G, ldg, U, ldu, d
              workspace=None, stream=None) -> int:
     """H = act(X Wg^T) * (X Wu^T) in one kernel; G and U (the two products) are stored when
     given."""
+    if _call is not None:
+        return _call.tg_gated(M, N, K, X, ldx, Wg, ldwg, Wu, ldwu, act, H, ldh, G, ldg, U, ldu, dtype,
+                              workspace, stream)
     ws, n = _space(workspace)
     return load().tg_gated(M, N, K, _ptr(X), ldx, _ptr(Wg), ldwg, _ptr(Wu), ldwu, _act(act),
                            _ptr(H), ldh, _ptr(G), ldg, _ptr(U), ldu, _dtype(dtype), ws, n,
@@ -510,17 +539,24 @@ def tg_gated_backward(M, N, K, dH, lddh, X, ldx, Wg, ldwg, Wu, ldwu, G, ldg, U, 
 def tg_layer_norm(M, N, X, ldx, gamma, beta, eps, Y, ldy, mean, rstd, dtype, stream=None) -> int:
     """Y = (X - mean) rstd gamma + beta per row; gamma, beta, mean and rstd may be None; dtype a
     name of OUT_CODES."""
+    if _call is not None:
+        return _call.tg_layer_norm(M, N, X, ldx, gamma, beta, eps, Y, ldy, mean, rstd, dtype, stream)
     return load().tg_layer_norm(M, N, _ptr(X), ldx, _ptr(gamma), _ptr(beta), eps, _ptr(Y), ldy,
                                 _ptr(mean), _ptr(rstd), _out(dtype), _stream(stream))
 
 
 def tg_layer_norm_backward_workspace_bytes(M, N) -> int:
+    if _call is not None:
+        return _call.tg_layer_norm_backward_workspace_bytes(M, N)
     return load().tg_layer_norm_backward_workspace_bytes(M, N)
 
 
 def tg_layer_norm_backward(M, N, dY, lddy, X, ldx, gamma, mean, rstd, dX, lddx, dgamma, dbeta,
                            dtype, workspace=None, stream=None) -> int:
     """dX, dgamma and dbeta (each may be None) of tg_layer_norm."""
+    if _call is not None:
+        return _call.tg_layer_norm_backward(M, N, dY, lddy, X, ldx, gamma, mean, rstd, dX, lddx, dgamma,
+                                            dbeta, dtype, workspace, stream)
     ws, n = _space(workspace)
     return load().tg_layer_norm_backward(M, N, _ptr(dY), lddy, _ptr(X), ldx, _ptr(gamma),
                                          _ptr(mean), _ptr(rstd), _ptr(dX), lddx, _ptr(dgamma),

@@ -13,12 +13,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_lib")
 LIB = os.path.join(OUT_DIR, "libtg_gemm.so")
+PYCALL = os.path.join(OUT_DIR, "_tgcall.so")
 OBJ_DIR = os.path.join(HERE, "_build")
 SOURCES = ["tg_gemm.cu", "tg_inst_bf16.cu", "tg_inst_fp16.cu", "tg_inst_tf32.cu",
            "tg_inst_e4m3.cu", "tg_inst_e5m2.cu", "tg_inst_mx.cu", "tg_noalloc.cu", "tg_mlp.cu",
@@ -42,7 +44,7 @@ def source_hash() -> str:
     h = hashlib.sha256()
     names = sorted(os.listdir(CSRC))
     for n in names:
-        if n.endswith((".cu", ".cuh", ".h")):
+        if n.endswith((".cu", ".cuh", ".h", ".c")):
             with open(os.path.join(CSRC, n), "rb") as f:
                 h.update(n.encode() + b"\0" + f.read())
     with open(os.path.join(ROOT, "include", "tg_gemm.h"), "rb") as f:
@@ -63,6 +65,24 @@ def _compile(src: str, verbose_ptxas: bool) -> str:
     return obj
 
 
+def _compile_pycall() -> None:
+    """The host-only module that marshals the hot Python calls (needs Python's
+    headers; without them, or a C compiler, the ctypes wrappers serve alone)."""
+    include = sysconfig.get_paths()["include"]
+    cc = shutil.which("gcc") or shutil.which("cc")
+    if os.path.exists(PYCALL):
+        os.remove(PYCALL)
+    if cc is None or not os.path.exists(os.path.join(include, "Python.h")):
+        return
+    tmp = PYCALL + ".tmp.%d" % os.getpid()
+    r = subprocess.run([cc, "-O2", "-std=c11", "-Wall", "-shared", "-fPIC", "-I", include, "-I",
+                        os.path.join(ROOT, "include"), os.path.join(CSRC, "tg_pycall.c"), "-o", tmp],
+                       capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cc} failed on tg_pycall.c:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, PYCALL)
+
+
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     stamp = os.path.join(OUT_DIR, "BUILD_HASH")
     want = source_hash()
@@ -80,6 +100,7 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    _compile_pycall()
     with open(stamp, "w") as f:
         f.write(want + "\n")
     return LIB

@@ -7,13 +7,20 @@ from __future__ import annotations
 import pytest
 
 
-@pytest.fixture(scope="module")
-def tg():
+@pytest.fixture(scope="module", params=["module", "ctypes"])
+def tg(request):
+    """Through the marshalling module, and through ctypes alone."""
     import dense_gemm_epilogue_gb300 as tg
 
     tg.build()
     tg.load()
-    return tg
+    kept = tg._call
+    if request.param == "ctypes":
+        tg._call = None
+    elif kept is None:
+        pytest.skip("built without Python's headers")
+    yield tg
+    tg._call = kept
 
 
 A = 1 << 20  # an aligned non-NULL address; never dereferenced here
@@ -188,3 +195,32 @@ def test_act_names(tg):
     assert tg.ACT_CODES == {"none": 0, "relu": 1, "silu": 2, "gelu_tanh": 3}
     with pytest.raises(KeyError):
         linear(tg, act="swish")
+
+
+def test_argument_kinds(tg):
+    """Integers, index-like objects, tensors and None; everything else is a
+    TypeError naming the type."""
+    class Seven:
+        def __index__(self):
+            return 7
+
+    assert norm(tg, M=0, N=Seven(), ldx=Seven(), ldy=Seven(), X=None, Y=None) == OK
+    with pytest.raises(TypeError):
+        linear(tg, X="not a pointer")
+    with pytest.raises(TypeError):
+        linear(tg, stream="not a stream")
+    with pytest.raises(TypeError):
+        linear(tg, K=1.5)
+
+    class Stream:
+        cuda_stream = 0
+
+    assert linear(tg, M=0, X=None, Y=None, R=None, Z=None, stream=Stream()) == OK
+
+
+def test_tensors_as_pointers_and_workspaces(tg):
+    torch = pytest.importorskip("torch")
+    x = torch.zeros(64, 129, dtype=torch.bfloat16)
+    ws = torch.empty(64, dtype=torch.uint8)
+    assert linear(tg, M=0, X=x, ldx=129, workspace=ws) == OK
+    assert linear(tg, X=x, ldx=129, workspace=ws) == INVALID  # a workspace too small
