@@ -170,6 +170,13 @@ struct MlpParams {
     int64_t ldr;
     int32_t r_vec;            // 1: the residual's rows are 16-byte aligned
     int32_t out_f32;          // PLAIN: outputs are FP32 (else the operands' type)
+    // 1: this product reads nothing that the kernel before it writes (a weight
+    // gradient after the input gradient), so it starts without waiting for that
+    // kernel and waits at its end, for whatever comes next on the stream.  That
+    // the kernels before that one are complete follows from when an input
+    // gradient lets its successor start: after its own wait.  Only one of the two
+    // may use the stream's workspace.
+    int32_t late_wait;
     MlpOut out[3];            // LINEAR: Y, Z; GATED: H, G, U; PLAIN: one per entry
 };
 
@@ -405,7 +412,14 @@ __global__ void __launch_bounds__(MlpConfig<KD, CG, BN, AM, BM, EP>::NUM_THREADS
     if constexpr (CG == 2) cluster_sync_all();
     else __syncthreads();
     tc_fence_after();
-    griddep_launch();
+    // The kernel before this one: waited for here, or (late_wait) at the end.
+    auto wait_before = [&] {
+        if (!mp.late_wait) griddep_wait();
+    };
+    // The next kernel may be set up beside this one from here on; an input
+    // gradient holds it back until its own wait (see late_wait).
+    constexpr bool HOLD = AM == 0 && BM == 1;
+    if (!HOLD) griddep_launch();
     const uint32_t tmem_base = *tmem_slot;
     const UnitPlan up = make_unit_plan(p, num_pairs);
     // Tickets as in the CTA-pair GEMM: the first unit static, later ones
@@ -443,7 +457,7 @@ __global__ void __launch_bounds__(MlpConfig<KD, CG, BN, AM, BM, EP>::NUM_THREADS
                 int bt, mb, nb;
                 batch_tile_coords(un.tile, p, bt, mb, nb);
                 if (!waited) {
-                    griddep_wait();
+                    wait_before();
                     waited = true;
                 }
                 if (tick) {
@@ -524,7 +538,8 @@ __global__ void __launch_bounds__(MlpConfig<KD, CG, BN, AM, BM, EP>::NUM_THREADS
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------------------ MMA issuer (leader)
-        griddep_wait();
+        wait_before();
+        if (HOLD) griddep_launch();
         if (leader && lane == 0) {
             int s = 0;
             uint32_t ph = 0;
@@ -581,7 +596,7 @@ __global__ void __launch_bounds__(MlpConfig<KD, CG, BN, AM, BM, EP>::NUM_THREADS
         __syncwarp();
     } else {
         // ------------------------------------------------------ epilogue (both CTAs)
-        griddep_wait();
+        wait_before();
         const int q = warp & 3;
         const int ew = warp - 2;
         constexpr int EPI_THREADS = C::EPI_WARPS * 32;
@@ -851,6 +866,7 @@ __global__ void __launch_bounds__(MlpConfig<KD, CG, BN, AM, BM, EP>::NUM_THREADS
         }
     }
 
+    if (mp.late_wait) griddep_wait();
     tc_fence_before();
     if constexpr (CG == 2) cluster_sync_all();
     else __syncthreads();

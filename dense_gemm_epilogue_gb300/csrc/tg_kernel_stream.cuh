@@ -178,7 +178,9 @@ __global__ void __launch_bounds__(StreamConfig<KD, NT, OP>::NUM_THREADS,
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    griddep_launch();
+    // (an input gradient holds its successor back until its own wait: see
+    // MlpParams::late_wait)
+    if (!TRANS) griddep_launch();
     const uint32_t tmem_base = *tmem_slot;
     const int nkb = p.num_k_blocks;
 
@@ -239,6 +241,8 @@ __global__ void __launch_bounds__(StreamConfig<KD, NT, OP>::NUM_THREADS,
         }
         __syncwarp();
     } else if (warp == 1) {
+        griddep_wait();
+        if (TRANS) griddep_launch();
         if (lane == 0) {
             int s = 0;
             uint32_t ph = 0;

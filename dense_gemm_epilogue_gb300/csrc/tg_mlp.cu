@@ -335,6 +335,7 @@ struct Product {
     int act;
     const float *bias;
     Mat r;             // residual (p NULL: none)
+    bool beside;       // reads nothing of the kernel before it: may run beside it
 };
 
 struct TilePlan {
@@ -342,6 +343,7 @@ struct TilePlan {
     int64_t tiles, tiles_per_entry;
     int grid, split_max, group;
     bool ticket;
+    double time;  // the model's, in microseconds
 };
 
 // Times of the planner's cost model, in microseconds, measured on long and
@@ -364,12 +366,15 @@ constexpr int kSplitMax = SPLIT_PARTS + 1;
 // (about 2 us: at one K block, 1 x 1168 x 7568, tickets cost 18 of 22 us).
 constexpr int64_t kMlpTicketWaves = 6, kMlpTicketBlocks = 16;
 
-TilePlan plan_tiles(const Product &q, int sms) {
+// The cheapest plan; or (shape >= 0) kTiles[shape] without split tiles.
+TilePlan plan_tiles(const Product &q, int sms, int shape = -1) {
     const bool dual = q.op == MlpOp::GATED;
     const int64_t nkb = div_up(q.k[0], 64) + div_up(q.k[1], 64);
     TilePlan best = {};
     double best_t = -1;
-    for (const TileCost &tc : kTiles) {
+    for (int i = 0; i < (int)(sizeof(kTiles) / sizeof(kTiles[0])); ++i) {
+        if (shape >= 0 && i != shape) continue;
+        const TileCost &tc = kTiles[i];
         const int64_t teams = sms / tc.cg > 0 ? sms / tc.cg : 1;
         const int64_t mb = div_up(q.m, 128 * tc.cg), nb = div_up(q.n, dual ? tc.bn / 2 : tc.bn);
         const int64_t tiles = q.entries * mb * nb;
@@ -377,7 +382,7 @@ TilePlan plan_tiles(const Product &q, int sms) {
         const double whole = (double)(tiles / teams) * nkb * tc.block;
         double t = whole + (rem ? nkb * tc.block : 0.0) + tc.epilogue;
         int split = 1;
-        for (int s = 2; s <= kSplitMax && rem > 0; ++s) {
+        for (int s = 2; s <= kSplitMax && rem > 0 && shape < 0; ++s) {
             if (s > teams / rem || s > nkb / SPLIT_MIN_KBLOCKS) break;
             const double ts = whole + nkb * tc.block / s + tc.epilogue + tc.join + tc.join_part * (s - 1);
             if (ts < t) {
@@ -386,7 +391,7 @@ TilePlan plan_tiles(const Product &q, int sms) {
             }
         }
         if (best_t >= 0 && t >= best_t) continue;
-        best_t = t;
+        best_t = best.time = t;
         best.cg = tc.cg;
         best.block_n = tc.bn;
         best.tiles = tiles;
@@ -402,6 +407,15 @@ TilePlan plan_tiles(const Product &q, int sms) {
     return best;
 }
 
+// Plans for an input gradient `x` and the weight gradient `w` after it, when
+// both fit the SMs together and running side by side is cheaper than in turn
+// (777 x 1001 x 1365: 128 x 256 tiles, 42 and 48 CTAs at once, against 77 and 88
+// CTAs of 128 x 128 tiles one after the other).
+struct Beside {
+    bool on = false;
+    TilePlan x, w;
+};
+
 tg_status run_stream(const Product &q, tg_dtype t, const Device &dev, cudaStream_t stream);
 
 // The weight-streaming kernel takes up to this many tokens: its token operand
@@ -409,10 +423,29 @@ tg_status run_stream(const Product &q, tg_dtype t, const Device &dev, cudaStream
 // of weights at 128 tokens); beyond, 128- and 256-row token tiles waste less.
 constexpr int64_t kStreamTokens = 128;
 
-tg_status run_product(const Product &q, tg_dtype t, const Device &dev, cudaStream_t stream) {
+Beside plan_beside(const Product &x, const Product &w, int sms) {
+    Beside best;
+    if (x.m <= kStreamTokens || x.k[0] == 0 || w.k[0] == 0) return best;
+    double t = plan_tiles(x, sms).time + plan_tiles(w, sms).time;
+    constexpr int SHAPES = sizeof(kTiles) / sizeof(kTiles[0]);
+    for (int i = 0; i < SHAPES; ++i)
+        for (int j = 0; j < SHAPES; ++j) {
+            const TilePlan a = plan_tiles(x, sms, i), b = plan_tiles(w, sms, j);
+            const double both = a.time > b.time ? a.time : b.time;
+            if (a.grid + b.grid > sms || a.ticket || b.ticket || both >= t) continue;
+            t = both;
+            best.on = true;
+            best.x = a;
+            best.w = b;
+        }
+    return best;
+}
+
+tg_status run_product(const Product &q, tg_dtype t, const Device &dev, cudaStream_t stream,
+                      const TilePlan *chosen = nullptr) {
     if (q.op != MlpOp::WGRAD && q.m <= kStreamTokens && q.k[0] > 0 && !q.out_f32)
         return run_stream(q, t, dev, stream);
-    const TilePlan plan = plan_tiles(q, dev.sms);
+    const TilePlan plan = chosen ? *chosen : plan_tiles(q, dev.sms);
     MlpLaunch la;
     std::memset(&la, 0, sizeof(la));
     const bool am = q.op == MlpOp::WGRAD, bm = q.op == MlpOp::DGRAD || am;
@@ -464,6 +497,8 @@ tg_status run_product(const Product &q, tg_dtype t, const Device &dev, cudaStrea
         g.k_snake = plan.ticket ? 1 : 0;
         if (plan.ticket) g.ticket = w.ticket;
     }
+    // Beside the kernel before it only without the workspace that it may use.
+    p.late_wait = q.beside && plan.split_max == 1 && !plan.ticket;
     la.op = q.op;
     la.cg = plan.cg;
     la.block_n = plan.block_n;
@@ -530,6 +565,18 @@ tg_status run_stream(const Product &q, tg_dtype t, const Device &dev, cudaStream
     la.stream = stream;
     const cudaError_t e = t == TG_BF16 ? launch_stream_bf16(la) : launch_stream_fp16(la);
     return e == cudaSuccess ? TG_OK : TG_ERR_CUDA;
+}
+
+// The input gradient, then the weight gradient (either may be missing).
+tg_status run_gradients(const Product *x, Product *w, tg_dtype t, const Device &dev, cudaStream_t stream) {
+    Beside both;
+    if (x && w) {
+        both = plan_beside(*x, *w, dev.sms);
+        w->beside = true;
+    }
+    tg_status st = x ? run_product(*x, t, dev, stream, both.on ? &both.x : nullptr) : TG_OK;
+    if (st == TG_OK && w) st = run_product(*w, t, dev, stream, both.on ? &both.w : nullptr);
+    return st;
 }
 
 bool space_ok(const Arena &need, const void *workspace, int64_t bytes) {
@@ -698,33 +745,26 @@ extern "C" tg_status tg_linear_backward(int64_t M, int64_t N, int64_t K, const v
     if (s.w_moved) work.repack(w, s.w);
     if (s.x_moved) work.repack(x, s.x);
     TG_TRY(work.launch(dtype, stream));
-    if (dx) {
-        Product q = {};
-        q.op = MlpOp::DGRAD;
-        q.m = M;
-        q.n = K;
-        q.k[0] = N;
-        q.entries = 1;
-        q.a[0] = s.dz;
-        q.b[0] = s.w;
-        q.out[0] = mat(dX, lddx, M, K);
-        st = run_product(q, dtype, dev, stream);
-        if (st != TG_OK) return st;
-    }
-    if (dw) {
-        Product q = {};
-        q.op = MlpOp::WGRAD;
-        q.m = N;
-        q.n = K;
-        q.k[0] = M;
-        q.entries = 1;
-        q.a[0] = s.dz;
-        q.b[0] = s.x;
-        q.out[0] = mat(dW, lddw, N, K, ew);
-        q.out_f32 = dw_dtype == TG_OUT_F32;
-        st = run_product(q, dtype, dev, stream);
-        if (st != TG_OK) return st;
-    }
+    Product qx = {}, qw = {};
+    qx.op = MlpOp::DGRAD;
+    qx.m = M;
+    qx.n = K;
+    qx.k[0] = N;
+    qx.entries = 1;
+    qx.a[0] = s.dz;
+    qx.b[0] = s.w;
+    qx.out[0] = mat(dX, lddx, M, K);
+    qw.op = MlpOp::WGRAD;
+    qw.m = N;
+    qw.n = K;
+    qw.k[0] = M;
+    qw.entries = 1;
+    qw.a[0] = s.dz;
+    qw.b[0] = s.x;
+    qw.out[0] = mat(dW, lddw, N, K, ew);
+    qw.out_f32 = dw_dtype == TG_OUT_F32;
+    st = run_gradients(dx ? &qx : nullptr, dw ? &qw : nullptr, dtype, dev, stream);
+    if (st != TG_OK) return st;
     if (sum)
         TG_TRY(host::colsum_finish(s.partial, nullptr, (int32_t)s.bands, N, db, nullptr, stream));
     return TG_OK;
@@ -840,38 +880,29 @@ extern "C" tg_status tg_gated_backward(int64_t M, int64_t N, int64_t K, const vo
     if (s.wu_moved) work.repack(wu, s.wu);
     if (s.x_moved) work.repack(x, s.x);
     TG_TRY(work.launch(dtype, stream));
-    if (dx) {
-        Product q = {};
-        q.op = MlpOp::DGRAD;
-        q.m = M;
-        q.n = K;
-        q.k[0] = q.k[1] = N;
-        q.entries = 1;
-        q.a[0] = s.dg;
-        q.a[1] = s.du;
-        q.b[0] = s.wg;
-        q.b[1] = s.wu;
-        q.out[0] = mat(dX, lddx, M, K);
-        st = run_product(q, dtype, dev, stream);
-        if (st != TG_OK) return st;
-    }
-    if (dw) {
-        Product q = {};
-        q.op = MlpOp::WGRAD;
-        q.m = N;
-        q.n = K;
-        q.k[0] = M;
-        q.entries = dWg && dWu ? 2 : 1;
-        q.a[0] = dWg ? s.dg : s.du;
-        q.a[1] = s.du;
-        q.b[0] = s.x;
-        q.out[0] = dWg ? mat(dWg, lddwg, N, K, ew) : mat(dWu, lddwu, N, K, ew);
-        if (q.entries == 2) q.out[1] = mat(dWu, lddwu, N, K, ew);
-        q.out_f32 = dw_dtype == TG_OUT_F32;
-        st = run_product(q, dtype, dev, stream);
-        if (st != TG_OK) return st;
-    }
-    return TG_OK;
+    Product qx = {}, qw = {};
+    qx.op = MlpOp::DGRAD;
+    qx.m = M;
+    qx.n = K;
+    qx.k[0] = qx.k[1] = N;
+    qx.entries = 1;
+    qx.a[0] = s.dg;
+    qx.a[1] = s.du;
+    qx.b[0] = s.wg;
+    qx.b[1] = s.wu;
+    qx.out[0] = mat(dX, lddx, M, K);
+    qw.op = MlpOp::WGRAD;
+    qw.m = N;
+    qw.n = K;
+    qw.k[0] = M;
+    qw.entries = dWg && dWu ? 2 : 1;
+    qw.a[0] = dWg ? s.dg : s.du;
+    qw.a[1] = s.du;
+    qw.b[0] = s.x;
+    qw.out[0] = dWg ? mat(dWg, lddwg, N, K, ew) : mat(dWu, lddwu, N, K, ew);
+    if (qw.entries == 2) qw.out[1] = mat(dWu, lddwu, N, K, ew);
+    qw.out_f32 = dw_dtype == TG_OUT_F32;
+    return run_gradients(dx ? &qx : nullptr, dw ? &qw : nullptr, dtype, dev, stream);
 }
 
 // ------------------------------------------------------------------ shared launch
