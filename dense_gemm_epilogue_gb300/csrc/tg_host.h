@@ -1,6 +1,6 @@
 // Host services shared by the operators' entry points: the device's state,
-// the per-stream workspace, tensor-map encoding and small launches.  Defined
-// in tg_gemm.cu (the first four) and tg_mlp.cu.
+// the per-stream workspace, tensor-map encoding (defined in tg_gemm.cu) and the
+// column sums' last step (in tg_mlp.cu).
 #pragma once
 
 #include <cstdint>

@@ -1,6 +1,5 @@
-// Row-wise helpers of the feed-forward operators: typed 16-byte loads and
-// stores with a bounds-checked scalar form, and the fixed-order reduction of
-// per-block column sums.
+// Row-wise helpers of the feed-forward operators: 16-byte vectors of typed
+// elements, and the fixed-order reduction of per-block column sums.
 #pragma once
 
 #include <cstdint>
@@ -39,25 +38,6 @@ struct TypeF16 {
         return *reinterpret_cast<const uint32_t *>(&v);
     }
 };
-
-// One 16-byte vector of a row at column c: whole when it lies inside the
-// row, element by element (zero outside) at the row's end.
-template <class Ty>
-__device__ __forceinline__ uint4 row_load(const typename Ty::T *row, int64_t c, int64_t n) {
-    if (c + Ty::VW <= n) return __ldcs(reinterpret_cast<const uint4 *>(row + c));
-    uint4 v = make_uint4(0, 0, 0, 0);
-    typename Ty::T e[Ty::VW];
-#pragma unroll
-    for (int i = 0; i < Ty::VW; ++i) e[i] = c + i < n ? row[c + i] : (typename Ty::T)0;
-    if constexpr (sizeof(typename Ty::T) == 4) {
-        v = make_uint4(__float_as_uint(e[0]), __float_as_uint(e[1]), __float_as_uint(e[2]),
-                       __float_as_uint(e[3]));
-    } else {
-        v = make_uint4((uint32_t)e[0] | ((uint32_t)e[1] << 16), (uint32_t)e[2] | ((uint32_t)e[3] << 16),
-                       (uint32_t)e[4] | ((uint32_t)e[5] << 16), (uint32_t)e[6] | ((uint32_t)e[7] << 16));
-    }
-    return v;
-}
 
 template <class Ty>
 __device__ __forceinline__ void row_unpack(const uint4 &v, float *y) {
