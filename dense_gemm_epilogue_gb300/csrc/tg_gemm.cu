@@ -908,7 +908,7 @@ tg_status scratch(const Device &dev, cudaStream_t stream, int64_t tiles, Scratch
 }
 
 bool encode_rows(CUtensorMap *map, tg_out_dtype t, const void *base, int64_t rows, int64_t cols,
-                 int64_t ld, int box_rows) {
+                 int64_t ld, int box_rows, int row_bytes) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
     const int e = t == TG_OUT_F32 ? 4 : 2;
@@ -917,10 +917,11 @@ bool encode_rows(CUtensorMap *map, tg_out_dtype t, const void *base, int64_t row
                                                       : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
     cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
     cuuint64_t strides[1] = {(cuuint64_t)(ld * e)};
-    cuuint32_t box[2] = {(cuuint32_t)(128 / e), (cuuint32_t)box_rows};
+    cuuint32_t box[2] = {(cuuint32_t)(row_bytes / e), (cuuint32_t)box_rows};
     cuuint32_t estr[2] = {1, 1};
     return fn(map, dt, 2, const_cast<void *>(base), dims, strides, box, estr,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_INTERLEAVE_NONE,
+              row_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }

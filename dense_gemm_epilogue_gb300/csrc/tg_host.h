@@ -35,9 +35,9 @@ constexpr int64_t kStreamFlags = 8 * 512;
 tg_status scratch(const Device &dev, cudaStream_t stream, int64_t tiles, Scratch *out);
 
 // 2-D tensor map of a row-major matrix of 2- or 4-byte elements: box of
-// 128 bytes (64 or 32 elements) x box_rows, 128-byte swizzle, zero fill.
+// row_bytes (128 or 64, with the swizzle of that width) x box_rows, zero fill.
 bool encode_rows(CUtensorMap *map, tg_out_dtype t, const void *base, int64_t rows, int64_t cols,
-                 int64_t ld, int box_rows);
+                 int64_t ld, int box_rows, int row_bytes = 128);
 
 // out0[c] (and out1[c] when given) = sum over `parts` rows of the partials.
 cudaError_t colsum_finish(const float *partial0, const float *partial1, int32_t parts, int64_t n,

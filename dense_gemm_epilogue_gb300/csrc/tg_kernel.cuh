@@ -136,6 +136,7 @@ enum WaitSite : uint32_t {
     SITE_SELFTEST = 7,
     SITE_SCHED = 10,
     SITE_PARTIAL = 8,
+    SITE_RESIDUAL = 11,
 };
 
 // Composed pointwise epilogue: after y = alpha * acc (and the ReLU flag),

@@ -28,16 +28,19 @@
 //   entries   A second problem of the same shape in the same launch (dWg and
 //             dWu share X): tiles from tiles_per_batch on use the second A map
 //             and the second output.
-//   epilogue  A thread holds one row's consecutive columns.  Its warp turns 32
-//             rows x 128 bytes round in shared memory (swizzled, 4 KB) and
-//             stores four whole 128-byte lines per instruction, fire and forget.
-//             4096 x 4096 x 64, all epilogue: 17.0 us, against 18.7 us with
-//             64-byte pieces and 16.3 us with TMA stores of such boxes, whose
-//             proxy fences and buffer waits made K = 2048 and small products
-//             slower; the chip takes about 5 TB/s of stores, 7 us of it.  The
-//             residual comes in the same way, one box ahead.  Outputs or
-//             residuals whose rows are not 16-byte aligned go through the same
-//             buffer with 2-byte accesses, a row per instruction.
+//   epilogue  A thread holds one row's consecutive columns.  Its warp stages 32
+//             rows x 64 bytes in shared memory (swizzled, two 2 KB buffers, so
+//             that one is filled while the other drains) and stores them by TMA,
+//             which clips at the rows' and columns' end.  The residual comes in
+//             through the same buffers by TMA, the first box before the
+//             accumulator is ready and each next one while the last is in work.
+//             Against plain 16-byte stores from a single staged box: 2048 x 4096 x
+//             1024 with GELU and residual 24.6 us, 26.6; gated 333 x 5640 x 2048
+//             18.4, 19.4; 1111 x 8200 x 2056 with GELU and saved Z 47.8, 50.0;
+//             without an activation no difference.  Rows that are not 16-byte
+//             aligned, and boxes that end inside 16 bytes (there a TMA store
+//             wrote into the row's padding), go through the same buffers with
+//             4-byte stores.
 //
 // Bound: tensor throughput for token counts above about 300 (arithmetic
 // intensity 256 x 256 / (256 + 256) = 128 FLOP per byte of L2 traffic).
@@ -131,6 +134,27 @@ __device__ __forceinline__ uint32_t mlp_pack2(float lo, float hi) {
     }
 }
 
+// TMA store of a swizzled shared-memory box; bounds are the map's.
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, uint32_t src, int32_t c0,
+                                             int32_t c1) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(src), "r"(c0), "r"(c1)
+                 : "memory");
+}
+__device__ __forceinline__ void bulk_commit() {
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+// All but the issuing thread's last LEFT stores have read their shared memory;
+// all its stores are complete.
+template <int LEFT>
+__device__ __forceinline__ void bulk_wait_read() {
+    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(LEFT) : "memory");
+}
+__device__ __forceinline__ void bulk_wait_all() {
+    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
+
 // Descriptor of an MN-major operand tile: 64-element rows of 128 bytes along
 // the role-space rows, one per reduction index, 128-byte swizzle.  Leading
 // byte offset: the next 64 role-space rows (one 64 x 64 box, 8 KB); stride
@@ -153,12 +177,12 @@ enum class MlpEpi : int { LINEAR = 0, GATED = 1, PLAIN = 2 };
 struct MlpOut {
     void *ptr;       // row-major output (NULL: not wanted)
     int64_t ld;      // elements between rows
-    int32_t vec;     // 1: rows are 16-byte aligned
+    int32_t tma;     // 1: stored by TMA through its map
     int32_t pad_;
 };
 
 struct MlpMaps {
-    CUtensorMap a[2], b[2];
+    CUtensorMap a[2], b[2], out[3], r;
 };
 
 struct MlpParams {
@@ -168,8 +192,9 @@ struct MlpParams {
     const float *bias;        // n values or NULL
     const void *r;            // residual (m x n) or NULL
     int64_t ldr;
-    int32_t r_vec;            // 1: the residual's rows are 16-byte aligned
+    int32_t r_tma;            // 1: loaded by TMA through its map
     int32_t out_f32;          // PLAIN: outputs are FP32 (else the operands' type)
+    int32_t clip;             // 1: a row's bytes are a multiple of 16, so TMA may clip a box there
     // 1: this product reads nothing that the kernel before it writes (a weight
     // gradient after the input gradient), so it starts without waiting for that
     // kernel and waits at its end, for whatever comes next on the stream.  That
@@ -193,22 +218,21 @@ struct MlpConfig {
     static constexpr int B_BYTES = B_ROWS * ROW_BYTES;
     static constexpr int EPI_WARPS = 8;
     static constexpr int COLS = OUT_N / 2;            // output columns of an epilogue warp
-    // A staged row: 128 bytes (64 16-bit columns), or the 64 bytes of the 32
-    // columns that a warp has in the gated 128-column tile.
-    static constexpr int STG_ROW = COLS * 2 < ROW_BYTES ? COLS * 2 : ROW_BYTES;
-    static constexpr int STG_BYTES = 32 * STG_ROW;    // a warp's staging buffer
-    static constexpr int FIT = (SMEM_LIMIT - 3072 - EPI_WARPS * STG_BYTES) / (A_BYTES + B_BYTES);
+    static constexpr int STG_ROW = 64;                // a staged row: 32 16-bit columns
+    static constexpr int STG_BYTES = 32 * STG_ROW;    // one staging buffer, two per warp
+    static constexpr int FIT = (SMEM_LIMIT - 3072 - 2 * EPI_WARPS * STG_BYTES) / (A_BYTES + B_BYTES);
     static constexpr int STAGES = FIT > 8 ? 8 : FIT;
     static constexpr int A_OFF = 0;
     static constexpr int B_OFF = STAGES * A_BYTES;
     static constexpr int STG_OFF = B_OFF + STAGES * B_BYTES;
-    static constexpr int BIAS_OFF = STG_OFF + EPI_WARPS * STG_BYTES;
+    static constexpr int BIAS_OFF = STG_OFF + 2 * EPI_WARPS * STG_BYTES;
     static constexpr int BAR_OFF = BIAS_OFF + EPI_WARPS * 128;  // 32 floats per warp
     static constexpr int FULL0 = 0, EMPTY0 = STAGES;
     static constexpr int ACCF0 = 2 * STAGES, ACCE0 = ACCF0 + 2, DRAIN = ACCE0 + 2;
     static constexpr int SLOTS = 4;
     static constexpr int TKF0 = DRAIN + 1, TKE0 = TKF0 + SLOTS;
-    static constexpr int NUM_BARS = TKE0 + SLOTS;
+    static constexpr int RES0 = TKE0 + SLOTS;  // two per epilogue warp: residual box landed
+    static constexpr int NUM_BARS = RES0 + 2 * EPI_WARPS;
     static constexpr int MISC_OFF = BAR_OFF + NUM_BARS * 8;
     static constexpr int TK_OFF = (MISC_OFF + 16 + 15) / 16 * 16;
     static constexpr int TICKET_OFF = TK_OFF + 16 * SLOTS;
@@ -227,128 +251,67 @@ struct MlpConfig {
     static_assert(BN == 128 || BN == 256, "tile N");
 };
 
-// Byte `b` of row `r` of a staging buffer with rows of ROW bytes (128 or 64),
-// whose 16-byte pieces are permuted so that neither one piece of eight rows nor
-// whole rows meet a bank twice.
-template <int ROW>
+// Byte `b` of row `r` of a staging buffer: 64-byte rows with TMA's 64-byte
+// swizzle (the 16-byte piece's index xor row bits 1-2).
 __device__ __forceinline__ int stg_offset(int r, int b) {
-    const int x = ROW == 128 ? (r & 7) : ((r >> 1) & 3);
-    return r * ROW + ((((b >> 4) ^ x) << 4) | (b & 15));
+    return r * 64 + ((((b >> 4) ^ ((r >> 1) & 3)) << 4) | (b & 15));
 }
 
-// The 16-bit values of a staged box (32 rows of ROW bytes) to output rows that
-// are not 16-byte aligned: a row per step, neighbouring lanes on neighbouring
-// four-byte words from the row's first 4-byte boundary on (element 0 or 1), and
-// single elements where one is left over; eight rows' reads before their
-// stores.  Out of line, so that the aligned path keeps its registers.
-template <int ROW>
-__device__ __noinline__ void stg_to_global_odd(const uint8_t *stg, uint16_t *dst, int64_t ld,
-                                               int32_t rows_left, int32_t cols_left, int lane) {
-    const int left = cols_left < ROW / 2 ? cols_left : ROW / 2;
+// A staged box (32 rows x 64 bytes) of 16-bit values to output rows that TMA
+// does not store: two rows per step, half a warp each, neighbouring lanes on
+// neighbouring four-byte words from the row's first 4-byte boundary on (element
+// 0 or 1), and single elements where one is left over; eight steps' reads before
+// their stores.  Out of line, so that the usual path keeps its registers.
+static __device__ __noinline__ void stg_to_global_odd(const uint8_t *stg, uint16_t *dst, int64_t ld,
+                                                      int32_t rows_left, int32_t cols_left, int lane) {
+    const int left = cols_left < 32 ? cols_left : 32;
     const int even = (int)((uintptr_t)dst >> 1), step = (int)(ld & 1);
+    const int r0 = lane >> 4, l = lane & 15;
 #pragma unroll 1
-    for (int g = 0; g < 32 && g < rows_left; g += 8) {
+    for (int g = 0; g < 32 && g < rows_left; g += 16) {
         uint32_t w[8], first[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const int r = g + i, c = 2 * lane + ((even + r * step) & 1);
-            const int c0 = c < ROW / 2 ? c : 0, c1 = c + 1 < ROW / 2 ? c + 1 : 0;
-            const uint32_t lo = *reinterpret_cast<const uint16_t *>(stg + stg_offset<ROW>(r, 2 * c0));
-            const uint32_t hi = *reinterpret_cast<const uint16_t *>(stg + stg_offset<ROW>(r, 2 * c1));
-            first[i] = *reinterpret_cast<const uint16_t *>(stg + stg_offset<ROW>(r, 0));
+            const int r = g + 2 * i + r0, c = 2 * l + ((even + r * step) & 1);
+            const int c1 = c + 1 < 32 ? c + 1 : 0;
+            const uint32_t lo = *reinterpret_cast<const uint16_t *>(stg + stg_offset(r, 2 * c));
+            const uint32_t hi = *reinterpret_cast<const uint16_t *>(stg + stg_offset(r, 2 * c1));
+            first[i] = *reinterpret_cast<const uint16_t *>(stg + stg_offset(r, 0));
             w[i] = lo | (hi << 16);
         }
+        uint16_t *q = dst + (int64_t)(g + r0) * ld;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int r = g + i, odd = (even + r * step) & 1, c = 2 * lane + odd;
+        for (int i = 0; i < 8; ++i, q += 2 * ld) {
+            const int r = g + 2 * i + r0, odd = (even + r * step) & 1, c = 2 * l + odd;
             if (r < rows_left) {
-                uint16_t *q = dst + (int64_t)r * ld;
                 if (c + 1 < left) *reinterpret_cast<uint32_t *>(q + c) = w[i];
                 else if (c < left) q[c] = (uint16_t)w[i];
-                if (odd && lane == 0) q[0] = (uint16_t)first[i];
+                if (odd && l == 0) q[0] = (uint16_t)first[i];
             }
         }
     }
 }
-
-// A staged box (32 rows of ROW bytes, E elements) to columns col0.. of rows
-// row0.. of an output, bounds checked.  vec: 16 bytes a lane; a piece that the
-// row's end cuts goes element by element.
-template <int ROW, typename E>
-__device__ __forceinline__ void stg_to_global(const uint8_t *stg, const MlpOut &o, int32_t row0,
-                                              int32_t col0, int32_t rows, int32_t cols, int lane) {
-    constexpr int PER = 16 / (int)sizeof(E), PIECES = ROW / 16, STEP = 32 / PIECES;
-    E *dst = static_cast<E *>(o.ptr) + (int64_t)row0 * o.ld + col0;
-    if (o.vec) {
-        const int piece = lane % PIECES, c = piece * PER;
-#pragma unroll
-        for (int i = 0; i < PIECES; ++i) {
-            const int r = i * STEP + lane / PIECES;
-            const uint4 v = *reinterpret_cast<const uint4 *>(stg + stg_offset<ROW>(r, piece * 16));
-            if (row0 + r < rows) {
-                E *q = dst + (int64_t)r * o.ld + c;
-                if (col0 + c + PER <= cols) {
-                    *reinterpret_cast<uint4 *>(q) = v;
-                } else {
-                    const E *e = reinterpret_cast<const E *>(&v);
-#pragma unroll
-                    for (int j = 0; j < PER; ++j)
-                        if (col0 + c + j < cols) q[j] = e[j];
-                }
-            }
-        }
-    } else if constexpr (sizeof(E) == 2) {
-        stg_to_global_odd<ROW>(stg, dst, o.ld, rows - row0, cols - col0, lane);
-    } else {
+// The same for FP32 values: two rows a step, half a warp each.
+static __device__ __noinline__ void stg_to_global_f32(const uint8_t *stg, float *dst, int64_t ld,
+                                                      int32_t rows_left, int32_t cols_left, int lane) {
+    const int c = lane & 15;
 #pragma unroll 4
-        for (int r = 0; r < 32; ++r) {
-            if (row0 + r >= rows) break;
-            if (lane < ROW / 4 && col0 + lane < cols)
-                dst[(int64_t)r * o.ld + lane] = *reinterpret_cast<const E *>(stg + stg_offset<ROW>(r, lane * 4));
-        }
-    }
+    for (int r = lane >> 4; r < 32; r += 2)
+        if (r < rows_left && c < cols_left)
+            dst[(int64_t)r * ld + c] = *reinterpret_cast<const float *>(stg + stg_offset(r, c * 4));
 }
 
-// The residual's box (32 rows x 64 16-bit columns), zero outside: loaded into
-// registers in the staged order (vec) and put into the buffer when its turn
-// comes; or straight into the buffer.
-__device__ __forceinline__ void residual_load(uint4 (&v)[8], const uint16_t *src, int64_t ld,
-                                              int32_t row0, int32_t col0, int32_t rows, int32_t cols,
-                                              int lane) {
-    const int c = (lane & 7) * 8;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int r = i * 4 + (lane >> 3);
-        v[i] = make_uint4(0, 0, 0, 0);
-        if (row0 + r < rows && col0 + c < cols) {
-            const uint16_t *q = src + (int64_t)(row0 + r) * ld + col0 + c;
-            if (col0 + c + 8 <= cols) {
-                v[i] = *reinterpret_cast<const uint4 *>(q);
-            } else {
-                uint32_t w[4] = {0, 0, 0, 0};
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (col0 + c + j < cols) w[j / 2] |= (uint32_t)q[j] << (16 * (j & 1));
-                v[i] = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-        }
-    }
-}
-__device__ __forceinline__ void residual_put(const uint4 (&v)[8], uint8_t *stg, int lane) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        *reinterpret_cast<uint4 *>(stg + stg_offset<128>(i * 4 + (lane >> 3), (lane & 7) * 16)) = v[i];
-}
+// The residual's box (32 rows x 32 values), zero outside, from rows that TMA
+// cannot address.
 __device__ __forceinline__ void residual_to_stg(uint8_t *stg, const uint16_t *src, int64_t ld,
                                                 int32_t row0, int32_t col0, int32_t rows,
                                                 int32_t cols, int lane) {
-    for (int r = 0; r < 32; ++r)
-#pragma unroll
-        for (int c = lane; c < 64; c += 32) {
-            const bool in = row0 + r < rows && col0 + c < cols;
-            *reinterpret_cast<uint16_t *>(stg + stg_offset<128>(r, c * 2)) =
-                in ? src[(int64_t)(row0 + r) * ld + col0 + c] : (uint16_t)0;
-        }
+#pragma unroll 8
+    for (int r = 0; r < 32; ++r) {
+        const bool in = row0 + r < rows && col0 + lane < cols;
+        *reinterpret_cast<uint16_t *>(stg + stg_offset(r, lane * 2)) =
+            in ? src[(int64_t)(row0 + r) * ld + col0 + lane] : (uint16_t)0;
+    }
 }
 
 template <Kind KD, int CG, int BN, int AM, int BM, MlpEpi EP>
@@ -392,12 +355,14 @@ __global__ void __launch_bounds__(MlpConfig<KD, CG, BN, AM, BM, EP>::NUM_THREADS
             mbar_init(bar(C::TKF0 + c), 1);
             mbar_init(bar(C::TKE0 + c), C::READERS);
         }
+        for (int w = 0; w < 2 * C::EPI_WARPS; ++w) mbar_init(bar(C::RES0 + w), 1);
         *abort_flag = 0;
         fence_mbar_init();
         if (nkb > 0) {
             prefetch_tensormap(&maps.a[0]);
             prefetch_tensormap(&maps.b[0]);
         }
+        if (mp.out[0].tma) prefetch_tensormap(&maps.out[0]);
     }
     if (warp == 1) {
         if constexpr (CG == 2) {
@@ -603,9 +568,11 @@ __global__ void __launch_bounds__(MlpConfig<KD, CG, BN, AM, BM, EP>::NUM_THREADS
         const int etid = threadIdx.x - 64;
         constexpr int COLS = C::COLS;
         const int cbase = (ew / 4) * COLS;
-        uint8_t *const stg = smem + C::STG_OFF + ew * C::STG_BYTES;
+        // Two staging buffers, used in turn: `cur` is the next one to fill.
+        uint8_t *const stg0 = smem + C::STG_OFF + ew * 2 * C::STG_BYTES;
         float4 *const bias_s = reinterpret_cast<float4 *>(smem + C::BIAS_OFF + ew * 128);
-        const uint16_t *const res = static_cast<const uint16_t *>(mp.r);
+        uint32_t cur = 0;
+        uint32_t res_phase = 0;  // one bit per buffer
         uint32_t tl = 0;
         int64_t step = 0;
         bool alive = true;
@@ -625,18 +592,34 @@ __global__ void __launch_bounds__(MlpConfig<KD, CG, BN, AM, BM, EP>::NUM_THREADS
             const bool writer = un.seg >= 0 && un.seg < up.segs - 1;
             const bool finisher = un.seg >= 0 && !writer;
 
-            // The first residual box, while the MMAs still run.
-            uint4 rv[8];
+            // Ask for the residual box at column `col` into buffer `at`, whose
+            // last store, if any, must have left it (wait: all stores so far).
+            auto ask_residual = [&](int32_t col, uint32_t at) {
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    bulk_wait_read<0>();
+                    const uint32_t b = bar(C::RES0 + 2 * ew + at);
+                    mbar_arrive_expect_tx(b, C::STG_BYTES);
+                    tma_load_2d(smem_u32(stg0 + at * C::STG_BYTES), &maps.r, b, col, row0);
+                }
+            };
+            bool asked = false;
             if constexpr (EP == MlpEpi::LINEAR) {
-                if (res && mp.r_vec && !writer)
-                    residual_load(rv, res, mp.ldr, row0, colw, p.m, p.n, lane);
+                if (mp.r && mp.r_tma && !mp.out[1].ptr && !writer && row0 < p.m && colw < p.n) {
+                    ask_residual(colw, cur);
+                    asked = true;
+                }
             }
 
             const bool got = pair_wait(bar(C::ACCF0 + acc), use & 1, ctl, SITE_ACC_FULL);
             if (up.segs > 1 ? named_bar_any(2, EPI_THREADS, !got) : !__all_sync(0xffffffffu, got)) {
                 alive = false;
             }
-            if (!alive) break;
+            if (!alive) {
+                if (asked) pair_pause_ns(200000);  // the box may still be landing
+                break;
+            }
             tc_fence_after();
             const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + acc * BN;
             auto part = [&](int32_t k) -> float * {
@@ -715,139 +698,171 @@ __global__ void __launch_bounds__(MlpConfig<KD, CG, BN, AM, BM, EP>::NUM_THREADS
                     }
                 };
                 auto stg16 = [&](int piece) -> uint4 * {
-                    return reinterpret_cast<uint4 *>(stg + stg_offset<C::STG_ROW>(lane, piece * 16));
+                    return reinterpret_cast<uint4 *>(stg0 + cur * C::STG_BYTES +
+                                                     stg_offset(lane, piece * 16));
                 };
-                // 32 values of this thread's row as half h of its staged row.
-                auto put = [&](int h, const float (&y)[32]) {
+                // Buffer `cur` may be written: its store, the one before the
+                // last, has left it.
+                auto free_stg = [&]() {
+                    if (lane == 0) bulk_wait_read<1>();
+                    __syncwarp();
+                };
+                // Buffer `cur` goes out as columns col.. of output o.
+                auto send = [&](int o, int32_t col) {
+                    const bool f32 = EP == MlpEpi::PLAIN && mp.out_f32;
+                    uint8_t *stg = stg0 + cur * C::STG_BYTES;
+                    if (mp.out[o].tma && (mp.clip || col + (f32 ? 16 : 32) <= p.n)) {
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) tma_store_2d(&maps.out[o], smem_u32(stg), col, row0);
+                    } else {
+                        __syncwarp();
+                        if (f32)
+                            stg_to_global_f32(stg, static_cast<float *>(mp.out[o].ptr) +
+                                                       (int64_t)row0 * mp.out[o].ld + col,
+                                              mp.out[o].ld, p.m - row0, p.n - col, lane);
+                        else
+                            stg_to_global_odd(stg, static_cast<uint16_t *>(mp.out[o].ptr) +
+                                                       (int64_t)row0 * mp.out[o].ld + col,
+                                              mp.out[o].ld, p.m - row0, p.n - col, lane);
+                        __syncwarp();
+                    }
+                    if (lane == 0) bulk_commit();  // one group per buffer filled
+                    cur ^= 1;
+                };
+                // 32 values as a 16-bit staged row.
+                auto put = [&](const float (&y)[32]) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        *stg16(4 * h + j) = make_uint4(mlp_pack2<KD>(y[8 * j], y[8 * j + 1]),
-                                                       mlp_pack2<KD>(y[8 * j + 2], y[8 * j + 3]),
-                                                       mlp_pack2<KD>(y[8 * j + 4], y[8 * j + 5]),
-                                                       mlp_pack2<KD>(y[8 * j + 6], y[8 * j + 7]));
-                };
-                // The buffer goes out as columns col.. of output o, and is free.
-                auto send = [&](int o, int32_t col) {
-                    __syncwarp();
-                    stg_to_global<C::STG_ROW, uint16_t>(stg, mp.out[o], row0, col, p.m, p.n, lane);
-                    __syncwarp();
+                        *stg16(j) = make_uint4(mlp_pack2<KD>(y[8 * j], y[8 * j + 1]),
+                                               mlp_pack2<KD>(y[8 * j + 2], y[8 * j + 3]),
+                                               mlp_pack2<KD>(y[8 * j + 4], y[8 * j + 5]),
+                                               mlp_pack2<KD>(y[8 * j + 6], y[8 * j + 7]));
                 };
                 const bool rows_in = ready && row0 < p.m;
-                constexpr int CW = C::STG_ROW / 2, HALVES = CW / 32;  // columns per staged box
+                if constexpr (EP == MlpEpi::LINEAR) {
 #pragma unroll 1
-                for (int c = 0; c < COLS && rows_in && colw + c < p.n; c += CW) {
-                    const int32_t col = colw + c;
-                    if constexpr (EP == MlpEpi::LINEAR) {
-                        auto pre = [&](int h, float (&y)[32]) {  // accumulator plus bias
-                            if (mp.bias) {
-                                __syncwarp();
-                                const int32_t cb = col + 32 * h + lane;
-                                reinterpret_cast<float *>(bias_s)[lane] =
-                                    cb < p.n ? __ldg(mp.bias + cb) : 0.0f;
-                                __syncwarp();
-                            }
-                            load_acc(cbase + c + 32 * h, y);
-                            if (mp.bias) {
+                    for (int c = 0; c < COLS && rows_in && colw + c < p.n; c += 32) {
+                        const int32_t col = colw + c;
+                        float y[32];
+                        if (mp.bias) {
+                            __syncwarp();
+                            reinterpret_cast<float *>(bias_s)[lane] =
+                                col + lane < p.n ? __ldg(mp.bias + col + lane) : 0.0f;
+                            __syncwarp();
+                        }
+                        load_acc(cbase + c, y);
+                        if (mp.bias) {
 #pragma unroll
-                                for (int j = 0; j < 8; ++j) {
-                                    const float4 b = bias_s[j];
-                                    y[4 * j] += b.x;
-                                    y[4 * j + 1] += b.y;
-                                    y[4 * j + 2] += b.z;
-                                    y[4 * j + 3] += b.w;
-                                }
+                            for (int j = 0; j < 8; ++j) {
+                                const float4 b = bias_s[j];
+                                y[4 * j] += b.x;
+                                y[4 * j + 1] += b.y;
+                                y[4 * j + 2] += b.z;
+                                y[4 * j + 3] += b.w;
                             }
-                        };
+                        }
                         if (mp.out[1].ptr) {
-#pragma unroll 1
-                            for (int h = 0; h < HALVES; ++h) {
-                                float y[32];
-                                pre(h, y);
-                                put(h, y);
-                            }
+                            free_stg();
+                            put(y);
                             send(1, col);
                         }
-                        if (res) {
-                            if (mp.r_vec) {
-                                residual_put(rv, stg, lane);
-                                if (c + CW < COLS)
-                                    residual_load(rv, res, mp.ldr, row0, col + CW, p.m, p.n, lane);
-                            } else {
-                                residual_to_stg(stg, res, mp.ldr, row0, col, p.m, p.n, lane);
-                            }
-                            __syncwarp();
+                        const bool r_tma = mp.r && mp.r_tma;
+                        if (r_tma) {
+                            // With Z both buffers turn over every 32 columns, so
+                            // the box is asked for here; else it was asked for one
+                            // step ago, and the next one goes out now.
+                            if (!asked) ask_residual(col, cur);
+                            asked = !mp.out[1].ptr && c + 32 < COLS && col + 32 < p.n;
+                            if (asked) ask_residual(col + 32, cur ^ 1);
                         }
-#pragma unroll 1
-                        for (int h = 0; h < HALVES; ++h) {
-                            float y[32];
-                            pre(h, y);
-                            mlp_with_act(mp.act, [&](auto a) {
+                        mlp_with_act(mp.act, [&](auto a) {
 #pragma unroll
-                                for (int j = 0; j < 32; ++j) y[j] = mlp_act<a.value>(y[j]);
-                            });
-                            if (res) {
+                            for (int j = 0; j < 32; ++j) y[j] = mlp_act<a.value>(y[j]);
+                        });
+                        if (r_tma) {
+                            const bool landed = pair_wait(bar(C::RES0 + 2 * ew + cur),
+                                                          (res_phase >> cur) & 1, ctl, SITE_RESIDUAL);
+                            res_phase ^= 1u << cur;
+                            if (!__all_sync(0xffffffffu, landed)) {
+                                pair_pause_ns(200000);
+                                asked = false;
+                                alive = false;
+                                break;
+                            }
+                        } else {
+                            free_stg();
+                            if (mp.r) {
+                                residual_to_stg(stg0 + cur * C::STG_BYTES,
+                                                static_cast<const uint16_t *>(mp.r), mp.ldr, row0, col,
+                                              p.m, p.n, lane);
+                                __syncwarp();
+                            }
+                        }
+                        if (mp.r) {
 #pragma unroll
-                                for (int j = 0; j < 4; ++j) {
-                                    const uint4 w = *stg16(4 * h + j);
-                                    const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+                            for (int j = 0; j < 4; ++j) {
+                                const uint4 w = *stg16(j);
+                                const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-                                    for (int e = 0; e < 4; ++e) {
-                                        y[8 * j + 2 * e] += mlp_to_float<KD>(ws[e] & 0xffffu);
-                                        y[8 * j + 2 * e + 1] += mlp_to_float<KD>(ws[e] >> 16);
-                                    }
+                                for (int e = 0; e < 4; ++e) {
+                                    y[8 * j + 2 * e] += mlp_to_float<KD>(ws[e] & 0xffffu);
+                                    y[8 * j + 2 * e + 1] += mlp_to_float<KD>(ws[e] >> 16);
                                 }
                             }
-                            put(h, y);  // over the residual this thread has just read
                         }
+                        put(y);
                         send(0, col);
-                    } else if constexpr (EP == MlpEpi::GATED) {
-                        constexpr int UP = BN / 2;  // accumulator column of the up half
+                    }
+                } else if constexpr (EP == MlpEpi::GATED) {
+                    constexpr int UP = BN / 2;  // accumulator column of the up half
 #pragma unroll 1
-                        for (int o = 1; o < 3; ++o) {
-                            if (!mp.out[o].ptr) continue;
+                    for (int c = 0; c < COLS && rows_in && colw + c < p.n; c += 32) {
+                        const int32_t col = colw + c;
+                        float y[32], w[32];
+                        load_acc(cbase + c, y);
+                        load_acc(UP + cbase + c, w);
+                        if (mp.out[1].ptr) {
+                            free_stg();
+                            put(y);
+                            send(1, col);
+                        }
+                        if (mp.out[2].ptr) {
+                            free_stg();
+                            put(w);
+                            send(2, col);
+                        }
+                        mlp_with_act(mp.act, [&](auto a) {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) y[j] = mlp_act<a.value>(y[j]) * w[j];
+                        });
+                        free_stg();
+                        put(y);
+                        send(0, col);
+                    }
+                } else {
 #pragma unroll 1
-                            for (int h = 0; h < HALVES; ++h) {
-                                float y[32];
-                                load_acc((o - 1) * UP + cbase + c + 32 * h, y);
-                                put(h, y);
+                    for (int c = 0; c < COLS && rows_in && colw + c < p.n; c += 32) {
+                        float y[32];
+                        load_acc(cbase + c, y);
+                        if (mp.out_f32) {
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                if (colw + c + 16 * h >= p.n) break;
+                                free_stg();
+#pragma unroll
+                                for (int j = 0; j < 4; ++j)
+                                    *stg16(j) = make_uint4(__float_as_uint(y[16 * h + 4 * j]),
+                                                           __float_as_uint(y[16 * h + 4 * j + 1]),
+                                                           __float_as_uint(y[16 * h + 4 * j + 2]),
+                                                           __float_as_uint(y[16 * h + 4 * j + 3]));
+                                send(bt, colw + c + 16 * h);
                             }
-                            send(o, col);
+                        } else {
+                            free_stg();
+                            put(y);
+                            send(bt, colw + c);
                         }
-#pragma unroll 1
-                        for (int h = 0; h < HALVES; ++h) {
-                            float y[32], w[32];
-                            load_acc(cbase + c + 32 * h, y);
-                            load_acc(UP + cbase + c + 32 * h, w);
-                            mlp_with_act(mp.act, [&](auto a) {
-#pragma unroll
-                                for (int j = 0; j < 32; ++j) y[j] = mlp_act<a.value>(y[j]) * w[j];
-                            });
-                            put(h, y);
-                        }
-                        send(0, col);
-                    } else if (mp.out_f32) {
-#pragma unroll 1
-                        for (int h = 0; h < HALVES; ++h) {
-                            float y[32];
-                            load_acc(cbase + c + 32 * h, y);
-#pragma unroll
-                            for (int j = 0; j < 8; ++j)
-                                *stg16(j) = make_uint4(
-                                    __float_as_uint(y[4 * j]), __float_as_uint(y[4 * j + 1]),
-                                    __float_as_uint(y[4 * j + 2]), __float_as_uint(y[4 * j + 3]));
-                            __syncwarp();
-                            stg_to_global<C::STG_ROW, float>(stg, mp.out[bt], row0, col + 32 * h, p.m,
-                                                             p.n, lane);
-                            __syncwarp();
-                        }
-                    } else {
-#pragma unroll 1
-                        for (int h = 0; h < HALVES; ++h) {
-                            float y[32];
-                            load_acc(cbase + c + 32 * h, y);
-                            put(h, y);
-                        }
-                        send(bt, col);
                     }
                 }
                 if (finisher) {
@@ -856,6 +871,7 @@ __global__ void __launch_bounds__(MlpConfig<KD, CG, BN, AM, BM, EP>::NUM_THREADS
                         for (int32_t k = 0; k < up.segs - 1; ++k) *flag(k) = 0u;
                 }
             }
+            if (asked) pair_pause_ns(200000);  // an unread box (the finisher gave up): let it land
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
@@ -864,6 +880,7 @@ __global__ void __launch_bounds__(MlpConfig<KD, CG, BN, AM, BM, EP>::NUM_THREADS
             }
             u = tick ? tk_read_warp(step++) : u + num_pairs;
         }
+        if (lane == 0) bulk_wait_all();
     }
 
     if (mp.late_wait) griddep_wait();

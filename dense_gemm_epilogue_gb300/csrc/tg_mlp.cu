@@ -464,11 +464,15 @@ tg_status run_product(const Product &q, tg_dtype t, const Device &dev, cudaStrea
     for (int i = 0; i < 3; ++i) {
         p.out[i].ptr = const_cast<void *>(q.out[i].p);
         p.out[i].ld = q.out[i].ld;
-        p.out[i].vec = q.out[i].p && aligned16(q.out[i]);
+        p.out[i].tma = q.out[i].p && aligned16(q.out[i]) &&
+                       host::encode_rows(&la.maps.out[i], q.out_f32 ? TG_OUT_F32 : ot, q.out[i].p,
+                                         q.out[i].rows, q.out[i].cols, q.out[i].ld, 32, 64);
     }
+    p.clip = (q.n * (q.out_f32 ? 4 : 2)) % 16 == 0;
     p.r = q.r.p;
     p.ldr = q.r.ld;
-    p.r_vec = q.r.p && aligned16(q.r);
+    p.r_tma = q.r.p && aligned16(q.r) &&
+              host::encode_rows(&la.maps.r, ot, q.r.p, q.r.rows, q.r.cols, q.r.ld, 32, 64);
     p.bias = q.bias;
     p.act = q.act;
     p.out_f32 = q.out_f32;
