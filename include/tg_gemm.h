@@ -531,7 +531,8 @@ const char *tg_status_string(tg_status status);
  * out since the last check, TG_ERR_DEVICE_TIMEOUT if one did (then *where, if
  * not NULL, receives a code naming the wait: 1 stage-full, 2 stage-empty,
  * 3 accumulator-full, 4 accumulator-empty, 5 converted-stage, 6 drain,
- * 7 self-test), TG_ERR_CUDA on a CUDA error.
+ * 7 self-test, 8 partial sums, 10 unit claim, 11 residual box), TG_ERR_CUDA on a
+ * CUDA error.
  */
 tg_status tg_check_device_status(void *stream, int32_t *where);
 
