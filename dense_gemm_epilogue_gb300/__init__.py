@@ -17,6 +17,7 @@ import importlib.machinery
 import importlib.util
 import os
 import threading
+import warnings
 
 from .build import LIB as LIBRARY_PATH
 from .build import PYCALL as _PYCALL_PATH
@@ -159,14 +160,21 @@ _CALLS = ("tg_linear_workspace_bytes", "tg_linear", "tg_gated_workspace_bytes", 
 
 
 def _load_calls(lib):
-    """The marshalling module bound to this library's entry points, or None."""
+    """The marshalling module bound to this library's entry points, or None.
+    It only saves time: one that does not load, or does not take these entry
+    points, is named in a warning and the ctypes wrappers serve."""
     if not os.path.exists(_PYCALL_PATH):
         return None
-    loader = importlib.machinery.ExtensionFileLoader("_tgcall", _PYCALL_PATH)
-    spec = importlib.util.spec_from_loader("_tgcall", loader)
-    mod = importlib.util.module_from_spec(spec)
-    loader.exec_module(mod)
-    mod.bind({n: ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in _CALLS})
+    try:
+        loader = importlib.machinery.ExtensionFileLoader("_tgcall", _PYCALL_PATH)
+        spec = importlib.util.spec_from_loader("_tgcall", loader)
+        mod = importlib.util.module_from_spec(spec)
+        loader.exec_module(mod)
+        mod.bind({n: ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in _CALLS})
+    except (ImportError, SystemError, AttributeError, KeyError, ValueError) as e:
+        warnings.warn(f"{_PYCALL_PATH} is left out, calls go through ctypes: {e}", RuntimeWarning,
+                      stacklevel=3)
+        return None
     return mod
 
 

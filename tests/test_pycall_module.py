@@ -1,0 +1,61 @@
+"""The marshalling module (csrc/tg_pycall.c) is an optional speed-up: whatever
+is wrong with it, the library builds, loads and answers through ctypes.  No
+GPU."""
+
+from __future__ import annotations
+
+import warnings
+
+import pytest
+
+
+@pytest.fixture(scope="module")
+def tg():
+    import dense_gemm_epilogue_gb300 as tg
+
+    tg.build()
+    tg.load()
+    return tg
+
+
+@pytest.fixture
+def unloaded(tg, monkeypatch):
+    """The package as before its first load()."""
+    monkeypatch.setattr(tg, "_lib", None)
+    monkeypatch.setattr(tg, "_call", None)
+    return tg
+
+
+def answers(tg):
+    assert tg.tg_version() == 100
+    assert tg.tg_linear_workspace_bytes(64, 96, 128, 1 << 20, 128, 1 << 20, 128, "bf16") == 0
+    assert tg.tg_layer_norm(0, 100, None, 100, None, None, 1e-5, None, 100, None, None, "f32") == tg.TG_OK
+
+
+def test_a_module_that_does_not_load_is_left_out(unloaded, monkeypatch, tmp_path):
+    bad = tmp_path / "_tgcall.so"
+    bad.write_bytes(b"not a shared object")
+    monkeypatch.setattr(unloaded, "_PYCALL_PATH", str(bad))
+    with pytest.warns(RuntimeWarning, match="ctypes"):
+        unloaded.load()
+    assert unloaded._call is None
+    answers(unloaded)
+
+
+def test_a_module_of_other_entry_points_is_left_out(unloaded, monkeypatch):
+    if not unloaded.os.path.exists(unloaded._PYCALL_PATH):
+        pytest.skip("built without Python's headers")
+    monkeypatch.setattr(unloaded, "_CALLS", ("tg_linear",))
+    with pytest.warns(RuntimeWarning, match="ctypes"):
+        unloaded.load()
+    assert unloaded._call is None
+    answers(unloaded)
+
+
+def test_a_missing_module_is_no_error(unloaded, monkeypatch, tmp_path):
+    monkeypatch.setattr(unloaded, "_PYCALL_PATH", str(tmp_path / "none.so"))
+    with warnings.catch_warnings():
+        warnings.simplefilter("error")
+        unloaded.load()
+    assert unloaded._call is None
+    answers(unloaded)
