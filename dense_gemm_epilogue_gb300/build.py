@@ -20,7 +20,9 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_lib")
 LIB = os.path.join(OUT_DIR, "libtg_gemm.so")
-PYCALL = os.path.join(OUT_DIR, "_tgcall.so")
+PYCALL_SOURCE = os.path.join(CSRC, "tg_pycall.c")
+# (an extension module belongs to one interpreter version: its name says which)
+PYCALL = os.path.join(OUT_DIR, "_tgcall" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 OBJ_DIR = os.path.join(HERE, "_build")
 SOURCES = ["tg_gemm.cu", "tg_inst_bf16.cu", "tg_inst_fp16.cu", "tg_inst_tf32.cu",
            "tg_inst_e4m3.cu", "tg_inst_e5m2.cu", "tg_inst_mx.cu", "tg_noalloc.cu", "tg_mlp.cu",
@@ -44,7 +46,7 @@ def source_hash() -> str:
     h = hashlib.sha256()
     names = sorted(os.listdir(CSRC))
     for n in names:
-        if n.endswith((".cu", ".cuh", ".h", ".c")):
+        if n.endswith((".cu", ".cuh", ".h")):
             with open(os.path.join(CSRC, n), "rb") as f:
                 h.update(n.encode() + b"\0" + f.read())
     with open(os.path.join(ROOT, "include", "tg_gemm.h"), "rb") as f:
@@ -65,31 +67,50 @@ def _compile(src: str, verbose_ptxas: bool) -> str:
     return obj
 
 
-def _compile_pycall() -> None:
-    """The host-only module that marshals the hot Python calls (needs Python's
-    headers; without them, or a C compiler, the ctypes wrappers serve alone)."""
+def _pycall_hash() -> str:
+    h = hashlib.sha256()
+    for name in (PYCALL_SOURCE, os.path.join(ROOT, "include", "tg_gemm.h")):
+        with open(name, "rb") as f:
+            h.update(f.read())
+    return h.hexdigest()[:16]
+
+
+def _build_pycall(force: bool) -> None:
+    """The host-only module that marshals the hot Python calls, with a stamp of
+    its own beside it.  Without Python's headers or a C compiler the ctypes
+    wrappers serve alone, and the next build() looks again."""
+    stamp = PYCALL + ".hash"
+    want = _pycall_hash()
+    if not force and os.path.exists(PYCALL) and os.path.exists(stamp):
+        with open(stamp) as f:
+            if f.read().strip() == want:
+                return
+    for old in (PYCALL, stamp):
+        if os.path.exists(old):
+            os.remove(old)
     include = sysconfig.get_paths()["include"]
     cc = shutil.which("gcc") or shutil.which("cc")
-    if os.path.exists(PYCALL):
-        os.remove(PYCALL)
     if cc is None or not os.path.exists(os.path.join(include, "Python.h")):
         return
+    os.makedirs(OUT_DIR, exist_ok=True)
     tmp = PYCALL + ".tmp.%d" % os.getpid()
     r = subprocess.run([cc, "-O2", "-std=c11", "-Wall", "-shared", "-fPIC", "-I", include, "-I",
-                        os.path.join(ROOT, "include"), os.path.join(CSRC, "tg_pycall.c"), "-o", tmp],
+                        os.path.join(ROOT, "include"), PYCALL_SOURCE, "-o", tmp],
                        capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"{cc} failed on tg_pycall.c:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, PYCALL)
+    with open(stamp, "w") as f:
+        f.write(want + "\n")
 
 
-def build(force: bool = False, verbose_ptxas: bool = False) -> str:
+def _build_library(force: bool, verbose_ptxas: bool) -> None:
     stamp = os.path.join(OUT_DIR, "BUILD_HASH")
     want = source_hash()
     if not force and os.path.exists(LIB) and os.path.exists(stamp):
         with open(stamp) as f:
             if f.read().strip() == want:
-                return LIB
+                return
     os.makedirs(OUT_DIR, exist_ok=True)
     os.makedirs(OBJ_DIR, exist_ok=True)
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
@@ -100,9 +121,13 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    _compile_pycall()
     with open(stamp, "w") as f:
         f.write(want + "\n")
+
+
+def build(force: bool = False, verbose_ptxas: bool = False) -> str:
+    _build_library(force, verbose_ptxas)
+    _build_pycall(force)
     return LIB
 
 

@@ -59,3 +59,44 @@ def test_a_missing_module_is_no_error(unloaded, monkeypatch, tmp_path):
         unloaded.load()
     assert unloaded._call is None
     answers(unloaded)
+
+
+@pytest.fixture
+def builder(tg, monkeypatch, tmp_path):
+    """build.py with the module's file in an empty folder and the library done."""
+    import importlib
+
+    b = importlib.import_module("dense_gemm_epilogue_gb300.build")
+    if not b.os.path.exists(b.os.path.join(b.sysconfig.get_paths()["include"], "Python.h")):
+        pytest.skip("no Python headers")
+    monkeypatch.setattr(b, "PYCALL", str(tmp_path / b.os.path.basename(b.PYCALL)))
+    return b
+
+
+def test_the_module_is_named_for_its_interpreter(builder):
+    """Another Python's build neither loads this one's module nor takes it for
+    its own."""
+    suffix = builder.sysconfig.get_config_var("EXT_SUFFIX")
+    assert len(suffix) > len(".so") and builder.PYCALL.endswith(suffix)
+
+
+def test_a_missing_module_is_built_beside_a_finished_library(builder):
+    """As after a first build without a compiler or Python's headers."""
+    assert not builder.os.path.exists(builder.PYCALL)
+    builder.build()
+    assert builder.os.path.exists(builder.PYCALL)
+    first = builder.os.stat(builder.PYCALL).st_mtime_ns
+    builder.build()
+    assert builder.os.stat(builder.PYCALL).st_mtime_ns == first
+
+
+def test_a_changed_source_rebuilds_the_module_alone(builder, monkeypatch, tmp_path):
+    builder.build()
+    first = builder.os.stat(builder.PYCALL).st_mtime_ns
+    library = builder.os.stat(builder.LIB).st_mtime_ns
+    changed = tmp_path / "tg_pycall.c"
+    changed.write_text(open(builder.PYCALL_SOURCE).read() + "/* changed */\n")
+    monkeypatch.setattr(builder, "PYCALL_SOURCE", str(changed))
+    builder.build()
+    assert builder.os.stat(builder.PYCALL).st_mtime_ns != first
+    assert builder.os.stat(builder.LIB).st_mtime_ns == library
