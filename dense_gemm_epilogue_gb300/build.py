@@ -14,6 +14,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -78,7 +79,8 @@ def _pycall_hash() -> str:
 def _build_pycall(force: bool) -> None:
     """The host-only module that marshals the hot Python calls, with a stamp of
     its own beside it.  Without Python's headers or a C compiler the ctypes
-    wrappers serve alone, and the next build() looks again."""
+    wrappers serve alone, and the next build() looks again; what the compiler
+    refuses (an old Python's headers, say) costs a warning, not the library."""
     stamp = PYCALL + ".hash"
     want = _pycall_hash()
     if not force and os.path.exists(PYCALL) and os.path.exists(stamp):
@@ -98,7 +100,9 @@ def _build_pycall(force: bool) -> None:
                         os.path.join(ROOT, "include"), PYCALL_SOURCE, "-o", tmp],
                        capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"{cc} failed on tg_pycall.c:\n{r.stdout}\n{r.stderr}")
+        warnings.warn(f"{cc} failed on tg_pycall.c, calls go through ctypes:\n{r.stdout}\n{r.stderr}",
+                      RuntimeWarning, stacklevel=3)
+        return
     os.replace(tmp, PYCALL)
     with open(stamp, "w") as f:
         f.write(want + "\n")

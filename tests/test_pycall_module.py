@@ -100,3 +100,13 @@ def test_a_changed_source_rebuilds_the_module_alone(builder, monkeypatch, tmp_pa
     builder.build()
     assert builder.os.stat(builder.PYCALL).st_mtime_ns != first
     assert builder.os.stat(builder.LIB).st_mtime_ns == library
+
+
+def test_a_source_that_does_not_compile_leaves_the_library(builder, monkeypatch, tmp_path):
+    bad = tmp_path / "tg_pycall.c"
+    bad.write_text("#error not with these headers\n")
+    monkeypatch.setattr(builder, "PYCALL_SOURCE", str(bad))
+    with pytest.warns(RuntimeWarning, match="ctypes"):
+        assert builder.build() == builder.LIB
+    assert not builder.os.path.exists(builder.PYCALL)
+    assert builder.os.path.exists(builder.LIB)
