@@ -170,8 +170,9 @@ def _load_calls(lib):
         spec = importlib.util.spec_from_loader("_tgcall", loader)
         mod = importlib.util.module_from_spec(spec)
         loader.exec_module(mod)
-        mod.bind({n: ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in _CALLS})
-    except (ImportError, SystemError, AttributeError, KeyError, ValueError) as e:
+        mod.bind({n: ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in _CALLS},
+                 DTYPE_CODES, ACT_CODES, OUT_CODES)
+    except (ImportError, SystemError, AttributeError, KeyError, TypeError, ValueError) as e:
         warnings.warn(f"{_PYCALL_PATH} is left out, calls go through ctypes: {e}", RuntimeWarning,
                       stacklevel=3)
         return None

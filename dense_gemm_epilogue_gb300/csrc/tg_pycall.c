@@ -107,24 +107,24 @@ static void *as_stream(PyObject *o, int *ok) {
     return p;
 }
 
-/* A name from a table, or its code. */
-static int as_code(PyObject *o, const char *const *names, int count, int *ok) {
+/* A name from one of the package's tables (bind() brings them), or its code. */
+static PyObject *t_dtypes, *t_acts, *t_outs;
+static int as_code(PyObject *o, PyObject *names, int *ok) {
     if (!*ok) return 0;
     if (PyUnicode_Check(o)) {
-        for (int i = 0; i < count; ++i)
-            if (PyUnicode_CompareWithASCIIString(o, names[i]) == 0) return i;
-        PyErr_SetObject(PyExc_KeyError, o);
-        *ok = 0;
-        return 0;
+        PyObject *v = PyDict_GetItemWithError(names, o);
+        if (!v) {
+            if (!PyErr_Occurred()) PyErr_SetObject(PyExc_KeyError, o);
+            *ok = 0;
+            return 0;
+        }
+        return (int)as_int(v, ok);
     }
     return (int)as_int(o, ok);
 }
-static const char *const DTYPES[] = {"bf16", "fp16", "tf32", "e4m3", "e5m2", "e2m1", "nvf4"};
-static const char *const ACTS[] = {"none", "relu", "silu", "gelu_tanh"};
-static const char *const OUTS[] = {"f32", "bf16", "fp16"};
-#define DTYPE(o) ((tg_dtype)as_code(o, DTYPES, 7, &ok))
-#define ACT(o) ((tg_activation)as_code(o, ACTS, 4, &ok))
-#define OUT(o) ((tg_out_dtype)as_code(o, OUTS, 3, &ok))
+#define DTYPE(o) ((tg_dtype)as_code(o, t_dtypes, &ok))
+#define ACT(o) ((tg_activation)as_code(o, t_acts, &ok))
+#define OUT(o) ((tg_out_dtype)as_code(o, t_outs, &ok))
 #define INT(o) as_int(o, &ok)
 #define PTR(o) as_ptr(o, &ok)
 
@@ -277,10 +277,17 @@ static PyObject *py_norm_back(PyObject *self, PyObject *const *a, Py_ssize_t n) 
     RUN(f_norm_back(m, nn, dy, lddy, x, ldx, gamma, mean, rstd, dx, lddx, dgamma, dbeta, t, ws, bytes, st))
 }
 
-/* bind({name: address}): every entry point the calls above use. */
-static PyObject *py_bind(PyObject *self, PyObject *table) {
+/* bind({name: address}, dtypes, acts, outs): every entry point the calls above
+ * use, and the {name: code} tables of their arguments. */
+static PyObject *py_bind(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+    PyObject *table;
+    if (n != 4 || !PyDict_Check(a[0]) || !PyDict_Check(a[1]) || !PyDict_Check(a[2]) || !PyDict_Check(a[3])) {
+        PyErr_SetString(PyExc_TypeError, "bind: four dictionaries");
+        return NULL;
+    }
+    table = a[0];
     for (size_t i = 0; i < N_ENTRIES; ++i) {
-        PyObject *v = PyDict_Check(table) ? PyDict_GetItemString(table, ENTRIES[i].name) : NULL;
+        PyObject *v = PyDict_GetItemString(table, ENTRIES[i].name);
         void *p;
         if (!v) {
             PyErr_Format(PyExc_KeyError, "%s", ENTRIES[i].name);
@@ -293,12 +300,18 @@ static PyObject *py_bind(PyObject *self, PyObject *table) {
         }
         memcpy(ENTRIES[i].slot, &p, sizeof(p));
     }
+    Py_INCREF(a[1]);
+    Py_INCREF(a[2]);
+    Py_INCREF(a[3]);
+    Py_XSETREF(t_dtypes, a[1]);
+    Py_XSETREF(t_acts, a[2]);
+    Py_XSETREF(t_outs, a[3]);
     Py_RETURN_NONE;
 }
 
 #define FAST(name, f) {name, (PyCFunction)(void (*)(void))f, METH_FASTCALL, NULL}
 static PyMethodDef METHODS[] = {
-    {"bind", py_bind, METH_O, NULL},
+    FAST("bind", py_bind),
     FAST("tg_linear_workspace_bytes", py_linear_ws),
     FAST("tg_linear", py_linear),
     FAST("tg_gated_workspace_bytes", py_gated_ws),

@@ -110,3 +110,23 @@ def test_a_source_that_does_not_compile_leaves_the_library(builder, monkeypatch,
         assert builder.build() == builder.LIB
     assert not builder.os.path.exists(builder.PYCALL)
     assert builder.os.path.exists(builder.LIB)
+
+
+@pytest.mark.parametrize("through", ["module", "ctypes"])
+def test_names_come_from_the_package_tables(tg, monkeypatch, through):
+    """A name that the package's tables learn is known on either path."""
+    if through == "ctypes":
+        monkeypatch.setattr(tg, "_call", None)
+    elif tg._call is None:
+        pytest.skip("built without Python's headers")
+    monkeypatch.setitem(tg.DTYPE_CODES, "brain", tg.TG_BF16)
+    monkeypatch.setitem(tg.ACT_CODES, "swish", tg.TG_ACT_SILU)
+    monkeypatch.setitem(tg.OUT_CODES, "single", tg.TG_OUT_F32)
+    a = 1 << 20
+    assert tg.tg_linear_workspace_bytes(64, 96, 128, a, 128, a, 128, "brain") == 0
+    assert tg.tg_gated(0, 96, 128, None, 128, a, 128, a, 128, "swish", None, 96, None, 0, None, 0,
+                       "brain") == tg.TG_OK
+    assert tg.tg_layer_norm(0, 8, None, 8, None, None, 1e-5, None, 8, None, None, "single") == tg.TG_OK
+    for bad in ("nothing", ""):
+        with pytest.raises(KeyError):
+            tg.tg_linear_workspace_bytes(64, 96, 128, a, 128, a, 128, bad)
