@@ -55,16 +55,27 @@ namespace tg {
 enum MlpAct : int32_t { MLP_NONE = 0, MLP_RELU = 1, MLP_SILU = 2, MLP_GELU = 3, MLP_ACTS = 4 };
 
 // The activations and their derivatives all come from one logistic function,
-// sigmoid(v) = 1 / (1 + 2^(-v log2 e)), by the hardware's base-2 exponential
+// sigmoid(v) = 1 / (1 + 2^u), u = -v log2 e, by the hardware's base-2 exponential
 // and reciprocal: relative error about 2^-21 for the |v| that matter, far
 // below a 16-bit output's 2^-9, and below the 1e-6 that an FP32 column sum over
-// it is held to.  2^(-v log2 e) = inf for large negative v gives 0, the limit.
+// it is held to.  The error grows with |u| (u's own rounding), to about 2^-17 at
+// the tail's end.
+//
+// Both instructions flush subnormal results, and 2^u overflows from u = 128 on,
+// while y sigmoid(y) stays a normal FP32 and BF16 number down to y = -91.8 (u =
+// 132).  So from u = 64 on numerator and denominator carry a factor 2^-64:
+// 2^-64 / (2^-64 + 2^(u - 64)).  u - 64 is exact there, the reciprocal stays
+// normal, and the last product rounds to a subnormal where the value is one.
+// Beyond u = 192 the limit 0 is right to FP32's smallest subnormal.
 constexpr float kLog2E = 1.4426950408889634f;
 __device__ __forceinline__ float mlp_sigmoid_2(float u) {  // u = -v log2 e
+    constexpr float FAR = 64.0f, SCALE = 5.421010862427522e-20f;  // 2^-64
+    const bool far = u > FAR;
+    const float one = far ? SCALE : 1.0f;
     float e, s;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(u));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.0f + e));
-    return s;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(far ? u - FAR : u));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(one + e));
+    return one * s;
 }
 
 // The tanh form of GELU is y/2 (1 + tanh(v)) = y sigmoid(2v), v =
