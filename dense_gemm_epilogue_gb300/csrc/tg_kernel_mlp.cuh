@@ -759,7 +759,7 @@ __global__ void __launch_bounds__(MlpConfig<KD, CG, BN, AM, BM, EP>::NUM_THREADS
                         if (mp.bias) {
                             __syncwarp();
                             reinterpret_cast<float *>(bias_s)[lane] =
-                                col + lane < p.n ? __ldg(mp.bias + col + lane) : 0.0f;
+                                col + lane < p.n ? mp.bias[col + lane] : 0.0f;
                             __syncwarp();
                         }
                         load_acc(cbase + c, y);

@@ -352,7 +352,7 @@ __global__ void __launch_bounds__(StreamConfig<KD, NT, OP>::NUM_THREADS,
                 }
                 const int32_t f = un.t * BLOCK_M + q * 32 + lane;
                 const bool in = f < p.features;
-                const float b = (p.bias && in) ? __ldg(p.bias + f) : 0.0f;
+                const float b = (p.bias && in) ? p.bias[f] : 0.0f;
                 // The epilogue of TC tokens from j0 on.
                 auto finish = [&](auto tc, int j0) {
                     constexpr int TC = tc.value;

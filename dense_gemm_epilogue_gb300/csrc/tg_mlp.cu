@@ -65,9 +65,9 @@ __device__ __forceinline__ uint4 load_shifted(const unsigned short *q) {
     const uintptr_t at = (uintptr_t)q;
     const uint4 *w = reinterpret_cast<const uint4 *>(at & ~(uintptr_t)15);
     const uint32_t s = (uint32_t)at & 15u;
-    const uint4 a = __ldg(w);
+    const uint4 a = w[0];
     if (s == 0) return a;
-    const uint4 b = __ldg(w + 1);
+    const uint4 b = w[1];
     const uint32_t bits = (s & 2u) * 8;
     uint32_t x0, x1, x2, x3, x4;
     switch (s >> 2) {

@@ -333,8 +333,8 @@ __global__ void __launch_bounds__(norm_block<TR>(), NORM_SM / norm_block<TR>())
 #pragma unroll
     for (int i = 0; i < NORM_PER / 2; ++i) {
         const int c = Cols::at(2 * i, t), d = Cols::at(2 * i + 1, t);
-        gam[i] = f2(p.gamma && c < n ? __ldg(p.gamma + c) : 1.0f, p.gamma && d < n ? __ldg(p.gamma + d) : 1.0f);
-        bet[i] = f2(p.beta && c < n ? __ldg(p.beta + c) : 0.0f, p.beta && d < n ? __ldg(p.beta + d) : 0.0f);
+        gam[i] = f2(p.gamma && c < n ? p.gamma[c] : 1.0f, p.gamma && d < n ? p.gamma[d] : 1.0f);
+        bet[i] = f2(p.beta && c < n ? p.beta[c] : 0.0f, p.beta && d < n ? p.beta[d] : 0.0f);
     }
     T *y = static_cast<T *>(p.y);
     const bool whole = n == THREADS * NORM_PER;
@@ -416,12 +416,12 @@ __global__ void __launch_bounds__(NORM_SM, 1) tg_norm_backward_kernel(const Norm
 #pragma unroll
     for (int i = 0; i < NORM_PER / 2; ++i) {
         const int c = Cols::at(2 * i, t), d = Cols::at(2 * i + 1, t);
-        gam[i] = f2(p.gamma && c < n ? __ldg(p.gamma + c) : 1.0f, p.gamma && d < n ? __ldg(p.gamma + d) : 1.0f);
+        gam[i] = f2(p.gamma && c < n ? p.gamma[c] : 1.0f, p.gamma && d < n ? p.gamma[d] : 1.0f);
         sg[i] = sb[i] = f2(0.0f);
     }
     const bool whole = n == THREADS * NORM_PER;
-    float nmean = group < p.m ? __ldg(p.mean_in + group) : 0.0f;
-    float nrstd = group < p.m ? __ldg(p.rstd_in + group) : 0.0f;
+    float nmean = group < p.m ? p.mean_in[group] : 0.0f;
+    float nrstd = group < p.m ? p.rstd_in[group] : 0.0f;
     for (int64_t r = group; r < p.m; r += groups) {
         F2 w[2][NORM_PER / 2];
         rows.take(w);
@@ -430,8 +430,8 @@ __global__ void __launch_bounds__(NORM_SM, 1) tg_norm_backward_kernel(const Norm
         const F2 minus = f2(-nmean), scale = f2(nrstd);
         const float rstd = nrstd;
         if (r + groups < p.m) {
-            nmean = __ldg(p.mean_in + r + groups);
-            nrstd = __ldg(p.rstd_in + r + groups);
+            nmean = p.mean_in[r + groups];
+            nrstd = p.rstd_in[r + groups];
         }
         F2 s1 = f2(0.0f), s2 = f2(0.0f);
 #pragma unroll

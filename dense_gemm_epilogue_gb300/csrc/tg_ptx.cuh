@@ -20,6 +20,11 @@ __device__ __forceinline__ uint32_t smem_u32(const void *p) {
 // complete, with its memory visible, before its first global-memory access.
 // The prologue (barrier set-up, tensor-memory allocation, the producer's
 // first tile coordinates) overlaps the previous kernel.
+//
+// So a kernel's inputs may still be written while it runs (before its wait),
+// and none of them may be read by non-coherent loads (ld.global.nc), which ask
+// for data that is read-only for the whole kernel and which a compiler may move
+// above the wait: plain and cache-hinted (__ldcg, __ldcs) loads only.
 __device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void griddep_launch() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
