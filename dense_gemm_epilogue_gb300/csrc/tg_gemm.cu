@@ -152,7 +152,8 @@ DeviceState g_dev[kMaxDevices];
 
 // Split-K workspace of one (device, stream): room for `tiles` partial
 // 256 x 256 FP32 pair tiles; ready flags (four per tile: one per segment and
-// tile half of a two-segment exchange), the ticket counter after them and the
+// tile half of a two-segment exchange), the ticket counter after them, the gate
+// between an input gradient and the weight gradient beside it, and the
 // weight-streaming kernel's flags after that, all kept at zero between
 // launches by the kernels themselves.
 constexpr int64_t kFlagsPerTile = 4;
@@ -903,6 +904,7 @@ tg_status scratch(const Device &dev, cudaStream_t stream, int64_t tiles, Scratch
     out->tiles = w.tiles;
     out->flags = w.flags;
     out->ticket = ticket_counter(w.flags, w.tiles);
+    out->gate = out->ticket + kTicketWords / 2;  // (a line of its own)
     out->stream_flags = out->ticket + kTicketWords;
     return TG_OK;
 }

@@ -29,6 +29,7 @@ struct Scratch {
     int64_t tiles = 0;
     uint32_t *flags = nullptr;         // of the CTA-pair kernels (four per tile)
     uint32_t *ticket = nullptr;
+    uint32_t *gate = nullptr;          // MlpParams::gate
     uint32_t *stream_flags = nullptr;  // of the weight-streaming kernel (kStreamFlags words)
 };
 constexpr int64_t kStreamFlags = 8 * 512;

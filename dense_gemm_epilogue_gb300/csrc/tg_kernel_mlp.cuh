@@ -208,11 +208,16 @@ struct MlpParams {
     int32_t clip;             // 1: a row's bytes are a multiple of 16, so TMA may clip a box there
     // 1: this product reads nothing that the kernel before it writes (a weight
     // gradient after the input gradient), so it starts without waiting for that
-    // kernel and waits at its end, for whatever comes next on the stream.  That
-    // the kernels before that one are complete follows from when an input
-    // gradient lets its successor start: after its own wait.  Only one of the two
-    // may use the stream's workspace.
+    // kernel and waits at its end, for whatever comes next on the stream.  Only
+    // one of the two may use the stream's workspace.
     int32_t late_wait;
+    // What makes the kernels before that one visible to it (NULL: neither side).
+    // The input gradient raises the gate (a release) once its own wait has
+    // returned, and only then lets its successor start; the weight gradient's
+    // producers acquire it before their first load.  A gate found down, which
+    // that order rules out, costs them the wait itself.  The weight gradient
+    // takes the gate down again, after its wait.
+    uint32_t *gate;
     MlpOut out[3];            // LINEAR: Y, Z; GATED: H, G, U; PLAIN: one per entry
 };
 
@@ -392,8 +397,15 @@ __global__ void __launch_bounds__(MlpConfig<KD, CG, BN, AM, BM, EP>::NUM_THREADS
     auto wait_before = [&] {
         if (!mp.late_wait) griddep_wait();
     };
+    // The same for a producer, whose loads everything else follows (through the
+    // stage barriers): with late_wait it acquires the gate.  The fence orders
+    // TMA's reads after it.
+    auto wait_inputs = [&] {
+        if (mp.late_wait && ld_acquire_gpu_u32(mp.gate) != 0u) fence_proxy_async();
+        else griddep_wait();
+    };
     // The next kernel may be set up beside this one from here on; an input
-    // gradient holds it back until its own wait (see late_wait).
+    // gradient holds it back until its own wait (see late_wait, gate).
     constexpr bool HOLD = AM == 0 && BM == 1;
     if (!HOLD) griddep_launch();
     const uint32_t tmem_base = *tmem_slot;
@@ -433,7 +445,7 @@ __global__ void __launch_bounds__(MlpConfig<KD, CG, BN, AM, BM, EP>::NUM_THREADS
                 int bt, mb, nb;
                 batch_tile_coords(un.tile, p, bt, mb, nb);
                 if (!waited) {
-                    wait_before();
+                    wait_inputs();
                     waited = true;
                 }
                 if (tick) {
@@ -515,7 +527,11 @@ __global__ void __launch_bounds__(MlpConfig<KD, CG, BN, AM, BM, EP>::NUM_THREADS
     } else if (warp == 1) {
         // ------------------------------------------------------ MMA issuer (leader)
         wait_before();
-        if (HOLD) griddep_launch();
+        if (HOLD) {
+            if (mp.gate && blockIdx.x == 0 && lane == 0) st_release_gpu_u32(mp.gate, 1u);
+            __syncwarp();
+            griddep_launch();
+        }
         if (leader && lane == 0) {
             int s = 0;
             uint32_t ph = 0;
@@ -894,7 +910,10 @@ __global__ void __launch_bounds__(MlpConfig<KD, CG, BN, AM, BM, EP>::NUM_THREADS
         if (lane == 0) bulk_wait_all();
     }
 
-    if (mp.late_wait) griddep_wait();
+    if (mp.late_wait) {
+        griddep_wait();
+        if (blockIdx.x == 0 && threadIdx.x == 0) st_release_gpu_u32(mp.gate, 0u);
+    }
     tc_fence_before();
     if constexpr (CG == 2) cluster_sync_all();
     else __syncthreads();

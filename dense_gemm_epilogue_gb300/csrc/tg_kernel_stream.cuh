@@ -91,6 +91,7 @@ struct StreamParams {
     MlpOut out[3];  // LINEAR: Y, Z; GATED: H, G, U
     float *ws;      // one slot of 128 x 256 floats per CTA
     uint32_t *flags;  // eight per CTA (one per epilogue warp), zero between launches
+    uint32_t *gate;   // DGRAD: as MlpParams::gate
     uint32_t *status;
     uint64_t wait_limit_ns;
 };
@@ -179,7 +180,7 @@ __global__ void __launch_bounds__(StreamConfig<KD, NT, OP>::NUM_THREADS,
     __syncthreads();
     tc_fence_after();
     // (an input gradient holds its successor back until its own wait: see
-    // MlpParams::late_wait)
+    // MlpParams::late_wait and gate)
     if (!TRANS) griddep_launch();
     const uint32_t tmem_base = *tmem_slot;
     const int nkb = p.num_k_blocks;
@@ -242,7 +243,11 @@ __global__ void __launch_bounds__(StreamConfig<KD, NT, OP>::NUM_THREADS,
         __syncwarp();
     } else if (warp == 1) {
         griddep_wait();
-        if (TRANS) griddep_launch();
+        if (TRANS) {
+            if (p.gate && blockIdx.x == 0 && lane == 0) st_release_gpu_u32(p.gate, 1u);
+            __syncwarp();
+            griddep_launch();
+        }
         if (lane == 0) {
             int s = 0;
             uint32_t ph = 0;

@@ -335,7 +335,7 @@ struct Product {
     int act;
     const float *bias;
     Mat r;             // residual (p NULL: none)
-    bool beside;       // reads nothing of the kernel before it: may run beside it
+    uint32_t *gate;    // MlpParams::gate (input gradient: raised; weight gradient: runs beside it)
 };
 
 struct TilePlan {
@@ -501,8 +501,8 @@ tg_status run_product(const Product &q, tg_dtype t, const Device &dev, cudaStrea
         g.k_snake = plan.ticket ? 1 : 0;
         if (plan.ticket) g.ticket = w.ticket;
     }
-    // Beside the kernel before it only without the workspace that it may use.
-    p.late_wait = q.beside && plan.split_max == 1 && !plan.ticket;
+    p.gate = q.gate;
+    p.late_wait = q.gate && q.op == MlpOp::WGRAD;
     la.op = q.op;
     la.cg = plan.cg;
     la.block_n = plan.block_n;
@@ -563,6 +563,7 @@ tg_status run_stream(const Product &q, tg_dtype t, const Device &dev, cudaStream
     if (st != TG_OK) return st;
     p.ws = w.ws;
     p.flags = w.stream_flags;
+    p.gate = q.gate;
     p.status = dev.status;
     p.wait_limit_ns = dev.wait_limit_ns;
     la.device = dev.id;
@@ -572,14 +573,23 @@ tg_status run_stream(const Product &q, tg_dtype t, const Device &dev, cudaStream
 }
 
 // The input gradient, then the weight gradient (either may be missing).
-tg_status run_gradients(const Product *x, Product *w, tg_dtype t, const Device &dev, cudaStream_t stream) {
+// A weight gradient that needs no workspace (no split tiles, no tickets) starts
+// beside the input gradient, which may be using it.
+tg_status run_gradients(Product *x, Product *w, tg_dtype t, const Device &dev, cudaStream_t stream) {
     Beside both;
-    if (x && w) {
-        both = plan_beside(*x, *w, dev.sms);
-        w->beside = true;
+    TilePlan wp = {};
+    if (w) {
+        if (x) both = plan_beside(*x, *w, dev.sms);
+        wp = both.on ? both.w : plan_tiles(*w, dev.sms);
+        if (x && wp.split_max == 1 && !wp.ticket) {
+            host::Scratch s;
+            const tg_status st = host::scratch(dev, stream, div_up(dev.sms, 2), &s);
+            if (st != TG_OK) return st;
+            x->gate = w->gate = s.gate;
+        }
     }
     tg_status st = x ? run_product(*x, t, dev, stream, both.on ? &both.x : nullptr) : TG_OK;
-    if (st == TG_OK && w) st = run_product(*w, t, dev, stream, both.on ? &both.w : nullptr);
+    if (st == TG_OK && w) st = run_product(*w, t, dev, stream, &wp);
     return st;
 }
 

@@ -111,6 +111,8 @@ __device__ __forceinline__ void prefetch_tensormap(const CUtensorMap *map) {
 
 // Orders this thread's generic-proxy shared-memory writes before later
 // async-proxy (TMA / tensor core) accesses.
+// Between ordinary accesses and TMA's, all state spaces.
+__device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async;" ::: "memory"); }
 __device__ __forceinline__ void fence_proxy_async_smem() {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
