@@ -52,6 +52,16 @@ TG_ACT_GELU_TANH = 3
 ACT_CODES = {"none": TG_ACT_NONE, "relu": TG_ACT_RELU, "silu": TG_ACT_SILU,
              "gelu_tanh": TG_ACT_GELU_TANH}
 
+TG_PRODUCT_LINEAR = 0
+TG_PRODUCT_GATED = 1
+TG_PRODUCT_LINEAR_DX = 2
+TG_PRODUCT_GATED_DX = 3
+TG_PRODUCT_LINEAR_DW = 4
+TG_PRODUCT_GATED_DW = 5
+PRODUCT_CODES = {"linear": TG_PRODUCT_LINEAR, "gated": TG_PRODUCT_GATED,
+                 "linear_dx": TG_PRODUCT_LINEAR_DX, "gated_dx": TG_PRODUCT_GATED_DX,
+                 "linear_dw": TG_PRODUCT_LINEAR_DW, "gated_dw": TG_PRODUCT_GATED_DW}
+
 OUT_CODES = {"f32": TG_OUT_F32, "bf16": TG_OUT_BF16, "fp16": TG_OUT_F16}
 
 # Every symbol include/tg_gemm.h declares.
@@ -86,6 +96,7 @@ EXPORTED = (
     "tg_layer_norm",
     "tg_layer_norm_backward_workspace_bytes",
     "tg_layer_norm_backward",
+    "tg_product_plan_describe",
 )
 
 
@@ -275,6 +286,9 @@ def load(path: str | None = None) -> ctypes.CDLL:
         lib.tg_layer_norm_backward.argtypes = [i64, i64, vp, i64, vp, i64, vp, vp, vp, vp, i64,
                                                vp, vp, c, vp, i64, vp]
         lib.tg_layer_norm_backward.restype = c
+        lib.tg_product_plan_describe.argtypes = [c, i64, i64, i64, i32, ctypes.c_char_p,
+                                                 ctypes.c_size_t]
+        lib.tg_product_plan_describe.restype = c
         lib.tg_version.argtypes = []
         lib.tg_version.restype = i32
         if path is None:
@@ -570,6 +584,15 @@ def tg_layer_norm_backward(M, N, dY, lddy, X, ldx, gamma, mean, rstd, dX, lddx, 
     return load().tg_layer_norm_backward(M, N, _ptr(dY), lddy, _ptr(X), ldx, _ptr(gamma),
                                          _ptr(mean), _ptr(rstd), _ptr(dX), lddx, _ptr(dgamma),
                                          _ptr(dbeta), _out(dtype), ws, n, _stream(stream))
+
+
+def tg_product_plan_describe(product, M, N, K, num_sms=0, size=256) -> str:
+    """The planner's choice for a feed-forward product (a name of PRODUCT_CODES) as text."""
+    buf = ctypes.create_string_buffer(size)
+    code = PRODUCT_CODES[product] if isinstance(product, str) else int(product)
+    check(load().tg_product_plan_describe(code, M, N, K, num_sms, buf, size),
+          "tg_product_plan_describe")
+    return buf.value.decode()
 
 
 def tg_status_string(status: int) -> str:

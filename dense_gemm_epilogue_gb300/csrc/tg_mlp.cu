@@ -6,6 +6,7 @@
 
 #include <climits>
 #include <cstdint>
+#include <cstdio>
 #include <cstring>
 
 #include "../../include/tg_gemm.h"
@@ -441,10 +442,11 @@ Beside plan_beside(const Product &x, const Product &w, int sms) {
     return best;
 }
 
+bool streams(const Product &q) { return q.op != MlpOp::WGRAD && q.m <= kStreamTokens && q.k[0] > 0; }
+
 tg_status run_product(const Product &q, tg_dtype t, const Device &dev, cudaStream_t stream,
                       const TilePlan *chosen = nullptr) {
-    if (q.op != MlpOp::WGRAD && q.m <= kStreamTokens && q.k[0] > 0 && !q.out_f32)
-        return run_stream(q, t, dev, stream);
+    if (streams(q)) return run_stream(q, t, dev, stream);
     const TilePlan plan = chosen ? *chosen : plan_tiles(q, dev.sms);
     MlpLaunch la;
     std::memset(&la, 0, sizeof(la));
@@ -520,13 +522,32 @@ tg_status run_product(const Product &q, tg_dtype t, const Device &dev, cudaStrea
 // us at 4 blocks).
 int64_t stream_min_blocks(int nt) { return nt <= 16 ? 4 : nt <= 32 ? 6 : nt <= 64 ? 8 : 12; }
 
+struct StreamPlan {
+    int nt;  // token columns of the MMA
+    int64_t tiles, k_blocks;
+    int grid;
+};
+StreamPlan plan_stream(const Product &q, int sms) {
+    StreamPlan s;
+    s.nt = q.m <= 16 ? 16 : q.m <= 32 ? 32 : q.m <= 64 ? 64 : 128;
+    s.tiles = div_up(q.n, BLOCK_M);
+    s.k_blocks = div_up(q.k[0], 64) + div_up(q.k[1], 64);
+    int64_t grid = s.tiles * s.k_blocks / stream_min_blocks(s.nt);
+    const int64_t cap = sms < 512 ? sms : 512;
+    if (grid > cap) grid = cap;
+    s.grid = (int)(grid < 1 ? 1 : grid);
+    return s;
+}
+
 tg_status run_stream(const Product &q, tg_dtype t, const Device &dev, cudaStream_t stream) {
+    const StreamPlan plan = plan_stream(q, dev.sms);
     StreamLaunch la;
     std::memset(&la, 0, sizeof(la));
     la.op = q.op == MlpOp::GATED   ? StreamOp::GATED
             : q.op == MlpOp::DGRAD ? StreamOp::DGRAD
                                    : StreamOp::LINEAR;
-    la.nt = q.m <= 16 ? 16 : q.m <= 32 ? 32 : q.m <= 64 ? 64 : 128;
+    la.nt = plan.nt;
+    la.grid = plan.grid;
     const tg_out_dtype ot = out_type(t);
     // Weights: 128-row boxes, or 64 x 64 ones where they are read transposed.
     const int box = q.op == MlpOp::DGRAD ? 64 : BLOCK_M;
@@ -540,10 +561,9 @@ tg_status run_stream(const Product &q, tg_dtype t, const Device &dev, cudaStream
     StreamParams &p = la.p;
     p.tokens = (int32_t)q.m;
     p.features = (int32_t)q.n;
-    p.tiles = (int32_t)div_up(q.n, BLOCK_M);
+    p.tiles = (int32_t)plan.tiles;
     p.k_blocks0 = (int32_t)div_up(q.k[0], 64);
-    if (p.k_blocks0 > INT32_MAX / 4) return TG_ERR_INVALID_VALUE;
-    p.num_k_blocks = p.k_blocks0 + (int32_t)div_up(q.k[1], 64);
+    p.num_k_blocks = (int32_t)plan.k_blocks;
     p.act = q.act;
     p.bias = q.bias;
     p.r = q.r.p;
@@ -552,12 +572,6 @@ tg_status run_stream(const Product &q, tg_dtype t, const Device &dev, cudaStream
         p.out[i].ptr = const_cast<void *>(q.out[i].p);
         p.out[i].ld = q.out[i].ld;
     }
-    const int64_t total = (int64_t)p.tiles * p.num_k_blocks;
-    int64_t grid = total / stream_min_blocks(la.nt);
-    const int64_t cap = dev.sms < 512 ? dev.sms : 512;
-    if (grid > cap) grid = cap;
-    if (grid < 1) grid = 1;
-    la.grid = (int)grid;
     host::Scratch w;
     const tg_status st = host::scratch(dev, stream, div_up(dev.sms, 2), &w);
     if (st != TG_OK) return st;
@@ -572,16 +586,18 @@ tg_status run_stream(const Product &q, tg_dtype t, const Device &dev, cudaStream
     return e == cudaSuccess ? TG_OK : TG_ERR_CUDA;
 }
 
+// A weight gradient that needs no workspace (no split tiles, no tickets) may
+// run beside the input gradient, which may be using it.
+bool runs_beside(const TilePlan &w) { return w.split_max == 1 && !w.ticket; }
+
 // The input gradient, then the weight gradient (either may be missing).
-// A weight gradient that needs no workspace (no split tiles, no tickets) starts
-// beside the input gradient, which may be using it.
 tg_status run_gradients(Product *x, Product *w, tg_dtype t, const Device &dev, cudaStream_t stream) {
     Beside both;
     TilePlan wp = {};
     if (w) {
         if (x) both = plan_beside(*x, *w, dev.sms);
         wp = both.on ? both.w : plan_tiles(*w, dev.sms);
-        if (x && wp.split_max == 1 && !wp.ticket) {
+        if (x && runs_beside(wp)) {
             host::Scratch s;
             const tg_status st = host::scratch(dev, stream, div_up(dev.sms, 2), &s);
             if (st != TG_OK) return st;
@@ -917,6 +933,68 @@ extern "C" tg_status tg_gated_backward(int64_t M, int64_t N, int64_t K, const vo
     if (qw.entries == 2) qw.out[1] = mat(dWu, lddwu, N, K, ew);
     qw.out_f32 = dw_dtype == TG_OUT_F32;
     return run_gradients(dx ? &qx : nullptr, dw ? &qw : nullptr, dtype, dev, stream);
+}
+
+// ------------------------------------------------------------------ the planner's choice as text
+
+namespace {
+
+Product shape_of(MlpOp op, int64_t m, int64_t n, int64_t k0, int64_t k1, int entries) {
+    Product q = {};
+    q.op = op;
+    q.m = m;
+    q.n = n;
+    q.k[0] = k0;
+    q.k[1] = k1;
+    q.entries = entries;
+    return q;
+}
+
+}  // namespace
+
+extern "C" tg_status tg_product_plan_describe(tg_product product, int64_t M, int64_t N, int64_t K,
+                                              int32_t num_sms, char *buf, size_t len) {
+    if (!buf || len == 0) return TG_ERR_INVALID_VALUE;
+    buf[0] = '\0';
+    if (!dims_ok(M, N, K) || (int)product < 0 || (int)product > (int)TG_PRODUCT_GATED_DW)
+        return TG_ERR_INVALID_VALUE;
+    int sms = num_sms;
+    if (sms <= 0) {
+        Device dev;
+        const tg_status st = host::device(&dev);
+        if (st != TG_OK) return st;
+        sms = dev.sms;
+    }
+    const bool gated = product == TG_PRODUCT_GATED || product == TG_PRODUCT_GATED_DX || product == TG_PRODUCT_GATED_DW;
+    const bool dw = product == TG_PRODUCT_LINEAR_DW || product == TG_PRODUCT_GATED_DW;
+    const bool dx = product == TG_PRODUCT_LINEAR_DX || product == TG_PRODUCT_GATED_DX;
+    const Product x = shape_of(MlpOp::DGRAD, M, K, N, gated ? N : 0, 1);
+    const Product w = shape_of(MlpOp::WGRAD, N, K, M, 0, gated ? 2 : 1);
+    const Product y = shape_of(gated ? MlpOp::GATED : MlpOp::LINEAR, M, N, K, 0, 1);
+    const Product &q = dw ? w : dx ? x : y;
+    int n;
+    if (q.m == 0 || q.n == 0) {
+        n = std::snprintf(buf, len, "empty");
+    } else if (streams(q)) {
+        const StreamPlan s = plan_stream(q, sms);
+        n = std::snprintf(buf, len, "stream 128x%d tiles=%lld k_blocks=%lld grid=%d", s.nt,
+                          (long long)s.tiles, (long long)s.k_blocks, s.grid);
+    } else {
+        const bool both = (dw || dx) && M > 0 && N > 0 && K > 0;
+        Beside b;
+        if (both) b = plan_beside(x, w, sms);
+        const TilePlan p = b.on ? (dw ? b.w : b.x) : plan_tiles(q, sms);
+        const TilePlan wp = b.on ? b.w : plan_tiles(w, sms);
+        const int64_t teams = sms / p.cg > 0 ? sms / p.cg : 1;
+        n = std::snprintf(buf, len,
+                          "%s %dx%d tiles=%lld k_blocks=%lld grid=%d raster=%d split=%lldx%d schedule=%s "
+                          "beside=%d",
+                          p.cg == 2 ? "pair" : "single", 128 * p.cg, p.block_n, (long long)p.tiles,
+                          (long long)(div_up(q.k[0], 64) + div_up(q.k[1], 64)), p.grid, p.group,
+                          (long long)(p.split_max > 1 ? p.tiles % teams : 0), p.split_max,
+                          p.ticket ? "ticket" : "static", both && runs_beside(wp) ? 1 : 0);
+    }
+    return (n >= 0 && (size_t)n < len) ? TG_OK : TG_ERR_INVALID_VALUE;
 }
 
 // ------------------------------------------------------------------ shared launch

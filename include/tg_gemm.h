@@ -522,6 +522,32 @@ tg_status tg_layer_norm_backward(int64_t M, int64_t N, const void *dY, int64_t l
                                  float *dgamma, float *dbeta, tg_out_dtype dtype,
                                  void *workspace, int64_t workspace_bytes, void *stream);
 
+/*
+ * The planner's choice for one product of these operators, as one line of
+ * text (host only when num_sms > 0; num_sms <= 0 queries the current device):
+ * a forward product, or dX or dW of the backward call with both asked for.
+ *   "stream 128x16 tiles=112 k_blocks=64 grid=152": up to 128 tokens, the
+ *       weights streamed through 128-row tiles by `grid` CTAs of equal shares;
+ *   "pair 256x256 tiles=561 k_blocks=17 grid=152 raster=12 split=0x1
+ *       schedule=ticket beside=0" (one line): tiles of CTA pairs (or "single"
+ *       CTAs) by the accumulator's rows and columns; the last split tiles cut
+ *       into that many K segments; beside=1: dW starts beside dX;
+ *   "empty": no output elements.
+ * The types and strides of the operands do not matter to it.  Returns TG_OK;
+ * TG_ERR_INVALID_VALUE for a bad size or product, or when the text did not fit
+ * (buf then holds its NUL-terminated start).
+ */
+typedef enum {
+    TG_PRODUCT_LINEAR = 0,
+    TG_PRODUCT_GATED = 1,
+    TG_PRODUCT_LINEAR_DX = 2,
+    TG_PRODUCT_GATED_DX = 3,
+    TG_PRODUCT_LINEAR_DW = 4,
+    TG_PRODUCT_GATED_DW = 5
+} tg_product;
+tg_status tg_product_plan_describe(tg_product product, int64_t M, int64_t N, int64_t K,
+                                   int32_t num_sms, char *buf, size_t len);
+
 /* Static text for a status code ("TG_OK", ...); never NULL. */
 const char *tg_status_string(tg_status status);
 

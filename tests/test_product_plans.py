@@ -1,0 +1,81 @@
+"""tg_product_plan_describe on the host (no GPU): its text, its refusals, and
+what the planner may choose."""
+
+from __future__ import annotations
+
+import ctypes
+import re
+
+import pytest
+
+SMS = 152
+PRODUCTS = ["linear", "gated", "linear_dx", "gated_dx", "linear_dw", "gated_dw"]
+
+
+@pytest.fixture(scope="module")
+def tg():
+    import dense_gemm_epilogue_gb300 as tg
+
+    tg.build()
+    tg.load()
+    return tg
+
+
+def test_text(tg):
+    d = tg.tg_product_plan_describe
+    assert d("gated", 4, 14336, 4096, SMS) == "stream 128x16 tiles=112 k_blocks=64 grid=152"
+    assert d("linear_dx", 100, 8, 300, SMS) == "stream 128x128 tiles=3 k_blocks=1 grid=1"
+    assert d("linear", 4097, 8200, 1032, SMS) == (
+        "pair 256x256 tiles=561 k_blocks=17 grid=152 raster=12 split=0x1 schedule=ticket beside=0")
+    assert d("linear", 0, 8, 8, SMS) == d("linear_dx", 8, 8, 0, SMS) == "empty"
+    assert d("gated_dx", 200, 1000, 136, SMS).split()[3] == "k_blocks=32"  # two pairs of 16
+
+
+def test_refusals(tg):
+    f = tg.load().tg_product_plan_describe
+    buf = ctypes.create_string_buffer(200)
+    assert f(0, 8, 8, 8, SMS, buf, 200) == tg.TG_OK
+    for bad in ((-1, 8, 8, 8), (6, 8, 8, 8), (0, -1, 8, 8), (0, 8, -1, 8), (0, 8, 8, 1 << 31)):
+        assert f(*bad, SMS, buf, 200) == tg.TG_ERR_INVALID_VALUE
+    assert f(0, 8, 8, 8, SMS, None, 200) == tg.TG_ERR_INVALID_VALUE
+    assert f(0, 8, 8, 8, SMS, buf, 0) == tg.TG_ERR_INVALID_VALUE
+    assert f(0, 8, 8, 8, SMS, buf, 9) == tg.TG_ERR_INVALID_VALUE
+    assert buf.value == b"stream 1"
+    with pytest.raises(KeyError):
+        tg.tg_product_plan_describe("product", 8, 8, 8, SMS)
+
+
+def test_streaming_ends_at_128_tokens(tg):
+    d = tg.tg_product_plan_describe
+    for p in ("linear", "gated", "linear_dx", "gated_dx"):
+        assert d(p, 128, 264, 520, SMS).startswith("stream ")
+        assert not d(p, 129, 264, 520, SMS).startswith("stream ")
+    for p in ("linear_dw", "gated_dw"):
+        assert not d(p, 3, 264, 520, SMS).startswith("stream ")
+
+
+def plans(tg, products=PRODUCTS):
+    """Tile plans over a fixed sweep of sizes: the text's fields."""
+    sizes = (1, 72, 129, 200, 333, 520, 777, 1001, 2056, 4096, 8200)
+    for p in products:
+        for m in sizes:
+            for n in sizes:
+                for k in (8, 136, 1000, 2100, 4096, 14336):
+                    t = tg.tg_product_plan_describe(p, m, n, k, SMS)
+                    r = re.fullmatch(r"(pair|single) (\d+)x(\d+) tiles=(\d+) k_blocks=(\d+) grid=(\d+) "
+                                     r"raster=(\d+) split=(\d+)x(\d+) schedule=(ticket|static) beside=([01])", t)
+                    if r:
+                        yield p, (m, n, k), r[1], *[int(v) for v in r.groups()[1:9]], r[10], r[11] == "1"
+
+
+def test_plans_keep_the_kernels_limits(tg):
+    for p, size, kind, rows, cols, tiles, kb, grid, raster, tail, segs, sched, beside in plans(tg):
+        cg = 2 if kind == "pair" else 1
+        teams = SMS // cg
+        assert rows == 128 * cg and cols in (128, 256), size
+        assert 0 < grid <= SMS and grid % cg == 0 and 1 <= segs <= 4 and raster >= 1, size
+        assert tail == (tiles % teams if segs > 1 else 0), size
+        assert segs == 1 or (kb // segs >= 8 and tail * segs <= teams), size
+        assert sched == "static" or (tiles >= 6 * teams and kb >= 16), size
+        if beside and p.endswith("_dw"):
+            assert segs == 1 and sched == "static", size
