@@ -69,7 +69,9 @@ static cudaError_t launch_mlp_bn(const MlpLaunch &a) {
 
 template <Kind KD, int CG>
 static cudaError_t launch_mlp_kind(const MlpLaunch &a) {
-    return a.block_n == 256 ? launch_mlp_bn<KD, CG, 256>(a) : launch_mlp_bn<KD, CG, 128>(a);
+    if (a.block_n == 256) return launch_mlp_bn<KD, CG, 256>(a);
+    if constexpr (CG == 1) return launch_mlp_bn<KD, 1, 128>(a);
+    return cudaErrorInvalidValue;  // (pairs: 256 columns only)
 }
 
 template <Kind KD, int NT, StreamOp OP>

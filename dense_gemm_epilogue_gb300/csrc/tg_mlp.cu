@@ -352,13 +352,14 @@ struct TilePlan {
 // its epilogue adds where nothing overlaps it; and what joining s segments adds
 // to a split tile (FP32 partial sums written, then s - 1 of them read back).
 // The 128-column tiles move 3/4 of the bytes per K block for half the work, so
-// they pay only where they fill SMs that 256-column tiles leave idle.
+// they pay only where they fill SMs that 256-column tiles leave idle.  (256 x 128
+// pair tiles took 0.286 us a K block, what two 128 x 128 CTAs on the same two SMs
+// take for the same work, so they were never the cheapest and are not built.)
 struct TileCost {
     int cg, bn;
     double block, epilogue, join, join_part;
 };
 constexpr TileCost kTiles[] = {{2, 256, 0.350, 4.5, 5.0, 3.0},
-                               {2, 128, 0.286, 2.0, 3.0, 1.2},
                                {1, 256, 0.395, 4.5, 5.0, 3.0},
                                {1, 128, 0.283, 2.0, 3.0, 1.2}};
 constexpr int kSplitMax = SPLIT_PARTS + 1;

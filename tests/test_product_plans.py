@@ -28,6 +28,7 @@ def test_text(tg):
     assert d("linear", 4097, 8200, 1032, SMS) == (
         "pair 256x256 tiles=561 k_blocks=17 grid=152 raster=12 split=0x1 schedule=ticket beside=0")
     assert d("linear", 0, 8, 8, SMS) == d("linear_dx", 8, 8, 0, SMS) == "empty"
+    assert d("linear", 8, 8, 0, SMS).startswith("single 128x128 tiles=1 k_blocks=0 ")
     assert d("gated_dx", 200, 1000, 136, SMS).split()[3] == "k_blocks=32"  # two pairs of 16
 
 
@@ -79,3 +80,12 @@ def test_plans_keep_the_kernels_limits(tg):
         assert sched == "static" or (tiles >= 6 * teams and kb >= 16), size
         if beside and p.endswith("_dw"):
             assert segs == 1 and sched == "static", size
+
+
+def test_every_instantiated_tile_shape_is_chosen(tg):
+    """Each product is compiled for exactly the tile shapes that its plans name."""
+    shapes = {}
+    for p, _, kind, rows, cols, *_ in plans(tg):
+        shapes.setdefault(p, set()).add((kind, rows, cols))
+    for p in PRODUCTS:
+        assert shapes[p] == {("pair", 256, 256), ("single", 128, 256), ("single", 128, 128)}, p
