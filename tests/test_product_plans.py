@@ -8,6 +8,8 @@ import re
 
 import pytest
 
+from mlp_schedules import SCHEDULES, schedule
+
 SMS = 152
 PRODUCTS = ["linear", "gated", "linear_dx", "gated_dx", "linear_dw", "gated_dw"]
 
@@ -89,3 +91,17 @@ def test_every_instantiated_tile_shape_is_chosen(tg):
         shapes.setdefault(p, set()).add((kind, rows, cols))
     for p in PRODUCTS:
         assert shapes[p] == {("pair", 256, 256), ("single", 128, 256), ("single", 128, 128)}, p
+
+
+@pytest.mark.parametrize("product,m,n,k,shape,order,split", SCHEDULES)
+def test_schedules_are_planned_as_listed(tg, product, m, n, k, shape, order, split):
+    """The GPU tests of these sizes run the schedules that they are listed for."""
+    text = tg.tg_product_plan_describe(product, m, n, k, SMS)
+    assert schedule(text, SMS) == (shape, order, split), text
+
+
+def test_every_schedule_of_the_sweep_is_listed(tg):
+    listed = {(s[0], s[4], s[5], s[6]) for s in SCHEDULES}
+    for p, (m, n, k), *_ in plans(tg):
+        found = schedule(tg.tg_product_plan_describe(p, m, n, k, SMS), SMS)
+        assert (p, *found) in listed, (p, m, n, k, found)
