@@ -96,3 +96,149 @@ def test_gradients_after_long_row_work(tg, m, n, k, pad, dtype):
     b.check(f"backward {m}x{n}x{k}")
     for other in kept[:-1]:
         assert all(torch.equal(p, q) for p, q in zip(kept[-1], other))
+
+
+def test_graph_replays_the_whole_backward(tg):
+    """Every output of a captured forward and backward chain, from NaN-filled
+    outputs and workspace, on new inputs, twice; the second weight gradient is
+    one that runs beside its input gradient."""
+    b = Backward(tg, 200, 264, 136, "bf16", pad=1)
+    assert tg.tg_product_plan_describe("linear_dw", 200, 264, 136).endswith("beside=1")
+    y = h.Rows(200, 264, "bf16")
+    ws = h.space(tg.tg_linear_workspace_bytes(200, 264, 136, b.x, b.x.ld, b.w, b.w.ld, "bf16"))
+    s = torch.cuda.Stream()
+
+    def chain():
+        tg.check(tg.tg_linear(200, 264, 136, b.x, b.x.ld, b.w, b.w.ld, None, "silu", None, 0, y, y.ld,
+                              b.z, b.z.ld, "bf16", ws, s))
+        b.run(s)
+
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        chain()
+    s.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        chain()
+    for seed in (31, 32):
+        g = h.gen(seed)
+        for m in (b.x, b.dy, b.w):
+            m.t.copy_(torch.randn(m.rows, m.cols, generator=g, device="cuda") * (0.1 if m is b.w else 1.0))
+        b.poison()
+        for t in (y.t, b.z.t, ws):
+            t.fill_(float("nan") if t.is_floating_point() else 255)
+        graph.replay()
+        torch.cuda.synchronize()
+        want, ye, wz, ze = h.ref_linear(b.x, b.w, None, "silu", None, "bf16")
+        h.check(y.t, want, ye, "replayed Y")
+        h.check(b.z.t, wz, ze, "replayed Z")
+        b.check("replayed")
+        assert all(m.padding_kept() for m in (y, b.z, b.dx, b.dw))
+
+
+class StreamWork:
+    """Calls of one host thread on a stream of its own (torch's current stream is
+    the thread's, so each method enters it)."""
+
+    def __init__(self, tg, seed):
+        self.tg, self.stream, self.out = tg, torch.cuda.Stream(), []
+        with torch.cuda.stream(self.stream):
+            self.back = [Backward(tg, *size, seed=seed) for size in
+                         ((200, 264, 136, "bf16"), (90, 1000, 520, "fp16", 1), (777, 1001, 1365, "fp16"))]
+            g = h.gen(seed)
+            self.forward = []
+            for m, n, k in ((20, 300, 6000), (300, 300, 4096), (1500, 1000, 2048)):
+                self.forward.append((h.rows(g, m, k, "bf16"), h.rows(g, n, k, "bf16", scale=0.02),
+                                     h.Rows(m, n, "bf16")))
+        self.stream.synchronize()
+
+    def run(self):
+        tg, st = self.tg, self.stream
+        with torch.cuda.stream(st):
+            for _ in range(20):
+                for x, w, y in self.forward:
+                    y.t.fill_(float("nan"))
+                    tg.check(tg.tg_linear(x.rows, w.rows, x.cols, x, x.ld, w, w.ld, None, "none", None, 0,
+                                          y, y.ld, None, 0, "bf16", None, st))
+                    self.out.append(y.t.clone())
+                for b in self.back:
+                    b.poison()
+                    b.run(st)
+                    self.out += [t.clone() for t in b.outputs()]
+        st.synchronize()
+
+
+def test_two_streams_at_once(tg):
+    """Two host threads, each with a stream, enqueue split, streaming and
+    backward calls; results equal those of the same calls alone, bit for bit
+    (flags, tickets, partial sums and the gate belong to a stream)."""
+    import threading
+
+    alone = [StreamWork(tg, seed) for seed in (41, 42)]
+    for w in alone:
+        w.run()
+    both = [StreamWork(tg, seed) for seed in (41, 42)]
+    threads = [threading.Thread(target=w.run) for w in both]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    st, where = tg.tg_check_device_status(torch.cuda.current_stream())
+    tg.check(st, f"wait site {where}")
+    for a, b in zip(alone, both):
+        assert len(a.out) == len(b.out) == 240 and all(torch.equal(p, q) for p, q in zip(a.out, b.out))
+
+
+GUARD = 8192
+
+
+class Guarded:
+    """A workspace of exactly the queried size, with sentinel bytes after it."""
+
+    def __init__(self, nbytes):
+        assert nbytes >= 0
+        self.n = nbytes
+        self.buf = torch.full((nbytes + GUARD,), 0x5A, dtype=torch.uint8, device="cuda")
+
+    def arg(self):
+        return self.buf.data_ptr(), self.n
+
+    def check(self, what):
+        assert (self.buf[self.n:] == 0x5A).all(), what
+
+
+@pytest.mark.parametrize("m,n,k", [(1, 1, 1), (3, 65, 33), (40, 70, 150), (129, 257, 65), (300, 93, 201),
+                                   (777, 1001, 1365)])
+@pytest.mark.parametrize("pad", [0, 1])
+def test_workspaces_are_not_overrun(tg, m, n, k, pad):
+    g = h.gen(51 + m)
+    st = torch.cuda.current_stream()
+    x, w, w2 = h.rows(g, m, k, "bf16", pad), h.rows(g, n, k, "bf16", pad), h.rows(g, n, k, "bf16", pad)
+    a, b, c = (h.rows(g, m, n, "bf16", pad) for _ in range(3))
+    y, dx, dw, dw2 = h.Rows(m, n, "bf16"), h.Rows(m, k, "bf16"), h.Rows(n, k, "f32"), h.Rows(n, k, "f32")
+    db = torch.empty(n, device="cuda")
+    s = Guarded(tg.tg_linear_workspace_bytes(m, n, k, x, x.ld, w, w.ld, "bf16"))
+    h.done(tg, tg.tg_linear(m, n, k, x, x.ld, w, w.ld, None, "silu", None, 0, y, y.ld, None, 0, "bf16",
+                            s.arg(), st), "linear")
+    s.check("tg_linear")
+    s = Guarded(tg.tg_gated_workspace_bytes(m, n, k, x, x.ld, w, w.ld, w2, w2.ld, "bf16"))
+    h.done(tg, tg.tg_gated(m, n, k, x, x.ld, w, w.ld, w2, w2.ld, "silu", y, y.ld, None, 0, None, 0, "bf16",
+                           s.arg(), st), "gated")
+    s.check("tg_gated")
+    for act in ("none", "silu"):
+        s = Guarded(tg.tg_linear_backward_workspace_bytes(m, n, k, a, a.ld, x, x.ld, w, w.ld, act, "bf16"))
+        h.done(tg, tg.tg_linear_backward(m, n, k, a, a.ld, x, x.ld, w, w.ld, b, b.ld, act, dx, dx.ld, dw,
+                                         dw.ld, "f32", db, "bf16", s.arg(), st), "linear_backward")
+        s.check("tg_linear_backward")
+    s = Guarded(tg.tg_gated_backward_workspace_bytes(m, n, k, x, x.ld, w, w.ld, w2, w2.ld, "bf16"))
+    h.done(tg, tg.tg_gated_backward(m, n, k, a, a.ld, x, x.ld, w, w.ld, w2, w2.ld, b, b.ld, c, c.ld, "silu",
+                                    dx, dx.ld, dw, dw.ld, dw2, dw2.ld, "f32", "bf16", s.arg(), st),
+           "gated_backward")
+    s.check("tg_gated_backward")
+    xn = x.t.float().contiguous()
+    mean, rstd = (t.float().contiguous() for t in h.norm_stats(xn.double(), 1e-5))
+    dn, dga, dbe = torch.empty_like(xn), torch.empty(k, device="cuda"), torch.empty(k, device="cuda")
+    s = Guarded(tg.tg_layer_norm_backward_workspace_bytes(m, k))
+    h.done(tg, tg.tg_layer_norm_backward(m, k, xn, k, xn, k, None, mean, rstd, dn, k, dga, dbe, "f32",
+                                         s.arg(), st), "norm_backward")
+    s.check("tg_layer_norm_backward")
