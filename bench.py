@@ -395,7 +395,7 @@ def load_peaks():
 
 def load_traffic(kernel_hash: str):
     """Per-launch DRAM bytes from the committed ncu summary, if it was taken
-    on the kernel as it is now (same source hash); else None."""
+    on the kernel as it is now (same hash of the GEMM's sources); else None."""
     p = os.path.join(ROOT, "profiles", "traffic.json")
     if not os.path.exists(p):
         return None
@@ -591,7 +591,7 @@ def run_gpu(args):
              "tg_gemm_pair_kernel" if plan.get("cta_pair") else "tg_gemm_kernel") + \
         f"<{dt.upper()}, {plan['block_m']}x{plan['block_n']}, " + \
         f"{'TMA' if plan['producer'] == 1 else 'plain loads'}>"
-    traffic = load_traffic(tg.source_hash()) if args.workload == WORKLOAD and not batched else None
+    traffic = load_traffic(tg.gemm_source_hash()) if args.workload == WORKLOAD and not batched else None
     default_run = args.workload == WORKLOAD and not batched
     line = {
         "metric": metric_name(w, nbat, out),

@@ -21,7 +21,7 @@ import warnings
 
 from .build import LIB as LIBRARY_PATH
 from .build import PYCALL as _PYCALL_PATH
-from .build import build, source_hash  # noqa: F401
+from .build import build, gemm_source_hash, source_hash  # noqa: F401
 
 TG_OK = 0
 TG_ERR_INVALID_VALUE = 1

@@ -42,17 +42,30 @@ def nvcc() -> str:
     raise RuntimeError("nvcc not found")
 
 
+# What the dense GEMM's kernels are compiled from and planned by.
+GEMM_SOURCES = ["tg_gemm.cu", "tg_inst.cuh", "tg_inst_bf16.cu", "tg_inst_e4m3.cu", "tg_inst_e5m2.cu",
+                "tg_inst_fp16.cu", "tg_inst_tf32.cu", "tg_kernel.cuh", "tg_kernel_mx.cuh",
+                "tg_kernel_pair.cuh", "tg_launch.h", "tg_ptx.cuh"]
+
+
+def _hash(paths) -> str:
+    h = hashlib.sha256()
+    for p in paths:
+        with open(p, "rb") as f:
+            h.update(os.path.basename(p).encode() + b"\0" + f.read())
+    return h.hexdigest()[:16]
+
+
 def source_hash() -> str:
     """Hash of every kernel/host source and header (identifies a build)."""
-    h = hashlib.sha256()
-    names = sorted(os.listdir(CSRC))
-    for n in names:
-        if n.endswith((".cu", ".cuh", ".h")):
-            with open(os.path.join(CSRC, n), "rb") as f:
-                h.update(n.encode() + b"\0" + f.read())
-    with open(os.path.join(ROOT, "include", "tg_gemm.h"), "rb") as f:
-        h.update(f.read())
-    return h.hexdigest()[:16]
+    names = sorted(n for n in os.listdir(CSRC) if n.endswith((".cu", ".cuh", ".h")))
+    return _hash([os.path.join(CSRC, n) for n in names] + [os.path.join(ROOT, "include", "tg_gemm.h")])
+
+
+def gemm_source_hash() -> str:
+    """Hash of the dense GEMM's sources alone: a figure measured on its kernels
+    holds while this one does, whatever the other operators' sources become."""
+    return _hash([os.path.join(CSRC, n) for n in GEMM_SOURCES])
 
 
 def _compile(src: str, verbose_ptxas: bool) -> str:
@@ -68,21 +81,13 @@ def _compile(src: str, verbose_ptxas: bool) -> str:
     return obj
 
 
-def _pycall_hash() -> str:
-    h = hashlib.sha256()
-    for name in (PYCALL_SOURCE, os.path.join(ROOT, "include", "tg_gemm.h")):
-        with open(name, "rb") as f:
-            h.update(f.read())
-    return h.hexdigest()[:16]
-
-
 def _build_pycall(force: bool) -> None:
     """The host-only module that marshals the hot Python calls, with a stamp of
     its own beside it.  Without Python's headers or a C compiler the ctypes
     wrappers serve alone, and the next build() looks again; what the compiler
     refuses (an old Python's headers, say) costs a warning, not the library."""
     stamp = PYCALL + ".hash"
-    want = _pycall_hash()
+    want = _hash([PYCALL_SOURCE, os.path.join(ROOT, "include", "tg_gemm.h")])
     if not force and os.path.exists(PYCALL) and os.path.exists(stamp):
         with open(stamp) as f:
             if f.read().strip() == want:
