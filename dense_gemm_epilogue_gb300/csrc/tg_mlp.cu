@@ -425,6 +425,15 @@ tg_status run_stream(const Product &q, tg_dtype t, const Device &dev, cudaStream
 // of weights at 128 tokens); beyond, 128- and 256-row token tiles waste less.
 constexpr int64_t kStreamTokens = 128;
 
+// Whether `w`'s CTAs find room while all of `x`'s run.  A CTA pair needs both SMs
+// of a neighbouring two, and single CTAs before it are spread over as many such
+// twos as there are.
+bool fit_beside(const TilePlan &x, const TilePlan &w, int sms) {
+    if (w.cg == 1) return x.grid + w.grid <= sms;
+    const int twos = sms / 2, taken = x.cg == 2 ? x.grid / 2 : x.grid < twos ? x.grid : twos;
+    return taken + w.grid / 2 <= twos;
+}
+
 Beside plan_beside(const Product &x, const Product &w, int sms) {
     Beside best;
     if (x.m <= kStreamTokens || x.k[0] == 0 || w.k[0] == 0) return best;
@@ -434,7 +443,7 @@ Beside plan_beside(const Product &x, const Product &w, int sms) {
         for (int j = 0; j < SHAPES; ++j) {
             const TilePlan a = plan_tiles(x, sms, i), b = plan_tiles(w, sms, j);
             const double both = a.time > b.time ? a.time : b.time;
-            if (a.grid + b.grid > sms || a.ticket || b.ticket || both >= t) continue;
+            if (!fit_beside(a, b, sms) || a.ticket || b.ticket || both >= t) continue;
             t = both;
             best.on = true;
             best.x = a;

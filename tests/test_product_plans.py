@@ -84,6 +84,20 @@ def test_plans_keep_the_kernels_limits(tg):
             assert segs == 1 and sched == "static", size
 
 
+@pytest.mark.parametrize("m,n,k", [(777, 1001, 1365), (777, 1000, 1368), (600, 1100, 1300), (900, 1030, 1290)])
+def test_gradients_planned_together_have_room(tg, m, n, k):
+    """Both products at once: a CTA pair needs both SMs of a neighbouring two,
+    and single CTAs in front of it take one SM of as many twos as there are."""
+    def plan(p):
+        r = re.match(r"(\w+) \S+ tiles=\d+ k_blocks=\d+ grid=(\d+) ", tg.tg_product_plan_describe(p, m, n, k, SMS))
+        return r[1], int(r[2])
+
+    (xkind, x), (wkind, w) = plan("linear_dx"), plan("linear_dw")
+    assert x + w <= SMS
+    if wkind == "pair":
+        assert (x // 2 if xkind == "pair" else min(x, SMS // 2)) + w // 2 <= SMS // 2
+
+
 def test_every_instantiated_tile_shape_is_chosen(tg):
     """Each product is compiled for exactly the tile shapes that its plans name."""
     shapes = {}
