@@ -58,20 +58,21 @@ static cudaError_t launch_mlp_one(const MlpLaunch &a) {
 
 template <Kind KD, int CG, int BN>
 static cudaError_t launch_mlp_bn(const MlpLaunch &a) {
+    if constexpr (CG == 1 || BN == 256) {  // (256 x 128 pair tiles: gradients only)
+        if (a.op == MlpOp::LINEAR) return launch_mlp_one<KD, CG, BN, 0, 0, MlpEpi::LINEAR>(a);
+        if (a.op == MlpOp::GATED) return launch_mlp_one<KD, CG, BN, 0, 0, MlpEpi::GATED>(a);
+    }
     switch (a.op) {
-    case MlpOp::LINEAR: return launch_mlp_one<KD, CG, BN, 0, 0, MlpEpi::LINEAR>(a);
-    case MlpOp::GATED: return launch_mlp_one<KD, CG, BN, 0, 0, MlpEpi::GATED>(a);
     case MlpOp::DGRAD: return launch_mlp_one<KD, CG, BN, 0, 1, MlpEpi::PLAIN>(a);
     case MlpOp::WGRAD: return launch_mlp_one<KD, CG, BN, 1, 1, MlpEpi::PLAIN>(a);
+    default: break;
     }
     return cudaErrorInvalidValue;
 }
 
 template <Kind KD, int CG>
 static cudaError_t launch_mlp_kind(const MlpLaunch &a) {
-    if (a.block_n == 256) return launch_mlp_bn<KD, CG, 256>(a);
-    if constexpr (CG == 1) return launch_mlp_bn<KD, 1, 128>(a);
-    return cudaErrorInvalidValue;  // (pairs: 256 columns only)
+    return a.block_n == 256 ? launch_mlp_bn<KD, CG, 256>(a) : launch_mlp_bn<KD, CG, 128>(a);
 }
 
 template <Kind KD, int NT, StreamOp OP>

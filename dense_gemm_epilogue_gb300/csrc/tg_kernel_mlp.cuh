@@ -264,7 +264,7 @@ struct MlpConfig {
                                       ((uint32_t)(TILE_M >> 4) << 24);
     static_assert(T::mma == MmaKind::F16, "16-bit kinds");
     static_assert(SMEM_BYTES <= SMEM_LIMIT, "shared memory budget");
-    static_assert(BN == 256 || (BN == 128 && CG == 1), "tile shapes");
+    static_assert(BN == 256 || (BN == 128 && (CG == 1 || EP == MlpEpi::PLAIN)), "tile shapes");
 };
 
 // Byte `b` of row `r` of a staging buffer: 64-byte rows with TMA's 64-byte

@@ -352,14 +352,17 @@ struct TilePlan {
 // its epilogue adds where nothing overlaps it; and what joining s segments adds
 // to a split tile (FP32 partial sums written, then s - 1 of them read back).
 // The 128-column tiles move 3/4 of the bytes per K block for half the work, so
-// they pay only where they fill SMs that 256-column tiles leave idle.  (256 x 128
-// pair tiles took 0.286 us a K block, what two 128 x 128 CTAs on the same two SMs
-// take for the same work, so they were never the cheapest and are not built.)
+// they pay only where they fill SMs that 256-column tiles leave idle.  A 256 x 128
+// pair tile takes what two 128 x 128 CTAs on the same two SMs take for the same
+// work, so it is never the cheapest alone; but it leaves whole twos of SMs to a
+// second product in pairs beside it (both gradients of 777 x 1001 x 1365: 32.5 us
+// with it, 33.3 with single CTAs for both), so the gradients have it.
 struct TileCost {
     int cg, bn;
     double block, epilogue, join, join_part;
 };
 constexpr TileCost kTiles[] = {{2, 256, 0.350, 4.5, 5.0, 3.0},
+                               {2, 128, 0.286, 2.0, 3.0, 1.2},
                                {1, 256, 0.395, 4.5, 5.0, 3.0},
                                {1, 128, 0.283, 2.0, 3.0, 1.2}};
 constexpr int kSplitMax = SPLIT_PARTS + 1;
@@ -377,6 +380,7 @@ TilePlan plan_tiles(const Product &q, int sms, int shape = -1) {
     for (int i = 0; i < (int)(sizeof(kTiles) / sizeof(kTiles[0])); ++i) {
         if (shape >= 0 && i != shape) continue;
         const TileCost &tc = kTiles[i];
+        if (tc.cg == 2 && tc.bn == 128 && q.op != MlpOp::DGRAD && q.op != MlpOp::WGRAD) continue;
         const int64_t teams = sms / tc.cg > 0 ? sms / tc.cg : 1;
         const int64_t mb = div_up(q.m, 128 * tc.cg), nb = div_up(q.n, dual ? tc.bn / 2 : tc.bn);
         const int64_t tiles = q.entries * mb * nb;
@@ -411,8 +415,8 @@ TilePlan plan_tiles(const Product &q, int sms, int shape = -1) {
 
 // Plans for an input gradient `x` and the weight gradient `w` after it, when
 // both fit the SMs together and running side by side is cheaper than in turn
-// (777 x 1001 x 1365: 128 x 256 tiles, 42 and 48 CTAs at once, against 77 and 88
-// CTAs of 128 x 128 tiles one after the other).
+// (777 x 1000 x 1368: 44 pairs of 256 x 128 tiles and 24 of 256 x 256 at once 22.2
+// us, one after the other 25.1; 3 x 1628 x 256, streaming, 12.5 and 15.6).
 struct Beside {
     bool on = false;
     TilePlan x, w;

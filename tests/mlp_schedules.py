@@ -46,7 +46,7 @@ SCHEDULES = [
     ("linear_dx", 1034, 2928, 4288, "pair 256x256", "waves", True),
     ("linear_dx", 5149, 72, 5176, "pair 256x256", "waves", False),
     ("linear_dx", 129, 3488, 64, "single 128x128", "under", True),
-    ("linear_dx", 129, 64, 64, "single 128x128", "under", False),
+    ("linear_dx", 133, 129, 64, "single 128x128", "under", False),
     ("linear_dx", 6936, 64, 264, "single 128x128", "waves", False),
     ("linear_dx", 7187, 1208, 3976, "single 128x256", "ticket", False),
     ("linear_dx", 266, 7348, 3371, "single 128x256", "under", True),
@@ -60,7 +60,7 @@ SCHEDULES = [
     ("gated_dx", 7767, 1528, 600, "pair 256x256", "waves", True),
     ("gated_dx", 2704, 72, 4448, "pair 256x256", "waves", False),
     ("gated_dx", 140, 1552, 64, "single 128x128", "under", True),
-    ("gated_dx", 142, 64, 64, "single 128x128", "under", False),
+    ("gated_dx", 133, 72, 64, "single 128x128", "under", False),
     ("gated_dx", 6624, 64, 312, "single 128x128", "waves", False),
     ("gated_dx", 7526, 456, 4504, "single 128x256", "ticket", False),
     ("gated_dx", 266, 2872, 3232, "single 128x256", "under", True),
@@ -97,6 +97,10 @@ SCHEDULES = [
     ("gated_dw", 164, 69, 5058, "single 128x256", "under", False),
     ("gated_dw", 4166, 296, 7696, "single 128x256", "waves", True),
     ("gated_dw", 154, 1304, 8584, "single 128x256", "waves", False),
+    ("gated_dw", 129, 66, 66, "pair 256x128", "under", False),
+    ("gated_dx", 142, 64, 64, "pair 256x128", "under", False),
+    ("linear_dw", 137, 197, 83, "pair 256x128", "under", False),
+    ("linear_dx", 129, 64, 64, "pair 256x128", "under", False),
 ]
 
 ROW = re.compile(r"((?:pair|single) \d+x\d+) tiles=(\d+) k_blocks=\d+ grid=\d+ raster=\d+ "
