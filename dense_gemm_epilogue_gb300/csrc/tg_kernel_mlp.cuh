@@ -213,10 +213,11 @@ struct MlpParams {
     int32_t late_wait;
     // What makes the kernels before that one visible to it (NULL: neither side).
     // The input gradient raises the gate (a release) once its own wait has
-    // returned, and only then lets its successor start; the weight gradient's
-    // producers acquire it before their first load.  A gate found down, which
-    // that order rules out, costs them the wait itself.  The weight gradient
-    // takes the gate down again, after its wait.
+    // returned, and only then lets its successor start; a thread of each of the
+    // weight gradient's CTAs acquires it while the others set the CTA up.  A gate
+    // found down, which that order all but rules out (the first CTA takes it down
+    // after its wait, when a late one may still be starting), costs the producer
+    // the wait itself.
     uint32_t *gate;
     MlpOut out[3];            // LINEAR: Y, Z; GATED: H, G, U; PLAIN: one per entry
 };
@@ -353,6 +354,7 @@ __global__ void __launch_bounds__(MlpConfig<KD, CG, BN, AM, BM, EP>::NUM_THREADS
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::MISC_OFF);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::MISC_OFF + 4);
     volatile int *fin_ready = reinterpret_cast<volatile int *>(smem + C::MISC_OFF + 8);
+    volatile uint32_t *gate_seen = reinterpret_cast<volatile uint32_t *>(smem + C::MISC_OFF + 12);
     const PairWaitCtl ctl{abort_flag, map_shared_rank(smem_u32(smem + C::MISC_OFF + 4), rank ^ (CG - 1u)),
                           p.status, p.wait_limit_ns};
     const int nkb = p.num_k_blocks;
@@ -389,6 +391,10 @@ __global__ void __launch_bounds__(MlpConfig<KD, CG, BN, AM, BM, EP>::NUM_THREADS
             tmem_relinquish();
         }
     }
+    if (mp.late_wait && threadIdx.x == 64) {
+        *gate_seen = ld_acquire_gpu_u32(mp.gate);
+        fence_proxy_async();  // TMA's reads after it (the barrier below passes that on)
+    }
     tc_fence_before();
     if constexpr (CG == 2) cluster_sync_all();
     else __syncthreads();
@@ -398,11 +404,9 @@ __global__ void __launch_bounds__(MlpConfig<KD, CG, BN, AM, BM, EP>::NUM_THREADS
         if (!mp.late_wait) griddep_wait();
     };
     // The same for a producer, whose loads everything else follows (through the
-    // stage barriers): with late_wait it acquires the gate.  The fence orders
-    // TMA's reads after it.
+    // stage barriers): with late_wait the gate, acquired above, stands for it.
     auto wait_inputs = [&] {
-        if (mp.late_wait && ld_acquire_gpu_u32(mp.gate) != 0u) fence_proxy_async();
-        else griddep_wait();
+        if (!mp.late_wait || *gate_seen == 0u) griddep_wait();
     };
     // The next kernel may be set up beside this one from here on; an input
     // gradient holds it back until its own wait (see late_wait, gate).
@@ -912,7 +916,7 @@ __global__ void __launch_bounds__(MlpConfig<KD, CG, BN, AM, BM, EP>::NUM_THREADS
 
     if (mp.late_wait) {
         griddep_wait();
-        if (blockIdx.x == 0 && threadIdx.x == 0) st_release_gpu_u32(mp.gate, 0u);
+        if (blockIdx.x == 0 && threadIdx.x == 0) *reinterpret_cast<volatile uint32_t *>(mp.gate) = 0u;
     }
     tc_fence_before();
     if constexpr (CG == 2) cluster_sync_all();
