@@ -34,16 +34,19 @@
 //             which clips at the rows' and columns' end.  The residual comes in
 //             through the same buffers by TMA, the first box before the
 //             accumulator is ready and each next one while the last is in work.
-//             Against plain 16-byte stores from a single staged box: 2048 x 4096 x
-//             1024 with GELU and residual 24.6 us, 26.6; gated 333 x 5640 x 2048
-//             18.4, 19.4; 1111 x 8200 x 2056 with GELU and saved Z 47.8, 50.0;
-//             without an activation no difference.  Rows that are not 16-byte
+//             Against plain 16-byte stores from a single staged box (calls back
+//             to back on the same inputs): 1111 x 8200 x 2056 with GELU and saved
+//             Z 41.7 us, 43.7; gated 333 x 5640 x 2048 19.3, 20.1; gated 8192 x
+//             14336 x 4096 with G and U 1172, 1187; without an activation no
+//             difference.  Rows that are not 16-byte
 //             aligned, and boxes that end inside 16 bytes (there a TMA store
 //             wrote into the row's padding), go through the same buffers with
 //             4-byte stores.
 //
 // Bound: tensor throughput for token counts above about 300 (arithmetic
-// intensity 256 x 256 / (256 + 256) = 128 FLOP per byte of L2 traffic).
+// intensity 256 x 256 / (256 + 256) = 128 FLOP per byte of L2 traffic).  8192 x
+// 4096 x 14336 with bias and residual: 573 us in a chain of launches, 1.68 PFLOP/s,
+// 593 us in a long run at the power limit (1.62; cuBLAS sustains 1.71 there).
 #pragma once
 
 #include <cstdint>

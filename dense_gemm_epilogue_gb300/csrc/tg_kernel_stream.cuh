@@ -12,8 +12,9 @@
 // TB/s at about 1 us of latency needs 44 KB per SM.  With the small ring the next
 // kernel's CTA fits beside this one: its set-up and, for short shares, an L2
 // prefetch of its first weights run under this kernel's end.  What a call costs
-// above its bytes is about 5 us of start, join and end; in between the weights
-// arrive at 6.5 TB/s.
+// above its bytes is about 5.5 us of start, join and end; in between the weights
+// arrive at 6.6 TB/s (1 x 4096 x 4096 10.7 us, 1 x 16384 x 4096 25.8; these and the
+// times below are of a captured chain of calls, inputs past L2).
 //
 // Work split: the (tile, K block) iterations of all 128-feature tiles are cut
 // into equal contiguous shares, one per CTA, so that 112 tiles (say) load 152
@@ -50,15 +51,16 @@ struct StreamConfig {
     static constexpr int B_BYTES = NT * ROW_BYTES;
     static constexpr int STAGE_BYTES = MATS * A_BYTES + B_BYTES;
     // One weight matrix and up to 32 tokens: a ring of about 100 KB, two CTAs to
-    // an SM (1 x 4096 x 4096 10.1 us, 10.4 with all of shared memory); else all of
-    // it (gated, 4 x 14336 x 4096: 40.9 us, 42.9 with half).
+    // an SM (1 x 4096 x 4096 10.7 us, 11.0 with all of shared memory; 1 x 16384 x
+    // 4096 25.8, 27.2); else all of it (gated, 4 x 14336 x 4096: 42.2 us either way,
+    // and more tokens leave a half ring too few stages).
     static constexpr bool SMALL = NT <= 32 && !DUAL;
     static constexpr int BUDGET = SMALL ? SMEM_LIMIT / 2 - 1024 : SMEM_LIMIT;
     static constexpr int FIT = (BUDGET - 2048) / STAGE_BYTES;
     static constexpr int STAGES = FIT > 12 ? 12 : FIT;
     // K blocks prefetched into L2 ahead of the first load (256 KB a CTA), and the
-    // longest share that this pays for: 1 x 4096 x 4096 (13 blocks a CTA) 10.1 us
-    // with it and 10.8 without, 1 x 16384 x 4096 (54) 26.6 and 25.9.
+    // longest share that this pays for: 1 x 4096 x 4096 (13 blocks a CTA) 10.7 us
+    // with it and 11.0 without, 1 x 16384 x 4096 (54) 27.0 and 25.8.
     static constexpr int PREFETCH = 16 / MATS, PREFETCH_SHARE = 32;
     static constexpr int BAR_OFF = STAGES * STAGE_BYTES;
     static constexpr int FULL0 = 0, EMPTY0 = STAGES, ACCF0 = 2 * STAGES, ACCE0 = ACCF0 + 2,

@@ -22,6 +22,14 @@
 // step through one reduction, and a thread holds 16 elements, over which a
 // reduction's shuffles spread.
 //
+// Measured (a captured chain of calls, inputs past L2; the copy rate is 6.79 TB/s):
+//   16384 x 4096 BF16        forward 42.4 us, 6.3 TB/s; backward 73.8 us, 5.5 TB/s
+//   4096 x 16384 BF16        forward 89 us, 3.0 TB/s; backward 119 us, 3.4 TB/s: a
+//                            cluster's barriers stand between the steps
+//   8 x 4096 BF16            forward 3.1 us: two dependent reductions after a launch
+//   4099 x 1001, odd rows    backward FP32 17.6 us, BF16 17.1 us; 16384 x 4097 BF16
+//                            forward 155 us: 4-byte copies, single 16-bit loads
+//
 // Backward keeps each thread's columns fixed over all rows of its group, so
 // the column sums dgamma and dbeta accumulate in registers; the block's groups
 // add theirs in shared memory in order, and tg_colsum_finish_kernel adds the

@@ -416,6 +416,11 @@ tg_status tg_gemm_mx_batched(int64_t M, int64_t N, int64_t K, float alpha,
  * allocation synchronises the device, so make one call of each operator on
  * the stream before capturing it).
  *
+ * Which call: tg_gemm_epilogue with W as A and X as B also gives act(X W^T +
+ * bias) in this layout (its column-major D has a token per column).  It is the
+ * call for other operand types, alpha, FP32 outputs or chains of ops; tg_linear
+ * is the one for a residual, a kept pre-activation, few tokens or gradients.
+ *
  * Ownership, asynchrony and errors are tg_gemm's: everything is enqueued on
  * `stream`, arguments are checked before anything is launched, and repeated
  * calls give bitwise identical results.  An output may not overlap an input
