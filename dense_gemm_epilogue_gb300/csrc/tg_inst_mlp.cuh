@@ -100,9 +100,10 @@ static cudaError_t launch_stream_nt(const StreamLaunch &a) {
     switch (a.nt) {
     case 16: return launch_stream_one<KD, 16, OP>(a);
     case 32: return launch_stream_one<KD, 32, OP>(a);
-    case 64: return launch_stream_one<KD, 64, OP>(a);
-    default: return launch_stream_one<KD, 128, OP>(a);
+    default: break;
     }
+    if constexpr (OP != StreamOp::GATED) return launch_stream_one<KD, 64, OP>(a);
+    return cudaErrorInvalidValue;  // (gated: up to 32 tokens)
 }
 
 template <Kind KD>

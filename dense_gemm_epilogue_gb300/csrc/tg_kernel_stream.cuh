@@ -5,8 +5,8 @@
 //
 // With few tokens a product reads N K weights for 2 M N K operations, so the
 // weights' bytes bound it (M = 1: 1 FLOP a byte).  Here the weights are the
-// 128-row operand and the tokens the NT-column one (NT = 16, 32, 64 or 128,
-// zero rows beyond the tokens), so every weight byte crosses shared memory
+// 128-row operand and the tokens the NT-column one (NT = 16, 32 or, not gated,
+// 64, zero rows beyond the tokens), so every weight byte crosses shared memory
 // once and the accumulator wastes columns, which cost nothing, instead of
 // rows.  One CTA per SM keeps a ring of 100 or 200 KB of TMA loads in flight: 6.7
 // TB/s at about 1 us of latency needs 44 KB per SM.  With the small ring the next
@@ -52,8 +52,7 @@ struct StreamConfig {
     static constexpr int STAGE_BYTES = MATS * A_BYTES + B_BYTES;
     // One weight matrix and up to 32 tokens: a ring of about 100 KB, two CTAs to
     // an SM (1 x 4096 x 4096 10.7 us, 11.0 with all of shared memory; 1 x 16384 x
-    // 4096 25.8, 27.2); else all of it (gated, 4 x 14336 x 4096: 42.2 us either way,
-    // and more tokens leave a half ring too few stages).
+    // 4096 25.8, 27.2); else all of it (gated, 4 x 14336 x 4096: 42.2 us either way).
     static constexpr bool SMALL = NT <= 32 && !DUAL;
     static constexpr int BUDGET = SMALL ? SMEM_LIMIT / 2 - 1024 : SMEM_LIMIT;
     static constexpr int FIT = (BUDGET - 2048) / STAGE_BYTES;

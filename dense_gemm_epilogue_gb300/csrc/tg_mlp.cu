@@ -426,10 +426,23 @@ struct Beside {
 
 tg_status run_stream(const Product &q, tg_dtype t, const Device &dev, cudaStream_t stream);
 
-// The weight-streaming kernel takes up to this many tokens: its token operand
-// is one MMA's columns, re-read by every weight tile from L2 (16 KB per 16 KB
-// of weights at 128 tokens); beyond, 128- and 256-row token tiles waste less.
-constexpr int64_t kStreamTokens = 128;
+// The weight-streaming kernel takes up to 64 tokens, gated 32.  Every weight tile
+// reads them again from L2, and the join's traffic grows with them (twice as much
+// for the gated unit's two products), while a 128-row token tile costs the same for
+// any count.  Streaming and tiles in us, a captured chain of calls, inputs past L2:
+//               N x K             32 tokens     64 tokens     96 tokens
+//   linear      4096 x 4096       12.2  16.8    14.9  16.9    17.5  17.3
+//               4096 x 14336      26.9  30.6    29.7  30.8    32.8  31.4
+//   dX          4096 x 4096       13.8  15.2    14.5  15.3    16.9  15.5
+//               14336 x 4096      25.4  27.6    29.1  27.7    31.8  28.2
+//   gated       4096 x 4096       18.1  20.1    22.4  20.4    26.2  20.4
+//               1024 x 4096       14.1  14.4    18.0  14.4    22.0  14.7
+//               14336 x 4096      45.4  43.0    48.2  43.0    52.2  43.0
+//   gated dX    4096 x 4096       25.0  24.6    26.5  25.4    28.5  25.9
+//               1024 x 4096       14.5  16.8    15.6  16.9    17.7  17.2
+bool streams(const Product &q) {
+    return q.m <= (q.op == MlpOp::GATED ? 32 : 64) && q.op != MlpOp::WGRAD && q.k[0] > 0;
+}
 
 // Whether `w`'s CTAs find room while all of `x`'s run.  A CTA pair needs both SMs
 // of a neighbouring two, and single CTAs before it are spread over as many such
@@ -442,7 +455,7 @@ bool fit_beside(const TilePlan &x, const TilePlan &w, int sms) {
 
 Beside plan_beside(const Product &x, const Product &w, int sms) {
     Beside best;
-    if (x.m <= kStreamTokens || x.k[0] == 0 || w.k[0] == 0) return best;
+    if (streams(x) || x.k[0] == 0 || w.k[0] == 0) return best;
     double t = plan_tiles(x, sms).time + plan_tiles(w, sms).time;
     constexpr int SHAPES = sizeof(kTiles) / sizeof(kTiles[0]);
     for (int i = 0; i < SHAPES; ++i)
@@ -457,8 +470,6 @@ Beside plan_beside(const Product &x, const Product &w, int sms) {
         }
     return best;
 }
-
-bool streams(const Product &q) { return q.op != MlpOp::WGRAD && q.m <= kStreamTokens && q.k[0] > 0; }
 
 tg_status run_product(const Product &q, tg_dtype t, const Device &dev, cudaStream_t stream,
                       const TilePlan *chosen = nullptr) {
@@ -534,9 +545,9 @@ tg_status run_product(const Product &q, tg_dtype t, const Device &dev, cudaStrea
 }
 
 // K blocks a CTA's share spans at least: below that the join, whose reads grow
-// with the tokens, costs more than the loads it spreads (68 x 1216 x 2560: 14.9
-// us at 4 blocks).
-int64_t stream_min_blocks(int nt) { return nt <= 16 ? 4 : nt <= 32 ? 6 : nt <= 64 ? 8 : 12; }
+// with the tokens, costs more than the loads it spreads (60 x 1216 x 2560: 11.0
+// us, 12.4 at 4 blocks; 30 tokens 9.8, 10.0).
+int64_t stream_min_blocks(int nt) { return nt <= 16 ? 4 : nt <= 32 ? 6 : 8; }
 
 struct StreamPlan {
     int nt;  // token columns of the MMA
@@ -545,7 +556,7 @@ struct StreamPlan {
 };
 StreamPlan plan_stream(const Product &q, int sms) {
     StreamPlan s;
-    s.nt = q.m <= 16 ? 16 : q.m <= 32 ? 32 : q.m <= 64 ? 64 : 128;
+    s.nt = q.m <= 16 ? 16 : q.m <= 32 ? 32 : 64;
     s.tiles = div_up(q.n, BLOCK_M);
     s.k_blocks = div_up(q.k[0], 64) + div_up(q.k[1], 64);
     int64_t grid = s.tiles * s.k_blocks / stream_min_blocks(s.nt);

@@ -531,8 +531,9 @@ tg_status tg_layer_norm_backward(int64_t M, int64_t N, const void *dY, int64_t l
  * The planner's choice for one product of these operators, as one line of
  * text (host only when num_sms > 0; num_sms <= 0 queries the current device):
  * a forward product, or dX or dW of the backward call with both asked for.
- *   "stream 128x16 tiles=112 k_blocks=64 grid=152": up to 128 tokens, the
- *       weights streamed through 128-row tiles by `grid` CTAs of equal shares;
+ *   "stream 128x16 tiles=112 k_blocks=64 grid=152": up to 64 tokens (gated
+ *       forward 32), the weights streamed through 128-row tiles by `grid` CTAs
+ *       of equal shares;
  *   "pair 256x256 tiles=561 k_blocks=17 grid=152 raster=12 split=0x1
  *       schedule=ticket beside=0" (one line): tiles of CTA pairs (or "single"
  *       CTAs) by the accumulator's rows and columns; the last split tiles cut

@@ -26,7 +26,7 @@ def tg():
 def test_text(tg):
     d = tg.tg_product_plan_describe
     assert d("gated", 4, 14336, 4096, SMS) == "stream 128x16 tiles=112 k_blocks=64 grid=152"
-    assert d("linear_dx", 100, 8, 300, SMS) == "stream 128x128 tiles=3 k_blocks=1 grid=1"
+    assert d("linear_dx", 50, 8, 300, SMS) == "stream 128x64 tiles=3 k_blocks=1 grid=1"
     assert d("linear", 4097, 8200, 1032, SMS) == (
         "pair 256x256 tiles=561 k_blocks=17 grid=152 raster=12 split=0x1 schedule=ticket beside=0")
     assert d("linear", 0, 8, 8, SMS) == d("linear_dx", 8, 8, 0, SMS) == "empty"
@@ -48,11 +48,11 @@ def test_refusals(tg):
         tg.tg_product_plan_describe("product", 8, 8, 8, SMS)
 
 
-def test_streaming_ends_at_128_tokens(tg):
+def test_streaming_ends_at_32_or_64_tokens(tg):
     d = tg.tg_product_plan_describe
-    for p in ("linear", "gated", "linear_dx", "gated_dx"):
-        assert d(p, 128, 264, 520, SMS).startswith("stream ")
-        assert not d(p, 129, 264, 520, SMS).startswith("stream ")
+    for p, most in (("linear", 64), ("gated", 32), ("linear_dx", 64), ("gated_dx", 64)):
+        assert d(p, most, 264, 520, SMS).startswith("stream ")
+        assert not d(p, most + 1, 264, 520, SMS).startswith("stream ")
     for p in ("linear_dw", "gated_dw"):
         assert not d(p, 3, 264, 520, SMS).startswith("stream ")
 
