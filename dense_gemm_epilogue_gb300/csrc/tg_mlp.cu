@@ -353,7 +353,9 @@ struct TilePlan {
 // short products of each tile shape: one 64-deep K block of a team's tile; what
 // its epilogue adds where nothing overlaps it; and what joining s segments adds
 // to a split tile (FP32 partial sums written, then s - 1 of them read back).
-// The 128-column tiles move 3/4 of the bytes per K block for half the work, so
+// (One wave of tiles, 2048 and 8192 deep, inputs past L2: 0.29, 0.28, 0.38 and 0.28 a
+// K block on the present build; the first takes 0.36 in long products, at the power
+// limit.)  The 128-column tiles move 3/4 of the bytes per K block for half the work, so
 // they pay only where they fill SMs that 256-column tiles leave idle.  A 256 x 128
 // pair tile takes what two 128 x 128 CTAs on the same two SMs take for the same
 // work, so it is never the cheapest alone; but it leaves whole twos of SMs to a
@@ -417,8 +419,8 @@ TilePlan plan_tiles(const Product &q, int sms, int shape = -1) {
 
 // Plans for an input gradient `x` and the weight gradient `w` after it, when
 // both fit the SMs together and running side by side is cheaper than in turn
-// (777 x 1000 x 1368: 44 pairs of 256 x 128 tiles and 24 of 256 x 256 at once 22.2
-// us, one after the other 25.1; 3 x 1628 x 256, streaming, 12.5 and 15.6).
+// (777 x 1000 x 1368: 44 pairs of 256 x 128 tiles and 24 of 256 x 256 at once 21.5
+// us, one after the other 25.1; 3 x 1628 x 256, streaming, 12.2 and 15.6).
 struct Beside {
     bool on = false;
     TilePlan x, w;
