@@ -909,6 +909,20 @@ tg_status scratch(const Device &dev, cudaStream_t stream, int64_t tiles, Scratch
     return TG_OK;
 }
 
+bool scratch_blocked(const Device &dev, cudaStream_t stream, int64_t tiles) {
+    {
+        std::lock_guard<std::mutex> lock(g_ws_mutex);
+        for (const Workspace &w : g_ws)
+            if (w.device == dev.id && w.stream == stream && w.tiles >= tiles) return false;
+    }
+    cudaStreamCaptureStatus c = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(stream, &c) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return true;
+    }
+    return c != cudaStreamCaptureStatusNone;
+}
+
 bool encode_rows(CUtensorMap *map, tg_out_dtype t, const void *base, int64_t rows, int64_t cols,
                  int64_t ld, int box_rows, int row_bytes) {
     EncodeTiledFn fn = encode_fn();

@@ -34,6 +34,9 @@ struct Scratch {
 };
 constexpr int64_t kStreamFlags = 8 * 512;
 tg_status scratch(const Device &dev, cudaStream_t stream, int64_t tiles, Scratch *out);
+// Whether scratch() would have to allocate while the stream is being captured,
+// which spoils the capture.
+bool scratch_blocked(const Device &dev, cudaStream_t stream, int64_t tiles);
 
 // 2-D tensor map of a row-major matrix of 2- or 4-byte elements: box of
 // row_bytes (128 or 64, with the swizzle of that width) x box_rows, zero fill.

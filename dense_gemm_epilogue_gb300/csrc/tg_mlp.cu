@@ -626,9 +626,12 @@ tg_status run_gradients(Product *x, Product *w, tg_dtype t, const Device &dev, c
     if (w) {
         if (x) both = plan_beside(*x, *w, dev.sms);
         wp = both.on ? both.w : plan_tiles(*w, dev.sms);
-        if (x && runs_beside(wp)) {
+        // (a captured stream that has no workspace yet goes without the gate: the
+        // weight gradient then waits its turn)
+        const int64_t room = div_up(dev.sms, 2);
+        if (x && runs_beside(wp) && !host::scratch_blocked(dev, stream, room)) {
             host::Scratch s;
-            const tg_status st = host::scratch(dev, stream, div_up(dev.sms, 2), &s);
+            const tg_status st = host::scratch(dev, stream, room, &s);
             if (st != TG_OK) return st;
             x->gate = w->gate = s.gate;
         }

@@ -136,6 +136,27 @@ def test_graph_replays_the_whole_backward(tg):
         assert all(m.padding_kept() for m in (y, b.z, b.dx, b.dw))
 
 
+def test_capture_on_a_stream_without_a_workspace(tg):
+    """A backward call that splits no tile needs no library workspace: it can be
+    captured on a stream that has made no call before (its kernels have run
+    elsewhere), as graph helpers with a stream of their own do."""
+    b = Backward(tg, 200, 264, 136, "bf16")
+    for p in ("linear_dx", "linear_dw"):
+        assert " split=0x1 schedule=static " in tg.tg_product_plan_describe(p, 200, 264, 136)
+    b.run()
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream(priority=-1)  # (of a pool that no other test takes from)
+    s.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        b.run(s)
+    for _ in range(2):
+        b.poison()
+        graph.replay()
+        torch.cuda.synchronize()
+        b.check("captured on a fresh stream")
+
+
 class StreamWork:
     """Calls of one host thread on a stream of its own (torch's current stream is
     the thread's, so each method enters it)."""
