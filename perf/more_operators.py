@@ -423,7 +423,7 @@ def _framework_rotary(state):
     st = torch.cuda.current_stream()
     if case["op"] == "rotary":
         tg.check(tg.tg_rotary(case["tokens"], case["heads"], case["dim"], case["rot"], *_lay(i["X"]),
-                              *_lay(y), i["positions"], None, state["steps"], case["layout"],
+                              *_lay(y), 0, i["positions"], None, state["steps"], case["layout"],
                               AMPLITUDE[case["scaling"]], case["dtype"], st))
     else:
         tg.check(tg.tg_rotary_backward(case["tokens"], case["heads"], case["dim"], case["rot"],
