@@ -62,6 +62,16 @@ PRODUCT_CODES = {"linear": TG_PRODUCT_LINEAR, "gated": TG_PRODUCT_GATED,
                  "linear_dx": TG_PRODUCT_LINEAR_DX, "gated_dx": TG_PRODUCT_GATED_DX,
                  "linear_dw": TG_PRODUCT_LINEAR_DW, "gated_dw": TG_PRODUCT_GATED_DW}
 
+TG_ROTARY_HALVES = 0
+TG_ROTARY_PAIRS = 1
+ROTARY_LAYOUTS = {"halves": TG_ROTARY_HALVES, "pairs": TG_ROTARY_PAIRS}
+TG_ROTARY_NONE = 0
+TG_ROTARY_LINEAR = 1
+TG_ROTARY_BASE = 2
+TG_ROTARY_BANDS = 3
+ROTARY_SCALINGS = {"none": TG_ROTARY_NONE, "linear": TG_ROTARY_LINEAR, "base": TG_ROTARY_BASE,
+                   "bands": TG_ROTARY_BANDS}
+
 OUT_CODES = {"f32": TG_OUT_F32, "bf16": TG_OUT_BF16, "fp16": TG_OUT_F16}
 
 # Every symbol include/tg_gemm.h declares.
@@ -97,6 +107,11 @@ EXPORTED = (
     "tg_layer_norm_backward_workspace_bytes",
     "tg_layer_norm_backward",
     "tg_product_plan_describe",
+    "tg_rotary_steps",
+    "tg_rotary",
+    "tg_rotary_backward",
+    "tg_attention_workspace_bytes",
+    "tg_attention",
 )
 
 
@@ -289,6 +304,21 @@ def load(path: str | None = None) -> ctypes.CDLL:
         lib.tg_product_plan_describe.argtypes = [c, i64, i64, i64, i32, ctypes.c_char_p,
                                                  ctypes.c_size_t]
         lib.tg_product_plan_describe.restype = c
+        f64 = ctypes.c_double
+        lib.tg_rotary_steps.argtypes = [i64, f64, c, f64, f64, f64, f64,
+                                        ctypes.POINTER(ctypes.c_uint64)]
+        lib.tg_rotary_steps.restype = c
+        lib.tg_rotary.argtypes = [i64, i64, i64, i64, vp, i64, i64, vp, i64, i64, i64, vp, vp, vp, c,
+                                  f32, c, vp]
+        lib.tg_rotary.restype = c
+        lib.tg_rotary_backward.argtypes = [i64, i64, i64, i64, vp, i64, i64, vp, i64, i64, vp, vp, c,
+                                           f32, c, vp]
+        lib.tg_rotary_backward.restype = c
+        lib.tg_attention_workspace_bytes.argtypes = [i64] * 8 + [c]
+        lib.tg_attention_workspace_bytes.restype = i64
+        lib.tg_attention.argtypes = ([i64] * 6 + [vp, i64, i64] * 3 + [vp] * 4 + [i64, i64, i32, f32]
+                                     + [vp, i64, i64, vp, c, vp, i64, vp])
+        lib.tg_attention.restype = c
         lib.tg_version.argtypes = []
         lib.tg_version.restype = i32
         if path is None:
@@ -584,6 +614,54 @@ def tg_layer_norm_backward(M, N, dY, lddy, X, ldx, gamma, mean, rstd, dX, lddx, 
     return load().tg_layer_norm_backward(M, N, _ptr(dY), lddy, _ptr(X), ldx, _ptr(gamma),
                                          _ptr(mean), _ptr(rstd), _ptr(dX), lddx, _ptr(dgamma),
                                          _ptr(dbeta), _out(dtype), ws, n, _stream(stream))
+
+
+def tg_rotary_steps(rot, base, scaling="none", factor=1.0, low=1.0, high=4.0, original=8192.0):
+    """Frequencies as 64-bit fractions of a turn a position, in a list of rot/2 integers as int64
+    holds them (a tensor of them on the device is what tg_rotary reads); raises TgError on invalid
+    arguments.  scaling is a name of ROTARY_SCALINGS."""
+    out = (ctypes.c_uint64 * max(int(rot) // 2, 1))()
+    code = ROTARY_SCALINGS[scaling] if isinstance(scaling, str) else int(scaling)
+    check(load().tg_rotary_steps(rot, base, code, factor, low, high, original, out), "tg_rotary_steps")
+    return [v - (1 << 64) if v >> 63 else v for v in out]
+
+
+def _rotary_layout(n):
+    return ROTARY_LAYOUTS[n] if isinstance(n, str) else int(n)
+
+
+def tg_rotary(tokens, heads, dim, rot, X, ldx, hx, Y, ldy, hy, y_rows, positions, rows, steps, layout,
+              amplitude, dtype, stream=None) -> int:
+    """Rotary positions on the first rot values of each head (rows of Y by `rows` when given);
+    positions and rows may be None; layout a name of ROTARY_LAYOUTS, dtype of OUT_CODES."""
+    return load().tg_rotary(tokens, heads, dim, rot, _ptr(X), ldx, hx, _ptr(Y), ldy, hy, y_rows,
+                            _ptr(positions), _ptr(rows), _ptr(steps), _rotary_layout(layout),
+                            amplitude, _out(dtype), _stream(stream))
+
+
+def tg_rotary_backward(tokens, heads, dim, rot, dY, lddy, hdy, dX, lddx, hdx, positions, steps, layout,
+                       amplitude, dtype, stream=None) -> int:
+    """The transposed map, from dY to dX (which may be dY)."""
+    return load().tg_rotary_backward(tokens, heads, dim, rot, _ptr(dY), lddy, hdy, _ptr(dX), lddx, hdx,
+                                     _ptr(positions), _ptr(steps), _rotary_layout(layout), amplitude,
+                                     _out(dtype), _stream(stream))
+
+
+def tg_attention_workspace_bytes(seqs, q_rows, k_rows, heads, kv_heads, dim, max_q, max_k, dtype) -> int:
+    return load().tg_attention_workspace_bytes(seqs, q_rows, k_rows, heads, kv_heads, dim, max_q, max_k,
+                                               _dtype(dtype))
+
+
+def tg_attention(seqs, q_rows, k_rows, heads, kv_heads, dim, Q, ldq, hq, K, ldk, hk, V, ldv, hv,
+                 q_starts, q_lengths, k_starts, k_lengths, max_q, max_k, causal, scale, O, ldo, ho, LSE,
+                 dtype, workspace=None, stream=None) -> int:
+    """O = softmax(scale Q K^T) V over packed sequences, and the rows' LSE; the lengths and LSE may be
+    None."""
+    ws, n = _space(workspace)
+    return load().tg_attention(seqs, q_rows, k_rows, heads, kv_heads, dim, _ptr(Q), ldq, hq, _ptr(K),
+                               ldk, hk, _ptr(V), ldv, hv, _ptr(q_starts), _ptr(q_lengths),
+                               _ptr(k_starts), _ptr(k_lengths), max_q, max_k, int(causal), scale,
+                               _ptr(O), ldo, ho, _ptr(LSE), _dtype(dtype), ws, n, _stream(stream))
 
 
 def tg_product_plan_describe(product, M, N, K, num_sms=0, size=256) -> str:

@@ -1,0 +1,235 @@
+// Attention over packed sequences: entry points, argument checks and planner
+// (kernels: tg_kernel_attn.cuh).
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <mutex>
+
+#include "../../include/tg_gemm.h"
+#include "tg_attn.h"
+#include "tg_host.h"
+
+namespace {
+
+using namespace tg;
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+constexpr int64_t kMaxRows = (int64_t)INT32_MAX - 512;
+constexpr double kLog2E = 1.4426950408889634;
+
+using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
+                                   const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
+                                   const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+    static EncodeTiledFn fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult qr;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                             &qr) == cudaSuccess &&
+            qr == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<EncodeTiledFn>(p);
+    });
+    return fn;
+}
+
+// A rows x heads x dim tensor of 16-bit values.
+struct Heads {
+    const void *ptr;
+    int64_t ld, hd;
+};
+
+bool heads_ok(const Heads &x, int64_t heads, int64_t dim) {
+    if (!x.ptr || (uintptr_t)x.ptr % 16) return false;
+    if (x.ld < dim || x.ld % 8 || x.ld >= ((int64_t)1 << 38)) return false;
+    return heads == 1 || (x.hd >= dim && x.hd % 8 == 0 && x.hd < ((int64_t)1 << 38) / heads);
+}
+
+// Tensor map (dim, group, heads / group, rows) of the query side, a box of 64 values x
+// group x 1 x box_rows; zeros outside.
+bool encode_query(CUtensorMap *map, tg_dtype t, const Heads &x, int64_t rows, int64_t heads,
+                  int64_t group, int64_t dim, int box_rows) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const int64_t hd = heads == 1 ? x.ld : x.hd;
+    cuuint64_t dims[4] = {(cuuint64_t)dim, (cuuint64_t)group, (cuuint64_t)(heads / group), (cuuint64_t)rows};
+    cuuint64_t strides[3] = {(cuuint64_t)(2 * hd), (cuuint64_t)(2 * hd * group), (cuuint64_t)(2 * x.ld)};
+    cuuint32_t box[4] = {64, (cuuint32_t)group, 1, (cuuint32_t)box_rows};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    return fn(map, t == TG_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+              const_cast<void *>(x.ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// Tensor map (dim, heads, rows) of keys or values, a box of 64 values x 1 x ATTN_KEYS.
+bool encode_keys(CUtensorMap *map, tg_dtype t, const Heads &x, int64_t rows, int64_t heads, int64_t dim) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const int64_t hd = heads == 1 ? x.ld : x.hd;
+    cuuint64_t dims[3] = {(cuuint64_t)dim, (cuuint64_t)heads, (cuuint64_t)rows};
+    cuuint64_t strides[2] = {(cuuint64_t)(2 * hd), (cuuint64_t)(2 * x.ld)};
+    cuuint32_t box[3] = {64, 1, ATTN_KEYS};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return fn(map, t == TG_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+              const_cast<void *>(x.ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The sizes that every call and workspace query takes.
+struct Sizes {
+    int64_t seqs, q_rows, k_rows, heads, kv_heads, dim, max_q, max_k;
+    tg_dtype dtype;
+};
+
+tg_status sizes_ok(const Sizes &z) {
+    if (z.seqs < 0 || z.q_rows < 0 || z.k_rows < 0 || z.max_q < 0 || z.max_k < 0) return TG_ERR_INVALID_VALUE;
+    if (z.seqs > INT32_MAX / 2 || z.q_rows > kMaxRows || z.k_rows > kMaxRows) return TG_ERR_INVALID_VALUE;
+    if (z.heads < 1 || z.kv_heads < 1 || z.heads % z.kv_heads || z.dim < 1) return TG_ERR_INVALID_VALUE;
+    if (z.heads > 65536) return TG_ERR_INVALID_VALUE;
+    if (z.dtype != TG_BF16 && z.dtype != TG_FP16) return TG_ERR_INVALID_VALUE;
+    if (z.dim % 8 || z.dim > ATTN_MAX_DIM || z.heads / z.kv_heads > ATTN_ROWS) return TG_ERR_UNSUPPORTED;
+    return TG_OK;
+}
+
+int64_t bound_of(int64_t given, int64_t rows) { return given == 0 || given > rows ? rows : given; }
+
+// Tiles of `per` rows that the sequences can have, at most.
+int64_t tile_bound(int64_t seqs, int64_t rows, int64_t longest, int64_t per) {
+    if (longest <= per) return seqs;
+    const int64_t a = seqs * ceil_div(longest, per), b = rows / per + seqs;
+    return a < b ? a : b;
+}
+
+struct ForwardPlan {
+    int nq;           // row tiles a CTA
+    int64_t tiles;    // of nq row tiles each
+    int64_t splits, chunk;
+    int64_t workspace;
+};
+
+// Two row tiles a CTA from more than one wave of single ones on, for sequences
+// that have a second tile.  Single tiles that leave SMs without work cut the
+// keys into ranges of at least four blocks.
+ForwardPlan plan_forward(const Sizes &z, int sms) {
+    ForwardPlan p = {};
+    const int64_t tokens = ATTN_ROWS / (z.heads / z.kv_heads);
+    const int64_t max_q = bound_of(z.max_q, z.q_rows), max_k = bound_of(z.max_k, z.k_rows);
+    const int64_t single = tile_bound(z.seqs, z.q_rows, max_q, tokens);
+    const int64_t blocks = ceil_div(max_k, ATTN_KEYS) > 0 ? ceil_div(max_k, ATTN_KEYS) : 1;
+    p.nq = max_q > tokens && single * z.kv_heads > sms ? 2 : 1;
+    p.tiles = p.nq == 2 ? tile_bound(z.seqs, z.q_rows, max_q, 2 * tokens) : single;
+    p.splits = 1;
+    if (p.nq == 1) {
+        const int64_t ctas = p.tiles * z.kv_heads, most = blocks / 4;
+        p.splits = 4 * (int64_t)sms / (ctas > 0 ? ctas : 1);
+        if (p.splits > most) p.splits = most;
+        if (p.splits < 1) p.splits = 1;
+    }
+    p.chunk = ceil_div(blocks, p.splits);
+    p.splits = ceil_div(blocks, p.chunk);
+    if (p.splits > 1) p.workspace = p.splits * z.heads * z.q_rows * (4 * z.dim + 8);
+    return p;
+}
+
+bool arrays_ok(const int64_t *qs, const int64_t *ql, const int64_t *ks, const int64_t *kl) {
+    return qs && ks && !(((uintptr_t)qs | (uintptr_t)ql | (uintptr_t)ks | (uintptr_t)kl) % 8);
+}
+bool f32_ok(const void *p) { return (uintptr_t)p % 4 == 0; }
+
+AttnHeads make_heads(const Sizes &z, float scale) {
+    AttnHeads h = {};
+    h.heads = (int32_t)z.heads;
+    h.kv_heads = (int32_t)z.kv_heads;
+    h.group = (int32_t)(z.heads / z.kv_heads);
+    h.tokens = ATTN_ROWS / h.group;
+    h.dim = (int32_t)z.dim;
+    h.scale = scale;
+    h.scale_log2 = (float)((double)scale * kLog2E);
+    return h;
+}
+
+AttnSeqs make_seqs(const Sizes &z, const int64_t *qs, const int64_t *ql, const int64_t *ks,
+                   const int64_t *kl, int32_t causal) {
+    AttnSeqs s = {};
+    s.q_starts = qs;
+    s.q_lengths = ql;
+    s.k_starts = ks;
+    s.k_lengths = kl;
+    s.seqs = (int32_t)z.seqs;
+    s.q_rows = (int32_t)z.q_rows;
+    s.k_rows = (int32_t)z.k_rows;
+    s.max_q = (int32_t)bound_of(z.max_q, z.q_rows);
+    s.max_k = (int32_t)bound_of(z.max_k, z.k_rows);
+    s.causal = causal;
+    return s;
+}
+
+bool scale_ok(float s) { return s > 0.0f && std::isfinite(s * (float)kLog2E); }
+
+}  // namespace
+
+extern "C" int64_t tg_attention_workspace_bytes(int64_t seqs, int64_t q_rows, int64_t k_rows,
+                                                int64_t heads, int64_t kv_heads, int64_t dim,
+                                                int64_t max_q, int64_t max_k, tg_dtype dtype) {
+    const Sizes z = {seqs, q_rows, k_rows, heads, kv_heads, dim, max_q, max_k, dtype};
+    if (sizes_ok(z) != TG_OK) return -1;
+    tg::host::Device dev;
+    if (tg::host::device(&dev) != TG_OK) return -1;
+    if (seqs == 0 || q_rows == 0) return 0;
+    return plan_forward(z, dev.sms).workspace;
+}
+
+extern "C" tg_status tg_attention(int64_t seqs, int64_t q_rows, int64_t k_rows, int64_t heads,
+                                  int64_t kv_heads, int64_t dim, const void *Q, int64_t ldq, int64_t hq,
+                                  const void *K, int64_t ldk, int64_t hk, const void *V, int64_t ldv,
+                                  int64_t hv, const int64_t *q_starts, const int64_t *q_lengths,
+                                  const int64_t *k_starts, const int64_t *k_lengths, int64_t max_q,
+                                  int64_t max_k, int32_t causal, float scale, void *O, int64_t ldo,
+                                  int64_t ho, float *LSE, tg_dtype dtype, void *workspace,
+                                  int64_t workspace_bytes, void *stream) {
+    const Sizes z = {seqs, q_rows, k_rows, heads, kv_heads, dim, max_q, max_k, dtype};
+    tg_status st = sizes_ok(z);
+    if (st != TG_OK) return st;
+    if (!scale_ok(scale) || (causal != 0 && causal != 1) || workspace_bytes < 0 || !f32_ok(LSE))
+        return TG_ERR_INVALID_VALUE;
+    if (seqs == 0 || q_rows == 0) return TG_OK;
+    const Heads q = {Q, ldq, hq}, k = {K, ldk, hk}, v = {V, ldv, hv}, o = {O, ldo, ho};
+    if (!heads_ok(q, heads, dim) || !heads_ok(o, heads, dim)) return TG_ERR_INVALID_VALUE;
+    if (k_rows > 0 && (!heads_ok(k, kv_heads, dim) || !heads_ok(v, kv_heads, dim))) return TG_ERR_INVALID_VALUE;
+    if (!arrays_ok(q_starts, q_lengths, k_starts, k_lengths)) return TG_ERR_INVALID_VALUE;
+    tg::host::Device dev;
+    st = tg::host::device(&dev);
+    if (st != TG_OK) return st;
+    const ForwardPlan p = plan_forward(z, dev.sms);
+    if (p.tiles * kv_heads * p.splits > INT32_MAX) return TG_ERR_UNSUPPORTED;
+    if (p.workspace && (!workspace || (uintptr_t)workspace % 16 || workspace_bytes < p.workspace))
+        return TG_ERR_INVALID_VALUE;
+    AttnForward a = {};
+    a.s = make_seqs(z, q_starts, q_lengths, k_starts, k_lengths, causal);
+    a.h = make_heads(z, scale);
+    // (Without keys nothing is loaded: any map will do.)
+    if (!encode_query(&a.q, dtype, q, q_rows, heads, a.h.group, dim, a.h.tokens) ||
+        !encode_keys(&a.k, dtype, k_rows ? k : q, k_rows ? k_rows : 1, k_rows ? kv_heads : 1, dim) ||
+        !encode_keys(&a.v, dtype, k_rows ? v : q, k_rows ? k_rows : 1, k_rows ? kv_heads : 1, dim))
+        return TG_ERR_CUDA;
+    a.o = {O, ldo, heads == 1 ? 0 : ho};
+    a.lse = LSE;
+    a.tiles = (int32_t)p.tiles;
+    a.splits = (int32_t)p.splits;
+    a.chunk = (int32_t)p.chunk;
+    if (p.workspace) {
+        a.part_o = static_cast<float *>(workspace);
+        a.part_ml = reinterpret_cast<float2 *>(a.part_o + p.splits * heads * q_rows * dim);
+    }
+    a.status = dev.status;
+    a.wait_limit_ns = dev.wait_limit_ns;
+    const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = dtype == TG_BF16 ? launch_attn_forward_bf16(a, p.nq, dev.id, cs)
+                                           : launch_attn_forward_fp16(a, p.nq, dev.id, cs);
+    return e == cudaSuccess ? TG_OK : TG_ERR_CUDA;
+}

@@ -1,0 +1,67 @@
+// Internal interface between the attention front end (tg_attn.cu) and the
+// kernel instantiations (one translation unit per operand type), and what both
+// sides of the ABI share about packed sequences.
+#pragma once
+
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+namespace tg {
+
+constexpr int ATTN_ROWS = 128;  // rows of a tile: tokens x heads of one group
+constexpr int ATTN_KEYS = 128;  // keys of a block
+constexpr int ATTN_MAX_DIM = 128;
+
+// Packed sequences: sequence s owns rows starts[s] to starts[s] + length[s] (or
+// starts[s + 1] when no lengths are given) of Q, and of K and V.
+struct AttnSeqs {
+    const int64_t *q_starts, *q_lengths, *k_starts, *k_lengths;
+    int32_t seqs;
+    int32_t q_rows, k_rows;  // rows of the tensors
+    int32_t max_q, max_k;    // no sequence is longer
+    int32_t causal;
+};
+
+struct AttnHeads {
+    int32_t heads, kv_heads, group;  // group: query heads that share a key head
+    int32_t tokens;                  // tokens of a tile: ATTN_ROWS / group
+    int32_t dim;
+    float scale, scale_log2;         // scale, scale log2 e
+};
+
+struct AttnOut {
+    void *ptr;
+    int64_t ld, hd;  // elements between rows, between heads
+};
+
+struct AttnForward {
+    CUtensorMap q, k, v;
+    AttnSeqs s;
+    AttnHeads h;
+    AttnOut o;
+    float *lse;             // heads x q_rows, or NULL
+    float *part_o;          // splits > 1: unnormalised rows, splits x heads x q_rows x dim
+    float2 *part_ml;        //   and their (reference exponent, sum)
+    int32_t tiles;          // bound on the row tiles (tile pairs) of all sequences
+    int32_t splits, chunk;  // key ranges of `chunk` blocks each
+    uint32_t *status;
+    uint64_t wait_limit_ns;
+};
+
+struct AttnBackward {
+    CUtensorMap q, k, v, dy;
+    AttnSeqs s;
+    AttnHeads h;
+    AttnOut dq, dk, dv;     // (NULL pointers: not wanted)
+    const float *lse;       // heads x q_rows
+    const float *delta;     // heads x q_rows: sum over d of dO O
+    int32_t tiles;          // bound on the row tiles, or on the key blocks, of all sequences
+    uint32_t *status;
+    uint64_t wait_limit_ns;
+};
+
+cudaError_t launch_attn_forward_bf16(const AttnForward &a, int tiles_per_cta, int device, cudaStream_t stream);
+cudaError_t launch_attn_forward_fp16(const AttnForward &a, int tiles_per_cta, int device, cudaStream_t stream);
+
+}  // namespace tg

@@ -1,0 +1,91 @@
+// Which rows and keys a block of the attention kernels works on.
+#pragma once
+
+#include "tg_attn.h"
+#include "tg_attn_ptx.cuh"
+
+namespace tg {
+
+// Codes of the attention kernels' bounded waits (beside WaitSite's).
+enum AttnSite : uint32_t {
+    SITE_SCORES = 12,         // scores in tensor memory
+    SITE_PROBABILITIES = 13,  // probabilities (or gradients of scores) back from the warps
+};
+
+// A sequence's rows, held inside the tensor and to the bound that the caller
+// gave: whatever the arrays hold, nothing outside is touched.
+__device__ __forceinline__ void attn_range(const int64_t *starts, const int64_t *lengths, int s,
+                                           int rows, int bound, int &at, int &len) {
+    const int64_t b = starts[s];
+    const int64_t n = lengths ? lengths[s] : starts[s + 1] - b;
+    const bool in = b >= 0 && b <= rows && n > 0;
+    const int64_t left = in ? rows - b : 0;
+    int64_t l = in ? n : 0;
+    if (l > left) l = left;
+    if (l > bound) l = bound;
+    at = in ? (int)b : 0;
+    len = (int)l;
+}
+
+struct AttnWork {
+    int seq;    // -1: nothing
+    int first;  // first token (or key) of the tile within the sequence
+    int q0, lq, k0, lk;
+};
+
+// Tile t, counted through the sequences in order, `per` tokens (or keys) each:
+// called by a whole warp.  KEYS: tiles of keys instead of tokens.
+template <bool KEYS>
+__device__ __forceinline__ AttnWork attn_find(const AttnSeqs &s, int t, int per, int lane) {
+    AttnWork w;
+    w.seq = -1;
+    w.first = w.q0 = w.lq = w.k0 = w.lk = 0;
+    const int64_t *starts = KEYS ? s.k_starts : s.q_starts;
+    const int64_t *lengths = KEYS ? s.k_lengths : s.q_lengths;
+    const int rows = KEYS ? s.k_rows : s.q_rows, bound = KEYS ? s.max_k : s.max_q;
+    int tile = 0;
+    if (bound <= per) {  // a sequence is a tile
+        if (t < s.seqs) w.seq = t;
+    } else {
+        int before = 0;
+        for (int base = 0; base < s.seqs; base += 32) {
+            int n = 0;
+            if (base + lane < s.seqs) {
+                int at, len;
+                attn_range(starts, lengths, base + lane, rows, bound, at, len);
+                n = (len + per - 1) / per;
+            }
+            int sum = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, sum, o);
+                if (lane >= o) sum += v;
+            }
+            const bool mine = t >= before + sum - n && t < before + sum;
+            const unsigned who = __ballot_sync(0xffffffffu, mine);
+            if (who) {
+                const int l = __ffs(who) - 1;
+                w.seq = base + l;
+                tile = t - (before + __shfl_sync(0xffffffffu, sum - n, l));
+                break;
+            }
+            before += __shfl_sync(0xffffffffu, sum, 31);
+        }
+    }
+    if (w.seq >= 0) {
+        attn_range(s.q_starts, s.q_lengths, w.seq, s.q_rows, s.max_q, w.q0, w.lq);
+        attn_range(s.k_starts, s.k_lengths, w.seq, s.k_rows, s.max_k, w.k0, w.lk);
+        w.first = tile * per;
+        if (w.first >= (KEYS ? w.lk : w.lq)) w.seq = -1;
+    }
+    return w;
+}
+
+// Keys that token i of a sequence sees: 0 to this, less one.
+__device__ __forceinline__ int attn_seen(const AttnSeqs &s, const AttnWork &w, int i) {
+    if (!s.causal) return w.lk;
+    const int n = i + w.lk - w.lq + 1;
+    return n < 0 ? 0 : n < w.lk ? n : w.lk;
+}
+
+}  // namespace tg

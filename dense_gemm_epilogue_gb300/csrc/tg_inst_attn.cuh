@@ -1,0 +1,57 @@
+// Instantiation and launch of the attention kernels for one operand type.
+#pragma once
+
+#include <atomic>
+#include "tg_attn.h"
+#include "tg_kernel_attn.cuh"
+
+namespace tg {
+
+template <class K>
+static cudaError_t attn_smem(K kernel, int smem, int device, std::atomic<uint64_t> &done) {
+    const uint64_t bit = (device >= 0 && device < 64) ? (1ull << device) : 0;
+    if (bit && (done.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess && bit) done.fetch_or(bit, std::memory_order_acq_rel);
+    return e;
+}
+
+template <class P>
+static cudaError_t attn_launch(void (*kernel)(const P), int64_t grid, int threads, int smem,
+                               cudaStream_t stream, const P &p) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3((unsigned)grid, 1, 1);
+    cfg.blockDim = dim3(threads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+template <Kind KD, int DT, int NQ>
+static cudaError_t launch_attn_one(const AttnForward &a, int device, cudaStream_t stream) {
+    using C = AttnConfig<KD, DT, NQ>;
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = attn_smem(tg_attn_kernel<KD, DT, NQ>, C::SMEM_BYTES, device, done);
+    if (e != cudaSuccess) return e;
+    return attn_launch<AttnForward>(tg_attn_kernel<KD, DT, NQ>,
+                                    (int64_t)a.tiles * a.h.kv_heads * a.splits, C::NUM_THREADS,
+                                    C::SMEM_BYTES, stream, a);
+}
+
+template <Kind KD>
+static cudaError_t launch_attn_forward_kind(const AttnForward &a, int nq, int device, cudaStream_t stream) {
+    cudaError_t e;
+    if (a.h.dim <= 64)
+        e = nq == 2 ? launch_attn_one<KD, 64, 2>(a, device, stream) : launch_attn_one<KD, 64, 1>(a, device, stream);
+    else
+        e = nq == 2 ? launch_attn_one<KD, 128, 2>(a, device, stream) : launch_attn_one<KD, 128, 1>(a, device, stream);
+    if (e != cudaSuccess || a.splits == 1) return e;
+    return attn_launch<AttnForward>(tg_attn_join_kernel<KD>, (int64_t)a.tiles * a.h.kv_heads, 256, 0, stream, a);
+}
+
+}  // namespace tg

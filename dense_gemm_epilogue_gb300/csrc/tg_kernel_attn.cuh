@@ -1,0 +1,487 @@
+// Attention forward: O = softmax(scale Q K^T) V over packed sequences.
+//
+// A tile is 128 rows: `tokens` consecutive tokens of a sequence times the
+// `group` query heads that share a key head, so that every key and value that
+// comes in serves the whole group.  Over blocks of 128 keys, for each row,
+//   s_j = q . k_j,  m' = max(m, s_j),  p_j = 2^(c (s_j - m')),  c = scale log2 e
+//   l' = l 2^(c (m - m')) + sum p_j,  o' = o 2^(c (m - m')) + sum p_j v_j
+// and in the end o / l: one pass, with O and S in tensor memory and a thread
+// for each row.  The reference m stands until the maximum has outgrown it by
+// 2^8 (p stays below 256, exact enough in 16 bits and far from FP16's end), so
+// that O is rescaled in a few blocks only.  p is rounded to 16 bits for the
+// second product; l sums it unrounded in FP32.
+//
+// NQ = 2 (many tiles): two tiles a CTA, four warps each for the softmax, one
+// warp for the loads, one thread for the MMAs.  While the warps of one tile
+// work on their scores the tensor core runs the other tile's two products.
+// P overwrites S (128-wide heads; the tensor core runs a CTA's MMAs of one
+// shape in the order of issue, so the next S waits for P V), or has columns of
+// its own (64-wide).
+// NQ = 1 (few rows, long keys; short sequences): one tile, S doubled, so that
+// the next block's S runs while the softmax is on this one's, and a deep ring
+// of keys and values; the keys may be cut into `splits` ranges of `chunk`
+// blocks, whose rows go unnormalised, in FP32, to the workspace, where
+// tg_attn_join_kernel adds them.
+#pragma once
+
+#include "tg_attn_work.cuh"
+
+namespace tg {
+
+template <Kind KD, int DT, int NQ>
+struct AttnConfig {
+    using T = KindTraits<KD>;
+    static constexpr int HALVES = DT / 64;                // 64-value boxes of a row
+    static constexpr int TILE_BYTES = HALVES * 128 * 128;  // 128 rows
+    static constexpr int FIT = (SMEM_LIMIT - 2048 - NQ * TILE_BYTES) / TILE_BYTES;
+    static constexpr int STAGES = FIT > 12 ? 12 : FIT;
+    static constexpr int Q_OFF = 0;
+    static constexpr int KV_OFF = NQ * TILE_BYTES;
+    static constexpr int BAR_OFF = KV_OFF + STAGES * TILE_BYTES;
+    static constexpr int QF = 0, FULL0 = 1, EMPTY0 = FULL0 + STAGES, SF0 = EMPTY0 + STAGES, PR0 = SF0 + 2,
+                         OD0 = PR0 + 2, PVD = OD0 + 2, DRAIN = PVD + 1, NUM_BARS = DRAIN + 1;
+    static constexpr int MISC_OFF = BAR_OFF + NUM_BARS * 8;
+    static constexpr int SMEM_BYTES = MISC_OFF + 64 + 1024;
+    static constexpr int SOFT_WARPS = 4 * NQ;
+    static constexpr int LOAD_WARP = SOFT_WARPS, MMA_WARP = SOFT_WARPS + 1;
+    static constexpr int NUM_THREADS = 32 * (SOFT_WARPS + 2);
+    static constexpr int TMEM_COLS = 512;
+    static constexpr int O_COL = 256;
+    static constexpr int P_COL = DT == 64 ? O_COL + NQ * DT : 0;  // (DT == 128: over S)
+    static constexpr int P_STEP = DT == 64 ? 64 : 128;
+    static constexpr uint32_t ID_BASE = (1u << 4) | (T::fmt << 7) | (T::fmt << 10) | ((128u >> 4) << 24);
+    static constexpr uint32_t ID_S = ID_BASE | ((128u >> 3) << 17);
+    static constexpr uint32_t ID_PV = ID_BASE | (1u << 16) | ((uint32_t)(DT >> 3) << 17);
+    static_assert(SMEM_BYTES <= SMEM_LIMIT && STAGES >= 4, "shared memory budget");
+};
+
+// S (128 x 128) = A (rows of DT) B^T (rows of DT), both K-major tiles of 64-value boxes.
+template <int DT>
+__device__ __forceinline__ void attn_mma_rows(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc) {
+#pragma unroll
+    for (int kk = 0; kk < DT / 16; ++kk) {
+        const uint32_t at = (kk >> 2) * 16384 + (kk & 3) * 32;
+        mma_f16(d, smem_desc_sw128(a + at), smem_desc_sw128(b + at), idesc, kk != 0);
+    }
+}
+// D (128 x N) (+)= A (tensor memory, 128 reduction values) B (MN-major tile of 128 rows).
+__device__ __forceinline__ void attn_mma_ta(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
+                                            bool accumulate) {
+#pragma unroll
+    for (int kk = 0; kk < 8; ++kk)
+        mma_f16_ta(d, a + kk * 8, smem_desc_mn_rows128(b + kk * 2048), idesc, accumulate || kk != 0);
+}
+
+// Zeroes rows `from` to 127 of a tile: rows behind a sequence's end hold others'
+// values, and 0 times an infinity or a NaN would reach the sums.  One row a thread.
+template <int HALVES>
+__device__ __forceinline__ void attn_zero_row(uint8_t *tile, int row) {
+#pragma unroll
+    for (int h = 0; h < HALVES; ++h) {
+        uint4 *q = reinterpret_cast<uint4 *>(tile + h * 16384 + row * 128);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) q[i] = make_uint4(0, 0, 0, 0);
+    }
+}
+
+template <Kind KD, int DT, int NQ>
+__global__ void __launch_bounds__(AttnConfig<KD, DT, NQ>::NUM_THREADS, 1)
+    tg_attn_kernel(const __grid_constant__ AttnForward p) {
+    using C = AttnConfig<KD, DT, NQ>;
+    constexpr int S = C::STAGES;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    const uint32_t sbase = smem_u32(smem);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    auto bar = [&](int i) -> uint32_t { return sbase + C::BAR_OFF + 8 * i; };
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::MISC_OFF);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::MISC_OFF + 4);
+    AttnWork *shared_work = reinterpret_cast<AttnWork *>(smem + C::MISC_OFF + 8);
+    const WaitCtl ctl{abort_flag, p.status, p.wait_limit_ns};
+
+    if (threadIdx.x == 0) {
+        mbar_init(bar(C::QF), 1);
+        for (int s = 0; s < S; ++s) {
+            mbar_init(bar(C::FULL0 + s), 1);
+            mbar_init(bar(C::EMPTY0 + s), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar(C::SF0 + i), 1);
+            mbar_init(bar(C::PR0 + i), 4);
+            mbar_init(bar(C::OD0 + i), 1);
+        }
+        mbar_init(bar(C::PVD), 1);
+        mbar_init(bar(C::DRAIN), 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+        prefetch_tensormap(&p.q);
+        prefetch_tensormap(&p.k);
+        prefetch_tensormap(&p.v);
+    }
+    if (warp == C::MMA_WARP) {
+        tmem_alloc(smem_u32(tmem_slot), C::TMEM_COLS);
+        tmem_relinquish();
+    }
+    // Blocks count down through the tiles: the last tokens of a sequence see the
+    // most keys, and the long work is better begun first.
+    const int split = blockIdx.x % p.splits;
+    const int rest = blockIdx.x / p.splits;
+    const int head = rest % p.h.kv_heads;
+    griddep_launch();
+    griddep_wait();
+    if (warp == C::LOAD_WARP) {
+        const AttnWork w = attn_find<false>(p.s, p.tiles - 1 - rest / p.h.kv_heads, NQ * p.h.tokens, lane);
+        if (lane == 0) *shared_work = w;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const AttnWork w = *shared_work;
+
+    // Blocks of keys: from jb, to je[t] for tile t.
+    const int jb = split * p.chunk;
+    int je[NQ], last = jb;
+#pragma unroll
+    for (int t = 0; t < NQ; ++t) {
+        const int end = w.first + (t + 1) * p.h.tokens;  // tokens before it are in tiles up to t
+        const int tokens = end < w.lq ? end : w.lq;
+        const int seen = tokens > w.first + t * p.h.tokens ? attn_seen(p.s, w, tokens - 1) : 0;
+        je[t] = (seen + ATTN_KEYS - 1) / ATTN_KEYS;
+        if (je[t] > jb + p.chunk) je[t] = jb + p.chunk;
+        if (w.seq < 0 || je[t] < jb) je[t] = jb;
+        if (je[t] > last) last = je[t];
+    }
+
+    if (warp == C::LOAD_WARP) {
+        if (lane == 0 && last > jb) {
+            mbar_arrive_expect_tx(bar(C::QF), NQ * C::HALVES * p.h.tokens * p.h.group * 128);
+#pragma unroll
+            for (int t = 0; t < NQ; ++t)
+#pragma unroll
+                for (int h = 0; h < C::HALVES; ++h)
+                    tma_load_4d(sbase + C::Q_OFF + t * C::TILE_BYTES + h * 16384, &p.q, bar(C::QF), h * 64,
+                                0, head, w.q0 + w.first + t * p.h.tokens);
+            const int items = 2 * (last - jb);
+            int s = 0, issued = 0;
+            uint32_t ph = 0;
+            bool ok = true;
+            for (int it = 0; it < items; ++it) {
+                if (!wait_phase(bar(C::EMPTY0 + s), ph ^ 1, ctl, SITE_EMPTY)) { ok = false; break; }
+                mbar_arrive_expect_tx(bar(C::FULL0 + s), C::TILE_BYTES);
+                const int row = w.k0 + (jb + (it >> 1)) * ATTN_KEYS;
+#pragma unroll
+                for (int h = 0; h < C::HALVES; ++h)
+                    tma_load_3d(sbase + C::KV_OFF + s * C::TILE_BYTES + h * 16384, it & 1 ? &p.v : &p.k,
+                                bar(C::FULL0 + s), h * 64, head, row);
+                ++issued;
+                if (++s == S) { s = 0; ph ^= 1; }
+            }
+            if (!ok) {
+                // Every copy already issued lands before the CTA exits.
+                wait_phase_drain(bar(C::QF), 0, ctl);
+                for (int st = 0; st < S && st < issued; ++st)
+                    wait_phase_drain(bar(C::FULL0 + st), (uint32_t)((issued - 1 - st) / S & 1), ctl);
+            }
+        }
+        __syncwarp();
+    } else if (warp == C::MMA_WARP) {
+        if (lane == 0 && last > jb) {
+            auto tile = [&](int it) -> uint32_t { return sbase + C::KV_OFF + (it % S) * C::TILE_BYTES; };
+            auto full = [&](int it) -> bool {
+                const bool ok = wait_phase(bar(C::FULL0 + it % S), (uint32_t)(it / S) & 1, ctl, SITE_FULL);
+                tc_fence_after();
+                return ok;
+            };
+            auto scores = [&](int t, int slot, int it) {
+                attn_mma_rows<DT>(tmem + slot * 128, sbase + C::Q_OFF + t * C::TILE_BYTES, tile(it), C::ID_S);
+                mma_commit(bar(C::SF0 + slot));
+            };
+            auto values = [&](int t, int slot, int it, bool more) {
+                attn_mma_ta(tmem + C::O_COL + t * DT, tmem + C::P_COL + slot * C::P_STEP, tile(it), C::ID_PV,
+                            more);
+            };
+            bool ok = wait_phase(bar(C::QF), 0, ctl, SITE_FULL) && full(0);
+            if (ok) {
+                if constexpr (NQ == 2) {
+#pragma unroll
+                    for (int t = 0; t < NQ; ++t)
+                        if (je[t] > jb) scores(t, t, 0);
+                } else {
+                    scores(0, 0, 0);
+                }
+                mma_commit(bar(C::EMPTY0));
+            }
+            for (int j = jb; ok && j < last; ++j) {
+                const int n = j - jb, kn = 2 * n + 2;
+                if constexpr (NQ == 2) {
+                    const int last_t = j < je[1] ? 1 : 0;
+#pragma unroll
+                    for (int t = 0; t < NQ; ++t) {
+                        if (!ok || j >= je[t]) continue;
+                        ok = wait_phase(bar(C::PR0 + t), n & 1, ctl, SITE_PROBABILITIES) && full(2 * n + 1);
+                        if (!ok) break;
+                        values(t, t, 2 * n + 1, n > 0);
+                        if (t == last_t) mma_commit(bar(C::EMPTY0 + (2 * n + 1) % S));
+                        if (j + 1 < je[t]) {
+                            ok = full(kn);
+                            if (!ok) break;
+                            scores(t, t, kn);
+                        } else {
+                            mma_commit(bar(C::OD0 + t));
+                        }
+                    }
+                    if (ok && j + 1 < last) mma_commit(bar(C::EMPTY0 + kn % S));
+                } else {
+                    if (j + 1 < last) {
+                        ok = full(kn);
+                        if (!ok) break;
+                        scores(0, (n + 1) & 1, kn);
+                        mma_commit(bar(C::EMPTY0 + kn % S));
+                    }
+                    ok = wait_phase(bar(C::PR0 + (n & 1)), (n >> 1) & 1, ctl, SITE_PROBABILITIES) &&
+                         full(2 * n + 1);
+                    if (!ok) break;
+                    values(0, n & 1, 2 * n + 1, n > 0);
+                    mma_commit(bar(C::EMPTY0 + (2 * n + 1) % S));
+                    mma_commit(bar(j + 1 < last ? C::PVD : C::OD0));
+                }
+            }
+            if (!ok) {
+                mma_commit(bar(C::DRAIN));
+                wait_phase_drain(bar(C::DRAIN), 0, ctl);
+            }
+        }
+        __syncwarp();
+    } else if (w.seq >= 0) {
+        // ------------------------------------------------------ softmax: a row a thread
+        const int t = NQ == 2 ? warp >> 2 : 0;
+        const int row = threadIdx.x & 127;
+        const uint32_t lane_base = (uint32_t)(warp & 3) << 21;  // lane field: bits 16 up
+        const int token = w.first + t * p.h.tokens + row / p.h.group;
+        const int qh = head * p.h.group + row % p.h.group;
+        const bool valid = row < p.h.tokens * p.h.group && token < w.lq;
+        const int seen = valid ? attn_seen(p.s, w, token) : 0;
+        const int first_seen = attn_seen(p.s, w, w.first + t * p.h.tokens);  // the tile's least
+        const float c = p.h.scale_log2;
+        const int end = NQ == 2 ? (t ? je[NQ - 1] : je[0]) : je[0];
+        float m = -INFINITY, l = 0.0f;
+        bool ok = true;
+        for (int j = jb; j < end; ++j) {
+            const int n = j - jb;
+            const int slot = NQ == 2 ? t : n & 1;
+            const uint32_t phase = NQ == 2 ? n & 1 : (n >> 1) & 1;
+            if (!wait_phase(bar(C::SF0 + slot), phase, ctl, SITE_SCORES)) { ok = false; break; }
+            tc_fence_after();
+            uint32_t s[128];
+            const uint32_t s_at = tmem + lane_base + slot * 128;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) tmem_ld_row32(s_at + 32 * i, s + 32 * i);
+            tmem_ld_wait();
+            if ((j + 1) * ATTN_KEYS > first_seen) {
+                const int lim = seen - j * ATTN_KEYS;
+#pragma unroll
+                for (int i = 0; i < 128; ++i)
+                    if (i >= lim) s[i] = 0xff800000u;
+                // Values behind the sequence's end: zero (see attn_zero_row).
+                const int left = w.lk - j * ATTN_KEYS;
+                if (left < ATTN_KEYS) {
+                    const int it = 2 * n + 1;
+                    if (!wait_phase(bar(C::FULL0 + it % S), (uint32_t)(it / S) & 1, ctl, SITE_FULL)) {
+                        ok = false;
+                        break;
+                    }
+                    if (row >= left) {
+                        attn_zero_row<C::HALVES>(smem + C::KV_OFF + (it % S) * C::TILE_BYTES, row);
+                        fence_proxy_async_smem();
+                    }
+                }
+            }
+            float mx[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) mx[i] = __uint_as_float(s[i]);
+#pragma unroll
+            for (int i = 4; i < 128; ++i) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(s[i]));
+            const float mn = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+            // (Every lane keeps its reference unless one has outgrown it.)
+            if (__any_sync(0xffffffffu, (mn - m) * c > 8.0f)) {
+                const float f = mn == m ? 1.0f : exp2_approx((m - mn) * c);
+                m = mn;
+                l *= f;
+                if (n > 0) {
+                    if (NQ == 1 && !wait_phase(bar(C::PVD), (n - 1) & 1, ctl, SITE_ACC_FULL)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t o_at = tmem + lane_base + C::O_COL + t * DT;
+#pragma unroll 1
+                    for (int i = 0; i < DT; i += 32) {
+                        uint32_t o[32];
+                        tmem_ld_row32(o_at + i, o);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                        tmem_st_32x32b_x32(o_at + i, o);
+                    }
+                }
+            }
+            const float mc = m == -INFINITY ? 0.0f : -m * c;
+            const uint64_t cc = pair2(c, c), mm = pair2(mc, mc);
+            uint64_t sum[2] = {0, 0};
+            const uint32_t p_at = tmem + lane_base + C::P_COL + slot * C::P_STEP;
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+                uint32_t y[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const int e = 32 * h + 2 * i;
+                    float a, b;
+                    unpair2(fma_pair(pair2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), cc, mm), a, b);
+                    a = exp2_approx(a);
+                    b = exp2_approx(b);
+                    sum[i & 1] = add_pair(sum[i & 1], pair2(a, b));
+                    y[i] = pack_half2<KD>(a, b);
+                }
+                tmem_st_32x32b_x16(p_at + 16 * h, y);
+            }
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(C::PR0 + slot));
+            float a, b;
+            unpair2(add_pair(sum[0], sum[1]), a, b);
+            l += a + b;
+        }
+        const bool some = end > jb;
+        if (ok && some) {
+            ok = wait_phase(bar(C::OD0 + t), 0, ctl, SITE_ACC_FULL);
+            tc_fence_after();
+        }
+        if (ok) {
+            const int64_t at = (int64_t)qh * p.s.q_rows + w.q0 + token;
+            const uint32_t o_at = tmem + lane_base + C::O_COL + t * DT;
+            if (p.splits > 1) {
+                const int64_t slot = (int64_t)split * p.h.heads * p.s.q_rows + at;
+                if (valid) p.part_ml[slot] = make_float2(m * c, l);
+                float4 *dst = reinterpret_cast<float4 *>(p.part_o + slot * p.h.dim);
+                if (some) {
+#pragma unroll 1
+                    for (int i = 0; i < DT; i += 32) {
+                        uint32_t o[32];
+                        tmem_ld_row32(o_at + i, o);
+                        tmem_ld_wait();
+                        if (valid && l != 0.0f) {
+#pragma unroll
+                            for (int e = 0; e < 32; e += 4)
+                                if (i + e < p.h.dim)
+                                    dst[(i + e) >> 2] = make_float4(
+                                        __uint_as_float(o[e]), __uint_as_float(o[e + 1]),
+                                        __uint_as_float(o[e + 2]), __uint_as_float(o[e + 3]));
+                        }
+                    }
+                }
+            } else {
+                if (valid && p.lse)
+                    p.lse[at] = l == 0.0f ? -INFINITY : (m * c + log2f(l)) * 0.6931471805599453f;
+                const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+                uint16_t *dst = static_cast<uint16_t *>(p.o.ptr) + (w.q0 + token) * p.o.ld + qh * p.o.hd;
+#pragma unroll 1
+                for (int i = 0; i < DT; i += 32) {
+                    uint32_t o[32];
+                    if (some) {
+                        tmem_ld_row32(o_at + i, o);
+                        tmem_ld_wait();
+                    }
+                    if (valid) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8) {
+                            if (i + e >= p.h.dim) break;
+                            uint4 v = make_uint4(0, 0, 0, 0);
+                            if (some && l != 0.0f) {
+                                uint32_t y[4];
+#pragma unroll
+                                for (int q = 0; q < 4; ++q)
+                                    y[q] = pack_half2<KD>(__uint_as_float(o[e + 2 * q]) * inv,
+                                                          __uint_as_float(o[e + 2 * q + 1]) * inv);
+                                v = make_uint4(y[0], y[1], y[2], y[3]);
+                            }
+                            *reinterpret_cast<uint4 *>(dst + i + e) = v;
+                        }
+                    }
+                }
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == C::MMA_WARP) {
+        tc_fence_after();
+        tmem_dealloc(tmem, C::TMEM_COLS);
+    }
+}
+
+// The rows of a tile from their key ranges: with M the largest reference,
+//   L = sum l_s 2^(m_s - M),  O = sum o_s 2^(m_s - M) / L,  LSE = (M + log2 L) ln 2,
+// in the order of the ranges.  A warp a row.
+template <Kind KD>
+__global__ void __launch_bounds__(256) tg_attn_join_kernel(const __grid_constant__ AttnForward p) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    griddep_launch();
+    griddep_wait();
+    const int head = blockIdx.x % p.h.kv_heads;
+    const AttnWork w = attn_find<false>(p.s, blockIdx.x / p.h.kv_heads, p.h.tokens, lane);
+    if (w.seq < 0) return;
+    const int64_t stride = (int64_t)p.h.heads * p.s.q_rows;
+    for (int row = warp; row < p.h.tokens * p.h.group; row += 8) {
+        const int token = w.first + row / p.h.group, qh = head * p.h.group + row % p.h.group;
+        if (token >= w.lq) break;
+        const int64_t at = (int64_t)qh * p.s.q_rows + w.q0 + token;
+        // Lane i looks at ranges i, i + 32, ...
+        float m = -INFINITY;
+        for (int s = lane; s < p.splits; s += 32) {
+            const float2 ml = p.part_ml[s * stride + at];
+            if (ml.y != 0.0f) m = fmaxf(m, ml.x);
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        float l = 0.0f, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int base = 0; base < p.splits; base += 32) {
+            float f = 0.0f, ls = 0.0f;
+            if (base + lane < p.splits) {
+                const float2 ml = p.part_ml[(base + lane) * stride + at];
+                if (ml.y != 0.0f) {
+                    f = exp2_approx(ml.x - m);
+                    ls = ml.y;
+                }
+            }
+            const int top = p.splits - base < 32 ? p.splits - base : 32;
+#pragma unroll 4
+            for (int i = 0; i < top; ++i) {
+                const float g = __shfl_sync(0xffffffffu, f, i);
+                const float li = __shfl_sync(0xffffffffu, ls, i);
+                if (li == 0.0f) continue;
+                l += li * g;
+                if (4 * lane < p.h.dim) {
+                    const float4 v = reinterpret_cast<const float4 *>(
+                        p.part_o + ((base + i) * stride + at) * p.h.dim)[lane];
+                    o[0] += v.x * g;
+                    o[1] += v.y * g;
+                    o[2] += v.z * g;
+                    o[3] += v.w * g;
+                }
+            }
+        }
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        if (lane == 0 && p.lse) p.lse[at] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+        if (4 * lane < p.h.dim) {
+            uint16_t *dst = static_cast<uint16_t *>(p.o.ptr) + (w.q0 + token) * p.o.ld + qh * p.o.hd;
+            *reinterpret_cast<uint2 *>(dst + 4 * lane) =
+                make_uint2(pack_half2<KD>(o[0] * inv, o[1] * inv), pack_half2<KD>(o[2] * inv, o[3] * inv));
+        }
+    }
+}
+
+}  // namespace tg

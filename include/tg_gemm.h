@@ -527,8 +527,107 @@ tg_status tg_layer_norm_backward(int64_t M, int64_t N, const void *dY, int64_t l
                                  float *dgamma, float *dbeta, tg_out_dtype dtype,
                                  void *workspace, int64_t workspace_bytes, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Attention operators: the other half of a transformer block, between its QKV
+ * and output projections (tg_linear), forward and backward.
+ *
+ * Layout: a tensor has rows (tokens) of `heads` heads of `dim` values; value d
+ * of head h of row t is at base + t*ld + h*hd + d (elements; hd is not looked
+ * at for one head).  The heads of a QKV projection's rows are addressed in
+ * place.  Packed sequences: sequence s owns the rows starts[s] to starts[s] +
+ * lengths[s], or to starts[s + 1] where lengths is NULL; starts and lengths are
+ * device arrays of int64 (starts has seqs + 1 entries, of which the last is
+ * read only without lengths).  A sequence may be empty.  Rows of no sequence are
+ * neither used nor written, whatever they hold.  Entries that point outside the
+ * tensors are cut to them.
+ *
+ * Workspace, ownership, asynchrony and errors are the feed-forward operators'
+ * (everything is enqueued on `stream`, arguments are checked before anything is
+ * launched, repeated calls agree bit for bit); these calls use no workspace of
+ * the library.  An output may not overlap an input unless the call says so.
+ */
+typedef enum {
+    TG_ROTARY_HALVES = 0, /* pairs (i, i + rot/2) */
+    TG_ROTARY_PAIRS = 1   /* pairs (2i, 2i + 1) */
+} tg_rotary_layout;
+
+typedef enum {
+    TG_ROTARY_NONE = 0,   /* f_i = base^(-2i/rot) radians a position */
+    TG_ROTARY_LINEAR = 1, /* f_i / factor: positions interpolated */
+    TG_ROTARY_BASE = 2,   /* base factor^(rot/(rot-2)) for base: the slowest pair turns
+                             1/factor as far, the fastest as far as before (rot >= 4) */
+    TG_ROTARY_BANDS = 3   /* by wavelength: with r = original f_i / 2 pi turns over the
+                             original context and g = (r - low)/(high - low) held to
+                             [0, 1], g f_i + (1 - g) f_i / factor */
+} tg_rotary_scaling;
+
 /*
- * The planner's choice for one product of these operators, as one line of
+ * Frequencies for tg_rotary, on the host (no CUDA): steps[i], i < rot/2, is
+ * f_i / 2 pi turns a position as a fraction of 2^64, so that position * step,
+ * modulo 2^64, is the angle to 2^-53 f_i of a position however far.  rot is even
+ * and positive, base and factor positive; low < high and original > 0 are read
+ * for TG_ROTARY_BANDS only.
+ */
+tg_status tg_rotary_steps(int64_t rot, double base, tg_rotary_scaling scaling, double factor,
+                          double low, double high, double original, uint64_t *steps);
+
+/*
+ * Rotary positions: of each head's first rot values (rot even, 0 <= rot <= dim)
+ * the pairs (a, b) of `layout` become
+ *   (amplitude (a cos p - b sin p), amplitude (a sin p + b cos p)),
+ * p = positions[t] f_i; the others are copied.  steps is tg_rotary_steps' array,
+ * in device memory.  positions (tokens int64, device; NULL: 0, 1, 2, ...) may be
+ * negative.  rows (tokens int64, device; NULL: t) is the row of Y that token t
+ * goes to, so that keys (and, with rot = 0, values) are written to a cache's
+ * rows; a row outside [0, y_rows) skips the token, and none may be given twice.  Without rows, Y has `tokens` rows, may be X itself (same
+ * pointer and strides), and y_rows is not looked at.  dtype is any tg_out_dtype;
+ * cos and sin are FP32; dim <= 4096 (TG_ERR_UNSUPPORTED
+ * beyond); X and Y need the alignment of an element only.
+ */
+tg_status tg_rotary(int64_t tokens, int64_t heads, int64_t dim, int64_t rot, const void *X,
+                    int64_t ldx, int64_t hx, void *Y, int64_t ldy, int64_t hy, int64_t y_rows,
+                    const int64_t *positions, const int64_t *rows, const uint64_t *steps,
+                    tg_rotary_layout layout, float amplitude, tg_out_dtype dtype, void *stream);
+
+/* Its gradient: the transposed map from dY to dX (which may be dY itself). */
+tg_status tg_rotary_backward(int64_t tokens, int64_t heads, int64_t dim, int64_t rot,
+                             const void *dY, int64_t lddy, int64_t hdy, void *dX, int64_t lddx,
+                             int64_t hdx, const int64_t *positions, const uint64_t *steps,
+                             tg_rotary_layout layout, float amplitude, tg_out_dtype dtype,
+                             void *stream);
+
+/*
+ * Attention: for row i of a sequence with lq rows of Q and lk rows of K and V,
+ *   S_j = scale q_i . k_j,  O_i = sum_j softmax(S)_j v_j,  LSE_i = log sum_j exp(S_j)
+ * over its keys j < lk, or with causal = 1 over j <= i + lk - lq (the last rows
+ * of Q stand at the last keys: a prompt, a chunk behind a cache, or one new
+ * token).  A row without keys has O = 0 and LSE = -infinity.  Query head h reads
+ * key head h / (heads / kv_heads).  LSE (heads x q_rows floats, what the backward
+ * pass reads) may be NULL.
+ *
+ * max_q and max_k bound the sequences' rows and keys (0: q_rows, k_rows); the
+ * plan goes by them, and a longer sequence is cut to them.  dtype is TG_BF16 or
+ * TG_FP16; products and sums are FP32, probabilities are rounded to dtype for
+ * the second product.  Bases must be 16-byte aligned, ld and hd multiples of 8
+ * and at least dim (TG_ERR_INVALID_VALUE); dim a multiple of 8 up to 128 and
+ * heads / kv_heads at most 128 (TG_ERR_UNSUPPORTED); scale positive and finite.
+ * An infinity or a NaN in a sequence's own V reaches every row of that sequence
+ * that is worked on beside a row that sees it (rows up to 256 before it); other
+ * sequences' and unused rows' never do.
+ */
+int64_t tg_attention_workspace_bytes(int64_t seqs, int64_t q_rows, int64_t k_rows, int64_t heads,
+                                     int64_t kv_heads, int64_t dim, int64_t max_q, int64_t max_k,
+                                     tg_dtype dtype);
+tg_status tg_attention(int64_t seqs, int64_t q_rows, int64_t k_rows, int64_t heads, int64_t kv_heads,
+                       int64_t dim, const void *Q, int64_t ldq, int64_t hq, const void *K, int64_t ldk,
+                       int64_t hk, const void *V, int64_t ldv, int64_t hv, const int64_t *q_starts,
+                       const int64_t *q_lengths, const int64_t *k_starts, const int64_t *k_lengths,
+                       int64_t max_q, int64_t max_k, int32_t causal, float scale, void *O, int64_t ldo,
+                       int64_t ho, float *LSE, tg_dtype dtype, void *workspace,
+                       int64_t workspace_bytes, void *stream);
+
+/*
+ * The planner's choice for one product of the feed-forward operators, as one line of
  * text (host only when num_sms > 0; num_sms <= 0 queries the current device):
  * a forward product, or dX or dW of the backward call with both asked for.
  *   "stream 128x16 tiles=112 k_blocks=64 grid=152": up to 64 tokens (gated
@@ -563,8 +662,8 @@ const char *tg_status_string(tg_status status);
  * out since the last check, TG_ERR_DEVICE_TIMEOUT if one did (then *where, if
  * not NULL, receives a code naming the wait: 1 stage-full, 2 stage-empty,
  * 3 accumulator-full, 4 accumulator-empty, 5 converted-stage, 6 drain,
- * 7 self-test, 8 partial sums, 10 unit claim, 11 residual box), TG_ERR_CUDA on a
- * CUDA error.
+ * 7 self-test, 8 partial sums, 10 unit claim, 11 residual box, 12 attention scores,
+ * 13 attention probabilities), TG_ERR_CUDA on a CUDA error.
  */
 tg_status tg_check_device_status(void *stream, int32_t *where);
 
