@@ -112,6 +112,8 @@ EXPORTED = (
     "tg_rotary_backward",
     "tg_attention_workspace_bytes",
     "tg_attention",
+    "tg_attention_backward_workspace_bytes",
+    "tg_attention_backward",
 )
 
 
@@ -319,6 +321,12 @@ def load(path: str | None = None) -> ctypes.CDLL:
         lib.tg_attention.argtypes = ([i64] * 6 + [vp, i64, i64] * 3 + [vp] * 4 + [i64, i64, i32, f32]
                                      + [vp, i64, i64, vp, c, vp, i64, vp])
         lib.tg_attention.restype = c
+        lib.tg_attention_backward_workspace_bytes.argtypes = [i64] * 8 + [c]
+        lib.tg_attention_backward_workspace_bytes.restype = i64
+        lib.tg_attention_backward.argtypes = ([i64] * 6 + [vp, i64, i64] * 5 + [vp] * 5
+                                              + [i64, i64, i32, f32] + [vp, i64, i64] * 3
+                                              + [c, vp, i64, vp])
+        lib.tg_attention_backward.restype = c
         lib.tg_version.argtypes = []
         lib.tg_version.restype = i32
         if path is None:
@@ -662,6 +670,25 @@ def tg_attention(seqs, q_rows, k_rows, heads, kv_heads, dim, Q, ldq, hq, K, ldk,
                                ldk, hk, _ptr(V), ldv, hv, _ptr(q_starts), _ptr(q_lengths),
                                _ptr(k_starts), _ptr(k_lengths), max_q, max_k, int(causal), scale,
                                _ptr(O), ldo, ho, _ptr(LSE), _dtype(dtype), ws, n, _stream(stream))
+
+
+def tg_attention_backward_workspace_bytes(seqs, q_rows, k_rows, heads, kv_heads, dim, max_q, max_k,
+                                          dtype) -> int:
+    return load().tg_attention_backward_workspace_bytes(seqs, q_rows, k_rows, heads, kv_heads, dim, max_q,
+                                                        max_k, _dtype(dtype))
+
+
+def tg_attention_backward(seqs, q_rows, k_rows, heads, kv_heads, dim, Q, ldq, hq, K, ldk, hk, V, ldv, hv,
+                          O, ldo, ho, dO, lddo, hdo, LSE, q_starts, q_lengths, k_starts, k_lengths,
+                          max_q, max_k, causal, scale, dQ, lddq, hdq, dK, lddk, hdk, dV, lddv, hdv, dtype,
+                          workspace=None, stream=None) -> int:
+    """dQ, dK and dV (each may be None) of tg_attention, from dO, O and LSE."""
+    ws, n = _space(workspace)
+    return load().tg_attention_backward(
+        seqs, q_rows, k_rows, heads, kv_heads, dim, _ptr(Q), ldq, hq, _ptr(K), ldk, hk, _ptr(V), ldv, hv,
+        _ptr(O), ldo, ho, _ptr(dO), lddo, hdo, _ptr(LSE), _ptr(q_starts), _ptr(q_lengths), _ptr(k_starts),
+        _ptr(k_lengths), max_q, max_k, int(causal), scale, _ptr(dQ), lddq, hdq, _ptr(dK), lddk, hdk,
+        _ptr(dV), lddv, hdv, _dtype(dtype), ws, n, _stream(stream))
 
 
 def tg_product_plan_describe(product, M, N, K, num_sms=0, size=256) -> str:

@@ -233,3 +233,83 @@ extern "C" tg_status tg_attention(int64_t seqs, int64_t q_rows, int64_t k_rows, 
                                            : launch_attn_forward_fp16(a, p.nq, dev.id, cs);
     return e == cudaSuccess ? TG_OK : TG_ERR_CUDA;
 }
+
+extern "C" int64_t tg_attention_backward_workspace_bytes(int64_t seqs, int64_t q_rows, int64_t k_rows,
+                                                         int64_t heads, int64_t kv_heads, int64_t dim,
+                                                         int64_t max_q, int64_t max_k, tg_dtype dtype) {
+    const Sizes z = {seqs, q_rows, k_rows, heads, kv_heads, dim, max_q, max_k, dtype};
+    if (sizes_ok(z) != TG_OK) return -1;
+    return seqs == 0 ? 0 : 4 * heads * q_rows;  // delta
+}
+
+extern "C" tg_status tg_attention_backward(
+    int64_t seqs, int64_t q_rows, int64_t k_rows, int64_t heads, int64_t kv_heads, int64_t dim,
+    const void *Q, int64_t ldq, int64_t hq, const void *K, int64_t ldk, int64_t hk, const void *V,
+    int64_t ldv, int64_t hv, const void *O, int64_t ldo, int64_t ho, const void *dO, int64_t lddo,
+    int64_t hdo, const float *LSE, const int64_t *q_starts, const int64_t *q_lengths,
+    const int64_t *k_starts, const int64_t *k_lengths, int64_t max_q, int64_t max_k, int32_t causal,
+    float scale, void *dQ, int64_t lddq, int64_t hdq, void *dK, int64_t lddk, int64_t hdk, void *dV,
+    int64_t lddv, int64_t hdv, tg_dtype dtype, void *workspace, int64_t workspace_bytes, void *stream) {
+    const Sizes z = {seqs, q_rows, k_rows, heads, kv_heads, dim, max_q, max_k, dtype};
+    tg_status st = sizes_ok(z);
+    if (st != TG_OK) return st;
+    if (!scale_ok(scale) || (causal != 0 && causal != 1) || workspace_bytes < 0 || !f32_ok(LSE))
+        return TG_ERR_INVALID_VALUE;
+    if (seqs == 0 || (!dQ && !dK && !dV)) return TG_OK;
+    const Heads q = {Q, ldq, hq}, k = {K, ldk, hk}, v = {V, ldv, hv}, o = {O, ldo, ho}, dy = {dO, lddo, hdo};
+    const Heads dq = {dQ, lddq, hdq}, dk = {dK, lddk, hdk}, dv = {dV, lddv, hdv};
+    if (q_rows > 0 && (!heads_ok(q, heads, dim) || !heads_ok(o, heads, dim) || !heads_ok(dy, heads, dim) || !LSE ||
+                       (dQ && !heads_ok(dq, heads, dim))))
+        return TG_ERR_INVALID_VALUE;
+    if (k_rows > 0 && (!heads_ok(k, kv_heads, dim) || !heads_ok(v, kv_heads, dim) ||
+                       (dK && !heads_ok(dk, kv_heads, dim)) || (dV && !heads_ok(dv, kv_heads, dim))))
+        return TG_ERR_INVALID_VALUE;
+    if (!arrays_ok(q_starts, q_lengths, k_starts, k_lengths)) return TG_ERR_INVALID_VALUE;
+    if (q_rows == 0 && k_rows == 0) return TG_OK;
+    const int64_t bytes = 4 * heads * q_rows;
+    if (bytes && (!workspace || (uintptr_t)workspace % 16 || workspace_bytes < bytes)) return TG_ERR_INVALID_VALUE;
+    tg::host::Device dev;
+    st = tg::host::device(&dev);
+    if (st != TG_OK) return st;
+    AttnBackward a = {};
+    a.s = make_seqs(z, q_starts, q_lengths, k_starts, k_lengths, causal);
+    a.h = make_heads(z, scale);
+    // (A side without rows is not loaded: any map will do.)
+    const Heads &any = q_rows ? q : k;
+    const int64_t any_rows = 1, any_heads = 1;
+    if (!encode_query(&a.q, dtype, q_rows ? q : any, q_rows ? q_rows : any_rows, q_rows ? heads : any_heads,
+                      q_rows ? a.h.group : 1, dim, a.h.tokens) ||
+        !encode_query(&a.dy, dtype, q_rows ? dy : any, q_rows ? q_rows : any_rows, q_rows ? heads : any_heads,
+                      q_rows ? a.h.group : 1, dim, a.h.tokens) ||
+        !encode_keys(&a.k, dtype, k_rows ? k : any, k_rows ? k_rows : any_rows, k_rows ? kv_heads : any_heads, dim) ||
+        !encode_keys(&a.v, dtype, k_rows ? v : any, k_rows ? k_rows : any_rows, k_rows ? kv_heads : any_heads, dim))
+        return TG_ERR_CUDA;
+    a.dq = {q_rows ? dQ : nullptr, lddq, heads == 1 ? 0 : hdq};
+    a.dk = {k_rows ? dK : nullptr, lddk, kv_heads == 1 ? 0 : hdk};
+    a.dv = {k_rows ? dV : nullptr, lddv, kv_heads == 1 ? 0 : hdv};
+    a.lse = LSE;
+    a.delta = static_cast<const float *>(workspace);
+    const int64_t tiles = q_rows ? tile_bound(seqs, q_rows, a.s.max_q, a.h.tokens) : 0;
+    const int64_t blocks = k_rows ? tile_bound(seqs, k_rows, a.s.max_k, ATTN_KEYS) : 0;
+    if (tiles * kv_heads > INT32_MAX || blocks * kv_heads > INT32_MAX || q_rows * heads / 16 > INT32_MAX - 1)
+        return TG_ERR_UNSUPPORTED;
+    a.tiles = (int32_t)tiles;
+    a.blocks = (int32_t)blocks;
+    a.status = dev.status;
+    a.wait_limit_ns = dev.wait_limit_ns;
+    AttnDelta d = {};
+    d.o = O;
+    d.dy = dO;
+    d.ldo = ldo;
+    d.ho = heads == 1 ? 0 : ho;
+    d.lddy = lddo;
+    d.hdy = heads == 1 ? 0 : hdo;
+    d.delta = static_cast<float *>(workspace);
+    d.rows = (int32_t)q_rows;
+    d.heads = (int32_t)heads;
+    d.dim = (int32_t)dim;
+    const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = dtype == TG_BF16 ? launch_attn_backward_bf16(a, d, dev.id, cs)
+                                           : launch_attn_backward_fp16(a, d, dev.id, cs);
+    return e == cudaSuccess ? TG_OK : TG_ERR_CUDA;
+}

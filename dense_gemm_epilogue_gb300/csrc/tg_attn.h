@@ -49,6 +49,14 @@ struct AttnForward {
     uint64_t wait_limit_ns;
 };
 
+constexpr int DELTA_THREADS = 256;
+struct AttnDelta {
+    const void *o, *dy;
+    int64_t ldo, ho, lddy, hdy;
+    float *delta;  // heads x rows
+    int32_t rows, heads, dim;
+};
+
 struct AttnBackward {
     CUtensorMap q, k, v, dy;
     AttnSeqs s;
@@ -56,12 +64,15 @@ struct AttnBackward {
     AttnOut dq, dk, dv;     // (NULL pointers: not wanted)
     const float *lse;       // heads x q_rows
     const float *delta;     // heads x q_rows: sum over d of dO O
-    int32_t tiles;          // bound on the row tiles, or on the key blocks, of all sequences
+    int32_t tiles, blocks;  // bounds on the row tiles and on the key blocks of all sequences
     uint32_t *status;
     uint64_t wait_limit_ns;
 };
 
 cudaError_t launch_attn_forward_bf16(const AttnForward &a, int tiles_per_cta, int device, cudaStream_t stream);
 cudaError_t launch_attn_forward_fp16(const AttnForward &a, int tiles_per_cta, int device, cudaStream_t stream);
+// delta, then the keys' kernel (unless neither dK nor dV is wanted), then the rows'.
+cudaError_t launch_attn_backward_bf16(const AttnBackward &a, const AttnDelta &d, int device, cudaStream_t stream);
+cudaError_t launch_attn_backward_fp16(const AttnBackward &a, const AttnDelta &d, int device, cudaStream_t stream);
 
 }  // namespace tg

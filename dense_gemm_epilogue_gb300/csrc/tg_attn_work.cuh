@@ -12,6 +12,11 @@ enum AttnSite : uint32_t {
     SITE_PROBABILITIES = 13,  // probabilities (or gradients of scores) back from the warps
 };
 
+// wait_phase by a whole warp, with one answer for it.
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, const WaitCtl &c, uint32_t site) {
+    return __all_sync(0xffffffffu, wait_phase(bar, parity, c, site));
+}
+
 // A sequence's rows, held inside the tensor and to the bound that the caller
 // gave: whatever the arrays hold, nothing outside is touched.
 __device__ __forceinline__ void attn_range(const int64_t *starts, const int64_t *lengths, int s,

@@ -3,7 +3,7 @@
 
 #include <atomic>
 #include "tg_attn.h"
-#include "tg_kernel_attn.cuh"
+#include "tg_kernel_attn_bwd.cuh"
 
 namespace tg {
 
@@ -52,6 +52,41 @@ static cudaError_t launch_attn_forward_kind(const AttnForward &a, int nq, int de
         e = nq == 2 ? launch_attn_one<KD, 128, 2>(a, device, stream) : launch_attn_one<KD, 128, 1>(a, device, stream);
     if (e != cudaSuccess || a.splits == 1) return e;
     return attn_launch<AttnForward>(tg_attn_join_kernel<KD>, (int64_t)a.tiles * a.h.kv_heads, 256, 0, stream, a);
+}
+
+template <Kind KD, int DT>
+static cudaError_t launch_attn_backward_dim(const AttnBackward &a, int device, cudaStream_t stream) {
+    using CK = AttnKeysConfig<KD, DT>;
+    using CR = AttnRowsConfig<KD, DT>;
+    static std::atomic<uint64_t> keys_done{0}, rows_done{0};
+    cudaError_t e = cudaSuccess;
+    if (a.dk.ptr || a.dv.ptr) {
+        e = attn_smem(tg_attn_keys_kernel<KD, DT>, CK::SMEM_BYTES, device, keys_done);
+        if (e != cudaSuccess) return e;
+        const int64_t grid = (int64_t)a.blocks * a.h.kv_heads;
+        if (grid > 0)
+            e = attn_launch<AttnBackward>(tg_attn_keys_kernel<KD, DT>, grid, CK::NUM_THREADS, CK::SMEM_BYTES, stream, a);
+    }
+    if (e == cudaSuccess && a.dq.ptr) {
+        e = attn_smem(tg_attn_rows_kernel<KD, DT>, CR::SMEM_BYTES, device, rows_done);
+        if (e != cudaSuccess) return e;
+        const int64_t grid = (int64_t)a.tiles * a.h.kv_heads;
+        if (grid > 0)
+            e = attn_launch<AttnBackward>(tg_attn_rows_kernel<KD, DT>, grid, CR::NUM_THREADS, CR::SMEM_BYTES, stream, a);
+    }
+    return e;
+}
+
+template <Kind KD>
+static cudaError_t launch_attn_backward_kind(const AttnBackward &a, const AttnDelta &d, int device,
+                                             cudaStream_t stream) {
+    if (d.rows > 0) {
+        const int64_t grid = ((int64_t)d.rows * d.heads + DELTA_THREADS / 16 - 1) / (DELTA_THREADS / 16);
+        const cudaError_t e = attn_launch<AttnDelta>(tg_attn_delta_kernel<KD>, grid, DELTA_THREADS, 0, stream, d);
+        if (e != cudaSuccess) return e;
+    }
+    return a.h.dim <= 64 ? launch_attn_backward_dim<KD, 64>(a, device, stream)
+                         : launch_attn_backward_dim<KD, 128>(a, device, stream);
 }
 
 }  // namespace tg

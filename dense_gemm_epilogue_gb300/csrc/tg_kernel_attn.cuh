@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(AttnConfig<KD, DT, NQ>::NUM_THREADS, 1)
             const int n = j - jb;
             const int slot = NQ == 2 ? t : n & 1;
             const uint32_t phase = NQ == 2 ? n & 1 : (n >> 1) & 1;
-            if (!wait_phase(bar(C::SF0 + slot), phase, ctl, SITE_SCORES)) { ok = false; break; }
+            if (!wait_warp(bar(C::SF0 + slot), phase, ctl, SITE_SCORES)) { ok = false; break; }
             tc_fence_after();
             uint32_t s[128];
             const uint32_t s_at = tmem + lane_base + slot * 128;
@@ -284,11 +284,13 @@ __global__ void __launch_bounds__(AttnConfig<KD, DT, NQ>::NUM_THREADS, 1)
 #pragma unroll
                 for (int i = 0; i < 128; ++i)
                     if (i >= lim) s[i] = 0xff800000u;
-                // Values behind the sequence's end: zero (see attn_zero_row).
+                // Values behind the sequence's end: zero (see attn_zero_row).  (The
+                // barrier is at most one phase behind: the thread that issued these
+                // scores has waited for the slot's earlier items.)
                 const int left = w.lk - j * ATTN_KEYS;
                 if (left < ATTN_KEYS) {
                     const int it = 2 * n + 1;
-                    if (!wait_phase(bar(C::FULL0 + it % S), (uint32_t)(it / S) & 1, ctl, SITE_FULL)) {
+                    if (!wait_warp(bar(C::FULL0 + it % S), (uint32_t)(it / S) & 1, ctl, SITE_FULL)) {
                         ok = false;
                         break;
                     }
@@ -310,7 +312,7 @@ __global__ void __launch_bounds__(AttnConfig<KD, DT, NQ>::NUM_THREADS, 1)
                 m = mn;
                 l *= f;
                 if (n > 0) {
-                    if (NQ == 1 && !wait_phase(bar(C::PVD), (n - 1) & 1, ctl, SITE_ACC_FULL)) {
+                    if (NQ == 1 && !wait_warp(bar(C::PVD), (n - 1) & 1, ctl, SITE_ACC_FULL)) {
                         ok = false;
                         break;
                     }
@@ -356,7 +358,7 @@ __global__ void __launch_bounds__(AttnConfig<KD, DT, NQ>::NUM_THREADS, 1)
         }
         const bool some = end > jb;
         if (ok && some) {
-            ok = wait_phase(bar(C::OD0 + t), 0, ctl, SITE_ACC_FULL);
+            ok = wait_warp(bar(C::OD0 + t), 0, ctl, SITE_ACC_FULL);
             tc_fence_after();
         }
         if (ok) {

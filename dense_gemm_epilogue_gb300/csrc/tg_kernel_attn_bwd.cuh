@@ -1,0 +1,664 @@
+// Attention backward over packed sequences:
+//   P = 2^(c s - LSE log2 e),  dP = dO V^T,  dS = P (dP - delta),  delta = sum_d dO O,
+//   dV = P^T dO,  dK = scale dS^T Q,  dQ = scale dS K
+// (s = q . k, c = scale log2 e), the heads of a group summed in dK and dV.
+//
+// Two kernels, each with its sums in tensor memory from the first term to the
+// last: one owns 128 keys and goes over the rows that see them (dK, dV: four
+// products a tile), one owns a tile of 128 rows and goes over its keys (dQ: three).
+// S and dP are computed in both, seven products where five are the least, and
+// for that no sum is added to memory by several CTAs: repeated calls agree bit
+// for bit, and nothing is cleared before or converted after.
+//
+// A row tile is the forward kernel's: `tokens` tokens x the group's heads, so the
+// keys' kernel adds up a group's heads as it adds up tokens.  P and dS are rounded
+// to 16 bits, as tensor-core operands; they stay in tensor memory.
+#pragma once
+
+#include "tg_kernel_attn.cuh"
+
+namespace tg {
+
+// delta = sum over d of dO O.
+template <Kind KD>
+__global__ void __launch_bounds__(DELTA_THREADS) tg_attn_delta_kernel(const __grid_constant__ AttnDelta p) {
+    griddep_launch();
+    griddep_wait();
+    // 16 lanes a row and head (8 values each): 16 of them a block, heads innermost.
+    const int lane = threadIdx.x & 15;
+    const int64_t i = (int64_t)blockIdx.x * (DELTA_THREADS / 16) + (threadIdx.x >> 4);
+    const int64_t row = i / p.heads;
+    const int head = (int)(i - row * p.heads);
+    float s = 0.0f;
+    if (row < p.rows && 8 * lane < p.dim) {
+        const uint4 a = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.o) + row * p.ldo +
+                                                         head * p.ho + 8 * lane);
+        const uint4 b = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.dy) + row * p.lddy +
+                                                         head * p.hdy + 8 * lane);
+        const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            float a0, a1, b0, b1;
+            unpack_half2<KD>(aw[q], a0, a1);
+            unpack_half2<KD>(bw[q], b0, b1);
+            s = fmaf(a0, b0, s);
+            s = fmaf(a1, b1, s);
+        }
+    }
+#pragma unroll
+    for (int o = 8; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (lane == 0 && row < p.rows) p.delta[(int64_t)head * p.rows + row] = s;
+}
+
+template <Kind KD, int DT>
+struct AttnBackConfig {
+    using T = KindTraits<KD>;
+    static constexpr int HALVES = DT / 64;
+    static constexpr int TILE_BYTES = HALVES * 128 * 128;
+    static constexpr int SOFT_WARPS = 8;
+    static constexpr int LOAD_WARP = 8, MMA_WARP = 9, ROWS_WARP = 10;
+    static constexpr int NUM_THREADS = 32 * 11;
+    static constexpr int TMEM_COLS = 512;
+    static constexpr uint32_t ID_BASE = (1u << 4) | (T::fmt << 7) | (T::fmt << 10) | ((128u >> 4) << 24);
+    static constexpr uint32_t ID_S = ID_BASE | ((128u >> 3) << 17);
+    static constexpr uint32_t ID_PV = ID_BASE | (1u << 16) | ((uint32_t)(DT >> 3) << 17);
+};
+
+// The keys' kernel: shared memory and tensor memory.
+template <Kind KD, int DT>
+struct AttnKeysConfig : AttnBackConfig<KD, DT> {
+    using B = AttnBackConfig<KD, DT>;
+    static constexpr int STAGES = 2;     // tiles of Q, and of dO
+    static constexpr int ROW_SLOTS = 3;  // rows' LSE, delta and keys seen
+    static constexpr int K_OFF = 0, V_OFF = B::TILE_BYTES, Q_OFF = 2 * B::TILE_BYTES;
+    static constexpr int DY_OFF = Q_OFF + STAGES * B::TILE_BYTES;
+    static constexpr int ROWS_OFF = DY_OFF + STAGES * B::TILE_BYTES;
+    static constexpr int BAR_OFF = ROWS_OFF + ROW_SLOTS * 1536;
+    static constexpr int KVF = 0, QF0 = 1, QE0 = QF0 + STAGES, DF0 = QE0 + STAGES, DE0 = DF0 + STAGES,
+                         SF = DE0 + STAGES, DPF = SF + 1, PR = DPF + 1, DSR = PR + 1, RF0 = DSR + 1,
+                         RE0 = RF0 + ROW_SLOTS, LAST = RE0 + ROW_SLOTS, OD = LAST + 2, DRAIN = OD + 1,
+                         NUM_BARS = DRAIN + 1;
+    static constexpr int MISC_OFF = BAR_OFF + NUM_BARS * 8;
+    static constexpr int SMEM_BYTES = MISC_OFF + 64 + 1024;
+    // 128-wide heads: P over S, dS over dP (each thread over the columns it has read).
+    static constexpr int S_COL = 0, DP_COL = 128, DV_COL = 256, DK_COL = 256 + DT;
+    static constexpr int P_COL = DT == 64 ? 384 : S_COL, DS_COL = DT == 64 ? 448 : DP_COL;
+    static constexpr int P_HALF = DT == 64 ? 32 : 64;  // columns from rows 0-63 to rows 64-127
+    static_assert(SMEM_BYTES <= SMEM_LIMIT, "shared memory budget");
+};
+
+template <int DT, int HALF>
+__device__ __forceinline__ void attn_mma_ta_halves(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
+                                                   bool accumulate) {
+#pragma unroll
+    for (int kk = 0; kk < 8; ++kk)
+        mma_f16_ta(d, a + (kk >> 2) * HALF + (kk & 3) * 8, smem_desc_mn_rows128(b + kk * 2048), idesc,
+                   accumulate || kk != 0);
+}
+
+// 64 FP32 values to 16 bits in 32 columns.
+template <Kind KD>
+__device__ __forceinline__ void attn_store_half(uint32_t at, const float *y) {
+    uint32_t w[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) w[i] = pack_half2<KD>(y[2 * i], y[2 * i + 1]);
+    tmem_st_32x32b_x32(at, w);
+    tmem_st_wait();
+}
+
+// `cols` columns from tensor memory, times f, to a 16-bit row of which `left` values exist.
+template <Kind KD, int COLS>
+__device__ __forceinline__ void attn_store_row(uint32_t at, bool some, float f, bool valid, int left,
+                                               uint16_t *dst) {
+#pragma unroll 1
+    for (int i = 0; i < COLS; i += 32) {
+        uint32_t o[32];
+        if (some) {
+            tmem_ld_row32(at + i, o);
+            tmem_ld_wait();
+        }
+        if (!valid) continue;
+#pragma unroll
+        for (int e = 0; e < 32; e += 8) {
+            if (i + e >= left) break;
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (some) {
+                uint32_t y[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    y[q] = pack_half2<KD>(__uint_as_float(o[e + 2 * q]) * f, __uint_as_float(o[e + 2 * q + 1]) * f);
+                v = make_uint4(y[0], y[1], y[2], y[3]);
+            }
+            *reinterpret_cast<uint4 *>(dst + i + e) = v;
+        }
+    }
+}
+
+template <Kind KD, int DT>
+__global__ void __launch_bounds__(AttnKeysConfig<KD, DT>::NUM_THREADS, 1)
+    tg_attn_keys_kernel(const __grid_constant__ AttnBackward p) {
+    using C = AttnKeysConfig<KD, DT>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    const uint32_t sbase = smem_u32(smem);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    auto bar = [&](int i) -> uint32_t { return sbase + C::BAR_OFF + 8 * i; };
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::MISC_OFF);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::MISC_OFF + 4);
+    AttnWork *shared_work = reinterpret_cast<AttnWork *>(smem + C::MISC_OFF + 8);
+    const WaitCtl ctl{abort_flag, p.status, p.wait_limit_ns};
+    const int box = p.h.tokens * p.h.group;  // rows of a tile that loads write
+
+    if (threadIdx.x == 0) {
+        mbar_init(bar(C::KVF), 1);
+        for (int s = 0; s < C::STAGES; ++s) {
+            mbar_init(bar(C::QF0 + s), 1);
+            mbar_init(bar(C::QE0 + s), 1);
+            mbar_init(bar(C::DF0 + s), 1);
+            mbar_init(bar(C::DE0 + s), 1);
+        }
+        mbar_init(bar(C::SF), 1);
+        mbar_init(bar(C::DPF), 1);
+        mbar_init(bar(C::PR), C::SOFT_WARPS);
+        mbar_init(bar(C::DSR), C::SOFT_WARPS);
+        for (int s = 0; s < C::ROW_SLOTS; ++s) {
+            mbar_init(bar(C::RF0 + s), 32);
+            mbar_init(bar(C::RE0 + s), C::SOFT_WARPS);
+        }
+        mbar_init(bar(C::LAST), 1);
+        mbar_init(bar(C::LAST + 1), 1);
+        mbar_init(bar(C::OD), 1);
+        mbar_init(bar(C::DRAIN), 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+        prefetch_tensormap(&p.q);
+        prefetch_tensormap(&p.dy);
+    }
+    // Rows that no load writes stay zero.
+    for (int i = threadIdx.x; i < 2 * C::STAGES * (ATTN_ROWS - box); i += C::NUM_THREADS)
+        attn_zero_row<C::HALVES>(smem + C::Q_OFF + (i / (ATTN_ROWS - box)) * C::TILE_BYTES,
+                                 box + i % (ATTN_ROWS - box));
+    fence_proxy_async_smem();
+    if (warp == C::MMA_WARP) {
+        tmem_alloc(smem_u32(tmem_slot), C::TMEM_COLS);
+        tmem_relinquish();
+    }
+    griddep_launch();
+    griddep_wait();
+    const int head = blockIdx.x % p.h.kv_heads;
+    if (warp == C::LOAD_WARP) {
+        const AttnWork w = attn_find<true>(p.s, blockIdx.x / p.h.kv_heads, ATTN_KEYS, lane);
+        if (lane == 0) *shared_work = w;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const AttnWork w = *shared_work;
+    // Tokens from i0 on see some of the keys.
+    int i0 = p.s.causal ? w.first - w.lk + w.lq : 0;
+    if (i0 < 0) i0 = 0;
+    const int tiles = w.seq >= 0 && i0 < w.lq ? (w.lq - i0 + p.h.tokens - 1) / p.h.tokens : 0;
+    const int tail = (w.lq - i0 - (tiles - 1) * p.h.tokens) * p.h.group;  // rows of the last tile
+    const bool fix = tiles > 0 && tail < box;
+    auto q_tile = [&](int n) -> int { return C::Q_OFF + n % C::STAGES * C::TILE_BYTES; };
+    auto dy_tile = [&](int n) -> int { return C::DY_OFF + n % C::STAGES * C::TILE_BYTES; };
+    auto parity = [&](int n) -> uint32_t { return (uint32_t)(n / C::STAGES) & 1; };
+    // Where the loads of tile n report: a last tile that ends inside reports to
+    // ROWS_WARP, which passes it on once the rest is zero.
+    auto landed = [&](int f0, int n) -> uint32_t {
+        return bar(fix && n == tiles - 1 ? (f0 == C::QF0 ? C::LAST : C::LAST + 1) : f0 + n % C::STAGES);
+    };
+    auto landed_parity = [&](int n) -> uint32_t { return fix && n == tiles - 1 ? 0 : parity(n); };
+
+    if (warp == C::LOAD_WARP) {
+        if (lane == 0 && tiles > 0) {
+            const uint32_t bytes = C::HALVES * box * 128;
+            mbar_arrive_expect_tx(bar(C::KVF), 2 * C::TILE_BYTES);
+#pragma unroll
+            for (int h = 0; h < C::HALVES; ++h) {
+                tma_load_3d(sbase + C::K_OFF + h * 16384, &p.k, bar(C::KVF), h * 64, head, w.k0 + w.first);
+                tma_load_3d(sbase + C::V_OFF + h * 16384, &p.v, bar(C::KVF), h * 64, head, w.k0 + w.first);
+            }
+            int q_n = 0, dy_n = 0;
+            bool ok = true;
+            for (int n = 0; n < tiles; ++n) {
+                const int s = n % C::STAGES, row = w.q0 + i0 + n * p.h.tokens;
+                if (!wait_phase(bar(C::QE0 + s), parity(n) ^ 1, ctl, SITE_EMPTY)) { ok = false; break; }
+                mbar_arrive_expect_tx(landed(C::QF0, n), bytes);
+                for (int h = 0; h < C::HALVES; ++h)
+                    tma_load_4d(sbase + q_tile(n) + h * 16384, &p.q, landed(C::QF0, n), h * 64, 0, head, row);
+                ++q_n;
+                if (!wait_phase(bar(C::DE0 + s), parity(n) ^ 1, ctl, SITE_EMPTY)) { ok = false; break; }
+                mbar_arrive_expect_tx(landed(C::DF0, n), bytes);
+                for (int h = 0; h < C::HALVES; ++h)
+                    tma_load_4d(sbase + dy_tile(n) + h * 16384, &p.dy, landed(C::DF0, n), h * 64, 0, head, row);
+                ++dy_n;
+            }
+            if (!ok) {
+                // Every copy already issued lands before the CTA exits.
+                wait_phase_drain(bar(C::KVF), 0, ctl);
+                for (int n = q_n > C::STAGES ? q_n - C::STAGES : 0; n < q_n; ++n)
+                    wait_phase_drain(landed(C::QF0, n), landed_parity(n), ctl);
+                for (int n = dy_n > C::STAGES ? dy_n - C::STAGES : 0; n < dy_n; ++n)
+                    wait_phase_drain(landed(C::DF0, n), landed_parity(n), ctl);
+            }
+        }
+        __syncwarp();
+    } else if (warp == C::MMA_WARP) {
+        if (lane == 0 && tiles > 0) {
+            auto full = [&](int f0, int n) -> bool {
+                const bool ok = wait_phase(bar(f0 + n % C::STAGES), parity(n), ctl, SITE_FULL);
+                tc_fence_after();
+                return ok;
+            };
+            auto scores = [&](int n) {
+                attn_mma_rows<DT>(tmem + C::S_COL, sbase + C::K_OFF, sbase + q_tile(n), C::ID_S);
+                mma_commit(bar(C::SF));
+            };
+            auto gradients = [&](int n) {
+                attn_mma_rows<DT>(tmem + C::DP_COL, sbase + C::V_OFF, sbase + dy_tile(n), C::ID_S);
+                mma_commit(bar(C::DPF));
+            };
+            bool ok = wait_phase(bar(C::KVF), 0, ctl, SITE_FULL) && full(C::QF0, 0);
+            if (ok) {
+                scores(0);
+                ok = full(C::DF0, 0);
+                if (ok) gradients(0);
+            }
+            for (int n = 0; ok && n < tiles; ++n) {
+                // While the warps turn S into P the tensor core runs dK and dP, and
+                // while they turn dP into dS, dV and the next S.
+                if (!wait_phase(bar(C::PR), n & 1, ctl, SITE_PROBABILITIES)) { ok = false; break; }
+                tc_fence_after();
+                attn_mma_ta_halves<DT, C::P_HALF>(tmem + C::DV_COL, tmem + C::P_COL, sbase + dy_tile(n), C::ID_PV,
+                                                  n > 0);
+                mma_commit(bar(C::DE0 + n % C::STAGES));
+                if (n + 1 < tiles) {
+                    if (!full(C::QF0, n + 1)) { ok = false; break; }
+                    scores(n + 1);
+                }
+                if (!wait_phase(bar(C::DSR), n & 1, ctl, SITE_PROBABILITIES)) { ok = false; break; }
+                tc_fence_after();
+                attn_mma_ta_halves<DT, C::P_HALF>(tmem + C::DK_COL, tmem + C::DS_COL, sbase + q_tile(n), C::ID_PV,
+                                                  n > 0);
+                mma_commit(bar(C::QE0 + n % C::STAGES));
+                if (n + 1 < tiles) {
+                    if (!full(C::DF0, n + 1)) { ok = false; break; }
+                    gradients(n + 1);
+                }
+            }
+            mma_commit(bar(ok ? C::OD : C::DRAIN));
+            if (!ok) wait_phase_drain(bar(C::DRAIN), 0, ctl);
+        }
+        __syncwarp();
+    } else if (warp == C::ROWS_WARP) {
+        // ------------------------------------------------------ the rows' LSE, delta, keys seen
+        for (int n = 0; n < tiles; ++n) {
+            const int s = n % C::ROW_SLOTS;
+            if (!wait_warp(bar(C::RE0 + s), (uint32_t)(n / C::ROW_SLOTS + 1) & 1, ctl, SITE_EMPTY)) break;
+            float *lse = reinterpret_cast<float *>(smem + C::ROWS_OFF + s * 1536);
+            float *delta = lse + 128;
+            int *seen = reinterpret_cast<int *>(lse + 256);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int row = lane + 32 * q, token = i0 + n * p.h.tokens + row / p.h.group;
+                // A row that is none, or sees nothing: P = 2^(-infinity) = 0.
+                float l = INFINITY, d = 0.0f;
+                int k = 0;
+                if (row < box && token < w.lq) {
+                    const int64_t at =
+                        (int64_t)(head * p.h.group + row % p.h.group) * p.s.q_rows + w.q0 + token;
+                    const float z = p.lse[at];
+                    if (z != -INFINITY) l = z * 1.4426950408889634f;
+                    d = p.delta[at];
+                    k = attn_seen(p.s, w, token);
+                }
+                lse[row] = -l;
+                delta[row] = -d;
+                seen[row] = k;
+            }
+            mbar_arrive(bar(C::RF0 + s));
+            if (fix && n == tiles - 1) {
+                // Rows of other sequences, in the last tile, become zero.
+                if (!wait_warp(bar(C::LAST), 0, ctl, SITE_FULL)) break;
+                for (int row = tail + lane; row < box; row += 32) attn_zero_row<C::HALVES>(smem + q_tile(n), row);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(C::QF0 + n % C::STAGES));
+                if (!wait_warp(bar(C::LAST + 1), 0, ctl, SITE_FULL)) break;
+                for (int row = tail + lane; row < box; row += 32) attn_zero_row<C::HALVES>(smem + dy_tile(n), row);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(C::DF0 + n % C::STAGES));
+            }
+        }
+        __syncwarp();
+    } else if (w.seq >= 0) {
+        // ------------------------------------------------------ a key a thread, 64 rows of it
+        const int half = warp >> 2;
+        const uint32_t lane_base = (uint32_t)(warp & 3) << 21;
+        const int key = w.first + (threadIdx.x & 127);
+        const float c = p.h.scale_log2;
+        const uint64_t cc = pair2(c, c);
+        bool ok = true;
+        for (int n = 0; n < tiles; ++n) {
+            const int s = n % C::ROW_SLOTS;
+            const float *rows = reinterpret_cast<const float *>(smem + C::ROWS_OFF + s * 1536) + 64 * half;
+            ok = wait_warp(bar(C::RF0 + s), (uint32_t)(n / C::ROW_SLOTS) & 1, ctl, SITE_FULL) &&
+                 wait_warp(bar(C::SF), n & 1, ctl, SITE_SCORES);
+            if (!ok) break;
+            tc_fence_after();
+            float y[64];
+            uint32_t *yw = reinterpret_cast<uint32_t *>(y);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) tmem_ld_row32(tmem + lane_base + C::S_COL + 64 * half + 32 * i, yw + 32 * i);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 64; i += 4) {
+                const float4 l = *reinterpret_cast<const float4 *>(rows + i);
+                unpair2(fma_pair(pair2(y[i], y[i + 1]), cc, pair2(l.x, l.y)), y[i], y[i + 1]);
+                unpair2(fma_pair(pair2(y[i + 2], y[i + 3]), cc, pair2(l.z, l.w)), y[i + 2], y[i + 3]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[i + e] = exp2_approx(y[i + e]);
+            }
+            // Some rows of the tile do not see all of the keys.
+            if (p.s.causal && attn_seen(p.s, w, i0 + n * p.h.tokens) < w.first + ATTN_KEYS) {
+                const int *seen = reinterpret_cast<const int *>(rows + 256);
+#pragma unroll
+                for (int i = 0; i < 64; ++i)
+                    if (key >= seen[i]) y[i] = 0.0f;
+            }
+            attn_store_half<KD>(tmem + lane_base + C::P_COL + C::P_HALF * half, y);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(C::PR));
+
+            ok = wait_warp(bar(C::DPF), n & 1, ctl, SITE_SCORES);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int i = 0; i < 64; i += 32) {
+                uint32_t d[32];
+                tmem_ld_row32(tmem + lane_base + C::DP_COL + 64 * half + i, d);
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 32; e += 4) {
+                    const float4 z = *reinterpret_cast<const float4 *>(rows + 128 + i + e);
+                    const float *f = reinterpret_cast<const float *>(d) + e;
+                    uint64_t a = mul_pair(pair2(y[i + e], y[i + e + 1]), add_pair(pair2(f[0], f[1]), pair2(z.x, z.y)));
+                    unpair2(a, y[i + e], y[i + e + 1]);
+                    a = mul_pair(pair2(y[i + e + 2], y[i + e + 3]), add_pair(pair2(f[2], f[3]), pair2(z.z, z.w)));
+                    unpair2(a, y[i + e + 2], y[i + e + 3]);
+                }
+            }
+            attn_store_half<KD>(tmem + lane_base + C::DS_COL + C::P_HALF * half, y);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(bar(C::DSR));
+                mbar_arrive(bar(C::RE0 + s));
+            }
+        }
+        if (ok && tiles > 0) {
+            ok = wait_warp(bar(C::OD), 0, ctl, SITE_ACC_FULL);
+            tc_fence_after();
+        }
+        const AttnOut &out = half ? p.dk : p.dv;
+        if (ok && out.ptr)
+            attn_store_row<KD, DT>(tmem + lane_base + (half ? C::DK_COL : C::DV_COL), tiles > 0,
+                                   half ? p.h.scale : 1.0f, key < w.lk, p.h.dim,
+                                   static_cast<uint16_t *>(out.ptr) + (w.k0 + (int64_t)key) * out.ld + head * out.hd);
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == C::MMA_WARP) {
+        tc_fence_after();
+        tmem_dealloc(tmem, C::TMEM_COLS);
+    }
+}
+
+// The rows' kernel.
+template <Kind KD, int DT>
+struct AttnRowsConfig : AttnBackConfig<KD, DT> {
+    using B = AttnBackConfig<KD, DT>;
+    static constexpr int FIT = (SMEM_LIMIT - 2048 - 2 * B::TILE_BYTES) / B::TILE_BYTES;
+    static constexpr int STAGES = FIT > 8 ? 8 : FIT;
+    static constexpr int Q_OFF = 0, DY_OFF = B::TILE_BYTES, KV_OFF = 2 * B::TILE_BYTES;
+    static constexpr int BAR_OFF = KV_OFF + STAGES * B::TILE_BYTES;
+    static constexpr int QF = 0, FULL0 = 1, EMPTY0 = FULL0 + STAGES, SF = EMPTY0 + STAGES, SE = SF + 1,
+                         DPF = SE + 1, DSR = DPF + 1, LAST = DSR + 1, OD = LAST + 2, DRAIN = OD + 1,
+                         NUM_BARS = DRAIN + 1;
+    static constexpr int MISC_OFF = BAR_OFF + NUM_BARS * 8;
+    static constexpr int SMEM_BYTES = MISC_OFF + 64 + 1024;
+    static constexpr int S_COL = 0, DP_COL = 128, DQ_COL = 256, DS_COL = 384;  // dS twice, 64 columns each
+    static_assert(SMEM_BYTES <= SMEM_LIMIT && STAGES >= 5, "shared memory budget");
+};
+
+template <Kind KD, int DT>
+__global__ void __launch_bounds__(AttnRowsConfig<KD, DT>::NUM_THREADS, 1)
+    tg_attn_rows_kernel(const __grid_constant__ AttnBackward p) {
+    using C = AttnRowsConfig<KD, DT>;
+    constexpr int S = C::STAGES;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    const uint32_t sbase = smem_u32(smem);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    auto bar = [&](int i) -> uint32_t { return sbase + C::BAR_OFF + 8 * i; };
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::MISC_OFF);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::MISC_OFF + 4);
+    AttnWork *shared_work = reinterpret_cast<AttnWork *>(smem + C::MISC_OFF + 8);
+    const WaitCtl ctl{abort_flag, p.status, p.wait_limit_ns};
+
+    if (threadIdx.x == 0) {
+        mbar_init(bar(C::QF), 1);
+        for (int s = 0; s < S; ++s) {
+            mbar_init(bar(C::FULL0 + s), 1);
+            mbar_init(bar(C::EMPTY0 + s), 1);
+        }
+        mbar_init(bar(C::SF), 1);
+        mbar_init(bar(C::SE), C::SOFT_WARPS);
+        mbar_init(bar(C::DPF), 1);
+        mbar_init(bar(C::DSR), C::SOFT_WARPS);
+        mbar_init(bar(C::LAST), 1);
+        mbar_init(bar(C::LAST + 1), 1);
+        mbar_init(bar(C::OD), 1);
+        mbar_init(bar(C::DRAIN), 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+        prefetch_tensormap(&p.k);
+        prefetch_tensormap(&p.v);
+    }
+    if (warp == C::MMA_WARP) {
+        tmem_alloc(smem_u32(tmem_slot), C::TMEM_COLS);
+        tmem_relinquish();
+    }
+    griddep_launch();
+    griddep_wait();
+    const int head = blockIdx.x % p.h.kv_heads;
+    if (warp == C::LOAD_WARP) {
+        const AttnWork w = attn_find<false>(p.s, p.tiles - 1 - blockIdx.x / p.h.kv_heads, p.h.tokens, lane);
+        if (lane == 0) *shared_work = w;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const AttnWork w = *shared_work;
+    const int end = w.first + p.h.tokens < w.lq ? w.first + p.h.tokens : w.lq;
+    const int seen_last = w.seq >= 0 ? attn_seen(p.s, w, end - 1) : 0;
+    const int blocks = (seen_last + ATTN_KEYS - 1) / ATTN_KEYS;
+    const int tail = w.lk - (blocks - 1) * ATTN_KEYS;  // keys of the sequence in the last block
+    const bool fix = blocks > 0 && tail < ATTN_KEYS;
+    auto tile = [&](int it) -> int { return C::KV_OFF + it % S * C::TILE_BYTES; };
+    auto parity = [&](int it) -> uint32_t { return (uint32_t)(it / S) & 1; };
+    // Where item `it`'s loads report: a last block that ends inside reports to
+    // ROWS_WARP, which passes it on once the rest is zero.
+    auto landed = [&](int it) -> uint32_t {
+        return bar(fix && (it >> 1) == blocks - 1 ? C::LAST + (it & 1) : C::FULL0 + it % S);
+    };
+
+    if (warp == C::LOAD_WARP) {
+        if (lane == 0 && blocks > 0) {
+            mbar_arrive_expect_tx(bar(C::QF), 2 * C::HALVES * p.h.tokens * p.h.group * 128);
+#pragma unroll
+            for (int h = 0; h < C::HALVES; ++h) {
+                tma_load_4d(sbase + C::Q_OFF + h * 16384, &p.q, bar(C::QF), h * 64, 0, head, w.q0 + w.first);
+                tma_load_4d(sbase + C::DY_OFF + h * 16384, &p.dy, bar(C::QF), h * 64, 0, head, w.q0 + w.first);
+            }
+            int issued = 0;
+            bool ok = true;
+            for (int it = 0; it < 2 * blocks; ++it) {
+                const int s = it % S;
+                if (!wait_phase(bar(C::EMPTY0 + s), parity(it) ^ 1, ctl, SITE_EMPTY)) { ok = false; break; }
+                mbar_arrive_expect_tx(landed(it), C::TILE_BYTES);
+#pragma unroll
+                for (int h = 0; h < C::HALVES; ++h)
+                    tma_load_3d(sbase + tile(it) + h * 16384, it & 1 ? &p.v : &p.k, landed(it), h * 64,
+                                head, w.k0 + (it >> 1) * ATTN_KEYS);
+                ++issued;
+            }
+            if (!ok) {
+                wait_phase_drain(bar(C::QF), 0, ctl);
+                for (int it = issued > S ? issued - S : 0; it < issued; ++it)
+                    wait_phase_drain(landed(it), fix && (it >> 1) == blocks - 1 ? 0 : parity(it), ctl);
+            }
+        }
+        __syncwarp();
+    } else if (warp == C::MMA_WARP) {
+        if (lane == 0 && blocks > 0) {
+            auto full = [&](int it) -> bool {
+                const bool ok = wait_phase(bar(C::FULL0 + it % S), parity(it), ctl, SITE_FULL);
+                tc_fence_after();
+                return ok;
+            };
+            auto scores = [&](int n) {
+                attn_mma_rows<DT>(tmem + C::S_COL, sbase + C::Q_OFF, sbase + tile(2 * n), C::ID_S);
+                mma_commit(bar(C::SF));
+            };
+            auto gradients = [&](int n) {
+                attn_mma_rows<DT>(tmem + C::DP_COL, sbase + C::DY_OFF, sbase + tile(2 * n + 1), C::ID_S);
+                mma_commit(bar(C::DPF));
+                mma_commit(bar(C::EMPTY0 + (2 * n + 1) % S));
+            };
+            bool ok = wait_phase(bar(C::QF), 0, ctl, SITE_FULL) && full(0);
+            if (ok) {
+                scores(0);
+                ok = full(1);
+                if (ok) gradients(0);
+            }
+            for (int n = 0; ok && n < blocks; ++n) {
+                if (n + 1 < blocks) {
+                    // (once the warps hold the scores of block n)
+                    ok = wait_phase(bar(C::SE), n & 1, ctl, SITE_PROBABILITIES) && full(2 * n + 2);
+                    if (!ok) break;
+                    scores(n + 1);
+                }
+                if (!wait_phase(bar(C::DSR), n & 1, ctl, SITE_PROBABILITIES)) { ok = false; break; }
+                tc_fence_after();
+                if (n + 1 < blocks) {
+                    if (!full(2 * n + 3)) { ok = false; break; }
+                    gradients(n + 1);
+                }
+                attn_mma_ta_halves<DT, 32>(tmem + C::DQ_COL, tmem + C::DS_COL + (n & 1) * 64, sbase + tile(2 * n),
+                                           C::ID_PV, n > 0);
+                mma_commit(bar(C::EMPTY0 + (2 * n) % S));
+            }
+            mma_commit(bar(ok ? C::OD : C::DRAIN));
+            if (!ok) wait_phase_drain(bar(C::DRAIN), 0, ctl);
+        }
+        __syncwarp();
+    } else if (warp == C::ROWS_WARP) {
+        // Keys and values behind the sequence's end become zero.
+        for (int i = 0; fix && i < 2; ++i) {
+            const int it = 2 * (blocks - 1) + i;
+            if (!wait_warp(bar(C::LAST + i), 0, ctl, SITE_FULL)) break;
+            for (int row = tail + lane; row < ATTN_KEYS; row += 32) attn_zero_row<C::HALVES>(smem + tile(it), row);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(C::FULL0 + it % S));
+        }
+        __syncwarp();
+    } else if (w.seq >= 0) {
+        // ------------------------------------------------------ a row a thread, 64 keys of a block
+        const int half = warp >> 2, row = threadIdx.x & 127;
+        const uint32_t lane_base = (uint32_t)(warp & 3) << 21;
+        const int token = w.first + row / p.h.group, qh = head * p.h.group + row % p.h.group;
+        const bool valid = row < p.h.tokens * p.h.group && token < w.lq;
+        const int seen = valid ? attn_seen(p.s, w, token) : 0;
+        const int first_seen = attn_seen(p.s, w, w.first);
+        float lse = -INFINITY, delta = 0.0f;
+        if (valid) {
+            const int64_t at = (int64_t)qh * p.s.q_rows + w.q0 + token;
+            const float z = p.lse[at];
+            if (z != -INFINITY) lse = -z * 1.4426950408889634f;
+            delta = -p.delta[at];
+        }
+        const uint64_t cc = pair2(p.h.scale_log2, p.h.scale_log2), ll = pair2(lse, lse), dd = pair2(delta, delta);
+        bool ok = true;
+        for (int n = 0; n < blocks; ++n) {
+            ok = wait_warp(bar(C::SF), n & 1, ctl, SITE_SCORES);
+            if (!ok) break;
+            tc_fence_after();
+            float y[64];
+            uint32_t *yw = reinterpret_cast<uint32_t *>(y);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) tmem_ld_row32(tmem + lane_base + C::S_COL + 64 * half + 32 * i, yw + 32 * i);
+            tmem_ld_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(C::SE));
+#pragma unroll
+            for (int i = 0; i < 64; i += 2) {
+                unpair2(fma_pair(pair2(y[i], y[i + 1]), cc, ll), y[i], y[i + 1]);
+                y[i] = exp2_approx(y[i]);
+                y[i + 1] = exp2_approx(y[i + 1]);
+            }
+            if ((n + 1) * ATTN_KEYS > first_seen) {
+                const int lim = seen - n * ATTN_KEYS - 64 * half;
+#pragma unroll
+                for (int i = 0; i < 64; ++i)
+                    if (i >= lim) y[i] = 0.0f;
+            }
+            ok = wait_warp(bar(C::DPF), n & 1, ctl, SITE_SCORES);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int i = 0; i < 64; i += 32) {
+                uint32_t d[32];
+                tmem_ld_row32(tmem + lane_base + C::DP_COL + 64 * half + i, d);
+                tmem_ld_wait();
+                const float *f = reinterpret_cast<const float *>(d);
+#pragma unroll
+                for (int e = 0; e < 32; e += 2)
+                    unpair2(mul_pair(pair2(y[i + e], y[i + e + 1]), add_pair(pair2(f[e], f[e + 1]), dd)), y[i + e],
+                            y[i + e + 1]);
+            }
+            attn_store_half<KD>(tmem + lane_base + C::DS_COL + (n & 1) * 64 + 32 * half, y);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(C::DSR));
+        }
+        if (ok && blocks > 0) {
+            ok = wait_warp(bar(C::OD), 0, ctl, SITE_ACC_FULL);
+            tc_fence_after();
+        }
+        if (ok)
+            attn_store_row<KD, DT / 2>(tmem + lane_base + C::DQ_COL + half * (DT / 2), blocks > 0, p.h.scale, valid,
+                                       p.h.dim - half * (DT / 2),
+                                       static_cast<uint16_t *>(p.dq.ptr) + (w.q0 + (int64_t)token) * p.dq.ld +
+                                           qh * p.dq.hd + half * (DT / 2));
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == C::MMA_WARP) {
+        tc_fence_after();
+        tmem_dealloc(tmem, C::TMEM_COLS);
+    }
+}
+
+}  // namespace tg

@@ -627,6 +627,31 @@ tg_status tg_attention(int64_t seqs, int64_t q_rows, int64_t k_rows, int64_t hea
                        int64_t workspace_bytes, void *stream);
 
 /*
+ * Gradients of the attention from dO, with the forward's O and LSE:
+ *   P = exp(S - LSE),  dP = dO V^T,  dS = P (dP - sum over d of dO O),
+ *   dV = P^T dO,  dQ = scale dS K,  dK = scale dS^T Q,
+ * dK and dV summed over the query heads of a key head.  dQ, dK and dV may each
+ * be NULL.  Layout, limits and alignment are tg_attention's; P and dS are rounded
+ * to dtype where the products read them (in FP16, dS below 2^-25 is lost: scale
+ * the loss).  Keys that no row sees, and rows without keys, get zeros; the key
+ * ranges of two sequences may not overlap.  No atomics: repeated calls agree bit
+ * for bit.
+ */
+int64_t tg_attention_backward_workspace_bytes(int64_t seqs, int64_t q_rows, int64_t k_rows,
+                                              int64_t heads, int64_t kv_heads, int64_t dim,
+                                              int64_t max_q, int64_t max_k, tg_dtype dtype);
+tg_status tg_attention_backward(int64_t seqs, int64_t q_rows, int64_t k_rows, int64_t heads,
+                                int64_t kv_heads, int64_t dim, const void *Q, int64_t ldq, int64_t hq,
+                                const void *K, int64_t ldk, int64_t hk, const void *V, int64_t ldv,
+                                int64_t hv, const void *O, int64_t ldo, int64_t ho, const void *dO,
+                                int64_t lddo, int64_t hdo, const float *LSE, const int64_t *q_starts,
+                                const int64_t *q_lengths, const int64_t *k_starts,
+                                const int64_t *k_lengths, int64_t max_q, int64_t max_k, int32_t causal,
+                                float scale, void *dQ, int64_t lddq, int64_t hdq, void *dK, int64_t lddk,
+                                int64_t hdk, void *dV, int64_t lddv, int64_t hdv, tg_dtype dtype,
+                                void *workspace, int64_t workspace_bytes, void *stream);
+
+/*
  * The planner's choice for one product of the feed-forward operators, as one line of
  * text (host only when num_sms > 0; num_sms <= 0 queries the current device):
  * a forward product, or dX or dW of the backward call with both asked for.

@@ -15,7 +15,11 @@ the 16-bit type (relative 2^-8 BF16, 2^-11 FP16):
   kernels' 32 a block and one for each block and range: (64 + n/32) 2^-23;
 * a product with V (or dO, K, Q) over n terms: (n/8 + 32) 2^-23 of the sum of
   magnitudes, and n/128 rescalings of the accumulator at 2^-22 each;
-* the result's rounding: U of the value, 2^-25 for FP16.
+* the result's rounding: U of the value, 2^-25 for FP16;
+* the hardware exponential gives 0 for a result below FP32's smallest normal
+  number, so a probability below 2^-126 is off by all of itself, less than 2^-126
+  (in FP16 2^-25 covers it).  In the gradients, which start from LSE, such
+  probabilities meet no larger one in a key's sum: 2^-126 stands in for 2^-25.
 """
 
 from __future__ import annotations
@@ -26,7 +30,7 @@ import torch
 
 TYPES = {"bf16": torch.bfloat16, "fp16": torch.float16}
 U = {"bf16": 2.0 ** -8, "fp16": 2.0 ** -11}
-TINY = {"bf16": 0.0, "fp16": 2.0 ** -25}
+TINY = {"bf16": 2.0 ** -126, "fp16": 2.0 ** -25}
 
 
 def gen(seed):
@@ -221,3 +225,81 @@ def check_forward(tg, p, what="attention"):
     assert o.kept_outside(rows), what + ": rows of no sequence were written"
     assert bool(torch.isnan(z[:, ~rows]).all()), what + ": LSE of no sequence was written"
     return o, z
+
+
+# ------------------------------------------------------------------ backward
+
+
+def given(p):
+    """The forward's O, rounded to the type, and LSE, as the backward pass reads them."""
+    o, _, lse, _ = reference(p)
+    rows = p.rows()
+    x = Tensor3(p.q_rows, p.heads, p.dim, p.dtype, **p.shape)
+    x.t[rows] = o[rows].to(TYPES[p.dtype])
+    z = lse.float()
+    z[:, ~rows] = float("nan")
+    return x, z
+
+
+def reference_backward(p, o, lse):
+    """{name: (gradient, its bound)}."""
+    f64 = dict(dtype=torch.float64, device="cuda")
+    u, tiny = U[p.dtype], TINY[p.dtype]
+    dq, dk, dv = (torch.zeros(r, h, p.dim, **f64) for r, h in ((p.q_rows, p.heads), (p.k_rows, p.kv), (p.k_rows, p.kv)))
+    eq, ek, ev, mq, mk, mv = (torch.zeros_like(x) for x in (dq, dk, dv, dq, dk, dv))
+    od, dod = o.d(), p.dO.d()
+    for rows, keys, h, kh, s, e, see in p.pieces():
+        z = lse[h, rows].double()[:, None]
+        q, k, v, do = p.Q.d()[rows, h], p.K.d()[keys, kh], p.V.d()[keys, kh], dod[rows, h]
+        some = z != -math.inf
+        w = torch.where(see & some, torch.exp(s - z), 0.0)
+        rel = torch.where(see, e + 2.0 ** -22 * (s.abs() + z.abs()), 0.0) + 2.0 ** -21
+        rel = torch.where(some, rel, 0.0)
+        ep = torch.where(see, w * (rel + u) + tiny, 0.0)
+        delta = (do * od[rows, h]).sum(1, keepdim=True)
+        dp = do @ v.t() - delta
+        short = (p.dim / 8 + 32) * 2.0 ** -23
+        edp = short * (do.abs() @ v.abs().t() + (do * od[rows, h]).abs().sum(1, keepdim=True)) + 2.0 ** -23 * dp.abs()
+        ds = w * dp
+        eds = w * (1 + rel) * edp + ds.abs() * (rel + 2.0 ** -22 + u)
+        eds = torch.where(see & some, eds + u * eds + tiny, 0.0)
+        dv[keys, kh] += w.t() @ do
+        ev[keys, kh] += ep.t() @ do.abs()
+        mv[keys, kh] += w.t() @ do.abs()
+        dk[keys, kh] += p.scale * (ds.t() @ q)
+        ek[keys, kh] += p.scale * (eds.t() @ q.abs())
+        mk[keys, kh] += p.scale * (ds.abs().t() @ q.abs())
+        dq[rows, h] = p.scale * (ds @ k)
+        eq[rows, h] = p.scale * (eds @ k.abs())
+        mq[rows, h] = p.scale * (ds.abs() @ k.abs())
+    out = {}
+    for name, x, e, m, n in (("dQ", dq, eq, mq, max(p.k_len + [0])),
+                             ("dK", dk, ek, mk, p.g * max(p.q_len + [0])),
+                             ("dV", dv, ev, mv, p.g * max(p.q_len + [0]))):
+        e = e + (n / 8 + 32) * 2.0 ** -23 * m + 2.0 ** -23 * x.abs()
+        out[name] = (x, e + u * (x.abs() + e) + tiny)
+    return out
+
+
+def run_backward(tg, p, o, lse, want=("dQ", "dK", "dV")):
+    out = {"dQ": Tensor3(p.q_rows, p.heads, p.dim, p.dtype, **p.shape),
+           "dK": Tensor3(p.k_rows, p.kv, p.dim, p.dtype, **p.shape),
+           "dV": Tensor3(p.k_rows, p.kv, p.dim, p.dtype, **p.shape)}
+    lay = [x for n in ("dQ", "dK", "dV") for x in (out[n].lay if n in want else (None, 0, 0))]
+    ws = space(tg.tg_attention_backward_workspace_bytes(*p.sizes(), p.max_q, p.max_k, p.dtype))
+    done(tg, tg.tg_attention_backward(*p.sizes(), *p.Q.lay, *p.K.lay, *p.V.lay, *o.lay, *p.dO.lay, lse,
+                                      *p.arrays(), p.max_q, p.max_k, p.causal, p.scale, *lay, p.dtype, ws,
+                                      torch.cuda.current_stream()), "tg_attention_backward")
+    return out
+
+
+def check_backward(tg, p, what="attention_backward"):
+    o, lse = given(p)
+    out = run_backward(tg, p, o, lse)
+    want = reference_backward(p, o, lse)
+    for name, got in out.items():
+        rows = p.rows(keys=name != "dQ")
+        x, bound = want[name]
+        check(got.t[rows], x[rows], bound[rows], f"{what} {name}")
+        assert got.kept_outside(rows), f"{what} {name}: rows of no sequence were written"
+    return out
