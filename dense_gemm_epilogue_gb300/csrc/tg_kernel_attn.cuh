@@ -39,12 +39,13 @@ struct AttnConfig {
     static constexpr int KV_OFF = NQ * TILE_BYTES;
     static constexpr int BAR_OFF = KV_OFF + STAGES * TILE_BYTES;
     static constexpr int QF = 0, FULL0 = 1, EMPTY0 = FULL0 + STAGES, SF0 = EMPTY0 + STAGES, PR0 = SF0 + 2,
-                         OD0 = PR0 + 2, PVD = OD0 + 2, DRAIN = PVD + 1, NUM_BARS = DRAIN + 1;
+                         PH0 = PR0 + 2, OD0 = PH0 + 2, PVD = OD0 + 2, TURN0 = PVD + 1, DRAIN0 = TURN0 + 2,
+                         NUM_BARS = DRAIN0 + 2;
     static constexpr int MISC_OFF = BAR_OFF + NUM_BARS * 8;
     static constexpr int SMEM_BYTES = MISC_OFF + 64 + 1024;
     static constexpr int SOFT_WARPS = 4 * NQ;
     static constexpr int LOAD_WARP = SOFT_WARPS, MMA_WARP = SOFT_WARPS + 1;
-    static constexpr int NUM_THREADS = 32 * (SOFT_WARPS + 2);
+    static constexpr int NUM_THREADS = 32 * (SOFT_WARPS + 1 + NQ);  // an MMA warp a tile
     static constexpr int TMEM_COLS = 512;
     static constexpr int O_COL = 256;
     static constexpr int P_COL = DT == 64 ? O_COL + NQ * DT : 0;  // (DT == 128: over S)
@@ -58,18 +59,22 @@ struct AttnConfig {
 // S (128 x 128) = A (rows of DT) B^T (rows of DT), both K-major tiles of 64-value boxes.
 template <int DT>
 __device__ __forceinline__ void attn_mma_rows(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc) {
+    const uint64_t da = smem_desc_sw128(a), db = smem_desc_sw128(b);
 #pragma unroll
     for (int kk = 0; kk < DT / 16; ++kk) {
-        const uint32_t at = (kk >> 2) * 16384 + (kk & 3) * 32;
-        mma_f16(d, smem_desc_sw128(a + at), smem_desc_sw128(b + at), idesc, kk != 0);
+        const int at = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
+        mma_f16(d, da + at, db + at, idesc, kk != 0);
     }
 }
-// D (128 x N) (+)= A (tensor memory, 128 reduction values) B (MN-major tile of 128 rows).
+// D (128 x N) (+)= A (tensor memory) B (MN-major tile of 128 rows), over the
+// reduction values 16 K0 to 16 K1; HALF: columns from A's value 0 to its value 64.
+template <int K0, int K1, int HALF>
 __device__ __forceinline__ void attn_mma_ta(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
                                             bool accumulate) {
+    const uint64_t db = smem_desc_mn_rows128(b);
 #pragma unroll
-    for (int kk = 0; kk < 8; ++kk)
-        mma_f16_ta(d, a + kk * 8, smem_desc_mn_rows128(b + kk * 2048), idesc, accumulate || kk != 0);
+    for (int kk = K0; kk < K1; ++kk)
+        mma_f16_ta(d, a + (kk >> 2) * HALF + (kk & 3) * 8, db + kk * (2048 >> 4), idesc, kk ? 1 : accumulate);
 }
 
 // Zeroes rows `from` to 127 of a tile: rows behind a sequence's end hold others'
@@ -104,15 +109,17 @@ __global__ void __launch_bounds__(AttnConfig<KD, DT, NQ>::NUM_THREADS, 1)
         mbar_init(bar(C::QF), 1);
         for (int s = 0; s < S; ++s) {
             mbar_init(bar(C::FULL0 + s), 1);
-            mbar_init(bar(C::EMPTY0 + s), 1);
+            mbar_init(bar(C::EMPTY0 + s), NQ);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar(C::SF0 + i), 1);
             mbar_init(bar(C::PR0 + i), 4);
+            mbar_init(bar(C::PH0 + i), 4);
             mbar_init(bar(C::OD0 + i), 1);
+            mbar_init(bar(C::TURN0 + i), 1);
+            mbar_init(bar(C::DRAIN0 + i), 1);
         }
         mbar_init(bar(C::PVD), 1);
-        mbar_init(bar(C::DRAIN), 1);
         *abort_flag = 0;
         fence_mbar_init();
         prefetch_tensormap(&p.q);
@@ -155,7 +162,7 @@ __global__ void __launch_bounds__(AttnConfig<KD, DT, NQ>::NUM_THREADS, 1)
     }
 
     if (warp == C::LOAD_WARP) {
-        if (lane == 0 && last > jb) {
+        if (last > jb && elect_one()) {
             mbar_arrive_expect_tx(bar(C::QF), NQ * C::HALVES * p.h.tokens * p.h.group * 128);
 #pragma unroll
             for (int t = 0; t < NQ; ++t)
@@ -186,71 +193,95 @@ __global__ void __launch_bounds__(AttnConfig<KD, DT, NQ>::NUM_THREADS, 1)
             }
         }
         __syncwarp();
-    } else if (warp == C::MMA_WARP) {
-        if (lane == 0 && last > jb) {
-            auto tile = [&](int it) -> uint32_t { return sbase + C::KV_OFF + (it % S) * C::TILE_BYTES; };
-            auto full = [&](int it) -> bool {
-                const bool ok = wait_phase(bar(C::FULL0 + it % S), (uint32_t)(it / S) & 1, ctl, SITE_FULL);
+    } else if (warp >= C::MMA_WARP) {
+        // A thread for each tile's products: while one waits for its probabilities
+        // the other's are in the tensor core's queue, which holds only a few (with
+        // one thread for both, 0.3 of the time was between a wait and the next MMA).
+        // They take turns, a tile's P V and next S at a time: mixed, both tiles'
+        // scores would be ready at once and both tiles' softmax stand idle at once.
+        const int t = warp - C::MMA_WARP;
+        if (last > jb && elect_one()) {
+            const int mine = (NQ == 2 && t ? je[NQ - 1] : je[0]) - jb, all = last - jb;
+            const uint32_t q = sbase + C::Q_OFF + t * C::TILE_BYTES;
+            const uint32_t o = tmem + C::O_COL + t * DT;
+            // The ring's items in order: K, V, K, V, ...
+            struct Ring {
+                int s = 0;
+                uint32_t ph = 0;
+                __device__ void next() {
+                    if (++s == S) { s = 0; ph ^= 1; }
+                }
+            } k, v;  // the next K, the next V
+            v.next();
+            auto tile = [&](const Ring &r) -> uint32_t { return sbase + C::KV_OFF + r.s * C::TILE_BYTES; };
+            auto full = [&](const Ring &r) -> bool {
+                const bool ok = wait_phase(bar(C::FULL0 + r.s), r.ph, ctl, SITE_FULL);
                 tc_fence_after();
                 return ok;
             };
-            auto scores = [&](int t, int slot, int it) {
-                attn_mma_rows<DT>(tmem + slot * 128, sbase + C::Q_OFF + t * C::TILE_BYTES, tile(it), C::ID_S);
+            auto release = [&](Ring &r) {
+                mma_commit(bar(C::EMPTY0 + r.s));
+                r.next();
+                r.next();
+            };
+            auto scores = [&](int slot) {
+                attn_mma_rows<DT>(tmem + slot * 128, q, tile(k), C::ID_S);
                 mma_commit(bar(C::SF0 + slot));
             };
-            auto values = [&](int t, int slot, int it, bool more) {
-                attn_mma_ta(tmem + C::O_COL + t * DT, tmem + C::P_COL + slot * C::P_STEP, tile(it), C::ID_PV,
-                            more);
+            uint32_t turns = t;  // of the other thread's awaited so far, odd for t = 1
+            auto turn = [&]() -> bool {
+                if (NQ == 1) return true;
+                const uint32_t n = turns++;  // (t = 0 begins: it awaits the other's n - 1)
+                return n == 0 || wait_phase(bar(C::TURN0 + t), (n - 1) & 1, ctl, SITE_ACC_EMPTY);
             };
-            bool ok = wait_phase(bar(C::QF), 0, ctl, SITE_FULL) && full(0);
+            auto pass = [&] {
+                if (NQ == 2) mbar_arrive(bar(C::TURN0 + (t ^ 1)));
+            };
+            bool ok = wait_phase(bar(C::QF), 0, ctl, SITE_FULL) && full(k) && turn();
             if (ok) {
-                if constexpr (NQ == 2) {
-#pragma unroll
-                    for (int t = 0; t < NQ; ++t)
-                        if (je[t] > jb) scores(t, t, 0);
-                } else {
-                    scores(0, 0, 0);
-                }
-                mma_commit(bar(C::EMPTY0));
+                if (mine > 0) scores(NQ == 2 ? t : 0);
+                release(k);
+                pass();
             }
-            for (int j = jb; ok && j < last; ++j) {
-                const int n = j - jb, kn = 2 * n + 2;
-                if constexpr (NQ == 2) {
-                    const int last_t = j < je[1] ? 1 : 0;
-#pragma unroll
-                    for (int t = 0; t < NQ; ++t) {
-                        if (!ok || j >= je[t]) continue;
-                        ok = wait_phase(bar(C::PR0 + t), n & 1, ctl, SITE_PROBABILITIES) && full(2 * n + 1);
-                        if (!ok) break;
-                        values(t, t, 2 * n + 1, n > 0);
-                        if (t == last_t) mma_commit(bar(C::EMPTY0 + (2 * n + 1) % S));
-                        if (j + 1 < je[t]) {
-                            ok = full(kn);
-                            if (!ok) break;
-                            scores(t, t, kn);
-                        } else {
-                            mma_commit(bar(C::OD0 + t));
-                        }
-                    }
-                    if (ok && j + 1 < last) mma_commit(bar(C::EMPTY0 + kn % S));
-                } else {
-                    if (j + 1 < last) {
-                        ok = full(kn);
-                        if (!ok) break;
-                        scores(0, (n + 1) & 1, kn);
-                        mma_commit(bar(C::EMPTY0 + kn % S));
-                    }
-                    ok = wait_phase(bar(C::PR0 + (n & 1)), (n >> 1) & 1, ctl, SITE_PROBABILITIES) &&
-                         full(2 * n + 1);
+            for (int n = 0; ok && n < all; ++n) {
+                const int slot = NQ == 2 ? t : n & 1;
+                const uint32_t phase = NQ == 2 ? n & 1 : (n >> 1) & 1;
+                if (NQ == 1 && n + 1 < all) {
+                    ok = full(k);
                     if (!ok) break;
-                    values(0, n & 1, 2 * n + 1, n > 0);
-                    mma_commit(bar(C::EMPTY0 + (2 * n + 1) % S));
-                    mma_commit(bar(j + 1 < last ? C::PVD : C::OD0));
+                    scores((n + 1) & 1);
+                    release(k);
                 }
+                ok = full(v);
+                if (!ok) break;
+                if (n < mine) {
+                    const uint32_t pr = tmem + C::P_COL + slot * C::P_STEP;
+                    ok = wait_phase(bar(C::PH0 + slot), phase, ctl, SITE_PROBABILITIES) && turn();
+                    if (!ok) break;
+                    tc_fence_after();
+                    attn_mma_ta<0, 4, 32>(o, pr, tile(v), C::ID_PV, n > 0);
+                    ok = wait_phase(bar(C::PR0 + slot), phase, ctl, SITE_PROBABILITIES);
+                    if (!ok) break;
+                    tc_fence_after();
+                    attn_mma_ta<4, 8, 32>(o, pr, tile(v), C::ID_PV, true);
+                } else {
+                    ok = turn();
+                    if (!ok) break;
+                }
+                release(v);
+                if (NQ == 1 && n + 1 < all) mma_commit(bar(C::PVD));
+                if (n + 1 == mine) mma_commit(bar(C::OD0 + t));
+                if (NQ == 2 && n + 1 < all) {
+                    ok = full(k);
+                    if (!ok) break;
+                    if (n + 1 < mine) scores(slot);
+                    release(k);
+                }
+                pass();
             }
             if (!ok) {
-                mma_commit(bar(C::DRAIN));
-                wait_phase_drain(bar(C::DRAIN), 0, ctl);
+                mma_commit(bar(C::DRAIN0 + t));
+                wait_phase_drain(bar(C::DRAIN0 + t), 0, ctl);
             }
         }
         __syncwarp();
@@ -274,16 +305,32 @@ __global__ void __launch_bounds__(AttnConfig<KD, DT, NQ>::NUM_THREADS, 1)
             const uint32_t phase = NQ == 2 ? n & 1 : (n >> 1) & 1;
             if (!wait_warp(bar(C::SF0 + slot), phase, ctl, SITE_SCORES)) { ok = false; break; }
             tc_fence_after();
-            uint32_t s[128];
             const uint32_t s_at = tmem + lane_base + slot * 128;
+            // Two readings of S, for the maximum and for the exponentials, 64 columns
+            // at a time: all 128 at once left the CTA's registers short.
+            const bool cut = (j + 1) * ATTN_KEYS > first_seen;
+            const int lim = cut ? seen - j * ATTN_KEYS : ATTN_KEYS;
+            float mn = m;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) tmem_ld_row32(s_at + 32 * i, s + 32 * i);
-            tmem_ld_wait();
-            if ((j + 1) * ATTN_KEYS > first_seen) {
-                const int lim = seen - j * ATTN_KEYS;
+            for (int h = 0; h < 128; h += 64) {
+                uint32_t s[64];
+                tmem_ld_row32(s_at + h, s);
+                tmem_ld_row32(s_at + h + 32, s + 32);
+                tmem_ld_wait();
+                if (cut) {
 #pragma unroll
-                for (int i = 0; i < 128; ++i)
-                    if (i >= lim) s[i] = 0xff800000u;
+                    for (int i = 0; i < 64; ++i)
+                        if (h + i >= lim) s[i] = 0xff800000u;
+                }
+                float mx[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) mx[i] = max3(__uint_as_float(s[3 * i]), __uint_as_float(s[3 * i + 1]), __uint_as_float(s[3 * i + 2]));
+#pragma unroll
+                for (int i = 12; i < 64; i += 2)
+                    mx[(i >> 1) & 3] = max3(mx[(i >> 1) & 3], __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
+                mn = max3(mn, max3(mx[0], mx[1], mx[2]), mx[3]);
+            }
+            if (cut) {
                 // Values behind the sequence's end: zero (see attn_zero_row).  (The
                 // barrier is at most one phase behind: the thread that issued these
                 // scores has waited for the slot's earlier items.)
@@ -300,12 +347,6 @@ __global__ void __launch_bounds__(AttnConfig<KD, DT, NQ>::NUM_THREADS, 1)
                     }
                 }
             }
-            float mx[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) mx[i] = __uint_as_float(s[i]);
-#pragma unroll
-            for (int i = 4; i < 128; ++i) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(s[i]));
-            const float mn = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
             // (Every lane keeps its reference unless one has outgrown it.)
             if (__any_sync(0xffffffffu, (mn - m) * c > 8.0f)) {
                 const float f = mn == m ? 1.0f : exp2_approx((m - mn) * c);
@@ -334,24 +375,32 @@ __global__ void __launch_bounds__(AttnConfig<KD, DT, NQ>::NUM_THREADS, 1)
             uint64_t sum[2] = {0, 0};
             const uint32_t p_at = tmem + lane_base + C::P_COL + slot * C::P_STEP;
 #pragma unroll
-            for (int h = 0; h < 4; ++h) {
-                uint32_t y[16];
+            for (int h = 0; h < 128; h += 64) {
+                uint32_t s[64], y[32];
+                tmem_ld_row32(s_at + h, s);
+                tmem_ld_row32(s_at + h + 32, s + 32);
+                tmem_ld_wait();
+                if (cut) {
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int e = 32 * h + 2 * i;
+                    for (int i = 0; i < 64; ++i)
+                        if (h + i >= lim) s[i] = 0xff800000u;
+                }
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
                     float a, b;
-                    unpair2(fma_pair(pair2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), cc, mm), a, b);
+                    unpair2(fma_pair(pair2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), cc, mm), a, b);
                     a = exp2_approx(a);
                     b = exp2_approx(b);
                     sum[i & 1] = add_pair(sum[i & 1], pair2(a, b));
                     y[i] = pack_half2<KD>(a, b);
                 }
-                tmem_st_32x32b_x16(p_at + 16 * h, y);
+                // (P over S: columns 0 to 31 and 32 to 63, both read by now.)
+                tmem_st_32x32b_x32(p_at + h / 2, y);
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar((h ? C::PR0 : C::PH0) + slot));
             }
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(C::PR0 + slot));
             float a, b;
             unpair2(add_pair(sum[0], sum[1]), a, b);
             l += a + b;

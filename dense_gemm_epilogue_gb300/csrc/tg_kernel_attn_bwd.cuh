@@ -56,8 +56,8 @@ struct AttnBackConfig {
     static constexpr int HALVES = DT / 64;
     static constexpr int TILE_BYTES = HALVES * 128 * 128;
     static constexpr int SOFT_WARPS = 8;
-    static constexpr int LOAD_WARP = 8, MMA_WARP = 9, ROWS_WARP = 10;
-    static constexpr int NUM_THREADS = 32 * 11;
+    static constexpr int LOAD_WARP = 8, MMA_WARP = 9, MMA2_WARP = 10, ROWS_WARP = 11;
+    static constexpr int NUM_THREADS = 32 * 12;
     static constexpr int TMEM_COLS = 512;
     static constexpr uint32_t ID_BASE = (1u << 4) | (T::fmt << 7) | (T::fmt << 10) | ((128u >> 4) << 24);
     static constexpr uint32_t ID_S = ID_BASE | ((128u >> 3) << 17);
@@ -77,7 +77,7 @@ struct AttnKeysConfig : AttnBackConfig<KD, DT> {
     static constexpr int KVF = 0, QF0 = 1, QE0 = QF0 + STAGES, DF0 = QE0 + STAGES, DE0 = DF0 + STAGES,
                          SF = DE0 + STAGES, DPF = SF + 1, PR = DPF + 1, DSR = PR + 1, RF0 = DSR + 1,
                          RE0 = RF0 + ROW_SLOTS, LAST = RE0 + ROW_SLOTS, OD = LAST + 2, DRAIN = OD + 1,
-                         NUM_BARS = DRAIN + 1;
+                         NUM_BARS = DRAIN + 2;
     static constexpr int MISC_OFF = BAR_OFF + NUM_BARS * 8;
     static constexpr int SMEM_BYTES = MISC_OFF + 64 + 1024;
     // 128-wide heads: P over S, dS over dP (each thread over the columns it has read).
@@ -86,15 +86,6 @@ struct AttnKeysConfig : AttnBackConfig<KD, DT> {
     static constexpr int P_HALF = DT == 64 ? 32 : 64;  // columns from rows 0-63 to rows 64-127
     static_assert(SMEM_BYTES <= SMEM_LIMIT, "shared memory budget");
 };
-
-template <int DT, int HALF>
-__device__ __forceinline__ void attn_mma_ta_halves(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
-                                                   bool accumulate) {
-#pragma unroll
-    for (int kk = 0; kk < 8; ++kk)
-        mma_f16_ta(d, a + (kk >> 2) * HALF + (kk & 3) * 8, smem_desc_mn_rows128(b + kk * 2048), idesc,
-                   accumulate || kk != 0);
-}
 
 // 64 FP32 values to 16 bits in 32 columns.
 template <Kind KD>
@@ -156,7 +147,7 @@ __global__ void __launch_bounds__(AttnKeysConfig<KD, DT>::NUM_THREADS, 1)
             mbar_init(bar(C::QF0 + s), 1);
             mbar_init(bar(C::QE0 + s), 1);
             mbar_init(bar(C::DF0 + s), 1);
-            mbar_init(bar(C::DE0 + s), 1);
+            mbar_init(bar(C::DE0 + s), 2);
         }
         mbar_init(bar(C::SF), 1);
         mbar_init(bar(C::DPF), 1);
@@ -168,8 +159,9 @@ __global__ void __launch_bounds__(AttnKeysConfig<KD, DT>::NUM_THREADS, 1)
         }
         mbar_init(bar(C::LAST), 1);
         mbar_init(bar(C::LAST + 1), 1);
-        mbar_init(bar(C::OD), 1);
+        mbar_init(bar(C::OD), 2);
         mbar_init(bar(C::DRAIN), 1);
+        mbar_init(bar(C::DRAIN + 1), 1);
         *abort_flag = 0;
         fence_mbar_init();
         prefetch_tensormap(&p.q);
@@ -213,7 +205,7 @@ __global__ void __launch_bounds__(AttnKeysConfig<KD, DT>::NUM_THREADS, 1)
     auto landed_parity = [&](int n) -> uint32_t { return fix && n == tiles - 1 ? 0 : parity(n); };
 
     if (warp == C::LOAD_WARP) {
-        if (lane == 0 && tiles > 0) {
+        if (tiles > 0 && elect_one()) {
             const uint32_t bytes = C::HALVES * box * 128;
             mbar_arrive_expect_tx(bar(C::KVF), 2 * C::TILE_BYTES);
 #pragma unroll
@@ -246,8 +238,13 @@ __global__ void __launch_bounds__(AttnKeysConfig<KD, DT>::NUM_THREADS, 1)
             }
         }
         __syncwarp();
-    } else if (warp == C::MMA_WARP) {
-        if (lane == 0 && tiles > 0) {
+    } else if (warp == C::MMA_WARP || warp == C::MMA2_WARP) {
+        // Two threads, for the products that wait for P (dV, then the next S, over
+        // the same columns) and those that wait for dS (dK, then the next dP): while
+        // one waits, the other's are in the tensor core's short queue.  The warps turn
+        // S into P while dK and dP run, and dP into dS while dV and S do.
+        const bool first = warp == C::MMA_WARP;
+        if (tiles > 0 && elect_one()) {
             auto full = [&](int f0, int n) -> bool {
                 const bool ok = wait_phase(bar(f0 + n % C::STAGES), parity(n), ctl, SITE_FULL);
                 tc_fence_after();
@@ -260,37 +257,41 @@ __global__ void __launch_bounds__(AttnKeysConfig<KD, DT>::NUM_THREADS, 1)
             auto gradients = [&](int n) {
                 attn_mma_rows<DT>(tmem + C::DP_COL, sbase + C::V_OFF, sbase + dy_tile(n), C::ID_S);
                 mma_commit(bar(C::DPF));
-            };
-            bool ok = wait_phase(bar(C::KVF), 0, ctl, SITE_FULL) && full(C::QF0, 0);
-            if (ok) {
-                scores(0);
-                ok = full(C::DF0, 0);
-                if (ok) gradients(0);
-            }
-            for (int n = 0; ok && n < tiles; ++n) {
-                // While the warps turn S into P the tensor core runs dK and dP, and
-                // while they turn dP into dS, dV and the next S.
-                if (!wait_phase(bar(C::PR), n & 1, ctl, SITE_PROBABILITIES)) { ok = false; break; }
-                tc_fence_after();
-                attn_mma_ta_halves<DT, C::P_HALF>(tmem + C::DV_COL, tmem + C::P_COL, sbase + dy_tile(n), C::ID_PV,
-                                                  n > 0);
                 mma_commit(bar(C::DE0 + n % C::STAGES));
-                if (n + 1 < tiles) {
-                    if (!full(C::QF0, n + 1)) { ok = false; break; }
-                    scores(n + 1);
+            };
+            bool ok = wait_phase(bar(C::KVF), 0, ctl, SITE_FULL) && full(first ? C::QF0 : C::DF0, 0);
+            if (first) {
+                if (ok) scores(0);
+                for (int n = 0; ok && n < tiles; ++n) {
+                    ok = full(C::DF0, n) && wait_phase(bar(C::PR), n & 1, ctl, SITE_PROBABILITIES);
+                    if (!ok) break;
+                    tc_fence_after();
+                    attn_mma_ta<0, 8, C::P_HALF>(tmem + C::DV_COL, tmem + C::P_COL, sbase + dy_tile(n), C::ID_PV,
+                                                 n > 0);
+                    mma_commit(bar(C::DE0 + n % C::STAGES));
+                    if (n + 1 < tiles) {
+                        ok = full(C::QF0, n + 1);
+                        if (ok) scores(n + 1);
+                    }
                 }
-                if (!wait_phase(bar(C::DSR), n & 1, ctl, SITE_PROBABILITIES)) { ok = false; break; }
-                tc_fence_after();
-                attn_mma_ta_halves<DT, C::P_HALF>(tmem + C::DK_COL, tmem + C::DS_COL, sbase + q_tile(n), C::ID_PV,
-                                                  n > 0);
-                mma_commit(bar(C::QE0 + n % C::STAGES));
-                if (n + 1 < tiles) {
-                    if (!full(C::DF0, n + 1)) { ok = false; break; }
-                    gradients(n + 1);
+            } else {
+                if (ok) gradients(0);
+                for (int n = 0; ok && n < tiles; ++n) {
+                    ok = full(C::QF0, n) && wait_phase(bar(C::DSR), n & 1, ctl, SITE_PROBABILITIES);
+                    if (!ok) break;
+                    tc_fence_after();
+                    attn_mma_ta<0, 8, C::P_HALF>(tmem + C::DK_COL, tmem + C::DS_COL, sbase + q_tile(n), C::ID_PV,
+                                                 n > 0);
+                    mma_commit(bar(C::QE0 + n % C::STAGES));
+                    if (n + 1 < tiles) {
+                        ok = full(C::DF0, n + 1);
+                        if (ok) gradients(n + 1);
+                    }
                 }
             }
-            mma_commit(bar(ok ? C::OD : C::DRAIN));
-            if (!ok) wait_phase_drain(bar(C::DRAIN), 0, ctl);
+            const uint32_t end = bar(ok ? C::OD : C::DRAIN + (first ? 0 : 1));
+            mma_commit(end);
+            if (!ok) wait_phase_drain(end, 0, ctl);
         }
         __syncwarp();
     } else if (warp == C::ROWS_WARP) {
@@ -426,11 +427,14 @@ struct AttnRowsConfig : AttnBackConfig<KD, DT> {
     using B = AttnBackConfig<KD, DT>;
     static constexpr int FIT = (SMEM_LIMIT - 2048 - 2 * B::TILE_BYTES) / B::TILE_BYTES;
     static constexpr int STAGES = FIT > 8 ? 8 : FIT;
+    // Rings of their own: values are done with after dP, keys only after dQ, and a
+    // common ring held up the next values' load behind them.
+    static constexpr int KS = (STAGES + 1) / 2, VS = STAGES / 2;
     static constexpr int Q_OFF = 0, DY_OFF = B::TILE_BYTES, KV_OFF = 2 * B::TILE_BYTES;
     static constexpr int BAR_OFF = KV_OFF + STAGES * B::TILE_BYTES;
     static constexpr int QF = 0, FULL0 = 1, EMPTY0 = FULL0 + STAGES, SF = EMPTY0 + STAGES, SE = SF + 1,
                          DPF = SE + 1, DSR = DPF + 1, LAST = DSR + 1, OD = LAST + 2, DRAIN = OD + 1,
-                         NUM_BARS = DRAIN + 1;
+                         NUM_BARS = DRAIN + 2;
     static constexpr int MISC_OFF = BAR_OFF + NUM_BARS * 8;
     static constexpr int SMEM_BYTES = MISC_OFF + 64 + 1024;
     static constexpr int S_COL = 0, DP_COL = 128, DQ_COL = 256, DS_COL = 384;  // dS twice, 64 columns each
@@ -467,6 +471,7 @@ __global__ void __launch_bounds__(AttnRowsConfig<KD, DT>::NUM_THREADS, 1)
         mbar_init(bar(C::LAST + 1), 1);
         mbar_init(bar(C::OD), 1);
         mbar_init(bar(C::DRAIN), 1);
+        mbar_init(bar(C::DRAIN + 1), 1);
         *abort_flag = 0;
         fence_mbar_init();
         prefetch_tensormap(&p.k);
@@ -493,16 +498,20 @@ __global__ void __launch_bounds__(AttnRowsConfig<KD, DT>::NUM_THREADS, 1)
     const int blocks = (seen_last + ATTN_KEYS - 1) / ATTN_KEYS;
     const int tail = w.lk - (blocks - 1) * ATTN_KEYS;  // keys of the sequence in the last block
     const bool fix = blocks > 0 && tail < ATTN_KEYS;
-    auto tile = [&](int it) -> int { return C::KV_OFF + it % S * C::TILE_BYTES; };
-    auto parity = [&](int it) -> uint32_t { return (uint32_t)(it / S) & 1; };
+    // Item 2n is block n's keys, 2n + 1 its values.
+    auto slot = [&](int it) -> int { return it & 1 ? C::KS + (it >> 1) % C::VS : (it >> 1) % C::KS; };
+    auto tile = [&](int it) -> int { return C::KV_OFF + slot(it) * C::TILE_BYTES; };
+    auto parity = [&](int it) -> uint32_t {
+        return (uint32_t)(it & 1 ? (it >> 1) / C::VS : (it >> 1) / C::KS) & 1;
+    };
     // Where item `it`'s loads report: a last block that ends inside reports to
     // ROWS_WARP, which passes it on once the rest is zero.
     auto landed = [&](int it) -> uint32_t {
-        return bar(fix && (it >> 1) == blocks - 1 ? C::LAST + (it & 1) : C::FULL0 + it % S);
+        return bar(fix && (it >> 1) == blocks - 1 ? C::LAST + (it & 1) : C::FULL0 + slot(it));
     };
 
     if (warp == C::LOAD_WARP) {
-        if (lane == 0 && blocks > 0) {
+        if (blocks > 0 && elect_one()) {
             mbar_arrive_expect_tx(bar(C::QF), 2 * C::HALVES * p.h.tokens * p.h.group * 128);
 #pragma unroll
             for (int h = 0; h < C::HALVES; ++h) {
@@ -512,8 +521,7 @@ __global__ void __launch_bounds__(AttnRowsConfig<KD, DT>::NUM_THREADS, 1)
             int issued = 0;
             bool ok = true;
             for (int it = 0; it < 2 * blocks; ++it) {
-                const int s = it % S;
-                if (!wait_phase(bar(C::EMPTY0 + s), parity(it) ^ 1, ctl, SITE_EMPTY)) { ok = false; break; }
+                if (!wait_phase(bar(C::EMPTY0 + slot(it)), parity(it) ^ 1, ctl, SITE_EMPTY)) { ok = false; break; }
                 mbar_arrive_expect_tx(landed(it), C::TILE_BYTES);
 #pragma unroll
                 for (int h = 0; h < C::HALVES; ++h)
@@ -523,52 +531,55 @@ __global__ void __launch_bounds__(AttnRowsConfig<KD, DT>::NUM_THREADS, 1)
             }
             if (!ok) {
                 wait_phase_drain(bar(C::QF), 0, ctl);
-                for (int it = issued > S ? issued - S : 0; it < issued; ++it)
-                    wait_phase_drain(landed(it), fix && (it >> 1) == blocks - 1 ? 0 : parity(it), ctl);
+                for (int it = issued > 2 * C::KS ? issued - 2 * C::KS : 0; it < issued; ++it)
+                    if (it + 2 * (it & 1 ? C::VS : C::KS) >= issued)
+                        wait_phase_drain(landed(it), fix && (it >> 1) == blocks - 1 ? 0 : parity(it), ctl);
             }
         }
         __syncwarp();
-    } else if (warp == C::MMA_WARP) {
-        if (lane == 0 && blocks > 0) {
+    } else if (warp == C::MMA_WARP || warp == C::MMA2_WARP) {
+        // Two threads: one for S, a block ahead, one for dP and dQ.
+        const bool first = warp == C::MMA_WARP;
+        if (blocks > 0 && elect_one()) {
             auto full = [&](int it) -> bool {
-                const bool ok = wait_phase(bar(C::FULL0 + it % S), parity(it), ctl, SITE_FULL);
+                const bool ok = wait_phase(bar(C::FULL0 + slot(it)), parity(it), ctl, SITE_FULL);
                 tc_fence_after();
                 return ok;
             };
-            auto scores = [&](int n) {
-                attn_mma_rows<DT>(tmem + C::S_COL, sbase + C::Q_OFF, sbase + tile(2 * n), C::ID_S);
-                mma_commit(bar(C::SF));
-            };
-            auto gradients = [&](int n) {
-                attn_mma_rows<DT>(tmem + C::DP_COL, sbase + C::DY_OFF, sbase + tile(2 * n + 1), C::ID_S);
-                mma_commit(bar(C::DPF));
-                mma_commit(bar(C::EMPTY0 + (2 * n + 1) % S));
-            };
-            bool ok = wait_phase(bar(C::QF), 0, ctl, SITE_FULL) && full(0);
-            if (ok) {
-                scores(0);
-                ok = full(1);
-                if (ok) gradients(0);
-            }
-            for (int n = 0; ok && n < blocks; ++n) {
-                if (n + 1 < blocks) {
-                    // (once the warps hold the scores of block n)
-                    ok = wait_phase(bar(C::SE), n & 1, ctl, SITE_PROBABILITIES) && full(2 * n + 2);
+            bool ok = wait_phase(bar(C::QF), 0, ctl, SITE_FULL);
+            if (first) {
+                for (int n = 0; ok && n < blocks; ++n) {
+                    // (once the warps hold the scores of the block before)
+                    ok = full(2 * n) && (n == 0 || wait_phase(bar(C::SE), (n - 1) & 1, ctl, SITE_PROBABILITIES));
                     if (!ok) break;
-                    scores(n + 1);
+                    tc_fence_after();
+                    attn_mma_rows<DT>(tmem + C::S_COL, sbase + C::Q_OFF, sbase + tile(2 * n), C::ID_S);
+                    mma_commit(bar(C::SF));
                 }
-                if (!wait_phase(bar(C::DSR), n & 1, ctl, SITE_PROBABILITIES)) { ok = false; break; }
-                tc_fence_after();
-                if (n + 1 < blocks) {
-                    if (!full(2 * n + 3)) { ok = false; break; }
-                    gradients(n + 1);
+            } else {
+                for (int n = 0; ok && n <= blocks; ++n) {
+                    if (n < blocks) ok = full(2 * n + 1);
+                    if (ok && n > 0) ok = wait_phase(bar(C::DSR), (n - 1) & 1, ctl, SITE_PROBABILITIES);
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (n < blocks) {
+                        attn_mma_rows<DT>(tmem + C::DP_COL, sbase + C::DY_OFF, sbase + tile(2 * n + 1), C::ID_S);
+                        mma_commit(bar(C::DPF));
+                        mma_commit(bar(C::EMPTY0 + slot(2 * n + 1)));
+                    }
+                    if (n > 0) {
+                        const int m = n - 1;
+                        attn_mma_ta<0, 8, 32>(tmem + C::DQ_COL, tmem + C::DS_COL + (m & 1) * 64, sbase + tile(2 * m),
+                                              C::ID_PV, m > 0);
+                        mma_commit(bar(C::EMPTY0 + slot(2 * m)));
+                    }
                 }
-                attn_mma_ta_halves<DT, 32>(tmem + C::DQ_COL, tmem + C::DS_COL + (n & 1) * 64, sbase + tile(2 * n),
-                                           C::ID_PV, n > 0);
-                mma_commit(bar(C::EMPTY0 + (2 * n) % S));
             }
-            mma_commit(bar(ok ? C::OD : C::DRAIN));
-            if (!ok) wait_phase_drain(bar(C::DRAIN), 0, ctl);
+            if (!ok || !first) {
+                const uint32_t end = bar(ok ? C::OD : C::DRAIN + (first ? 0 : 1));
+                mma_commit(end);
+                if (!ok) wait_phase_drain(end, 0, ctl);
+            }
         }
         __syncwarp();
     } else if (warp == C::ROWS_WARP) {
@@ -579,7 +590,7 @@ __global__ void __launch_bounds__(AttnRowsConfig<KD, DT>::NUM_THREADS, 1)
             for (int row = tail + lane; row < ATTN_KEYS; row += 32) attn_zero_row<C::HALVES>(smem + tile(it), row);
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar(C::FULL0 + it % S));
+            if (lane == 0) mbar_arrive(bar(C::FULL0 + slot(it)));
         }
         __syncwarp();
     } else if (w.seq >= 0) {
