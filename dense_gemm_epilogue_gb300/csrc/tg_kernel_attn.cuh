@@ -56,12 +56,13 @@ struct AttnConfig {
     static_assert(SMEM_BYTES <= SMEM_LIMIT && STAGES >= 4, "shared memory budget");
 };
 
-// S (128 x 128) = A (rows of DT) B^T (rows of DT), both K-major tiles of 64-value boxes.
-template <int DT>
+// S (128 x 128) = A (rows of DT) B^T (rows of DT), both K-major tiles of 64-value boxes
+// (the 16-value steps K0 to K1 of the reduction).
+template <int K0, int K1>
 __device__ __forceinline__ void attn_mma_rows(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc) {
     const uint64_t da = smem_desc_sw128(a), db = smem_desc_sw128(b);
 #pragma unroll
-    for (int kk = 0; kk < DT / 16; ++kk) {
+    for (int kk = K0; kk < K1; ++kk) {
         const int at = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
         mma_f16(d, da + at, db + at, idesc, kk != 0);
     }
@@ -225,7 +226,7 @@ __global__ void __launch_bounds__(AttnConfig<KD, DT, NQ>::NUM_THREADS, 1)
                 r.next();
             };
             auto scores = [&](int slot) {
-                attn_mma_rows<DT>(tmem + slot * 128, q, tile(k), C::ID_S);
+                attn_mma_rows<0, DT / 16>(tmem + slot * 128, q, tile(k), C::ID_S);
                 mma_commit(bar(C::SF0 + slot));
             };
             uint32_t turns = t;  // of the other thread's awaited so far, odd for t = 1

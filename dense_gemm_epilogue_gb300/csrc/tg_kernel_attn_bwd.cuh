@@ -62,21 +62,58 @@ struct AttnBackConfig {
     static constexpr uint32_t ID_BASE = (1u << 4) | (T::fmt << 7) | (T::fmt << 10) | ((128u >> 4) << 24);
     static constexpr uint32_t ID_S = ID_BASE | ((128u >> 3) << 17);
     static constexpr uint32_t ID_PV = ID_BASE | (1u << 16) | ((uint32_t)(DT >> 3) << 17);
+    static constexpr uint32_t ID_64 = ID_BASE | (1u << 16) | ((64u >> 3) << 17);  // half the columns
 };
+
+// -LSE/scale and -delta come into S and dP as products: the keys' kernel has a key a
+// thread, and reading 64 rows' values from shared memory for every tile took 1100
+// of its 3500 cycles, against MMAs that read shared memory all the time.  Instead
+// one more MMA (16 values of the reduction index) adds weights x parts: a value in
+// up to four parts v = sum w_i v_i, each a 16-bit number, good to 2^-24 of v
+// (BF16: w = 1; FP16: 2^15, 2^5, 2^-5, 2^-15, for |v| below 2^31).
+template <Kind KD>
+__device__ __forceinline__ uint4 attn_parts(float v) {
+    constexpr bool BF = KD == Kind::BF16;
+    float part[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float w = BF ? 1.0f : i == 0 ? 32768.0f : i == 1 ? 32.0f : i == 2 ? 0.03125f : 3.0517578125e-5f;
+        const uint32_t h = pack_half2<KD>(v / w, 0.0f);
+        float lo, hi;
+        unpack_half2<KD>(h, lo, hi);
+        part[i] = lo;
+        // (an infinity is all in the first part)
+        v = fabsf(lo) == INFINITY ? 0.0f : v - lo * w;
+    }
+    return make_uint4(pack_half2<KD>(part[0], part[1]), pack_half2<KD>(part[2], part[3]), 0u, 0u);
+}
+template <Kind KD>
+__device__ __forceinline__ uint4 attn_weights() {
+    return KD == Kind::BF16 ? make_uint4(pack_half2<KD>(1.0f, 1.0f), pack_half2<KD>(1.0f, 1.0f), 0u, 0u)
+                            : make_uint4(pack_half2<KD>(32768.0f, 32.0f), pack_half2<KD>(0.03125f, 3.0517578125e-5f),
+                                         0u, 0u);
+}
 
 // The keys' kernel: shared memory and tensor memory.
 template <Kind KD, int DT>
 struct AttnKeysConfig : AttnBackConfig<KD, DT> {
     using B = AttnBackConfig<KD, DT>;
-    static constexpr int STAGES = 2;     // tiles of Q, and of dO
-    static constexpr int ROW_SLOTS = 3;  // rows' LSE, delta and keys seen
+    // Tiles of Q, and of dO.  Two of 128-wide heads fit.  A tile of Q stays from S(n)
+    // to dK(n), almost two rounds, and the next but one has a third of a round to
+    // arrive in, so its two 64-wide boxes are loaded and given back one by one.
+    static constexpr int STAGES = DT == 64 ? 4 : 2;
+    static constexpr int QB = STAGES * B::HALVES;  // boxes of Q
+    static constexpr int ROW_SLOTS = 3;  // rows' LSE, delta (16 bytes of parts each), keys seen
+    static constexpr int ROW_BYTES_ = 2048 + 2048 + 512;
     static constexpr int K_OFF = 0, V_OFF = B::TILE_BYTES, Q_OFF = 2 * B::TILE_BYTES;
     static constexpr int DY_OFF = Q_OFF + STAGES * B::TILE_BYTES;
     static constexpr int ROWS_OFF = DY_OFF + STAGES * B::TILE_BYTES;
-    static constexpr int BAR_OFF = ROWS_OFF + ROW_SLOTS * 1536;
-    static constexpr int KVF = 0, QF0 = 1, QE0 = QF0 + STAGES, DF0 = QE0 + STAGES, DE0 = DF0 + STAGES,
+    static constexpr int WEIGHTS_OFF = ROWS_OFF + ROW_SLOTS * ROW_BYTES_;  // 128 rows of 16 bytes
+    static constexpr int ZERO_OFF = WEIGHTS_OFF + 2048;                    // 128 rows of 16 zero bytes
+    static constexpr int BAR_OFF = ZERO_OFF + 2048;
+    static constexpr int KVF = 0, QF0 = 1, QE0 = QF0 + QB, DF0 = QE0 + QB, DE0 = DF0 + STAGES,
                          SF = DE0 + STAGES, DPF = SF + 1, PR = DPF + 1, DSR = PR + 1, RF0 = DSR + 1,
-                         RE0 = RF0 + ROW_SLOTS, LAST = RE0 + ROW_SLOTS, OD = LAST + 2, DRAIN = OD + 1,
+                         RE0 = RF0 + ROW_SLOTS, LAST = RE0 + ROW_SLOTS, OD = LAST + 3, TURN = OD + 1, DRAIN = TURN + 2,
                          NUM_BARS = DRAIN + 2;
     static constexpr int MISC_OFF = BAR_OFF + NUM_BARS * 8;
     static constexpr int SMEM_BYTES = MISC_OFF + 64 + 1024;
@@ -144,10 +181,12 @@ __global__ void __launch_bounds__(AttnKeysConfig<KD, DT>::NUM_THREADS, 1)
     if (threadIdx.x == 0) {
         mbar_init(bar(C::KVF), 1);
         for (int s = 0; s < C::STAGES; ++s) {
-            mbar_init(bar(C::QF0 + s), 1);
-            mbar_init(bar(C::QE0 + s), 1);
             mbar_init(bar(C::DF0 + s), 1);
             mbar_init(bar(C::DE0 + s), 2);
+        }
+        for (int s = 0; s < C::QB; ++s) {
+            mbar_init(bar(C::QF0 + s), 1);
+            mbar_init(bar(C::QE0 + s), 1);
         }
         mbar_init(bar(C::SF), 1);
         mbar_init(bar(C::DPF), 1);
@@ -157,9 +196,10 @@ __global__ void __launch_bounds__(AttnKeysConfig<KD, DT>::NUM_THREADS, 1)
             mbar_init(bar(C::RF0 + s), 32);
             mbar_init(bar(C::RE0 + s), C::SOFT_WARPS);
         }
-        mbar_init(bar(C::LAST), 1);
-        mbar_init(bar(C::LAST + 1), 1);
+        for (int i = 0; i < 3; ++i) mbar_init(bar(C::LAST + i), 1);
         mbar_init(bar(C::OD), 2);
+        mbar_init(bar(C::TURN), 1);
+        mbar_init(bar(C::TURN + 1), 1);
         mbar_init(bar(C::DRAIN), 1);
         mbar_init(bar(C::DRAIN + 1), 1);
         *abort_flag = 0;
@@ -171,6 +211,10 @@ __global__ void __launch_bounds__(AttnKeysConfig<KD, DT>::NUM_THREADS, 1)
     for (int i = threadIdx.x; i < 2 * C::STAGES * (ATTN_ROWS - box); i += C::NUM_THREADS)
         attn_zero_row<C::HALVES>(smem + C::Q_OFF + (i / (ATTN_ROWS - box)) * C::TILE_BYTES,
                                  box + i % (ATTN_ROWS - box));
+    if (threadIdx.x < 128) {
+        *reinterpret_cast<uint4 *>(smem + C::WEIGHTS_OFF + 16 * threadIdx.x) = attn_weights<KD>();
+        *reinterpret_cast<uint4 *>(smem + C::ZERO_OFF + 16 * threadIdx.x) = make_uint4(0, 0, 0, 0);
+    }
     fence_proxy_async_smem();
     if (warp == C::MMA_WARP) {
         tmem_alloc(smem_u32(tmem_slot), C::TMEM_COLS);
@@ -197,44 +241,51 @@ __global__ void __launch_bounds__(AttnKeysConfig<KD, DT>::NUM_THREADS, 1)
     auto q_tile = [&](int n) -> int { return C::Q_OFF + n % C::STAGES * C::TILE_BYTES; };
     auto dy_tile = [&](int n) -> int { return C::DY_OFF + n % C::STAGES * C::TILE_BYTES; };
     auto parity = [&](int n) -> uint32_t { return (uint32_t)(n / C::STAGES) & 1; };
+    auto q_box = [&](int n, int h) -> int { return n % C::STAGES * C::HALVES + h; };
     // Where the loads of tile n report: a last tile that ends inside reports to
     // ROWS_WARP, which passes it on once the rest is zero.
-    auto landed = [&](int f0, int n) -> uint32_t {
-        return bar(fix && n == tiles - 1 ? (f0 == C::QF0 ? C::LAST : C::LAST + 1) : f0 + n % C::STAGES);
-    };
-    auto landed_parity = [&](int n) -> uint32_t { return fix && n == tiles - 1 ? 0 : parity(n); };
+    const int last = fix ? tiles - 1 : tiles;
+    auto q_landed = [&](int n, int h) -> uint32_t { return bar(n == last ? C::LAST + h : C::QF0 + q_box(n, h)); };
+    auto dy_landed = [&](int n) -> uint32_t { return bar(n == last ? C::LAST + 2 : C::DF0 + n % C::STAGES); };
+    auto landed_parity = [&](int n) -> uint32_t { return n == last ? 0 : parity(n); };
 
     if (warp == C::LOAD_WARP) {
         if (tiles > 0 && elect_one()) {
-            const uint32_t bytes = C::HALVES * box * 128;
+            const uint32_t bytes = box * 128;  // of a box
             mbar_arrive_expect_tx(bar(C::KVF), 2 * C::TILE_BYTES);
 #pragma unroll
             for (int h = 0; h < C::HALVES; ++h) {
                 tma_load_3d(sbase + C::K_OFF + h * 16384, &p.k, bar(C::KVF), h * 64, head, w.k0 + w.first);
                 tma_load_3d(sbase + C::V_OFF + h * 16384, &p.v, bar(C::KVF), h * 64, head, w.k0 + w.first);
             }
-            int q_n = 0, dy_n = 0;
+            int q_n = 0, dy_n = 0;  // boxes of Q, tiles of dO under way
             bool ok = true;
-            for (int n = 0; n < tiles; ++n) {
-                const int s = n % C::STAGES, row = w.q0 + i0 + n * p.h.tokens;
-                if (!wait_phase(bar(C::QE0 + s), parity(n) ^ 1, ctl, SITE_EMPTY)) { ok = false; break; }
-                mbar_arrive_expect_tx(landed(C::QF0, n), bytes);
+            for (int n = 0; ok && n < tiles; ++n) {
+                const int row = w.q0 + i0 + n * p.h.tokens;
+                // (dO first: its stage is free half a round before Q's.)
+                ok = wait_phase(bar(C::DE0 + n % C::STAGES), parity(n) ^ 1, ctl, SITE_EMPTY);
+                if (!ok) break;
+                mbar_arrive_expect_tx(dy_landed(n), C::HALVES * bytes);
+#pragma unroll
                 for (int h = 0; h < C::HALVES; ++h)
-                    tma_load_4d(sbase + q_tile(n) + h * 16384, &p.q, landed(C::QF0, n), h * 64, 0, head, row);
-                ++q_n;
-                if (!wait_phase(bar(C::DE0 + s), parity(n) ^ 1, ctl, SITE_EMPTY)) { ok = false; break; }
-                mbar_arrive_expect_tx(landed(C::DF0, n), bytes);
-                for (int h = 0; h < C::HALVES; ++h)
-                    tma_load_4d(sbase + dy_tile(n) + h * 16384, &p.dy, landed(C::DF0, n), h * 64, 0, head, row);
+                    tma_load_4d(sbase + dy_tile(n) + h * 16384, &p.dy, dy_landed(n), h * 64, 0, head, row);
                 ++dy_n;
+#pragma unroll
+                for (int h = 0; ok && h < C::HALVES; ++h) {
+                    ok = wait_phase(bar(C::QE0 + q_box(n, h)), parity(n) ^ 1, ctl, SITE_EMPTY);
+                    if (!ok) break;
+                    mbar_arrive_expect_tx(q_landed(n, h), bytes);
+                    tma_load_4d(sbase + q_tile(n) + h * 16384, &p.q, q_landed(n, h), h * 64, 0, head, row);
+                    ++q_n;
+                }
             }
             if (!ok) {
                 // Every copy already issued lands before the CTA exits.
                 wait_phase_drain(bar(C::KVF), 0, ctl);
-                for (int n = q_n > C::STAGES ? q_n - C::STAGES : 0; n < q_n; ++n)
-                    wait_phase_drain(landed(C::QF0, n), landed_parity(n), ctl);
+                for (int i = q_n > C::QB ? q_n - C::QB : 0; i < q_n; ++i)
+                    wait_phase_drain(q_landed(i / C::HALVES, i % C::HALVES), landed_parity(i / C::HALVES), ctl);
                 for (int n = dy_n > C::STAGES ? dy_n - C::STAGES : 0; n < dy_n; ++n)
-                    wait_phase_drain(landed(C::DF0, n), landed_parity(n), ctl);
+                    wait_phase_drain(dy_landed(n), landed_parity(n), ctl);
             }
         }
         __syncwarp();
@@ -242,52 +293,83 @@ __global__ void __launch_bounds__(AttnKeysConfig<KD, DT>::NUM_THREADS, 1)
         // Two threads, for the products that wait for P (dV, then the next S, over
         // the same columns) and those that wait for dS (dK, then the next dP): while
         // one waits, the other's are in the tensor core's short queue.  The warps turn
-        // S into P while dK and dP run, and dP into dS while dV and S do.
+        // S into P while dK and dP run, and dP into dS while dV and S do; the threads
+        // take turns, so that one pair is done before the other begins.
         const bool first = warp == C::MMA_WARP;
         if (tiles > 0 && elect_one()) {
-            auto full = [&](int f0, int n) -> bool {
-                const bool ok = wait_phase(bar(f0 + n % C::STAGES), parity(n), ctl, SITE_FULL);
+            // The rows' own terms (attn_parts) of S, and 2 KB on, of dP.
+            auto terms = [&](uint32_t d, int n, int at) {
+                const uint32_t rows = sbase + C::ROWS_OFF + n % C::ROW_SLOTS * C::ROW_BYTES_ + at;
+                mma_f16(d, smem_desc_k2(sbase + C::WEIGHTS_OFF, C::ZERO_OFF - C::WEIGHTS_OFF),
+                        smem_desc_k2(rows, sbase + C::ZERO_OFF - rows), C::ID_S, 1);
+            };
+            auto rows_ready = [&](int n) -> bool {
+                const bool ok = wait_phase(bar(C::RF0 + n % C::ROW_SLOTS), (uint32_t)(n / C::ROW_SLOTS) & 1, ctl,
+                                           SITE_FULL);
                 tc_fence_after();
                 return ok;
             };
-            auto scores = [&](int n) {
-                attn_mma_rows<DT>(tmem + C::S_COL, sbase + C::K_OFF, sbase + q_tile(n), C::ID_S);
+            // S(n), each half of its reduction as its box of Q comes.
+            auto scores = [&](int n) -> bool {
+#pragma unroll
+                for (int h = 0; h < C::HALVES; ++h) {
+                    if (!wait_phase(bar(C::QF0 + q_box(n, h)), parity(n), ctl, SITE_FULL)) return false;
+                    tc_fence_after();
+                    if (h == 0) attn_mma_rows<0, 4>(tmem + C::S_COL, sbase + C::K_OFF, sbase + q_tile(n), C::ID_S);
+                    else attn_mma_rows<4, 8>(tmem + C::S_COL, sbase + C::K_OFF, sbase + q_tile(n), C::ID_S);
+                }
+                terms(tmem + C::S_COL, n, 0);
                 mma_commit(bar(C::SF));
+                return true;
             };
             auto gradients = [&](int n) {
-                attn_mma_rows<DT>(tmem + C::DP_COL, sbase + C::V_OFF, sbase + dy_tile(n), C::ID_S);
+                attn_mma_rows<0, DT / 16>(tmem + C::DP_COL, sbase + C::V_OFF, sbase + dy_tile(n), C::ID_S);
+                terms(tmem + C::DP_COL, n, 2048);
                 mma_commit(bar(C::DPF));
                 mma_commit(bar(C::DE0 + n % C::STAGES));
             };
-            bool ok = wait_phase(bar(C::KVF), 0, ctl, SITE_FULL) && full(first ? C::QF0 : C::DF0, 0);
-            if (first) {
-                if (ok) scores(0);
-                for (int n = 0; ok && n < tiles; ++n) {
-                    ok = full(C::DF0, n) && wait_phase(bar(C::PR), n & 1, ctl, SITE_PROBABILITIES);
-                    if (!ok) break;
-                    tc_fence_after();
-                    attn_mma_ta<0, 8, C::P_HALF>(tmem + C::DV_COL, tmem + C::P_COL, sbase + dy_tile(n), C::ID_PV,
-                                                 n > 0);
-                    mma_commit(bar(C::DE0 + n % C::STAGES));
-                    if (n + 1 < tiles) {
-                        ok = full(C::QF0, n + 1);
-                        if (ok) scores(n + 1);
-                    }
+            // Turn n of either (S(0), then dV(n - 1) and S(n); dP(0), then dK and dP).
+            auto turn = [&](int n) -> bool {
+                const bool ok = first ? n == 0 || wait_phase(bar(C::TURN), (n - 1) & 1, ctl, SITE_ACC_EMPTY)
+                                      : wait_phase(bar(C::TURN + 1), n & 1, ctl, SITE_ACC_EMPTY);
+                tc_fence_after();
+                return ok;
+            };
+            auto pass = [&] { mbar_arrive(bar(first ? C::TURN + 1 : C::TURN)); };
+            // Under the MMAs' own reads a wait on shared memory takes 150 cycles even
+            // when its phase is over: what comes early is awaited early, and what
+            // the other thread has awaited before its turn is not awaited again (dO
+            // for dV, Q for dK, the rows' terms for dP).
+            bool ok = wait_phase(bar(C::KVF), 0, ctl, SITE_FULL);
+            for (int n = 0; ok && n <= tiles; ++n) {
+                if (n < tiles)
+                    ok = first ? rows_ready(n)
+                               : wait_phase(bar(C::DF0 + n % C::STAGES), parity(n), ctl, SITE_FULL);
+                if (ok && n > 0)
+                    ok = wait_phase(bar(first ? C::PR : C::DSR), (n - 1) & 1, ctl, SITE_PROBABILITIES);
+                if (!ok || !turn(n)) {
+                    ok = false;
+                    break;
                 }
-            } else {
-                if (ok) gradients(0);
-                for (int n = 0; ok && n < tiles; ++n) {
-                    ok = full(C::QF0, n) && wait_phase(bar(C::DSR), n & 1, ctl, SITE_PROBABILITIES);
-                    if (!ok) break;
-                    tc_fence_after();
-                    attn_mma_ta<0, 8, C::P_HALF>(tmem + C::DK_COL, tmem + C::DS_COL, sbase + q_tile(n), C::ID_PV,
-                                                 n > 0);
-                    mma_commit(bar(C::QE0 + n % C::STAGES));
-                    if (n + 1 < tiles) {
-                        ok = full(C::DF0, n + 1);
-                        if (ok) gradients(n + 1);
+                if (first) {
+                    if (n > 0) {
+                        attn_mma_ta<0, 8, C::P_HALF>(tmem + C::DV_COL, tmem + C::P_COL, sbase + dy_tile(n - 1),
+                                                     C::ID_PV, n > 1);
+                        mma_commit(bar(C::DE0 + (n - 1) % C::STAGES));
                     }
+                    if (n < tiles) ok = scores(n);
+                } else {
+                    if (n > 0) {
+#pragma unroll
+                        for (int h = 0; h < C::HALVES; ++h) {
+                            attn_mma_ta<0, 8, C::P_HALF>(tmem + C::DK_COL + 64 * h, tmem + C::DS_COL,
+                                                         sbase + q_tile(n - 1) + h * 16384, C::ID_64, n > 1);
+                            mma_commit(bar(C::QE0 + q_box(n - 1, h)));
+                        }
+                    }
+                    if (n < tiles) gradients(n);
                 }
+                pass();
             }
             const uint32_t end = bar(ok ? C::OD : C::DRAIN + (first ? 0 : 1));
             mma_commit(end);
@@ -296,43 +378,55 @@ __global__ void __launch_bounds__(AttnKeysConfig<KD, DT>::NUM_THREADS, 1)
         __syncwarp();
     } else if (warp == C::ROWS_WARP) {
         // ------------------------------------------------------ the rows' LSE, delta, keys seen
+        // (the next tile's values are on their way while this one's are written)
+        const float over_scale = 1.0f / p.h.scale;
+        float z[4], d[4];
+        auto fetch = [&](int n) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int row = lane + 32 * q, token = i0 + n * p.h.tokens + row / p.h.group;
+                z[q] = -INFINITY;
+                d[q] = 0.0f;
+                if (row < box && token < w.lq) {
+                    const int64_t at =
+                        (int64_t)(head * p.h.group + row % p.h.group) * p.s.q_rows + w.q0 + token;
+                    z[q] = p.lse[at];
+                    d[q] = p.delta[at];
+                }
+            }
+        };
+        if (tiles > 0) fetch(0);
         for (int n = 0; n < tiles; ++n) {
             const int s = n % C::ROW_SLOTS;
             if (!wait_warp(bar(C::RE0 + s), (uint32_t)(n / C::ROW_SLOTS + 1) & 1, ctl, SITE_EMPTY)) break;
-            float *lse = reinterpret_cast<float *>(smem + C::ROWS_OFF + s * 1536);
-            float *delta = lse + 128;
-            int *seen = reinterpret_cast<int *>(lse + 256);
+            uint8_t *rows = smem + C::ROWS_OFF + s * C::ROW_BYTES_;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const int row = lane + 32 * q, token = i0 + n * p.h.tokens + row / p.h.group;
                 // A row that is none, or sees nothing: P = 2^(-infinity) = 0.
-                float l = INFINITY, d = 0.0f;
-                int k = 0;
-                if (row < box && token < w.lq) {
-                    const int64_t at =
-                        (int64_t)(head * p.h.group + row % p.h.group) * p.s.q_rows + w.q0 + token;
-                    const float z = p.lse[at];
-                    if (z != -INFINITY) l = z * 1.4426950408889634f;
-                    d = p.delta[at];
-                    k = attn_seen(p.s, w, token);
-                }
-                lse[row] = -l;
-                delta[row] = -d;
-                seen[row] = k;
+                *reinterpret_cast<uint4 *>(rows + 16 * row) =
+                    attn_parts<KD>(z[q] == -INFINITY ? -INFINITY : -z[q] * over_scale);
+                *reinterpret_cast<uint4 *>(rows + 2048 + 16 * row) = attn_parts<KD>(-d[q]);
+                *reinterpret_cast<int *>(rows + 4096 + 4 * row) =
+                    row < box && token < w.lq ? attn_seen(p.s, w, token) : 0;
             }
+            if (n + 1 < tiles) fetch(n + 1);
+            fence_proxy_async_smem();
             mbar_arrive(bar(C::RF0 + s));
             if (fix && n == tiles - 1) {
                 // Rows of other sequences, in the last tile, become zero.
-                if (!wait_warp(bar(C::LAST), 0, ctl, SITE_FULL)) break;
-                for (int row = tail + lane; row < box; row += 32) attn_zero_row<C::HALVES>(smem + q_tile(n), row);
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(C::QF0 + n % C::STAGES));
-                if (!wait_warp(bar(C::LAST + 1), 0, ctl, SITE_FULL)) break;
-                for (int row = tail + lane; row < box; row += 32) attn_zero_row<C::HALVES>(smem + dy_tile(n), row);
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(C::DF0 + n % C::STAGES));
+#pragma unroll
+                for (int h = 0; h < C::HALVES + 1; ++h) {
+                    const bool q = h < C::HALVES;
+                    if (!wait_warp(bar(q ? C::LAST + h : C::LAST + 2), 0, ctl, SITE_FULL)) break;
+                    for (int row = tail + lane; row < box; row += 32) {
+                        if (q) attn_zero_row<1>(smem + q_tile(n) + h * 16384, row);
+                        else attn_zero_row<C::HALVES>(smem + dy_tile(n), row);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(q ? C::QF0 + q_box(n, h) : C::DF0 + n % C::STAGES));
+                }
             }
         }
         __syncwarp();
@@ -346,9 +440,7 @@ __global__ void __launch_bounds__(AttnKeysConfig<KD, DT>::NUM_THREADS, 1)
         bool ok = true;
         for (int n = 0; n < tiles; ++n) {
             const int s = n % C::ROW_SLOTS;
-            const float *rows = reinterpret_cast<const float *>(smem + C::ROWS_OFF + s * 1536) + 64 * half;
-            ok = wait_warp(bar(C::RF0 + s), (uint32_t)(n / C::ROW_SLOTS) & 1, ctl, SITE_FULL) &&
-                 wait_warp(bar(C::SF), n & 1, ctl, SITE_SCORES);
+            ok = wait_warp(bar(C::SF), n & 1, ctl, SITE_SCORES);
             if (!ok) break;
             tc_fence_after();
             float y[64];
@@ -356,17 +448,20 @@ __global__ void __launch_bounds__(AttnKeysConfig<KD, DT>::NUM_THREADS, 1)
 #pragma unroll
             for (int i = 0; i < 2; ++i) tmem_ld_row32(tmem + lane_base + C::S_COL + 64 * half + 32 * i, yw + 32 * i);
             tmem_ld_wait();
-#pragma unroll
-            for (int i = 0; i < 64; i += 4) {
-                const float4 l = *reinterpret_cast<const float4 *>(rows + i);
-                unpair2(fma_pair(pair2(y[i], y[i + 1]), cc, pair2(l.x, l.y)), y[i], y[i + 1]);
-                unpair2(fma_pair(pair2(y[i + 2], y[i + 3]), cc, pair2(l.z, l.w)), y[i + 2], y[i + 3]);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) y[i + e] = exp2_approx(y[i + e]);
-            }
             // Some rows of the tile do not see all of the keys.
-            if (p.s.causal && attn_seen(p.s, w, i0 + n * p.h.tokens) < w.first + ATTN_KEYS) {
-                const int *seen = reinterpret_cast<const int *>(rows + 256);
+            const bool cut = p.s.causal && attn_seen(p.s, w, i0 + n * p.h.tokens) < w.first + ATTN_KEYS;
+            if (cut) {
+                ok = wait_warp(bar(C::RF0 + s), (uint32_t)(n / C::ROW_SLOTS) & 1, ctl, SITE_FULL);
+                if (!ok) break;
+            }
+            const int *seen = reinterpret_cast<const int *>(smem + C::ROWS_OFF + s * C::ROW_BYTES_ + 4096) + 64 * half;
+#pragma unroll
+            for (int i = 0; i < 64; i += 2) {
+                unpair2(mul_pair(pair2(y[i], y[i + 1]), cc), y[i], y[i + 1]);
+                y[i] = exp2_approx(y[i]);
+                y[i + 1] = exp2_approx(y[i + 1]);
+            }
+            if (cut) {
 #pragma unroll
                 for (int i = 0; i < 64; ++i)
                     if (key >= seen[i]) y[i] = 0.0f;
@@ -384,15 +479,10 @@ __global__ void __launch_bounds__(AttnKeysConfig<KD, DT>::NUM_THREADS, 1)
                 uint32_t d[32];
                 tmem_ld_row32(tmem + lane_base + C::DP_COL + 64 * half + i, d);
                 tmem_ld_wait();
+                const float *f = reinterpret_cast<const float *>(d);
 #pragma unroll
-                for (int e = 0; e < 32; e += 4) {
-                    const float4 z = *reinterpret_cast<const float4 *>(rows + 128 + i + e);
-                    const float *f = reinterpret_cast<const float *>(d) + e;
-                    uint64_t a = mul_pair(pair2(y[i + e], y[i + e + 1]), add_pair(pair2(f[0], f[1]), pair2(z.x, z.y)));
-                    unpair2(a, y[i + e], y[i + e + 1]);
-                    a = mul_pair(pair2(y[i + e + 2], y[i + e + 3]), add_pair(pair2(f[2], f[3]), pair2(z.z, z.w)));
-                    unpair2(a, y[i + e + 2], y[i + e + 3]);
-                }
+                for (int e = 0; e < 32; e += 2)
+                    unpair2(mul_pair(pair2(y[i + e], y[i + e + 1]), pair2(f[e], f[e + 1])), y[i + e], y[i + e + 1]);
             }
             attn_store_half<KD>(tmem + lane_base + C::DS_COL + C::P_HALF * half, y);
             tc_fence_before();
@@ -553,7 +643,7 @@ __global__ void __launch_bounds__(AttnRowsConfig<KD, DT>::NUM_THREADS, 1)
                     ok = full(2 * n) && (n == 0 || wait_phase(bar(C::SE), (n - 1) & 1, ctl, SITE_PROBABILITIES));
                     if (!ok) break;
                     tc_fence_after();
-                    attn_mma_rows<DT>(tmem + C::S_COL, sbase + C::Q_OFF, sbase + tile(2 * n), C::ID_S);
+                    attn_mma_rows<0, DT / 16>(tmem + C::S_COL, sbase + C::Q_OFF, sbase + tile(2 * n), C::ID_S);
                     mma_commit(bar(C::SF));
                 }
             } else {
@@ -563,7 +653,7 @@ __global__ void __launch_bounds__(AttnRowsConfig<KD, DT>::NUM_THREADS, 1)
                     if (!ok) break;
                     tc_fence_after();
                     if (n < blocks) {
-                        attn_mma_rows<DT>(tmem + C::DP_COL, sbase + C::DY_OFF, sbase + tile(2 * n + 1), C::ID_S);
+                        attn_mma_rows<0, DT / 16>(tmem + C::DP_COL, sbase + C::DY_OFF, sbase + tile(2 * n + 1), C::ID_S);
                         mma_commit(bar(C::DPF));
                         mma_commit(bar(C::EMPTY0 + slot(2 * n + 1)));
                     }
