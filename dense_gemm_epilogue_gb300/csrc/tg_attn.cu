@@ -112,28 +112,41 @@ struct ForwardPlan {
     int64_t workspace;
 };
 
-// Two row tiles a CTA from more than one wave of single ones on, for sequences
-// that have a second tile.  Single tiles that leave SMs without work cut the
-// keys into ranges of at least four blocks.
+// The choice with the least estimated time, in cycles: CTAs of one or two row tiles,
+// one an SM at a time, over key ranges of `chunk` blocks; a round of a block takes
+// 2000 cycles with one tile (its chain: S, softmax, P V), 2700 with two; a CTA's start
+// and end 7000; ranges cost a second kernel and their rows' way through memory.
+// Sequences may be shorter than max_k says, so long ones are cut to 48 blocks
+// anyway, for an even load.
 ForwardPlan plan_forward(const Sizes &z, int sms) {
-    ForwardPlan p = {};
+    ForwardPlan best = {};
     const int64_t tokens = ATTN_ROWS / (z.heads / z.kv_heads);
     const int64_t max_q = bound_of(z.max_q, z.q_rows), max_k = bound_of(z.max_k, z.k_rows);
-    const int64_t single = tile_bound(z.seqs, z.q_rows, max_q, tokens);
     const int64_t blocks = ceil_div(max_k, ATTN_KEYS) > 0 ? ceil_div(max_k, ATTN_KEYS) : 1;
-    p.nq = max_q > tokens && single * z.kv_heads > sms ? 2 : 1;
-    p.tiles = p.nq == 2 ? tile_bound(z.seqs, z.q_rows, max_q, 2 * tokens) : single;
-    p.splits = 1;
-    if (p.nq == 1) {
-        const int64_t ctas = p.tiles * z.kv_heads, most = blocks / 4;
-        p.splits = 4 * (int64_t)sms / (ctas > 0 ? ctas : 1);
-        if (p.splits > most) p.splits = most;
-        if (p.splits < 1) p.splits = 1;
+    double least = -1.0;
+    for (int nq = 1; nq <= (max_q > tokens ? 2 : 1); ++nq) {
+        const int64_t tiles = tile_bound(z.seqs, z.q_rows, max_q, nq * tokens);
+        const int64_t ctas = tiles * z.kv_heads;
+        int64_t most = ctas < 2 * sms ? ceil_div(2 * sms, ctas > 0 ? ctas : 1) : 1;
+        if (most < ceil_div(blocks, 48) && max_q <= tokens) most = ceil_div(blocks, 48);
+        if (most > ceil_div(blocks, 4)) most = ceil_div(blocks, 4);
+        for (int64_t s = 1; s <= most; ++s) {
+            const int64_t chunk = ceil_div(blocks, s), splits = ceil_div(blocks, chunk);
+            if (splits != s) continue;
+            const double waves = (double)ceil_div(ctas * splits, sms);
+            double cycles = waves * (7000.0 + chunk * (nq == 2 ? 2700.0 : 2000.0));
+            if (splits > 1) cycles += 6000.0 + 8.0 * splits * z.heads * z.q_rows * z.dim / 2500.0;
+            if (max_q <= tokens && chunk > 48) cycles *= 1.0 + (chunk - 48) / 96.0;
+            if (least >= 0.0 && cycles >= least) continue;
+            least = cycles;
+            best.nq = nq;
+            best.tiles = tiles;
+            best.splits = splits;
+            best.chunk = chunk;
+        }
     }
-    p.chunk = ceil_div(blocks, p.splits);
-    p.splits = ceil_div(blocks, p.chunk);
-    if (p.splits > 1) p.workspace = p.splits * z.heads * z.q_rows * (4 * z.dim + 8);
-    return p;
+    if (best.splits > 1) best.workspace = best.splits * z.heads * z.q_rows * (4 * z.dim + 8);
+    return best;
 }
 
 bool arrays_ok(const int64_t *qs, const int64_t *ql, const int64_t *ks, const int64_t *kl) {
@@ -222,6 +235,8 @@ extern "C" tg_status tg_attention(int64_t seqs, int64_t q_rows, int64_t k_rows, 
     a.tiles = (int32_t)p.tiles;
     a.splits = (int32_t)p.splits;
     a.chunk = (int32_t)p.chunk;
+    a.join_tokens = p.nq * a.h.tokens;
+    a.join_rows = (a.s.max_q < a.join_tokens ? a.s.max_q : a.join_tokens) * a.h.group;
     if (p.workspace) {
         a.part_o = static_cast<float *>(workspace);
         a.part_ml = reinterpret_cast<float2 *>(a.part_o + p.splits * heads * q_rows * dim);

@@ -45,6 +45,8 @@ struct AttnForward {
     float2 *part_ml;        //   and their (reference exponent, sum)
     int32_t tiles;          // bound on the row tiles (tile pairs) of all sequences
     int32_t splits, chunk;  // key ranges of `chunk` blocks each
+    int32_t join_tokens;    // tokens of a CTA's tiles
+    int32_t join_rows;      // rows of these that a sequence can have, at most
     uint32_t *status;
     uint64_t wait_limit_ns;
 };

@@ -45,43 +45,42 @@ __device__ __forceinline__ AttnWork attn_find(const AttnSeqs &s, int t, int per,
     AttnWork w;
     w.seq = -1;
     w.first = w.q0 = w.lq = w.k0 = w.lk = 0;
-    const int64_t *starts = KEYS ? s.k_starts : s.q_starts;
-    const int64_t *lengths = KEYS ? s.k_lengths : s.q_lengths;
-    const int rows = KEYS ? s.k_rows : s.q_rows, bound = KEYS ? s.max_k : s.max_q;
-    int tile = 0;
-    if (bound <= per) {  // a sequence is a tile
-        if (t < s.seqs) w.seq = t;
-    } else {
-        int before = 0;
-        for (int base = 0; base < s.seqs; base += 32) {
-            int n = 0;
-            if (base + lane < s.seqs) {
-                int at, len;
-                attn_range(starts, lengths, base + lane, rows, bound, at, len);
-                n = (len + per - 1) / per;
-            }
+    // One round of loads: every lane holds a sequence's ranges, the one found passes
+    // its own to all.
+    const bool one = (KEYS ? s.max_k : s.max_q) <= per;  // a sequence is a tile
+    int tile = 0, before = 0;
+    for (int base = one ? t : 0; base < s.seqs; base += 32) {
+        const int q = one ? t : base + lane;
+        int q0 = 0, lq = 0, k0 = 0, lk = 0;
+        if (q < s.seqs) {
+            attn_range(s.q_starts, s.q_lengths, q, s.q_rows, s.max_q, q0, lq);
+            attn_range(s.k_starts, s.k_lengths, q, s.k_rows, s.max_k, k0, lk);
+        }
+        int from = 0;
+        if (!one) {
+            const int n = ((KEYS ? lk : lq) + per - 1) / per;
             int sum = n;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int v = __shfl_up_sync(0xffffffffu, sum, o);
                 if (lane >= o) sum += v;
             }
-            const bool mine = t >= before + sum - n && t < before + sum;
-            const unsigned who = __ballot_sync(0xffffffffu, mine);
-            if (who) {
-                const int l = __ffs(who) - 1;
-                w.seq = base + l;
-                tile = t - (before + __shfl_sync(0xffffffffu, sum - n, l));
-                break;
+            const unsigned who = __ballot_sync(0xffffffffu, t >= before + sum - n && t < before + sum);
+            if (!who) {
+                before += __shfl_sync(0xffffffffu, sum, 31);
+                continue;
             }
-            before += __shfl_sync(0xffffffffu, sum, 31);
+            from = __ffs(who) - 1;
+            tile = t - (before + __shfl_sync(0xffffffffu, sum - n, from));
         }
-    }
-    if (w.seq >= 0) {
-        attn_range(s.q_starts, s.q_lengths, w.seq, s.q_rows, s.max_q, w.q0, w.lq);
-        attn_range(s.k_starts, s.k_lengths, w.seq, s.k_rows, s.max_k, w.k0, w.lk);
+        w.seq = __shfl_sync(0xffffffffu, q, from);
+        w.q0 = __shfl_sync(0xffffffffu, q0, from);
+        w.lq = __shfl_sync(0xffffffffu, lq, from);
+        w.k0 = __shfl_sync(0xffffffffu, k0, from);
+        w.lk = __shfl_sync(0xffffffffu, lk, from);
         w.first = tile * per;
         if (w.first >= (KEYS ? w.lk : w.lq)) w.seq = -1;
+        break;
     }
     return w;
 }

@@ -17,13 +17,13 @@ static cudaError_t attn_smem(K kernel, int smem, int device, std::atomic<uint64_
 }
 
 template <class P>
-static cudaError_t attn_launch(void (*kernel)(const P), int64_t grid, int threads, int smem,
+static cudaError_t attn_launch(void (*kernel)(const P), dim3 grid, int threads, int smem,
                                cudaStream_t stream, const P &p) {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3((unsigned)grid, 1, 1);
+    cfg.gridDim = grid;
     cfg.blockDim = dim3(threads, 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
@@ -39,7 +39,7 @@ static cudaError_t launch_attn_one(const AttnForward &a, int device, cudaStream_
     const cudaError_t e = attn_smem(tg_attn_kernel<KD, DT, NQ>, C::SMEM_BYTES, device, done);
     if (e != cudaSuccess) return e;
     return attn_launch<AttnForward>(tg_attn_kernel<KD, DT, NQ>,
-                                    (int64_t)a.tiles * a.h.kv_heads * a.splits, C::NUM_THREADS,
+                                    dim3((unsigned)(a.tiles * a.h.kv_heads * a.splits)), C::NUM_THREADS,
                                     C::SMEM_BYTES, stream, a);
 }
 
@@ -51,7 +51,12 @@ static cudaError_t launch_attn_forward_kind(const AttnForward &a, int nq, int de
     else
         e = nq == 2 ? launch_attn_one<KD, 128, 2>(a, device, stream) : launch_attn_one<KD, 128, 1>(a, device, stream);
     if (e != cudaSuccess || a.splits == 1) return e;
-    return attn_launch<AttnForward>(tg_attn_join_kernel<KD>, (int64_t)a.tiles * a.h.kv_heads, 256, 0, stream, a);
+    // A block a row where that is a few blocks an SM at most.
+    const int64_t tiles = (int64_t)a.tiles * a.h.kv_heads;
+    const bool wide = tiles * a.join_rows <= 1024;
+    const dim3 grid((unsigned)tiles, wide ? a.join_rows : (a.join_rows + JOIN_WARPS - 1) / JOIN_WARPS);
+    return wide ? attn_launch<AttnForward>(tg_attn_join_kernel<KD, true>, grid, 32 * JOIN_WARPS, 0, stream, a)
+                : attn_launch<AttnForward>(tg_attn_join_kernel<KD, false>, grid, 32 * JOIN_WARPS, 0, stream, a);
 }
 
 template <Kind KD, int DT>
@@ -65,14 +70,14 @@ static cudaError_t launch_attn_backward_dim(const AttnBackward &a, int device, c
         if (e != cudaSuccess) return e;
         const int64_t grid = (int64_t)a.blocks * a.h.kv_heads;
         if (grid > 0)
-            e = attn_launch<AttnBackward>(tg_attn_keys_kernel<KD, DT>, grid, CK::NUM_THREADS, CK::SMEM_BYTES, stream, a);
+            e = attn_launch<AttnBackward>(tg_attn_keys_kernel<KD, DT>, dim3((unsigned)grid), CK::NUM_THREADS, CK::SMEM_BYTES, stream, a);
     }
     if (e == cudaSuccess && a.dq.ptr) {
         e = attn_smem(tg_attn_rows_kernel<KD, DT>, CR::SMEM_BYTES, device, rows_done);
         if (e != cudaSuccess) return e;
         const int64_t grid = (int64_t)a.tiles * a.h.kv_heads;
         if (grid > 0)
-            e = attn_launch<AttnBackward>(tg_attn_rows_kernel<KD, DT>, grid, CR::NUM_THREADS, CR::SMEM_BYTES, stream, a);
+            e = attn_launch<AttnBackward>(tg_attn_rows_kernel<KD, DT>, dim3((unsigned)grid), CR::NUM_THREADS, CR::SMEM_BYTES, stream, a);
     }
     return e;
 }
@@ -82,7 +87,7 @@ static cudaError_t launch_attn_backward_kind(const AttnBackward &a, const AttnDe
                                              cudaStream_t stream) {
     if (d.rows > 0) {
         const int64_t grid = ((int64_t)d.rows * d.heads + DELTA_THREADS / 16 - 1) / (DELTA_THREADS / 16);
-        const cudaError_t e = attn_launch<AttnDelta>(tg_attn_delta_kernel<KD>, grid, DELTA_THREADS, 0, stream, d);
+        const cudaError_t e = attn_launch<AttnDelta>(tg_attn_delta_kernel<KD>, dim3((unsigned)grid), DELTA_THREADS, 0, stream, d);
         if (e != cudaSuccess) return e;
     }
     return a.h.dim <= 64 ? launch_attn_backward_dim<KD, 64>(a, device, stream)

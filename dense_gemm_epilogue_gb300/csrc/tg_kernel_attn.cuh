@@ -477,62 +477,67 @@ __global__ void __launch_bounds__(AttnConfig<KD, DT, NQ>::NUM_THREADS, 1)
 
 // The rows of a tile from their key ranges: with M the largest reference,
 //   L = sum l_s 2^(m_s - M),  O = sum o_s 2^(m_s - M) / L,  LSE = (M + log2 L) ln 2,
-// in the order of the ranges.  A warp a row.
-template <Kind KD>
-__global__ void __launch_bounds__(256) tg_attn_join_kernel(const __grid_constant__ AttnForward p) {
+// always in the same order.  WIDE: the block's eight warps share a row's ranges (a
+// few rows with many ranges); else a warp a row.  blockIdx.y: which rows of the tile.
+constexpr int JOIN_WARPS = 8;
+template <Kind KD, bool WIDE>
+__global__ void __launch_bounds__(32 * JOIN_WARPS) tg_attn_join_kernel(const __grid_constant__ AttnForward p) {
+    __shared__ float4 part[WIDE ? JOIN_WARPS : 1][32];
+    __shared__ float sums[WIDE ? JOIN_WARPS : 1];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     griddep_launch();
     griddep_wait();
     const int head = blockIdx.x % p.h.kv_heads;
-    const AttnWork w = attn_find<false>(p.s, blockIdx.x / p.h.kv_heads, p.h.tokens, lane);
-    if (w.seq < 0) return;
+    const AttnWork w = attn_find<false>(p.s, blockIdx.x / p.h.kv_heads, p.join_tokens, lane);
+    const int row = WIDE ? blockIdx.y : blockIdx.y * JOIN_WARPS + warp;
+    const int token = w.first + row / p.h.group, qh = head * p.h.group + row % p.h.group;
+    if (w.seq < 0 || row >= p.join_tokens * p.h.group || token >= w.lq) return;  // (WIDE: the whole block)
     const int64_t stride = (int64_t)p.h.heads * p.s.q_rows;
-    for (int row = warp; row < p.h.tokens * p.h.group; row += 8) {
-        const int token = w.first + row / p.h.group, qh = head * p.h.group + row % p.h.group;
-        if (token >= w.lq) break;
-        const int64_t at = (int64_t)qh * p.s.q_rows + w.q0 + token;
-        // Lane i looks at ranges i, i + 32, ...
-        float m = -INFINITY;
-        for (int s = lane; s < p.splits; s += 32) {
-            const float2 ml = p.part_ml[s * stride + at];
-            if (ml.y != 0.0f) m = fmaxf(m, ml.x);
-        }
+    const int64_t at = (int64_t)qh * p.s.q_rows + w.q0 + token;
+    // Lane i looks at ranges i, i + 32, ...
+    float m = -INFINITY;
+    for (int s = lane; s < p.splits; s += 32) {
+        const float2 ml = p.part_ml[s * stride + at];
+        if (ml.y != 0.0f) m = fmaxf(m, ml.x);
+    }
 #pragma unroll
-        for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        float l = 0.0f, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        for (int base = 0; base < p.splits; base += 32) {
-            float f = 0.0f, ls = 0.0f;
-            if (base + lane < p.splits) {
-                const float2 ml = p.part_ml[(base + lane) * stride + at];
-                if (ml.y != 0.0f) {
-                    f = exp2_approx(ml.x - m);
-                    ls = ml.y;
-                }
-            }
-            const int top = p.splits - base < 32 ? p.splits - base : 32;
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    float l = 0.0f, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    const int step = WIDE ? JOIN_WARPS : 1;
 #pragma unroll 4
-            for (int i = 0; i < top; ++i) {
-                const float g = __shfl_sync(0xffffffffu, f, i);
-                const float li = __shfl_sync(0xffffffffu, ls, i);
-                if (li == 0.0f) continue;
-                l += li * g;
-                if (4 * lane < p.h.dim) {
-                    const float4 v = reinterpret_cast<const float4 *>(
-                        p.part_o + ((base + i) * stride + at) * p.h.dim)[lane];
-                    o[0] += v.x * g;
-                    o[1] += v.y * g;
-                    o[2] += v.z * g;
-                    o[3] += v.w * g;
-                }
-            }
-        }
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-        if (lane == 0 && p.lse) p.lse[at] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+    for (int s = WIDE ? warp : 0; s < p.splits; s += step) {
+        const float2 ml = p.part_ml[s * stride + at];
+        if (ml.y == 0.0f) continue;  // (nothing was stored)
+        const float g = exp2_approx(ml.x - m);
+        l += ml.y * g;
         if (4 * lane < p.h.dim) {
-            uint16_t *dst = static_cast<uint16_t *>(p.o.ptr) + (w.q0 + token) * p.o.ld + qh * p.o.hd;
-            *reinterpret_cast<uint2 *>(dst + 4 * lane) =
-                make_uint2(pack_half2<KD>(o[0] * inv, o[1] * inv), pack_half2<KD>(o[2] * inv, o[3] * inv));
+            const float4 v = reinterpret_cast<const float4 *>(p.part_o + (s * stride + at) * p.h.dim)[lane];
+            o[0] += v.x * g;
+            o[1] += v.y * g;
+            o[2] += v.z * g;
+            o[3] += v.w * g;
         }
+    }
+    if constexpr (WIDE) {
+        part[warp][lane] = make_float4(o[0], o[1], o[2], o[3]);
+        if (lane == 0) sums[warp] = l;
+        __syncthreads();
+        if (warp) return;
+        for (int i = 1; i < JOIN_WARPS; ++i) {
+            const float4 v = part[i][lane];
+            o[0] += v.x;
+            o[1] += v.y;
+            o[2] += v.z;
+            o[3] += v.w;
+            l += sums[i];
+        }
+    }
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    if (lane == 0 && p.lse) p.lse[at] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+    if (4 * lane < p.h.dim) {
+        uint16_t *dst = static_cast<uint16_t *>(p.o.ptr) + (w.q0 + token) * p.o.ld + qh * p.o.hd;
+        *reinterpret_cast<uint2 *>(dst + 4 * lane) =
+            make_uint2(pack_half2<KD>(o[0] * inv, o[1] * inv), pack_half2<KD>(o[2] * inv, o[3] * inv));
     }
 }
 
