@@ -306,7 +306,7 @@ extern "C" tg_status tg_attention_backward(
     a.delta = static_cast<const float *>(workspace);
     const int64_t tiles = q_rows ? tile_bound(seqs, q_rows, a.s.max_q, a.h.tokens) : 0;
     const int64_t blocks = k_rows ? tile_bound(seqs, k_rows, a.s.max_k, ATTN_KEYS) : 0;
-    if (tiles * kv_heads > INT32_MAX || blocks * kv_heads > INT32_MAX || q_rows * heads / 16 > INT32_MAX - 1)
+    if ((tiles + blocks) * kv_heads > INT32_MAX || q_rows * heads / 16 > INT32_MAX - 1)
         return TG_ERR_UNSUPPORTED;
     a.tiles = (int32_t)tiles;
     a.blocks = (int32_t)blocks;

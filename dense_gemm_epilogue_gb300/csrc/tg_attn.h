@@ -67,13 +67,14 @@ struct AttnBackward {
     const float *lse;       // heads x q_rows
     const float *delta;     // heads x q_rows: sum over d of dO O
     int32_t tiles, blocks;  // bounds on the row tiles and on the key blocks of all sequences
+    int32_t key_ctas;       // CTAs that work on keys; the rest work on rows
     uint32_t *status;
     uint64_t wait_limit_ns;
 };
 
 cudaError_t launch_attn_forward_bf16(const AttnForward &a, int tiles_per_cta, int device, cudaStream_t stream);
 cudaError_t launch_attn_forward_fp16(const AttnForward &a, int tiles_per_cta, int device, cudaStream_t stream);
-// delta, then the keys' kernel (unless neither dK nor dV is wanted), then the rows'.
+// delta, then the gradients that are wanted.
 cudaError_t launch_attn_backward_bf16(const AttnBackward &a, const AttnDelta &d, int device, cudaStream_t stream);
 cudaError_t launch_attn_backward_fp16(const AttnBackward &a, const AttnDelta &d, int device, cudaStream_t stream);
 

@@ -60,26 +60,19 @@ static cudaError_t launch_attn_forward_kind(const AttnForward &a, int nq, int de
 }
 
 template <Kind KD, int DT>
-static cudaError_t launch_attn_backward_dim(const AttnBackward &a, int device, cudaStream_t stream) {
+static cudaError_t launch_attn_backward_dim(AttnBackward a, int device, cudaStream_t stream) {
     using CK = AttnKeysConfig<KD, DT>;
     using CR = AttnRowsConfig<KD, DT>;
-    static std::atomic<uint64_t> keys_done{0}, rows_done{0};
-    cudaError_t e = cudaSuccess;
-    if (a.dk.ptr || a.dv.ptr) {
-        e = attn_smem(tg_attn_keys_kernel<KD, DT>, CK::SMEM_BYTES, device, keys_done);
-        if (e != cudaSuccess) return e;
-        const int64_t grid = (int64_t)a.blocks * a.h.kv_heads;
-        if (grid > 0)
-            e = attn_launch<AttnBackward>(tg_attn_keys_kernel<KD, DT>, dim3((unsigned)grid), CK::NUM_THREADS, CK::SMEM_BYTES, stream, a);
-    }
-    if (e == cudaSuccess && a.dq.ptr) {
-        e = attn_smem(tg_attn_rows_kernel<KD, DT>, CR::SMEM_BYTES, device, rows_done);
-        if (e != cudaSuccess) return e;
-        const int64_t grid = (int64_t)a.tiles * a.h.kv_heads;
-        if (grid > 0)
-            e = attn_launch<AttnBackward>(tg_attn_rows_kernel<KD, DT>, dim3((unsigned)grid), CR::NUM_THREADS, CR::SMEM_BYTES, stream, a);
-    }
-    return e;
+    constexpr int SMEM = CK::SMEM_BYTES > CR::SMEM_BYTES ? CK::SMEM_BYTES : CR::SMEM_BYTES;
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = attn_smem(tg_attn_backward_kernel<KD, DT>, SMEM, device, done);
+    if (e != cudaSuccess) return e;
+    const int64_t keys = a.dk.ptr || a.dv.ptr ? (int64_t)a.blocks * a.h.kv_heads : 0;
+    const int64_t rows = a.dq.ptr ? (int64_t)a.tiles * a.h.kv_heads : 0;
+    if (keys + rows == 0) return cudaSuccess;
+    a.key_ctas = (int32_t)keys;
+    return attn_launch<AttnBackward>(tg_attn_backward_kernel<KD, DT>, dim3((unsigned)(keys + rows)), CK::NUM_THREADS,
+                                     SMEM, stream, a);
 }
 
 template <Kind KD>

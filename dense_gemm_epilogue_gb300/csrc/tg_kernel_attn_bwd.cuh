@@ -3,7 +3,7 @@
 //   dV = P^T dO,  dK = scale dS^T Q,  dQ = scale dS K
 // (s = q . k, c = scale log2 e), the heads of a group summed in dK and dV.
 //
-// Two kernels, each with its sums in tensor memory from the first term to the
+// Two kinds of CTAs, each with its sums in tensor memory from the first term to the
 // last: one owns 128 keys and goes over the rows that see them (dK, dV: four
 // products a tile), one owns a tile of 128 rows and goes over its keys (dQ: three).
 // S and dP are computed in both, seven products where five are the least, and
@@ -11,7 +11,7 @@
 // for bit, and nothing is cleared before or converted after.
 //
 // A row tile is the forward kernel's: `tokens` tokens x the group's heads, so the
-// keys' kernel adds up a group's heads as it adds up tokens.  P and dS are rounded
+// keys' CTA adds up a group's heads as it adds up tokens.  P and dS are rounded
 // to 16 bits, as tensor-core operands; they stay in tensor memory.
 #pragma once
 
@@ -65,7 +65,7 @@ struct AttnBackConfig {
     static constexpr uint32_t ID_64 = ID_BASE | (1u << 16) | ((64u >> 3) << 17);  // half the columns
 };
 
-// -LSE/scale and -delta come into S and dP as products: the keys' kernel has a key a
+// -LSE/scale and -delta come into S and dP as products: a keys' CTA has a key a
 // thread, and reading 64 rows' values from shared memory for every tile took 1100
 // of its 3500 cycles, against MMAs that read shared memory all the time.  Instead
 // one more MMA (16 values of the reduction index) adds weights x parts: a value in
@@ -94,7 +94,7 @@ __device__ __forceinline__ uint4 attn_weights() {
                                          0u, 0u);
 }
 
-// The keys' kernel: shared memory and tensor memory.
+// The keys' CTAs: shared memory and tensor memory.
 template <Kind KD, int DT>
 struct AttnKeysConfig : AttnBackConfig<KD, DT> {
     using B = AttnBackConfig<KD, DT>;
@@ -163,8 +163,7 @@ __device__ __forceinline__ void attn_store_row(uint32_t at, bool some, float f, 
 }
 
 template <Kind KD, int DT>
-__global__ void __launch_bounds__(AttnKeysConfig<KD, DT>::NUM_THREADS, 1)
-    tg_attn_keys_kernel(const __grid_constant__ AttnBackward p) {
+__device__ __forceinline__ void attn_keys(const AttnBackward &p, const int block) {
     using C = AttnKeysConfig<KD, DT>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
@@ -222,9 +221,9 @@ __global__ void __launch_bounds__(AttnKeysConfig<KD, DT>::NUM_THREADS, 1)
     }
     griddep_launch();
     griddep_wait();
-    const int head = blockIdx.x % p.h.kv_heads;
+    const int head = block % p.h.kv_heads;
     if (warp == C::LOAD_WARP) {
-        const AttnWork w = attn_find<true>(p.s, blockIdx.x / p.h.kv_heads, ATTN_KEYS, lane);
+        const AttnWork w = attn_find<true>(p.s, block / p.h.kv_heads, ATTN_KEYS, lane);
         if (lane == 0) *shared_work = w;
     }
     tc_fence_before();
@@ -511,7 +510,7 @@ __global__ void __launch_bounds__(AttnKeysConfig<KD, DT>::NUM_THREADS, 1)
     }
 }
 
-// The rows' kernel.
+// The rows' CTAs.
 template <Kind KD, int DT>
 struct AttnRowsConfig : AttnBackConfig<KD, DT> {
     using B = AttnBackConfig<KD, DT>;
@@ -532,8 +531,7 @@ struct AttnRowsConfig : AttnBackConfig<KD, DT> {
 };
 
 template <Kind KD, int DT>
-__global__ void __launch_bounds__(AttnRowsConfig<KD, DT>::NUM_THREADS, 1)
-    tg_attn_rows_kernel(const __grid_constant__ AttnBackward p) {
+__device__ __forceinline__ void attn_rows(const AttnBackward &p, const int block) {
     using C = AttnRowsConfig<KD, DT>;
     constexpr int S = C::STAGES;
     extern __shared__ uint8_t smem_raw[];
@@ -573,9 +571,9 @@ __global__ void __launch_bounds__(AttnRowsConfig<KD, DT>::NUM_THREADS, 1)
     }
     griddep_launch();
     griddep_wait();
-    const int head = blockIdx.x % p.h.kv_heads;
+    const int head = block % p.h.kv_heads;
     if (warp == C::LOAD_WARP) {
-        const AttnWork w = attn_find<false>(p.s, p.tiles - 1 - blockIdx.x / p.h.kv_heads, p.h.tokens, lane);
+        const AttnWork w = attn_find<false>(p.s, p.tiles - 1 - block / p.h.kv_heads, p.h.tokens, lane);
         if (lane == 0) *shared_work = w;
     }
     tc_fence_before();
@@ -760,6 +758,15 @@ __global__ void __launch_bounds__(AttnRowsConfig<KD, DT>::NUM_THREADS, 1)
         tc_fence_after();
         tmem_dealloc(tmem, C::TMEM_COLS);
     }
+}
+
+// Both in one launch, the keys' CTAs (the longer work) first: the rows' fill in
+// where the keys' run out.
+template <Kind KD, int DT>
+__global__ void __launch_bounds__(AttnBackConfig<KD, DT>::NUM_THREADS, 1)
+    tg_attn_backward_kernel(const __grid_constant__ AttnBackward p) {
+    if ((int)blockIdx.x < p.key_ctas) attn_keys<KD, DT>(p, blockIdx.x);
+    else attn_rows<KD, DT>(p, blockIdx.x - p.key_ctas);
 }
 
 }  // namespace tg
