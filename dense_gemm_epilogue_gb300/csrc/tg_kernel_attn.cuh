@@ -3,13 +3,12 @@
 // A tile is 128 rows: `tokens` consecutive tokens of a sequence times the
 // `group` query heads that share a key head, so that every key and value that
 // comes in serves the whole group.  Over blocks of 128 keys, for each row,
-//   s_j = q . k_j,  m' = max(m, s_j),  p_j = 2^(c (s_j - m')),  c = scale log2 e
-//   l' = l 2^(c (m - m')) + sum p_j,  o' = o 2^(c (m - m')) + sum p_j v_j
+//   s_j = q . k_j,  p_j = 2^(c s_j - r),  c = scale log2 e
+//   l' = l 2^(r - r') + sum p_j,  o' = o 2^(r - r') + sum p_j v_j
 // and in the end o / l: one pass, with O and S in tensor memory and a thread
-// for each row.  The reference m stands until the maximum has outgrown it by
-// 2^8 (p stays below 256, exact enough in 16 bits and far from FP16's end), so
-// that O is rescaled in a few blocks only.  p is rounded to 16 bits for the
-// second product; l sums it unrounded in FP32.
+// for each row.  Any reference r' >= r near the row's maximum (times c) will do;
+// it is raised, and O rescaled, in a few blocks only.  p is rounded to 16 bits for
+// the second product; l sums it unrounded in FP32.
 //
 // NQ = 2 (many tiles): two tiles a CTA, four warps each for the softmax, one
 // warp for the loads, one thread for the MMAs.  While the warps of one tile
@@ -39,7 +38,7 @@ struct AttnConfig {
     static constexpr int KV_OFF = NQ * TILE_BYTES;
     static constexpr int BAR_OFF = KV_OFF + STAGES * TILE_BYTES;
     static constexpr int QF = 0, FULL0 = 1, EMPTY0 = FULL0 + STAGES, SF0 = EMPTY0 + STAGES, PR0 = SF0 + 2,
-                         PH0 = PR0 + 2, OD0 = PH0 + 2, PVD = OD0 + 2, TURN0 = PVD + 1, DRAIN0 = TURN0 + 2,
+                         PH0 = PR0 + 2, PVA0 = PH0 + 2, OD0 = PVA0 + 2, PVD = OD0 + 2, TURN0 = PVD + 1, DRAIN0 = TURN0 + 2,
                          NUM_BARS = DRAIN0 + 2;
     static constexpr int MISC_OFF = BAR_OFF + NUM_BARS * 8;
     static constexpr int SMEM_BYTES = MISC_OFF + 64 + 1024;
@@ -90,6 +89,35 @@ __device__ __forceinline__ void attn_zero_row(uint8_t *tile, int row) {
     }
 }
 
+// COLS columns from tensor memory, times f, to a 16-bit row of which `left` values
+// exist; zeros where a thread has none.  (A warp loads when any has: `load`.)
+template <Kind KD, int COLS>
+__device__ __forceinline__ void attn_store_row(uint32_t at, bool some, bool load, float f, bool valid,
+                                               int left, uint16_t *dst) {
+#pragma unroll 1
+    for (int i = 0; i < COLS; i += 32) {
+        uint32_t o[32];
+        if (load) {
+            tmem_ld_row32(at + i, o);
+            tmem_ld_wait();
+        }
+        if (!valid) continue;
+#pragma unroll
+        for (int e = 0; e < 32; e += 8) {
+            if (i + e >= left) break;
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (some) {
+                uint32_t y[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    y[q] = pack_half2<KD>(__uint_as_float(o[e + 2 * q]) * f, __uint_as_float(o[e + 2 * q + 1]) * f);
+                v = make_uint4(y[0], y[1], y[2], y[3]);
+            }
+            *reinterpret_cast<uint4 *>(dst + i + e) = v;
+        }
+    }
+}
+
 template <Kind KD, int DT, int NQ>
 __global__ void __launch_bounds__(AttnConfig<KD, DT, NQ>::NUM_THREADS, 1)
     tg_attn_kernel(const __grid_constant__ AttnForward p) {
@@ -116,6 +144,7 @@ __global__ void __launch_bounds__(AttnConfig<KD, DT, NQ>::NUM_THREADS, 1)
             mbar_init(bar(C::SF0 + i), 1);
             mbar_init(bar(C::PR0 + i), 4);
             mbar_init(bar(C::PH0 + i), 4);
+            mbar_init(bar(C::PVA0 + i), 1);
             mbar_init(bar(C::OD0 + i), 1);
             mbar_init(bar(C::TURN0 + i), 1);
             mbar_init(bar(C::DRAIN0 + i), 1);
@@ -261,6 +290,7 @@ __global__ void __launch_bounds__(AttnConfig<KD, DT, NQ>::NUM_THREADS, 1)
                     if (!ok) break;
                     tc_fence_after();
                     attn_mma_ta<0, 4, 32>(o, pr, tile(v), C::ID_PV, n > 0);
+                    mma_commit(bar(C::PVA0 + t));
                     ok = wait_phase(bar(C::PR0 + slot), phase, ctl, SITE_PROBABILITIES);
                     if (!ok) break;
                     tc_fence_after();
@@ -298,7 +328,15 @@ __global__ void __launch_bounds__(AttnConfig<KD, DT, NQ>::NUM_THREADS, 1)
         const int first_seen = attn_seen(p.s, w, w.first + t * p.h.tokens);  // the tile's least
         const float c = p.h.scale_log2;
         const int end = NQ == 2 ? (t ? je[NQ - 1] : je[0]) : je[0];
-        float m = -INFINITY, l = 0.0f;
+        // The reference r, in units of log2, is the maximum of the first block; later
+        // it stands until a half block's sum of 2^(c s - r) says that it is too small
+        // (the sum is needed anyway, the maximum would cost a quarter of the softmax's
+        // time).  FP32 sums and BF16 probabilities are as exact far above 1 as below; in
+        // FP16 the limit keeps them from overflow.
+        constexpr float LIMIT = KD == Kind::BF16 ? 1073741824.0f : 16384.0f;
+        const uint32_t o_at = tmem + lane_base + C::O_COL + t * DT;
+        const uint64_t cc = pair2(c, c);
+        float r = 0.0f, l = 0.0f;
         bool ok = true;
         for (int j = jb; j < end; ++j) {
             const int n = j - jb;
@@ -307,14 +345,11 @@ __global__ void __launch_bounds__(AttnConfig<KD, DT, NQ>::NUM_THREADS, 1)
             if (!wait_warp(bar(C::SF0 + slot), phase, ctl, SITE_SCORES)) { ok = false; break; }
             tc_fence_after();
             const uint32_t s_at = tmem + lane_base + slot * 128;
-            // Two readings of S, for the maximum and for the exponentials, 64 columns
-            // at a time: all 128 at once left the CTA's registers short.
             const bool cut = (j + 1) * ATTN_KEYS > first_seen;
             const int lim = cut ? seen - j * ATTN_KEYS : ATTN_KEYS;
-            float mn = m;
-#pragma unroll
-            for (int h = 0; h < 128; h += 64) {
-                uint32_t s[64];
+            // Half the row's scores at a time: all 128 at once leave the CTA's
+            // registers short.
+            auto half = [&](int h, uint32_t *s) {
                 tmem_ld_row32(s_at + h, s);
                 tmem_ld_row32(s_at + h + 32, s + 32);
                 tmem_ld_wait();
@@ -323,88 +358,100 @@ __global__ void __launch_bounds__(AttnConfig<KD, DT, NQ>::NUM_THREADS, 1)
                     for (int i = 0; i < 64; ++i)
                         if (h + i >= lim) s[i] = 0xff800000u;
                 }
+            };
+            auto largest = [&](const uint32_t *s) -> float {
                 float mx[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) mx[i] = max3(__uint_as_float(s[3 * i]), __uint_as_float(s[3 * i + 1]), __uint_as_float(s[3 * i + 2]));
+                for (int i = 0; i < 4; ++i)
+                    mx[i] = max3(__uint_as_float(s[3 * i]), __uint_as_float(s[3 * i + 1]), __uint_as_float(s[3 * i + 2]));
 #pragma unroll
                 for (int i = 12; i < 64; i += 2)
                     mx[(i >> 1) & 3] = max3(mx[(i >> 1) & 3], __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
-                mn = max3(mn, max3(mx[0], mx[1], mx[2]), mx[3]);
-            }
-            if (cut) {
-                // Values behind the sequence's end: zero (see attn_zero_row).  (The
-                // barrier is at most one phase behind: the thread that issued these
-                // scores has waited for the slot's earlier items.)
-                const int left = w.lk - j * ATTN_KEYS;
-                if (left < ATTN_KEYS) {
-                    const int it = 2 * n + 1;
-                    if (!wait_warp(bar(C::FULL0 + it % S), (uint32_t)(it / S) & 1, ctl, SITE_FULL)) {
-                        ok = false;
-                        break;
-                    }
-                    if (row >= left) {
-                        attn_zero_row<C::HALVES>(smem + C::KV_OFF + (it % S) * C::TILE_BYTES, row);
-                        fence_proxy_async_smem();
-                    }
-                }
-            }
-            // (Every lane keeps its reference unless one has outgrown it.)
-            if (__any_sync(0xffffffffu, (mn - m) * c > 8.0f)) {
-                const float f = mn == m ? 1.0f : exp2_approx((m - mn) * c);
-                m = mn;
-                l *= f;
-                if (n > 0) {
-                    if (NQ == 1 && !wait_warp(bar(C::PVD), (n - 1) & 1, ctl, SITE_ACC_FULL)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t o_at = tmem + lane_base + C::O_COL + t * DT;
-#pragma unroll 1
-                    for (int i = 0; i < DT; i += 32) {
-                        uint32_t o[32];
-                        tmem_ld_row32(o_at + i, o);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                        tmem_st_32x32b_x32(o_at + i, o);
-                    }
-                }
-            }
-            const float mc = m == -INFINITY ? 0.0f : -m * c;
-            const uint64_t cc = pair2(c, c), mm = pair2(mc, mc);
-            uint64_t sum[2] = {0, 0};
-            const uint32_t p_at = tmem + lane_base + C::P_COL + slot * C::P_STEP;
-#pragma unroll
-            for (int h = 0; h < 128; h += 64) {
-                uint32_t s[64], y[32];
-                tmem_ld_row32(s_at + h, s);
-                tmem_ld_row32(s_at + h + 32, s + 32);
-                tmem_ld_wait();
-                if (cut) {
-#pragma unroll
-                    for (int i = 0; i < 64; ++i)
-                        if (h + i >= lim) s[i] = 0xff800000u;
-                }
+                return max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
+            };
+            uint32_t s[64], y[32];
+            auto exponentials = [&]() -> float {
+                const uint64_t rr = pair2(-r, -r);
+                uint64_t sum[2] = {0, 0};
 #pragma unroll
                 for (int i = 0; i < 32; ++i) {
                     float a, b;
-                    unpair2(fma_pair(pair2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), cc, mm), a, b);
+                    unpair2(fma_pair(pair2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), cc, rr), a, b);
                     a = exp2_approx(a);
                     b = exp2_approx(b);
                     sum[i & 1] = add_pair(sum[i & 1], pair2(a, b));
                     y[i] = pack_half2<KD>(a, b);
                 }
-                // (P over S: columns 0 to 31 and 32 to 63, both read by now.)
-                tmem_st_32x32b_x32(p_at + h / 2, y);
+                float a, b;
+                unpair2(add_pair(sum[0], sum[1]), a, b);
+                return a + b;
+            };
+            // A reference that is not below `top`, and what was summed by the old one.
+            auto raise = [&](float top) {
+                const float to = fmaxf(r, top), f = exp2_approx(r - to);
+                r = to;
+                l *= f;
+#pragma unroll 1
+                for (int i = 0; i < DT; i += 32) {
+                    uint32_t o[32];
+                    tmem_ld_row32(o_at + i, o);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                    tmem_st_32x32b_x32(o_at + i, o);
+                }
+            };
+            auto put = [&](int h, uint32_t arrived) {
+                tmem_st_32x32b_x32(tmem + lane_base + C::P_COL + slot * C::P_STEP + h / 2, y);
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar((h ? C::PR0 : C::PH0) + slot));
+                if (lane == 0) mbar_arrive(bar(arrived + slot));
+            };
+            if (n == 0) {
+                half(64, s);
+                const float mx = largest(s);
+                half(0, s);
+                const float top = fmaxf(mx, largest(s));
+                r = top == -INFINITY ? 0.0f : top * c;
+            } else {
+                half(0, s);
             }
-            float a, b;
-            unpair2(add_pair(sum[0], sum[1]), a, b);
-            l += a + b;
+            float sum = exponentials();
+            if (n > 0 && __any_sync(0xffffffffu, sum > LIMIT)) {
+                // (P over S: the first half is not stored before this is known.)
+                if (NQ == 1 && !wait_warp(bar(C::PVD), (n - 1) & 1, ctl, SITE_ACC_FULL)) { ok = false; break; }
+                tc_fence_after();
+                half(64, s);
+                const float mx = largest(s);
+                half(0, s);
+                raise(fmaxf(mx, largest(s)) * c);
+                sum = exponentials();
+            }
+            // Values behind the sequence's end: zero (see attn_zero_row).  (The barrier is
+            // at most one phase behind: the thread that issued these scores has waited
+            // for the slot's earlier items.)
+            if (w.lk - j * ATTN_KEYS < ATTN_KEYS) {
+                const int it = 2 * n + 1;
+                if (!wait_warp(bar(C::FULL0 + it % S), (uint32_t)(it / S) & 1, ctl, SITE_FULL)) { ok = false; break; }
+                if (row >= w.lk - j * ATTN_KEYS) {
+                    attn_zero_row<C::HALVES>(smem + C::KV_OFF + (it % S) * C::TILE_BYTES, row);
+                    fence_proxy_async_smem();
+                }
+            }
+            put(0, C::PH0);
+            l += sum;
+            half(64, s);
+            sum = exponentials();
+            if (n > 0 && __any_sync(0xffffffffu, sum > LIMIT)) {
+                // (The first half's product is under way by the old reference.)
+                if (!wait_warp(bar(C::PVA0 + t), n & 1, ctl, SITE_ACC_FULL)) { ok = false; break; }
+                tc_fence_after();
+                raise(largest(s) * c);
+                sum = exponentials();
+            }
+            put(64, C::PR0);
+            l += sum;
         }
         const bool some = end > jb;
         if (ok && some) {
@@ -413,10 +460,9 @@ __global__ void __launch_bounds__(AttnConfig<KD, DT, NQ>::NUM_THREADS, 1)
         }
         if (ok) {
             const int64_t at = (int64_t)qh * p.s.q_rows + w.q0 + token;
-            const uint32_t o_at = tmem + lane_base + C::O_COL + t * DT;
             if (p.splits > 1) {
                 const int64_t slot = (int64_t)split * p.h.heads * p.s.q_rows + at;
-                if (valid) p.part_ml[slot] = make_float2(m * c, l);
+                if (valid) p.part_ml[slot] = make_float2(r, l);
                 float4 *dst = reinterpret_cast<float4 *>(p.part_o + slot * p.h.dim);
                 if (some) {
 #pragma unroll 1
@@ -435,34 +481,10 @@ __global__ void __launch_bounds__(AttnConfig<KD, DT, NQ>::NUM_THREADS, 1)
                     }
                 }
             } else {
-                if (valid && p.lse)
-                    p.lse[at] = l == 0.0f ? -INFINITY : (m * c + log2f(l)) * 0.6931471805599453f;
-                const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-                uint16_t *dst = static_cast<uint16_t *>(p.o.ptr) + (w.q0 + token) * p.o.ld + qh * p.o.hd;
-#pragma unroll 1
-                for (int i = 0; i < DT; i += 32) {
-                    uint32_t o[32];
-                    if (some) {
-                        tmem_ld_row32(o_at + i, o);
-                        tmem_ld_wait();
-                    }
-                    if (valid) {
-#pragma unroll
-                        for (int e = 0; e < 32; e += 8) {
-                            if (i + e >= p.h.dim) break;
-                            uint4 v = make_uint4(0, 0, 0, 0);
-                            if (some && l != 0.0f) {
-                                uint32_t y[4];
-#pragma unroll
-                                for (int q = 0; q < 4; ++q)
-                                    y[q] = pack_half2<KD>(__uint_as_float(o[e + 2 * q]) * inv,
-                                                          __uint_as_float(o[e + 2 * q + 1]) * inv);
-                                v = make_uint4(y[0], y[1], y[2], y[3]);
-                            }
-                            *reinterpret_cast<uint4 *>(dst + i + e) = v;
-                        }
-                    }
-                }
+                if (valid && p.lse) p.lse[at] = l == 0.0f ? -INFINITY : (r + log2f(l)) * 0.6931471805599453f;
+                attn_store_row<KD, DT>(o_at, some && l != 0.0f, some, l == 0.0f ? 0.0f : 1.0f / l, valid, p.h.dim,
+                                       static_cast<uint16_t *>(p.o.ptr) + (w.q0 + (int64_t)token) * p.o.ld +
+                                           qh * p.o.hd);
             }
         }
     }

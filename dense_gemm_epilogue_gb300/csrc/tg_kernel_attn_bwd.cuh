@@ -134,34 +134,6 @@ __device__ __forceinline__ void attn_store_half(uint32_t at, const float *y) {
     tmem_st_wait();
 }
 
-// `cols` columns from tensor memory, times f, to a 16-bit row of which `left` values exist.
-template <Kind KD, int COLS>
-__device__ __forceinline__ void attn_store_row(uint32_t at, bool some, float f, bool valid, int left,
-                                               uint16_t *dst) {
-#pragma unroll 1
-    for (int i = 0; i < COLS; i += 32) {
-        uint32_t o[32];
-        if (some) {
-            tmem_ld_row32(at + i, o);
-            tmem_ld_wait();
-        }
-        if (!valid) continue;
-#pragma unroll
-        for (int e = 0; e < 32; e += 8) {
-            if (i + e >= left) break;
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (some) {
-                uint32_t y[4];
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    y[q] = pack_half2<KD>(__uint_as_float(o[e + 2 * q]) * f, __uint_as_float(o[e + 2 * q + 1]) * f);
-                v = make_uint4(y[0], y[1], y[2], y[3]);
-            }
-            *reinterpret_cast<uint4 *>(dst + i + e) = v;
-        }
-    }
-}
-
 template <Kind KD, int DT>
 __device__ __forceinline__ void attn_keys(const AttnBackward &p, const int block) {
     using C = AttnKeysConfig<KD, DT>;
@@ -497,7 +469,7 @@ __device__ __forceinline__ void attn_keys(const AttnBackward &p, const int block
         }
         const AttnOut &out = half ? p.dk : p.dv;
         if (ok && out.ptr)
-            attn_store_row<KD, DT>(tmem + lane_base + (half ? C::DK_COL : C::DV_COL), tiles > 0,
+            attn_store_row<KD, DT>(tmem + lane_base + (half ? C::DK_COL : C::DV_COL), tiles > 0, tiles > 0,
                                    half ? p.h.scale : 1.0f, key < w.lk, p.h.dim,
                                    static_cast<uint16_t *>(out.ptr) + (w.k0 + (int64_t)key) * out.ld + head * out.hd);
     }
@@ -746,7 +718,7 @@ __device__ __forceinline__ void attn_rows(const AttnBackward &p, const int block
             tc_fence_after();
         }
         if (ok)
-            attn_store_row<KD, DT / 2>(tmem + lane_base + C::DQ_COL + half * (DT / 2), blocks > 0, p.h.scale, valid,
+            attn_store_row<KD, DT / 2>(tmem + lane_base + C::DQ_COL + half * (DT / 2), blocks > 0, blocks > 0, p.h.scale, valid,
                                        p.h.dim - half * (DT / 2),
                                        static_cast<uint16_t *>(p.dq.ptr) + (w.q0 + (int64_t)token) * p.dq.ld +
                                            qh * p.dq.hd + half * (DT / 2));
