@@ -276,18 +276,18 @@ __global__ void __launch_bounds__(AttnConfig<KD, DT, NQ>::NUM_THREADS, 1)
             for (int n = 0; ok && n < all; ++n) {
                 const int slot = NQ == 2 ? t : n & 1;
                 const uint32_t phase = NQ == 2 ? n & 1 : (n >> 1) & 1;
+                // (Waits that can be before the turn are: one on shared memory takes 150
+                // cycles under the MMAs' reads even when its phase is over.)
+                ok = full(v) && (n + 1 == all || full(k));
+                if (!ok) break;
                 if (NQ == 1 && n + 1 < all) {
-                    ok = full(k);
-                    if (!ok) break;
                     scores((n + 1) & 1);
                     release(k);
                 }
-                ok = full(v);
+                ok = (n >= mine || wait_phase(bar(C::PH0 + slot), phase, ctl, SITE_PROBABILITIES)) && turn();
                 if (!ok) break;
                 if (n < mine) {
                     const uint32_t pr = tmem + C::P_COL + slot * C::P_STEP;
-                    ok = wait_phase(bar(C::PH0 + slot), phase, ctl, SITE_PROBABILITIES) && turn();
-                    if (!ok) break;
                     tc_fence_after();
                     attn_mma_ta<0, 4, 32>(o, pr, tile(v), C::ID_PV, n > 0);
                     mma_commit(bar(C::PVA0 + t));
@@ -295,16 +295,11 @@ __global__ void __launch_bounds__(AttnConfig<KD, DT, NQ>::NUM_THREADS, 1)
                     if (!ok) break;
                     tc_fence_after();
                     attn_mma_ta<4, 8, 32>(o, pr, tile(v), C::ID_PV, true);
-                } else {
-                    ok = turn();
-                    if (!ok) break;
                 }
                 release(v);
                 if (NQ == 1 && n + 1 < all) mma_commit(bar(C::PVD));
                 if (n + 1 == mine) mma_commit(bar(C::OD0 + t));
                 if (NQ == 2 && n + 1 < all) {
-                    ok = full(k);
-                    if (!ok) break;
                     if (n + 1 < mine) scores(slot);
                     release(k);
                 }
