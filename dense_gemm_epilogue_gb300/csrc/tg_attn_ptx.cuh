@@ -71,6 +71,17 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map
         : "memory");
 }
 
+// Cluster launch control for CTAs on their own: ask for a CTA of this grid that has
+// not started, to do its work here.  The answer (clc_cancelled_x) lands at `resp`, 16
+// bytes on the barrier at `bar`.
+__device__ __forceinline__ void clc_try_cancel(uint32_t resp, uint32_t bar) {
+    asm volatile(
+        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+            resp),
+        "r"(bar)
+        : "memory");
+}
+
 // Descriptor of an MN-major operand held as boxes of 64 values (128 bytes,
 // 128-byte swizzle) x 128 reduction rows: the next 64 values 16 KB on (leading
 // byte offset), the next 8 reduction rows 1 KB on (stride byte offset).

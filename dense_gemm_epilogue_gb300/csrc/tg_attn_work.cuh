@@ -36,6 +36,7 @@ struct AttnWork {
     int seq;    // -1: nothing
     int first;  // first token (or key) of the tile within the sequence
     int q0, lq, k0, lk;
+    int head, split;  // (set by the kernels that need them; head < 0: no more work)
 };
 
 // Tile t, counted through the sequences in order, `per` tokens (or keys) each:

@@ -39,9 +39,12 @@ struct AttnConfig {
     static constexpr int BAR_OFF = KV_OFF + STAGES * TILE_BYTES;
     static constexpr int QF = 0, FULL0 = 1, EMPTY0 = FULL0 + STAGES, SF0 = EMPTY0 + STAGES, PR0 = SF0 + 2,
                          PH0 = PR0 + 2, PVA0 = PH0 + 2, OD0 = PVA0 + 2, PVD = OD0 + 2, TURN0 = PVD + 1, DRAIN0 = TURN0 + 2,
-                         NUM_BARS = DRAIN0 + 2;
-    static constexpr int MISC_OFF = BAR_OFF + NUM_BARS * 8;
-    static constexpr int SMEM_BYTES = MISC_OFF + 64 + 1024;
+                         QE = DRAIN0 + 2, OE0 = QE + 1, WF0 = OE0 + 2, WE0 = WF0 + 2, NEXT = WE0 + 2,
+                         NUM_BARS = NEXT + 1;
+    static constexpr int NEXT_OFF = (BAR_OFF + NUM_BARS * 8 + 15) / 16 * 16;  // launch control's answer
+    static constexpr int MISC_OFF = NEXT_OFF + 16;
+    static constexpr int WORK_OFF = MISC_OFF + 16;  // two pieces of work
+    static constexpr int SMEM_BYTES = WORK_OFF + 2 * sizeof(AttnWork) + 1024;
     static constexpr int SOFT_WARPS = 4 * NQ;
     static constexpr int LOAD_WARP = SOFT_WARPS, MMA_WARP = SOFT_WARPS + 1;
     static constexpr int NUM_THREADS = 32 * (SOFT_WARPS + 1 + NQ);  // an MMA warp a tile
@@ -118,6 +121,27 @@ __device__ __forceinline__ void attn_store_row(uint32_t at, bool some, bool load
     }
 }
 
+// Key blocks of a piece of work: from jb, to je[t] for tile t; `all` together.
+template <int NQ>
+struct AttnBlocks {
+    int jb, je[NQ], all;
+    __device__ __forceinline__ AttnBlocks(const AttnForward &p, const AttnWork &w) {
+        jb = w.split * p.chunk;
+        int last = jb;
+#pragma unroll
+        for (int t = 0; t < NQ; ++t) {
+            const int end = w.first + (t + 1) * p.h.tokens;  // tokens before it are in tiles up to t
+            const int tokens = end < w.lq ? end : w.lq;
+            const int seen = tokens > w.first + t * p.h.tokens ? attn_seen(p.s, w, tokens - 1) : 0;
+            je[t] = (seen + ATTN_KEYS - 1) / ATTN_KEYS;
+            if (je[t] > jb + p.chunk) je[t] = jb + p.chunk;
+            if (je[t] < jb) je[t] = jb;
+            if (je[t] > last) last = je[t];
+        }
+        all = last - jb;
+    }
+};
+
 template <Kind KD, int DT, int NQ>
 __global__ void __launch_bounds__(AttnConfig<KD, DT, NQ>::NUM_THREADS, 1)
     tg_attn_kernel(const __grid_constant__ AttnForward p) {
@@ -131,11 +155,11 @@ __global__ void __launch_bounds__(AttnConfig<KD, DT, NQ>::NUM_THREADS, 1)
     auto bar = [&](int i) -> uint32_t { return sbase + C::BAR_OFF + 8 * i; };
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::MISC_OFF);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::MISC_OFF + 4);
-    AttnWork *shared_work = reinterpret_cast<AttnWork *>(smem + C::MISC_OFF + 8);
     const WaitCtl ctl{abort_flag, p.status, p.wait_limit_ns};
 
     if (threadIdx.x == 0) {
         mbar_init(bar(C::QF), 1);
+        mbar_init(bar(C::QE), NQ);
         for (int s = 0; s < S; ++s) {
             mbar_init(bar(C::FULL0 + s), 1);
             mbar_init(bar(C::EMPTY0 + s), NQ);
@@ -146,10 +170,14 @@ __global__ void __launch_bounds__(AttnConfig<KD, DT, NQ>::NUM_THREADS, 1)
             mbar_init(bar(C::PH0 + i), 4);
             mbar_init(bar(C::PVA0 + i), 1);
             mbar_init(bar(C::OD0 + i), 1);
+            mbar_init(bar(C::OE0 + i), 4);
             mbar_init(bar(C::TURN0 + i), 1);
             mbar_init(bar(C::DRAIN0 + i), 1);
+            mbar_init(bar(C::WF0 + i), 1);
+            mbar_init(bar(C::WE0 + i), C::SOFT_WARPS + NQ);
         }
         mbar_init(bar(C::PVD), 1);
+        mbar_init(bar(C::NEXT), 1);
         *abort_flag = 0;
         fence_mbar_init();
         prefetch_tensormap(&p.q);
@@ -160,69 +188,125 @@ __global__ void __launch_bounds__(AttnConfig<KD, DT, NQ>::NUM_THREADS, 1)
         tmem_alloc(smem_u32(tmem_slot), C::TMEM_COLS);
         tmem_relinquish();
     }
-    // Blocks count down through the tiles: the last tokens of a sequence see the
-    // most keys, and the long work is better begun first.
-    const int split = blockIdx.x % p.splits;
-    const int rest = blockIdx.x / p.splits;
-    const int head = rest % p.h.kv_heads;
-    griddep_launch();
-    griddep_wait();
-    if (warp == C::LOAD_WARP) {
-        const AttnWork w = attn_find<false>(p.s, p.tiles - 1 - rest / p.h.kv_heads, NQ * p.h.tokens, lane);
-        if (lane == 0) *shared_work = w;
-    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    griddep_launch();
+    griddep_wait();
     const uint32_t tmem = *tmem_slot;
-    const AttnWork w = *shared_work;
+    // Piece `step` of this CTA's work, from LOAD_WARP.
+    auto work_at = [&](int step) -> volatile AttnWork * {
+        return reinterpret_cast<volatile AttnWork *>(smem + C::WORK_OFF) + (step & 1);
+    };
+    auto read_work = [&](int step) -> AttnWork {
+        const volatile AttnWork *v = work_at(step);
+        AttnWork w;
+        w.seq = v->seq;
+        w.first = v->first;
+        w.q0 = v->q0;
+        w.lq = v->lq;
+        w.k0 = v->k0;
+        w.lk = v->lk;
+        w.head = v->head;
+        w.split = v->split;
+        return w;
+    };
 
-    // Blocks of keys: from jb, to je[t] for tile t.
-    const int jb = split * p.chunk;
-    int je[NQ], last = jb;
-#pragma unroll
-    for (int t = 0; t < NQ; ++t) {
-        const int end = w.first + (t + 1) * p.h.tokens;  // tokens before it are in tiles up to t
-        const int tokens = end < w.lq ? end : w.lq;
-        const int seen = tokens > w.first + t * p.h.tokens ? attn_seen(p.s, w, tokens - 1) : 0;
-        je[t] = (seen + ATTN_KEYS - 1) / ATTN_KEYS;
-        if (je[t] > jb + p.chunk) je[t] = jb + p.chunk;
-        if (w.seq < 0 || je[t] < jb) je[t] = jb;
-        if (je[t] > last) last = je[t];
-    }
-
+    int asked = 0, loads = 0, tiles_q = 0;  // LOAD_WARP: answers, ring items, Q tiles asked for so far
     if (warp == C::LOAD_WARP) {
-        if (last > jb && elect_one()) {
-            mbar_arrive_expect_tx(bar(C::QF), NQ * C::HALVES * p.h.tokens * p.h.group * 128);
-#pragma unroll
-            for (int t = 0; t < NQ; ++t)
-#pragma unroll
-                for (int h = 0; h < C::HALVES; ++h)
-                    tma_load_4d(sbase + C::Q_OFF + t * C::TILE_BYTES + h * 16384, &p.q, bar(C::QF), h * 64,
-                                0, head, w.q0 + w.first + t * p.h.tokens);
-            const int items = 2 * (last - jb);
-            int s = 0, issued = 0;
-            uint32_t ph = 0;
-            bool ok = true;
-            for (int it = 0; it < items; ++it) {
-                if (!wait_phase(bar(C::EMPTY0 + s), ph ^ 1, ctl, SITE_EMPTY)) { ok = false; break; }
-                mbar_arrive_expect_tx(bar(C::FULL0 + s), C::TILE_BYTES);
-                const int row = w.k0 + (jb + (it >> 1)) * ATTN_KEYS;
-#pragma unroll
-                for (int h = 0; h < C::HALVES; ++h)
-                    tma_load_3d(sbase + C::KV_OFF + s * C::TILE_BYTES + h * 16384, it & 1 ? &p.v : &p.k,
-                                bar(C::FULL0 + s), h * 64, head, row);
-                ++issued;
-                if (++s == S) { s = 0; ph ^= 1; }
+        // ------------------------------------------------------ work and loads
+        // A CTA that is done takes over the work of one that has not started (launch
+        // control), so that only its first piece waits for its set-up: the next piece
+        // is asked for, found and loaded while the ring's last blocks are in work.  (Asked
+        // for earlier, the last pieces went to CTAs that were not the first to be free.)
+        int item = blockIdx.x, step = 0;
+        bool ok = true;
+        while (ok) {
+            AttnWork w;
+            w.head = -1;
+            if (item >= 0) {
+                // Pieces count down through the tiles: the last tokens of a sequence see
+                // the most keys, and the long work is better begun first.
+                const int rest = item / p.splits;
+                w = attn_find<false>(p.s, p.tiles - 1 - rest / p.h.kv_heads, NQ * p.h.tokens, lane);
+                w.head = rest % p.h.kv_heads;
+                w.split = item % p.splits;
             }
-            if (!ok) {
-                // Every copy already issued lands before the CTA exits.
-                wait_phase_drain(bar(C::QF), 0, ctl);
-                for (int st = 0; st < S && st < issued; ++st)
-                    wait_phase_drain(bar(C::FULL0 + st), (uint32_t)((issued - 1 - st) / S & 1), ctl);
+            if (w.seq >= 0) {
+                if (!wait_warp(bar(C::WE0 + (step & 1)), (uint32_t)(step >> 1 & 1) ^ 1, ctl, SITE_SCHED)) break;
+                if (lane == 0) {
+                    volatile AttnWork *v = work_at(step);
+                    v->seq = w.seq;
+                    v->first = w.first;
+                    v->q0 = w.q0;
+                    v->lq = w.lq;
+                    v->k0 = w.k0;
+                    v->lk = w.lk;
+                    v->head = w.head;
+                    v->split = w.split;
+                    mbar_arrive(bar(C::WF0 + (step & 1)));
+                }
+                ++step;
+                __syncwarp();
+                const AttnBlocks<NQ> b(p, w);
+                if (b.all > 0) {
+                    if (elect_one()) {
+                        ok = wait_phase(bar(C::QE), (uint32_t)(tiles_q & 1) ^ 1, ctl, SITE_EMPTY);
+                        if (ok) {
+                            mbar_arrive_expect_tx(bar(C::QF), NQ * C::HALVES * p.h.tokens * p.h.group * 128);
+#pragma unroll
+                            for (int t = 0; t < NQ; ++t)
+#pragma unroll
+                                for (int h = 0; h < C::HALVES; ++h)
+                                    tma_load_4d(sbase + C::Q_OFF + t * C::TILE_BYTES + h * 16384, &p.q, bar(C::QF),
+                                                h * 64, 0, w.head, w.q0 + w.first + t * p.h.tokens);
+                            ++tiles_q;
+                        }
+                        int s = loads % S;
+                        uint32_t ph = (uint32_t)(loads / S) & 1;
+                        for (int it = 0; ok && it < 2 * b.all; ++it) {
+                            if (!wait_phase(bar(C::EMPTY0 + s), ph ^ 1, ctl, SITE_EMPTY)) { ok = false; break; }
+                            mbar_arrive_expect_tx(bar(C::FULL0 + s), C::TILE_BYTES);
+                            const int row = w.k0 + (b.jb + (it >> 1)) * ATTN_KEYS;
+#pragma unroll
+                            for (int h = 0; h < C::HALVES; ++h)
+                                tma_load_3d(sbase + C::KV_OFF + s * C::TILE_BYTES + h * 16384, it & 1 ? &p.v : &p.k,
+                                            bar(C::FULL0 + s), h * 64, w.head, row);
+                            ++loads;
+                            if (++s == S) { s = 0; ph ^= 1; }
+                        }
+                    }
+                    // (the counts of the lane that loaded, the only one that counted)
+                    loads = __reduce_max_sync(0xffffffffu, loads);
+                    tiles_q = __reduce_max_sync(0xffffffffu, tiles_q);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                }
+            }
+            if (lane == 0) {
+                fence_proxy_async_smem();
+                mbar_arrive_expect_tx(bar(C::NEXT), 16);
+                clc_try_cancel(sbase + C::NEXT_OFF, bar(C::NEXT));
+            }
+            ++asked;
+            __syncwarp();
+            ok = wait_warp(bar(C::NEXT), (uint32_t)(asked - 1) & 1, ctl, SITE_SCHED);
+            if (!ok) break;
+            const volatile uint64_t *answer = reinterpret_cast<const volatile uint64_t *>(smem + C::NEXT_OFF);
+            item = clc_cancelled_x(answer[0], answer[1]);
+            __syncwarp();
+            if (item < 0) {
+                if (!wait_warp(bar(C::WE0 + (step & 1)), (uint32_t)(step >> 1 & 1) ^ 1, ctl, SITE_SCHED)) {
+                    ok = false;
+                    break;
+                }
+                if (lane == 0) {
+                    work_at(step)->head = -1;
+                    mbar_arrive(bar(C::WF0 + (step & 1)));
+                }
+                break;
             }
         }
-        __syncwarp();
     } else if (warp >= C::MMA_WARP) {
         // A thread for each tile's products: while one waits for its probabilities
         // the other's are in the tensor core's queue, which holds only a few (with
@@ -230,8 +314,7 @@ __global__ void __launch_bounds__(AttnConfig<KD, DT, NQ>::NUM_THREADS, 1)
         // They take turns, a tile's P V and next S at a time: mixed, both tiles'
         // scores would be ready at once and both tiles' softmax stand idle at once.
         const int t = warp - C::MMA_WARP;
-        if (last > jb && elect_one()) {
-            const int mine = (NQ == 2 && t ? je[NQ - 1] : je[0]) - jb, all = last - jb;
+        if (elect_one()) {
             const uint32_t q = sbase + C::Q_OFF + t * C::TILE_BYTES;
             const uint32_t o = tmem + C::O_COL + t * DT;
             // The ring's items in order: K, V, K, V, ...
@@ -254,10 +337,6 @@ __global__ void __launch_bounds__(AttnConfig<KD, DT, NQ>::NUM_THREADS, 1)
                 r.next();
                 r.next();
             };
-            auto scores = [&](int slot) {
-                attn_mma_rows<0, DT / 16>(tmem + slot * 128, q, tile(k), C::ID_S);
-                mma_commit(bar(C::SF0 + slot));
-            };
             uint32_t turns = t;  // of the other thread's awaited so far, odd for t = 1
             auto turn = [&]() -> bool {
                 if (NQ == 1) return true;
@@ -267,43 +346,69 @@ __global__ void __launch_bounds__(AttnConfig<KD, DT, NQ>::NUM_THREADS, 1)
             auto pass = [&] {
                 if (NQ == 2) mbar_arrive(bar(C::TURN0 + (t ^ 1)));
             };
-            bool ok = wait_phase(bar(C::QF), 0, ctl, SITE_FULL) && full(k) && turn();
-            if (ok) {
-                if (mine > 0) scores(NQ == 2 ? t : 0);
+            bool ok = true;
+            uint32_t g = 0;             // blocks of this tile so far
+            uint32_t pieces = 0, o_used = 0;  // pieces with keys; those with keys for this tile
+            for (int step = 0; ok; ++step) {
+                ok = wait_phase(bar(C::WF0 + (step & 1)), (uint32_t)(step >> 1) & 1, ctl, SITE_SCHED);
+                if (!ok) break;
+                const AttnWork w = read_work(step);
+                mbar_arrive(bar(C::WE0 + (step & 1)));
+                if (w.head < 0) break;
+                const AttnBlocks<NQ> b(p, w);
+                const int all = b.all, mine = (NQ == 2 && t ? b.je[NQ - 1] : b.je[0]) - b.jb;
+                if (all == 0) continue;
+                auto scores = [&](int n) {
+                    const int slot = NQ == 2 ? t : (int)((g + n) & 1);
+                    attn_mma_rows<0, DT / 16>(tmem + slot * 128, q, tile(k), C::ID_S);
+                    mma_commit(bar(C::SF0 + slot));
+                    if (n + 1 == mine) mma_commit(bar(C::QE));
+                };
+                ok = wait_phase(bar(C::QF), pieces & 1, ctl, SITE_FULL) && full(k) && turn();
+                if (!ok) break;
+                ++pieces;
+                if (mine > 0) scores(0);
+                else mma_commit(bar(C::QE));
                 release(k);
                 pass();
-            }
-            for (int n = 0; ok && n < all; ++n) {
-                const int slot = NQ == 2 ? t : n & 1;
-                const uint32_t phase = NQ == 2 ? n & 1 : (n >> 1) & 1;
-                // (Waits that can be before the turn are: one on shared memory takes 150
-                // cycles under the MMAs' reads even when its phase is over.)
-                ok = full(v) && (n + 1 == all || full(k));
-                if (!ok) break;
-                if (NQ == 1 && n + 1 < all) {
-                    scores((n + 1) & 1);
-                    release(k);
-                }
-                ok = (n >= mine || wait_phase(bar(C::PH0 + slot), phase, ctl, SITE_PROBABILITIES)) && turn();
-                if (!ok) break;
-                if (n < mine) {
-                    const uint32_t pr = tmem + C::P_COL + slot * C::P_STEP;
-                    tc_fence_after();
-                    attn_mma_ta<0, 4, 32>(o, pr, tile(v), C::ID_PV, n > 0);
-                    mma_commit(bar(C::PVA0 + t));
-                    ok = wait_phase(bar(C::PR0 + slot), phase, ctl, SITE_PROBABILITIES);
+                for (int n = 0; n < all; ++n) {
+                    const int slot = NQ == 2 ? t : (int)((g + n) & 1);
+                    const uint32_t phase = NQ == 2 ? (g + n) & 1 : ((g + n) >> 1) & 1;
+                    // (Waits that can be before the turn are: one on shared memory takes
+                    // 150 cycles under the MMAs' reads even when its phase is over.)
+                    ok = full(v) && (n + 1 == all || full(k));
                     if (!ok) break;
-                    tc_fence_after();
-                    attn_mma_ta<4, 8, 32>(o, pr, tile(v), C::ID_PV, true);
+                    if (NQ == 1 && n + 1 < all) {
+                        scores(n + 1);
+                        release(k);
+                    }
+                    if (n == 0 && mine > 0 && o_used > 0)  // (O is still the piece's before)
+                        ok = wait_phase(bar(C::OE0 + t), (o_used - 1) & 1, ctl, SITE_ACC_EMPTY);
+                    ok = ok && (n >= mine || wait_phase(bar(C::PH0 + slot), phase, ctl, SITE_PROBABILITIES)) && turn();
+                    if (!ok) break;
+                    if (n < mine) {
+                        const uint32_t pr = tmem + C::P_COL + slot * C::P_STEP;
+                        tc_fence_after();
+                        attn_mma_ta<0, 4, 32>(o, pr, tile(v), C::ID_PV, n > 0);
+                        mma_commit(bar(C::PVA0 + t));
+                        ok = wait_phase(bar(C::PR0 + slot), phase, ctl, SITE_PROBABILITIES);
+                        if (!ok) break;
+                        tc_fence_after();
+                        attn_mma_ta<4, 8, 32>(o, pr, tile(v), C::ID_PV, true);
+                    }
+                    release(v);
+                    if (NQ == 1) mma_commit(bar(C::PVD));
+                    if (n + 1 == mine) mma_commit(bar(C::OD0 + t));
+                    if (NQ == 2 && n + 1 < all) {
+                        if (n + 1 < mine) scores(n + 1);
+                        release(k);
+                    }
+                    pass();
                 }
-                release(v);
-                if (NQ == 1 && n + 1 < all) mma_commit(bar(C::PVD));
-                if (n + 1 == mine) mma_commit(bar(C::OD0 + t));
-                if (NQ == 2 && n + 1 < all) {
-                    if (n + 1 < mine) scores(slot);
-                    release(k);
+                if (mine > 0) {
+                    g += mine;
+                    ++o_used;
                 }
-                pass();
             }
             if (!ok) {
                 mma_commit(bar(C::DRAIN0 + t));
@@ -311,181 +416,210 @@ __global__ void __launch_bounds__(AttnConfig<KD, DT, NQ>::NUM_THREADS, 1)
             }
         }
         __syncwarp();
-    } else if (w.seq >= 0) {
+    } else {
         // ------------------------------------------------------ softmax: a row a thread
         const int t = NQ == 2 ? warp >> 2 : 0;
         const int row = threadIdx.x & 127;
         const uint32_t lane_base = (uint32_t)(warp & 3) << 21;  // lane field: bits 16 up
-        const int token = w.first + t * p.h.tokens + row / p.h.group;
-        const int qh = head * p.h.group + row % p.h.group;
-        const bool valid = row < p.h.tokens * p.h.group && token < w.lq;
-        const int seen = valid ? attn_seen(p.s, w, token) : 0;
-        const int first_seen = attn_seen(p.s, w, w.first + t * p.h.tokens);  // the tile's least
-        const float c = p.h.scale_log2;
-        const int end = NQ == 2 ? (t ? je[NQ - 1] : je[0]) : je[0];
         // The reference r, in units of log2, is the maximum of the first block; later
         // it stands until a half block's sum of 2^(c s - r) says that it is too small
         // (the sum is needed anyway, the maximum would cost a quarter of the softmax's
         // time).  FP32 sums and BF16 probabilities are as exact far above 1 as below; in
         // FP16 the limit keeps them from overflow.
         constexpr float LIMIT = KD == Kind::BF16 ? 1073741824.0f : 16384.0f;
-        const uint32_t o_at = tmem + lane_base + C::O_COL + t * DT;
+        const float c = p.h.scale_log2;
         const uint64_t cc = pair2(c, c);
-        float r = 0.0f, l = 0.0f;
+        const uint32_t o_at = tmem + lane_base + C::O_COL + t * DT;
         bool ok = true;
-        for (int j = jb; j < end; ++j) {
-            const int n = j - jb;
-            const int slot = NQ == 2 ? t : n & 1;
-            const uint32_t phase = NQ == 2 ? n & 1 : (n >> 1) & 1;
-            if (!wait_warp(bar(C::SF0 + slot), phase, ctl, SITE_SCORES)) { ok = false; break; }
-            tc_fence_after();
-            const uint32_t s_at = tmem + lane_base + slot * 128;
-            const bool cut = (j + 1) * ATTN_KEYS > first_seen;
-            const int lim = cut ? seen - j * ATTN_KEYS : ATTN_KEYS;
-            // Half the row's scores at a time: all 128 at once leave the CTA's
-            // registers short.
-            auto half = [&](int h, uint32_t *s) {
-                tmem_ld_row32(s_at + h, s);
-                tmem_ld_row32(s_at + h + 32, s + 32);
-                tmem_ld_wait();
-                if (cut) {
-#pragma unroll
-                    for (int i = 0; i < 64; ++i)
-                        if (h + i >= lim) s[i] = 0xff800000u;
-                }
-            };
-            auto largest = [&](const uint32_t *s) -> float {
-                float mx[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    mx[i] = max3(__uint_as_float(s[3 * i]), __uint_as_float(s[3 * i + 1]), __uint_as_float(s[3 * i + 2]));
-#pragma unroll
-                for (int i = 12; i < 64; i += 2)
-                    mx[(i >> 1) & 3] = max3(mx[(i >> 1) & 3], __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
-                return max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
-            };
-            uint32_t s[64], y[32];
-            auto exponentials = [&]() -> float {
-                const uint64_t rr = pair2(-r, -r);
-                uint64_t sum[2] = {0, 0};
-#pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    float a, b;
-                    unpair2(fma_pair(pair2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), cc, rr), a, b);
-                    a = exp2_approx(a);
-                    b = exp2_approx(b);
-                    sum[i & 1] = add_pair(sum[i & 1], pair2(a, b));
-                    y[i] = pack_half2<KD>(a, b);
-                }
-                float a, b;
-                unpair2(add_pair(sum[0], sum[1]), a, b);
-                return a + b;
-            };
-            // A reference that is not below `top`, and what was summed by the old one.
-            auto raise = [&](float top) {
-                const float to = fmaxf(r, top), f = exp2_approx(r - to);
-                r = to;
-                l *= f;
-#pragma unroll 1
-                for (int i = 0; i < DT; i += 32) {
-                    uint32_t o[32];
-                    tmem_ld_row32(o_at + i, o);
+        uint32_t g = 0, o_used = 0;  // blocks of this tile so far; pieces with any
+        int ring = 0;                // ring items of the pieces so far
+        for (int step = 0; ok; ++step) {
+            ok = wait_warp(bar(C::WF0 + (step & 1)), (uint32_t)(step >> 1) & 1, ctl, SITE_SCHED);
+            if (!ok) break;
+            const AttnWork w = read_work(step);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(C::WE0 + (step & 1)));
+            if (w.head < 0) break;
+            const AttnBlocks<NQ> b(p, w);
+            const int head = w.head, jb = b.jb;
+            const int token = w.first + t * p.h.tokens + row / p.h.group;
+            const int qh = head * p.h.group + row % p.h.group;
+            const bool valid = row < p.h.tokens * p.h.group && token < w.lq;
+            const int seen = valid ? attn_seen(p.s, w, token) : 0;
+            const int first_seen = attn_seen(p.s, w, w.first + t * p.h.tokens);  // the tile's least
+            const int end = NQ == 2 && t ? b.je[NQ - 1] : b.je[0];
+            float r = 0.0f, l = 0.0f;
+            for (int j = jb; j < end; ++j) {
+                const int n = j - jb;
+                const int slot = NQ == 2 ? t : (int)((g + n) & 1);
+                const uint32_t phase = NQ == 2 ? (g + n) & 1 : ((g + n) >> 1) & 1;
+                if (!wait_warp(bar(C::SF0 + slot), phase, ctl, SITE_SCORES)) { ok = false; break; }
+                tc_fence_after();
+                const uint32_t s_at = tmem + lane_base + slot * 128;
+                const bool cut = (j + 1) * ATTN_KEYS > first_seen;
+                const int lim = cut ? seen - j * ATTN_KEYS : ATTN_KEYS;
+                // Half the row's scores at a time: all 128 at once leave the CTA's
+                // registers short.
+                auto half = [&](int h, uint32_t *s) {
+                    tmem_ld_row32(s_at + h, s);
+                    tmem_ld_row32(s_at + h + 32, s + 32);
                     tmem_ld_wait();
+                    if (cut) {
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                    tmem_st_32x32b_x32(o_at + i, o);
-                }
-            };
-            auto put = [&](int h, uint32_t arrived) {
-                tmem_st_32x32b_x32(tmem + lane_base + C::P_COL + slot * C::P_STEP + h / 2, y);
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(arrived + slot));
-            };
-            if (n == 0) {
-                half(64, s);
-                const float mx = largest(s);
-                half(0, s);
-                const float top = fmaxf(mx, largest(s));
-                r = top == -INFINITY ? 0.0f : top * c;
-            } else {
-                half(0, s);
-            }
-            float sum = exponentials();
-            if (n > 0 && __any_sync(0xffffffffu, sum > LIMIT)) {
-                // (P over S: the first half is not stored before this is known.)
-                if (NQ == 1 && !wait_warp(bar(C::PVD), (n - 1) & 1, ctl, SITE_ACC_FULL)) { ok = false; break; }
-                tc_fence_after();
-                half(64, s);
-                const float mx = largest(s);
-                half(0, s);
-                raise(fmaxf(mx, largest(s)) * c);
-                sum = exponentials();
-            }
-            // Values behind the sequence's end: zero (see attn_zero_row).  (The barrier is
-            // at most one phase behind: the thread that issued these scores has waited
-            // for the slot's earlier items.)
-            if (w.lk - j * ATTN_KEYS < ATTN_KEYS) {
-                const int it = 2 * n + 1;
-                if (!wait_warp(bar(C::FULL0 + it % S), (uint32_t)(it / S) & 1, ctl, SITE_FULL)) { ok = false; break; }
-                if (row >= w.lk - j * ATTN_KEYS) {
-                    attn_zero_row<C::HALVES>(smem + C::KV_OFF + (it % S) * C::TILE_BYTES, row);
-                    fence_proxy_async_smem();
-                }
-            }
-            put(0, C::PH0);
-            l += sum;
-            half(64, s);
-            sum = exponentials();
-            if (n > 0 && __any_sync(0xffffffffu, sum > LIMIT)) {
-                // (The first half's product is under way by the old reference.)
-                if (!wait_warp(bar(C::PVA0 + t), n & 1, ctl, SITE_ACC_FULL)) { ok = false; break; }
-                tc_fence_after();
-                raise(largest(s) * c);
-                sum = exponentials();
-            }
-            put(64, C::PR0);
-            l += sum;
-        }
-        const bool some = end > jb;
-        if (ok && some) {
-            ok = wait_warp(bar(C::OD0 + t), 0, ctl, SITE_ACC_FULL);
-            tc_fence_after();
-        }
-        if (ok) {
-            const int64_t at = (int64_t)qh * p.s.q_rows + w.q0 + token;
-            if (p.splits > 1) {
-                const int64_t slot = (int64_t)split * p.h.heads * p.s.q_rows + at;
-                if (valid) p.part_ml[slot] = make_float2(r, l);
-                float4 *dst = reinterpret_cast<float4 *>(p.part_o + slot * p.h.dim);
-                if (some) {
+                        for (int i = 0; i < 64; ++i)
+                            if (h + i >= lim) s[i] = 0xff800000u;
+                    }
+                };
+                auto largest = [&](const uint32_t *s) -> float {
+                    float mx[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        mx[i] = max3(__uint_as_float(s[3 * i]), __uint_as_float(s[3 * i + 1]), __uint_as_float(s[3 * i + 2]));
+#pragma unroll
+                    for (int i = 12; i < 64; i += 2)
+                        mx[(i >> 1) & 3] = max3(mx[(i >> 1) & 3], __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
+                    return max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
+                };
+                uint32_t s[64], y[32];
+                auto exponentials = [&]() -> float {
+                    const uint64_t rr = pair2(-r, -r);
+                    uint64_t sum[2] = {0, 0};
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        float a, b;
+                        unpair2(fma_pair(pair2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), cc, rr), a, b);
+                        a = exp2_approx(a);
+                        b = exp2_approx(b);
+                        sum[i & 1] = add_pair(sum[i & 1], pair2(a, b));
+                        y[i] = pack_half2<KD>(a, b);
+                    }
+                    float a, b;
+                    unpair2(add_pair(sum[0], sum[1]), a, b);
+                    return a + b;
+                };
+                // A reference that is not below `top`, and what was summed by the old one.
+                auto raise = [&](float top) {
+                    const float to = fmaxf(r, top), f = exp2_approx(r - to);
+                    r = to;
+                    l *= f;
 #pragma unroll 1
                     for (int i = 0; i < DT; i += 32) {
                         uint32_t o[32];
                         tmem_ld_row32(o_at + i, o);
                         tmem_ld_wait();
-                        if (valid && l != 0.0f) {
 #pragma unroll
-                            for (int e = 0; e < 32; e += 4)
-                                if (i + e < p.h.dim)
-                                    dst[(i + e) >> 2] = make_float4(
-                                        __uint_as_float(o[e]), __uint_as_float(o[e + 1]),
-                                        __uint_as_float(o[e + 2]), __uint_as_float(o[e + 3]));
-                        }
+                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                        tmem_st_32x32b_x32(o_at + i, o);
+                    }
+                };
+                auto put = [&](int h, uint32_t arrived) {
+                    tmem_st_32x32b_x32(tmem + lane_base + C::P_COL + slot * C::P_STEP + h / 2, y);
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(arrived + slot));
+                };
+                if (n == 0) {
+                    half(64, s);
+                    const float mx = largest(s);
+                    half(0, s);
+                    const float top = fmaxf(mx, largest(s));
+                    r = top == -INFINITY ? 0.0f : top * c;
+                } else {
+                    half(0, s);
+                }
+                float sum = exponentials();
+                if (n > 0 && __any_sync(0xffffffffu, sum > LIMIT)) {
+                    // (P over S: the first half is not stored before this is known.)
+                    if (NQ == 1 && !wait_warp(bar(C::PVD), (g + n - 1) & 1, ctl, SITE_ACC_FULL)) { ok = false; break; }
+                    tc_fence_after();
+                    half(64, s);
+                    const float mx = largest(s);
+                    half(0, s);
+                    raise(fmaxf(mx, largest(s)) * c);
+                    sum = exponentials();
+                }
+                // Values behind the sequence's end: zero (see attn_zero_row).  (The barrier is
+                // at most one phase behind: the thread that issued these scores has waited
+                // for the slot's earlier items.)
+                if (w.lk - j * ATTN_KEYS < ATTN_KEYS) {
+                    const int it = ring + 2 * n + 1;
+                    if (!wait_warp(bar(C::FULL0 + it % S), (uint32_t)(it / S) & 1, ctl, SITE_FULL)) { ok = false; break; }
+                    if (row >= w.lk - j * ATTN_KEYS) {
+                        attn_zero_row<C::HALVES>(smem + C::KV_OFF + (it % S) * C::TILE_BYTES, row);
+                        fence_proxy_async_smem();
                     }
                 }
-            } else {
-                if (valid && p.lse) p.lse[at] = l == 0.0f ? -INFINITY : (r + log2f(l)) * 0.6931471805599453f;
-                attn_store_row<KD, DT>(o_at, some && l != 0.0f, some, l == 0.0f ? 0.0f : 1.0f / l, valid, p.h.dim,
-                                       static_cast<uint16_t *>(p.o.ptr) + (w.q0 + (int64_t)token) * p.o.ld +
-                                           qh * p.o.hd);
+                put(0, C::PH0);
+                l += sum;
+                half(64, s);
+                sum = exponentials();
+                if (n > 0 && __any_sync(0xffffffffu, sum > LIMIT)) {
+                    // (The first half's product is under way by the old reference.)
+                    if (!wait_warp(bar(C::PVA0 + t), (g + n) & 1, ctl, SITE_ACC_FULL)) { ok = false; break; }
+                    tc_fence_after();
+                    raise(largest(s) * c);
+                    sum = exponentials();
+                }
+                put(64, C::PR0);
+                l += sum;
             }
+            const bool some = end > jb;
+            if (ok && some) {
+                ok = wait_warp(bar(C::OD0 + t), o_used & 1, ctl, SITE_ACC_FULL);
+                tc_fence_after();
+            }
+            if (!ok) break;
+            {
+                const int64_t at = (int64_t)qh * p.s.q_rows + w.q0 + token;
+                if (p.splits > 1) {
+                    const int64_t slot = (int64_t)w.split * p.h.heads * p.s.q_rows + at;
+                    if (valid) p.part_ml[slot] = make_float2(r, l);
+                    float4 *dst = reinterpret_cast<float4 *>(p.part_o + slot * p.h.dim);
+                    if (some) {
+#pragma unroll 1
+                        for (int i = 0; i < DT; i += 32) {
+                            uint32_t o[32];
+                            tmem_ld_row32(o_at + i, o);
+                            tmem_ld_wait();
+                            if (valid && l != 0.0f) {
+#pragma unroll
+                                for (int e = 0; e < 32; e += 4)
+                                    if (i + e < p.h.dim)
+                                        dst[(i + e) >> 2] = make_float4(
+                                            __uint_as_float(o[e]), __uint_as_float(o[e + 1]),
+                                            __uint_as_float(o[e + 2]), __uint_as_float(o[e + 3]));
+                            }
+                        }
+                    }
+                } else {
+                    if (valid && p.lse) p.lse[at] = l == 0.0f ? -INFINITY : (r + log2f(l)) * 0.6931471805599453f;
+                    attn_store_row<KD, DT>(o_at, some && l != 0.0f, some, l == 0.0f ? 0.0f : 1.0f / l, valid, p.h.dim,
+                                           static_cast<uint16_t *>(p.o.ptr) + (w.q0 + (int64_t)token) * p.o.ld +
+                                               qh * p.o.hd);
+                }
+            }
+            if (some) {
+                // (the next piece may use O)
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(C::OE0 + t));
+                g += end - jb;
+                ++o_used;
+            }
+            ring += 2 * b.all;
         }
     }
 
     tc_fence_before();
     __syncthreads();
+    if (*abort_flag && warp == C::LOAD_WARP && lane == 0) {
+        // What was asked for lands before the CTA exits.
+        if (asked) wait_phase_drain(bar(C::NEXT), (uint32_t)(asked - 1) & 1, ctl);
+        if (tiles_q) wait_phase_drain(bar(C::QF), (uint32_t)(tiles_q - 1) & 1, ctl);
+        for (int i = loads > S ? loads - S : 0; i < loads; ++i)
+            wait_phase_drain(bar(C::FULL0 + i % S), (uint32_t)(i / S) & 1, ctl);
+    }
     if (warp == C::MMA_WARP) {
         tc_fence_after();
         tmem_dealloc(tmem, C::TMEM_COLS);
