@@ -184,7 +184,9 @@ _lock = threading.Lock()
 _lib = None
 _call = None  # the hot calls without ctypes (csrc/tg_pycall.c), when built
 _CALLS = ("tg_linear_workspace_bytes", "tg_linear", "tg_gated_workspace_bytes", "tg_gated",
-          "tg_layer_norm", "tg_layer_norm_backward_workspace_bytes", "tg_layer_norm_backward")
+          "tg_layer_norm", "tg_layer_norm_backward_workspace_bytes", "tg_layer_norm_backward",
+          "tg_rotary", "tg_rotary_backward", "tg_attention_workspace_bytes", "tg_attention",
+          "tg_attention_backward_workspace_bytes", "tg_attention_backward")
 
 
 def _load_calls(lib):
@@ -642,6 +644,9 @@ def tg_rotary(tokens, heads, dim, rot, X, ldx, hx, Y, ldy, hy, y_rows, positions
               amplitude, dtype, stream=None) -> int:
     """Rotary positions on the first rot values of each head (rows of Y by `rows` when given);
     positions and rows may be None; layout a name of ROTARY_LAYOUTS, dtype of OUT_CODES."""
+    if _call is not None:
+        return _call.tg_rotary(tokens, heads, dim, rot, X, ldx, hx, Y, ldy, hy, y_rows, positions, rows,
+                               steps, _rotary_layout(layout), amplitude, dtype, stream)
     return load().tg_rotary(tokens, heads, dim, rot, _ptr(X), ldx, hx, _ptr(Y), ldy, hy, y_rows,
                             _ptr(positions), _ptr(rows), _ptr(steps), _rotary_layout(layout),
                             amplitude, _out(dtype), _stream(stream))
@@ -650,12 +655,18 @@ def tg_rotary(tokens, heads, dim, rot, X, ldx, hx, Y, ldy, hy, y_rows, positions
 def tg_rotary_backward(tokens, heads, dim, rot, dY, lddy, hdy, dX, lddx, hdx, positions, steps, layout,
                        amplitude, dtype, stream=None) -> int:
     """The transposed map, from dY to dX (which may be dY)."""
+    if _call is not None:
+        return _call.tg_rotary_backward(tokens, heads, dim, rot, dY, lddy, hdy, dX, lddx, hdx, positions,
+                                        steps, _rotary_layout(layout), amplitude, dtype, stream)
     return load().tg_rotary_backward(tokens, heads, dim, rot, _ptr(dY), lddy, hdy, _ptr(dX), lddx, hdx,
                                      _ptr(positions), _ptr(steps), _rotary_layout(layout), amplitude,
                                      _out(dtype), _stream(stream))
 
 
 def tg_attention_workspace_bytes(seqs, q_rows, k_rows, heads, kv_heads, dim, max_q, max_k, dtype) -> int:
+    if _call is not None:
+        return _call.tg_attention_workspace_bytes(seqs, q_rows, k_rows, heads, kv_heads, dim, max_q, max_k,
+                                                  dtype)
     return load().tg_attention_workspace_bytes(seqs, q_rows, k_rows, heads, kv_heads, dim, max_q, max_k,
                                                _dtype(dtype))
 
@@ -665,6 +676,10 @@ def tg_attention(seqs, q_rows, k_rows, heads, kv_heads, dim, Q, ldq, hq, K, ldk,
                  dtype, workspace=None, stream=None) -> int:
     """O = softmax(scale Q K^T) V over packed sequences, and the rows' LSE; the lengths and LSE may be
     None."""
+    if _call is not None:
+        return _call.tg_attention(seqs, q_rows, k_rows, heads, kv_heads, dim, Q, ldq, hq, K, ldk, hk, V, ldv,
+                                  hv, q_starts, q_lengths, k_starts, k_lengths, max_q, max_k, causal, scale,
+                                  O, ldo, ho, LSE, dtype, workspace, stream)
     ws, n = _space(workspace)
     return load().tg_attention(seqs, q_rows, k_rows, heads, kv_heads, dim, _ptr(Q), ldq, hq, _ptr(K),
                                ldk, hk, _ptr(V), ldv, hv, _ptr(q_starts), _ptr(q_lengths),
@@ -674,6 +689,9 @@ def tg_attention(seqs, q_rows, k_rows, heads, kv_heads, dim, Q, ldq, hq, K, ldk,
 
 def tg_attention_backward_workspace_bytes(seqs, q_rows, k_rows, heads, kv_heads, dim, max_q, max_k,
                                           dtype) -> int:
+    if _call is not None:
+        return _call.tg_attention_backward_workspace_bytes(seqs, q_rows, k_rows, heads, kv_heads, dim,
+                                                           max_q, max_k, dtype)
     return load().tg_attention_backward_workspace_bytes(seqs, q_rows, k_rows, heads, kv_heads, dim, max_q,
                                                         max_k, _dtype(dtype))
 
@@ -683,6 +701,11 @@ def tg_attention_backward(seqs, q_rows, k_rows, heads, kv_heads, dim, Q, ldq, hq
                           max_q, max_k, causal, scale, dQ, lddq, hdq, dK, lddk, hdk, dV, lddv, hdv, dtype,
                           workspace=None, stream=None) -> int:
     """dQ, dK and dV (each may be None) of tg_attention, from dO, O and LSE."""
+    if _call is not None:
+        return _call.tg_attention_backward(
+            seqs, q_rows, k_rows, heads, kv_heads, dim, Q, ldq, hq, K, ldk, hk, V, ldv, hv, O, ldo, ho, dO,
+            lddo, hdo, LSE, q_starts, q_lengths, k_starts, k_lengths, max_q, max_k, causal, scale, dQ, lddq,
+            hdq, dK, lddk, hdk, dV, lddv, hdv, dtype, workspace, stream)
     ws, n = _space(workspace)
     return load().tg_attention_backward(
         seqs, q_rows, k_rows, heads, kv_heads, dim, _ptr(Q), ldq, hq, _ptr(K), ldk, hk, _ptr(V), ldv, hv,

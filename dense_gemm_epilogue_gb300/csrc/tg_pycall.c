@@ -1,4 +1,4 @@
-/* The feed-forward operators' Python calls without ctypes: the same argument
+/* The feed-forward and attention operators' Python calls without ctypes: the same argument
  * marshalling as __init__.py's ctypes wrappers (integers, objects with
  * data_ptr(), None; streams as integers or objects with cuda_stream; names of
  * types and activations), at about 0.7 us a call instead of 3.3.  Nothing of
@@ -31,6 +31,29 @@ static tg_status (*f_norm_back)(int64_t, int64_t, const void *, int64_t, const v
                                 const float *, const float *, const float *, void *, int64_t, float *,
                                 float *, tg_out_dtype, void *, int64_t, void *);
 
+static tg_status (*f_rotary)(int64_t, int64_t, int64_t, int64_t, const void *, int64_t, int64_t, void *,
+                             int64_t, int64_t, int64_t, const int64_t *, const int64_t *,
+                             const uint64_t *, tg_rotary_layout, float, tg_out_dtype, void *);
+static tg_status (*f_rotary_back)(int64_t, int64_t, int64_t, int64_t, const void *, int64_t, int64_t,
+                                  void *, int64_t, int64_t, const int64_t *, const uint64_t *,
+                                  tg_rotary_layout, float, tg_out_dtype, void *);
+static int64_t (*f_attn_ws)(int64_t, int64_t, int64_t, int64_t, int64_t, int64_t, int64_t, int64_t,
+                            tg_dtype);
+static tg_status (*f_attn)(int64_t, int64_t, int64_t, int64_t, int64_t, int64_t, const void *, int64_t,
+                           int64_t, const void *, int64_t, int64_t, const void *, int64_t, int64_t,
+                           const int64_t *, const int64_t *, const int64_t *, const int64_t *, int64_t,
+                           int64_t, int32_t, float, void *, int64_t, int64_t, float *, tg_dtype, void *,
+                           int64_t, void *);
+static int64_t (*f_attn_back_ws)(int64_t, int64_t, int64_t, int64_t, int64_t, int64_t, int64_t, int64_t,
+                                 tg_dtype);
+static tg_status (*f_attn_back)(int64_t, int64_t, int64_t, int64_t, int64_t, int64_t, const void *,
+                                int64_t, int64_t, const void *, int64_t, int64_t, const void *, int64_t,
+                                int64_t, const void *, int64_t, int64_t, const void *, int64_t, int64_t,
+                                const float *, const int64_t *, const int64_t *, const int64_t *,
+                                const int64_t *, int64_t, int64_t, int32_t, float, void *, int64_t,
+                                int64_t, void *, int64_t, int64_t, void *, int64_t, int64_t, tg_dtype,
+                                void *, int64_t, void *);
+
 static const struct {
     const char *name;
     void *slot;
@@ -39,6 +62,10 @@ static const struct {
     {"tg_gated_workspace_bytes", &f_gated_ws},   {"tg_gated", &f_gated},
     {"tg_layer_norm", &f_norm},                  {"tg_layer_norm_backward_workspace_bytes", &f_norm_back_ws},
     {"tg_layer_norm_backward", &f_norm_back},
+    {"tg_rotary", &f_rotary},                    {"tg_rotary_backward", &f_rotary_back},
+    {"tg_attention_workspace_bytes", &f_attn_ws}, {"tg_attention", &f_attn},
+    {"tg_attention_backward_workspace_bytes", &f_attn_back_ws},
+    {"tg_attention_backward", &f_attn_back},
 };
 #define N_ENTRIES (sizeof(ENTRIES) / sizeof(ENTRIES[0]))
 
@@ -277,6 +304,123 @@ static PyObject *py_norm_back(PyObject *self, PyObject *const *a, Py_ssize_t n) 
     RUN(f_norm_back(m, nn, dy, lddy, x, ldx, gamma, mean, rstd, dx, lddx, dgamma, dbeta, t, ws, bytes, st))
 }
 
+static float as_float(PyObject *o, int *ok) {
+    double v;
+    if (!*ok) return 0.0f;
+    v = PyFloat_AsDouble(o);
+    if (v == -1.0 && PyErr_Occurred()) *ok = 0;
+    return (float)v;
+}
+#define FLT(o) as_float(o, &ok)
+
+static PyObject *py_rotary(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+    TAKE(18, "tg_rotary")
+    const int64_t tokens = INT(a[0]), heads = INT(a[1]), dim = INT(a[2]), rot = INT(a[3]);
+    const void *x = PTR(a[4]);
+    const int64_t ldx = INT(a[5]), hx = INT(a[6]);
+    void *y = PTR(a[7]);
+    const int64_t ldy = INT(a[8]), hy = INT(a[9]), rows = INT(a[10]);
+    const int64_t *pos = PTR(a[11]), *to = PTR(a[12]);
+    const uint64_t *steps = PTR(a[13]);
+    const int layout = (int)INT(a[14]);
+    const float amp = FLT(a[15]);
+    const tg_out_dtype t = OUT(a[16]);
+    void *st = as_stream(a[17], &ok);
+    RUN(f_rotary(tokens, heads, dim, rot, x, ldx, hx, y, ldy, hy, rows, pos, to, steps,
+                 (tg_rotary_layout)layout, amp, t, st))
+}
+
+static PyObject *py_rotary_back(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+    TAKE(16, "tg_rotary_backward")
+    const int64_t tokens = INT(a[0]), heads = INT(a[1]), dim = INT(a[2]), rot = INT(a[3]);
+    const void *dy = PTR(a[4]);
+    const int64_t lddy = INT(a[5]), hdy = INT(a[6]);
+    void *dx = PTR(a[7]);
+    const int64_t lddx = INT(a[8]), hdx = INT(a[9]);
+    const int64_t *pos = PTR(a[10]);
+    const uint64_t *steps = PTR(a[11]);
+    const int layout = (int)INT(a[12]);
+    const float amp = FLT(a[13]);
+    const tg_out_dtype t = OUT(a[14]);
+    void *st = as_stream(a[15], &ok);
+    RUN(f_rotary_back(tokens, heads, dim, rot, dy, lddy, hdy, dx, lddx, hdx, pos, steps,
+                      (tg_rotary_layout)layout, amp, t, st))
+}
+
+/* The sizes that the attention calls and queries begin with. */
+#define SIZES                                                                                     \
+    const int64_t seqs = INT(a[0]), q_rows = INT(a[1]), k_rows = INT(a[2]), heads = INT(a[3]),     \
+                  kv = INT(a[4]), dim = INT(a[5]);
+
+static PyObject *attn_ws(int64_t (*f)(int64_t, int64_t, int64_t, int64_t, int64_t, int64_t, int64_t,
+                                      int64_t, tg_dtype),
+                         PyObject *const *a, Py_ssize_t n) {
+    TAKE(9, "tg_attention_workspace_bytes")
+    SIZES
+    const int64_t max_q = INT(a[6]), max_k = INT(a[7]);
+    const tg_dtype t = DTYPE(a[8]);
+    return ok ? PyLong_FromLongLong(f(seqs, q_rows, k_rows, heads, kv, dim, max_q, max_k, t)) : NULL;
+}
+static PyObject *py_attn_ws(PyObject *self, PyObject *const *a, Py_ssize_t n) { return attn_ws(f_attn_ws, a, n); }
+static PyObject *py_attn_back_ws(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+    return attn_ws(f_attn_back_ws, a, n);
+}
+
+static PyObject *py_attn(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+    TAKE(30, "tg_attention")
+    int64_t bytes;
+    SIZES
+    const void *q = PTR(a[6]);
+    const int64_t ldq = INT(a[7]), hq = INT(a[8]);
+    const void *k = PTR(a[9]);
+    const int64_t ldk = INT(a[10]), hk = INT(a[11]);
+    const void *v = PTR(a[12]);
+    const int64_t ldv = INT(a[13]), hv = INT(a[14]);
+    const int64_t *qs = PTR(a[15]), *ql = PTR(a[16]), *ks = PTR(a[17]), *kl = PTR(a[18]);
+    const int64_t max_q = INT(a[19]), max_k = INT(a[20]);
+    const int32_t causal = (int32_t)INT(a[21]);
+    const float scale = FLT(a[22]);
+    void *o = PTR(a[23]);
+    const int64_t ldo = INT(a[24]), ho = INT(a[25]);
+    float *lse = PTR(a[26]);
+    const tg_dtype t = DTYPE(a[27]);
+    void *ws = as_space(a[28], &bytes, &ok);
+    void *st = as_stream(a[29], &ok);
+    RUN(f_attn(seqs, q_rows, k_rows, heads, kv, dim, q, ldq, hq, k, ldk, hk, v, ldv, hv, qs, ql, ks, kl,
+               max_q, max_k, causal, scale, o, ldo, ho, lse, t, ws, bytes, st))
+}
+
+static PyObject *py_attn_back(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+    TAKE(42, "tg_attention_backward")
+    int64_t bytes;
+    SIZES
+    const void *in[5];
+    void *out[3];
+    int64_t ld[8], hd[8];
+    for (int i = 0; i < 5; ++i) {
+        in[i] = PTR(a[6 + 3 * i]);
+        ld[i] = INT(a[7 + 3 * i]);
+        hd[i] = INT(a[8 + 3 * i]);
+    }
+    const float *lse = PTR(a[21]);
+    const int64_t *qs = PTR(a[22]), *ql = PTR(a[23]), *ks = PTR(a[24]), *kl = PTR(a[25]);
+    const int64_t max_q = INT(a[26]), max_k = INT(a[27]);
+    const int32_t causal = (int32_t)INT(a[28]);
+    const float scale = FLT(a[29]);
+    for (int i = 0; i < 3; ++i) {
+        out[i] = PTR(a[30 + 3 * i]);
+        ld[5 + i] = INT(a[31 + 3 * i]);
+        hd[5 + i] = INT(a[32 + 3 * i]);
+    }
+    const tg_dtype t = DTYPE(a[39]);
+    void *ws = as_space(a[40], &bytes, &ok);
+    void *st = as_stream(a[41], &ok);
+    RUN(f_attn_back(seqs, q_rows, k_rows, heads, kv, dim, in[0], ld[0], hd[0], in[1], ld[1], hd[1], in[2],
+                    ld[2], hd[2], in[3], ld[3], hd[3], in[4], ld[4], hd[4], lse, qs, ql, ks, kl, max_q,
+                    max_k, causal, scale, out[0], ld[5], hd[5], out[1], ld[6], hd[6], out[2], ld[7], hd[7],
+                    t, ws, bytes, st))
+}
+
 /* bind({name: address}, dtypes, acts, outs): every entry point the calls above
  * use, and the {name: code} tables of their arguments. */
 static PyObject *py_bind(PyObject *self, PyObject *const *a, Py_ssize_t n) {
@@ -319,6 +463,12 @@ static PyMethodDef METHODS[] = {
     FAST("tg_layer_norm", py_norm),
     FAST("tg_layer_norm_backward_workspace_bytes", py_norm_back_ws),
     FAST("tg_layer_norm_backward", py_norm_back),
+    FAST("tg_rotary", py_rotary),
+    FAST("tg_rotary_backward", py_rotary_back),
+    FAST("tg_attention_workspace_bytes", py_attn_ws),
+    FAST("tg_attention", py_attn),
+    FAST("tg_attention_backward_workspace_bytes", py_attn_back_ws),
+    FAST("tg_attention_backward", py_attn_back),
     {NULL, NULL, 0, NULL},
 };
 static struct PyModuleDef MODULE = {PyModuleDef_HEAD_INIT, "_tgcall", NULL, -1, METHODS,

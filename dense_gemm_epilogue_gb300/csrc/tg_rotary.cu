@@ -57,53 +57,49 @@ __device__ __forceinline__ float2 turn_cos_sin(uint64_t phase) {
 
 // An item: VW pairs in halves (two vectors) or VW / 2 pairs side by side (one
 // vector); single elements' rows: one pair.  Past the turning ones, a vector (or
-// element) that is copied.
+// element) that is copied.  In the table a token's items lie side by side, two pairs'
+// cos and sin (16 bytes) at a time, so that neighbouring threads read neighbouring
+// words (a pair after the other: four-way bank conflicts).
 template <class Ty, bool HALVES, bool VEC>
-__global__ void __launch_bounds__(ROT_THREADS) tg_rotary_kernel(const RotaryParams p) {
+__global__ void __launch_bounds__(ROT_THREADS, 4) tg_rotary_kernel(const RotaryParams p) {
     using T = typename Ty::T;
     constexpr int VW = VEC ? Ty::VW : 1;
     constexpr int PAIRS = !VEC ? 1 : HALVES ? VW : VW / 2;  // pairs of an item
-    extern __shared__ float2 table[];
+    constexpr int CHUNK = PAIRS > 1 ? 2 : 1;                // pairs side by side in the table
+    extern __shared__ __align__(16) float2 table[];
     griddep_launch();
     griddep_wait();
     const int64_t r0 = (int64_t)blockIdx.x * p.block_rows;
-    const int64_t r1 = r0 + p.block_rows < p.rows ? r0 + p.block_rows : p.rows;
+    const int rows = (int)(p.rows - r0 < p.block_rows ? p.rows - r0 : p.block_rows);
     const int64_t t0 = r0 / p.heads;
-    const int half = p.rot / 2, tokens = (int)((r1 - 1) / p.heads - t0) + 1;
-    for (int i = threadIdx.x; i < tokens * half; i += ROT_THREADS) {
-        const int t = i / half, f = i - t * half;
-        const int64_t pos = p.positions ? p.positions[t0 + t] : t0 + t;
-        float2 cs = turn_cos_sin((uint64_t)pos * p.steps[f]);
-        cs.x *= p.amplitude;
-        cs.y *= p.transpose ? -p.amplitude : p.amplitude;
-        table[i] = cs;
-    }
-    __syncthreads();
+    const int h0 = (int)(r0 - t0 * p.heads);
+    const int half = p.rot / 2;
     const int lane = threadIdx.x % p.lanes, slot = threadIdx.x / p.lanes;
     const int slots = ROT_THREADS / p.lanes;
-    if (slot >= slots) return;
-    const T *x = static_cast<const T *>(p.x);
+    const T *x = static_cast<const T *>(p.x) + t0 * p.ldx;
     T *y = static_cast<T *>(p.y);
-    for (int v = lane; v < p.per; v += p.lanes) {
+    const bool in = slot < slots;
+    bool ready = false;  // the table
+    for (int v = lane; v < p.per || !ready; v += p.lanes) {
         const bool turn = v < p.turning;
-        if (!turn && !p.copy) break;
+        const bool work = in && v < p.per && (turn || p.copy);
         // Offsets of the item's two parts within a head (a copied one: the first).
-        const int d = turn ? (HALVES ? v * VW : VEC ? v * VW : 2 * v)
-                           : p.rot + (v - p.turning) * VW;
+        const int d = turn ? (HALVES || VEC ? v * VW : 2 * v) : p.rot + (v - p.turning) * VW;
         const int d2 = HALVES ? d + half : d + 1;
-        for (int64_t r = r0 + slot; r < r1; r += ROT_UNROLL * slots) {
+        for (int i0 = slot; i0 < rows || !ready; i0 += ROT_UNROLL * slots) {
             uint4 a[ROT_UNROLL], b[ROT_UNROLL];
             T sa[ROT_UNROLL], sb[ROT_UNROLL];
             int64_t to[ROT_UNROLL];
             int tok[ROT_UNROLL];
 #pragma unroll
             for (int u = 0; u < ROT_UNROLL; ++u) {
-                const int64_t ru = r + u * slots;
+                const int i = i0 + u * slots;
                 to[u] = -1;
-                if (ru >= r1) continue;
-                const int64_t t = ru / p.heads, h = ru - t * p.heads;
-                tok[u] = (int)(t - t0);
-                const int64_t row = p.to ? p.to[t] : t;
+                tok[u] = 0;
+                if (!work || i >= rows) continue;
+                const int t = (h0 + i) / p.heads, h = h0 + i - t * p.heads;
+                tok[u] = t;
+                const int64_t row = p.to ? p.to[t0 + t] : t0 + t;
                 if (p.to && (row < 0 || row >= p.y_rows)) continue;
                 to[u] = row * p.ldy + h * p.hy;
                 const T *src = x + t * p.ldx + h * p.hx;
@@ -115,6 +111,21 @@ __global__ void __launch_bounds__(ROT_THREADS) tg_rotary_kernel(const RotaryPara
                     if (turn) sb[u] = src[d2];
                 }
             }
+            if (!ready) {
+                // (while the first values are on their way)
+                const int n = ((h0 + rows - 1) / p.heads + 1) * half;
+                for (int i = threadIdx.x; i < n; i += ROT_THREADS) {
+                    const int t = i / half, f = i - t * half;
+                    const int64_t pos = p.positions ? p.positions[t0 + t] : t0 + t;
+                    float2 cs = turn_cos_sin((uint64_t)pos * p.steps[f]);
+                    cs.x *= p.amplitude;
+                    cs.y *= p.transpose ? -p.amplitude : p.amplitude;
+                    const int item = f / PAIRS, q = f % PAIRS;
+                    table[t * half + (q / CHUNK * p.turning + item) * CHUNK + q % CHUNK] = cs;
+                }
+                __syncthreads();
+                ready = true;
+            }
 #pragma unroll
             for (int u = 0; u < ROT_UNROLL; ++u) {
                 if (to[u] < 0) continue;
@@ -124,36 +135,36 @@ __global__ void __launch_bounds__(ROT_THREADS) tg_rotary_kernel(const RotaryPara
                     else dst[d] = sa[u];
                     continue;
                 }
-                const float2 *cs = table + tok[u] * half + v * PAIRS;
+                const float2 *row = table + tok[u] * half + v * CHUNK;
                 if constexpr (!VEC) {
                     const float fa = Ty::up(sa[u]), fb = Ty::up(sb[u]);
-                    dst[d] = Ty::down(fa * cs[0].x - fb * cs[0].y);
-                    dst[d2] = Ty::down(fa * cs[0].y + fb * cs[0].x);
-                } else if constexpr (HALVES) {
+                    const float2 cs = row[0];
+                    dst[d] = Ty::down(fa * cs.x - fb * cs.y);
+                    dst[d2] = Ty::down(fa * cs.y + fb * cs.x);
+                } else {
                     float fa[VW], fb[VW];
                     row_unpack<Ty>(a[u], fa);
-                    row_unpack<Ty>(b[u], fb);
+                    if constexpr (HALVES) row_unpack<Ty>(b[u], fb);
 #pragma unroll
-                    for (int i = 0; i < VW; ++i) {
-                        const float ya = fa[i] * cs[i].x - fb[i] * cs[i].y;
-                        fb[i] = fa[i] * cs[i].y + fb[i] * cs[i].x;
-                        fa[i] = ya;
+                    for (int q = 0; q < PAIRS; q += 2) {
+                        const float4 cs = *reinterpret_cast<const float4 *>(row + q / 2 * p.turning * CHUNK);
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const float c = e ? cs.z : cs.x, s = e ? cs.w : cs.y;
+                            float &va = HALVES ? fa[q + e] : fa[(2 * (q + e)) % VW];
+                            float &vb = HALVES ? fb[q + e] : fa[(2 * (q + e) + 1) % VW];
+                            const float ya = va * c - vb * s;
+                            vb = va * s + vb * c;
+                            va = ya;
+                        }
                     }
                     row_store_vec<Ty>(dst + d, fa);
-                    row_store_vec<Ty>(dst + d2, fb);
-                } else {
-                    float f[VW];
-                    row_unpack<Ty>(a[u], f);
-#pragma unroll
-                    for (int i = 0; i < VW / 2; ++i) {
-                        const float ya = f[2 * i] * cs[i].x - f[2 * i + 1] * cs[i].y;
-                        f[2 * i + 1] = f[2 * i] * cs[i].y + f[2 * i + 1] * cs[i].x;
-                        f[2 * i] = ya;
-                    }
-                    row_store_vec<Ty>(dst + d, f);
+                    if constexpr (HALVES) row_store_vec<Ty>(dst + d2, fb);
                 }
             }
+            if (i0 + ROT_UNROLL * slots >= rows) break;
         }
+        if (v + p.lanes >= p.per) break;
     }
 }
 
