@@ -116,8 +116,10 @@ struct ForwardPlan {
 // one an SM at a time, over key ranges of `chunk` blocks; a round of a block takes
 // 2000 cycles with one tile (its chain: S, softmax, P V), 2700 with two; a CTA's start
 // and end 7000; ranges cost a second kernel and their rows' way through memory.
-// Sequences may be shorter than max_k says, so long ones are cut to 48 blocks
-// anyway, for an even load.
+// Several sequences may be of very different lengths, of which max_k says nothing, so
+// ranges are of 16 blocks at most there, for an even load (32 single tokens over 355
+// to 11800 keys: 91 us; 24 blocks 94, 48 blocks 101; one over 131072: 93 with the 74
+// ranges of two rounds of CTAs, 99 with 64 ranges of 16 blocks).
 ForwardPlan plan_forward(const Sizes &z, int sms) {
     ForwardPlan best = {};
     const int64_t tokens = ATTN_ROWS / (z.heads / z.kv_heads);
@@ -128,7 +130,8 @@ ForwardPlan plan_forward(const Sizes &z, int sms) {
         const int64_t tiles = tile_bound(z.seqs, z.q_rows, max_q, nq * tokens);
         const int64_t ctas = tiles * z.kv_heads;
         int64_t most = ctas < 2 * sms ? ceil_div(2 * sms, ctas > 0 ? ctas : 1) : 1;
-        if (most < ceil_div(blocks, 48) && max_q <= tokens) most = ceil_div(blocks, 48);
+        const bool uneven = z.seqs > 1 && max_q <= tokens;
+        if (uneven && most < ceil_div(blocks, 16)) most = ceil_div(blocks, 16);
         if (most > ceil_div(blocks, 4)) most = ceil_div(blocks, 4);
         for (int64_t s = 1; s <= most; ++s) {
             const int64_t chunk = ceil_div(blocks, s), splits = ceil_div(blocks, chunk);
@@ -136,7 +139,7 @@ ForwardPlan plan_forward(const Sizes &z, int sms) {
             const double waves = (double)ceil_div(ctas * splits, sms);
             double cycles = waves * (7000.0 + chunk * (nq == 2 ? 2700.0 : 2000.0));
             if (splits > 1) cycles += 6000.0 + 8.0 * splits * z.heads * z.q_rows * z.dim / 2500.0;
-            if (max_q <= tokens && chunk > 48) cycles *= 1.0 + (chunk - 48) / 96.0;
+            if (uneven && chunk > 16) cycles *= 1.0 + (chunk - 16) / 8.0;
             if (least >= 0.0 && cycles >= least) continue;
             least = cycles;
             best.nq = nq;
