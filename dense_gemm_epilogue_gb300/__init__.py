@@ -112,6 +112,7 @@ EXPORTED = (
     "tg_rotary_backward",
     "tg_attention_workspace_bytes",
     "tg_attention",
+    "tg_attention_plan_describe",
     "tg_attention_backward_workspace_bytes",
     "tg_attention_backward",
 )
@@ -329,6 +330,8 @@ def load(path: str | None = None) -> ctypes.CDLL:
                                               + [i64, i64, i32, f32] + [vp, i64, i64] * 3
                                               + [c, vp, i64, vp])
         lib.tg_attention_backward.restype = c
+        lib.tg_attention_plan_describe.argtypes = [i64] * 8 + [c, i32, ctypes.c_char_p, ctypes.c_size_t]
+        lib.tg_attention_plan_describe.restype = c
         lib.tg_version.argtypes = []
         lib.tg_version.restype = i32
         if path is None:
@@ -685,6 +688,16 @@ def tg_attention(seqs, q_rows, k_rows, heads, kv_heads, dim, Q, ldq, hq, K, ldk,
                                ldk, hk, _ptr(V), ldv, hv, _ptr(q_starts), _ptr(q_lengths),
                                _ptr(k_starts), _ptr(k_lengths), max_q, max_k, int(causal), scale,
                                _ptr(O), ldo, ho, _ptr(LSE), _dtype(dtype), ws, n, _stream(stream))
+
+
+def tg_attention_plan_describe(seqs, q_rows, k_rows, heads, kv_heads, dim, max_q, max_k, dtype, num_sms=0,
+                               size=256) -> str:
+    """The plan of a tg_attention call as text; raises TgError on invalid arguments."""
+    buf = ctypes.create_string_buffer(size)
+    check(load().tg_attention_plan_describe(seqs, q_rows, k_rows, heads, kv_heads, dim, max_q, max_k,
+                                            _dtype(dtype), num_sms, buf, size),
+          "tg_attention_plan_describe")
+    return buf.value.decode()
 
 
 def tg_attention_backward_workspace_bytes(seqs, q_rows, k_rows, heads, kv_heads, dim, max_q, max_k,

@@ -3,6 +3,7 @@
 #include <cuda_runtime.h>
 
 #include <cmath>
+#include <cstdio>
 #include <mutex>
 
 #include "../../include/tg_gemm.h"
@@ -47,6 +48,12 @@ bool heads_ok(const Heads &x, int64_t heads, int64_t dim) {
     if (!x.ptr || (uintptr_t)x.ptr % 16) return false;
     if (x.ld < dim || x.ld % 8 || x.ld >= ((int64_t)1 << 38)) return false;
     return heads == 1 || (x.hd >= dim && x.hd % 8 == 0 && x.hd < ((int64_t)1 << 38) / heads);
+}
+
+// An output's rows and heads may not run into each other: heads lie within a row, or
+// rows within a head.
+bool apart(const Heads &x, int64_t rows, int64_t heads, int64_t dim) {
+    return heads == 1 || rows <= 1 || x.ld >= (heads - 1) * x.hd + dim || x.hd >= (rows - 1) * x.ld + dim;
 }
 
 // Tensor map (dim, group, heads / group, rows) of the query side, a box of 64 values x
@@ -118,8 +125,8 @@ struct ForwardPlan {
 // and end 7000; ranges cost a second kernel and their rows' way through memory.
 // Several sequences may be of very different lengths, of which max_k says nothing, so
 // ranges are of 16 blocks at most there, for an even load (32 single tokens over 355
-// to 11800 keys: 91 us; 24 blocks 94, 48 blocks 101; one over 131072: 93 with the 74
-// ranges of two rounds of CTAs, 99 with 64 ranges of 16 blocks).
+// to 11800 keys: 91 us; 24 blocks 94, 48 blocks 101; one over 131072: 88.5 in one
+// round of CTAs over 54 blocks each, 99 over 16 each).
 ForwardPlan plan_forward(const Sizes &z, int sms) {
     ForwardPlan best = {};
     const int64_t tokens = ATTN_ROWS / (z.heads / z.kv_heads);
@@ -200,6 +207,31 @@ extern "C" int64_t tg_attention_workspace_bytes(int64_t seqs, int64_t q_rows, in
     return plan_forward(z, dev.sms).workspace;
 }
 
+extern "C" tg_status tg_attention_plan_describe(int64_t seqs, int64_t q_rows, int64_t k_rows, int64_t heads,
+                                                int64_t kv_heads, int64_t dim, int64_t max_q,
+                                                int64_t max_k, tg_dtype dtype, int32_t num_sms, char *buf,
+                                                size_t len) {
+    const Sizes z = {seqs, q_rows, k_rows, heads, kv_heads, dim, max_q, max_k, dtype};
+    tg_status st = sizes_ok(z);
+    if (st != TG_OK) return st;
+    if (!buf || len == 0) return TG_ERR_INVALID_VALUE;
+    if (num_sms <= 0) {
+        tg::host::Device dev;
+        st = tg::host::device(&dev);
+        if (st != TG_OK) return st;
+        num_sms = dev.sms;
+    }
+    int n;
+    if (seqs == 0 || q_rows == 0) {
+        n = std::snprintf(buf, len, "empty");
+    } else {
+        const ForwardPlan p = plan_forward(z, num_sms);
+        n = std::snprintf(buf, len, "tiles=%d ctas=%lld ranges=%lld blocks=%lld", p.nq,
+                          (long long)(p.tiles * kv_heads * p.splits), (long long)p.splits, (long long)p.chunk);
+    }
+    return n >= 0 && (size_t)n < len ? TG_OK : TG_ERR_INVALID_VALUE;
+}
+
 extern "C" tg_status tg_attention(int64_t seqs, int64_t q_rows, int64_t k_rows, int64_t heads,
                                   int64_t kv_heads, int64_t dim, const void *Q, int64_t ldq, int64_t hq,
                                   const void *K, int64_t ldk, int64_t hk, const void *V, int64_t ldv,
@@ -215,7 +247,8 @@ extern "C" tg_status tg_attention(int64_t seqs, int64_t q_rows, int64_t k_rows, 
         return TG_ERR_INVALID_VALUE;
     if (seqs == 0 || q_rows == 0) return TG_OK;
     const Heads q = {Q, ldq, hq}, k = {K, ldk, hk}, v = {V, ldv, hv}, o = {O, ldo, ho};
-    if (!heads_ok(q, heads, dim) || !heads_ok(o, heads, dim)) return TG_ERR_INVALID_VALUE;
+    if (!heads_ok(q, heads, dim) || !heads_ok(o, heads, dim) || !apart(o, q_rows, heads, dim))
+        return TG_ERR_INVALID_VALUE;
     if (k_rows > 0 && (!heads_ok(k, kv_heads, dim) || !heads_ok(v, kv_heads, dim))) return TG_ERR_INVALID_VALUE;
     if (!arrays_ok(q_starts, q_lengths, k_starts, k_lengths)) return TG_ERR_INVALID_VALUE;
     tg::host::Device dev;
@@ -277,10 +310,11 @@ extern "C" tg_status tg_attention_backward(
     const Heads q = {Q, ldq, hq}, k = {K, ldk, hk}, v = {V, ldv, hv}, o = {O, ldo, ho}, dy = {dO, lddo, hdo};
     const Heads dq = {dQ, lddq, hdq}, dk = {dK, lddk, hdk}, dv = {dV, lddv, hdv};
     if (q_rows > 0 && (!heads_ok(q, heads, dim) || !heads_ok(o, heads, dim) || !heads_ok(dy, heads, dim) || !LSE ||
-                       (dQ && !heads_ok(dq, heads, dim))))
+                       (dQ && (!heads_ok(dq, heads, dim) || !apart(dq, q_rows, heads, dim)))))
         return TG_ERR_INVALID_VALUE;
     if (k_rows > 0 && (!heads_ok(k, kv_heads, dim) || !heads_ok(v, kv_heads, dim) ||
-                       (dK && !heads_ok(dk, kv_heads, dim)) || (dV && !heads_ok(dv, kv_heads, dim))))
+                       (dK && (!heads_ok(dk, kv_heads, dim) || !apart(dk, k_rows, kv_heads, dim))) ||
+                       (dV && (!heads_ok(dv, kv_heads, dim) || !apart(dv, k_rows, kv_heads, dim)))))
         return TG_ERR_INVALID_VALUE;
     if (!arrays_ok(q_starts, q_lengths, k_starts, k_lengths)) return TG_ERR_INVALID_VALUE;
     if (q_rows == 0 && k_rows == 0) return TG_OK;

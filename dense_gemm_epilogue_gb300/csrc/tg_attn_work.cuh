@@ -49,7 +49,8 @@ __device__ __forceinline__ AttnWork attn_find(const AttnSeqs &s, int t, int per,
     // One round of loads: every lane holds a sequence's ranges, the one found passes
     // its own to all.
     const bool one = (KEYS ? s.max_k : s.max_q) <= per;  // a sequence is a tile
-    int tile = 0, before = 0;
+    // (64 bits: the arrays may say anything, and every range may be the whole tensor)
+    int64_t tile = 0, before = 0;
     for (int base = one ? t : 0; base < s.seqs; base += 32) {
         const int q = one ? t : base + lane;
         int q0 = 0, lq = 0, k0 = 0, lk = 0;
@@ -59,11 +60,11 @@ __device__ __forceinline__ AttnWork attn_find(const AttnSeqs &s, int t, int per,
         }
         int from = 0;
         if (!one) {
-            const int n = ((KEYS ? lk : lq) + per - 1) / per;
-            int sum = n;
+            const int64_t n = ((KEYS ? lk : lq) + (int64_t)per - 1) / per;
+            int64_t sum = n;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const int v = __shfl_up_sync(0xffffffffu, sum, o);
+                const int64_t v = __shfl_up_sync(0xffffffffu, sum, o);
                 if (lane >= o) sum += v;
             }
             const unsigned who = __ballot_sync(0xffffffffu, t >= before + sum - n && t < before + sum);
@@ -79,7 +80,7 @@ __device__ __forceinline__ AttnWork attn_find(const AttnSeqs &s, int t, int per,
         w.lq = __shfl_sync(0xffffffffu, lq, from);
         w.k0 = __shfl_sync(0xffffffffu, k0, from);
         w.lk = __shfl_sync(0xffffffffu, lk, from);
-        w.first = tile * per;
+        w.first = (int)(tile * per);  // (of a range that holds it: below 2^31)
         if (w.first >= (KEYS ? w.lk : w.lq)) w.seq = -1;
         break;
     }

@@ -237,6 +237,10 @@ tg_status rotary(int64_t tokens, int64_t heads, int64_t dim, int64_t rot, const 
     if (ldx >= (int64_t)1 << 38 || ldy >= (int64_t)1 << 38 ||
         (heads > 1 && (hx >= (int64_t)1 << 38 || hy >= (int64_t)1 << 38)))
         return TG_ERR_INVALID_VALUE;
+    // Y's rows and heads may not run into each other.
+    const int64_t out_rows = rows ? y_rows : tokens;
+    if (heads > 1 && out_rows > 1 && ldy < (heads - 1) * hy + dim && (double)hy < (double)(out_rows - 1) * ldy + dim)
+        return TG_ERR_INVALID_VALUE;
     if (((uintptr_t)positions | (uintptr_t)rows | (uintptr_t)steps) % 8 || (rot > 0 && !steps))
         return TG_ERR_INVALID_VALUE;
     if (heads == 1) hx = hy = 0;

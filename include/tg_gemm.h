@@ -533,7 +533,8 @@ tg_status tg_layer_norm_backward(int64_t M, int64_t N, const void *dY, int64_t l
  *
  * Layout: a tensor has rows (tokens) of `heads` heads of `dim` values; value d
  * of head h of row t is at base + t*ld + h*hd + d (elements; hd is not looked
- * at for one head).  The heads of a QKV projection's rows are addressed in
+ * at for one head); an output's heads lie within its rows (ld >= (heads - 1)*hd +
+ * dim) or its rows within its heads (hd >= (rows - 1)*ld + dim).  The heads of a QKV projection's rows are addressed in
  * place.  Packed sequences: sequence s owns the rows starts[s] to starts[s] +
  * lengths[s], or to starts[s + 1] where lengths is NULL; starts and lengths are
  * device arrays of int64 (starts has seqs + 1 entries, of which the last is
@@ -627,13 +628,27 @@ tg_status tg_attention(int64_t seqs, int64_t q_rows, int64_t k_rows, int64_t hea
                        int64_t workspace_bytes, void *stream);
 
 /*
+ * The plan of a tg_attention call as one line of text (host only when num_sms > 0;
+ * num_sms <= 0 queries the current device): "tiles=2 ctas=512 ranges=3 blocks=11":
+ * row tiles of 128 a CTA, CTAs' pieces of work, key ranges and their length in
+ * blocks of 128 keys.  Returns TG_OK; TG_ERR_INVALID_VALUE or TG_ERR_UNSUPPORTED as
+ * tg_attention for the sizes, TG_ERR_INVALID_VALUE when the text did not fit (buf
+ * then holds its NUL-terminated start).
+ */
+tg_status tg_attention_plan_describe(int64_t seqs, int64_t q_rows, int64_t k_rows, int64_t heads,
+                                     int64_t kv_heads, int64_t dim, int64_t max_q, int64_t max_k,
+                                     tg_dtype dtype, int32_t num_sms, char *buf, size_t len);
+
+/*
  * Gradients of the attention from dO, with the forward's O and LSE:
  *   P = exp(S - LSE),  dP = dO V^T,  dS = P (dP - sum over d of dO O),
  *   dV = P^T dO,  dQ = scale dS K,  dK = scale dS^T Q,
  * dK and dV summed over the query heads of a key head.  dQ, dK and dV may each
  * be NULL.  Layout, limits and alignment are tg_attention's; P and dS are rounded
  * to dtype where the products read them (in FP16, dS below 2^-25 is lost: scale
- * the loss).  Keys that no row sees, and rows without keys, get zeros; the key
+ * the loss; and |LSE| / scale has to stay below 2^31).  An infinity or a NaN in a
+ * row, key or value may reach the gradients of the 128 keys, or of the rows, that it
+ * is worked on with.  Keys that no row sees, and rows without keys, get zeros; the key
  * ranges of two sequences may not overlap.  No atomics: repeated calls agree bit
  * for bit.
  */

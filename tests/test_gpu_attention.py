@@ -97,3 +97,147 @@ def test_growing_maxima(tg):
     ramp = torch.arange(400, device="cuda").float()[:, None, None] / 16
     p.K.t.copy_(ramp.expand(400, 2, 64).to(torch.bfloat16))
     ah.check_forward(tg, p)
+
+
+def plan(tg, p):
+    text = tg.tg_attention_plan_describe(*p.sizes(), p.max_q, p.max_k, p.dtype)
+    return dict((k, int(v)) for k, v in (x.split("=") for x in text.split()))
+
+
+@pytest.mark.parametrize("dim,dtype", [(64, "bf16"), (128, "fp16")])
+@pytest.mark.parametrize("tiles,ranges", [(1, False), (1, True), (2, False), (2, True)])
+def test_every_plan(tg, tiles, ranges, dim, dtype):
+    """One and two row tiles a CTA, whole keys and ranges of them."""
+    if tiles == 1:
+        p = ah.Problem([3, 1, 2], [2000, 700, 1500] if ranges else [5, 300, 128], heads=8, kv=2, dim=dim, dtype=dtype)
+    elif ranges:
+        p = ah.Problem([300, 200], [3000, 2900], heads=16, kv=16, dim=dim, dtype=dtype)
+    else:
+        p = ah.Problem([700, 300], heads=32, kv=16, dim=dim, dtype=dtype)
+    got = plan(tg, p)
+    assert got["tiles"] == tiles and (got["ranges"] > 1) == ranges, got
+    ah.check_forward(tg, p)
+
+
+def test_outgrown_reference(tg):
+    """Sums far beyond what the first block's maximum can hold: scores that jump within
+    a block, in its first half, its second half, and in single rows, with FP16's limit
+    and with BF16's."""
+    for dtype, jump in (("fp16", 30.0), ("bf16", 30.0), ("bf16", 200.0), ("fp16", 300.0)):
+        for at in (130, 200, 255, 256, 390):
+            p = ah.Problem([3], [400], heads=2, kv=2, dim=64, dtype=dtype, causal=False, scale=1.0, sigma=0.25)
+            # key `at` scores `jump` for row 1 alone
+            p.Q.t[1, :, 0] = jump ** 0.5
+            p.K.t[:, :, 0] = 0.0
+            p.K.t[at, :, 0] = jump ** 0.5
+            ah.check_forward(tg, p, f"{dtype} jump {jump} at key {at}")
+
+
+def test_shared_keys_and_mixed_arrays(tg):
+    """Two sequences over the same keys (a common prefix), lengths for one side only."""
+    p = ah.Problem([64, 5], [200, 130], heads=4, kv=2, dim=64, k_at=[0, 0], k_rows=200)
+    p.K.before, p.V.before = p.K.buf.clone(), p.V.buf.clone()
+    ah.check_forward(tg, p)
+    q = ah.Problem([64, 5], [200, 130], heads=4, kv=2, dim=64)
+    qa, ql, ka, kl = q.dev
+    want, _ = ah.run_forward(tg, q)
+    for arrays in ((qa, ql, ka, None), (qa, None, ka, kl), (qa, ql, ka, kl)):
+        q.arrays = lambda a=arrays: a
+        got, _ = ah.run_forward(tg, q)
+        assert torch.equal(got.t, want.t)
+
+
+def test_arrays_that_point_outside(tg):
+    """Entries are cut to the tensors: nothing outside is touched, other sequences keep
+    their results."""
+    p = ah.Problem([50, 60], [50, 60], heads=2, kv=1, dim=64, q_at=[0, 50], k_at=[0, 50], q_rows=110, k_rows=110)
+    want, _ = ah.run_forward(tg, p)
+    big = 1 << 40
+    for starts, lengths in (([0, 5000], [50, 60]), ([0, -3], [50, 60]), ([0, big], [50, big]), ([0, 50], [50, -7]),
+                            ([0, -big], [50, big])):
+        dev = [torch.tensor(v, dtype=torch.int64, device="cuda") for v in (starts + [0], lengths)]
+        p.arrays = lambda d=dev: (d[0], d[1], d[0], d[1])
+        got, z = ah.run_forward(tg, p)
+        assert torch.equal(got.t[:50], want.t[:50])
+        assert bool(torch.isnan(got.t[50:]).all()) and bool(torch.isnan(z[:, 50:]).all())
+    # a length that runs past the end is cut there
+    dev = [torch.tensor(v, dtype=torch.int64, device="cuda") for v in ([0, 50, 0], [50, big])]
+    p.arrays = lambda: (dev[0], dev[1], dev[0], dev[1])
+    got, _ = ah.run_forward(tg, p)
+    assert torch.equal(got.t, want.t)
+
+
+def test_infinities_behind_a_sequence(tg):
+    """Keys and values of other sequences in the same block never matter."""
+    for bad in (float("inf"), float("-inf"), float("nan")):
+        p = ah.Problem([40, 30], [70, 90], heads=2, kv=1, dim=128, q_at=[0, 40], k_at=[0, 200], q_rows=70, k_rows=300)
+        want, _ = ah.run_forward(tg, p)
+        for x in (p.K, p.V):
+            x.t[70:200] = bad
+            x.t[290:] = bad
+        got, _ = ah.run_forward(tg, p)
+        assert torch.equal(got.t, want.t)
+
+
+def test_rows_past_32_bit_offsets(tg):
+    """A cache whose later rows lie beyond 2^31 elements."""
+    ld, rows = 1 << 21, 1100
+    buf = torch.zeros(rows * ld // 4 + 4096, 4, dtype=torch.bfloat16, device="cuda").view(-1)
+    p = ah.Problem([1, 9], [600, 500], heads=4, kv=2, dim=64, k_at=[0, 600], k_rows=rows)
+    for name, at in (("K", 0), ("V", 512)):
+        small = getattr(p, name)
+        view = torch.as_strided(buf, (rows, 2, 64), (ld, 64, 1), at)
+        view.copy_(small.t)
+
+        class Wide:
+            t, lay = view, (view, ld, 64)
+
+            @staticmethod
+            def d(x=view):
+                return x.double()
+
+        setattr(p, name, Wide)
+    ah.check_forward(tg, p)
+
+
+def test_repeats_streams_and_graphs(tg):
+    """Bitwise the same again, on two streams at once, and replayed with other lengths."""
+    cases = [ah.Problem([1] * 4, [900, 3000, 1, 2000], heads=8, kv=2, dim=128, seed=5),
+             ah.Problem([700, 300], heads=32, kv=16, dim=64, dtype="fp16", seed=6)]
+    want = [ah.run_forward(tg, p) for p in cases]
+    side = [torch.cuda.Stream() for _ in cases]
+    for _ in range(3):
+        got = []
+        for p, s in zip(cases, side):
+            s.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(s):
+                o = ah.Tensor3(p.q_rows, p.heads, p.dim, p.dtype)
+                z = torch.empty(p.heads, p.q_rows, device="cuda")
+                ws = ah.space(tg.tg_attention_workspace_bytes(*p.sizes(), p.max_q, p.max_k, p.dtype))
+                tg.check(tg.tg_attention(*p.sizes(), *p.Q.lay, *p.K.lay, *p.V.lay, *p.arrays(), p.max_q, p.max_k,
+                                         p.causal, p.scale, *o.lay, z, p.dtype, ws, s))
+                got.append((o, z, ws))
+        torch.cuda.synchronize()
+        for (o, z, _), (wo, wz) in zip(got, want):
+            assert torch.equal(o.t, wo.t) and torch.equal(z, wz)
+    # captured once, replayed after the lengths have changed on the device
+    p = ah.Problem([1] * 4, [900, 3000, 1, 2000], heads=8, kv=2, dim=128, seed=5,
+                   k_at=[0, 3000, 6000, 9000], q_at=[0, 1, 2, 3], k_rows=12000)
+    p.K.t.normal_()
+    p.V.t.normal_()
+    o = ah.Tensor3(4, 8, 128, "bf16")
+    z = torch.empty(8, 4, device="cuda")
+    ws = ah.space(tg.tg_attention_workspace_bytes(*p.sizes(), 1, 3000, "bf16"))
+    g = torch.cuda.CUDAGraph()
+    s = torch.cuda.Stream()
+    with torch.cuda.graph(g, stream=s):
+        tg.check(tg.tg_attention(*p.sizes(), *p.Q.lay, *p.K.lay, *p.V.lay, *p.arrays(), 1, 3000, True, p.scale,
+                                 *o.lay, z, "bf16", ws, s))
+    for lens in ([900, 3000, 1, 2000], [1, 2, 3000, 0], [2500, 129, 128, 127]):
+        p.dev[3].copy_(torch.tensor(lens))
+        p.k_len = lens
+        g.replay()
+        torch.cuda.synchronize()
+        want, eo, lse, el = ah.reference(p)
+        ah.check(o.t, want, eo, f"replayed with {lens}")
+        ah.check(z, lse, el, f"replayed with {lens} LSE")

@@ -126,3 +126,75 @@ def test_against_differences(tg):
         slack = float((bound["d" + n][1] * d.abs()).sum()) + 2.0 ** -11 * float(
             (bound["d" + n][0].abs() * d.abs()).sum()) + 1e-5 * abs(slope)
         assert abs(got - slope) <= slack, (n, got, slope, slack)
+
+
+def test_infinities_behind_a_sequence(tg):
+    """Rows, keys and values of other sequences in the same tile or block never matter."""
+    for bad in (float("inf"), float("nan")):
+        for heads, dim in ((2, 128), (6, 64)):
+            p = ah.Problem([40, 30], [70, 90], heads=heads, kv=2, dim=dim, q_at=[0, 100], k_at=[0, 200], q_rows=200,
+                           k_rows=400)
+            o, lse = ah.given(p)
+            want = ah.run_backward(tg, p, o, lse)
+            for x in (p.K, p.V):
+                x.t[70:200] = bad
+                x.t[290:] = bad
+            for x in (p.Q, p.dO, o):
+                x.t[40:100] = bad
+                x.t[130:] = bad
+            lse[:, 40:100] = bad
+            got = ah.run_backward(tg, p, o, lse)
+            for n in want:
+                rows = p.rows(keys=n != "dQ")
+                assert torch.equal(got[n].t[rows], want[n].t[rows]), (n, bad, dim)
+
+
+def test_repeats_streams_and_graphs(tg):
+    """No sum depends on an order: bitwise the same again, on two streams at once, and
+    replayed."""
+    cases = [ah.Problem([500, 129, 1, 300], heads=8, kv=2, dim=128, seed=5),
+             ah.Problem([700, 300], heads=16, kv=16, dim=64, dtype="fp16", seed=6)]
+    given = [ah.given(p) for p in cases]
+    want = [ah.run_backward(tg, p, *g) for p, g in zip(cases, given)]
+    side = [torch.cuda.Stream() for _ in cases]
+
+    def launch(p, o, lse, out, ws, s):
+        lay = [x for n in ("dQ", "dK", "dV") for x in out[n].lay]
+        tg.check(tg.tg_attention_backward(*p.sizes(), *p.Q.lay, *p.K.lay, *p.V.lay, *o.lay, *p.dO.lay, lse,
+                                          *p.arrays(), p.max_q, p.max_k, p.causal, p.scale, *lay, p.dtype, ws, s))
+
+    def fresh(p):
+        return {"dQ": ah.Tensor3(p.q_rows, p.heads, p.dim, p.dtype), "dK": ah.Tensor3(p.k_rows, p.kv, p.dim, p.dtype),
+                "dV": ah.Tensor3(p.k_rows, p.kv, p.dim, p.dtype)}
+
+    spaces = [ah.space(tg.tg_attention_backward_workspace_bytes(*p.sizes(), p.max_q, p.max_k, p.dtype)) for p in cases]
+    for _ in range(3):
+        got = [fresh(p) for p in cases]
+        torch.cuda.synchronize()
+        for p, g, out, ws, s in zip(cases, given, got, spaces, side):
+            launch(p, *g, out, ws, s)
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert all(torch.equal(a[n].t, b[n].t) for n in b)
+    for p, (o, lse), ws, b in zip(cases, given, spaces, want):
+        out = fresh(p)
+        graph, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+        with torch.cuda.graph(graph, stream=s):
+            launch(p, o, lse, out, ws, s)
+        for _ in range(2):
+            graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(out[n].t, b[n].t) for n in b)
+
+
+def test_workspace_is_not_overrun(tg):
+    p = ah.Problem([77, 1], heads=3, kv=1, dim=64)
+    o, lse = ah.given(p)
+    n = tg.tg_attention_backward_workspace_bytes(*p.sizes(), p.max_q, p.max_k, p.dtype)
+    guard = torch.full((n + 256,), 0x5A, dtype=torch.uint8, device="cuda")
+    out = ah.run_backward(tg, p, o, lse)
+    lay = [x for k in ("dQ", "dK", "dV") for x in out[k].lay]
+    ah.done(tg, tg.tg_attention_backward(*p.sizes(), *p.Q.lay, *p.K.lay, *p.V.lay, *o.lay, *p.dO.lay, lse,
+                                         *p.arrays(), p.max_q, p.max_k, p.causal, p.scale, *lay, p.dtype,
+                                         (guard, n), torch.cuda.current_stream()), "tg_attention_backward")
+    assert bool((guard[n:] == 0x5A).all())
