@@ -159,6 +159,53 @@ ForwardPlan plan_forward(const Sizes &z, int sms) {
     return best;
 }
 
+struct BackwardPlan {
+    int64_t tiles, blocks;  // row tiles and key blocks of all sequences, at most
+    int64_t key_parts, key_tiles, row_parts, row_blocks;
+    int64_t delta, part_keys, part_rows;  // workspace bytes, in this order
+    int64_t workspace() const { return delta + part_keys + part_rows; }
+};
+
+// The longest sequence's key block sees all its row tiles, and a CTA takes them one
+// after the other.  Where that is much longer than the whole work shared by all SMs
+// (few key heads, one long sequence among short ones) the tiles are cut into parts for
+// as many CTAs, and likewise a row tile's key blocks; another kernel adds the parts'
+// FP32 sums in order, at about 18000 cycles with what the parts write.  (Cycles a tile:
+// 128-wide heads 2700 for keys, 1700 for rows; 64-wide 2000 and 1100.  309 rows of 3
+// heads over 258 keys, 8 tiles: 22 us whole, 25 in two parts.)
+BackwardPlan plan_backward(const Sizes &z, int sms) {
+    BackwardPlan p = {};
+    const int64_t group = z.heads / z.kv_heads, tokens = ATTN_ROWS / group;
+    const int64_t max_q = bound_of(z.max_q, z.q_rows), max_k = bound_of(z.max_k, z.k_rows);
+    p.tiles = z.q_rows ? tile_bound(z.seqs, z.q_rows, max_q, tokens) : 0;
+    p.blocks = z.k_rows ? tile_bound(z.seqs, z.k_rows, max_k, ATTN_KEYS) : 0;
+    p.delta = ceil_div(4 * z.heads * z.q_rows, 16) * 16;
+    const int64_t long_tiles = ceil_div(max_q, tokens), long_blocks = ceil_div(max_k, ATTN_KEYS);
+    p.key_parts = p.row_parts = 1;
+    p.key_tiles = long_tiles > 0 ? long_tiles : 1;
+    p.row_blocks = long_blocks > 0 ? long_blocks : 1;
+    const double all_tiles = (double)z.q_rows / tokens;                            // of all sequences
+    const double mean_blocks = 0.5 + (double)z.k_rows / ((double)z.seqs * ATTN_KEYS);  // of one
+    const double key_cycles = z.dim > 64 ? 2700.0 : 2000.0, row_cycles = z.dim > 64 ? 1700.0 : 1100.0;
+    const double share = all_tiles * mean_blocks * z.kv_heads * (key_cycles + row_cycles) / sms;
+    auto cut = [&](int64_t most, double cycles, int64_t &parts, int64_t &each) {
+        double least = most * cycles > share ? most * cycles : share;
+        for (int64_t n = 2; n <= 16 && n <= most; ++n) {
+            const int64_t e = ceil_div(most, n);
+            const double t = (e * cycles > share ? e * cycles : share) + 18000.0;
+            if (t >= least) continue;
+            least = t;
+            each = e;
+            parts = ceil_div(most, e);
+        }
+    };
+    cut(long_tiles, key_cycles, p.key_parts, p.key_tiles);
+    cut(long_blocks, row_cycles, p.row_parts, p.row_blocks);
+    if (p.key_parts > 1) p.part_keys = 8 * p.key_parts * z.k_rows * z.kv_heads * z.dim;
+    if (p.row_parts > 1) p.part_rows = 4 * p.row_parts * z.q_rows * z.heads * z.dim;
+    return p;
+}
+
 bool arrays_ok(const int64_t *qs, const int64_t *ql, const int64_t *ks, const int64_t *kl) {
     return qs && ks && !(((uintptr_t)qs | (uintptr_t)ql | (uintptr_t)ks | (uintptr_t)kl) % 8);
 }
@@ -290,7 +337,10 @@ extern "C" int64_t tg_attention_backward_workspace_bytes(int64_t seqs, int64_t q
                                                          int64_t max_q, int64_t max_k, tg_dtype dtype) {
     const Sizes z = {seqs, q_rows, k_rows, heads, kv_heads, dim, max_q, max_k, dtype};
     if (sizes_ok(z) != TG_OK) return -1;
-    return seqs == 0 ? 0 : 4 * heads * q_rows;  // delta
+    if (seqs == 0) return 0;
+    tg::host::Device dev;
+    if (tg::host::device(&dev) != TG_OK) return -1;
+    return plan_backward(z, dev.sms).workspace();
 }
 
 extern "C" tg_status tg_attention_backward(
@@ -318,11 +368,14 @@ extern "C" tg_status tg_attention_backward(
         return TG_ERR_INVALID_VALUE;
     if (!arrays_ok(q_starts, q_lengths, k_starts, k_lengths)) return TG_ERR_INVALID_VALUE;
     if (q_rows == 0 && k_rows == 0) return TG_OK;
-    const int64_t bytes = 4 * heads * q_rows;
-    if (bytes && (!workspace || (uintptr_t)workspace % 16 || workspace_bytes < bytes)) return TG_ERR_INVALID_VALUE;
+    if (q_rows && (!workspace || (uintptr_t)workspace % 16 || workspace_bytes < 4 * heads * q_rows))
+        return TG_ERR_INVALID_VALUE;
     tg::host::Device dev;
     st = tg::host::device(&dev);
     if (st != TG_OK) return st;
+    const BackwardPlan plan = plan_backward(z, dev.sms);
+    if (plan.workspace() && (!workspace || (uintptr_t)workspace % 16 || workspace_bytes < plan.workspace()))
+        return TG_ERR_INVALID_VALUE;
     AttnBackward a = {};
     a.s = make_seqs(z, q_starts, q_lengths, k_starts, k_lengths, causal);
     a.h = make_heads(z, scale);
@@ -341,12 +394,18 @@ extern "C" tg_status tg_attention_backward(
     a.dv = {k_rows ? dV : nullptr, lddv, kv_heads == 1 ? 0 : hdv};
     a.lse = LSE;
     a.delta = static_cast<const float *>(workspace);
-    const int64_t tiles = q_rows ? tile_bound(seqs, q_rows, a.s.max_q, a.h.tokens) : 0;
-    const int64_t blocks = k_rows ? tile_bound(seqs, k_rows, a.s.max_k, ATTN_KEYS) : 0;
-    if ((tiles + blocks) * kv_heads > INT32_MAX || q_rows * heads / 16 > INT32_MAX - 1)
+    if (plan.tiles * plan.row_parts * kv_heads + plan.blocks * plan.key_parts * kv_heads > INT32_MAX ||
+        q_rows * heads / 16 > INT32_MAX - 1)
         return TG_ERR_UNSUPPORTED;
-    a.tiles = (int32_t)tiles;
-    a.blocks = (int32_t)blocks;
+    a.tiles = (int32_t)plan.tiles;
+    a.blocks = (int32_t)plan.blocks;
+    a.key_parts = a.dk.ptr || a.dv.ptr ? (int32_t)plan.key_parts : 1;
+    a.key_tiles = (int32_t)plan.key_tiles;
+    a.row_parts = a.dq.ptr ? (int32_t)plan.row_parts : 1;
+    a.row_blocks = (int32_t)plan.row_blocks;
+    uint8_t *space = static_cast<uint8_t *>(workspace);
+    a.part_keys = reinterpret_cast<float *>(space + plan.delta);
+    a.part_rows = reinterpret_cast<float *>(space + plan.delta + plan.part_keys);
     a.status = dev.status;
     a.wait_limit_ns = dev.wait_limit_ns;
     AttnDelta d = {};

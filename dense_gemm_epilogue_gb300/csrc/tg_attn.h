@@ -68,6 +68,11 @@ struct AttnBackward {
     const float *delta;     // heads x q_rows: sum over d of dO O
     int32_t tiles, blocks;  // bounds on the row tiles and on the key blocks of all sequences
     int32_t key_ctas;       // CTAs that work on keys; the rest work on rows
+    // A key block's row tiles, and a row tile's key blocks, in so many parts of so many
+    // tiles (blocks) each, one a CTA.  With several, FP32 sums go to the workspace:
+    // (part, dV or dK, key head, key) and (part, query head, row), dim values each.
+    int32_t key_parts, key_tiles, row_parts, row_blocks;
+    float *part_keys, *part_rows;
     uint32_t *status;
     uint64_t wait_limit_ns;
 };

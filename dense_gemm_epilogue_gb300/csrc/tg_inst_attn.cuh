@@ -67,8 +67,8 @@ static cudaError_t launch_attn_backward_dim(AttnBackward a, int device, cudaStre
     static std::atomic<uint64_t> done{0};
     const cudaError_t e = attn_smem(tg_attn_backward_kernel<KD, DT>, SMEM, device, done);
     if (e != cudaSuccess) return e;
-    const int64_t keys = a.dk.ptr || a.dv.ptr ? (int64_t)a.blocks * a.h.kv_heads : 0;
-    const int64_t rows = a.dq.ptr ? (int64_t)a.tiles * a.h.kv_heads : 0;
+    const int64_t keys = a.dk.ptr || a.dv.ptr ? (int64_t)a.blocks * a.h.kv_heads * a.key_parts : 0;
+    const int64_t rows = a.dq.ptr ? (int64_t)a.tiles * a.h.kv_heads * a.row_parts : 0;
     if (keys + rows == 0) return cudaSuccess;
     a.key_ctas = (int32_t)keys;
     return attn_launch<AttnBackward>(tg_attn_backward_kernel<KD, DT>, dim3((unsigned)(keys + rows)), CK::NUM_THREADS,
@@ -83,8 +83,14 @@ static cudaError_t launch_attn_backward_kind(const AttnBackward &a, const AttnDe
         const cudaError_t e = attn_launch<AttnDelta>(tg_attn_delta_kernel<KD>, dim3((unsigned)grid), DELTA_THREADS, 0, stream, d);
         if (e != cudaSuccess) return e;
     }
-    return a.h.dim <= 64 ? launch_attn_backward_dim<KD, 64>(a, device, stream)
-                         : launch_attn_backward_dim<KD, 128>(a, device, stream);
+    const cudaError_t e = a.h.dim <= 64 ? launch_attn_backward_dim<KD, 64>(a, device, stream)
+                                        : launch_attn_backward_dim<KD, 128>(a, device, stream);
+    const int64_t keys = a.key_parts > 1 ? (int64_t)a.blocks * a.h.kv_heads : 0;
+    const int64_t rows = a.row_parts > 1 ? (int64_t)a.tiles * a.h.kv_heads : 0;
+    if (e != cudaSuccess || keys + rows == 0) return e;
+    // (four blocks to a tile: 16 to 64 rows a warp would be a long chain of loads)
+    return attn_launch<AttnBackward>(tg_attn_parts_kernel<KD>, dim3((unsigned)(keys + rows), 4), PARTS_THREADS, 0,
+                                     stream, a);
 }
 
 }  // namespace tg

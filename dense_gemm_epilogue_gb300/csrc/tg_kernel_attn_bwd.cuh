@@ -134,6 +134,37 @@ __device__ __forceinline__ void attn_store_half(uint32_t at, const float *y) {
     tmem_st_wait();
 }
 
+// COLS columns from tensor memory as FP32 to a row of which `left` values exist.
+template <int COLS>
+__device__ __forceinline__ void attn_store_part(uint32_t at, bool valid, int left, float *dst) {
+#pragma unroll 1
+    for (int i = 0; i < COLS; i += 32) {
+        uint32_t o[32];
+        tmem_ld_row32(at + i, o);
+        tmem_ld_wait();
+        if (!valid) continue;
+#pragma unroll
+        for (int e = 0; e < 32; e += 4)
+            if (i + e < left)
+                *reinterpret_cast<float4 *>(dst + i + e) =
+                    make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]), __uint_as_float(o[e + 2]),
+                                __uint_as_float(o[e + 3]));
+    }
+}
+
+// The first token that sees a key of the block, and the row tiles from there on.
+__device__ __forceinline__ int attn_key_tiles(const AttnBackward &p, const AttnWork &w, int &i0) {
+    i0 = p.s.causal ? w.first - w.lk + w.lq : 0;
+    if (i0 < 0) i0 = 0;
+    return w.seq >= 0 && i0 < w.lq ? (w.lq - i0 + p.h.tokens - 1) / p.h.tokens : 0;
+}
+// The key blocks that a row tile sees.
+__device__ __forceinline__ int attn_row_blocks(const AttnBackward &p, const AttnWork &w) {
+    const int end = w.first + p.h.tokens < w.lq ? w.first + p.h.tokens : w.lq;
+    const int seen = w.seq >= 0 ? attn_seen(p.s, w, end - 1) : 0;
+    return (seen + ATTN_KEYS - 1) / ATTN_KEYS;
+}
+
 template <Kind KD, int DT>
 __device__ __forceinline__ void attn_keys(const AttnBackward &p, const int block) {
     using C = AttnKeysConfig<KD, DT>;
@@ -193,9 +224,10 @@ __device__ __forceinline__ void attn_keys(const AttnBackward &p, const int block
     }
     griddep_launch();
     griddep_wait();
-    const int head = block % p.h.kv_heads;
+    const int part = block % p.key_parts, rest = block / p.key_parts;
+    const int head = rest % p.h.kv_heads;
     if (warp == C::LOAD_WARP) {
-        const AttnWork w = attn_find<true>(p.s, block / p.h.kv_heads, ATTN_KEYS, lane);
+        const AttnWork w = attn_find<true>(p.s, rest / p.h.kv_heads, ATTN_KEYS, lane);
         if (lane == 0) *shared_work = w;
     }
     tc_fence_before();
@@ -203,10 +235,10 @@ __device__ __forceinline__ void attn_keys(const AttnBackward &p, const int block
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     const AttnWork w = *shared_work;
-    // Tokens from i0 on see some of the keys.
-    int i0 = p.s.causal ? w.first - w.lk + w.lq : 0;
-    if (i0 < 0) i0 = 0;
-    const int tiles = w.seq >= 0 && i0 < w.lq ? (w.lq - i0 + p.h.tokens - 1) / p.h.tokens : 0;
+    int i0;  // the first token of this part
+    int tiles = attn_key_tiles(p, w, i0) - part * p.key_tiles;
+    i0 += part * p.key_tiles * p.h.tokens;
+    tiles = tiles < 0 ? 0 : tiles < p.key_tiles ? tiles : p.key_tiles;
     const int tail = (w.lq - i0 - (tiles - 1) * p.h.tokens) * p.h.group;  // rows of the last tile
     const bool fix = tiles > 0 && tail < box;
     auto q_tile = [&](int n) -> int { return C::Q_OFF + n % C::STAGES * C::TILE_BYTES; };
@@ -468,10 +500,17 @@ __device__ __forceinline__ void attn_keys(const AttnBackward &p, const int block
             tc_fence_after();
         }
         const AttnOut &out = half ? p.dk : p.dv;
-        if (ok && out.ptr)
-            attn_store_row<KD, DT>(tmem + lane_base + (half ? C::DK_COL : C::DV_COL), tiles > 0, tiles > 0,
-                                   half ? p.h.scale : 1.0f, key < w.lk, p.h.dim,
-                                   static_cast<uint16_t *>(out.ptr) + (w.k0 + (int64_t)key) * out.ld + head * out.hd);
+        const uint32_t at = tmem + lane_base + (half ? C::DK_COL : C::DV_COL);
+        if (ok && out.ptr) {
+            if (p.key_parts == 1)
+                attn_store_row<KD, DT>(at, tiles > 0, tiles > 0, half ? p.h.scale : 1.0f, key < w.lk, p.h.dim,
+                                       static_cast<uint16_t *>(out.ptr) + (w.k0 + (int64_t)key) * out.ld +
+                                           head * out.hd);
+            else if (tiles > 0)
+                attn_store_part<DT>(at, key < w.lk, p.h.dim,
+                                    p.part_keys + ((((int64_t)part * 2 + half) * p.h.kv_heads + head) * p.s.k_rows +
+                                                   w.k0 + key) * p.h.dim);
+        }
     }
 
     tc_fence_before();
@@ -543,9 +582,10 @@ __device__ __forceinline__ void attn_rows(const AttnBackward &p, const int block
     }
     griddep_launch();
     griddep_wait();
-    const int head = block % p.h.kv_heads;
+    const int part = block % p.row_parts, rest = block / p.row_parts;
+    const int head = rest % p.h.kv_heads;
     if (warp == C::LOAD_WARP) {
-        const AttnWork w = attn_find<false>(p.s, p.tiles - 1 - block / p.h.kv_heads, p.h.tokens, lane);
+        const AttnWork w = attn_find<false>(p.s, p.tiles - 1 - rest / p.h.kv_heads, p.h.tokens, lane);
         if (lane == 0) *shared_work = w;
     }
     tc_fence_before();
@@ -553,10 +593,10 @@ __device__ __forceinline__ void attn_rows(const AttnBackward &p, const int block
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     const AttnWork w = *shared_work;
-    const int end = w.first + p.h.tokens < w.lq ? w.first + p.h.tokens : w.lq;
-    const int seen_last = w.seq >= 0 ? attn_seen(p.s, w, end - 1) : 0;
-    const int blocks = (seen_last + ATTN_KEYS - 1) / ATTN_KEYS;
-    const int tail = w.lk - (blocks - 1) * ATTN_KEYS;  // keys of the sequence in the last block
+    const int b0 = part * p.row_blocks;  // the first block of this part
+    int blocks = attn_row_blocks(p, w) - b0;
+    blocks = blocks < 0 ? 0 : blocks < p.row_blocks ? blocks : p.row_blocks;
+    const int tail = w.lk - (b0 + blocks - 1) * ATTN_KEYS;  // keys of the sequence from the last block on
     const bool fix = blocks > 0 && tail < ATTN_KEYS;
     // Item 2n is block n's keys, 2n + 1 its values.
     auto slot = [&](int it) -> int { return it & 1 ? C::KS + (it >> 1) % C::VS : (it >> 1) % C::KS; };
@@ -586,7 +626,7 @@ __device__ __forceinline__ void attn_rows(const AttnBackward &p, const int block
 #pragma unroll
                 for (int h = 0; h < C::HALVES; ++h)
                     tma_load_3d(sbase + tile(it) + h * 16384, it & 1 ? &p.v : &p.k, landed(it), h * 64,
-                                head, w.k0 + (it >> 1) * ATTN_KEYS);
+                                head, w.k0 + (b0 + (it >> 1)) * ATTN_KEYS);
                 ++issued;
             }
             if (!ok) {
@@ -688,8 +728,8 @@ __device__ __forceinline__ void attn_rows(const AttnBackward &p, const int block
                 y[i] = exp2_approx(y[i]);
                 y[i + 1] = exp2_approx(y[i + 1]);
             }
-            if ((n + 1) * ATTN_KEYS > first_seen) {
-                const int lim = seen - n * ATTN_KEYS - 64 * half;
+            if ((b0 + n + 1) * ATTN_KEYS > first_seen) {
+                const int lim = seen - (b0 + n) * ATTN_KEYS - 64 * half;
 #pragma unroll
                 for (int i = 0; i < 64; ++i)
                     if (i >= lim) y[i] = 0.0f;
@@ -717,11 +757,16 @@ __device__ __forceinline__ void attn_rows(const AttnBackward &p, const int block
             ok = wait_warp(bar(C::OD), 0, ctl, SITE_ACC_FULL);
             tc_fence_after();
         }
-        if (ok)
-            attn_store_row<KD, DT / 2>(tmem + lane_base + C::DQ_COL + half * (DT / 2), blocks > 0, blocks > 0, p.h.scale, valid,
-                                       p.h.dim - half * (DT / 2),
+        const uint32_t at = tmem + lane_base + C::DQ_COL + half * (DT / 2);
+        const int left = p.h.dim - half * (DT / 2);
+        if (ok && p.row_parts == 1)
+            attn_store_row<KD, DT / 2>(at, blocks > 0, blocks > 0, p.h.scale, valid, left,
                                        static_cast<uint16_t *>(p.dq.ptr) + (w.q0 + (int64_t)token) * p.dq.ld +
                                            qh * p.dq.hd + half * (DT / 2));
+        else if (ok && blocks > 0)
+            attn_store_part<DT / 2>(at, valid, left,
+                                    p.part_rows + (((int64_t)part * p.h.heads + qh) * p.s.q_rows + w.q0 + token) *
+                                                      p.h.dim + half * (DT / 2));
     }
 
     tc_fence_before();
@@ -739,6 +784,61 @@ __global__ void __launch_bounds__(AttnBackConfig<KD, DT>::NUM_THREADS, 1)
     tg_attn_backward_kernel(const __grid_constant__ AttnBackward p) {
     if ((int)blockIdx.x < p.key_ctas) attn_keys<KD, DT>(p, blockIdx.x);
     else attn_rows<KD, DT>(p, blockIdx.x - p.key_ctas);
+}
+
+// The parts' sums, in their order: a warp a row, its lanes four values each.
+// blockIdx.x: the key blocks first (when they have parts), then the row tiles.
+constexpr int PARTS_THREADS = 256;
+template <Kind KD>
+__global__ void __launch_bounds__(PARTS_THREADS) tg_attn_parts_kernel(const __grid_constant__ AttnBackward p) {
+    griddep_launch();
+    griddep_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int key_blocks = p.key_parts > 1 ? p.blocks * p.h.kv_heads : 0;
+    const bool keys = (int)blockIdx.x < key_blocks;
+    const int block = keys ? blockIdx.x : blockIdx.x - key_blocks;
+    const int head = block % p.h.kv_heads;
+    const AttnWork w = keys ? attn_find<true>(p.s, block / p.h.kv_heads, ATTN_KEYS, lane)
+                            : attn_find<false>(p.s, block / p.h.kv_heads, p.h.tokens, lane);
+    if (w.seq < 0) return;
+    int i0, parts;
+    if (keys) parts = (attn_key_tiles(p, w, i0) + p.key_tiles - 1) / p.key_tiles;
+    else parts = (attn_row_blocks(p, w) + p.row_blocks - 1) / p.row_blocks;
+    const int rows = keys ? 2 * ATTN_KEYS : p.h.tokens * p.h.group;
+    for (int i = blockIdx.y * (PARTS_THREADS / 32) + warp; i < rows; i += gridDim.y * (PARTS_THREADS / 32)) {
+        const float *src;
+        uint16_t *dst;
+        int64_t step;
+        float f = 1.0f;
+        if (keys) {
+            const int half = i & 1, key = w.first + (i >> 1);
+            const AttnOut &out = half ? p.dk : p.dv;
+            if (key >= w.lk || !out.ptr) continue;
+            step = (int64_t)2 * p.h.kv_heads * p.s.k_rows * p.h.dim;
+            src = p.part_keys + (((int64_t)half * p.h.kv_heads + head) * p.s.k_rows + w.k0 + key) * p.h.dim;
+            dst = static_cast<uint16_t *>(out.ptr) + (w.k0 + (int64_t)key) * out.ld + head * out.hd;
+            if (half) f = p.h.scale;
+        } else {
+            const int token = w.first + i / p.h.group, qh = head * p.h.group + i % p.h.group;
+            if (token >= w.lq) break;
+            step = (int64_t)p.h.heads * p.s.q_rows * p.h.dim;
+            src = p.part_rows + ((int64_t)qh * p.s.q_rows + w.q0 + token) * p.h.dim;
+            dst = static_cast<uint16_t *>(p.dq.ptr) + (w.q0 + (int64_t)token) * p.dq.ld + qh * p.dq.hd;
+            f = p.h.scale;
+        }
+        if (4 * lane >= p.h.dim) continue;
+        float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+        for (int q = 0; q < parts; ++q) {
+            const float4 v = reinterpret_cast<const float4 *>(src + q * step)[lane];
+            a.x += v.x;
+            a.y += v.y;
+            a.z += v.z;
+            a.w += v.w;
+        }
+        *reinterpret_cast<uint2 *>(dst + 4 * lane) =
+            make_uint2(pack_half2<KD>(a.x * f, a.y * f), pack_half2<KD>(a.z * f, a.w * f));
+    }
 }
 
 }  // namespace tg

@@ -57,6 +57,23 @@ def test_packed_lengths(tg, q_len, k_len, causal):
     ah.check_backward(tg, ah.Problem(q_len, k_len, heads=3, kv=1, dim=128, causal=causal, dtype="fp16"))
 
 
+@pytest.mark.parametrize("dim,dtype", [(64, "bf16"), (128, "fp16")])
+@pytest.mark.parametrize("causal", [True, False])
+def test_work_in_parts(tg, dim, dtype, causal):
+    """One key head for many rows, and few rows over many keys: a key block's row tiles,
+    and a row tile's key blocks, shared by several CTAs (the workspace holds their sums)."""
+    for p in (ah.Problem([1500, 40, 0, 130], [300, 129, 5, 130], heads=8, kv=1, dim=dim, dtype=dtype, causal=causal),
+              ah.Problem([60, 9], [4000, 700], heads=2, kv=2, dim=dim, dtype=dtype, causal=causal),
+              ah.Problem([1300], heads=4, kv=1, dim=dim, dtype=dtype, causal=causal, scale=0.05)):
+        delta = -(-4 * p.heads * p.q_rows // 16) * 16
+        assert tg.tg_attention_backward_workspace_bytes(*p.sizes(), p.max_q, p.max_k, dtype) > delta
+        out = ah.check_backward(tg, p)
+        o, lse = ah.given(p)
+        for n in ("dQ", "dK", "dV"):  # each wanted alone
+            some = ah.run_backward(tg, p, o, lse, (n,))
+            assert torch.equal(some[n].t, out[n].t), n
+
+
 def test_many_tiles(tg):
     ah.check_backward(tg, ah.Problem([700, 129, 385, 1, 0, 1000], heads=16, kv=16, dim=64, dtype="fp16"))
     ah.check_backward(tg, ah.Problem([1111, 260], heads=16, kv=4, dim=128))
