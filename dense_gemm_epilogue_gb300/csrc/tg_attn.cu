@@ -170,9 +170,10 @@ struct BackwardPlan {
 // after the other.  Where that is much longer than the whole work shared by all SMs
 // (few key heads, one long sequence among short ones) the tiles are cut into parts for
 // as many CTAs, and likewise a row tile's key blocks; another kernel adds the parts'
-// FP32 sums in order, at about 18000 cycles with what the parts write.  (Cycles a tile:
-// 128-wide heads 2700 for keys, 1700 for rows; 64-wide 2000 and 1100.  309 rows of 3
-// heads over 258 keys, 8 tiles: 22 us whole, 25 in two parts.)
+// FP32 sums in order, at about 24000 cycles with what the parts write.  (Cycles a tile:
+// 128-wide heads 2700 for keys, 1700 for rows; 64-wide 2000 and 1100.  2048 rows of
+// 8 heads over one key head: 198 us whole, 63 in parts; 64 rows over 8192 keys 91 and
+// 57; 309 rows of 3 heads, 8 tiles, 22 whole, 25 and 28 in 2 and 8 parts.)
 BackwardPlan plan_backward(const Sizes &z, int sms) {
     BackwardPlan p = {};
     const int64_t group = z.heads / z.kv_heads, tokens = ATTN_ROWS / group;
@@ -192,7 +193,7 @@ BackwardPlan plan_backward(const Sizes &z, int sms) {
         double least = most * cycles > share ? most * cycles : share;
         for (int64_t n = 2; n <= 16 && n <= most; ++n) {
             const int64_t e = ceil_div(most, n);
-            const double t = (e * cycles > share ? e * cycles : share) + 18000.0;
+            const double t = (e * cycles > share ? e * cycles : share) + 24000.0 + 500.0 * n;
             if (t >= least) continue;
             least = t;
             each = e;
