@@ -103,7 +103,7 @@ struct AttnKeysConfig : AttnBackConfig<KD, DT> {
     // arrive in, so its two 64-wide boxes are loaded and given back one by one.
     static constexpr int STAGES = DT == 64 ? 4 : 2;
     static constexpr int QB = STAGES * B::HALVES;  // boxes of Q
-    static constexpr int ROW_SLOTS = 3;  // rows' LSE, delta (16 bytes of parts each), keys seen
+    static constexpr int ROW_SLOTS = DT == 64 ? 6 : 3;  // rows' LSE, delta (16 bytes of parts each), keys seen
     static constexpr int ROW_BYTES_ = 2048 + 2048 + 512;
     static constexpr int K_OFF = 0, V_OFF = B::TILE_BYTES, Q_OFF = 2 * B::TILE_BYTES;
     static constexpr int DY_OFF = Q_OFF + STAGES * B::TILE_BYTES;
@@ -112,15 +112,18 @@ struct AttnKeysConfig : AttnBackConfig<KD, DT> {
     static constexpr int ZERO_OFF = WEIGHTS_OFF + 2048;                    // 128 rows of 16 zero bytes
     static constexpr int BAR_OFF = ZERO_OFF + 2048;
     static constexpr int KVF = 0, QF0 = 1, QE0 = QF0 + QB, DF0 = QE0 + QB, DE0 = DF0 + STAGES,
-                         SF = DE0 + STAGES, DPF = SF + 1, PR = DPF + 1, DSR = PR + 1, RF0 = DSR + 1,
+                         SF0 = DE0 + STAGES, DPF = SF0 + 2, PR0 = DPF + 1, DSR = PR0 + 2, RF0 = DSR + 1,
                          RE0 = RF0 + ROW_SLOTS, LAST = RE0 + ROW_SLOTS, OD = LAST + 3, TURN = OD + 1, DRAIN = TURN + 2,
                          NUM_BARS = DRAIN + 2;
     static constexpr int MISC_OFF = BAR_OFF + NUM_BARS * 8;
     static constexpr int SMEM_BYTES = MISC_OFF + 64 + 1024;
-    // 128-wide heads: P over S, dS over dP (each thread over the columns it has read).
-    static constexpr int S_COL = 0, DP_COL = 128, DV_COL = 256, DK_COL = 256 + DT;
-    static constexpr int P_COL = DT == 64 ? 384 : S_COL, DS_COL = DT == 64 ? 448 : DP_COL;
-    static constexpr int P_HALF = DT == 64 ? 32 : 64;  // columns from rows 0-63 to rows 64-127
+    // P over S, dS over dP (each thread over the columns it has read).  64-wide heads
+    // leave room for S twice, a tile ahead of the warps (which may then be a tile ahead
+    // of the thread that awaits P: a barrier for each slot, of S and of P).
+    static constexpr int S_SLOTS = DT == 64 ? 2 : 1;
+    static constexpr int S_COL = 0, DP_COL = 128 * S_SLOTS, DV_COL = DP_COL + 128, DK_COL = DV_COL + DT;
+    static constexpr int P_HALF = 64;  // columns from rows 0-63 to rows 64-127
+    static_assert(DK_COL + DT <= 512, "tensor memory");
     static_assert(SMEM_BYTES <= SMEM_LIMIT, "shared memory budget");
 };
 
@@ -190,9 +193,11 @@ __device__ __forceinline__ void attn_keys(const AttnBackward &p, const int block
             mbar_init(bar(C::QF0 + s), 1);
             mbar_init(bar(C::QE0 + s), 1);
         }
-        mbar_init(bar(C::SF), 1);
+        mbar_init(bar(C::SF0), 1);
+        mbar_init(bar(C::SF0 + 1), 1);
         mbar_init(bar(C::DPF), 1);
-        mbar_init(bar(C::PR), C::SOFT_WARPS);
+        mbar_init(bar(C::PR0), C::SOFT_WARPS);
+        mbar_init(bar(C::PR0 + 1), C::SOFT_WARPS);
         mbar_init(bar(C::DSR), C::SOFT_WARPS);
         for (int s = 0; s < C::ROW_SLOTS; ++s) {
             mbar_init(bar(C::RF0 + s), 32);
@@ -244,6 +249,7 @@ __device__ __forceinline__ void attn_keys(const AttnBackward &p, const int block
     auto q_tile = [&](int n) -> int { return C::Q_OFF + n % C::STAGES * C::TILE_BYTES; };
     auto dy_tile = [&](int n) -> int { return C::DY_OFF + n % C::STAGES * C::TILE_BYTES; };
     auto parity = [&](int n) -> uint32_t { return (uint32_t)(n / C::STAGES) & 1; };
+    auto s_col = [&](int n) -> int { return C::S_COL + n % C::S_SLOTS * 128; };
     auto q_box = [&](int n, int h) -> int { return n % C::STAGES * C::HALVES + h; };
     // Where the loads of tile n report: a last tile that ends inside reports to
     // ROWS_WARP, which passes it on once the rest is zero.
@@ -318,11 +324,11 @@ __device__ __forceinline__ void attn_keys(const AttnBackward &p, const int block
                 for (int h = 0; h < C::HALVES; ++h) {
                     if (!wait_phase(bar(C::QF0 + q_box(n, h)), parity(n), ctl, SITE_FULL)) return false;
                     tc_fence_after();
-                    if (h == 0) attn_mma_rows<0, 4>(tmem + C::S_COL, sbase + C::K_OFF, sbase + q_tile(n), C::ID_S);
-                    else attn_mma_rows<4, 8>(tmem + C::S_COL, sbase + C::K_OFF, sbase + q_tile(n), C::ID_S);
+                    if (h == 0) attn_mma_rows<0, 4>(tmem + s_col(n), sbase + C::K_OFF, sbase + q_tile(n), C::ID_S);
+                    else attn_mma_rows<4, 8>(tmem + s_col(n), sbase + C::K_OFF, sbase + q_tile(n), C::ID_S);
                 }
-                terms(tmem + C::S_COL, n, 0);
-                mma_commit(bar(C::SF));
+                terms(tmem + s_col(n), n, 0);
+                mma_commit(bar(C::SF0 + n % C::S_SLOTS));
                 return true;
             };
             auto gradients = [&](int n) {
@@ -331,7 +337,7 @@ __device__ __forceinline__ void attn_keys(const AttnBackward &p, const int block
                 mma_commit(bar(C::DPF));
                 mma_commit(bar(C::DE0 + n % C::STAGES));
             };
-            // Turn n of either (S(0), then dV(n - 1) and S(n); dP(0), then dK and dP).
+            // Turn n of either (S(0), then dV(n - 1) and the next S; dP(0), then dK and dP).
             auto turn = [&](int n) -> bool {
                 const bool ok = first ? n == 0 || wait_phase(bar(C::TURN), (n - 1) & 1, ctl, SITE_ACC_EMPTY)
                                       : wait_phase(bar(C::TURN + 1), n & 1, ctl, SITE_ACC_EMPTY);
@@ -343,29 +349,32 @@ __device__ __forceinline__ void attn_keys(const AttnBackward &p, const int block
             // when its phase is over: what comes early is awaited early, and what
             // the other thread has awaited before its turn is not awaited again (dO
             // for dV, Q for dK, the rows' terms for dP).
+            constexpr int AHEAD = C::S_SLOTS - 1;  // S(n + AHEAD) goes with dV(n - 1)
             bool ok = wait_phase(bar(C::KVF), 0, ctl, SITE_FULL);
+            for (int n = 0; first && ok && n < AHEAD && n < tiles; ++n) ok = rows_ready(n) && scores(n);
             for (int n = 0; ok && n <= tiles; ++n) {
-                if (n < tiles)
-                    ok = first ? rows_ready(n)
-                               : wait_phase(bar(C::DF0 + n % C::STAGES), parity(n), ctl, SITE_FULL);
+                if (first && n + AHEAD < tiles) ok = rows_ready(n + AHEAD);
+                if (!first && n < tiles) ok = wait_phase(bar(C::DF0 + n % C::STAGES), parity(n), ctl, SITE_FULL);
                 if (ok && n > 0)
-                    ok = wait_phase(bar(first ? C::PR : C::DSR), (n - 1) & 1, ctl, SITE_PROBABILITIES);
+                    ok = first ? wait_phase(bar(C::PR0 + (n - 1) % C::S_SLOTS),
+                                            (uint32_t)((n - 1) / C::S_SLOTS) & 1, ctl, SITE_PROBABILITIES)
+                               : wait_phase(bar(C::DSR), (n - 1) & 1, ctl, SITE_PROBABILITIES);
                 if (!ok || !turn(n)) {
                     ok = false;
                     break;
                 }
                 if (first) {
                     if (n > 0) {
-                        attn_mma_ta<0, 8, C::P_HALF>(tmem + C::DV_COL, tmem + C::P_COL, sbase + dy_tile(n - 1),
+                        attn_mma_ta<0, 8, C::P_HALF>(tmem + C::DV_COL, tmem + s_col(n - 1), sbase + dy_tile(n - 1),
                                                      C::ID_PV, n > 1);
                         mma_commit(bar(C::DE0 + (n - 1) % C::STAGES));
                     }
-                    if (n < tiles) ok = scores(n);
+                    if (n + AHEAD < tiles) ok = scores(n + AHEAD);
                 } else {
                     if (n > 0) {
 #pragma unroll
                         for (int h = 0; h < C::HALVES; ++h) {
-                            attn_mma_ta<0, 8, C::P_HALF>(tmem + C::DK_COL + 64 * h, tmem + C::DS_COL,
+                            attn_mma_ta<0, 8, C::P_HALF>(tmem + C::DK_COL + 64 * h, tmem + C::DP_COL,
                                                          sbase + q_tile(n - 1) + h * 16384, C::ID_64, n > 1);
                             mma_commit(bar(C::QE0 + q_box(n - 1, h)));
                         }
@@ -443,13 +452,13 @@ __device__ __forceinline__ void attn_keys(const AttnBackward &p, const int block
         bool ok = true;
         for (int n = 0; n < tiles; ++n) {
             const int s = n % C::ROW_SLOTS;
-            ok = wait_warp(bar(C::SF), n & 1, ctl, SITE_SCORES);
+            ok = wait_warp(bar(C::SF0 + n % C::S_SLOTS), (uint32_t)(n / C::S_SLOTS) & 1, ctl, SITE_SCORES);
             if (!ok) break;
             tc_fence_after();
             float y[64];
             uint32_t *yw = reinterpret_cast<uint32_t *>(y);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) tmem_ld_row32(tmem + lane_base + C::S_COL + 64 * half + 32 * i, yw + 32 * i);
+            for (int i = 0; i < 2; ++i) tmem_ld_row32(tmem + lane_base + s_col(n) + 64 * half + 32 * i, yw + 32 * i);
             tmem_ld_wait();
             // Some rows of the tile do not see all of the keys.
             const bool cut = p.s.causal && attn_seen(p.s, w, i0 + n * p.h.tokens) < w.first + ATTN_KEYS;
@@ -469,10 +478,10 @@ __device__ __forceinline__ void attn_keys(const AttnBackward &p, const int block
                 for (int i = 0; i < 64; ++i)
                     if (key >= seen[i]) y[i] = 0.0f;
             }
-            attn_store_half<KD>(tmem + lane_base + C::P_COL + C::P_HALF * half, y);
+            attn_store_half<KD>(tmem + lane_base + s_col(n) + C::P_HALF * half, y);
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar(C::PR));
+            if (lane == 0) mbar_arrive(bar(C::PR0 + n % C::S_SLOTS));
 
             ok = wait_warp(bar(C::DPF), n & 1, ctl, SITE_SCORES);
             if (!ok) break;
@@ -487,7 +496,7 @@ __device__ __forceinline__ void attn_keys(const AttnBackward &p, const int block
                 for (int e = 0; e < 32; e += 2)
                     unpair2(mul_pair(pair2(y[i + e], y[i + e + 1]), pair2(f[e], f[e + 1])), y[i + e], y[i + e + 1]);
             }
-            attn_store_half<KD>(tmem + lane_base + C::DS_COL + C::P_HALF * half, y);
+            attn_store_half<KD>(tmem + lane_base + C::DP_COL + C::P_HALF * half, y);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
