@@ -448,7 +448,7 @@ __global__ void __launch_bounds__(AttnConfig<KD, DT, NQ>::NUM_THREADS, 1)
             const int seen = valid ? attn_seen(p.s, w, token) : 0;
             const int first_seen = attn_seen(p.s, w, w.first + t * p.h.tokens);  // the tile's least
             const int end = NQ == 2 && t ? b.je[NQ - 1] : b.je[0];
-            float r = 0.0f, l = 0.0f;
+            float r = 0.0f, l = 0.0f, limit = LIMIT;
             for (int j = jb; j < end; ++j) {
                 const int n = j - jb;
                 const int slot = NQ == 2 ? t : (int)((g + n) & 1);
@@ -498,8 +498,13 @@ __global__ void __launch_bounds__(AttnConfig<KD, DT, NQ>::NUM_THREADS, 1)
                     return a + b;
                 };
                 // A reference that is not below `top`, and what was summed by the old one.
+                // (A row whose scores were all -infinity so far has summed nothing: `top`
+                // is its first reference, however low.)
                 auto raise = [&](float top) {
-                    const float to = fmaxf(r, top), f = exp2_approx(r - to);
+                    const bool first = limit < 0.0f;
+                    const float to = first ? (top == -INFINITY ? 0.0f : top) : fmaxf(r, top);
+                    const float f = first ? 0.0f : exp2_approx(r - to);
+                    if (first && top != -INFINITY) limit = LIMIT;
                     r = to;
                     l *= f;
 #pragma unroll 1
@@ -524,12 +529,16 @@ __global__ void __launch_bounds__(AttnConfig<KD, DT, NQ>::NUM_THREADS, 1)
                     const float mx = largest(s);
                     half(0, s);
                     const float top = fmaxf(mx, largest(s));
-                    r = top == -INFINITY ? 0.0f : top * c;
+                    r = top * c;
+                    if (top == -INFINITY) {
+                        r = 0.0f;
+                        if (lim > 0) limit = -1.0f;
+                    }
                 } else {
                     half(0, s);
                 }
                 float sum = exponentials();
-                if (n > 0 && __any_sync(0xffffffffu, sum > LIMIT)) {
+                if (n > 0 && __any_sync(0xffffffffu, sum > limit)) {
                     // (P over S: the first half is not stored before this is known.)
                     if (NQ == 1 && !wait_warp(bar(C::PVD), (g + n - 1) & 1, ctl, SITE_ACC_FULL)) { ok = false; break; }
                     tc_fence_after();
@@ -554,7 +563,7 @@ __global__ void __launch_bounds__(AttnConfig<KD, DT, NQ>::NUM_THREADS, 1)
                 l += sum;
                 half(64, s);
                 sum = exponentials();
-                if (n > 0 && __any_sync(0xffffffffu, sum > LIMIT)) {
+                if (n > 0 && __any_sync(0xffffffffu, sum > limit)) {
                     // (The first half's product is under way by the old reference.)
                     if (!wait_warp(bar(C::PVA0 + t), (g + n) & 1, ctl, SITE_ACC_FULL)) { ok = false; break; }
                     tc_fence_after();

@@ -179,6 +179,33 @@ def test_infinities_behind_a_sequence(tg):
         assert torch.equal(got.t, want.t)
 
 
+@pytest.mark.parametrize("q_len,heads,dtype", [([3], 2, "bf16"), ([3], 2, "fp16"), ([300, 700], 32, "bf16")])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_scores_of_minus_infinity_before_low_ones(tg, q_len, heads, dtype, dim):
+    """Two blocks of keys whose scores are all -infinity, then scores of -240 and
+    less: the keys before have no part, bit for bit."""
+    n = [200] * len(q_len)
+    k_at = [256 + 500 * i for i in range(len(n))]
+
+    def problem(at, length):
+        p = ah.Problem(q_len, length, heads=heads, kv=heads, dim=dim, dtype=dtype, causal=False, scale=1 / 8,
+                       k_at=at, k_rows=500 * len(n), max_k=456, seed=5)
+        g = ah.gen(6)
+        p.Q.t.copy_(torch.rand(p.Q.t.shape, generator=g, device="cuda") + 1)
+        p.V.t.copy_(torch.randn(p.V.t.shape, generator=g, device="cuda"))
+        p.K.t.copy_(-30 - torch.rand(p.K.t.shape, generator=g, device="cuda"))
+        return p
+
+    p = problem(k_at, n)
+    want, z = ah.run_forward(tg, p)
+    ah.check_forward(tg, p)
+    late = problem([a - 256 for a in k_at], [m + 256 for m in n])
+    for a in k_at:
+        late.K.t[a - 256: a] = float("-inf")
+    got, y = ah.run_forward(tg, late)
+    assert torch.equal(got.t, want.t) and torch.equal(y, z)
+
+
 def test_rows_past_32_bit_offsets(tg):
     """A cache whose later rows lie beyond 2^31 elements."""
     ld, rows = 1 << 21, 1100
