@@ -10,17 +10,26 @@
 // it is raised, and O rescaled, in a few blocks only.  p is rounded to 16 bits for
 // the second product; l sums it unrounded in FP32.
 //
-// NQ = 2 (many tiles): two tiles a CTA, four warps each for the softmax, one
-// warp for the loads, one thread for the MMAs.  While the warps of one tile
-// work on their scores the tensor core runs the other tile's two products.
-// P overwrites S (128-wide heads; the tensor core runs a CTA's MMAs of one
-// shape in the order of issue, so the next S waits for P V), or has columns of
-// its own (64-wide).
+// NQ = 2 (many tiles): two tiles a CTA, four warps each for the softmax, a warp for
+// the loads, a thread for each tile's MMAs.  While the warps of one tile work on
+// their scores the tensor core runs the other tile's two products.  P overwrites
+// S (128-wide heads; the tensor core runs a CTA's MMAs in the order of issue,
+// so the next S waits for P V), or has columns of its own (64-wide).
 // NQ = 1 (few rows, long keys; short sequences): one tile, S doubled, so that
 // the next block's S runs while the softmax is on this one's, and a deep ring
 // of keys and values; the keys may be cut into `splits` ranges of `chunk`
 // blocks, whose rows go unnormalised, in FP32, to the workspace, where
 // tg_attn_join_kernel adds them.
+//
+// Bound, many tiles: the tensor core in principle (4 x 128 x 128 x 128 multiply-adds
+// a block of two tiles, 2048 cycles), in fact the chain S, softmax, P V of a tile,
+// whose next S has no columns before P V is through: 2950 cycles a block.  8192
+// tokens, 32 heads over 8 of 128, causal: 336 us alone, 1.64 PFLOP/s; 356 (1.54) in
+// long runs at the power limit.  Tried and slower there: eight softmax warps a tile
+// (378 to 405), the loads' registers given to the softmax, and blocks of 64 keys with S
+// twice (377; S of 128 x 64 reads its operands at 48 cycles a step for 32 of
+// arithmetic).  Bound, single tokens: memory (32 tokens over 355 to 11800 keys, 91
+// us, 5.9 TB/s; one over 131072 keys 88.5, 6.06).
 #pragma once
 
 #include "tg_attn_work.cuh"
@@ -80,8 +89,8 @@ __device__ __forceinline__ void attn_mma_ta(uint32_t d, uint32_t a, uint32_t b, 
         mma_f16_ta(d, a + (kk >> 2) * HALF + (kk & 3) * 8, db + kk * (2048 >> 4), idesc, kk ? 1 : accumulate);
 }
 
-// Zeroes rows `from` to 127 of a tile: rows behind a sequence's end hold others'
-// values, and 0 times an infinity or a NaN would reach the sums.  One row a thread.
+// Zeroes a row of a tile: rows behind a sequence's end hold others' values, and 0
+// times an infinity or a NaN would reach the sums.
 template <int HALVES>
 __device__ __forceinline__ void attn_zero_row(uint8_t *tile, int row) {
 #pragma unroll
@@ -639,6 +648,7 @@ __global__ void __launch_bounds__(AttnConfig<KD, DT, NQ>::NUM_THREADS, 1)
 //   L = sum l_s 2^(m_s - M),  O = sum o_s 2^(m_s - M) / L,  LSE = (M + log2 L) ln 2,
 // always in the same order.  WIDE: the block's eight warps share a row's ranges (a
 // few rows with many ranges); else a warp a row.  blockIdx.y: which rows of the tile.
+// Bound: its launch and two dependent reads (32 single tokens: 7.6 us by itself).
 constexpr int JOIN_WARPS = 8;
 template <Kind KD, bool WIDE>
 __global__ void __launch_bounds__(32 * JOIN_WARPS) tg_attn_join_kernel(const __grid_constant__ AttnForward p) {

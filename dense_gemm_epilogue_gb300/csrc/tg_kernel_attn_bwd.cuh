@@ -13,13 +13,20 @@
 // A row tile is the forward kernel's: `tokens` tokens x the group's heads, so the
 // keys' CTA adds up a group's heads as it adds up tokens.  P and dS are rounded
 // to 16 bits, as tensor-core operands; they stay in tensor memory.
+//
+// Bound: the chain S, dP, dS, products of a tile, like the forward kernel's: keys'
+// CTAs 2900 cycles a tile for 2176 of MMAs, rows' CTAs 1800 for 1536 (128-wide
+// heads).  8192 tokens, 32 heads over 8 of 128, causal: 1171 us alone, 1260 in long
+// runs at the power limit, 1.09 PFLOP/s of the five products (1.53 of the seven).  CTAs
+// that stay for several tiles took 1441, halves of P 720 for 693 in the keys' part.
 #pragma once
 
 #include "tg_kernel_attn.cuh"
 
 namespace tg {
 
-// delta = sum over d of dO O.
+// delta = sum over d of dO O.  Bound: memory (4096 tokens x 32 heads of 128: 14.5 us with
+// a cold L2, 4.6 TB/s).
 template <Kind KD>
 __global__ void __launch_bounds__(DELTA_THREADS) tg_attn_delta_kernel(const __grid_constant__ AttnDelta p) {
     griddep_launch();
@@ -104,11 +111,11 @@ struct AttnKeysConfig : AttnBackConfig<KD, DT> {
     static constexpr int STAGES = DT == 64 ? 4 : 2;
     static constexpr int QB = STAGES * B::HALVES;  // boxes of Q
     static constexpr int ROW_SLOTS = DT == 64 ? 6 : 3;  // rows' LSE, delta (16 bytes of parts each), keys seen
-    static constexpr int ROW_BYTES_ = 2048 + 2048 + 512;
+    static constexpr int ROW_SLOT_BYTES = 2048 + 2048 + 512;
     static constexpr int K_OFF = 0, V_OFF = B::TILE_BYTES, Q_OFF = 2 * B::TILE_BYTES;
     static constexpr int DY_OFF = Q_OFF + STAGES * B::TILE_BYTES;
     static constexpr int ROWS_OFF = DY_OFF + STAGES * B::TILE_BYTES;
-    static constexpr int WEIGHTS_OFF = ROWS_OFF + ROW_SLOTS * ROW_BYTES_;  // 128 rows of 16 bytes
+    static constexpr int WEIGHTS_OFF = ROWS_OFF + ROW_SLOTS * ROW_SLOT_BYTES;  // 128 rows of 16 bytes
     static constexpr int ZERO_OFF = WEIGHTS_OFF + 2048;                    // 128 rows of 16 zero bytes
     static constexpr int BAR_OFF = ZERO_OFF + 2048;
     static constexpr int KVF = 0, QF0 = 1, QE0 = QF0 + QB, DF0 = QE0 + QB, DE0 = DF0 + STAGES,
@@ -308,7 +315,7 @@ __device__ __forceinline__ void attn_keys(const AttnBackward &p, const int block
         if (tiles > 0 && elect_one()) {
             // The rows' own terms (attn_parts) of S, and 2 KB on, of dP.
             auto terms = [&](uint32_t d, int n, int at) {
-                const uint32_t rows = sbase + C::ROWS_OFF + n % C::ROW_SLOTS * C::ROW_BYTES_ + at;
+                const uint32_t rows = sbase + C::ROWS_OFF + n % C::ROW_SLOTS * C::ROW_SLOT_BYTES + at;
                 mma_f16(d, smem_desc_k2(sbase + C::WEIGHTS_OFF, C::ZERO_OFF - C::WEIGHTS_OFF),
                         smem_desc_k2(rows, sbase + C::ZERO_OFF - rows), C::ID_S, 1);
             };
@@ -411,7 +418,7 @@ __device__ __forceinline__ void attn_keys(const AttnBackward &p, const int block
         for (int n = 0; n < tiles; ++n) {
             const int s = n % C::ROW_SLOTS;
             if (!wait_warp(bar(C::RE0 + s), (uint32_t)(n / C::ROW_SLOTS + 1) & 1, ctl, SITE_EMPTY)) break;
-            uint8_t *rows = smem + C::ROWS_OFF + s * C::ROW_BYTES_;
+            uint8_t *rows = smem + C::ROWS_OFF + s * C::ROW_SLOT_BYTES;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const int row = lane + 32 * q, token = i0 + n * p.h.tokens + row / p.h.group;
@@ -466,7 +473,7 @@ __device__ __forceinline__ void attn_keys(const AttnBackward &p, const int block
                 ok = wait_warp(bar(C::RF0 + s), (uint32_t)(n / C::ROW_SLOTS) & 1, ctl, SITE_FULL);
                 if (!ok) break;
             }
-            const int *seen = reinterpret_cast<const int *>(smem + C::ROWS_OFF + s * C::ROW_BYTES_ + 4096) + 64 * half;
+            const int *seen = reinterpret_cast<const int *>(smem + C::ROWS_OFF + s * C::ROW_SLOT_BYTES + 4096) + 64 * half;
 #pragma unroll
             for (int i = 0; i < 64; i += 2) {
                 unpair2(mul_pair(pair2(y[i], y[i + 1]), cc), y[i], y[i + 1]);

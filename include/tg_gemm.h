@@ -534,11 +534,12 @@ tg_status tg_layer_norm_backward(int64_t M, int64_t N, const void *dY, int64_t l
  * Layout: a tensor has rows (tokens) of `heads` heads of `dim` values; value d
  * of head h of row t is at base + t*ld + h*hd + d (elements; hd is not looked
  * at for one head); an output's heads lie within its rows (ld >= (heads - 1)*hd +
- * dim) or its rows within its heads (hd >= (rows - 1)*ld + dim).  The heads of a QKV projection's rows are addressed in
- * place.  Packed sequences: sequence s owns the rows starts[s] to starts[s] +
+ * dim) or its rows within its heads (hd >= (rows - 1)*ld + dim).  The heads of a
+ * QKV projection's rows are addressed in place.  Packed sequences: sequence s owns the rows starts[s] to starts[s] +
  * lengths[s], or to starts[s + 1] where lengths is NULL; starts and lengths are
  * device arrays of int64 (starts has seqs + 1 entries, of which the last is
- * read only without lengths).  A sequence may be empty.  Rows of no sequence are
+ * read only without lengths).  A sequence may be empty; no row of Q is in two
+ * (keys may be shared: a common prefix).  Rows of no sequence are
  * neither used nor written, whatever they hold.  Entries that point outside the
  * tensors are cut to them.
  *
@@ -580,8 +581,9 @@ tg_status tg_rotary_steps(int64_t rot, double base, tg_rotary_scaling scaling, d
  * in device memory.  positions (tokens int64, device; NULL: 0, 1, 2, ...) may be
  * negative.  rows (tokens int64, device; NULL: t) is the row of Y that token t
  * goes to, so that keys (and, with rot = 0, values) are written to a cache's
- * rows; a row outside [0, y_rows) skips the token, and none may be given twice.  Without rows, Y has `tokens` rows, may be X itself (same
- * pointer and strides), and y_rows is not looked at.  dtype is any tg_out_dtype;
+ * rows; a row outside [0, y_rows) skips the token, and none may be given twice.
+ * Without rows, Y has `tokens` rows, may be X itself (same pointer and strides),
+ * and y_rows is not looked at.  dtype is any tg_out_dtype;
  * cos and sin are FP32; dim <= 4096 (TG_ERR_UNSUPPORTED
  * beyond); X and Y need the alignment of an element only.
  */

@@ -179,6 +179,13 @@ def test_infinities_behind_a_sequence(tg):
         assert torch.equal(got.t, want.t)
 
 
+@pytest.mark.parametrize("causal", [True, False])
+def test_shared_keys(tg, causal):
+    """Sequences that read the same rows of a cache: a common prefix."""
+    ah.check_forward(tg, ah.Problem([1, 5, 40], [300, 300, 170], heads=4, kv=2, dim=64, causal=causal,
+                                    q_at=[0, 1, 6], k_at=[0, 0, 130], q_rows=46, k_rows=300))
+
+
 @pytest.mark.parametrize("q_len,heads,dtype", [([3], 2, "bf16"), ([3], 2, "fp16"), ([300, 700], 32, "bf16")])
 @pytest.mark.parametrize("dim", [64, 128])
 def test_scores_of_minus_infinity_before_low_ones(tg, q_len, heads, dtype, dim):
