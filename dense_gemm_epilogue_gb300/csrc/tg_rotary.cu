@@ -237,6 +237,8 @@ tg_status rotary(int64_t tokens, int64_t heads, int64_t dim, int64_t rot, const 
     if (ldx >= (int64_t)1 << 38 || ldy >= (int64_t)1 << 38 ||
         (heads > 1 && (hx >= (int64_t)1 << 38 || hy >= (int64_t)1 << 38)))
         return TG_ERR_INVALID_VALUE;
+    // In place: value for value.
+    if (X == Y && !rows && ((tokens > 1 && ldx != ldy) || (heads > 1 && hx != hy))) return TG_ERR_INVALID_VALUE;
     // Y's rows and heads may not run into each other.
     const int64_t out_rows = rows ? y_rows : tokens;
     if (heads > 1 && out_rows > 1 && ldy < (heads - 1) * hy + dim && (double)hy < (double)(out_rows - 1) * ldy + dim)

@@ -609,7 +609,9 @@ tg_status tg_rotary_backward(int64_t tokens, int64_t heads, int64_t dim, int64_t
  * pass reads) may be NULL.
  *
  * max_q and max_k bound the sequences' rows and keys (0: q_rows, k_rows); the
- * plan goes by them, and a longer sequence is cut to them.  dtype is TG_BF16 or
+ * plan goes by them, and a longer sequence is cut to them.  (Bounds far above the
+ * lengths cost time and, for single tokens over a cache, workspace: pieces of work
+ * without keys, and room for their rows.)  dtype is TG_BF16 or
  * TG_FP16; products and sums are FP32, probabilities are rounded to dtype for
  * the second product.  Bases must be 16-byte aligned, ld and hd multiples of 8
  * and at least dim (TG_ERR_INVALID_VALUE); dim a multiple of 8 up to 128 and

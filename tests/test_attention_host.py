@@ -103,6 +103,7 @@ def rotary(tg, **over):
     (dict(steps=A + 4), INVALID), (dict(positions=A + 4), INVALID), (dict(rows=A + 1, y_rows=9), INVALID),
     (dict(rows=A, y_rows=-1), INVALID), (dict(layout=2), INVALID), (dict(layout=-1), INVALID),
     (dict(amplitude=NAN), INVALID), (dict(amplitude=INF), INVALID), (dict(dtype=3), INVALID),
+    (dict(ldy=136), INVALID), (dict(ldx=160, hx=80), INVALID),  # in place, but for other strides
     (dict(tokens=0, X=None, Y=None), OK), (dict(heads=0, X=None, Y=None), OK), (dict(dim=0, rot=0), OK),
 ])
 def test_rotary_statuses(tg, over, status):
