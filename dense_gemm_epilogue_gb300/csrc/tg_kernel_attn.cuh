@@ -573,7 +573,11 @@ __global__ void __launch_bounds__(AttnConfig<KD, DT, NQ>::NUM_THREADS, 1)
                 half(64, s);
                 sum = exponentials();
                 if (n > 0 && __any_sync(0xffffffffu, sum > limit)) {
-                    // (The first half's product is under way by the old reference.)
+                    // The first half's product is under way by the old reference.  With one tile
+                    // S runs ahead: these scores say that P V(n - 2) is over, and another warp may
+                    // still keep P V(n - 1) waiting, so PVA0 may be a phase behind, whose parity
+                    // would pass for this one's.  P V(n - 1) first.
+                    if (NQ == 1 && !wait_warp(bar(C::PVD), (g + n - 1) & 1, ctl, SITE_ACC_FULL)) { ok = false; break; }
                     if (!wait_warp(bar(C::PVA0 + t), (g + n) & 1, ctl, SITE_ACC_FULL)) { ok = false; break; }
                     tc_fence_after();
                     raise(largest(s) * c);

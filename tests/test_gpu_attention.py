@@ -275,3 +275,50 @@ def test_repeats_streams_and_graphs(tg):
         want, eo, lse, el = ah.reference(p)
         ah.check(o.t, want, eo, f"replayed with {lens}")
         ah.check(z, lse, el, f"replayed with {lens} LSE")
+
+
+def staircase(q_len, k_len, heads, dim, dtype, seed):
+    """A problem whose rows outgrow their reference again and again: a warp's rows (32
+    of a tile's 128) score the same for a key but for noise, and every warp has
+    its own half blocks from which on its keys score `step` more, beyond what a reference
+    may lag behind (2^30 BF16, 2^14 FP16).  So warps rescale O in different halves of
+    successive blocks.  (Steps are whole numbers, exact in both types.)"""
+    p = ah.Problem(q_len, k_len, heads=heads, kv=heads, dim=dim, dtype=dtype, causal=False, scale=1.0, sigma=0.25,
+                   seed=seed)
+    step = 24 if dtype == "bf16" else 12
+    g = torch.Generator().manual_seed(seed)
+    p.Q.t[:, :, :4] = 0.0
+    for at, n in zip(p.q_at, q_len):
+        i = torch.arange(n, device="cuda")
+        p.Q.t[at + i, :, i % 128 // 32] = 4.0
+    for at, n in zip(p.k_at, k_len):
+        first = torch.randint(0, 64, (-(-n // 64), heads, 4), generator=g)  # where in the half block
+        rise = torch.rand(-(-n // 64), heads, 4, generator=g) < 0.4
+        rise[:2] = False  # (the first block's maximum is the first reference)
+        where = torch.arange(n)[:, None, None]
+        level = torch.zeros(n, heads, 4)
+        for b in range(2, rise.shape[0]):
+            level += (rise[b] & (where >= 64 * b + first[b])).float()
+        p.K.t[at: at + n, :, :4] = (level * (step // 4)).to("cuda", p.K.t.dtype)
+    p.Q.before, p.K.before = p.Q.buf.clone(), p.K.buf.clone()
+    return p
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("tiles,ranges", [(1, False), (1, True), (2, False), (2, True)])
+def test_warps_outgrow_their_reference_in_different_halves(tg, tiles, ranges, dim, dtype):
+    """Against FP64, and bit for bit the same again."""
+    if tiles == 1:
+        p = staircase([128, 100], [1500, 1300], 8, dim, dtype, 3) if ranges else \
+            staircase([128] * 20, [1000] * 20, 16, dim, dtype, 4)
+    elif ranges:
+        p = staircase([300, 200], [3000, 2900], 16, dim, dtype, 5)
+    else:
+        p = staircase([1500, 900], [900, 1000], 16, dim, dtype, 6)
+    got = plan(tg, p)
+    assert got["tiles"] == tiles and (got["ranges"] > 1) == ranges, got
+    o, z = ah.check_forward(tg, p)
+    for _ in range(10):
+        again, y = ah.run_forward(tg, p)
+        assert torch.equal(again.t, o.t) and torch.equal(y, z)
