@@ -457,7 +457,9 @@ __global__ void __launch_bounds__(AttnConfig<KD, DT, NQ>::NUM_THREADS, 1)
             const int seen = valid ? attn_seen(p.s, w, token) : 0;
             const int first_seen = attn_seen(p.s, w, w.first + t * p.h.tokens);  // the tile's least
             const int end = NQ == 2 && t ? b.je[NQ - 1] : b.je[0];
-            float r = 0.0f, l = 0.0f, limit = LIMIT;
+            // A row that is not the sequence's (another's, or one that no load wrote) has no say
+            // in when its warp raises: the others' last bits would go by what it holds.
+            float r = 0.0f, l = 0.0f, limit = valid ? LIMIT : INFINITY;
             for (int j = jb; j < end; ++j) {
                 const int n = j - jb;
                 const int slot = NQ == 2 ? t : (int)((g + n) & 1);
@@ -541,7 +543,7 @@ __global__ void __launch_bounds__(AttnConfig<KD, DT, NQ>::NUM_THREADS, 1)
                     r = top * c;
                     if (top == -INFINITY) {
                         r = 0.0f;
-                        if (lim > 0) limit = -1.0f;
+                        if (valid && lim > 0) limit = -1.0f;
                     }
                 } else {
                     half(0, s);

@@ -322,3 +322,55 @@ def test_warps_outgrow_their_reference_in_different_halves(tg, tiles, ranges, di
     for _ in range(10):
         again, y = ah.run_forward(tg, p)
         assert torch.equal(again.t, o.t) and torch.equal(y, z)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("q_len,k_len,heads,kv", [
+    ([1] * 6, [5000, 1, 0, 4097, 640, 700], 8, 2),  # single tokens, key ranges
+    ([3, 40, 100], [400, 300, 700], 2, 2),          # a tile a sequence
+    ([300, 700], [900, 700], 32, 16),               # two tiles a CTA
+    ([1] * 300, [300] * 300, 4, 4),                 # whole key ranges
+])
+def test_queries_of_others_have_no_say(tg, q_len, k_len, heads, kv, dim, dtype):
+    """Rows of Q between and behind the sequences, and the other sequences' own, lie in the
+    same tiles: whatever they hold, a sequence's results are the same bits."""
+    at, gap = [], 5
+    for n in q_len:
+        at.append((at[-1] + q_len[len(at) - 1] if at else 0) + gap)
+    p = ah.Problem(q_len, k_len, heads=heads, kv=kv, dim=dim, dtype=dtype, causal=False, q_at=at,
+                   q_rows=at[-1] + q_len[-1] + 130, seed=8)
+    rows = p.rows()
+    noise = torch.randn(p.Q.t.shape, generator=ah.gen(9), device="cuda").to(p.Q.t.dtype)
+    p.Q.t[~rows] = 0
+    want, z = ah.run_forward(tg, p)
+    for f in (100.0, 10000.0, float("inf"), float("-inf"), float("nan")):
+        p.Q.t[~rows] = noise[~rows].abs() * f if f != 100.0 else noise[~rows] * f
+        got, y = ah.run_forward(tg, p)
+        assert torch.equal(got.t[rows], want.t[rows]) and torch.equal(y[:, rows], z[:, rows]), f
+    # every other sequence's queries changed
+    p.Q.t[~rows] = 0
+    kept = torch.zeros_like(rows)
+    for a, n in zip(at[::2], q_len[::2]):
+        kept[a: a + n] = True
+    p.Q.t[rows & ~kept] = noise[rows & ~kept] * 100
+    got, y = ah.run_forward(tg, p)
+    assert torch.equal(got.t[kept], want.t[kept]) and torch.equal(y[:, kept], z[:, kept])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("q_len,heads,kv", [([100, 18], 7, 1), ([126], 12, 4), ([900, 1500], 28, 4), ([60], 48, 8)])
+def test_groups_that_leave_rows_of_a_tile(tg, q_len, heads, kv, dim, dtype):
+    """The same bits again, whatever an earlier call left in the rows that no load writes."""
+    p = ah.Problem(q_len, [700] * len(q_len), heads=heads, kv=kv, dim=dim, dtype=dtype, causal=False, seed=8)
+    outs = []
+    for f in (0.0, 100.0, 0.01, float("inf"), 30000.0):
+        # 128 rows a tile, of one value: one tile a CTA and two
+        for fill in (ah.Problem([128] * 40, [64] * 40, heads=8, kv=8, dim=dim, dtype=dtype),
+                     ah.Problem([2048], [64], heads=32, kv=32, dim=dim, dtype=dtype)):
+            fill.Q.t.copy_(torch.randn(fill.Q.t.shape, generator=ah.gen(10), device="cuda") * f)
+            ah.run_forward(tg, fill)
+        outs.append(ah.run_forward(tg, p))
+    for o, z in outs[1:]:
+        assert torch.equal(o.t, outs[0][0].t) and torch.equal(z, outs[0][1])
