@@ -13,6 +13,14 @@ constexpr int ATTN_ROWS = 128;  // rows of a tile: tokens x heads of one group
 constexpr int ATTN_KEYS = 128;  // keys of a block
 constexpr int ATTN_MAX_DIM = 128;
 
+// Rows of the last of `tiles` row tiles that begin at token i0 of a sequence of lq.  (Held
+// to a tile's tokens before the product: the tiles may be one part of the sequence's, and
+// what is left of 2^31 rows, times a group of 128, is more than 32 bits hold.)
+__host__ __device__ inline int attn_tail_rows(int lq, int i0, int tiles, int tokens, int group) {
+    const int left = lq - i0 - (tiles - 1) * tokens;
+    return (left < tokens ? left : tokens) * group;
+}
+
 // Packed sequences: sequence s owns rows starts[s] to starts[s] + length[s] (or
 // starts[s + 1] when no lengths are given) of Q, and of K and V.
 struct AttnSeqs {

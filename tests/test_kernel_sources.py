@@ -4,6 +4,11 @@ from __future__ import annotations
 
 import os
 import re
+import shutil
+import subprocess
+import sys
+
+import pytest
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 CSRC = os.path.join(ROOT, "dense_gemm_epilogue_gb300", "csrc")
@@ -40,3 +45,48 @@ def test_attention_rescales_o_behind_the_block_before():
         assert re.search(r"NQ == 1 && !wait_warp\(bar\(C::PVD\), \(g \+ n - 1\) & 1", block), block
         if "PVA0" in block:
             assert block.index("C::PVD") < block.index("C::PVA0")
+
+
+TAIL = r"""
+#include <cstdio>
+#include "tg_attn.h"
+int main() {
+    long long lq, i0, tiles, tokens, group;
+    while (std::scanf("%lld %lld %lld %lld %lld", &lq, &i0, &tiles, &tokens, &group) == 5)
+        std::printf("%d\n", tg::attn_tail_rows((int)lq, (int)i0, (int)tiles, (int)tokens, (int)group));
+}
+"""
+
+
+def test_rows_of_a_parts_last_tile(tmp_path):
+    """The kernel's own arithmetic on the host.  A part's last tile is full unless it is
+    the sequence's last one, however much of the sequence is left behind it (2^31 rows,
+    times 128 heads of a group)."""
+    import dense_gemm_epilogue_gb300 as tg
+
+    tg.build()
+    build = sys.modules["dense_gemm_epilogue_gb300.build"]
+    if shutil.which("g++") is None:
+        pytest.skip("no C++ compiler")
+    include = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(build.nvcc()))), "include")
+    src, exe = tmp_path / "tail.cpp", str(tmp_path / "tail")
+    src.write_text(TAIL)
+    subprocess.run(["g++", "-std=c++17", "-fsanitize=undefined", "-fno-sanitize-recover", "-I", CSRC, "-I", include,
+                    str(src), "-o", exe], check=True)
+    most = 2 ** 31 - 1 - 512
+    cases = []
+    for group in (1, 3, 7, 8, 100, 128):
+        tokens = 128 // group
+        for lq in (1, tokens, tokens + 1, 1000, 2 ** 24, 2 ** 24 + 1, 2 ** 30, most - 3, most):
+            for i0 in (0, 1, lq // 2, lq - 1):
+                every = -(-(lq - i0) // tokens)
+                for tiles in (1, 2, every // 16, every // 2, every - 1, every):
+                    if 1 <= tiles <= every:
+                        cases.append((lq, i0, tiles, tokens, group))
+    out = subprocess.run([exe], input="\n".join(" ".join(map(str, c)) for c in cases), text=True, check=True,
+                         capture_output=True).stdout
+    got = [int(v) for v in out.split()]
+    want = [min(lq - i0 - (tiles - 1) * tokens, tokens) * group for lq, i0, tiles, tokens, group in cases]
+    assert got == want
+    # what a product of all that is left would wrap to
+    assert any((lq - i0 - (tiles - 1) * tokens) * group >= 2 ** 31 for lq, i0, tiles, tokens, group in cases)
