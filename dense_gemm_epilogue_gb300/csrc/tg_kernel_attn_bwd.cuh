@@ -249,10 +249,10 @@ __device__ __forceinline__ void attn_keys(const AttnBackward &p, const int block
     const AttnWork w = *shared_work;
     int i0;  // the first token of this part
     int tiles = attn_key_tiles(p, w, i0) - part * p.key_tiles;
-    i0 += part * p.key_tiles * p.h.tokens;
     tiles = tiles < 0 ? 0 : tiles < p.key_tiles ? tiles : p.key_tiles;
-    const int tail = (w.lq - i0 - (tiles - 1) * p.h.tokens) * p.h.group;  // rows of the last tile
-    const bool fix = tiles > 0 && tail < box;
+    if (tiles > 0) i0 += part * p.key_tiles * p.h.tokens;
+    const int tail = tiles > 0 ? attn_tail_rows(w.lq, i0, tiles, p.h.tokens, p.h.group) : box;  // rows of the last tile
+    const bool fix = tail < box;
     auto q_tile = [&](int n) -> int { return C::Q_OFF + n % C::STAGES * C::TILE_BYTES; };
     auto dy_tile = [&](int n) -> int { return C::DY_OFF + n % C::STAGES * C::TILE_BYTES; };
     auto parity = [&](int n) -> uint32_t { return (uint32_t)(n / C::STAGES) & 1; };
