@@ -234,7 +234,6 @@ __device__ __forceinline__ void attn_keys(const AttnBackward &p, const int block
         tmem_alloc(smem_u32(tmem_slot), C::TMEM_COLS);
         tmem_relinquish();
     }
-    griddep_launch();
     griddep_wait();
     const int part = block % p.key_parts, rest = block / p.key_parts;
     const int head = rest % p.h.kv_heads;
@@ -245,6 +244,7 @@ __device__ __forceinline__ void attn_keys(const AttnBackward &p, const int block
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    griddep_launch();
     const uint32_t tmem = *tmem_slot;
     const AttnWork w = *shared_work;
     int i0;  // the first token of this part
@@ -596,7 +596,6 @@ __device__ __forceinline__ void attn_rows(const AttnBackward &p, const int block
         tmem_alloc(smem_u32(tmem_slot), C::TMEM_COLS);
         tmem_relinquish();
     }
-    griddep_launch();
     griddep_wait();
     const int part = block % p.row_parts, rest = block / p.row_parts;
     const int head = rest % p.h.kv_heads;
@@ -607,6 +606,7 @@ __device__ __forceinline__ void attn_rows(const AttnBackward &p, const int block
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    griddep_launch();
     const uint32_t tmem = *tmem_slot;
     const AttnWork w = *shared_work;
     const int b0 = part * p.row_blocks;  // the first block of this part

@@ -90,3 +90,19 @@ def test_rows_of_a_parts_last_tile(tmp_path):
     assert got == want
     # what a product of all that is left would wrap to
     assert any((lq - i0 - (tiles - 1) * tokens) * group >= 2 ** 31 for lq, i0, tiles, tokens, group in cases)
+
+
+def test_dependents_start_behind_tensor_memory():
+    """A kernel lets the next one start only behind the barrier that its allocation of
+    tensor memory is before: one that allocated first would wait for this kernel to end,
+    and this one for its columns."""
+    for name in sorted(os.listdir(CSRC)):
+        if not name.startswith("tg_kernel"):
+            continue
+        with open(os.path.join(CSRC, name)) as f:
+            text = re.sub(r"//[^\n]*", "", f.read())
+        at = [m.start() for m in re.finditer(r"\btmem_alloc(_pair)?\(", text)]
+        for start, end in zip(at, at[1:] + [len(text)]):
+            launch = text.find("griddep_launch()", start, end)
+            if launch >= 0:
+                assert re.search(r"__syncthreads\(\)|cluster_sync_all\(\)", text[start:launch]), (name, start)
