@@ -301,8 +301,9 @@ extern "C" tg_status tg_rotary_steps(int64_t rot, double base, tg_rotary_scaling
         double turns = f / kTwoPi;
         turns -= std::floor(turns);
         if (!(turns >= 0.0)) return TG_ERR_INVALID_VALUE;  // an overflow above
-        // (the largest double below 1 times 2^64 is below 2^64)
-        steps[i] = turns >= 1.0 ? 0 : (uint64_t)std::ldexp(turns, 64);
+        // To the nearest step: truncated, low frequencies would lose twice as much a position.
+        // (The largest double below 1 times 2^64 is a whole number below 2^64.)
+        steps[i] = turns >= 1.0 ? 0 : (uint64_t)std::nearbyint(std::ldexp(turns, 64));
     }
     return TG_OK;
 }

@@ -196,3 +196,30 @@ def test_argument_kinds(tg):
         backward(tg, scale="x")
     with pytest.raises(TypeError):
         backward(tg, stream="not a stream")
+
+
+@pytest.mark.parametrize("rot,base", [(128, 500000.0), (64, 10000.0), (4096, 1e6), (2, 10000.0)])
+@pytest.mark.parametrize("scaling", ["none", "linear", "base", "bands"])
+def test_frequencies_to_the_nearest_step(tg, rot, base, scaling):
+    """Against 60 digits.  A step is off by half of 2^-64 turns and by FP64's roundings: the
+    exponent's, times ln base, and those of pow, 2 pi, base and the scaling, fewer than 32."""
+    from decimal import Decimal as D
+    from decimal import localcontext
+
+    if scaling == "base" and rot == 2:
+        pytest.skip("refused")
+    got = tg.tg_rotary_steps(rot, base, scaling, 8.0, 1.0, 4.0, 8192.0)
+    with localcontext() as c:
+        c.prec = 60
+        two_pi = 2 * D("3.14159265358979323846264338327950288419716939937510582097494459")
+        b = D(base) * (D(8) ** (D(rot) / D(rot - 2)) if scaling == "base" else 1)
+        for i, step in enumerate(got):
+            f = b ** (-D(2 * i) / D(rot))
+            if scaling == "linear":
+                f /= 8
+            if scaling == "bands":
+                g = min(max((8192 * f / two_pi - 1) / 3, D(0)), D(1))
+                f = g * f + (1 - g) * f / 8
+            want = f / two_pi * 2 ** 64
+            rel = (math.log(base * 8) + 32) * 2.0 ** -53
+            assert abs(step % (1 << 64) - want) <= D(0.5) + want * D(rel), i
