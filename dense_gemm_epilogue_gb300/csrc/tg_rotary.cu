@@ -290,6 +290,8 @@ extern "C" tg_status tg_rotary_steps(int64_t rot, double base, tg_rotary_scaling
          !std::isfinite(original)))
         return TG_ERR_INVALID_VALUE;
     if (scaling == TG_ROTARY_BASE) base *= std::pow(factor, (double)rot / (double)(rot - 2));
+    // (with an infinite base all pairs but the first would stand still)
+    if (!(base > 0.0) || !std::isfinite(base)) return TG_ERR_INVALID_VALUE;
     for (int64_t i = 0; i < rot / 2; ++i) {
         double f = std::pow(base, -(double)(2 * i) / (double)rot);
         if (scaling == TG_ROTARY_LINEAR) f /= factor;

@@ -568,7 +568,8 @@ typedef enum {
  * f_i / 2 pi turns a position, to the nearest fraction of 2^64, so that position *
  * step, modulo 2^64, is the angle however far the position: for each position it is
  * off by 2^-65 turns and by FP64's roundings of f_i ((ln base)/2 + 8 times 2^-53 f_i
- * without scaling).  rot is even and positive, base and factor positive; low < high and original > 0 are read
+ * without scaling).  rot is even and positive, base and factor positive, the scaled
+ * base and all f_i finite (TG_ERR_INVALID_VALUE); low < high and original > 0 are read
  * for TG_ROTARY_BANDS only.
  */
 tg_status tg_rotary_steps(int64_t rot, double base, tg_rotary_scaling scaling, double factor,

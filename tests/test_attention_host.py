@@ -223,3 +223,11 @@ def test_frequencies_to_the_nearest_step(tg, rot, base, scaling):
             want = f / two_pi * 2 ** 64
             rel = (math.log(base * 8) + 32) * 2.0 ** -53
             assert abs(step % (1 << 64) - want) <= D(0.5) + want * D(rel), i
+
+
+@pytest.mark.parametrize("over", [dict(base=1e300, factor=1e10), dict(base=10000.0, factor=1e200, rot=4),
+                                  dict(base=1e-200, factor=1e-200, rot=4)])
+def test_scaled_base_out_of_range(tg, over):
+    """base factor^(rot/(rot-2)) beyond FP64: no frequencies that never turn."""
+    with pytest.raises(tg.TgError):
+        tg.tg_rotary_steps(**dict(dict(rot=64, scaling="base"), **over))
