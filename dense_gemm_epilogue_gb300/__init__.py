@@ -633,7 +633,8 @@ def tg_rotary_steps(rot, base, scaling="none", factor=1.0, low=1.0, high=4.0, or
     """Frequencies as 64-bit fractions of a turn a position, in a list of rot/2 integers as int64
     holds them (a tensor of them on the device is what tg_rotary reads); raises TgError on invalid
     arguments.  scaling is a name of ROTARY_SCALINGS."""
-    out = (ctypes.c_uint64 * max(int(rot) // 2, 1))()
+    # (room for every rot that the library takes: 4096 at most)
+    out = (ctypes.c_uint64 * min(max(int(rot) // 2, 1), 2048))()
     code = ROTARY_SCALINGS[scaling] if isinstance(scaling, str) else int(scaling)
     check(load().tg_rotary_steps(rot, base, code, factor, low, high, original, out), "tg_rotary_steps")
     return [v - (1 << 64) if v >> 63 else v for v in out]

@@ -231,3 +231,10 @@ def test_scaled_base_out_of_range(tg, over):
     """base factor^(rot/(rot-2)) beyond FP64: no frequencies that never turn."""
     with pytest.raises(tg.TgError):
         tg.tg_rotary_steps(**dict(dict(rot=64, scaling="base"), **over))
+
+
+def test_frequencies_of_a_huge_rotary(tg):
+    """Refused by the library, not by the memory for its answer."""
+    for rot in (1 << 40, 1 << 62):
+        with pytest.raises(tg.TgError):
+            tg.tg_rotary_steps(rot, 10000.0)
