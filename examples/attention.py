@@ -161,11 +161,13 @@ class Attention:
 
     def prefill(self, x: torch.Tensor, lengths, capacity: int) -> torch.Tensor:
         """The prompts' outputs; their keys and values go to a cache of `capacity` rows
-        for each sequence."""
+        for each sequence, as many as its prompt and the tokens to come may have."""
+        if max(lengths) > capacity:
+            raise ValueError(f"a prompt of {max(lengths)} tokens for {capacity} rows of a cache")
         starts = starts_of(lengths)
         positions = torch.cat([torch.arange(n, device="cuda") for n in lengths])
         y = self.forward(x, starts, positions, max(lengths))
-        self.capacity, self.seqs = capacity, len(lengths)
+        self.capacity, self.seqs, self.longest = capacity, len(lengths), max(lengths)
         self.cache = torch.empty(2, self.seqs * capacity, self.kv * self.dim, dtype=BF16, device="cuda")
         self.slabs = torch.arange(self.seqs, device="cuda") * capacity
         self.lengths = torch.tensor(lengths, dtype=torch.int64, device="cuda")
@@ -184,6 +186,9 @@ class Attention:
 
     def decode(self, x: torch.Tensor) -> torch.Tensor:
         """One new token of each sequence (its row of x)."""
+        if self.longest == self.capacity:  # (its next row is another sequence's first)
+            raise ValueError(f"a sequence has filled the cache's {self.capacity} rows of its own")
+        self.longest += 1
         m, st = self.seqs, torch.cuda.current_stream()
         _, _, _, qkv = self._project(x, False)
         positions = self.lengths  # the new token's

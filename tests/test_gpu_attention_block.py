@@ -103,3 +103,24 @@ def test_decoding_continues_the_prompt(at):
     for i in range(7):
         got = block.decode(torch.stack([x[n + i] for x, n in zip(xs, prompt)]))
         close(got, torch.stack([ref[n + i] for ref, n in zip(want, prompt)]), f"token {i}")
+
+
+def test_full_cache_is_refused(at):
+    """A sequence that has filled its rows of the cache: an error before anything is
+    written, and no other sequence's keys and values change.  Nor is a prompt taken that
+    is longer than its rows."""
+    torch.manual_seed(7)
+    block = at.Attention(4, 2, 64, seed=5)
+    x = torch.randn(9, 256, device="cuda").to(torch.bfloat16)
+    with pytest.raises(ValueError):
+        block.prefill(x, [7, 2], 6)
+    block.prefill(x, [7, 2], 8)
+    block.decode(x[:2])
+    kept, lengths = block.cache.clone(), block.lengths.clone()
+    for _ in range(2):
+        with pytest.raises(ValueError):
+            block.decode(x[:2])
+    torch.cuda.synchronize()
+    # (rows that nothing was written to hold anything)
+    assert torch.equal(block.cache.view(torch.int16), kept.view(torch.int16))
+    assert torch.equal(block.lengths, lengths)
