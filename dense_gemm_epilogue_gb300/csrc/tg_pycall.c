@@ -180,7 +180,7 @@ static void *as_space(PyObject *o, int64_t *bytes, int *ok) {
 #define TAKE(count, what)                                                                        \
     int ok = 1;                                                                                  \
     if (n != (count)) {                                                                          \
-        PyErr_Format(PyExc_TypeError, what ": %zd arguments for %d", n, (count));                \
+        PyErr_Format(PyExc_TypeError, "%s: %zd arguments for %d", what, n, (count));             \
         return NULL;                                                                             \
     }
 
@@ -354,16 +354,18 @@ static PyObject *py_rotary_back(PyObject *self, PyObject *const *a, Py_ssize_t n
 
 static PyObject *attn_ws(int64_t (*f)(int64_t, int64_t, int64_t, int64_t, int64_t, int64_t, int64_t,
                                       int64_t, tg_dtype),
-                         PyObject *const *a, Py_ssize_t n) {
-    TAKE(9, "tg_attention_workspace_bytes")
+                         const char *name, PyObject *const *a, Py_ssize_t n) {
+    TAKE(9, name)
     SIZES
     const int64_t max_q = INT(a[6]), max_k = INT(a[7]);
     const tg_dtype t = DTYPE(a[8]);
     return ok ? PyLong_FromLongLong(f(seqs, q_rows, k_rows, heads, kv, dim, max_q, max_k, t)) : NULL;
 }
-static PyObject *py_attn_ws(PyObject *self, PyObject *const *a, Py_ssize_t n) { return attn_ws(f_attn_ws, a, n); }
+static PyObject *py_attn_ws(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+    return attn_ws(f_attn_ws, "tg_attention_workspace_bytes", a, n);
+}
 static PyObject *py_attn_back_ws(PyObject *self, PyObject *const *a, Py_ssize_t n) {
-    return attn_ws(f_attn_back_ws, a, n);
+    return attn_ws(f_attn_back_ws, "tg_attention_backward_workspace_bytes", a, n);
 }
 
 static PyObject *py_attn(PyObject *self, PyObject *const *a, Py_ssize_t n) {

@@ -238,3 +238,13 @@ def test_frequencies_of_a_huge_rotary(tg):
     for rot in (1 << 40, 1 << 62):
         with pytest.raises(tg.TgError):
             tg.tg_rotary_steps(rot, 10000.0)
+
+
+def test_argument_counts_name_their_call(tg):
+    """A wrong number of arguments is reported under the name of the call that was made."""
+    if tg._call is None:
+        pytest.skip("ctypes counts them")
+    for name in ("tg_rotary", "tg_rotary_backward", "tg_attention_workspace_bytes", "tg_attention",
+                 "tg_attention_backward_workspace_bytes", "tg_attention_backward"):
+        with pytest.raises(TypeError, match=f"^{name}: 1 arguments"):
+            getattr(tg._call, name)(1)
