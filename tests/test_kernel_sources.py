@@ -106,3 +106,12 @@ def test_dependents_start_behind_tensor_memory():
             launch = text.find("griddep_launch()", start, end)
             if launch >= 0:
                 assert re.search(r"__syncthreads\(\)|cluster_sync_all\(\)", text[start:launch]), (name, start)
+
+
+def test_attention_helpers_are_reached():
+    """Every device function of the attention sources is called by another."""
+    every = " ".join(line for _, _, line in code())
+    for name in ("tg_attn_ptx.cuh", "tg_attn_work.cuh", "tg_kernel_attn.cuh", "tg_kernel_attn_bwd.cuh"):
+        text = "\n".join(line for f, _, line in code() if f == name)
+        for f in re.findall(r"__forceinline__ \w+ (\w+)\(", text):
+            assert len(re.findall(rf"\b{f}\b", every)) > 1, (name, f)
