@@ -127,8 +127,8 @@ struct ForwardPlan {
 // ranges are of 16 blocks at most there, for an even load (32 single tokens over 355
 // to 11800 keys: 91 us; 24 blocks 94, 48 blocks 101; one over 131072: 88.5 in one
 // round of CTAs over 54 blocks each, 99 over 16 each).
-ForwardPlan plan_forward(const Sizes &z, int sms) {
-    ForwardPlan best = {};
+tg_status plan_forward(const Sizes &z, int sms, ForwardPlan *plan) {
+    ForwardPlan &best = *plan = {};
     const int64_t tokens = ATTN_ROWS / (z.heads / z.kv_heads);
     const int64_t max_q = bound_of(z.max_q, z.q_rows), max_k = bound_of(z.max_k, z.k_rows);
     const int64_t blocks = ceil_div(max_k, ATTN_KEYS) > 0 ? ceil_div(max_k, ATTN_KEYS) : 1;
@@ -143,6 +143,7 @@ ForwardPlan plan_forward(const Sizes &z, int sms) {
         for (int64_t s = 1; s <= most; ++s) {
             const int64_t chunk = ceil_div(blocks, s), splits = ceil_div(blocks, chunk);
             if (splits != s) continue;
+            if (ctas > INT32_MAX / splits) break;  // more pieces than a grid
             const double waves = (double)ceil_div(ctas * splits, sms);
             double cycles = waves * (7000.0 + chunk * (nq == 2 ? 2700.0 : 2000.0));
             if (splits > 1) cycles += 6000.0 + 8.0 * splits * z.heads * z.q_rows * z.dim / 2500.0;
@@ -155,8 +156,12 @@ ForwardPlan plan_forward(const Sizes &z, int sms) {
             best.chunk = chunk;
         }
     }
-    if (best.splits > 1) best.workspace = best.splits * z.heads * z.q_rows * (4 * z.dim + 8);
-    return best;
+    if (least < 0.0) return TG_ERR_UNSUPPORTED;
+    if (best.splits > 1) {
+        if ((double)best.splits * z.heads * z.q_rows * (4 * z.dim + 8) > 4e18) return TG_ERR_UNSUPPORTED;
+        best.workspace = best.splits * z.heads * z.q_rows * (4 * z.dim + 8);
+    }
+    return TG_OK;
 }
 
 struct BackwardPlan {
@@ -174,8 +179,8 @@ struct BackwardPlan {
 // 128-wide heads 2700 for keys, 1700 for rows; 64-wide 2000 and 1100.  2048 rows of
 // 8 heads over one key head: 198 us whole, 63 in parts; 64 rows over 8192 keys 91 and
 // 57; 309 rows of 3 heads, 8 tiles, 22 whole, 25 and 28 in 2 and 8 parts.)
-BackwardPlan plan_backward(const Sizes &z, int sms) {
-    BackwardPlan p = {};
+tg_status plan_backward(const Sizes &z, int sms, BackwardPlan *plan) {
+    BackwardPlan &p = *plan = {};
     const int64_t group = z.heads / z.kv_heads, tokens = ATTN_ROWS / group;
     const int64_t max_q = bound_of(z.max_q, z.q_rows), max_k = bound_of(z.max_k, z.k_rows);
     p.tiles = z.q_rows ? tile_bound(z.seqs, z.q_rows, max_q, tokens) : 0;
@@ -204,7 +209,8 @@ BackwardPlan plan_backward(const Sizes &z, int sms) {
     cut(long_blocks, row_cycles, p.row_parts, p.row_blocks);
     if (p.key_parts > 1) p.part_keys = 8 * p.key_parts * z.k_rows * z.kv_heads * z.dim;
     if (p.row_parts > 1) p.part_rows = 4 * p.row_parts * z.q_rows * z.heads * z.dim;
-    return p;
+    const int64_t ctas = (p.tiles * p.row_parts + p.blocks * p.key_parts) * z.kv_heads;
+    return ctas > INT32_MAX || z.q_rows * z.heads / 16 > INT32_MAX - 1 ? TG_ERR_UNSUPPORTED : TG_OK;
 }
 
 bool arrays_ok(const int64_t *qs, const int64_t *ql, const int64_t *ks, const int64_t *kl) {
@@ -252,7 +258,8 @@ extern "C" int64_t tg_attention_workspace_bytes(int64_t seqs, int64_t q_rows, in
     tg::host::Device dev;
     if (tg::host::device(&dev) != TG_OK) return -1;
     if (seqs == 0 || q_rows == 0) return 0;
-    return plan_forward(z, dev.sms).workspace;
+    ForwardPlan p;
+    return plan_forward(z, dev.sms, &p) == TG_OK ? p.workspace : -1;
 }
 
 extern "C" tg_status tg_attention_plan_describe(int64_t seqs, int64_t q_rows, int64_t k_rows, int64_t heads,
@@ -273,7 +280,9 @@ extern "C" tg_status tg_attention_plan_describe(int64_t seqs, int64_t q_rows, in
     if (seqs == 0 || q_rows == 0) {
         n = std::snprintf(buf, len, "empty");
     } else {
-        const ForwardPlan p = plan_forward(z, num_sms);
+        ForwardPlan p;
+        st = plan_forward(z, num_sms, &p);
+        if (st != TG_OK) return st;
         n = std::snprintf(buf, len, "tiles=%d ctas=%lld ranges=%lld blocks=%lld", p.nq,
                           (long long)(p.tiles * kv_heads * p.splits), (long long)p.splits, (long long)p.chunk);
     }
@@ -302,8 +311,9 @@ extern "C" tg_status tg_attention(int64_t seqs, int64_t q_rows, int64_t k_rows, 
     tg::host::Device dev;
     st = tg::host::device(&dev);
     if (st != TG_OK) return st;
-    const ForwardPlan p = plan_forward(z, dev.sms);
-    if (p.tiles * kv_heads * p.splits > INT32_MAX) return TG_ERR_UNSUPPORTED;
+    ForwardPlan p;
+    st = plan_forward(z, dev.sms, &p);
+    if (st != TG_OK) return st;
     if (p.workspace && (!workspace || (uintptr_t)workspace % 16 || workspace_bytes < p.workspace))
         return TG_ERR_INVALID_VALUE;
     AttnForward a = {};
@@ -341,7 +351,8 @@ extern "C" int64_t tg_attention_backward_workspace_bytes(int64_t seqs, int64_t q
     if (seqs == 0) return 0;
     tg::host::Device dev;
     if (tg::host::device(&dev) != TG_OK) return -1;
-    return plan_backward(z, dev.sms).workspace();
+    BackwardPlan p;
+    return plan_backward(z, dev.sms, &p) == TG_OK ? p.workspace() : -1;
 }
 
 extern "C" tg_status tg_attention_backward(
@@ -374,7 +385,9 @@ extern "C" tg_status tg_attention_backward(
     tg::host::Device dev;
     st = tg::host::device(&dev);
     if (st != TG_OK) return st;
-    const BackwardPlan plan = plan_backward(z, dev.sms);
+    BackwardPlan plan;
+    st = plan_backward(z, dev.sms, &plan);
+    if (st != TG_OK) return st;
     if (plan.workspace() && (!workspace || (uintptr_t)workspace % 16 || workspace_bytes < plan.workspace()))
         return TG_ERR_INVALID_VALUE;
     AttnBackward a = {};
@@ -395,9 +408,6 @@ extern "C" tg_status tg_attention_backward(
     a.dv = {k_rows ? dV : nullptr, lddv, kv_heads == 1 ? 0 : hdv};
     a.lse = LSE;
     a.delta = static_cast<const float *>(workspace);
-    if (plan.tiles * plan.row_parts * kv_heads + plan.blocks * plan.key_parts * kv_heads > INT32_MAX ||
-        q_rows * heads / 16 > INT32_MAX - 1)
-        return TG_ERR_UNSUPPORTED;
     a.tiles = (int32_t)plan.tiles;
     a.blocks = (int32_t)plan.blocks;
     a.key_parts = a.dk.ptr || a.dv.ptr ? (int32_t)plan.key_parts : 1;

@@ -248,3 +248,21 @@ def test_argument_counts_name_their_call(tg):
                  "tg_attention_backward_workspace_bytes", "tg_attention_backward"):
         with pytest.raises(TypeError, match=f"^{name}: 1 arguments"):
             getattr(tg._call, name)(1)
+
+
+@pytest.mark.parametrize("sizes", [(1 << 29, (1 << 31) - 600, (1 << 31) - 600, 65536, 65536, 128, 1, 0),
+                                   (1 << 29, 1 << 30, (1 << 31) - 600, 128, 128, 8, 2, 0)])
+def test_more_pieces_than_a_grid(tg, sizes):
+    """More row tiles than a grid has CTAs: TG_ERR_UNSUPPORTED, in the description as in the
+    call."""
+    with pytest.raises(tg.TgError, match="TG_ERR_UNSUPPORTED"):
+        tg.tg_attention_plan_describe(*sizes, "bf16", 152)
+
+
+@pytest.mark.parametrize("sizes", [(1 << 16, 1 << 16, (1 << 31) - 600, 64, 64, 64, 1, 0),
+                                   (1 << 26, 1 << 26, (1 << 31) - 600, 8, 8, 8, 1, 0),
+                                   (2, 3, (1 << 31) - 600, 8, 8, 8, 1, 0)])
+def test_key_ranges_stay_within_a_grid(tg, sizes):
+    p = plan(tg, *sizes, "bf16")
+    assert p["ctas"] == sizes[0] * sizes[4] * p["ranges"] < 1 << 31
+    assert p["ranges"] * p["blocks"] >= -(-sizes[2] // 128)
