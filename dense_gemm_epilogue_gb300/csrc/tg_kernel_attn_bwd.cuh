@@ -12,7 +12,9 @@
 //
 // A row tile is the forward kernel's: `tokens` tokens x the group's heads, so the
 // keys' CTA adds up a group's heads as it adds up tokens.  P and dS are rounded
-// to 16 bits, as tensor-core operands; they stay in tensor memory.
+// to 16 bits, as tensor-core operands; they stay in tensor memory.  (Those roundings are
+// the gradients' distance from FP32 ones, 0.0026 of their norms in BF16 and 0.0003 in
+// FP16: to a form that rounds likewise it is 0.0006 and 0.00006 at most.)
 //
 // Bound: the chain S, dP, dS, products of a tile, like the forward kernel's: keys'
 // CTAs 2900 cycles a tile for 2176 of MMAs, rows' CTAs 1800 for 1536 (128-wide
@@ -370,6 +372,9 @@ __device__ __forceinline__ void attn_keys(const AttnBackward &p, const int block
                     ok = false;
                     break;
                 }
+                // (S over P, and dP over dS, are issued behind the products that read what they
+                // overwrite by the same thread: the tensor core's order is that of issue, and
+                // nothing else keeps them apart.)
                 if (first) {
                     if (n > 0) {
                         attn_mma_ta<0, 8, C::P_HALF>(tmem + C::DV_COL, tmem + s_col(n - 1), sbase + dy_tile(n - 1),

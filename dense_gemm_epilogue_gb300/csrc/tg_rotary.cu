@@ -13,7 +13,8 @@
 // it touches once, in shared memory, and its threads then each hold eight pairs
 // of one place in the head, two rows apart at a time, loads before the table and before
 // the stores.  (8192 x 40 heads of 128: 29.7 us, 5.7 TB/s; four rows a thread and four
-// blocks an SM, 4.2 waves, 32.9; one row and eight blocks 33.5.)
+// blocks an SM, 4.2 waves, 32.9; one row and eight blocks 33.5.  Six blocks an SM hold the
+// kernel to 40 registers: vectors of halves spill 24 bytes, 16 in FP32.)
 #include <cuda_runtime.h>
 
 #include <atomic>

@@ -535,13 +535,13 @@ tg_status tg_layer_norm_backward(int64_t M, int64_t N, const void *dY, int64_t l
  * of head h of row t is at base + t*ld + h*hd + d (elements; hd is not looked
  * at for one head); an output's heads lie within its rows (ld >= (heads - 1)*hd +
  * dim) or its rows within its heads (hd >= (rows - 1)*ld + dim).  The heads of a
- * QKV projection's rows are addressed in place.  Packed sequences: sequence s owns the rows starts[s] to starts[s] +
- * lengths[s], or to starts[s + 1] where lengths is NULL; starts and lengths are
- * device arrays of int64 (starts has seqs + 1 entries, of which the last is
- * read only without lengths).  A sequence may be empty; no row of Q is in two
- * (keys may be shared: a common prefix).  Rows of no sequence are
- * neither used nor written, whatever they hold.  Entries that point outside the
- * tensors are cut to them.
+ * QKV projection's rows are addressed in place.  Packed sequences: sequence s owns
+ * the rows starts[s] to starts[s] + lengths[s], or to starts[s + 1] where lengths is
+ * NULL; starts and lengths are device arrays of int64 (starts has seqs + 1 entries, of
+ * which the last is read only without lengths).  A sequence may be empty; no row of Q
+ * is in two (keys may be shared: a common prefix).  Rows of no sequence are neither
+ * used nor written, whatever they hold.  A sequence that runs past the tensor's end
+ * is cut there; one that starts outside is empty.
  *
  * Workspace, ownership, asynchrony and errors are the feed-forward operators'
  * (everything is enqueued on `stream`, arguments are checked before anything is
@@ -615,9 +615,11 @@ tg_status tg_rotary_backward(int64_t tokens, int64_t heads, int64_t dim, int64_t
  * lengths cost time and, for single tokens over a cache, workspace: pieces of work
  * without keys, and room for their rows.)  dtype is TG_BF16 or
  * TG_FP16; products and sums are FP32, probabilities are rounded to dtype for
- * the second product.  Bases must be 16-byte aligned, ld and hd multiples of 8
- * and at least dim (TG_ERR_INVALID_VALUE); dim a multiple of 8 up to 128 and
- * heads / kv_heads at most 128 (TG_ERR_UNSUPPORTED); scale positive and finite.
+ * the second product (in BF16 their sums of products may be 2^48 times O: finite
+ * values of V above 2^80 can overflow there).  Bases must be 16-byte aligned, ld
+ * and hd multiples of 8 and at least dim (TG_ERR_INVALID_VALUE); dim a multiple of 8
+ * up to 128 and heads / kv_heads at most 128 (TG_ERR_UNSUPPORTED); scale positive
+ * and finite.
  * An infinity or a NaN in a sequence's own V reaches every row of that sequence
  * that is worked on beside a row that sees it (rows up to 256 before it); other
  * sequences' and unused rows' never do.
@@ -652,11 +654,12 @@ tg_status tg_attention_plan_describe(int64_t seqs, int64_t q_rows, int64_t k_row
  * dK and dV summed over the query heads of a key head.  dQ, dK and dV may each
  * be NULL.  Layout, limits and alignment are tg_attention's; P and dS are rounded
  * to dtype where the products read them (in FP16, dS below 2^-25 is lost: scale
- * the loss; and |LSE| / scale has to stay below 2^31).  An infinity or a NaN in a
- * row, key or value may reach the gradients of the 128 keys, or of the rows, that it
- * is worked on with.  Keys that no row sees, and rows without keys, get zeros; the key
- * ranges of two sequences may not overlap.  No atomics: repeated calls agree bit
- * for bit.
+ * the loss; a P below 2^-14, as of tens of thousands of keys of even weight, is held
+ * to a step of 2^-24; and |LSE| / scale and |sum of dO O| have to stay below 2^31).
+ * An infinity or a NaN in a row, key or value may reach the gradients of the 128
+ * keys, or of the rows, that it is worked on with.  Keys that no row sees, and rows
+ * without keys, get zeros; the key ranges of two sequences may not overlap.  No
+ * atomics: repeated calls agree bit for bit.
  */
 int64_t tg_attention_backward_workspace_bytes(int64_t seqs, int64_t q_rows, int64_t k_rows,
                                               int64_t heads, int64_t kv_heads, int64_t dim,
